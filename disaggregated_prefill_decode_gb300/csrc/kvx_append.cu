@@ -1,0 +1,98 @@
+// kvx_cache_append: new keys and values to their slots, 16-bit values as they are, 8-bit codes rounded
+// to nearest even from value * (1 / scale) in 32 bits.
+//
+// A thread keeps one column (plane, head, 8 elements) and walks tokens, so shard, head and element
+// offsets are computed once; only the slot changes. Reads are 16 bytes a thread, writes 16 or 8.
+// Bound by memory: each value is read and written once.
+#include "kvx_internal.h"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+namespace kvx {
+
+constexpr int kAppendThreads = 256;
+
+template <int IO> __device__ __forceinline__ float2 to_float2(uint32_t x);
+template <> __device__ __forceinline__ float2 to_float2<KVX_BF16>(uint32_t x) {
+    return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
+template <> __device__ __forceinline__ float2 to_float2<KVX_F16>(uint32_t x) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&x));
+}
+
+// Two codes of two values; values beyond the largest code saturate there, NaN stays.
+template <int IO> __device__ __forceinline__ uint32_t codes(uint32_t x, float inverse) {
+    float2 f = to_float2<IO>(x);
+    f.x *= inverse;
+    f.y *= inverse;
+    return __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+}
+
+// IO 0: 16-bit values copied; KVX_BF16 / KVX_F16: converted to 8 bits. UNROLL tokens per thread.
+template <int IO, int UNROLL>
+__global__ void __launch_bounds__(kAppendThreads) kvx_append_kernel(const __grid_constant__ AppendArgs a, int cols, int rows) {
+    const int my_row = threadIdx.x / cols, col = blockIdx.y * cols + threadIdx.x % cols;
+    const int vecs = a.head_dim / 8, heads = a.pool.heads_per_shard * a.pool.n_shards;
+    const int plane = col / (heads * vecs), head = col / vecs % heads, vec = col % vecs;
+    if (my_row >= rows || plane >= a.planes) return;
+    const uint8_t *src = (plane ? a.v : a.k) + (int64_t)(head * vecs + vec) * 16;
+    const int64_t stride = plane ? a.v_stride : a.k_stride;
+    const int shard = head / a.pool.heads_per_shard;
+    uint8_t *dst = (plane ? a.pool.v[shard] : a.pool.k[shard]) +
+                   (int64_t)(head - shard * a.pool.heads_per_shard) * a.pool.head_pitch + vec * (IO ? 8 : 16);
+    const float inverse = plane ? a.v_inverse : a.k_inverse;
+    int64_t slot[UNROLL];
+    uint4 x[UNROLL];
+    const int64_t t0 = (int64_t)blockIdx.x * UNROLL * rows + my_row;
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+        const int64_t t = t0 + u * rows;
+        slot[u] = t < a.n_tokens ? a.slots[t] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+        const int64_t t = t0 + u * rows;
+        if (t < a.n_tokens) x[u] = __ldg(reinterpret_cast<const uint4 *>(src + t * stride));
+    }
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+        if (slot[u] < 0 || slot[u] >= a.n_rows) {
+            if (slot[u] != -1 && col == 0) atomicAdd(a.pool.skipped, 1ull);
+            continue;
+        }
+        const uint32_t row = (uint32_t)slot[u], blk = row / (uint32_t)a.pool.block_size;
+        uint8_t *d = dst + (int64_t)blk * a.pool.block_pitch + (int64_t)(row - blk * a.pool.block_size) * a.pool.token_pitch;
+        if constexpr (IO == 0) {
+            *reinterpret_cast<uint4 *>(d) = x[u];
+        } else {
+            uint2 y;
+            y.x = codes<IO>(x[u].x, inverse) | codes<IO>(x[u].y, inverse) << 16;
+            y.y = codes<IO>(x[u].z, inverse) | codes<IO>(x[u].w, inverse) << 16;
+            *reinterpret_cast<uint2 *>(d) = y;
+        }
+    }
+}
+
+template <int IO> static cudaError_t launch(const AppendArgs &a, int32_t sms, cudaStream_t stream) {
+    const int64_t all = (int64_t)a.planes * a.pool.n_shards * a.pool.heads_per_shard * (a.head_dim / 8);
+    const int cols = (int)std::min<int64_t>(all, kAppendThreads), rows = kAppendThreads / cols;
+    const unsigned y = (unsigned)((all + cols - 1) / cols);
+    const bool few = (a.n_tokens + rows - 1) / rows * y < 4 * sms;
+    const int unroll = few ? 1 : 4;
+    const dim3 grid((unsigned)((a.n_tokens + rows * unroll - 1) / (rows * unroll)), y);
+    if (few) kvx_append_kernel<IO, 1><<<grid, kAppendThreads, 0, stream>>>(a, cols, rows);
+    else kvx_append_kernel<IO, 4><<<grid, kAppendThreads, 0, stream>>>(a, cols, rows);
+    count_launch();
+    return cudaGetLastError();
+}
+
+cudaError_t launch_append(const AppendArgs &a, int32_t value_type, int32_t io_type, int32_t sms, cudaStream_t stream) {
+    if (value_type != KVX_E4M3) return launch<0>(a, sms, stream);
+    return io_type == KVX_BF16 ? launch<KVX_BF16>(a, sms, stream) : launch<KVX_F16>(a, sms, stream);
+}
+
+}  // namespace kvx

@@ -129,6 +129,9 @@ kvx_status cuda_fail(cudaError_t e, const char *what);
 void count_launch(int64_t n = 1);
 size_t align_up(size_t x, size_t a);
 
+// Counts and buffer table of a pool, checked (kvx_plan.cpp).
+kvx_status read_geom(const kvx_pool *p, const char *side, Geom *g, std::vector<void *> *bases);
+
 // Device memory from a library-owned stream-ordered pool (one per device; it keeps freed memory
 // for reuse instead of returning it to the driver at every synchronisation).
 kvx_status pool_alloc(void **ptr, size_t bytes, cudaStream_t stream);
@@ -160,6 +163,76 @@ constexpr int64_t kBulkRingMax = 192 << 10;
 inline bool valid_stages(int32_t s) { return s == 0 || s == 2 || s == 3 || s == 4 || s == 6 || s == 8; }
 
 }  // namespace kvx
+
+// ------------------------------------------------------------------------------------------------
+// Decode side: typed pools
+// ------------------------------------------------------------------------------------------------
+namespace kvx {
+
+constexpr int32_t kCacheMaxShards = 64;
+constexpr int32_t kCacheMaxDim = 256, kCacheMaxLatent = 576, kCacheMaxLatentValue = 512;
+
+// One layer of a typed pool as the kernels see it (passed by value). Bytes from one block, token slot
+// and head of a shard to the next.
+struct CacheLayer {
+    uint8_t *k[kCacheMaxShards];
+    uint8_t *v[kCacheMaxShards];      // the latents again for one-plane pools
+    int64_t block_pitch;
+    int32_t token_pitch, head_pitch;
+    int32_t n_blocks, block_size;
+    int32_t heads_per_shard, n_shards;
+    unsigned long long *skipped;      // slots, blocks and lengths out of bounds
+};
+
+struct SlotArgs {
+    const int32_t *ctx_len, *new_len, *free_blocks;
+    int32_t *block_table, *positions, *seq_len;
+    int64_t *tok_off, *slots;
+    kvx_slot_result *result;
+    int64_t n_free, table_stride, max_tokens;
+    int32_t n_reqs, block_size, max_blocks;
+};
+cudaError_t launch_slot_map(const SlotArgs &a, int32_t sms, cudaStream_t stream);      // kvx_slots.cu
+
+struct AppendArgs {
+    CacheLayer pool;
+    const uint8_t *k, *v;
+    int64_t k_stride, v_stride;       // bytes
+    const int64_t *slots;
+    int64_t n_tokens, n_rows;         // n_rows: slots of the pool
+    int32_t head_dim, planes;
+    float k_inverse, v_inverse;       // E4M3: 1 / scale
+};
+cudaError_t launch_append(const AppendArgs &a, int32_t value_type, int32_t io_type, int32_t sms, cudaStream_t stream);
+
+struct AttendArgs {
+    CacheLayer pool;
+    const uint8_t *q;
+    uint8_t *out;
+    float *lse;
+    const int32_t *block_table, *seq_len;
+    int64_t q_stride, out_stride;     // bytes
+    int64_t table_stride;
+    int32_t max_blocks, n_reqs;
+    int32_t n_q_heads, n_kv_heads, head_dim, v_dim, window;
+    float scale;                      // of q . code, times log2(e)
+    float v_scale;
+    uint8_t *scratch;                 // of the handle
+};
+cudaError_t launch_attend(const AttendArgs &a, int32_t value_type, int32_t io_type, int32_t sms, cudaStream_t stream);
+size_t attend_scratch_bytes(int32_t sms);
+
+}  // namespace kvx
+
+// The object behind kvx_cache_t.
+struct kvx_cache_s {
+    kvx::Geom g{};
+    std::vector<void *> base;
+    kvx_cache_config cfg{};                    // defaults filled in
+    int32_t device = -1;                       // of the scratch, set by the first append or attend
+    int32_t sms = 0;
+    uint8_t *dev = nullptr;                    // [256 bytes: skipped][scratch of the attend kernels]
+};
 
 // The plan object behind kvx_plan_t.
 struct kvx_plan_s {

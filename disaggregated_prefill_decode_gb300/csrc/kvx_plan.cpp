@@ -40,7 +40,7 @@ size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-static kvx_status read_geom(const kvx_pool *p, const char *side, Geom *g, std::vector<void *> *bases) {
+kvx_status read_geom(const kvx_pool *p, const char *side, Geom *g, std::vector<void *> *bases) {
     if (!p) return fail(KVX_EINVAL, "%s pool is NULL", side);
     if (p->n_layers < 1 || p->n_planes < 1 || p->n_shards < 1 || p->heads_per_shard < 1 || p->head_dim < 1 ||
         p->elem_bytes < 1 || p->block_size < 1 || p->n_blocks < 0)

@@ -67,6 +67,15 @@ class kvx_match_result(ctypes.Structure):
                 ("push", c_i32), ("dst_start", c_i64)]
 
 
+KVX_BF16, KVX_F16, KVX_E4M3 = 1, 2, 3
+
+
+class kvx_cache_config(ctypes.Structure):
+    _fields_ = [("value_type", c_i32), ("io_type", c_i32), ("n_q_heads", c_i32), ("v_dim", c_i32), ("window", c_i32),
+                ("scale", ctypes.c_float), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
+                ("reserved", c_i32 * 4)]
+
+
 MATCH_RESULT_DTYPE = np.dtype([("local_hit_blocks", "<i4"), ("remote_hit_blocks", "<i4"), ("missing_tokens", "<i4"),
                                ("push", "<i4"), ("dst_start", "<i8")])
 assert MATCH_RESULT_DTYPE.itemsize == ctypes.sizeof(kvx_match_result)
@@ -122,6 +131,13 @@ _sig = {
     "kvx_match_prefix_ex": (c_i32, [c_vp, c_vp, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_i32, c_vp, c_i64,
                                     _P(kvx_pool), _P(kvx_pool), c_vp, c_vp, _P(c_vp), c_vp]),
     "kvx_match_prefix_static": (c_i32, [c_vp, c_vp, c_i32, c_i32, c_vp, c_vp, c_vp, c_i32, c_i64, c_vp, c_vp]),
+    "kvx_slot_map": (c_i32, [c_vp, c_vp, c_i32, c_i32, c_vp, c_i64, c_vp, c_i64, c_i32, c_i64, c_vp, c_vp, c_vp, c_vp,
+                             c_vp, c_vp]),
+    "kvx_cache_create": (c_i32, [_P(kvx_pool), _P(kvx_cache_config), _P(c_vp)]),
+    "kvx_cache_destroy": (c_i32, [c_vp]),
+    "kvx_cache_append": (c_i32, [c_vp, c_i32, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp]),
+    "kvx_cache_attend": (c_i32, [c_vp, c_i32, c_vp, c_i64, c_vp, c_i64, c_i32, c_vp, c_i32, c_vp, c_i64, c_vp, c_vp]),
+    "kvx_cache_status": (c_i32, [c_vp, c_vp]),
     "kvx_conn_create": (c_i32, [_P(kvx_conn_config), _P(c_vp)]),
     "kvx_conn_destroy": (c_i32, [c_vp]),
     "kvx_conn_register": (c_i32, [c_vp, c_i64, c_i32, _P(c_i32), c_i32, c_i64]),
@@ -446,6 +462,73 @@ def kvx_match_prefix_static(tokens, tok_off, n_sessions: int, block_size: int, t
                                       _stream(stream))
     if st not in (KVX_OK, KVX_ENOMEM):
         raise KvxError(st, "kvx_match_prefix_static")
+    return st
+
+
+# ---------------------------------------------------------------------------------------------
+# decode side: slots, append, attention
+# ---------------------------------------------------------------------------------------------
+
+class Cache:
+    """Owns a kvx_cache_t handle; kvx_cache_destroy (or `with`, or the last reference) frees it. Keeps its
+    pool's buffers alive."""
+
+    def __init__(self, handle: int, pool: Pool):
+        self.handle = handle
+        self.pool = pool
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        kvx_cache_destroy(self)
+
+    def __del__(self):
+        if self.handle:
+            _lib.kvx_cache_destroy(self.handle)
+
+
+def kvx_slot_map(ctx_len, new_len, n_reqs: int, block_size: int, free_blocks, n_free: int, block_table,
+                 table_stride: int, max_blocks: int, max_tokens: int, tok_off, slots, positions, seq_len, result,
+                 stream=None) -> None:
+    """result: three device int64 (n_tokens, n_blocks, status)."""
+    _check(_lib.kvx_slot_map(_ptr(ctx_len), _ptr(new_len), n_reqs, block_size, _ptr(free_blocks), n_free,
+                             _ptr(block_table), table_stride, max_blocks, max_tokens, _ptr(tok_off), _ptr(slots),
+                             _ptr(positions), _ptr(seq_len), _ptr(result), _stream(stream)), "kvx_slot_map")
+
+
+def kvx_cache_create(pool: Pool, value_type: int, io_type: int = 0, n_q_heads: int = 0, v_dim: int = 0,
+                     window: int = 0, scale: float = 0.0, k_scale: float = 0.0, v_scale: float = 0.0) -> Cache:
+    cfg = kvx_cache_config(value_type, io_type, n_q_heads, v_dim, window, scale, k_scale, v_scale)
+    out = c_vp()
+    _check(_lib.kvx_cache_create(ctypes.byref(pool.struct), ctypes.byref(cfg), ctypes.byref(out)), "kvx_cache_create")
+    return Cache(out.value, pool)
+
+
+def kvx_cache_destroy(cache: Cache) -> None:
+    h, cache.handle = cache.handle, 0
+    if h:
+        _check(_lib.kvx_cache_destroy(h), "kvx_cache_destroy")
+
+
+def kvx_cache_append(cache: Cache, layer: int, k, k_stride: int, v, v_stride: int, slots, n_tokens: int,
+                     stream=None) -> None:
+    _check(_lib.kvx_cache_append(cache.handle, layer, _ptr(k), k_stride, _ptr(v), v_stride, _ptr(slots), n_tokens,
+                                 _stream(stream)), "kvx_cache_append")
+
+
+def kvx_cache_attend(cache: Cache, layer: int, q, q_stride: int, block_table, table_stride: int, max_blocks: int,
+                     seq_len, n_reqs: int, out, out_stride: int, lse=None, stream=None) -> None:
+    _check(_lib.kvx_cache_attend(cache.handle, layer, _ptr(q), q_stride, _ptr(block_table), table_stride, max_blocks,
+                                 _ptr(seq_len), n_reqs, _ptr(out), out_stride, _ptr(lse), _stream(stream)),
+           "kvx_cache_attend")
+
+
+def kvx_cache_status(cache: Cache, stream=None) -> int:
+    """Waits for the stream. Returns KVX_OK or KVX_ERANGE; other statuses raise."""
+    st = _lib.kvx_cache_status(cache.handle, _stream(stream))
+    if st not in (KVX_OK, KVX_ERANGE):
+        raise KvxError(st, "kvx_cache_status")
     return st
 
 

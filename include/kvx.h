@@ -490,6 +490,121 @@ kvx_status kvx_match_prefix_static(const uint32_t *tokens, const int64_t *tok_of
                                    kvx_match_result *out, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------------------------------
+ * Decode side: what a decode worker does with the blocks a push delivered -- give every request the
+ * slots of its new tokens, write their keys and values there, and attend to the cache.
+ *
+ * A slot is block * block_size + offset, the row index of the plan's runs. All three calls only
+ * enqueue on `stream`; none waits, copies to the host or allocates (but for the first call on a cache,
+ * see kvx_cache_create), so a step of them can be captured in a CUDA graph. Lengths, tables and slots
+ * are device arrays and are checked on the device: what lies outside its bounds is skipped there, never
+ * read or written, and reported in kvx_slot_result or by kvx_cache_status.
+ * ---------------------------------------------------------------------------------------------- */
+
+/* What kvx_slot_map found (device). */
+typedef struct kvx_slot_result {
+    int64_t n_tokens;      /* sum of new_len */
+    int64_t n_blocks;      /* entries of free_blocks taken, or needed when there are too few */
+    int64_t status;        /* KVX_OK; KVX_ENOMEM: n_blocks > n_free; KVX_ERANGE: n_tokens > max_tokens,
+                              a request longer than max_blocks blocks or 2^31 - 1 tokens, a negative
+                              length, or a token that goes on in a block the table does not hold
+                              (KVX_ENOMEM when both) */
+} kvx_slot_result;
+
+/*
+ * kvx_slot_map -- block tables and slot maps from request lengths.
+ * Request r holds ctx_len[r] cached tokens in the blocks block_table[r][0 .. ceil(ctx / block_size))
+ * and is about to add new_len[r] (1 when decoding, a chunk of a prompt, or 0). Taken in request order,
+ * the blocks it lacks are the next entries of free_blocks and are written to its row of the table.
+ * Outputs, requests concatenated in order:
+ *   tok_off[n_reqs + 1]   where each request's new tokens start;
+ *   slots[max_tokens]     slot of every new token; -1 for a token without one (see the status) and in
+ *                         the tail [n_tokens, max_tokens), so that a fixed-size batch can be appended;
+ *   positions[max_tokens] position of every new token in its request (the tail is left alone), or NULL;
+ *   seq_len[n_reqs]       ctx_len + new_len, what kvx_cache_attend takes.
+ * Row r of the table starts at block_table + r * table_stride and has max_blocks <= table_stride
+ * entries. All pointers are device memory; seq_len must not be ctx_len or new_len itself.
+ * Negative lengths count as 0. n_reqs up to 2^24.
+ */
+kvx_status kvx_slot_map(const int32_t *ctx_len, const int32_t *new_len, int32_t n_reqs, int32_t block_size,
+                        const int32_t *free_blocks, int64_t n_free, int32_t *block_table, int64_t table_stride,
+                        int32_t max_blocks, int64_t max_tokens, int64_t *tok_off, int64_t *slots,
+                        int32_t *positions, int32_t *seq_len, kvx_slot_result *result, cudaStream_t stream);
+
+/* Types of a pool's values. The push moves them as opaque bytes; reading them needs the type. */
+#define KVX_BF16 1
+#define KVX_F16 2
+#define KVX_E4M3 3      /* 8 bits; a code stands for code * scale */
+
+/* How a pool's values are read. Zero fields take the defaults. */
+typedef struct kvx_cache_config {
+    int32_t value_type;    /* KVX_BF16, KVX_F16 (elem_bytes 2) or KVX_E4M3 (elem_bytes 1) */
+    int32_t io_type;       /* type of new keys and values, queries and outputs: value_type for the
+                              16-bit ones; KVX_BF16 (0) or KVX_F16 for KVX_E4M3 */
+    int32_t n_q_heads;     /* query heads, a multiple of the pool's KV heads (0: the same number); query
+                              head h reads KV head h / (n_q_heads / KV heads) */
+    int32_t v_dim;         /* one-plane pools: the first v_dim elements of a latent are its value
+                              (0: head_dim). Two-plane pools: 0 or head_dim */
+    int32_t window;        /* a token sees the last `window` cached tokens only (0: all) */
+    float scale;           /* of the products q . k (0: 1 / sqrt(head_dim)) */
+    float k_scale;         /* KVX_E4M3: scale of the key plane (or the latents); 0: 1 */
+    float v_scale;         /* KVX_E4M3: scale of the value plane; 0: 1 (one-plane pools: must be 0 or
+                              k_scale) */
+    int32_t reserved[4];   /* must be 0 */
+} kvx_cache_config;
+
+typedef struct kvx_cache_s *kvx_cache_t;
+
+/*
+ * kvx_cache_create -- a typed handle on a pool, for the two calls below. The pool's counts and buffer
+ * pointers are copied; its memory stays the caller's. No CUDA call is made here: the first append or
+ * attend allocates the handle's scratch (device memory of the current device, a few MiB) and waits for
+ * it, so make that first call before any stream capture (KVX_EINVAL inside one).
+ * Refused: KVX_EINVAL for what contradicts the pool (types and elem_bytes, head counts, v_dim, negative
+ * or non-finite values, reserved != 0), KVX_EUNSUPPORTED for more than 64 shards, 2^31 - 1 rows in a
+ * buffer or more, head rows (head_dim * elem_bytes, and v_dim * elem_bytes) that are not whole 16-byte
+ * vectors, buffers off a 16-byte boundary, head_dim above 256 (two planes) or 576 (one plane).
+ * Calls on one handle use its scratch: their device work must not overlap (one stream, or ordered by
+ * events). Handles are independent of one another; several may share a pool.
+ */
+kvx_status kvx_cache_create(const kvx_pool *pool, const kvx_cache_config *cfg, kvx_cache_t *out);
+kvx_status kvx_cache_destroy(kvx_cache_t cache);   /* waits for the device; NULL is a no-op */
+
+/*
+ * kvx_cache_append -- write the keys and values of n_tokens tokens to their slots of one layer.
+ * Token t's key of (global) head h is k[t * k_stride + h * head_dim ..], its value v[t * v_stride + ...]
+ * in io_type (strides in elements; multiples of 16 bytes, as the pointers); v is NULL for one-plane
+ * pools. 16-bit values are copied; an 8-bit one is the nearest code (ties to even, saturated at 448, NaN
+ * kept) of value * (1 / scale) in 32 bits. slots: device array as kvx_slot_map makes it; -1 skips the token,
+ * any other slot outside the pool too, and kvx_cache_status reports it. Two tokens with one slot: either.
+ */
+kvx_status kvx_cache_append(kvx_cache_t cache, int32_t layer, const void *k, int64_t k_stride, const void *v,
+                            int64_t v_stride, const int64_t *slots, int64_t n_tokens, cudaStream_t stream);
+
+/*
+ * kvx_cache_attend -- attention of one new token of each request over its cached tokens in one layer.
+ * With the positions t of the last `window` (or all) of request r's seq_len[r] cached tokens:
+ *   s_t = scale * <q, key_t>,  lse = log sum_t exp(s_t),  out = sum_t exp(s_t - lse) value_t
+ * Position t is in block block_table[r * table_stride + t / block_size], so the token's own key and
+ * value are appended first. q: [n_reqs][n_q_heads][head_dim] with q_stride elements from one request to
+ * the next, out: [n_reqs][n_q_heads][v_dim] with out_stride, both in io_type, pointers and strides
+ * multiples of 16 bytes; lse: [n_reqs][n_q_heads] in 32 bits (the weight with which parts of a cache
+ * held in several pools join), or NULL. A request with no positions gets out 0 and lse -inf.
+ * seq_len beyond max_blocks * block_size is cut there, a negative one counts as 0, and positions in a
+ * block outside the pool are left out; kvx_cache_status reports each of these. KVX_EUNSUPPORTED for
+ * v_dim above 512. Unused slots may hold
+ * anything, NaN too. Products are taken in 16 bits with 32-bit sums; two calls on the same inputs give the
+ * same bits.
+ */
+kvx_status kvx_cache_attend(kvx_cache_t cache, int32_t layer, const void *q, int64_t q_stride,
+                            const int32_t *block_table, int64_t table_stride, int32_t max_blocks,
+                            const int32_t *seq_len, int32_t n_reqs, void *out, int64_t out_stride, float *lse,
+                            cudaStream_t stream);
+
+/* Waits for `stream` and returns KVX_ERANGE when an append or attend enqueued on the handle since the
+ * last call here skipped a slot, a block or a length out of bounds, else KVX_OK. */
+kvx_status kvx_cache_status(kvx_cache_t cache, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------------------------------
  * Connector state machine (host only; no CUDA call, usable without a GPU).
  *
  * The protocol around the push, one record per request id:
