@@ -1,0 +1,220 @@
+// What the attention kernels share: the warp matrix product, conversions, and the split of a batch's work
+// over the CTAs.
+#pragma once
+
+#include "kvx_internal.h"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace kvx {
+
+constexpr int kAttendWarps = 8;
+constexpr int kAttendThreads = 32 * kAttendWarps;
+constexpr uint32_t kNoRow = 0xffffffffu;      // offset of a position that is left out
+constexpr float kLn2 = 0.6931471805599453f;
+
+// D += A B, 16 x 8 x 16, 32-bit sums. bf16 values for KVX_BF16, else f16.
+template <int VT>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    if constexpr (VT == KVX_BF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transposes an 8 x 8 matrix of 16-bit elements held by the warp, two of a row per lane.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// Two 8-bit codes to two f16 values (exact).
+__device__ __forceinline__ uint32_t f16_of_codes(uint32_t two) {
+    uint32_t y;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"((uint16_t)two));
+    return y;
+}
+
+template <int VT> __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    uint32_t y;
+    if constexpr (VT == KVX_BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+    return y;
+}
+
+template <int VT> __device__ __forceinline__ float2 unpack(uint32_t x) {
+    if constexpr (VT == KVX_BF16) return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+    else return __half22float2(*reinterpret_cast<const __half2 *>(&x));
+}
+
+__device__ __forceinline__ float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 16 or 8 bytes of the cache, zeros where the position is left out. Volatile: issued where it stands, so that
+// the loads of the next tile are in flight during the products of this one.
+__device__ __forceinline__ void load_row(uint32_t (&x)[4], const uint8_t *p, bool ok) {
+    asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %5, 0;\nmov.u32 %0, 0;\nmov.u32 %1, 0;\nmov.u32 %2, 0;\nmov.u32 %3, 0;\n"
+                 "@p ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n}"
+                 : "=&r"(x[0]), "=&r"(x[1]), "=&r"(x[2]), "=&r"(x[3]) : "l"(p), "r"((uint32_t)ok));
+}
+__device__ __forceinline__ void load_row(uint32_t (&x)[2], const uint8_t *p, bool ok) {
+    asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %3, 0;\nmov.u32 %0, 0;\nmov.u32 %1, 0;\n"
+                 "@p ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];\n}"
+                 : "=&r"(x[0]), "=&r"(x[1]) : "l"(p), "r"((uint32_t)ok));
+}
+
+// ------------------------------------------------------------------------------------------------
+// The split of a batch. A segment is what one softmax runs over for one set of query heads: (request,
+// head set); its positions are cut into tiles. All segments' tiles stand in one line, requests in order,
+// and each CTA takes an equal stretch of it, so the load is level whatever the lengths. A segment that
+// crosses from one CTA to the next is joined from the CTAs' partial sums in the scratch by whichever CTA
+// finishes last, in the order of the line, so the result does not depend on which that is.
+// ------------------------------------------------------------------------------------------------
+
+struct Split {
+    int64_t tiles;        // in all
+    int32_t ctas;         // that have work, at least one tile each
+    __device__ __forceinline__ int64_t begin(int64_t cta) const { return cta * tiles / ctas; }
+    __device__ __forceinline__ int32_t cta_of(int64_t tile) const { return (int32_t)(((tile + 1) * ctas - 1) / tiles); }
+};
+
+// A request's live positions [first, len) and its tiles of TOK positions, aligned to TOK; at least one, so that an
+// empty request is answered too.
+template <int TOK> struct Span {
+    int32_t len, first, tiles;
+    __device__ __forceinline__ Span(const AttendArgs &a, int32_t r) {
+        const int64_t cap = (int64_t)a.max_blocks * a.pool.block_size;
+        len = (int32_t)min((int64_t)max(a.seq_len[r], 0), cap);
+        first = a.window ? max(0, len - a.window) : 0;
+        tiles = max(1, (int32_t)(((uint32_t)len + TOK - 1) / TOK) - first / TOK);
+    }
+};
+
+// Where a tile stands in the line.
+template <int TOK> struct Place {
+    int32_t r, seg, tile;      // request, segment of the request, tile of the segment
+    int64_t before;            // tiles of the requests before r, per segment
+    int32_t len, first, tiles;
+    __device__ __forceinline__ void request(const AttendArgs &a) {
+        const Span<TOK> s(a, r);
+        len = s.len;
+        first = s.first;
+        tiles = s.tiles;
+    }
+    __device__ __forceinline__ void next(const AttendArgs &a, int32_t segs) {
+        if (++tile < tiles) return;
+        tile = 0;
+        if (++seg < segs) return;
+        seg = 0;
+        before += tiles;
+        if (++r < a.n_reqs) request(a);
+    }
+    __device__ __forceinline__ int64_t seg_begin(int32_t segs) const { return before * segs + (int64_t)seg * tiles; }
+};
+
+__device__ __forceinline__ int64_t warp_inclusive(int64_t x) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(~0u, x, d);
+        if (lane >= d) x += o;
+    }
+    return x;
+}
+
+// Exclusive sum over the CTA's kAttendThreads threads and the total.
+__device__ __forceinline__ int64_t cta_exclusive(int64_t x, int64_t *total) {
+    __shared__ int64_t sums[kAttendWarps];
+    const int64_t s = warp_inclusive(x);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 31) sums[threadIdx.x >> 5] = s;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < kAttendWarps; ++i) {
+        if (i == (int)(threadIdx.x >> 5)) before = all;
+        all += sums[i];
+    }
+    *total = all;
+    return before + s - x;
+}
+
+// All threads: the split over gridDim.x CTAs (of at least min_tiles tiles), and the request in which this CTA's
+// stretch begins with the tiles before it.
+template <int TOK>
+__device__ __forceinline__ Split split_batch(const AttendArgs &a, int32_t segs, int32_t min_tiles, int32_t *r0, int64_t *before0) {
+    __shared__ int32_t s_r;
+    __shared__ int64_t s_before;
+    const int64_t cap = (int64_t)a.max_blocks * a.pool.block_size;
+    int64_t mine = 0, ex = 0, total = 0;
+    for (int32_t r = threadIdx.x; r < a.n_reqs; r += kAttendThreads) {
+        mine += Span<TOK>(a, r).tiles;
+        if (blockIdx.x == 0 && (a.seq_len[r] < 0 || a.seq_len[r] > cap)) atomicAdd(a.pool.skipped, 1ull);
+    }
+    ex = cta_exclusive(mine, &total);
+    Split s;
+    s.tiles = total * segs;
+    s.ctas = (int32_t)min((int64_t)gridDim.x, (s.tiles + min_tiles - 1) / min_tiles);
+    if ((int32_t)blockIdx.x >= s.ctas) return s;
+    const int64_t y = s.begin(blockIdx.x) / segs;
+    if (a.n_reqs <= kAttendThreads) {
+        if ((int32_t)threadIdx.x < a.n_reqs && ex <= y && y < ex + mine) {
+            s_r = threadIdx.x;
+            s_before = ex;
+        }
+    } else {
+        int64_t base = 0;
+        for (int32_t c = 0; c < a.n_reqs; c += kAttendThreads) {
+            const int32_t r = c + threadIdx.x;
+            mine = r < a.n_reqs ? Span<TOK>(a, r).tiles : 0;
+            ex = base + cta_exclusive(mine, &total);
+            if (ex <= y && y < ex + mine) {
+                s_r = r;
+                s_before = ex;
+            }
+            base += total;
+            if (base > y) break;
+        }
+    }
+    __syncthreads();
+    *r0 = s_r;
+    *before0 = s_before;
+    return s;
+}
+
+// Whole warp: the place of tile x of the line, found from a request at or before it.
+template <int TOK>
+__device__ __forceinline__ Place<TOK> locate(const AttendArgs &a, int32_t segs, int64_t x, int32_t r, int64_t before) {
+    const int lane = threadIdx.x & 31;
+    const int64_t y = x / segs;
+    for (;;) {
+        const int64_t n = r + lane < a.n_reqs ? Span<TOK>(a, r + lane).tiles : 0;
+        const int64_t in = before + warp_inclusive(n);
+        const uint32_t past = __ballot_sync(~0u, in > y);
+        const int at = past ? __ffs(past) - 1 : 31;
+        const int64_t to = __shfl_sync(~0u, in, at), here = __shfl_sync(~0u, n, at);
+        if (past) {
+            Place<TOK> p;
+            p.r = r + at;
+            p.before = to - here;
+            p.request(a);
+            const int64_t rest = x - p.before * segs;
+            p.seg = (int32_t)(rest / p.tiles);
+            p.tile = (int32_t)(rest - (int64_t)p.seg * p.tiles);
+            return p;
+        }
+        before = to;
+        r += 32;
+    }
+}
+
+}  // namespace kvx

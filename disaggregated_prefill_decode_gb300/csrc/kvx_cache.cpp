@@ -136,6 +136,7 @@ kvx_status kvx_cache_create(const kvx_pool *pool, const kvx_cache_config *cfg, k
         return fail(KVX_EUNSUPPORTED, "head rows of %lld bytes are not whole 16-byte vectors", (long long)g.head_bytes());
     if (g.block_size * g.row_bytes() > std::numeric_limits<int32_t>::max())
         return fail(KVX_EUNSUPPORTED, "blocks of 2^31 bytes or more");
+    if (g.buf_bytes() >= (int64_t)1 << 36) return fail(KVX_EUNSUPPORTED, "buffers of 64 GiB or more");
     for (void *p : base)
         if (!aligned16(p)) return fail(KVX_EUNSUPPORTED, "a buffer is not on a 16-byte boundary");
     if (f.window < 0) return fail(KVX_EINVAL, "window must be >= 0");
@@ -149,6 +150,8 @@ kvx_status kvx_cache_create(const kvx_pool *pool, const kvx_cache_config *cfg, k
     if (!f.v_scale) f.v_scale = latent ? f.k_scale : 1.0f;
     if (!std::isfinite(1.0f / f.k_scale) || !std::isfinite(1.0f / f.v_scale))
         return fail(KVX_EINVAL, "a scale has no finite inverse");
+    if (!std::isnormal((float)((double)f.scale * f.k_scale * 1.4426950408889634)))
+        return fail(KVX_EINVAL, "scale * k_scale is out of range");
     kvx_cache_s *c = new (std::nothrow) kvx_cache_s;
     if (!c) return fail(KVX_ENOMEM, "host allocation failed");
     c->g = g;
@@ -246,6 +249,13 @@ kvx_status kvx_cache_attend(kvx_cache_t c, int32_t layer, const void *q, int64_t
     a.window = f.window;
     a.scale = (float)((double)f.scale * (double)f.k_scale * 1.4426950408889634);
     a.v_scale = f.v_scale;
+    uint32_t shift = 0;
+    while (((uint64_t)1 << shift) < (uint64_t)g.block_size) ++shift;
+    a.block_shift = shift;
+    a.block_mul = (uint32_t)(((((uint64_t)1 << shift) - g.block_size) << 32) / g.block_size + 1);
+    a.block_pitch16 = (uint32_t)(a.pool.block_pitch / 16);
+    a.token_pitch16 = (uint32_t)(a.pool.token_pitch / 16);
+    a.latent = g.n_planes == 1;
     a.scratch = c->dev + 256;
     const cudaError_t e = launch_attend(a, f.value_type, f.io_type, c->sms, stream);
     return e == cudaSuccess ? KVX_OK : cuda_fail(e, "launching the attention");

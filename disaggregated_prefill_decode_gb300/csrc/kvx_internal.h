@@ -217,9 +217,15 @@ struct AttendArgs {
     int32_t n_q_heads, n_kv_heads, head_dim, v_dim, window;
     float scale;                      // of q . code, times log2(e)
     float v_scale;
-    uint8_t *scratch;                 // of the handle
+    uint32_t block_mul, block_shift;  // position / block_size = (mulhi(position, mul) + position) >> shift, below 2^31
+    uint32_t block_pitch16, token_pitch16;   // of the pool, in 16-byte units
+    bool latent;                      // one plane
+    uint8_t *scratch;                 // of the handle: counters (zero between calls), partial results
 };
+constexpr int32_t kScratchCounters = 4096;
+constexpr int32_t kPartialMax = 32 << 10;
 cudaError_t launch_attend(const AttendArgs &a, int32_t value_type, int32_t io_type, int32_t sms, cudaStream_t stream);
+cudaError_t launch_attend_latent(const AttendArgs &a, int32_t value_type, int32_t io_type, int32_t sms, cudaStream_t stream);
 size_t attend_scratch_bytes(int32_t sms);
 
 }  // namespace kvx

@@ -562,7 +562,7 @@ typedef struct kvx_cache_s *kvx_cache_t;
  * Refused: KVX_EINVAL for what contradicts the pool (types and elem_bytes, head counts, v_dim, negative
  * or non-finite values, reserved != 0), KVX_EUNSUPPORTED for more than 64 shards, 2^31 - 1 rows in a
  * buffer or more, head rows (head_dim * elem_bytes, and v_dim * elem_bytes) that are not whole 16-byte
- * vectors, buffers off a 16-byte boundary, head_dim above 256 (two planes) or 576 (one plane).
+ * vectors, buffers off a 16-byte boundary or of 64 GiB or more, head_dim above 256 (two planes) or 576 (one plane).
  * Calls on one handle use its scratch: their device work must not overlap (one stream, or ordered by
  * events). Handles are independent of one another; several may share a pool.
  */
