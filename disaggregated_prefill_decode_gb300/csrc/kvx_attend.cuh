@@ -9,8 +9,6 @@
 
 namespace kvx {
 
-constexpr int kAttendWarps = 8;
-constexpr int kAttendThreads = 32 * kAttendWarps;
 constexpr uint32_t kNoRow = 0xffffffffu;      // offset of a position that is left out
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -59,17 +57,21 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
-// 16 or 8 bytes of the cache, zeros where the position is left out. Volatile: issued where it stands, so that
-// the loads of the next tile are in flight during the products of this one.
-__device__ __forceinline__ void load_row(uint32_t (&x)[4], const uint8_t *p, bool ok) {
-    asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %5, 0;\nmov.u32 %0, 0;\nmov.u32 %1, 0;\nmov.u32 %2, 0;\nmov.u32 %3, 0;\n"
-                 "@p ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n}"
-                 : "=&r"(x[0]), "=&r"(x[1]), "=&r"(x[2]), "=&r"(x[3]) : "l"(p), "r"((uint32_t)ok));
+// Copies BYTES of the cache to shared memory in the background, zeros where the position is left out.
+template <int BYTES> __device__ __forceinline__ void copy_async(uint32_t to, const uint8_t *p, bool ok) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(p), "r"(ok ? 16 : 0) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(p), "r"(ok ? 8 : 0) : "memory");
 }
-__device__ __forceinline__ void load_row(uint32_t (&x)[2], const uint8_t *p, bool ok) {
-    asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %3, 0;\nmov.u32 %0, 0;\nmov.u32 %1, 0;\n"
-                 "@p ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];\n}"
-                 : "=&r"(x[0]), "=&r"(x[1]) : "l"(p), "r"((uint32_t)ok));
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void shared_read(uint32_t (&x)[4], uint32_t at) {
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void shared_read(uint32_t (&x)[2], uint32_t at) {
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "r"(at) : "memory");
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -80,11 +82,22 @@ __device__ __forceinline__ void load_row(uint32_t (&x)[2], const uint8_t *p, boo
 // finishes last, in the order of the line, so the result does not depend on which that is.
 // ------------------------------------------------------------------------------------------------
 
+// x / d, in 32 bits where they suffice.
+__device__ __forceinline__ int64_t divide(int64_t x, int32_t d) {
+    return (uint64_t)x >> 32 ? x / d : (int64_t)((uint32_t)x / (uint32_t)d);
+}
+
 struct Split {
     int64_t tiles;        // in all
     int32_t ctas;         // that have work, at least one tile each
-    __device__ __forceinline__ int64_t begin(int64_t cta) const { return cta * tiles / ctas; }
-    __device__ __forceinline__ int32_t cta_of(int64_t tile) const { return (int32_t)(((tile + 1) * ctas - 1) / tiles); }
+    int64_t each;         // tiles of a CTA; the first `more` CTAs have one more
+    int32_t more;
+    __device__ __forceinline__ int64_t begin(int32_t cta) const { return cta * each + min(cta, more); }
+    __device__ __forceinline__ int32_t cta_of(int64_t tile) const {
+        const int64_t large = more * (each + 1);
+        if (each >> 31) return (int32_t)(tile < large ? tile / (each + 1) : more + (tile - large) / each);
+        return (int32_t)(tile < large ? divide(tile, (int32_t)each + 1) : more + divide(tile - large, (int32_t)each));
+    }
 };
 
 // A request's live positions [first, len) and its tiles of TOK positions, aligned to TOK; at least one, so that an
@@ -131,16 +144,16 @@ __device__ __forceinline__ int64_t warp_inclusive(int64_t x) {
     return x;
 }
 
-// Exclusive sum over the CTA's kAttendThreads threads and the total.
-__device__ __forceinline__ int64_t cta_exclusive(int64_t x, int64_t *total) {
-    __shared__ int64_t sums[kAttendWarps];
+// Exclusive sum over the CTA's threads and the total.
+template <int WARPS> __device__ __forceinline__ int64_t cta_exclusive(int64_t x, int64_t *total) {
+    __shared__ int64_t sums[WARPS];
     const int64_t s = warp_inclusive(x);
     __syncthreads();
     if ((threadIdx.x & 31) == 31) sums[threadIdx.x >> 5] = s;
     __syncthreads();
     int64_t before = 0, all = 0;
 #pragma unroll
-    for (int i = 0; i < kAttendWarps; ++i) {
+    for (int i = 0; i < WARPS; ++i) {
         if (i == (int)(threadIdx.x >> 5)) before = all;
         all += sums[i];
     }
@@ -148,73 +161,105 @@ __device__ __forceinline__ int64_t cta_exclusive(int64_t x, int64_t *total) {
     return before + s - x;
 }
 
-// All threads: the split over gridDim.x CTAs (of at least min_tiles tiles), and the request in which this CTA's
-// stretch begins with the tiles before it.
-template <int TOK>
-__device__ __forceinline__ Split split_batch(const AttendArgs &a, int32_t segs, int32_t min_tiles, int32_t *r0, int64_t *before0) {
-    __shared__ int32_t s_r;
-    __shared__ int64_t s_before;
-    const int64_t cap = (int64_t)a.max_blocks * a.pool.block_size;
-    int64_t mine = 0, ex = 0, total = 0;
-    for (int32_t r = threadIdx.x; r < a.n_reqs; r += kAttendThreads) {
-        mine += Span<TOK>(a, r).tiles;
-        if (blockIdx.x == 0 && (a.seq_len[r] < 0 || a.seq_len[r] > cap)) atomicAdd(a.pool.skipped, 1ull);
-    }
-    ex = cta_exclusive(mine, &total);
-    Split s;
-    s.tiles = total * segs;
-    s.ctas = (int32_t)min((int64_t)gridDim.x, (s.tiles + min_tiles - 1) / min_tiles);
-    if ((int32_t)blockIdx.x >= s.ctas) return s;
-    const int64_t y = s.begin(blockIdx.x) / segs;
-    if (a.n_reqs <= kAttendThreads) {
-        if ((int32_t)threadIdx.x < a.n_reqs && ex <= y && y < ex + mine) {
-            s_r = threadIdx.x;
-            s_before = ex;
+// The batch as a CTA sees it: the split over gridDim.x CTAs (of at least a tile per warp), and how to find a place in it.
+// Up to 256 requests each warp keeps all the sums, a lane those of up to 8 consecutive requests, with no barrier; beyond that
+// the CTA looks for the request in which its own stretch begins, and its warps go on from there.
+template <int TOK, int WARPS> struct Batch {
+    static constexpr int PER = 8;
+    Split split;
+    int32_t per;                       // requests of a lane
+    int32_t tiles[PER];                // of each of them
+    int64_t upto;                      // tiles of this lane's requests and those before
+    int32_t r0;                        // beyond 256 requests: at or before this CTA's stretch, and the tiles before it
+    int64_t before0;
+
+    __device__ __forceinline__ Batch(const AttendArgs &a, int32_t segs) {
+        const int lane = threadIdx.x & 31;
+        const int64_t cap = (int64_t)a.max_blocks * a.pool.block_size;
+        int64_t total = 0;
+        per = (a.n_reqs + 31) / 32;
+        if (per <= PER) {
+            int64_t mine = 0;
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+                const int32_t r = lane * per + k;
+                tiles[k] = k < per && r < a.n_reqs ? Span<TOK>(a, r).tiles : 0;
+                mine += tiles[k];
+            }
+            upto = warp_inclusive(mine);
+            total = __shfl_sync(~0u, upto, 31);
+        } else {
+            int64_t mine = 0;
+            for (int32_t r = threadIdx.x; r < a.n_reqs; r += 32 * WARPS) mine += Span<TOK>(a, r).tiles;
+            cta_exclusive<WARPS>(mine, &total);
         }
-    } else {
-        int64_t base = 0;
-        for (int32_t c = 0; c < a.n_reqs; c += kAttendThreads) {
+        split.tiles = total * segs;
+        split.ctas = (int32_t)min((int64_t)gridDim.x, divide(split.tiles + WARPS - 1, WARPS));
+        split.each = divide(split.tiles, split.ctas);
+        split.more = (int32_t)(split.tiles - split.each * split.ctas);
+        if (blockIdx.x == 0)
+            for (int32_t r = threadIdx.x; r < a.n_reqs; r += 32 * WARPS)
+                if (a.seq_len[r] < 0 || a.seq_len[r] > cap) atomicAdd(a.pool.skipped, 1ull);
+        if (per > PER) find(a, divide(split.begin(blockIdx.x), segs));
+    }
+
+    // All threads: the request that holds tile y of the requests' line.
+    __device__ __forceinline__ void find(const AttendArgs &a, int64_t y) {
+        __shared__ int32_t s_r;
+        __shared__ int64_t s_before;
+        int64_t base = 0, total;
+        for (int32_t c = 0; c < a.n_reqs && base <= y; c += 32 * WARPS) {
             const int32_t r = c + threadIdx.x;
-            mine = r < a.n_reqs ? Span<TOK>(a, r).tiles : 0;
-            ex = base + cta_exclusive(mine, &total);
+            const int64_t mine = r < a.n_reqs ? Span<TOK>(a, r).tiles : 0, ex = base + cta_exclusive<WARPS>(mine, &total);
             if (ex <= y && y < ex + mine) {
                 s_r = r;
                 s_before = ex;
             }
             base += total;
-            if (base > y) break;
         }
+        __syncthreads();
+        r0 = s_r;
+        before0 = s_before;
     }
-    __syncthreads();
-    *r0 = s_r;
-    *before0 = s_before;
-    return s;
-}
 
-// Whole warp: the place of tile x of the line, found from a request at or before it.
-template <int TOK>
-__device__ __forceinline__ Place<TOK> locate(const AttendArgs &a, int32_t segs, int64_t x, int32_t r, int64_t before) {
-    const int lane = threadIdx.x & 31;
-    const int64_t y = x / segs;
-    for (;;) {
-        const int64_t n = r + lane < a.n_reqs ? Span<TOK>(a, r + lane).tiles : 0;
-        const int64_t in = before + warp_inclusive(n);
-        const uint32_t past = __ballot_sync(~0u, in > y);
-        const int at = past ? __ffs(past) - 1 : 31;
-        const int64_t to = __shfl_sync(~0u, in, at), here = __shfl_sync(~0u, n, at);
-        if (past) {
-            Place<TOK> p;
-            p.r = r + at;
-            p.before = to - here;
-            p.request(a);
-            const int64_t rest = x - p.before * segs;
-            p.seg = (int32_t)(rest / p.tiles);
-            p.tile = (int32_t)(rest - (int64_t)p.seg * p.tiles);
-            return p;
+    // Whole warp: the place of tile x of the line.
+    __device__ __forceinline__ Place<TOK> locate(const AttendArgs &a, int32_t segs, int64_t x) const {
+        const int lane = threadIdx.x & 31;
+        const int64_t y = divide(x, segs);
+        Place<TOK> p;
+        if (per <= PER) {
+            const int at = __ffs(__ballot_sync(~0u, upto > y)) - 1;
+            int64_t left = upto;
+            int32_t r = lane * per + per;
+#pragma unroll
+            for (int k = PER - 1; k >= 0; --k)
+                if (k < per && left > y) left -= tiles[k], --r;    // back to the request that holds y
+            p.r = __shfl_sync(~0u, r, at);
+            p.before = __shfl_sync(~0u, left, at);
+        } else {
+            int32_t r = r0;
+            int64_t before = before0;
+            for (;;) {
+                const int64_t n = r + lane < a.n_reqs ? Span<TOK>(a, r + lane).tiles : 0;
+                const int64_t in = before + warp_inclusive(n);
+                const uint32_t past = __ballot_sync(~0u, in > y);
+                const int at = past ? __ffs(past) - 1 : 31;
+                const int64_t to = __shfl_sync(~0u, in, at), here = __shfl_sync(~0u, n, at);
+                if (past) {
+                    p.r = r + at;
+                    p.before = to - here;
+                    break;
+                }
+                before = to;
+                r += 32;
+            }
         }
-        before = to;
-        r += 32;
+        p.request(a);
+        const int64_t rest = x - p.before * segs;
+        p.seg = (int32_t)divide(rest, p.tiles);
+        p.tile = (int32_t)(rest - (int64_t)p.seg * p.tiles);
+        return p;
     }
-}
+};
 
 }  // namespace kvx

@@ -1,0 +1,575 @@
+// kvx_cache_attend over separate key and value planes: the kernel, instantiated per value type in
+// kvx_attend_*.cu (latents: kvx_latent.cu).
+//
+// The softmax runs once over the positions with a running maximum m and sum l per query:
+//   m' = max(m, s), l' = l 2^(m - m') + 2^(s - m'), O' = O 2^(m - m') + 2^(s - m') v,
+// scores in units of log2. Bound by memory: each key and value is used by the queries of one KV head
+// only, 2 group flops per element, so all that counts is bytes in flight.
+//
+// A warp works alone on its stretch of tiles, with a ring of key and value tiles in shared memory that
+// asynchronous copies fill. A lane copies just the 16-byte pieces that it feeds to the matrix products
+// itself: S^T = K Q^T takes a lane's 16 bytes of a key row as the k elements of the product (the queries
+// are loaded in the same order of elements), and O^T = V^T P^T takes the bytes of two neighbouring
+// positions interleaved. So the ring needs no layout, no barrier and no bank is hit twice. Both products
+// have the 8 queries as their narrow side, so a group of up to 8 query heads wastes nothing that the
+// memory would wait for.
+#pragma once
+
+#include "kvx_attend.cuh"
+
+namespace kvx {
+
+constexpr int kSharedBytes = 226 << 10;       // of a CTA, one per SM
+
+template <int VT_, int IO_, int D_, int NT_, bool FULL_> struct Shape {
+    static constexpr int VT = VT_, IO = IO_, D = D_, NT = NT_;   // D: head_dim rounded up; NT: query sets of 8
+    static constexpr bool FULL = FULL_;                           // head_dim is D
+    static constexpr bool F8 = VT == KVX_E4M3;
+    static constexpr int MT = F8 ? KVX_F16 : VT;                  // type of the products
+    // 8-bit caches with bf16 outputs: f16 weights, whose unit is an eighth of the outputs', suffice. Else a weight is the sum
+    // of two 16-bit values, so that its rounding does not add to the outputs'.
+    static constexpr bool SPLIT = !(F8 && IO == KVX_BF16);
+    static constexpr int ESZ = F8 ? 1 : 2;
+    static constexpr int TOK = D * ESZ <= 128 ? 32 : 16;          // positions of a tile
+    static constexpr int SUB = TOK / 16;
+    static constexpr int KCH = D * ESZ / 64;                      // 64-byte chunks of a key row, 16 bytes a lane
+    static constexpr int KSTEP = F8 ? 4 : 2;                      // products per chunk
+    static constexpr int PIECE = D * ESZ / 8 < 16 ? 8 : 16;       // bytes of a value row a lane copies at once
+    static constexpr int NP = D * ESZ / 8 / PIECE;
+    static constexpr int PE = PIECE / ESZ;
+    static constexpr int NE = D / 8;                              // value elements of a lane
+    static constexpr int F4 = D / 16;                             // partial sums of a query set: float4 per lane
+    static constexpr int PARTIAL = NT * (F4 * 32 * 16 + 2 * 8 * 4);   // bytes of a partial result: O, m, l
+    static constexpr int WARPS = NT * D <= 128 ? 12 : 8;          // of the CTA: 168 or 255 registers a thread
+    static constexpr int THREADS = 32 * WARPS;
+    static constexpr int STAGE = TOK * D * ESZ;                   // one tile of keys or of values
+    static constexpr int ROOM = (kSharedBytes / WARPS - PARTIAL) / STAGE;
+    static constexpr int STAGES = ROOM < 6 ? ROOM : 6;            // of a warp's ring: keys and values in turn
+    static constexpr int AHEAD = STAGES / 2;                      // tiles whose keys are under way
+    static constexpr int RING = STAGES * STAGE;
+    static constexpr int WARP_BYTES = RING + PARTIAL;
+    static_assert(STAGES >= 2 && RING >= PARTIAL, "a warp's last partial result reuses its ring");
+    // value elements 2e and 2e + 1 of a lane in row group g are rows g and g + 8 of product e
+    static __device__ __forceinline__ int dim(int g, int e) { return e / PE * (8 * PE) + g * PE + e % PE; }
+};
+
+// A partial result in shared memory or in the scratch: O as [set][query of the lane's two][e / 4][lane] float4 of four
+// value elements, then m and l of the queries.
+template <class S> struct Partial {
+    float4 *o;
+    float *m, *l;
+    __device__ __forceinline__ explicit Partial(uint8_t *p)
+        : o((float4 *)p), m((float *)(p + S::NT * S::F4 * 512)), l(m + 8 * S::NT) {}
+};
+
+template <class S>
+__device__ __forceinline__ void write_lse(const AttendArgs &a, int32_t r, int32_t head, float m, float l) {
+    if (a.lse) a.lse[(int64_t)r * a.n_q_heads + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// One warp: float4 f of every lane of n partial results, `at(x)` the x-th (in shared memory, or put into the scratch by other
+// CTAs), joined into the outputs or into another partial result. Sixteen are read at once; lane (g, t) takes the maxima and
+// sums of two of them for its query, the others' weights come by shuffles.
+template <class S, bool SCRATCH, class At>
+__device__ __forceinline__ void join(const AttendArgs &a, int f, int n, At at, bool final, uint8_t *to, int32_t r, int32_t head0,
+                                     int32_t heads) {
+    const int lane = threadIdx.x & 31, t = lane & 3, g = lane >> 2;
+    const int set = f / S::F4, i = f % S::F4 / (S::F4 / 2), e4 = f % (S::F4 / 2), q = set * 8 + 2 * t + i;
+    auto get = [](const auto *p) {
+        if constexpr (SCRATCH) return __ldcg(p);
+        else return *p;
+    };
+    float top = -INFINITY, l = 0.0f;
+    float4 o = make_float4(0, 0, 0, 0);
+    for (int x0 = 0; x0 < n; x0 += 16) {
+        float4 y[16];
+        float m[2], s[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const bool in = x0 + 8 * k + g < n;
+            const Partial<S> p(at(in ? x0 + 8 * k + g : 0));
+            m[k] = in ? get(p.m + q) : -INFINITY;
+            s[k] = in ? get(p.l + q) : 0.0f;
+        }
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+            y[x] = x0 + x < n ? get(Partial<S>(at(x0 + x)).o + f * 32 + lane) : make_float4(0, 0, 0, 0);
+        float up = fmaxf(m[0], m[1]);
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) up = fmaxf(up, __shfl_xor_sync(~0u, up, d));
+        up = fmaxf(up, top);
+        const float ref = up == -INFINITY ? 0.0f : up, old = fast_exp2(top - ref);
+        top = up;
+        m[0] = fast_exp2(m[0] - ref);
+        m[1] = fast_exp2(m[1] - ref);
+        l = l * old + m[0] * s[0] + m[1] * s[1];
+        o = make_float4(o.x * old, o.y * old, o.z * old, o.w * old);
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+            const float w = __shfl_sync(~0u, m[x >> 3], (x & 7) * 4 + t);
+            o.x += w * y[x].x;
+            o.y += w * y[x].y;
+            o.z += w * y[x].z;
+            o.w += w * y[x].w;
+        }
+    }
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(~0u, l, d);
+    if (final) {
+        const int d = S::dim(g, e4 * 4);
+        if (q < heads && (S::FULL || d < a.head_dim)) {
+            const float inv = l == 0.0f ? 0.0f : a.v_scale / l;
+            const uint2 y = make_uint2(pack<S::IO>(o.x * inv, o.y * inv), pack<S::IO>(o.z * inv, o.w * inv));
+            *reinterpret_cast<uint2 *>(a.out + r * a.out_stride + ((int64_t)(head0 + q) * a.head_dim + d) * 2) = y;
+        }
+        if (q < heads && e4 == 0 && g == 0) write_lse<S>(a, r, head0 + q, top, l);
+    } else {
+        const Partial<S> p(to);
+        __stcg(p.o + f * 32 + lane, o);
+        if (e4 == 0 && g == 0) {
+            __stcg(p.m + q, top);
+            __stcg(p.l + q, l);
+        }
+    }
+}
+
+// Offset, in 16-byte units, of the position `lane` of a tile in its buffer; kNoRow for a position that is left out. In two
+// steps, so that other loads can start before the block id is waited for.
+template <int TOK> struct Row {
+    uint32_t rest;                                                 // within the block, in 16-byte units
+    int32_t blk;                                                   // -2: no live position
+    __device__ __forceinline__ Row(const AttendArgs &a, const Place<TOK> &p) : rest(0), blk(-2) {
+        const int lane = threadIdx.x & 31;
+        const uint32_t pos = (uint32_t)p.first / TOK * TOK + (uint32_t)p.tile * TOK + lane;
+        if (lane >= TOK || pos < (uint32_t)p.first || pos >= (uint32_t)p.len) return;
+        const uint32_t col = (__umulhi(pos, a.block_mul) + pos) >> a.block_shift;
+        blk = max(a.block_table[p.r * a.table_stride + col], -1);
+        rest = (pos - col * (uint32_t)a.pool.block_size) * a.token_pitch16;
+    }
+    __device__ __forceinline__ uint32_t offset(const AttendArgs &a, bool report) const {
+        if (blk >= 0 && blk < a.pool.n_blocks) return (uint32_t)blk * a.block_pitch16 + rest;
+        if (blk != -2 && report) atomicAdd(a.pool.skipped, 1ull);
+        return kNoRow;
+    }
+};
+
+template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_planes(const __grid_constant__ AttendArgs a) {
+    constexpr int TOK = S::TOK, NT = S::NT;
+    extern __shared__ __align__(16) uint8_t smem[];                // [warp] ring and partial result
+    __shared__ int64_t s_seg[S::WARPS][2];                     // first tile of each one's segment; -1: none
+    __shared__ int32_t s_where[S::WARPS][2][3];                // request, segment of the request, tiles
+    __shared__ bool s_last[2];
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int32_t group = a.n_q_heads / a.n_kv_heads, sets = (group + 8 * NT - 1) / (8 * NT), segs = a.n_kv_heads * sets;
+
+    const Batch<TOK, S::WARPS> batch(a, segs);
+    const Split &split = batch.split;
+    if ((int32_t)blockIdx.x >= split.ctas) return;
+    uint32_t *const arrived = (uint32_t *)a.scratch;
+    uint8_t *const cta_parts = a.scratch + kScratchCounters * sizeof(uint32_t);             // [CTA][2]
+    const int64_t c_begin = split.begin(blockIdx.x), c_end = split.begin(blockIdx.x + 1);
+    const int64_t per = (c_end - c_begin) / S::WARPS, more = (c_end - c_begin) % S::WARPS;   // warps without work come last
+    const int64_t x0 = c_begin + w * per + min((int64_t)w, more), x1 = x0 + per + (w < more);
+    if (lane < 2) s_seg[w][lane] = -1;
+    __syncwarp();
+
+    if (x0 < x1) {
+        const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem + w * S::WARP_BYTES);
+        uint32_t q[NT][S::KCH * S::KSTEP][2];
+        float o[NT][S::NE / 2][4], m[NT][2], l[NT][2], sc[NT][2];
+        Place<TOK> cur = batch.locate(a, segs, x0), far = cur;
+        const uint8_t *k_ptr, *v_ptr;                              // this lane's bytes of row 0 of the head
+
+        auto pointers = [&](const Place<TOK> &p) {
+            const int32_t kvh = p.seg / sets, shard = kvh / a.pool.heads_per_shard;
+            const int64_t off = (int64_t)(kvh - shard * a.pool.heads_per_shard) * a.pool.head_pitch;
+            k_ptr = a.pool.k[shard] + off + t * 16;
+            v_ptr = a.pool.v[shard] + off + g * S::PIECE;
+        };
+        auto load_k = [&](uint32_t row, int stage) {
+            const uint32_t to = ring + stage * S::STAGE + lane * 16;
+#pragma unroll
+            for (int s = 0; s < S::SUB; ++s)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t x = __shfl_sync(~0u, row, s * 16 + h * 8 + g);
+                    const uint8_t *p = x == kNoRow ? k_ptr : k_ptr + (uint64_t)x * 16;
+#pragma unroll
+                    for (int c = 0; c < S::KCH; ++c)
+                        copy_async<16>(to + ((s * S::KCH + c) * 2 + h) * 512, p + c * 64, x != kNoRow && (S::FULL || c * 64 + t * 16 < a.head_dim * S::ESZ));
+                }
+        };
+        auto load_v = [&](uint32_t row, int stage) {
+            const uint32_t to = ring + stage * S::STAGE + lane * S::PIECE;
+#pragma unroll
+            for (int s = 0; s < S::SUB; ++s)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {                      // positions 2t, 2t + 1, 2t + 8, 2t + 9
+                    const uint32_t x = __shfl_sync(~0u, row, s * 16 + 2 * t + (j & 1) + (j >> 1) * 8);
+                    const uint8_t *p = x == kNoRow ? v_ptr : v_ptr + (uint64_t)x * 16;
+#pragma unroll
+                    for (int c = 0; c < S::NP; ++c)
+                        copy_async<S::PIECE>(to + ((s * 4 + j) * S::NP + c) * 32 * S::PIECE, p + c * 8 * S::PIECE,
+                                             x != kNoRow && (S::FULL || (c * 8 + g) * S::PIECE < a.head_dim * S::ESZ));
+                }
+        };
+        // Queries of a segment. 8-bit caches multiply in f16: a bf16 row is brought by a power of two to where f16 holds
+        // its elements exactly down to 2^-33 of the largest.
+        auto load_q = [&](const Place<TOK> &p) {
+            const int32_t kvh = p.seg / sets, first = p.seg % sets * 8 * NT;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int32_t qi = first + n * 8 + g;
+                const uint8_t *src = a.q + p.r * a.q_stride + ((int64_t)kvh * group + qi) * a.head_dim * 2;
+#pragma unroll
+                for (int c = 0; c < S::KCH; ++c)
+#pragma unroll
+                    for (int h = 0; h < S::KSTEP / 2; ++h) {
+                        const int d = (c * 64 + t * 16) / S::ESZ + h * 8;
+                        uint4 x = make_uint4(0, 0, 0, 0);
+                        if (qi < group && (S::FULL || d < a.head_dim)) x = __ldg(reinterpret_cast<const uint4 *>(src + d * 2));
+                        uint32_t *y = &q[n][c * S::KSTEP + h * 2][0];
+                        y[0] = x.x;
+                        y[1] = x.y;
+                        y[2] = x.z;
+                        y[3] = x.w;
+                    }
+                float scale = a.scale;
+                if constexpr (S::F8 && S::IO == KVX_BF16) {
+                    uint32_t *y = &q[n][0][0];
+                    float top = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < S::KCH * S::KSTEP * 2; ++i) {
+                        const float2 f = unpack<KVX_BF16>(y[i]);
+                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+                    top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+                    const int e = top > 0.0f && top < INFINITY ? max(-100, min(100, 14 - ilogbf(top))) : 0;
+                    const float up = __int_as_float((127 + e) << 23);
+                    scale *= __int_as_float((127 - e) << 23);
+#pragma unroll
+                    for (int i = 0; i < S::KCH * S::KSTEP * 2; ++i) {
+                        const float2 f = unpack<KVX_BF16>(y[i]);
+                        y[i] = pack<KVX_F16>(f.x * up, f.y * up);
+                    }
+                }
+                sc[n][0] = __shfl_sync(~0u, scale, 8 * t);         // of queries 2t and 2t + 1
+                sc[n][1] = __shfl_sync(~0u, scale, 8 * t + 4);
+                m[n][0] = m[n][1] = -INFINITY;
+                l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+                for (int e = 0; e < S::NE / 2; ++e) o[n][e][0] = o[n][e][1] = o[n][e][2] = o[n][e][3] = 0.0f;
+            }
+        };
+        // The end of this warp's part of a segment, [from, to) of the line: outputs if it is the whole of it, else a partial result.
+        auto flush = [&](const Place<TOK> &p, int64_t from, int64_t to) {
+            const int64_t begin = p.seg_begin(segs);
+            const int32_t kvh = p.seg / sets, first = p.seg % sets * 8 * NT;
+            const bool whole = from == begin && to == begin + p.tiles;
+            const int slot = from == begin;                        // 1: the warp's last, with nothing left in its ring
+            if (!whole && lane == 0) {
+                s_seg[w][slot] = begin;
+                s_where[w][slot][0] = p.r;
+                s_where[w][slot][1] = p.seg;
+                s_where[w][slot][2] = p.tiles;
+            }
+            const Partial<S> part(smem + w * S::WARP_BYTES + (slot ? 0 : S::RING));
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) l[n][i] += __shfl_xor_sync(~0u, l[n][i], d);
+                if (whole) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int32_t qi = first + n * 8 + 2 * t + i, head = kvh * group + qi;
+                        if (qi >= group) continue;
+                        const float inv = l[n][i] == 0.0f ? 0.0f : a.v_scale / l[n][i];
+                        uint8_t *dst = a.out + p.r * a.out_stride + (int64_t)head * a.head_dim * 2;
+#pragma unroll
+                        for (int e = 0; e < S::NE / 2; e += 2) {
+                            const int d = S::dim(g, 2 * e);
+                            if (S::FULL || d < a.head_dim)
+                                *reinterpret_cast<uint2 *>(dst + d * 2) = make_uint2(pack<S::IO>(o[n][e][i] * inv, o[n][e][2 + i] * inv),
+                                                                                     pack<S::IO>(o[n][e + 1][i] * inv, o[n][e + 1][2 + i] * inv));
+                        }
+                        if (g == 0) write_lse<S>(a, p.r, head, m[n][i], l[n][i]);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int e = 0; e < S::NE / 2; e += 2)
+                            part.o[((n * 2 + i) * (S::F4 / 2) + e / 2) * 32 + lane] =
+                                make_float4(o[n][e][i], o[n][e][2 + i], o[n][e + 1][i], o[n][e + 1][2 + i]);
+                    if (g == 0)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            part.m[n * 8 + 2 * t + i] = m[n][i];
+                            part.l[n * 8 + 2 * t + i] = l[n][i];
+                        }
+                }
+            }
+        };
+
+        // Tiles' keys and values go round the ring in turn, K_0 V_0 K_1 V_1 ...; whenever one is consumed the copy STAGES - 1
+        // after it starts. rows[n]: offsets of the tile n after this one; `far` is tile AHEAD after this one.
+        constexpr bool ODD = S::STAGES % 2;
+        uint32_t rows[S::AHEAD + 1];
+        const int64_t n_tiles = x1 - x0;
+        pointers(far);
+#pragma unroll
+        for (int n = 0; n < S::AHEAD; ++n) {
+            rows[n] = kNoRow;
+            if (n < n_tiles) {
+                const Row<TOK> row(a, far);
+                if (n == 0) load_q(cur);
+                else if (far.tile == 0) pointers(far);
+                rows[n] = row.offset(a, far.seg == 0);
+                load_k(rows[n], 2 * n);
+                copies_commit();
+                if (ODD || n + 1 < S::AHEAD) load_v(rows[n], 2 * n + 1);
+                far.next(a, segs);
+            } else copies_commit();
+            if (ODD || n + 1 < S::AHEAD) copies_commit();
+        }
+        int64_t from = x0;
+        int stage = 0;                                             // of this tile's keys
+        for (int64_t i = 0; i < n_tiles; ++i) {
+            const bool ahead = i + S::AHEAD < n_tiles;
+            rows[S::AHEAD] = ahead ? Row<TOK>(a, far).offset(a, far.seg == 0) : kNoRow;
+            const int v_stage = stage + 1 == S::STAGES ? 0 : stage + 1, before = stage ? stage - 1 : S::STAGES - 1;
+
+            copies_wait<S::STAGES - 2>();
+            if constexpr (ODD) {
+                if (ahead) {
+                    if (far.tile == 0) pointers(far);
+                    load_k(rows[S::AHEAD], before);
+                }
+            } else if (i + S::AHEAD - 1 < n_tiles) load_v(rows[S::AHEAD - 1], before);
+            copies_commit();
+            float s[NT][S::SUB][4];
+#pragma unroll
+            for (int u = 0; u < S::SUB; ++u) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) s[n][u][0] = s[n][u][1] = s[n][u][2] = s[n][u][3] = 0.0f;
+#pragma unroll
+                for (int c = 0; c < S::KCH; ++c) {
+                    uint32_t k[2][4];
+                    shared_read(k[0], ring + stage * S::STAGE + ((u * S::KCH + c) * 2 + 0) * 512 + lane * 16);
+                    shared_read(k[1], ring + stage * S::STAGE + ((u * S::KCH + c) * 2 + 1) * 512 + lane * 16);
+#pragma unroll
+                    for (int i = 0; i < S::KSTEP; ++i) {
+                        uint32_t a0, a1, a2, a3;
+                        if constexpr (S::F8) {
+                            a0 = f16_of_codes(k[0][i]), a2 = f16_of_codes(k[0][i] >> 16);
+                            a1 = f16_of_codes(k[1][i]), a3 = f16_of_codes(k[1][i] >> 16);
+                        } else {
+                            a0 = k[0][2 * i], a2 = k[0][2 * i + 1], a1 = k[1][2 * i], a3 = k[1][2 * i + 1];
+                        }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            mma<S::MT>(s[n][u], a0, a1, a2, a3, q[n][c * S::KSTEP + i][0], q[n][c * S::KSTEP + i][1]);
+                    }
+                }
+            }
+            copies_wait<S::STAGES - 2>();
+            if (ahead) {
+                if constexpr (ODD) load_v(rows[S::AHEAD], stage);
+                else {
+                    if (far.tile == 0) pointers(far);
+                    load_k(rows[S::AHEAD], stage);
+                }
+                far.next(a, segs);
+            }
+            copies_commit();
+            uint32_t p_hi[NT][S::SUB][2], p_lo[NT][S::SUB][2];
+            if (__any_sync(~0u, lane < TOK && rows[0] == kNoRow)) {
+#pragma unroll
+                for (int u = 0; u < S::SUB; ++u)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (__shfl_sync(~0u, rows[0], u * 16 + h * 8 + g) == kNoRow)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) s[n][u][2 * h] = s[n][u][2 * h + 1] = -INFINITY;
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float old[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float top = fmaxf(s[n][0][i], s[n][0][2 + i]);
+#pragma unroll
+                    for (int u = 1; u < S::SUB; ++u) top = fmaxf(top, fmaxf(s[n][u][i], s[n][u][2 + i]));
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+                    top = fmaxf(m[n][i], top * sc[n][i]);
+                    const float ref = top == -INFINITY ? 0.0f : top;
+                    old[i] = fast_exp2(m[n][i] - ref);
+                    m[n][i] = top;
+                    l[n][i] *= old[i];
+#pragma unroll
+                    for (int u = 0; u < S::SUB; ++u)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float p = fast_exp2(fmaf(s[n][u][2 * h + i], sc[n][i], -ref));
+                            s[n][u][2 * h + i] = p;
+                            l[n][i] += p;
+                        }
+                }
+                if (__any_sync(~0u, old[0] != 1.0f || old[1] != 1.0f)) {
+#pragma unroll
+                    for (int e = 0; e < S::NE / 2; ++e) {
+                        o[n][e][0] *= old[0];
+                        o[n][e][1] *= old[1];
+                        o[n][e][2] *= old[0];
+                        o[n][e][3] *= old[1];
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < S::SUB; ++u)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float p0 = s[n][u][2 * h], p1 = s[n][u][2 * h + 1];
+                        const uint32_t hi = pack<S::MT>(p0, p1);
+                        p_hi[n][u][h] = transpose8x8(hi);
+                        if constexpr (S::SPLIT) {
+                            const float2 f = unpack<S::MT>(hi);
+                            p_lo[n][u][h] = transpose8x8(pack<S::MT>(p0 - f.x, p1 - f.y));
+                        }
+                    }
+            }
+#pragma unroll
+            for (int u = 0; u < S::SUB; ++u)
+#pragma unroll
+                for (int c = 0; c < S::NP; ++c) {
+                    uint32_t v[4][S::PIECE / 4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        shared_read(v[j], ring + v_stage * S::STAGE + (((u * 4 + j) * S::NP + c) * 32 + lane) * S::PIECE);
+#pragma unroll
+                    for (int e = 0; e < S::PE / 2; ++e) {
+                        uint32_t av[4];                             // element 2e, element 2e + 1; the same 8 positions on
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            if constexpr (S::F8) {
+                                const uint32_t x = __byte_perm(v[2 * j][e / 2], v[2 * j + 1][e / 2], e & 1 ? 0x7362 : 0x5140);
+                                av[2 * j] = f16_of_codes(x);
+                                av[2 * j + 1] = f16_of_codes(x >> 16);
+                            } else {
+                                av[2 * j] = __byte_perm(v[2 * j][e], v[2 * j + 1][e], 0x5410);
+                                av[2 * j + 1] = __byte_perm(v[2 * j][e], v[2 * j + 1][e], 0x7632);
+                            }
+                        }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            mma<S::MT>(o[n][c * (S::PE / 2) + e], av[0], av[1], av[2], av[3], p_hi[n][u][0], p_hi[n][u][1]);
+                            if constexpr (S::SPLIT)
+                                mma<S::MT>(o[n][c * (S::PE / 2) + e], av[0], av[1], av[2], av[3], p_lo[n][u][0], p_lo[n][u][1]);
+                        }
+                    }
+                }
+            const bool last = i + 1 == n_tiles;
+            if (cur.tile + 1 == cur.tiles || last) {
+                flush(cur, from, x0 + i + 1);
+                from = x0 + i + 1;
+            }
+            if (!last) {
+                cur.next(a, segs);
+                if (cur.tile == 0) load_q(cur);
+            }
+#pragma unroll
+            for (int n = 0; n < S::AHEAD; ++n) rows[n] = rows[n + 1];
+            stage = v_stage + 1 == S::STAGES ? 0 : v_stage + 1;
+        }
+    }
+    __syncthreads();
+
+    // Segments whose pieces several warps hold, in order: the second of one warp, the first ones of those after it. Each warp joins
+    // some float4s of some of them. At most two go on in other CTAs: one that began before this one's stretch, one that ends after it.
+    auto heads_of = [&](int32_t seg, int32_t *head0) {
+        const int32_t first = seg % sets * 8 * NT;
+        *head0 = seg / sets * group + first;
+        return min(group - first, 8 * NT);
+    };
+    constexpr int FS = NT * S::F4;
+    static_assert(2 * S::WARPS <= 32, "a lane per piece");
+    const int64_t my_seg = lane < 2 * S::WARPS ? s_seg[lane >> 1][lane & 1] : -1;
+    const uint32_t pieces = __ballot_sync(~0u, my_seg >= 0), lower = pieces & ((1u << lane) - 1);
+    const int64_t prev_seg = __shfl_sync(~0u, my_seg, lower ? 31 - __clz(lower) : lane);
+    const bool leads = my_seg >= 0 && (!lower || prev_seg != my_seg);
+    uint32_t leaders = __ballot_sync(~0u, leads);                  // the first piece of each segment
+    int my_open = 0;                                               // 1: begun before, 2: goes on after this CTA
+    if (leads) my_open = my_seg < c_begin ? 1 : my_seg + s_where[lane >> 1][lane & 1][2] > c_end ? 2 : 0;
+    const uint32_t open1 = __ballot_sync(~0u, my_open == 1), open2 = __ballot_sync(~0u, my_open == 2);
+    const int open[2] = {__ffs(open1) - 1, __ffs(open2) - 1};
+    for (int task = w; leaders; task -= FS, leaders &= leaders - 1) {
+        if (task >= FS) continue;
+        const int i = __ffs(leaders) - 1;
+        const uint32_t rest = leaders & (leaders - 1);
+        const int n = __popc(pieces & (rest ? (1u << (__ffs(rest) - 1)) - 1 : ~0u) & ~((1u << i) - 1));
+        const int32_t *where = s_where[i >> 1][i & 1];
+        const int side = i == open[1];
+        int32_t head0;
+        const int32_t heads = heads_of(where[1], &head0);
+        auto at = [&](int x) { return smem + ((i >> 1) + x) * S::WARP_BYTES + (x || !(i & 1) ? S::RING : 0); };
+        for (; task < FS; task += S::WARPS)
+            join<S, false>(a, task, n, at, i != open[0] && i != open[1], cta_parts + (size_t)(blockIdx.x * 2 + side) * S::PARTIAL, where[0],
+                           head0, heads);
+    }
+    if (open[0] < 0 && open[1] < 0) return;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x < 2) {
+        const int i = open[threadIdx.x];
+        s_last[threadIdx.x] = false;
+        if (i >= 0) {
+            const int64_t seg = s_seg[i >> 1][i & 1];
+            const int32_t from = split.cta_of(seg), upto = split.cta_of(seg + s_where[i >> 1][i & 1][2] - 1);
+            const bool last = atomicAdd(arrived + from, 1u) == (uint32_t)(upto - from);
+            if (last) arrived[from] = 0;                           // for the next call
+            s_last[threadIdx.x] = last;
+            __threadfence();
+        }
+    }
+    __syncthreads();
+    for (int k = 0; k < 2; ++k) {
+        if (!s_last[k]) continue;
+        const int i = open[k];
+        const int64_t seg = s_seg[i >> 1][i & 1];
+        const int32_t *where = s_where[i >> 1][i & 1];
+        const int32_t from = split.cta_of(seg), n = split.cta_of(seg + where[2] - 1) - from + 1;
+        int32_t head0;
+        const int32_t heads = heads_of(where[1], &head0);
+        for (int f = w; f < FS; f += S::WARPS)
+            join<S, true>(a, f, n, [&](int x) { return cta_parts + (size_t)((from + x) * 2 + (x == 0)) * S::PARTIAL; }, true, nullptr, where[0],
+                          head0, heads);
+    }
+}
+
+// ------------------------------------------------------------------------------------------------
+
+template <class S> static cudaError_t launch(const AttendArgs &a, int32_t sms, cudaStream_t stream) {
+    constexpr int bytes = S::WARPS * S::WARP_BYTES;
+    static const cudaError_t set = cudaFuncSetAttribute(kvx_attend_planes<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (set != cudaSuccess) return set;
+    kvx_attend_planes<S><<<sms, S::THREADS, bytes, stream>>>(a);
+    count_launch();
+    return cudaGetLastError();
+}
+
+template <int VT, int IO, int D, int NT> static cudaError_t launch(const AttendArgs &a, int32_t sms, cudaStream_t stream) {
+    return a.head_dim == D ? launch<Shape<VT, IO, D, NT, true>>(a, sms, stream) : launch<Shape<VT, IO, D, NT, false>>(a, sms, stream);
+}
+
+// Head dims are rounded up to 64, 128 or 256; more than 8 query heads to a KV head are taken 16 at a time.
+template <int VT, int IO> static cudaError_t launch_planes(const AttendArgs &a, int32_t sms, cudaStream_t stream) {
+    const bool wide = a.n_q_heads / a.n_kv_heads > 8;
+    if (a.head_dim <= 64) return wide ? launch<VT, IO, 64, 2>(a, sms, stream) : launch<VT, IO, 64, 1>(a, sms, stream);
+    if (a.head_dim <= 128) return wide ? launch<VT, IO, 128, 2>(a, sms, stream) : launch<VT, IO, 128, 1>(a, sms, stream);
+    return launch<VT, IO, 256, 1>(a, sms, stream);
+}
+
+}  // namespace kvx

@@ -223,8 +223,12 @@ struct AttendArgs {
     uint8_t *scratch;                 // of the handle: counters (zero between calls), partial results
 };
 constexpr int32_t kScratchCounters = 4096;
-constexpr int32_t kPartialMax = 32 << 10;
+constexpr int32_t kScratchPerSm = 84 << 10;
 cudaError_t launch_attend(const AttendArgs &a, int32_t value_type, int32_t io_type, int32_t sms, cudaStream_t stream);
+cudaError_t launch_attend_bf16(const AttendArgs &a, int32_t sms, cudaStream_t stream);
+cudaError_t launch_attend_f16(const AttendArgs &a, int32_t sms, cudaStream_t stream);
+cudaError_t launch_attend_e4m3_bf16(const AttendArgs &a, int32_t sms, cudaStream_t stream);
+cudaError_t launch_attend_e4m3_f16(const AttendArgs &a, int32_t sms, cudaStream_t stream);
 cudaError_t launch_attend_latent(const AttendArgs &a, int32_t value_type, int32_t io_type, int32_t sms, cudaStream_t stream);
 size_t attend_scratch_bytes(int32_t sms);
 
