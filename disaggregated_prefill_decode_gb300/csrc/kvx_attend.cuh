@@ -57,12 +57,9 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
-// Copies BYTES of the cache to shared memory in the background, zeros where the position is left out.
-template <int BYTES> __device__ __forceinline__ void copy_async(uint32_t to, const uint8_t *p, bool ok) {
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(p), "r"(ok ? 16 : 0) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(p), "r"(ok ? 8 : 0) : "memory");
+// Copies 16 bytes of the cache to shared memory in the background, zeros where the position is left out.
+__device__ __forceinline__ void copy_async(uint32_t to, const uint8_t *p, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(p), "r"(ok ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }

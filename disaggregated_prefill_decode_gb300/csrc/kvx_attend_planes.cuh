@@ -6,13 +6,12 @@
 // scores in units of log2. Bound by memory: each key and value is used by the queries of one KV head
 // only, 2 group flops per element, so all that counts is bytes in flight.
 //
-// A warp works alone on its stretch of tiles, with a ring of key and value tiles in shared memory that
-// asynchronous copies fill. A lane copies just the 16-byte pieces that it feeds to the matrix products
-// itself: S^T = K Q^T takes a lane's 16 bytes of a key row as the k elements of the product (the queries
-// are loaded in the same order of elements), and O^T = V^T P^T takes the bytes of two neighbouring
-// positions interleaved. So the ring needs no layout, no barrier and no bank is hit twice. Both products
-// have the 8 queries as their narrow side, so a group of up to 8 query heads wastes nothing that the
-// memory would wait for.
+// A warp works alone on its stretch of tiles, with a ring of tiles (keys and values of 16 or 32 positions)
+// in shared memory that asynchronous copies fill. S^T = K Q^T takes 16 bytes of a key row as the k
+// elements that a lane gives to the products (the queries are loaded in the same order of elements), and
+// O^T = V^T P^T takes the bytes of two neighbouring positions interleaved, so every lane reads the ring in
+// pieces of 16 bytes and the pieces are swizzled for that alone. Both products have the 8 queries as their
+// narrow side, so a group of up to 8 query heads wastes nothing that the memory would wait for.
 #pragma once
 
 #include "kvx_attend.cuh"
@@ -40,15 +39,23 @@ template <int VT_, int IO_, int D_, int NT_, bool FULL_> struct Shape {
     static constexpr int NE = D / 8;                              // value elements of a lane
     static constexpr int F4 = D / 16;                             // partial sums of a query set: float4 per lane
     static constexpr int PARTIAL = NT * (F4 * 32 * 16 + 2 * 8 * 4);   // bytes of a partial result: O, m, l
-    static constexpr int WARPS = NT * D <= 128 ? 12 : 8;          // of the CTA: 168 or 255 registers a thread
+    static constexpr int WARPS = D > 128 ? 4 : 8;                 // of the CTA, 255 registers a thread
     static constexpr int THREADS = 32 * WARPS;
-    static constexpr int STAGE = TOK * D * ESZ;                   // one tile of keys or of values
-    static constexpr int ROOM = (kSharedBytes / WARPS - PARTIAL) / STAGE;
-    static constexpr int STAGES = ROOM < 6 ? ROOM : 6;            // of a warp's ring: keys and values in turn
-    static constexpr int AHEAD = STAGES / 2;                      // tiles whose keys are under way
-    static constexpr int RING = STAGES * STAGE;
-    static constexpr int WARP_BYTES = RING + PARTIAL;
-    static_assert(STAGES >= 2 && RING >= PARTIAL, "a warp's last partial result reuses its ring");
+    static constexpr int RP = D * ESZ / 16;                       // 16-byte pieces of a row
+    static constexpr int PLANE = TOK * D * ESZ, STAGE = 2 * PLANE;   // a tile: keys, then values
+    static constexpr int ROOM = kSharedBytes / WARPS;
+    static constexpr bool SLOT = (ROOM - PARTIAL) / STAGE >= 3;   // room for a partial result beside the ring
+    static constexpr int STAGES = (ROOM - (SLOT ? PARTIAL : 0)) / STAGE < 6 ? (ROOM - (SLOT ? PARTIAL : 0)) / STAGE : 6;
+    static constexpr int RING = STAGES * STAGE, WARP_BYTES = RING + (SLOT ? PARTIAL : 0);
+    static_assert(STAGES >= 3 && RING >= PARTIAL, "a warp's last partial result reuses its ring");
+    // places of a 16-byte piece of a row, and of the 16 (8) bytes that lane (g, t) takes, in a plane of a tile
+    static __device__ __forceinline__ uint32_t key_at(int u, int c, int h, int g, int t) {
+        return ((u * KCH + c) * 2 + h) * 512 + (((g * 4 + t) ^ (c & 1) * 4)) * 16;
+    }
+    static __device__ __forceinline__ uint32_t value_at(int u, int j, int c, int g, int t) {
+        if constexpr (PIECE == 16) return ((u * 4 + j) * NP + c) * 512 + (t * 8 + (g ^ t * 2)) * 16;
+        else return (u * 4 + j) * 256 + t * 64 + (g / 2 ^ t / 2 * 2) * 16 + g % 2 * 8;
+    }
     // value elements 2e and 2e + 1 of a lane in row group g are rows g and g + 8 of product e
     static __device__ __forceinline__ int dim(int g, int e) { return e / PE * (8 * PE) + g * PE + e % PE; }
 };
@@ -168,6 +175,9 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
     uint32_t *const arrived = (uint32_t *)a.scratch;
     uint8_t *const cta_parts = a.scratch + kScratchCounters * sizeof(uint32_t);             // [CTA][2]
     const int64_t c_begin = split.begin(blockIdx.x), c_end = split.begin(blockIdx.x + 1);
+    auto first_slot = [&](int warp) {
+        return S::SLOT ? smem + warp * S::WARP_BYTES + S::RING : cta_parts + (size_t)(2 * gridDim.x + blockIdx.x * S::WARPS + warp) * S::PARTIAL;
+    };
     const int64_t per = (c_end - c_begin) / S::WARPS, more = (c_end - c_begin) % S::WARPS;   // warps without work come last
     const int64_t x0 = c_begin + w * per + min((int64_t)w, more), x1 = x0 + per + (w < more);
     if (lane < 2) s_seg[w][lane] = -1;
@@ -178,40 +188,29 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
         uint32_t q[NT][S::KCH * S::KSTEP][2];
         float o[NT][S::NE / 2][4], m[NT][2], l[NT][2], sc[NT][2];
         Place<TOK> cur = batch.locate(a, segs, x0), far = cur;
-        const uint8_t *k_ptr, *v_ptr;                              // this lane's bytes of row 0 of the head
+        const uint8_t *k_ptr, *v_ptr;                              // this lane's piece of row 0 of the head
+        constexpr int RI = 32 / S::RP;                             // rows that a copy of the warp covers
+        const int piece = lane % S::RP;
+        const bool piece_in = S::FULL || piece * 16 < a.head_dim * S::ESZ;
 
         auto pointers = [&](const Place<TOK> &p) {
             const int32_t kvh = p.seg / sets, shard = kvh / a.pool.heads_per_shard;
             const int64_t off = (int64_t)(kvh - shard * a.pool.heads_per_shard) * a.pool.head_pitch;
-            k_ptr = a.pool.k[shard] + off + t * 16;
-            v_ptr = a.pool.v[shard] + off + g * S::PIECE;
+            k_ptr = a.pool.k[shard] + off + piece * 16;
+            v_ptr = a.pool.v[shard] + off + piece * 16;
         };
-        auto load_k = [&](uint32_t row, int stage) {
-            const uint32_t to = ring + stage * S::STAGE + lane * 16;
+        auto load_tile = [&](uint32_t row, uint32_t to) {
 #pragma unroll
-            for (int s = 0; s < S::SUB; ++s)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t x = __shfl_sync(~0u, row, s * 16 + h * 8 + g);
-                    const uint8_t *p = x == kNoRow ? k_ptr : k_ptr + (uint64_t)x * 16;
-#pragma unroll
-                    for (int c = 0; c < S::KCH; ++c)
-                        copy_async<16>(to + ((s * S::KCH + c) * 2 + h) * 512, p + c * 64, x != kNoRow && (S::FULL || c * 64 + t * 16 < a.head_dim * S::ESZ));
-                }
-        };
-        auto load_v = [&](uint32_t row, int stage) {
-            const uint32_t to = ring + stage * S::STAGE + lane * S::PIECE;
-#pragma unroll
-            for (int s = 0; s < S::SUB; ++s)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {                      // positions 2t, 2t + 1, 2t + 8, 2t + 9
-                    const uint32_t x = __shfl_sync(~0u, row, s * 16 + 2 * t + (j & 1) + (j >> 1) * 8);
-                    const uint8_t *p = x == kNoRow ? v_ptr : v_ptr + (uint64_t)x * 16;
-#pragma unroll
-                    for (int c = 0; c < S::NP; ++c)
-                        copy_async<S::PIECE>(to + ((s * 4 + j) * S::NP + c) * 32 * S::PIECE, p + c * 8 * S::PIECE,
-                                             x != kNoRow && (S::FULL || (c * 8 + g) * S::PIECE < a.head_dim * S::ESZ));
-                }
+            for (int i = 0; i < TOK / RI; ++i) {
+                const int x = i * RI + lane / S::RP, y = x % 16;   // row of the tile
+                const uint32_t at = __shfl_sync(~0u, row, x);
+                const uint64_t off = at == kNoRow ? 0 : (uint64_t)at * 16;
+                const bool in = at != kNoRow && piece_in;
+                copy_async(to + S::key_at(x / 16, piece / 4, y / 8, y % 8, piece % 4), k_ptr + off, in);
+                const int g = S::PIECE == 16 ? piece % 8 : piece * 2;
+                copy_async(to + S::PLANE + S::value_at(x / 16, (y & 1) + y / 8 * 2, piece / 8, g, y % 8 / 2), v_ptr + off, in);
+            }
+            copies_commit();
         };
         // Queries of a segment. 8-bit caches multiply in f16: a bf16 row is brought by a power of two to where f16 holds
         // its elements exactly down to 2^-33 of the largest.
@@ -274,7 +273,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
                 s_where[w][slot][1] = p.seg;
                 s_where[w][slot][2] = p.tiles;
             }
-            const Partial<S> part(smem + w * S::WARP_BYTES + (slot ? 0 : S::RING));
+            const Partial<S> part(slot ? smem + w * S::WARP_BYTES : first_slot(w));
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -314,42 +313,36 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
             }
         };
 
-        // Tiles' keys and values go round the ring in turn, K_0 V_0 K_1 V_1 ...; whenever one is consumed the copy STAGES - 1
-        // after it starts. rows[n]: offsets of the tile n after this one; `far` is tile AHEAD after this one.
-        constexpr bool ODD = S::STAGES % 2;
-        uint32_t rows[S::AHEAD + 1];
+        // rows[n]: offsets of the tile n after this one; `far` is the tile AHEAD after this one, the next to be copied.
+        constexpr int AHEAD = S::STAGES - 1;
+        uint32_t rows[AHEAD + 1];
         const int64_t n_tiles = x1 - x0;
         pointers(far);
 #pragma unroll
-        for (int n = 0; n < S::AHEAD; ++n) {
+        for (int n = 0; n < AHEAD; ++n) {
             rows[n] = kNoRow;
             if (n < n_tiles) {
                 const Row<TOK> row(a, far);
                 if (n == 0) load_q(cur);
                 else if (far.tile == 0) pointers(far);
                 rows[n] = row.offset(a, far.seg == 0);
-                load_k(rows[n], 2 * n);
-                copies_commit();
-                if (ODD || n + 1 < S::AHEAD) load_v(rows[n], 2 * n + 1);
+                load_tile(rows[n], ring + n * S::STAGE);
                 far.next(a, segs);
             } else copies_commit();
-            if (ODD || n + 1 < S::AHEAD) copies_commit();
         }
         int64_t from = x0;
-        int stage = 0;                                             // of this tile's keys
+        int stage = 0, free_stage = AHEAD;
         for (int64_t i = 0; i < n_tiles; ++i) {
-            const bool ahead = i + S::AHEAD < n_tiles;
-            rows[S::AHEAD] = ahead ? Row<TOK>(a, far).offset(a, far.seg == 0) : kNoRow;
-            const int v_stage = stage + 1 == S::STAGES ? 0 : stage + 1, before = stage ? stage - 1 : S::STAGES - 1;
-
-            copies_wait<S::STAGES - 2>();
-            if constexpr (ODD) {
-                if (ahead) {
-                    if (far.tile == 0) pointers(far);
-                    load_k(rows[S::AHEAD], before);
-                }
-            } else if (i + S::AHEAD - 1 < n_tiles) load_v(rows[S::AHEAD - 1], before);
-            copies_commit();
+            const bool ahead = i + AHEAD < n_tiles;
+            rows[AHEAD] = ahead ? Row<TOK>(a, far).offset(a, far.seg == 0) : kNoRow;
+            copies_wait<AHEAD - 1>();
+            __syncwarp();                                          // lanes read what others copied; all are done with free_stage
+            if (ahead) {
+                if (far.tile == 0) pointers(far);
+                load_tile(rows[AHEAD], ring + free_stage * S::STAGE);
+                far.next(a, segs);
+            } else copies_commit();
+            const uint32_t keys = ring + stage * S::STAGE, values = keys + S::PLANE;
             float s[NT][S::SUB][4];
 #pragma unroll
             for (int u = 0; u < S::SUB; ++u) {
@@ -358,8 +351,8 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
 #pragma unroll
                 for (int c = 0; c < S::KCH; ++c) {
                     uint32_t k[2][4];
-                    shared_read(k[0], ring + stage * S::STAGE + ((u * S::KCH + c) * 2 + 0) * 512 + lane * 16);
-                    shared_read(k[1], ring + stage * S::STAGE + ((u * S::KCH + c) * 2 + 1) * 512 + lane * 16);
+                    shared_read(k[0], keys + S::key_at(u, c, 0, g, t));
+                    shared_read(k[1], keys + S::key_at(u, c, 1, g, t));
 #pragma unroll
                     for (int i = 0; i < S::KSTEP; ++i) {
                         uint32_t a0, a1, a2, a3;
@@ -375,16 +368,6 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
                     }
                 }
             }
-            copies_wait<S::STAGES - 2>();
-            if (ahead) {
-                if constexpr (ODD) load_v(rows[S::AHEAD], stage);
-                else {
-                    if (far.tile == 0) pointers(far);
-                    load_k(rows[S::AHEAD], stage);
-                }
-                far.next(a, segs);
-            }
-            copies_commit();
             uint32_t p_hi[NT][S::SUB][2], p_lo[NT][S::SUB][2];
             if (__any_sync(~0u, lane < TOK && rows[0] == kNoRow)) {
 #pragma unroll
@@ -448,7 +431,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
                     uint32_t v[4][S::PIECE / 4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        shared_read(v[j], ring + v_stage * S::STAGE + (((u * 4 + j) * S::NP + c) * 32 + lane) * S::PIECE);
+                        shared_read(v[j], values + S::value_at(u, j, c, g, t));
 #pragma unroll
                     for (int e = 0; e < S::PE / 2; ++e) {
                         uint32_t av[4];                             // element 2e, element 2e + 1; the same 8 positions on
@@ -481,8 +464,9 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
                 if (cur.tile == 0) load_q(cur);
             }
 #pragma unroll
-            for (int n = 0; n < S::AHEAD; ++n) rows[n] = rows[n + 1];
-            stage = v_stage + 1 == S::STAGES ? 0 : v_stage + 1;
+            for (int n = 0; n < AHEAD; ++n) rows[n] = rows[n + 1];
+            free_stage = stage;
+            stage = stage + 1 == S::STAGES ? 0 : stage + 1;
         }
     }
     __syncthreads();
@@ -514,7 +498,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
         const int side = i == open[1];
         int32_t head0;
         const int32_t heads = heads_of(where[1], &head0);
-        auto at = [&](int x) { return smem + ((i >> 1) + x) * S::WARP_BYTES + (x || !(i & 1) ? S::RING : 0); };
+        auto at = [&](int x) { return x || !(i & 1) ? first_slot((i >> 1) + x) : smem + (i >> 1) * S::WARP_BYTES; };
         for (; task < FS; task += S::WARPS)
             join<S, false>(a, task, n, at, i != open[0] && i != open[1], cta_parts + (size_t)(blockIdx.x * 2 + side) * S::PARTIAL, where[0],
                            head0, heads);
