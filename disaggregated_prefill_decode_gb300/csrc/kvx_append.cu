@@ -4,7 +4,7 @@
 // A thread keeps one column (plane, head, 8 elements) and walks tokens, so shard, head and element
 // offsets are computed once; only the slot changes. Reads are 16 bytes a thread, writes 16 or 8.
 // Bound by memory: each value is read and written once.
-#include "kvx_internal.h"
+#include "kvx_launch.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -35,6 +35,7 @@ template <int IO> __device__ __forceinline__ uint32_t codes(uint32_t x, float in
 // IO 0: 16-bit values copied; KVX_BF16 / KVX_F16: converted to 8 bits. UNROLL tokens per thread.
 template <int IO, int UNROLL>
 __global__ void __launch_bounds__(kAppendThreads) kvx_append_kernel(const __grid_constant__ AppendArgs a, int cols, int rows) {
+    wait_for_earlier();
     const int my_row = threadIdx.x / cols, col = blockIdx.y * cols + threadIdx.x % cols;
     const int vecs = a.head_dim / 8, heads = a.pool.heads_per_shard * a.pool.n_shards;
     const int plane = col / (heads * vecs), head = col / vecs % heads, vec = col % vecs;
@@ -84,10 +85,7 @@ template <int IO> static cudaError_t launch(const AppendArgs &a, int32_t sms, cu
     const bool few = (a.n_tokens + rows - 1) / rows * y < 4 * sms;
     const int unroll = few ? 1 : 4;
     const dim3 grid((unsigned)((a.n_tokens + rows * unroll - 1) / (rows * unroll)), y);
-    if (few) kvx_append_kernel<IO, 1><<<grid, kAppendThreads, 0, stream>>>(a, cols, rows);
-    else kvx_append_kernel<IO, 4><<<grid, kAppendThreads, 0, stream>>>(a, cols, rows);
-    count_launch();
-    return cudaGetLastError();
+    return launch_after(few ? kvx_append_kernel<IO, 1> : kvx_append_kernel<IO, 4>, grid, kAppendThreads, 0, stream, a, cols, rows);
 }
 
 cudaError_t launch_append(const AppendArgs &a, int32_t value_type, int32_t io_type, int32_t sms, cudaStream_t stream) {

@@ -2,7 +2,7 @@
 // over the CTAs.
 #pragma once
 
-#include "kvx_internal.h"
+#include "kvx_launch.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -80,21 +80,16 @@ __device__ __forceinline__ void shared_read(uint32_t (&x)[2], uint32_t at) {
 // ------------------------------------------------------------------------------------------------
 
 // x / d, in 32 bits where they suffice.
-__device__ __forceinline__ int64_t divide(int64_t x, int32_t d) {
-    return (uint64_t)x >> 32 ? x / d : (int64_t)((uint32_t)x / (uint32_t)d);
+__device__ __forceinline__ int64_t divide(int64_t x, int64_t d) {
+    return (uint64_t)(x | d) >> 32 ? x / d : (int64_t)((uint32_t)x / (uint32_t)d);
 }
 
+// In proportion, not in whole tiles each: where the segments are alike and divide the CTAs, no CTA has parts of two.
 struct Split {
     int64_t tiles;        // in all
     int32_t ctas;         // that have work, at least one tile each
-    int64_t each;         // tiles of a CTA; the first `more` CTAs have one more
-    int32_t more;
-    __device__ __forceinline__ int64_t begin(int32_t cta) const { return cta * each + min(cta, more); }
-    __device__ __forceinline__ int32_t cta_of(int64_t tile) const {
-        const int64_t large = more * (each + 1);
-        if (each >> 31) return (int32_t)(tile < large ? tile / (each + 1) : more + (tile - large) / each);
-        return (int32_t)(tile < large ? divide(tile, (int32_t)each + 1) : more + divide(tile - large, (int32_t)each));
-    }
+    __device__ __forceinline__ int64_t begin(int32_t cta) const { return divide(cta * tiles, ctas); }
+    __device__ __forceinline__ int32_t cta_of(int64_t tile) const { return (int32_t)divide((tile + 1) * ctas - 1, tiles); }
 };
 
 // A request's live positions [first, len) and its tiles of TOK positions, aligned to TOK; at least one, so that an
@@ -192,8 +187,6 @@ template <int TOK, int WARPS> struct Batch {
         }
         split.tiles = total * segs;
         split.ctas = (int32_t)min((int64_t)gridDim.x, divide(split.tiles + WARPS - 1, WARPS));
-        split.each = divide(split.tiles, split.ctas);
-        split.more = (int32_t)(split.tiles - split.each * split.ctas);
         if (blockIdx.x == 0)
             for (int32_t r = threadIdx.x; r < a.n_reqs; r += 32 * WARPS)
                 if (a.seq_len[r] < 0 || a.seq_len[r] > cap) atomicAdd(a.pool.skipped, 1ull);

@@ -74,13 +74,20 @@ __device__ __forceinline__ void write_lse(const AttendArgs &a, int32_t r, int32_
     if (a.lse) a.lse[(int64_t)r * a.n_q_heads + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-// One warp: float4 f of every lane of n partial results, `at(x)` the x-th (in shared memory, or put into the scratch by other
-// CTAs), joined into the outputs or into another partial result. Sixteen are read at once; lane (g, t) takes the maxima and
-// sums of two of them for its query, the others' weights come by shuffles.
-template <class S, bool SCRATCH, class At>
-__device__ __forceinline__ void join(const AttendArgs &a, int f, int n, At at, bool final, uint8_t *to, int32_t r, int32_t head0,
-                                     int32_t heads) {
-    const int lane = threadIdx.x & 31, t = lane & 3, g = lane >> 2;
+// Partial results to join: one, and those at equal distances.
+struct Pieces {
+    uint8_t *first, *others;
+    int step, n;
+    __device__ __forceinline__ uint8_t *at(int x) const { return x ? others + x * step : first; }
+};
+
+// One warp: float4 f of every lane of some partial results, joined into the outputs or into another partial result. They lie in
+// shared memory, or in the scratch, where other CTAs put them: then they come from L2, and more of them at once. Lane (g, t)
+// takes the maxima and sums of every eighth for its query, the others' weights come by shuffles.
+template <class S, bool SCRATCH>
+__device__ __noinline__ void join(const AttendArgs &a, int f, const Pieces &from, uint8_t *to, int32_t r, int32_t head0, int32_t heads) {
+    constexpr int ROUNDS = SCRATCH ? 3 : 1;
+    const int lane = threadIdx.x & 31, t = lane & 3, g = lane >> 2, n = from.n;
     const int set = f / S::F4, i = f % S::F4 / (S::F4 / 2), e4 = f % (S::F4 / 2), q = set * 8 + 2 * t + i;
     auto get = [](const auto *p) {
         if constexpr (SCRATCH) return __ldcg(p);
@@ -88,41 +95,46 @@ __device__ __forceinline__ void join(const AttendArgs &a, int f, int n, At at, b
     };
     float top = -INFINITY, l = 0.0f;
     float4 o = make_float4(0, 0, 0, 0);
-    for (int x0 = 0; x0 < n; x0 += 16) {
-        float4 y[16];
-        float m[2], s[2];
+    for (int x0 = 0; x0 < n; x0 += 8 * ROUNDS) {
+        float4 y[ROUNDS][8];
+        float m[ROUNDS], s[ROUNDS], up = top;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const bool in = x0 + 8 * k + g < n;
-            const Partial<S> p(at(in ? x0 + 8 * k + g : 0));
-            m[k] = in ? get(p.m + q) : -INFINITY;
-            s[k] = in ? get(p.l + q) : 0.0f;
+        for (int k = 0; k < ROUNDS; ++k) {
+            const int x = x0 + 8 * k + g;
+            const Partial<S> p(from.at(min(x, n - 1)));
+            m[k] = x < n ? get(p.m + q) : -INFINITY;
+            s[k] = x < n ? get(p.l + q) : 0.0f;
+            if (x0 + 8 * k < n) {
+#pragma unroll
+                for (int x = 0; x < 8; ++x) y[k][x] = get(Partial<S>(from.at(min(x0 + 8 * k + x, n - 1))).o + f * 32 + lane);
+            }
         }
 #pragma unroll
-        for (int x = 0; x < 16; ++x)
-            y[x] = x0 + x < n ? get(Partial<S>(at(x0 + x)).o + f * 32 + lane) : make_float4(0, 0, 0, 0);
-        float up = fmaxf(m[0], m[1]);
+        for (int k = 0; k < ROUNDS; ++k) up = fmaxf(up, m[k]);
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) up = fmaxf(up, __shfl_xor_sync(~0u, up, d));
-        up = fmaxf(up, top);
         const float ref = up == -INFINITY ? 0.0f : up, old = fast_exp2(top - ref);
         top = up;
-        m[0] = fast_exp2(m[0] - ref);
-        m[1] = fast_exp2(m[1] - ref);
-        l = l * old + m[0] * s[0] + m[1] * s[1];
+        l *= old;
         o = make_float4(o.x * old, o.y * old, o.z * old, o.w * old);
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-            const float w = __shfl_sync(~0u, m[x >> 3], (x & 7) * 4 + t);
-            o.x += w * y[x].x;
-            o.y += w * y[x].y;
-            o.z += w * y[x].z;
-            o.w += w * y[x].w;
-        }
+        for (int k = 0; k < ROUNDS; ++k)
+            if (x0 + 8 * k < n) {
+                const float mine = fast_exp2(m[k] - ref);
+                l += mine * s[k];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const float w = __shfl_sync(~0u, mine, x * 4 + t);
+                    o.x += w * y[k][x].x;
+                    o.y += w * y[k][x].y;
+                    o.z += w * y[k][x].z;
+                    o.w += w * y[k][x].w;
+                }
+            }
     }
 #pragma unroll
     for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(~0u, l, d);
-    if (final) {
+    if (!to) {
         const int d = S::dim(g, e4 * 4);
         if (q < heads && (S::FULL || d < a.head_dim)) {
             const float inv = l == 0.0f ? 0.0f : a.v_scale / l;
@@ -169,6 +181,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int32_t group = a.n_q_heads / a.n_kv_heads, sets = (group + 8 * NT - 1) / (8 * NT), segs = a.n_kv_heads * sets;
 
+    wait_for_earlier();
     const Batch<TOK, S::WARPS> batch(a, segs);
     const Split &split = batch.split;
     if ((int32_t)blockIdx.x >= split.ctas) return;
@@ -495,18 +508,17 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
         const uint32_t rest = leaders & (leaders - 1);
         const int n = __popc(pieces & (rest ? (1u << (__ffs(rest) - 1)) - 1 : ~0u) & ~((1u << i) - 1));
         const int32_t *where = s_where[i >> 1][i & 1];
-        const int side = i == open[1];
         int32_t head0;
         const int32_t heads = heads_of(where[1], &head0);
-        auto at = [&](int x) { return x || !(i & 1) ? first_slot((i >> 1) + x) : smem + (i >> 1) * S::WARP_BYTES; };
-        for (; task < FS; task += S::WARPS)
-            join<S, false>(a, task, n, at, i != open[0] && i != open[1], cta_parts + (size_t)(blockIdx.x * 2 + side) * S::PARTIAL, where[0],
-                           head0, heads);
+        uint8_t *const first = i & 1 ? smem + (i >> 1) * S::WARP_BYTES : first_slot(i >> 1);
+        const Pieces from = {first, first_slot(i >> 1), S::SLOT ? S::WARP_BYTES : S::PARTIAL, n};
+        uint8_t *const to = i == open[0] || i == open[1] ? cta_parts + (size_t)(blockIdx.x * 2 + (i == open[1])) * S::PARTIAL : nullptr;
+        for (; task < FS; task += S::WARPS) join<S, false>(a, task, from, to, where[0], head0, heads);
     }
     if (open[0] < 0 && open[1] < 0) return;
-    __threadfence();
     __syncthreads();
     if (threadIdx.x < 2) {
+        __threadfence();
         const int i = open[threadIdx.x];
         s_last[threadIdx.x] = false;
         if (i >= 0) {
@@ -527,9 +539,8 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
         const int32_t from = split.cta_of(seg), n = split.cta_of(seg + where[2] - 1) - from + 1;
         int32_t head0;
         const int32_t heads = heads_of(where[1], &head0);
-        for (int f = w; f < FS; f += S::WARPS)
-            join<S, true>(a, f, n, [&](int x) { return cta_parts + (size_t)((from + x) * 2 + (x == 0)) * S::PARTIAL; }, true, nullptr, where[0],
-                          head0, heads);
+        const Pieces pieces = {cta_parts + (size_t)(2 * from + 1) * S::PARTIAL, cta_parts + (size_t)(2 * from) * S::PARTIAL, 2 * S::PARTIAL, n};
+        for (int f = w; f < FS; f += S::WARPS) join<S, true>(a, f, pieces, nullptr, where[0], head0, heads);
     }
 }
 
@@ -539,9 +550,7 @@ template <class S> static cudaError_t launch(const AttendArgs &a, int32_t sms, c
     constexpr int bytes = S::WARPS * S::WARP_BYTES;
     static const cudaError_t set = cudaFuncSetAttribute(kvx_attend_planes<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (set != cudaSuccess) return set;
-    kvx_attend_planes<S><<<sms, S::THREADS, bytes, stream>>>(a);
-    count_launch();
-    return cudaGetLastError();
+    return launch_after(kvx_attend_planes<S>, dim3(sms), S::THREADS, bytes, stream, a);
 }
 
 template <int VT, int IO, int D, int NT> static cudaError_t launch(const AttendArgs &a, int32_t sms, cudaStream_t stream) {

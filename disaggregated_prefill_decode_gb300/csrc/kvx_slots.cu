@@ -8,7 +8,7 @@
 // its share of the outputs: output tiles go round-robin over the CTAs, and a token or block finds its
 // request by bisection of the sums. So nothing is handed from CTA to CTA and no scratch is needed; the
 // repeated reads are 8 bytes per request and CTA, from L2.
-#include "kvx_internal.h"
+#include "kvx_launch.cuh"
 
 #include <algorithm>
 
@@ -65,6 +65,7 @@ __device__ __forceinline__ int64_t first_tile(int64_t lo) {
 __global__ void __launch_bounds__(kSlotThreads) kvx_slot_map_kernel(const SlotArgs a) {
     __shared__ int64_t s_tok[kReqs], s_blk[kReqs];      // sums before each request, within the pass
     __shared__ int32_t s_ctx[kReqs], s_had[kReqs];
+    wait_for_earlier();
     const uint32_t bs = (uint32_t)a.block_size;
     const int64_t inf = INT32_MAX;
     Sums base = {0, 0};
@@ -174,9 +175,7 @@ __global__ void __launch_bounds__(kSlotThreads) kvx_slot_map_kernel(const SlotAr
 cudaError_t launch_slot_map(const SlotArgs &a, int32_t sms, cudaStream_t stream) {
     const int64_t tiles = std::max((a.max_tokens + kTokTile - 1) / kTokTile, (int64_t)(a.n_reqs + 1023) / 1024);
     const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, 4 * sms));
-    kvx_slot_map_kernel<<<grid, kSlotThreads, 0, stream>>>(a);
-    count_launch();
-    return cudaGetLastError();
+    return launch_after(kvx_slot_map_kernel, dim3(grid), kSlotThreads, 0, stream, a);
 }
 
 }  // namespace kvx
