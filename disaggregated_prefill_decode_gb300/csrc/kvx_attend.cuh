@@ -153,10 +153,10 @@ template <int WARPS> __device__ __forceinline__ int64_t cta_exclusive(int64_t x,
     return before + s - x;
 }
 
-// The batch as a CTA sees it: the split over gridDim.x CTAs (of at least a tile per warp), and how to find a place in it.
+// The batch as a CTA sees it: the split over gridDim.x CTAs (of at least MIN tiles each), and how to find a place in it.
 // Up to 256 requests each warp keeps all the sums, a lane those of up to 8 consecutive requests, with no barrier; beyond that
 // the CTA looks for the request in which its own stretch begins, and its warps go on from there.
-template <int TOK, int WARPS> struct Batch {
+template <int TOK, int WARPS, int MIN> struct Batch {
     static constexpr int PER = 8;
     Split split;
     int32_t per;                       // requests of a lane
@@ -186,7 +186,7 @@ template <int TOK, int WARPS> struct Batch {
             cta_exclusive<WARPS>(mine, &total);
         }
         split.tiles = total * segs;
-        split.ctas = (int32_t)min((int64_t)gridDim.x, divide(split.tiles + WARPS - 1, WARPS));
+        split.ctas = (int32_t)min((int64_t)gridDim.x, divide(split.tiles + MIN - 1, MIN));
         if (blockIdx.x == 0)
             for (int32_t r = threadIdx.x; r < a.n_reqs; r += 32 * WARPS)
                 if (a.seq_len[r] < 0 || a.seq_len[r] > cap) atomicAdd(a.pool.skipped, 1ull);

@@ -182,7 +182,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
     const int32_t group = a.n_q_heads / a.n_kv_heads, sets = (group + 8 * NT - 1) / (8 * NT), segs = a.n_kv_heads * sets;
 
     wait_for_earlier();
-    const Batch<TOK, S::WARPS> batch(a, segs);
+    const Batch<TOK, S::WARPS, S::WARPS> batch(a, segs);
     const Split &split = batch.split;
     if ((int32_t)blockIdx.x >= split.ctas) return;
     uint32_t *const arrived = (uint32_t *)a.scratch;

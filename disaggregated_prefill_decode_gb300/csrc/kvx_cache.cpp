@@ -32,8 +32,14 @@ static kvx_status ready(kvx_cache_t c, cudaStream_t stream) {
     int32_t device = 0, sms = 0;
     kvx_status st = device_sms(&device, &sms);
     if (st) return st;
+    for (void *p : {c->base.front(), c->base.back()}) {
+        cudaPointerAttributes at;
+        e = cudaPointerGetAttributes(&at, p);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaPointerGetAttributes(cache buffer)");
+        c->outside_device |= at.type != cudaMemoryTypeDevice;
+    }
     void *dev = nullptr;
-    const size_t bytes = 256 + attend_scratch_bytes(sms);
+    const size_t bytes = 256 + attend_scratch_bytes(sms, c->g.n_planes == 1);
     st = pool_alloc(&dev, bytes, stream);
     if (st) return st;
     e = cudaMemsetAsync(dev, 0, bytes, stream);
@@ -230,6 +236,7 @@ kvx_status kvx_cache_attend(kvx_cache_t c, int32_t layer, const void *q, int64_t
         return fail(KVX_EINVAL, "q and out: pointers and strides must be multiples of 16 bytes");
     if (n_reqs == 0) return KVX_OK;
     if ((st = ready(c, stream))) return st;
+    if (g.n_planes == 1 && c->outside_device) return fail(KVX_EUNSUPPORTED, "attention over latents outside device memory");
     AttendArgs a;
     fill_layer(c, layer, &a.pool);
     a.q = (const uint8_t *)q;
@@ -264,17 +271,18 @@ kvx_status kvx_cache_attend(kvx_cache_t c, int32_t layer, const void *q, int64_t
 kvx_status kvx_cache_status(kvx_cache_t c, cudaStream_t stream) {
     if (!c) return fail(KVX_EINVAL, "cache is NULL");
     cudaError_t e = cudaStreamSynchronize(stream);
-    unsigned long long n = 0;
+    unsigned long long n[2] = {0, 0};
     if (e == cudaSuccess && c->dev) {
-        e = cudaMemcpyAsync(&n, c->dev, sizeof n, cudaMemcpyDeviceToHost, stream);
+        e = cudaMemcpyAsync(n, c->dev, sizeof n, cudaMemcpyDeviceToHost, stream);
         if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
-        if (e == cudaSuccess && n) {
+        if (e == cudaSuccess && (n[0] || n[1])) {
             e = cudaMemsetAsync(c->dev, 0, sizeof n, stream);
             if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
         }
     }
     if (e != cudaSuccess) return cuda_fail(e, "kvx_cache_status");
-    if (n) return fail(KVX_ERANGE, "%llu slots, blocks or lengths out of bounds were skipped", n);
+    if (n[1]) return fail(KVX_ETIMEDOUT, "a copy into shared memory did not arrive: the outputs since the last check are not valid");
+    if (n[0]) return fail(KVX_ERANGE, "%llu slots, blocks or lengths out of bounds were skipped", n[0]);
     return KVX_OK;
 }
 

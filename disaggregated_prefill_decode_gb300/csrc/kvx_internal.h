@@ -181,7 +181,7 @@ struct CacheLayer {
     int32_t token_pitch, head_pitch;
     int32_t n_blocks, block_size;
     int32_t heads_per_shard, n_shards;
-    unsigned long long *skipped;      // slots, blocks and lengths out of bounds
+    unsigned long long *skipped;      // slots, blocks and lengths out of bounds; then waits that ran out
 };
 
 struct SlotArgs {
@@ -230,7 +230,8 @@ cudaError_t launch_attend_f16(const AttendArgs &a, int32_t sms, cudaStream_t str
 cudaError_t launch_attend_e4m3_bf16(const AttendArgs &a, int32_t sms, cudaStream_t stream);
 cudaError_t launch_attend_e4m3_f16(const AttendArgs &a, int32_t sms, cudaStream_t stream);
 cudaError_t launch_attend_latent(const AttendArgs &a, int32_t value_type, int32_t io_type, int32_t sms, cudaStream_t stream);
-size_t attend_scratch_bytes(int32_t sms);
+size_t attend_scratch_bytes(int32_t sms, bool latent);
+size_t latent_scratch_bytes(int32_t sms);
 
 }  // namespace kvx
 
@@ -241,6 +242,7 @@ struct kvx_cache_s {
     kvx_cache_config cfg{};                    // defaults filled in
     int32_t device = -1;                       // of the scratch, set by the first append or attend
     int32_t sms = 0;
+    bool outside_device = false;               // a buffer is not device memory
     uint8_t *dev = nullptr;                    // [256 bytes: skipped][scratch of the attend kernels]
 };
 

@@ -591,7 +591,7 @@ kvx_status kvx_cache_append(kvx_cache_t cache, int32_t layer, const void *k, int
  * held in several pools join), or NULL. A request with no positions gets out 0 and lse -inf.
  * seq_len beyond max_blocks * block_size is cut there, a negative one counts as 0, and positions in a
  * block outside the pool are left out; kvx_cache_status reports each of these. KVX_EUNSUPPORTED for
- * v_dim above 512. Unused slots may hold
+ * latents with v_dim above 512 or outside device memory. Unused slots may hold
  * anything, NaN too. Products are taken in 16 bits with 32-bit sums; two calls on the same inputs give the
  * same bits.
  */
@@ -601,7 +601,8 @@ kvx_status kvx_cache_attend(kvx_cache_t cache, int32_t layer, const void *q, int
                             cudaStream_t stream);
 
 /* Waits for `stream` and returns KVX_ERANGE when an append or attend enqueued on the handle since the
- * last call here skipped a slot, a block or a length out of bounds, else KVX_OK. */
+ * last call here skipped a slot, a block or a length out of bounds, KVX_ETIMEDOUT when a copy into shared
+ * memory did not arrive within 2 s (the outputs are then not valid), else KVX_OK. */
 kvx_status kvx_cache_status(kvx_cache_t cache, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------------------------------
