@@ -37,9 +37,9 @@ template <int VT_, int IO_> struct LatentShape {
     static constexpr int MPW = TOK / 32;                          // 16-position products of half a tile
     static constexpr int PITCH = kCacheMaxLatent * ESZ + 32;
     static constexpr int STAGE = TOK * PITCH;
-    static constexpr int SROW = TOK + 4;                          // floats of a head's scores in shared memory
+    static constexpr int ROWS = TOK / kLatentWarps;               // copied by a warp
     static constexpr int PENTRY = SPLIT ? 16 : 8;
-    static constexpr int OFF_S = 2 * STAGE, OFF_P = OFF_S + 4 * kLatentHeads * SROW * 4;
+    static constexpr int OFF_S = 2 * STAGE, OFF_P = OFF_S + 4 * kLatentHeads * TOK * 4;
     static constexpr int BYTES = OFF_P + TOK / 16 * 2 * 32 * PENTRY;
 };
 
@@ -67,11 +67,15 @@ struct OpenSegment {
     int32_t r, seg, pieces, unused;
 };
 
+// Position s of the four that an entry of the weights holds, from the first.
+__device__ __forceinline__ int entry_position(int s) { return 4 * ((s & 1) * 2 + (s >> 1)); }
+
 template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_attend_latent(const __grid_constant__ AttendArgs a) {
     constexpr int TOK = S::TOK;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t s_full[2];
-    __shared__ uint32_t s_live[2][2];                              // live positions of a stage's tile
+    __shared__ __align__(8) uint8_t s_live[2][kLatentWarps];       // live positions of a stage's tile, a warp's rows each
+    __shared__ Place<TOK> s_cur, s_far;                            // this tile, and the next one to look up
     __shared__ float s_old[kLatentHeads], s_m[kLatentHeads], s_l[kLatentHeads], s_up[kLatentHeads];
     __shared__ int32_t s_timeout;
     float *const scores = (float *)(smem + S::OFF_S);
@@ -89,7 +93,7 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
     if (threadIdx.x == 0) {
         if ((int32_t)blockIdx.x >= batch.split.ctas) open[blockIdx.x].pieces = 0;
         s_timeout = 0;
-        for (int i = 0; i < 2; ++i) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_addr(&s_full[i])) : "memory");
+        for (int i = 0; i < 2; ++i) asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_addr(&s_full[i])), "n"(kLatentWarps) : "memory");
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if ((int32_t)blockIdx.x >= batch.split.ctas) return;
@@ -100,76 +104,73 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
 
-    Place<TOK> cur = batch.locate(a, segs, c_begin), far = cur;
+    {
+        const Place<TOK> begin = batch.locate(a, segs, c_begin);
+        if (threadIdx.x == 0) s_cur = s_far = begin;
+    }
+    __syncthreads();
 
-    // Warp 0: the block ids of tile `far`, and its rows' copies.
-    int32_t blk[TOK / 32];
-    uint32_t rest[TOK / 32];
+    // A warp copies ROWS rows of each tile: the block id of lane x's row, its place in the block, and where its head begins.
+    // A row that is not live (blk -2: no such position) is filled with zeros.
+    int32_t blk = -2;
+    uint32_t rest = 0;
+    const uint8_t *base = nullptr;
+    bool report = false;
     auto lookup = [&]() {
-#pragma unroll
-        for (int i = 0; i < TOK / 32; ++i) {
-            const uint32_t pos = (uint32_t)far.first / TOK * TOK + (uint32_t)far.tile * TOK + i * 32 + lane;
-            blk[i] = -2;
-            if (pos < (uint32_t)far.first || pos >= (uint32_t)far.len) continue;
-            const uint32_t col = (__umulhi(pos, a.block_mul) + pos) >> a.block_shift;
-            blk[i] = max(a.block_table[far.r * a.table_stride + col], -1);
-            rest[i] = (pos - col * (uint32_t)a.pool.block_size) * a.token_pitch16;
-        }
+        const int32_t seg = s_far.seg, first = s_far.first, kvh = seg / sets, shard = kvh / a.pool.heads_per_shard;
+        const uint32_t pos = (uint32_t)first / TOK * TOK + (uint32_t)s_far.tile * TOK + w * S::ROWS + lane;
+        base = a.pool.k[shard] + (int64_t)(kvh - shard * a.pool.heads_per_shard) * a.pool.head_pitch;
+        report = seg == 0;
+        blk = -2;
+        if (lane >= S::ROWS || pos < (uint32_t)first || pos >= (uint32_t)s_far.len) return;
+        const uint32_t col = (__umulhi(pos, a.block_mul) + pos) >> a.block_shift;
+        blk = max(a.block_table[s_far.r * a.table_stride + col], -1);
+        rest = (pos - col * (uint32_t)a.pool.block_size) * a.token_pitch16;
     };
-    auto copy_tile = [&](int stage) {
-        const int32_t kvh = far.seg / sets, shard = kvh / a.pool.heads_per_shard;
-        const uint8_t *base = a.pool.k[shard] + (int64_t)(kvh - shard * a.pool.heads_per_shard) * a.pool.head_pitch;
-        uint8_t *const to = smem + stage * S::STAGE;
+    auto copy_rows = [&](int stage) {
+        uint8_t *const to = smem + stage * S::STAGE + w * S::ROWS * S::PITCH;
         const uint32_t bar = shared_addr(&s_full[stage]);
-        uint32_t live[2] = {~0u, ~0u}, bytes = 0;
-        bool dead = false;
-#pragma unroll
-        for (int i = 0; i < TOK / 32; ++i) {
-            const bool in = blk[i] >= 0 && blk[i] < a.pool.n_blocks;
-            if (!in && blk[i] != -2 && far.seg == 0) atomicAdd(a.pool.skipped, 1ull);
-            live[i] = __ballot_sync(~0u, in);
-            bytes += __popc(live[i]) * row_bytes;
-            dead |= live[i] != ~0u;
-        }
-        if (dead) {                                                // rows that no copy fills read as zero
-            for (int i = 0; i < TOK; ++i)
-                if (!(live[i >> 5] >> (i & 31) & 1))
+        const bool in = blk >= 0 && blk < a.pool.n_blocks;
+        if (!in && blk != -2 && report) atomicAdd(a.pool.skipped, 1ull);
+        const uint32_t live = __ballot_sync(~0u, in);
+        if (live != (1u << S::ROWS) - 1)
+            for (int i = 0; i < S::ROWS; ++i)
+                if (!(live >> i & 1))
                     for (uint32_t b = lane * 16; b < row_bytes; b += 512) *(uint4 *)(to + i * S::PITCH + b) = make_uint4(0, 0, 0, 0);
-        }
-        if (lane < 2) s_live[stage][lane] = live[lane];
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < TOK / 32; ++i)
-            if (live[i] >> lane & 1) {
-                const uint8_t *src = base + ((uint64_t)((uint32_t)blk[i] * a.block_pitch16 + rest[i])) * 16;
-                asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                                 shared_addr(to + (i * 32 + lane) * S::PITCH)),
-                             "l"(src), "r"(row_bytes), "r"(bar)
-                             : "memory");
-            }
-    };
-    if (w == 0) {
-        lookup();
-        copy_tile(0);
-        far.next(a, segs);
-        if (n_tiles > 1) {
-            lookup();
-            copy_tile(1);
-            far.next(a, segs);
+        if (lane == 0) {
+            s_live[stage][w] = (uint8_t)live;
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(__popc(live) * row_bytes) : "memory");
         }
-        if (n_tiles > 2) lookup();
-    }
+        __syncwarp();
+        if (in)
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                             shared_addr(to + lane * S::PITCH)),
+                         "l"(base + (uint64_t)((uint32_t)blk * a.block_pitch16 + rest) * 16), "r"(row_bytes), "r"(bar)
+                         : "memory");
+    };
+    // Thread 0 moves s_far on where a barrier stands before and after.
+    auto advance = [&](Place<TOK> &p) {
+        if (threadIdx.x == 0) p.next(a, segs);
+    };
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+        if (k < n_tiles) {
+            lookup();
+            if (k < 2) copy_rows(k);
+            __syncthreads();
+            if (k + 1 < n_tiles) advance(s_far);
+            __syncthreads();
+        }
 
     uint32_t q[S::CM + 1][S::KSTEP][2][2];                         // this quarter's chunks, then a left-over one
     float o[4][2][4], m = -INFINITY, l = 0.0f, scale = a.scale;    // m, l, scale: of head h
     const int left_chunk = 4 * S::CM + (S::F8 ? 0 : kq & 1);       // the left-over chunks go round the warps
     const bool left = (kq >> 1) == half;
     auto load_q = [&]() {
-        const int32_t kvh = cur.seg / sets, first = cur.seg % sets * kLatentHeads;
-        const uint8_t *src = a.q + cur.r * a.q_stride + (int64_t)(kvh * group + first) * a.head_dim * 2;
+        const int32_t kvh = s_cur.seg / sets, first = s_cur.seg % sets * kLatentHeads;
+        const uint8_t *src = a.q + s_cur.r * a.q_stride + (int64_t)(kvh * group + first) * a.head_dim * 2;
         if constexpr (S::F8 && S::IO == KVX_BF16) {                // a power of two per query, as in kvx_attend_planes.cuh
             float top = 0.0f;
             if (first + h < group)
@@ -220,8 +221,9 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
     };
     load_q();
 
-    bool begun = cur.seg_begin(segs) == c_begin;                   // the segment at hand begins in this CTA
-    int32_t last_r = 0, last_seg = 0, last_pieces = 0;
+    bool begun = s_cur.seg_begin(segs) == c_begin;                 // the segment at hand begins in this CTA
+    int32_t tiles_left = s_cur.tiles - s_cur.tile;                 // of it
+    OpenSegment opened = {0, 0, 0, 0};
     for (int32_t k = 0; k < n_tiles; ++k) {
         const int stage = k & 1;
         const uint32_t rows = shared_addr(smem + stage * S::STAGE);
@@ -255,45 +257,52 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
             for (int c = 0; c < S::CM; ++c) score_chunk(i, c, kq * S::CM + c);
             if (left && (S::MPW == 1 || i == (kq & 1))) score_chunk(i, S::CM, left_chunk);
         }
-        // [quarter][head][16-position product][position % 4][position / 4]
+        // [quarter][head][16-position product][position % 4][place in the entry], swizzled by the head for the two stores of a lane
 #pragma unroll
         for (int i = 0; i < S::MPW; ++i)
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int pos = ((g & 4) | (g & 1) << 1 | (g >> 1 & 1)) + (c >> 1) * 8;
-                    scores[(kq * kLatentHeads + n * 8 + 2 * t + (c & 1)) * S::SROW + (half * S::MPW + i) * 16 + (pos & 3) * 4 + (pos >> 2)] = s[i][n][c];
+                for (int c = 0; c < 2; ++c) {
+                    const int word = (half * S::MPW + i) * 16 + ((g & 1) << 1 | (g >> 1 & 1)) * 4 + (g >> 2) * 2;
+                    *(float2 *)(scores + (kq * kLatentHeads + n * 8 + 2 * t + c) * TOK + (word ^ (t & 1) * 16 ^ (t >> 1) * 2)) =
+                        make_float2(s[i][n][c], s[i][n][2 + c]);
                 }
         __syncthreads();
         if (s_timeout) {
             if (k + 1 < n_tiles) wait_full(&s_full[stage ^ 1], k + 1 >> 1 & 1);   // its copies may be under way
             break;
         }
+        if (k > 0 && k + 3 < n_tiles) advance(s_far);
 
-        // softmax of head h: lane x has positions 16 u + y + 4 j for (u, y) = (x / 4, x % 4) and all j, or (x / 8, x / 2 % 4) and two j
+        // softmax of head h: lane x has an entry (or half of one) of the weights: positions 16 u + y + entry_position(s)
         {
             constexpr int E = TOK / 16;
+            const int u = E == 4 ? x >> 2 : x >> 3, y = E == 4 ? x & 3 : x >> 1 & 3, s0 = E == 4 ? 0 : 2 * (x & 1), th = h >> 1 & 3;
+            const float *src = scores + h * TOK + (u * 16 + y * 4 + s0 ^ (th & 1) * 16 ^ (E == 4 ? 0 : (th >> 1) * 2));
             float p[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) p[e] = 0.0f;
 #pragma unroll
-            for (int k4 = 0; k4 < 4; ++k4) {
-                const float *src = scores + (k4 * kLatentHeads + h) * S::SROW + x * E;
+            for (int k4 = 0; k4 < 4; ++k4, src += kLatentHeads * TOK) {
                 if constexpr (E == 4) {
-                    const float4 y = *(const float4 *)src;
-                    p[0] += y.x, p[1] += y.y, p[2] += y.z, p[3] += y.w;
+                    const float4 z = *(const float4 *)src;
+                    p[0] += z.x, p[1] += z.y, p[2] += z.z, p[3] += z.w;
                 } else {
-                    const float2 y = *(const float2 *)src;
-                    p[0] += y.x, p[1] += y.y;
+                    const float2 z = *(const float2 *)src;
+                    p[0] += z.x, p[1] += z.y;
                 }
             }
-            const int u = E == 4 ? x >> 2 : x >> 3, y = E == 4 ? x & 3 : x >> 1 & 3, j0 = E == 4 ? 0 : 2 * (x & 1);
-            if ((s_live[stage][0] & s_live[stage][1]) != ~0u)
+            if (E == 4 && th >> 1) {
+                const float z0 = p[0], z1 = p[1];
+                p[0] = p[E - 2], p[1] = p[E - 1], p[E - 2] = z0, p[E - 1] = z1;
+            }
+            const uint64_t live = *(const uint64_t *)s_live[stage];
+            if (live != (S::ROWS == 8 ? ~0ull : 0x0f0f0f0f0f0f0f0full))
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
-                    const int pos = 16 * u + y + 4 * (j0 + e);
-                    if (!(s_live[stage][pos >> 5] >> (pos & 31) & 1)) p[e] = -INFINITY;
+                    const int pos = 16 * u + y + entry_position(s0 + e);
+                    if (!(live >> (pos / S::ROWS * 8 + pos % S::ROWS) & 1)) p[e] = -INFINITY;
                 }
             float top = p[0];
 #pragma unroll
@@ -310,7 +319,7 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
                 l += p[e];
             }
             if (x == 0) s_old[h] = old;
-            uint8_t *to = weights + ((u * 2 + (h >> 3)) * 32 + (h & 7) * 4 + y) * S::PENTRY + j0 * 2;
+            uint8_t *to = weights + ((u * 2 + (h >> 3)) * 32 + (h & 7) * 4 + y) * S::PENTRY + s0 * 2;
 #pragma unroll
             for (int e = 0; e < E; e += 2) {
                 const uint32_t hi = pack<S::MT>(p[e], p[e + 1]);
@@ -323,7 +332,7 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
         }
         __syncthreads();
 
-        // values: k elements (2t, 2t + 1, 2t + 8, 2t + 9) of a product are positions t, t + 4, t + 8, t + 12
+        // values: k elements (2t, 2t + 1, 2t + 8, 2t + 9) of a product are the positions of an entry
         {
             float old[2][2];
             bool moved = false;
@@ -352,7 +361,7 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
 #pragma unroll
                 for (int n = 0; n < 2; ++n) shared_read(p[n], my_weights + (u * 2 + n) * 32 * S::PENTRY);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) shared_read(v[j], my_values + (u * 16 + j * 4) * S::PITCH);
+                for (int j = 0; j < 4; ++j) shared_read(v[j], my_values + (u * 16 + entry_position(j)) * S::PITCH);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     uint32_t av[4];
@@ -376,7 +385,7 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
             }
         }
 
-        const bool ends = cur.tile + 1 == cur.tiles;
+        const bool ends = --tiles_left == 0;
         if (ends || k + 1 == n_tiles) {
 #pragma unroll
             for (int d = 1; d < 16; d <<= 1) l += __shfl_xor_sync(~0u, l, d);
@@ -385,7 +394,7 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
                 s_l[h] = l;
             }
             __syncthreads();
-            const int32_t kvh = cur.seg / sets, first = cur.seg % sets * kLatentHeads, head0 = kvh * group + first;
+            const int32_t kvh = s_cur.seg / sets, first = s_cur.seg % sets * kLatentHeads, head0 = kvh * group + first;
             const int32_t heads = min(group - first, kLatentHeads);
             if (ends && begun) {
 #pragma unroll
@@ -400,10 +409,10 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
                         y.y = pack<S::IO>(o[1][n][i] * inv, o[1][n][2 + i] * inv);
                         y.z = pack<S::IO>(o[2][n][i] * inv, o[2][n][2 + i] * inv);
                         y.w = pack<S::IO>(o[3][n][i] * inv, o[3][n][2 + i] * inv);
-                        *reinterpret_cast<uint4 *>(a.out + cur.r * a.out_stride + ((int64_t)(head0 + qh) * a.v_dim + d) * 2) = y;
+                        *reinterpret_cast<uint4 *>(a.out + s_cur.r * a.out_stride + ((int64_t)(head0 + qh) * a.v_dim + d) * 2) = y;
                     }
                 if (a.lse && threadIdx.x < heads)
-                    a.lse[(int64_t)cur.r * a.n_q_heads + head0 + threadIdx.x] =
+                    a.lse[(int64_t)s_cur.r * a.n_q_heads + head0 + threadIdx.x] =
                         s_l[threadIdx.x] == 0.0f ? -INFINITY : (s_m[threadIdx.x] + log2f(s_l[threadIdx.x])) * kLn2;
             } else {
                 uint8_t *const part = parts + (size_t)(blockIdx.x * 2 + begun) * kLatentPartial;
@@ -421,133 +430,119 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
                     __stcg(ml + threadIdx.x, s_m[threadIdx.x]);
                     __stcg(ml + kLatentHeads + threadIdx.x, s_l[threadIdx.x]);
                 }
-                if (begun) {
-                    last_r = cur.r;
-                    last_seg = cur.seg;
-                    last_pieces = batch.split.cta_of(cur.seg_begin(segs) + cur.tiles - 1) - blockIdx.x + 1;
-                }
+                if (begun && threadIdx.x == 0)
+                    opened = OpenSegment{s_cur.r, s_cur.seg,
+                                         batch.split.cta_of(s_cur.seg_begin(segs) + s_cur.tiles - 1) - (int32_t)blockIdx.x + 1, 0};
             }
         }
         if (k + 1 < n_tiles) {
-            cur.next(a, segs);
-            __syncthreads();                                       // nobody reads this stage any more
-            if (w == 0 && k + 2 < n_tiles) {
-                copy_tile(stage);
-                far.next(a, segs);
-                if (k + 3 < n_tiles) lookup();
-            }
+            __syncthreads();                                       // nobody reads this stage, or s_cur, any more
+            if (k + 2 < n_tiles) copy_rows(stage);
+            if (k + 3 < n_tiles) lookup();
             if (ends) {
+                if (threadIdx.x == 0) {
+                    s_cur.tile = s_cur.tiles - 1;                  // only kept for the segment's ends
+                    s_cur.next(a, segs);
+                }
+                __syncthreads();
                 begun = true;
+                tiles_left = s_cur.tiles;
                 load_q();
             }
         }
     }
     if (s_timeout && threadIdx.x == 0) atomicAdd(a.pool.skipped + 1, 1ull);
-    if (threadIdx.x == 0) open[blockIdx.x] = OpenSegment{last_r, last_seg, s_timeout ? 0 : last_pieces, 0};
+    if (threadIdx.x == 0) open[blockIdx.x] = s_timeout ? OpenSegment{0, 0, 0, 0} : opened;
 }
 
-// Joins the segments that go over several CTAs: 64 value elements of one segment at a time, 256 threads for its float4s four
-// times over, each with every fourth piece.
-constexpr int kJoinThreads = 1024, kJoinGroups = kJoinThreads / 256, kJoinPieces = 256;
+// Joins the segments that go over several CTAs: 64 float4s of a segment's sums at a time, in four groups of 64 threads that take
+// every fourth piece.
+constexpr int kJoinThreads = 256, kJoinSlices = kLatentFloat4 / 64, kJoinCtas = 8;      // CTAs per SM
+constexpr int kJoinList = 512;                                                          // at least the CTAs of the first kernel
 
-template <int IO> __global__ void __launch_bounds__(kJoinThreads, 1) kvx_attend_latent_join(const __grid_constant__ AttendArgs a, int ctas) {
-    __shared__ int32_t s_list[kJoinThreads], s_count[kJoinThreads / 32], s_n;
-    __shared__ float s_w[kJoinPieces][kLatentHeads];           // weights of 256 pieces at a time
-    __shared__ float4 s_o[kJoinGroups - 1][256];
-    __shared__ float s_l[kLatentHeads], s_m[kLatentHeads];
+template <int IO> __global__ void __launch_bounds__(kJoinThreads) kvx_attend_latent_join(const __grid_constant__ AttendArgs a, int ctas) {
+    __shared__ int32_t s_list[kJoinList], s_count[kJoinList / 32];
+    __shared__ float4 s_o[4][64];
+    __shared__ float s_top[4][64], s_sum[4][64];
     wait_for_earlier();
     const OpenSegment *const open = (const OpenSegment *)a.scratch;
     const uint8_t *const parts = a.scratch + kScratchCounters * sizeof(uint32_t);
     const int32_t group = a.n_q_heads / a.n_kv_heads, sets = (group + kLatentHeads - 1) / kLatentHeads;
+    int n_open = 0;
     {                                                              // in order: every CTA has to number them alike
-        const uint32_t found = __ballot_sync(~0u, (int)threadIdx.x < ctas && open[threadIdx.x].pieces > 0);
-        if ((threadIdx.x & 31) == 0) s_count[threadIdx.x >> 5] = __popc(found);
+        uint32_t found[kJoinList / kJoinThreads];
+#pragma unroll
+        for (int i = 0; i < kJoinList / kJoinThreads; ++i) {
+            const int c = i * kJoinThreads + threadIdx.x;
+            found[i] = __ballot_sync(~0u, c < ctas && open[c].pieces > 0);
+            if ((threadIdx.x & 31) == 0) s_count[c >> 5] = __popc(found[i]);
+        }
         __syncthreads();
-        int before = 0;
-        for (int i = 0; i < (int)(threadIdx.x >> 5); ++i) before += s_count[i];
-        if (found >> (threadIdx.x & 31) & 1) s_list[before + __popc(found & ((1u << (threadIdx.x & 31)) - 1))] = threadIdx.x;
-        if (threadIdx.x == kJoinThreads - 1) s_n = before + __popc(found);
+        for (int y = 0; y < kJoinList / 32; ++y) {
+#pragma unroll
+            for (int i = 0; i < kJoinList / kJoinThreads; ++i)
+                if (y == (i * kJoinThreads + (int)threadIdx.x) >> 5 && found[i] >> (threadIdx.x & 31) & 1)
+                    s_list[n_open + __popc(found[i] & ((1u << (threadIdx.x & 31)) - 1))] = i * kJoinThreads + threadIdx.x;
+            n_open += s_count[y];
+        }
         __syncthreads();
     }
-    for (int item = blockIdx.x; item < s_n * kLatentWarps; item += gridDim.x) {
-        const int cta = s_list[item / kLatentWarps], w = item % kLatentWarps;
+    const int f = threadIdx.x & 63, part = threadIdx.x >> 6, lane = f & 31, t = lane & 3, g = lane >> 2;
+    for (int item = blockIdx.x; item < n_open * kJoinSlices; item += gridDim.x) {
+        const int cta = s_list[item / kJoinSlices], slice = item % kJoinSlices;
         const OpenSegment seg = open[cta];
-        auto part = [&](int x) { return parts + (size_t)((cta + x) * 2 + (x == 0)) * kLatentPartial; };
-        auto ml = [&](int x) { return (const float *)(part(x) + kLatentFloat4 * 16); };
-        const int f = threadIdx.x & 255, piece0 = threadIdx.x >> 8;
-        const int n = f >> 7, i = f >> 6 & 1, e4 = f >> 5 & 1, lane = f & 31, t = lane & 3, g = lane >> 2, q = n * 8 + 2 * t + i;
-        // maxima and sums: head threadIdx / 64, 64 threads each
-        {
-            const int hq = threadIdx.x >> 6, y = threadIdx.x & 63;
-            float top = -INFINITY, l = 0.0f;
-            for (int x = y; x < seg.pieces; x += 64) top = fmaxf(top, __ldcg(ml(x) + hq));
-            __syncthreads();
-            float *const red = &s_w[0][0];
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-            if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
-            __syncthreads();
-            top = fmaxf(red[hq * 2], red[hq * 2 + 1]);
-            const float ref = top == -INFINITY ? 0.0f : top;
-            for (int x = y; x < seg.pieces; x += 64) l += fast_exp2(__ldcg(ml(x) + hq) - ref) * __ldcg(ml(x) + kLatentHeads + hq);
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) l += __shfl_xor_sync(~0u, l, d);
-            __syncthreads();
-            if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = l;
-            __syncthreads();
-            if (y == 0) {
-                s_m[hq] = top;
-                s_l[hq] = red[hq * 2] + red[hq * 2 + 1];
-            }
-        }
+        const int q = (slice >> 1 & 1) * 8 + 2 * t + (slice & 1), d = (slice >> 2) * 64 + g * 8 + (f >> 5) * 4;
+        const uint8_t *const first = parts + (size_t)(2 * cta + 1) * kLatentPartial;         // the others: slot 0 of the CTAs after it
+        auto at = [&](int x) { return x ? first + (size_t)(2 * x - 1) * kLatentPartial : first; };
+        float top = -INFINITY, l = 0.0f;
         float4 o = make_float4(0, 0, 0, 0);
-        for (int x0 = 0; x0 < seg.pieces; x0 += kJoinPieces) {
-            const int here = min(seg.pieces - x0, kJoinPieces);
-            __syncthreads();
-            for (int y = threadIdx.x; y < here * kLatentHeads; y += kJoinThreads) {
-                const float top = s_m[y % kLatentHeads];
-                s_w[y / kLatentHeads][y % kLatentHeads] = fast_exp2(__ldcg(ml(x0 + y / kLatentHeads) + y % kLatentHeads) - (top == -INFINITY ? 0.0f : top));
-            }
-            __syncthreads();
-#pragma unroll 8
-            for (int x = piece0; x < here; x += kJoinGroups) {
-                const float4 y = __ldcg((const float4 *)part(x0 + x) + w * 256 + f);
-                const float z = s_w[x][q];
-                o.x += z * y.x;
-                o.y += z * y.y;
-                o.z += z * y.z;
-                o.w += z * y.w;
-            }
-        }
-        if (piece0) s_o[piece0 - 1][f] = o;
+#pragma unroll 4
+        for (int x = part; x < seg.pieces; x += 4) top = fmaxf(top, __ldcg((const float *)(at(x) + kLatentFloat4 * 16) + q));
+        s_top[part][f] = top;
         __syncthreads();
-        if (piece0 == 0) {
+        top = fmaxf(fmaxf(s_top[0][f], s_top[1][f]), fmaxf(s_top[2][f], s_top[3][f]));
+        const float ref = top == -INFINITY ? 0.0f : top;
+#pragma unroll 8
+        for (int x = part; x < seg.pieces; x += 4) {
+            const float *const ml = (const float *)(at(x) + kLatentFloat4 * 16);
+            const float4 y = __ldcg((const float4 *)at(x) + slice * 64 + f);
+            const float z = fast_exp2(__ldcg(ml + q) - ref);
+            l += z * __ldcg(ml + kLatentHeads + q);
+            o.x += z * y.x;
+            o.y += z * y.y;
+            o.z += z * y.z;
+            o.w += z * y.w;
+        }
+        s_o[part][f] = o;
+        s_sum[part][f] = l;
+        __syncthreads();
+        if (part == 0) {
 #pragma unroll
-            for (int x = 0; x < kJoinGroups - 1; ++x) {
-                const float4 y = s_o[x][f];
+            for (int i = 1; i < 4; ++i) {
+                const float4 y = s_o[i][f];
                 o = make_float4(o.x + y.x, o.y + y.y, o.z + y.z, o.w + y.w);
+                l += s_sum[i][f];
             }
-            const int32_t first = seg.seg % sets * kLatentHeads, head = seg.seg / sets * group + first + q, d = w * 64 + g * 8 + e4 * 4;
-            if (first + q < group) {
-                const float l = s_l[q], inv = l == 0.0f ? 0.0f : a.v_scale / l;
+            const int32_t in_group = seg.seg % sets * kLatentHeads + q, head = seg.seg / sets * group + in_group;
+            if (in_group < group) {
+                const float inv = l == 0.0f ? 0.0f : a.v_scale / l;
                 if (d < a.v_dim)
                     *reinterpret_cast<uint2 *>(a.out + seg.r * a.out_stride + ((int64_t)head * a.v_dim + d) * 2) =
                         make_uint2(pack<IO>(o.x * inv, o.y * inv), pack<IO>(o.z * inv, o.w * inv));
-                if (a.lse && w == 0 && e4 == 0 && g == 0)
-                    a.lse[(int64_t)seg.r * a.n_q_heads + head] = l == 0.0f ? -INFINITY : (s_m[q] + log2f(l)) * kLn2;
+                if (a.lse && d == 0) a.lse[(int64_t)seg.r * a.n_q_heads + head] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
             }
         }
-        __syncthreads();
     }
 }
 
 size_t latent_scratch_bytes(int32_t sms) { return kScratchCounters * sizeof(uint32_t) + (size_t)4 * sms * kLatentPartial; }
 
 template <class S> static cudaError_t launch(const AttendArgs &a, int32_t sms, cudaStream_t stream) {
+    if (2 * sms > kJoinList) return cudaErrorInvalidValue;
     static const cudaError_t set = cudaFuncSetAttribute(kvx_attend_latent<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
     if (set != cudaSuccess) return set;
     const cudaError_t e = launch_after(kvx_attend_latent<S>, dim3(2 * sms), kLatentThreads, S::BYTES, stream, a);
-    return e != cudaSuccess ? e : launch_after(kvx_attend_latent_join<S::IO>, dim3(sms), kJoinThreads, 0, stream, a, 2 * sms);
+    return e != cudaSuccess ? e : launch_after(kvx_attend_latent_join<S::IO>, dim3(kJoinCtas * sms), kJoinThreads, 0, stream, a, 2 * sms);
 }
 
 cudaError_t launch_attend_latent(const AttendArgs &a, int32_t vt, int32_t io, int32_t sms, cudaStream_t stream) {
