@@ -32,11 +32,9 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     return y;
 }
 
-// Two 8-bit codes to two f16 values (exact).
-__device__ __forceinline__ uint32_t f16_of_codes(uint32_t two) {
-    uint32_t y;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"((uint16_t)two));
-    return y;
+// The four f16 values that a register of 8-bit codes stands for (exact).
+__device__ __forceinline__ void f16_of_codes(uint32_t x, uint32_t &lo, uint32_t &hi) {
+    asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %2;\ncvt.rn.f16x2.e4m3x2 %0, l;\ncvt.rn.f16x2.e4m3x2 %1, h;\n}" : "=r"(lo), "=r"(hi) : "r"(x));
 }
 
 template <int VT> __device__ __forceinline__ uint32_t pack(float lo, float hi) {

@@ -370,8 +370,8 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
                     for (int i = 0; i < S::KSTEP; ++i) {
                         uint32_t a0, a1, a2, a3;
                         if constexpr (S::F8) {
-                            a0 = f16_of_codes(k[0][i]), a2 = f16_of_codes(k[0][i] >> 16);
-                            a1 = f16_of_codes(k[1][i]), a3 = f16_of_codes(k[1][i] >> 16);
+                            f16_of_codes(k[0][i], a0, a2);
+                            f16_of_codes(k[1][i], a1, a3);
                         } else {
                             a0 = k[0][2 * i], a2 = k[0][2 * i + 1], a1 = k[1][2 * i], a3 = k[1][2 * i + 1];
                         }
@@ -452,8 +452,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
                         for (int j = 0; j < 2; ++j) {
                             if constexpr (S::F8) {
                                 const uint32_t x = __byte_perm(v[2 * j][e / 2], v[2 * j + 1][e / 2], e & 1 ? 0x7362 : 0x5140);
-                                av[2 * j] = f16_of_codes(x);
-                                av[2 * j + 1] = f16_of_codes(x >> 16);
+                                f16_of_codes(x, av[2 * j], av[2 * j + 1]);
                             } else {
                                 av[2 * j] = __byte_perm(v[2 * j][e], v[2 * j + 1][e], 0x5410);
                                 av[2 * j + 1] = __byte_perm(v[2 * j][e], v[2 * j + 1][e], 0x7632);

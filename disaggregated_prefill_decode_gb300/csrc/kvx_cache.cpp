@@ -11,11 +11,23 @@ using namespace kvx;
 
 static bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
+// x / d = (mulhi(x, mul) + x) >> shift for x below 2^31.
+static void divisor(uint32_t d, uint32_t *mul, uint32_t *shift) {
+    uint32_t s = 0;
+    while (((uint64_t)1 << s) < d) ++s;
+    *shift = s;
+    *mul = (uint32_t)(((((uint64_t)1 << s) - d) << 32) / d + 1);
+}
+
+// Multiprocessors of the current device, asked for once.
 static kvx_status device_sms(int32_t *device, int32_t *sms) {
+    static std::atomic<int32_t> known[64];
     int dev = 0, n = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess && dev < 64) n = known[dev].load(std::memory_order_relaxed);
+    if (e == cudaSuccess && !n) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
     *device = dev;
     *sms = n;
     return KVX_OK;
@@ -97,8 +109,9 @@ kvx_status kvx_slot_map(const int32_t *ctx_len, const int32_t *new_len, int32_t 
     int32_t device = 0, sms = 0;
     kvx_status st = device_sms(&device, &sms);
     if (st) return st;
-    const SlotArgs a = {ctx_len, new_len, free_blocks, block_table, positions, seq_len, tok_off, slots, result,
-                        n_free, table_stride, max_tokens, n_reqs, block_size, max_blocks};
+    SlotArgs a = {ctx_len, new_len, free_blocks, block_table, positions, seq_len, tok_off, slots, result,
+                  n_free, table_stride, max_tokens, n_reqs, block_size, max_blocks, 0, 0};
+    divisor((uint32_t)block_size, &a.block_mul, &a.block_shift);
     const cudaError_t e = launch_slot_map(a, sms, stream);
     return e == cudaSuccess ? KVX_OK : cuda_fail(e, "launching the slot map");
 }
@@ -256,10 +269,7 @@ kvx_status kvx_cache_attend(kvx_cache_t c, int32_t layer, const void *q, int64_t
     a.window = f.window;
     a.scale = (float)((double)f.scale * (double)f.k_scale * 1.4426950408889634);
     a.v_scale = f.v_scale;
-    uint32_t shift = 0;
-    while (((uint64_t)1 << shift) < (uint64_t)g.block_size) ++shift;
-    a.block_shift = shift;
-    a.block_mul = (uint32_t)(((((uint64_t)1 << shift) - g.block_size) << 32) / g.block_size + 1);
+    divisor((uint32_t)g.block_size, &a.block_mul, &a.block_shift);
     a.block_pitch16 = (uint32_t)(a.pool.block_pitch / 16);
     a.token_pitch16 = (uint32_t)(a.pool.token_pitch / 16);
     a.latent = g.n_planes == 1;

@@ -191,6 +191,7 @@ struct SlotArgs {
     kvx_slot_result *result;
     int64_t n_free, table_stride, max_tokens;
     int32_t n_reqs, block_size, max_blocks;
+    uint32_t block_mul, block_shift;  // as in AttendArgs
 };
 cudaError_t launch_slot_map(const SlotArgs &a, int32_t sms, cudaStream_t stream);      // kvx_slots.cu
 

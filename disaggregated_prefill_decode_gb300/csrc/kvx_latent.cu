@@ -240,8 +240,8 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
             for (int y = 0; y < S::KSTEP; ++y) {
                 uint32_t a0, a1, a2, a3;
                 if constexpr (S::F8) {
-                    a0 = f16_of_codes(ka[0][y]), a2 = f16_of_codes(ka[0][y] >> 16);
-                    a1 = f16_of_codes(ka[1][y]), a3 = f16_of_codes(ka[1][y] >> 16);
+                    f16_of_codes(ka[0][y], a0, a2);
+                    f16_of_codes(ka[1][y], a1, a3);
                 } else {
                     a0 = ka[0][2 * y], a2 = ka[0][2 * y + 1], a1 = ka[1][2 * y], a3 = ka[1][2 * y + 1];
                 }
@@ -369,8 +369,7 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
                     for (int j = 0; j < 2; ++j) {
                         if constexpr (S::F8) {
                             const uint32_t z = __byte_perm(v[2 * j][e / 2], v[2 * j + 1][e / 2], e & 1 ? 0x7362 : 0x5140);
-                            av[2 * j] = f16_of_codes(z);
-                            av[2 * j + 1] = f16_of_codes(z >> 16);
+                            f16_of_codes(z, av[2 * j], av[2 * j + 1]);
                         } else {
                             av[2 * j] = __byte_perm(v[2 * j][e], v[2 * j + 1][e], 0x5410);
                             av[2 * j + 1] = __byte_perm(v[2 * j][e], v[2 * j + 1][e], 0x7632);

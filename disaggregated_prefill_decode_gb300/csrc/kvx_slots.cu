@@ -5,9 +5,9 @@
 // exclusive sums of need - had and new over the requests before it.
 //
 // Every CTA takes the sums over all requests itself, kReqs at a time in shared memory, and then writes
-// its share of the outputs: output tiles go round-robin over the CTAs, and a token or block finds its
-// request by bisection of the sums. So nothing is handed from CTA to CTA and no scratch is needed; the
-// repeated reads are 8 bytes per request and CTA, from L2.
+// its share of the outputs: output tiles go round-robin over the warps, and a tile finds its request by
+// bisection of the sums (by the warp, then a lane among the requests of its tile). So nothing is handed
+// from CTA to CTA and no scratch is needed; the repeated reads are 8 bytes per request and CTA, from L2.
 #include "kvx_launch.cuh"
 
 #include <algorithm>
@@ -15,8 +15,9 @@
 namespace kvx {
 
 constexpr int kSlotThreads = 256;
-constexpr int kReqs = 1024;            // requests per pass over shared memory
-constexpr int kTokTile = 2 * kSlotThreads;
+constexpr int kReqs = 1024;            // requests per pass over shared memory (at most: warp_last_at_most)
+constexpr int kTokTile = 256;          // tokens of a warp: two neighbours per lane, four times
+constexpr int kTokRounds = kTokTile / 64;
 
 struct Sums { int64_t tok, blk; };
 
@@ -54,13 +55,17 @@ __device__ __forceinline__ int last_at_most(const int64_t *off, int n, int64_t x
     return lo;
 }
 
+// The same by a whole warp, n up to 1024.
+__device__ __forceinline__ int warp_last_at_most(const int64_t *off, int n, int64_t x) {
+    const int lane = threadIdx.x & 31, step = (n + 31) / 32;
+    const int lo = (31 - __clz(__ballot_sync(~0u, lane * step < n && off[min(lane * step, n - 1)] <= x))) * step;
+    return lo + 31 - __clz(__ballot_sync(~0u, lane < step && lo + lane < n && off[min(lo + lane, n - 1)] <= x));
+}
+
 __device__ __forceinline__ uint32_t blocks_of(uint32_t tokens, uint32_t bs) { return tokens ? (tokens - 1) / bs + 1 : 0; }
 
-// First tile at or after `lo` that is this CTA's.
-__device__ __forceinline__ int64_t first_tile(int64_t lo) {
-    const int64_t g = gridDim.x;
-    return lo + ((int64_t)blockIdx.x - lo % g + g) % g;
-}
+// First tile at or after `lo` that is number `mine` of `of`.
+__device__ __forceinline__ int64_t first_tile(int64_t lo, int64_t mine, int64_t of) { return lo + (mine - lo % of + of) % of; }
 
 __global__ void __launch_bounds__(kSlotThreads) kvx_slot_map_kernel(const SlotArgs a) {
     __shared__ int64_t s_tok[kReqs], s_blk[kReqs];      // sums before each request, within the pass
@@ -106,7 +111,7 @@ __global__ void __launch_bounds__(kSlotThreads) kvx_slot_map_kernel(const SlotAr
             }
 
         const int64_t b_end = base.blk + total.blk;
-        for (int64_t tile = first_tile(base.blk / kSlotThreads); tile * kSlotThreads < b_end; tile += gridDim.x) {
+        for (int64_t tile = first_tile(base.blk / kSlotThreads, blockIdx.x, gridDim.x); tile * kSlotThreads < b_end; tile += gridDim.x) {
             const int64_t b = tile * kSlotThreads + threadIdx.x;
             if (b < base.blk || b >= b_end) continue;
             const int i = last_at_most(s_blk, m, b - base.blk);
@@ -115,37 +120,56 @@ __global__ void __launch_bounds__(kSlotThreads) kvx_slot_map_kernel(const SlotAr
         }
 
         const int64_t t_end = min(base.tok + total.tok, a.max_tokens);
-        for (int64_t tile = first_tile(base.tok / kTokTile); tile * kTokTile < t_end; tile += gridDim.x) {
-            const int64_t t0 = tile * kTokTile + 2 * threadIdx.x;
-            int64_t slot[2] = {-1, -1};
-            int32_t pos[2] = {0, 0};
-            if (t0 + 1 < base.tok || t0 >= t_end) continue;
-            int i = last_at_most(s_tok, m, max(t0, base.tok) - base.tok);
+        const int lane = threadIdx.x & 31, warps = gridDim.x * (kSlotThreads / 32);
+        for (int64_t tile = first_tile(base.tok / kTokTile, (int64_t)(threadIdx.x >> 5) * gridDim.x + blockIdx.x, warps);
+             tile * kTokTile < t_end; tile += warps) {
+            const int64_t first = tile * kTokTile, from = max(first, base.tok), upto = min(first + kTokTile, t_end);
+            const int r_lo = warp_last_at_most(s_tok, m, from - base.tok), r_hi = warp_last_at_most(s_tok, m, upto - 1 - base.tok);
+            int32_t blk[kTokRounds][2], rest[kTokRounds][2], pos[kTokRounds][2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int64_t t = t0 + u - base.tok;
-                if (t < 0 || t0 + u >= t_end) continue;
-                while (i + 1 < m && s_tok[i + 1] <= t) ++i;
-                pos[u] = s_ctx[i] + (int32_t)(t - s_tok[i]);
-                const int32_t col = (int32_t)((uint32_t)pos[u] / bs), had = s_had[i];
-                int32_t blk = -1;
-                if (col < had) blk = a.block_table[(r0 + i) * a.table_stride + col];
-                else if (col < a.max_blocks) {
-                    const int64_t b = base.blk + s_blk[i] + (col - had);
-                    if (b < a.n_free) blk = a.free_blocks[b];
-                }
-                if (blk >= 0) slot[u] = (int64_t)blk * bs + (uint32_t)(pos[u] - col * (int32_t)bs);
-            }
-            if (pairs && t0 >= base.tok && t0 + 1 < t_end) {
-                *reinterpret_cast<longlong2 *>(a.slots + t0) = make_longlong2(slot[0], slot[1]);
-                if (a.positions) *reinterpret_cast<int2 *>(a.positions + t0) = make_int2(pos[0], pos[1]);
-            } else {
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    if (t0 + u >= base.tok && t0 + u < t_end) {
-                        a.slots[t0 + u] = slot[u];
-                        if (a.positions) a.positions[t0 + u] = pos[u];
+            for (int u = 0; u < kTokRounds; ++u) {
+                const int64_t x = first - base.tok + 64 * u + 2 * lane;     // of the first of two tokens
+                int i = r_lo;
+                if (r_lo < r_hi) {                                 // the tile has tokens of several requests
+                    int hi = r_hi + 1;
+                    while (hi - i > 1) {
+                        const int mid = (i + hi) >> 1;
+                        if (s_tok[mid] <= x) i = mid; else hi = mid;
                     }
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    while (k && i < r_hi && s_tok[i + 1] <= x + 1) ++i;
+                    const int32_t p = s_ctx[i] + (int32_t)(x + k - s_tok[i]), had = s_had[i];
+                    const int32_t col = (int32_t)((__umulhi((uint32_t)p, a.block_mul) + (uint32_t)p) >> a.block_shift);
+                    pos[u][k] = p;
+                    rest[u][k] = p - col * (int32_t)bs;
+                    blk[u][k] = -1;
+                    if (k && rest[u][1] && x + 1 > s_tok[i]) blk[u][1] = blk[u][0];     // in the block of the token before
+                    else if (x + k + base.tok >= from && x + k + base.tok < upto) {
+                        const int64_t b = base.blk + s_blk[i] + (col - had);
+                        if (col < had) blk[u][k] = a.block_table[(r0 + i) * a.table_stride + col];
+                        else if (col < a.max_blocks && b < a.n_free) blk[u][k] = a.free_blocks[b];
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kTokRounds; ++u) {
+                const int64_t t = first + 64 * u + 2 * lane;
+                int64_t slot[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) slot[k] = blk[u][k] < 0 ? -1 : (int64_t)blk[u][k] * bs + rest[u][k];
+                if (pairs && t >= from && t + 1 < upto) {
+                    *reinterpret_cast<longlong2 *>(a.slots + t) = make_longlong2(slot[0], slot[1]);
+                    if (a.positions) *reinterpret_cast<int2 *>(a.positions + t) = make_int2(pos[u][0], pos[u][1]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (t + k >= from && t + k < upto) {
+                            a.slots[t + k] = slot[k];
+                            if (a.positions) a.positions[t + k] = pos[u][k];
+                        }
+                }
             }
         }
 
@@ -173,7 +197,8 @@ __global__ void __launch_bounds__(kSlotThreads) kvx_slot_map_kernel(const SlotAr
 }
 
 cudaError_t launch_slot_map(const SlotArgs &a, int32_t sms, cudaStream_t stream) {
-    const int64_t tiles = std::max((a.max_tokens + kTokTile - 1) / kTokTile, (int64_t)(a.n_reqs + 1023) / 1024);
+    // a CTA for every 8 tiles, or 4 tokens a thread where there are few
+    const int64_t tiles = std::max((a.max_tokens + 1023) / 1024, (int64_t)(a.n_reqs + 1023) / 1024);
     const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, 4 * sms));
     return launch_after(kvx_slot_map_kernel, dim3(grid), kSlotThreads, 0, stream, a);
 }

@@ -199,9 +199,10 @@ def _ptr(x) -> int:
     """Device pointer of a torch tensor, or an int passed through. None -> 0."""
     if x is None:
         return 0
-    if isinstance(x, (int, np.integer)):
+    try:
+        return x.data_ptr()
+    except AttributeError:
         return int(x)
-    return int(x.data_ptr())
 
 
 def _stream(s) -> int:
