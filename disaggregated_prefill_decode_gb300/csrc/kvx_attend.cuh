@@ -102,10 +102,11 @@ template <int TOK> struct Span {
     }
 };
 
-// Where a tile stands in the line.
-template <int TOK> struct Place {
+// Where a tile stands in the line. A segment has EXTRA places after its tiles, for what the change to the next one costs: they
+// make the stretches even in time.
+template <int TOK, int EXTRA> struct Place {
     int32_t r, seg, tile;      // request, segment of the request, tile of the segment
-    int64_t before;            // tiles of the requests before r, per segment
+    int64_t before;            // places of the requests before r, per segment
     int32_t len, first, tiles;
     __device__ __forceinline__ void request(const AttendArgs &a) {
         const Span<TOK> s(a, r);
@@ -113,15 +114,18 @@ template <int TOK> struct Place {
         first = s.first;
         tiles = s.tiles;
     }
-    __device__ __forceinline__ void next(const AttendArgs &a, int32_t segs) {
+    // To the next tile, and x with it.
+    __device__ __forceinline__ void next(const AttendArgs &a, int32_t segs, int64_t &x) {
+        ++x;
         if (++tile < tiles) return;
+        x += EXTRA;
         tile = 0;
         if (++seg < segs) return;
         seg = 0;
-        before += tiles;
+        before += tiles + EXTRA;
         if (++r < a.n_reqs) request(a);
     }
-    __device__ __forceinline__ int64_t seg_begin(int32_t segs) const { return before * segs + (int64_t)seg * tiles; }
+    __device__ __forceinline__ int64_t seg_begin(int32_t segs) const { return before * segs + (int64_t)seg * (tiles + EXTRA); }
 };
 
 __device__ __forceinline__ int64_t warp_inclusive(int64_t x) {
@@ -154,7 +158,7 @@ template <int WARPS> __device__ __forceinline__ int64_t cta_exclusive(int64_t x,
 // The batch as a CTA sees it: the split over gridDim.x CTAs (of at least MIN tiles each), and how to find a place in it.
 // Up to 256 requests each warp keeps all the sums, a lane those of up to 8 consecutive requests, with no barrier; beyond that
 // the CTA looks for the request in which its own stretch begins, and its warps go on from there.
-template <int TOK, int WARPS, int MIN> struct Batch {
+template <int TOK, int WARPS, int MIN, int EXTRA> struct Batch {
     static constexpr int PER = 8;
     Split split;
     int32_t per;                       // requests of a lane
@@ -173,14 +177,14 @@ template <int TOK, int WARPS, int MIN> struct Batch {
 #pragma unroll
             for (int k = 0; k < PER; ++k) {
                 const int32_t r = lane * per + k;
-                tiles[k] = k < per && r < a.n_reqs ? Span<TOK>(a, r).tiles : 0;
+                tiles[k] = k < per && r < a.n_reqs ? Span<TOK>(a, r).tiles + EXTRA : 0;
                 mine += tiles[k];
             }
             upto = warp_inclusive(mine);
             total = __shfl_sync(~0u, upto, 31);
         } else {
             int64_t mine = 0;
-            for (int32_t r = threadIdx.x; r < a.n_reqs; r += 32 * WARPS) mine += Span<TOK>(a, r).tiles;
+            for (int32_t r = threadIdx.x; r < a.n_reqs; r += 32 * WARPS) mine += Span<TOK>(a, r).tiles + EXTRA;
             cta_exclusive<WARPS>(mine, &total);
         }
         split.tiles = total * segs;
@@ -198,7 +202,7 @@ template <int TOK, int WARPS, int MIN> struct Batch {
         int64_t base = 0, total;
         for (int32_t c = 0; c < a.n_reqs && base <= y; c += 32 * WARPS) {
             const int32_t r = c + threadIdx.x;
-            const int64_t mine = r < a.n_reqs ? Span<TOK>(a, r).tiles : 0, ex = base + cta_exclusive<WARPS>(mine, &total);
+            const int64_t mine = r < a.n_reqs ? Span<TOK>(a, r).tiles + EXTRA : 0, ex = base + cta_exclusive<WARPS>(mine, &total);
             if (ex <= y && y < ex + mine) {
                 s_r = r;
                 s_before = ex;
@@ -210,11 +214,11 @@ template <int TOK, int WARPS, int MIN> struct Batch {
         before0 = s_before;
     }
 
-    // Whole warp: the place of tile x of the line.
-    __device__ __forceinline__ Place<TOK> locate(const AttendArgs &a, int32_t segs, int64_t x) const {
+    // Whole warp: the first tile at or after place x of the line, to which x is moved.
+    __device__ __forceinline__ Place<TOK, EXTRA> locate(const AttendArgs &a, int32_t segs, int64_t &x) const {
         const int lane = threadIdx.x & 31;
         const int64_t y = divide(x, segs);
-        Place<TOK> p;
+        Place<TOK, EXTRA> p;
         if (per <= PER) {
             const int at = __ffs(__ballot_sync(~0u, upto > y)) - 1;
             int64_t left = upto;
@@ -228,7 +232,7 @@ template <int TOK, int WARPS, int MIN> struct Batch {
             int32_t r = r0;
             int64_t before = before0;
             for (;;) {
-                const int64_t n = r + lane < a.n_reqs ? Span<TOK>(a, r + lane).tiles : 0;
+                const int64_t n = r + lane < a.n_reqs ? Span<TOK>(a, r + lane).tiles + EXTRA : 0;
                 const int64_t in = before + warp_inclusive(n);
                 const uint32_t past = __ballot_sync(~0u, in > y);
                 const int at = past ? __ffs(past) - 1 : 31;
@@ -244,8 +248,13 @@ template <int TOK, int WARPS, int MIN> struct Batch {
         }
         p.request(a);
         const int64_t rest = x - p.before * segs;
-        p.seg = (int32_t)divide(rest, p.tiles);
-        p.tile = (int32_t)(rest - (int64_t)p.seg * p.tiles);
+        p.seg = (int32_t)divide(rest, p.tiles + EXTRA);
+        p.tile = (int32_t)(rest - (int64_t)p.seg * (p.tiles + EXTRA));
+        if (p.tile >= p.tiles) {
+            x -= p.tile - (p.tiles - 1);
+            p.tile = p.tiles - 1;
+            p.next(a, segs, x);
+        }
         return p;
     }
 };

@@ -19,6 +19,7 @@
 namespace kvx {
 
 constexpr int kSharedBytes = 226 << 10;       // of a CTA, one per SM
+constexpr int kSwitchTiles = 2;               // what the change to another segment costs a warp, in tiles: outputs, then queries
 
 template <int VT_, int IO_, int D_, int NT_, bool FULL_> struct Shape {
     static constexpr int VT = VT_, IO = IO_, D = D_, NT = NT_;   // D: head_dim rounded up; NT: query sets of 8
@@ -81,83 +82,134 @@ struct Pieces {
     __device__ __forceinline__ uint8_t *at(int x) const { return x ? others + x * step : first; }
 };
 
-// One warp: float4 f of every lane of some partial results, joined into the outputs or into another partial result. They lie in
-// shared memory, or in the scratch, where other CTAs put them: then they come from L2, and more of them at once. Lane (g, t)
-// takes the maxima and sums of every eighth for its query, the others' weights come by shuffles.
+// What one lane has of a join: float4 f of the sums, for query q.
+template <class S> struct Joined {
+    int f, q, e4;
+    float top, l;
+    float4 o;
+    __device__ __forceinline__ explicit Joined(int f_) : f(f_), top(-INFINITY), l(0.0f), o(make_float4(0, 0, 0, 0)) {
+        const int t = threadIdx.x & 3, i = f % S::F4 / (S::F4 / 2);
+        e4 = f % (S::F4 / 2);
+        q = f / S::F4 * 8 + 2 * t + i;
+    }
+    // Into another partial result, or, without one, the outputs.
+    __device__ __forceinline__ void put(const AttendArgs &a, uint8_t *to, int32_t r, int32_t head0, int32_t heads) const {
+        const int lane = threadIdx.x & 31, g = lane >> 2;
+        if (!to) {
+            const int d = S::dim(g, e4 * 4);
+            if (q < heads && (S::FULL || d < a.head_dim)) {
+                const float inv = l == 0.0f ? 0.0f : a.v_scale / l;
+                const uint2 y = make_uint2(pack<S::IO>(o.x * inv, o.y * inv), pack<S::IO>(o.z * inv, o.w * inv));
+                *reinterpret_cast<uint2 *>(a.out + r * a.out_stride + ((int64_t)(head0 + q) * a.head_dim + d) * 2) = y;
+            }
+            if (q < heads && e4 == 0 && g == 0) write_lse<S>(a, r, head0 + q, top, l);
+        } else {
+            const Partial<S> p(to);
+            __stcg(p.o + f * 32 + lane, o);
+            if (e4 == 0 && g == 0) {
+                __stcg(p.m + q, top);
+                __stcg(p.l + q, l);
+            }
+        }
+    }
+};
+
+// One warp: float4 f of a few partial results of this CTA's warps, or (SCRATCH) of other CTAs, which come from L2.
 template <class S, bool SCRATCH>
-__device__ __noinline__ void join(const AttendArgs &a, int f, const Pieces &from, uint8_t *to, int32_t r, int32_t head0, int32_t heads) {
-    constexpr int ROUNDS = SCRATCH ? 3 : 1;
-    const int lane = threadIdx.x & 31, t = lane & 3, g = lane >> 2, n = from.n;
-    const int set = f / S::F4, i = f % S::F4 / (S::F4 / 2), e4 = f % (S::F4 / 2), q = set * 8 + 2 * t + i;
+__device__ __forceinline__ Joined<S> join_few(int f, const Pieces &from) {
+    constexpr int AT_ONCE = 4;
+    Joined<S> j(f);
     auto get = [](const auto *p) {
         if constexpr (SCRATCH) return __ldcg(p);
         else return *p;
     };
-    float top = -INFINITY, l = 0.0f;
-    float4 o = make_float4(0, 0, 0, 0);
+    for (int x0 = 0; x0 < from.n; x0 += AT_ONCE) {
+        float4 y[AT_ONCE];
+        float m[AT_ONCE], l[AT_ONCE], up = j.top;
+#pragma unroll
+        for (int x = 0; x < AT_ONCE; ++x) {
+            m[x] = -INFINITY;
+            if (x0 + x < from.n) {
+                const Partial<S> p(from.at(x0 + x));
+                y[x] = get(p.o + f * 32 + (threadIdx.x & 31));
+                m[x] = get(p.m + j.q);
+                l[x] = get(p.l + j.q);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < AT_ONCE; ++x) up = fmaxf(up, m[x]);
+        const float ref = up == -INFINITY ? 0.0f : up, old = fast_exp2(j.top - ref);
+        j.top = up;
+        j.l *= old;
+        j.o = make_float4(j.o.x * old, j.o.y * old, j.o.z * old, j.o.w * old);
+#pragma unroll
+        for (int x = 0; x < AT_ONCE; ++x)
+            if (x0 + x < from.n) {
+                const float w = fast_exp2(m[x] - ref);
+                j.l += w * l[x];
+                j.o.x += w * y[x].x;
+                j.o.y += w * y[x].y;
+                j.o.z += w * y[x].z;
+                j.o.w += w * y[x].w;
+            }
+    }
+    return j;
+}
+
+// The same of many in the scratch, 24 at once: lane (g, t) takes the maxima and sums of every eighth for its query, the others'
+// weights come by shuffles.
+template <class S> __device__ __noinline__ Joined<S> join_many(int f, const Pieces &from) {
+    constexpr int ROUNDS = 3;
+    const int lane = threadIdx.x & 31, t = lane & 3, g = lane >> 2, n = from.n;
+    Joined<S> j(f);
     for (int x0 = 0; x0 < n; x0 += 8 * ROUNDS) {
         float4 y[ROUNDS][8];
-        float m[ROUNDS], s[ROUNDS], up = top;
+        float m[ROUNDS], s[ROUNDS], up = j.top;
 #pragma unroll
         for (int k = 0; k < ROUNDS; ++k) {
             const int x = x0 + 8 * k + g;
             const Partial<S> p(from.at(min(x, n - 1)));
-            m[k] = x < n ? get(p.m + q) : -INFINITY;
-            s[k] = x < n ? get(p.l + q) : 0.0f;
+            m[k] = x < n ? __ldcg(p.m + j.q) : -INFINITY;
+            s[k] = x < n ? __ldcg(p.l + j.q) : 0.0f;
             if (x0 + 8 * k < n) {
 #pragma unroll
-                for (int x = 0; x < 8; ++x) y[k][x] = get(Partial<S>(from.at(min(x0 + 8 * k + x, n - 1))).o + f * 32 + lane);
+                for (int x = 0; x < 8; ++x) y[k][x] = __ldcg(Partial<S>(from.at(min(x0 + 8 * k + x, n - 1))).o + f * 32 + lane);
             }
         }
 #pragma unroll
         for (int k = 0; k < ROUNDS; ++k) up = fmaxf(up, m[k]);
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) up = fmaxf(up, __shfl_xor_sync(~0u, up, d));
-        const float ref = up == -INFINITY ? 0.0f : up, old = fast_exp2(top - ref);
-        top = up;
-        l *= old;
-        o = make_float4(o.x * old, o.y * old, o.z * old, o.w * old);
+        const float ref = up == -INFINITY ? 0.0f : up, old = fast_exp2(j.top - ref);
+        j.top = up;
+        j.l *= old;
+        j.o = make_float4(j.o.x * old, j.o.y * old, j.o.z * old, j.o.w * old);
 #pragma unroll
         for (int k = 0; k < ROUNDS; ++k)
             if (x0 + 8 * k < n) {
                 const float mine = fast_exp2(m[k] - ref);
-                l += mine * s[k];
+                j.l += mine * s[k];
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
                     const float w = __shfl_sync(~0u, mine, x * 4 + t);
-                    o.x += w * y[k][x].x;
-                    o.y += w * y[k][x].y;
-                    o.z += w * y[k][x].z;
-                    o.w += w * y[k][x].w;
+                    j.o.x += w * y[k][x].x;
+                    j.o.y += w * y[k][x].y;
+                    j.o.z += w * y[k][x].z;
+                    j.o.w += w * y[k][x].w;
                 }
             }
     }
 #pragma unroll
-    for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(~0u, l, d);
-    if (!to) {
-        const int d = S::dim(g, e4 * 4);
-        if (q < heads && (S::FULL || d < a.head_dim)) {
-            const float inv = l == 0.0f ? 0.0f : a.v_scale / l;
-            const uint2 y = make_uint2(pack<S::IO>(o.x * inv, o.y * inv), pack<S::IO>(o.z * inv, o.w * inv));
-            *reinterpret_cast<uint2 *>(a.out + r * a.out_stride + ((int64_t)(head0 + q) * a.head_dim + d) * 2) = y;
-        }
-        if (q < heads && e4 == 0 && g == 0) write_lse<S>(a, r, head0 + q, top, l);
-    } else {
-        const Partial<S> p(to);
-        __stcg(p.o + f * 32 + lane, o);
-        if (e4 == 0 && g == 0) {
-            __stcg(p.m + q, top);
-            __stcg(p.l + q, l);
-        }
-    }
+    for (int d = 4; d < 32; d <<= 1) j.l += __shfl_xor_sync(~0u, j.l, d);
+    return j;
 }
 
 // Offset, in 16-byte units, of the position `lane` of a tile in its buffer; kNoRow for a position that is left out. In two
 // steps, so that other loads can start before the block id is waited for.
-template <int TOK> struct Row {
+template <int TOK, class Line> struct Row {
     uint32_t rest;                                                 // within the block, in 16-byte units
     int32_t blk;                                                   // -2: no live position
-    __device__ __forceinline__ Row(const AttendArgs &a, const Place<TOK> &p) : rest(0), blk(-2) {
+    __device__ __forceinline__ Row(const AttendArgs &a, const Line &p) : rest(0), blk(-2) {
         const int lane = threadIdx.x & 31;
         const uint32_t pos = (uint32_t)p.first / TOK * TOK + (uint32_t)p.tile * TOK + lane;
         if (lane >= TOK || pos < (uint32_t)p.first || pos >= (uint32_t)p.len) return;
@@ -174,6 +226,7 @@ template <int TOK> struct Row {
 
 template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_planes(const __grid_constant__ AttendArgs a) {
     constexpr int TOK = S::TOK, NT = S::NT;
+    using Line = Place<TOK, kSwitchTiles>;
     extern __shared__ __align__(16) uint8_t smem[];                // [warp] ring and partial result
     __shared__ int64_t s_seg[S::WARPS][2];                     // first tile of each one's segment; -1: none
     __shared__ int32_t s_where[S::WARPS][2][3];                // request, segment of the request, tiles
@@ -182,7 +235,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
     const int32_t group = a.n_q_heads / a.n_kv_heads, sets = (group + 8 * NT - 1) / (8 * NT), segs = a.n_kv_heads * sets;
 
     wait_for_earlier();
-    const Batch<TOK, S::WARPS, S::WARPS> batch(a, segs);
+    const Batch<TOK, S::WARPS, S::WARPS, kSwitchTiles> batch(a, segs);
     const Split &split = batch.split;
     if ((int32_t)blockIdx.x >= split.ctas) return;
     uint32_t *const arrived = (uint32_t *)a.scratch;
@@ -192,7 +245,8 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
         return S::SLOT ? smem + warp * S::WARP_BYTES + S::RING : cta_parts + (size_t)(2 * gridDim.x + blockIdx.x * S::WARPS + warp) * S::PARTIAL;
     };
     const int64_t per = (c_end - c_begin) / S::WARPS, more = (c_end - c_begin) % S::WARPS;   // warps without work come last
-    const int64_t x0 = c_begin + w * per + min((int64_t)w, more), x1 = x0 + per + (w < more);
+    int64_t x0 = c_begin + w * per + min((int64_t)w, more);
+    const int64_t x1 = x0 + per + (w < more);
     if (lane < 2) s_seg[w][lane] = -1;
     __syncwarp();
 
@@ -200,13 +254,13 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
         const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem + w * S::WARP_BYTES);
         uint32_t q[NT][S::KCH * S::KSTEP][2];
         float o[NT][S::NE / 2][4], m[NT][2], l[NT][2], sc[NT][2];
-        Place<TOK> cur = batch.locate(a, segs, x0), far = cur;
+        Line cur = batch.locate(a, segs, x0), far = cur;
         const uint8_t *k_ptr, *v_ptr;                              // this lane's piece of row 0 of the head
         constexpr int RI = 32 / S::RP;                             // rows that a copy of the warp covers
         const int piece = lane % S::RP;
         const bool piece_in = S::FULL || piece * 16 < a.head_dim * S::ESZ;
 
-        auto pointers = [&](const Place<TOK> &p) {
+        auto pointers = [&](const Line &p) {
             const int32_t kvh = p.seg / sets, shard = kvh / a.pool.heads_per_shard;
             const int64_t off = (int64_t)(kvh - shard * a.pool.heads_per_shard) * a.pool.head_pitch;
             k_ptr = a.pool.k[shard] + off + piece * 16;
@@ -227,7 +281,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
         };
         // Queries of a segment. 8-bit caches multiply in f16: a bf16 row is brought by a power of two to where f16 holds
         // its elements exactly down to 2^-33 of the largest.
-        auto load_q = [&](const Place<TOK> &p) {
+        auto load_q = [&](const Line &p) {
             const int32_t kvh = p.seg / sets, first = p.seg % sets * 8 * NT;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -275,7 +329,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
             }
         };
         // The end of this warp's part of a segment, [from, to) of the line: outputs if it is the whole of it, else a partial result.
-        auto flush = [&](const Place<TOK> &p, int64_t from, int64_t to) {
+        auto flush = [&](const Line &p, int64_t from, int64_t to) {
             const int64_t begin = p.seg_begin(segs);
             const int32_t kvh = p.seg / sets, first = p.seg % sets * 8 * NT;
             const bool whole = from == begin && to == begin + p.tiles;
@@ -329,31 +383,31 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
         // rows[n]: offsets of the tile n after this one; `far` is the tile AHEAD after this one, the next to be copied.
         constexpr int AHEAD = S::STAGES - 1;
         uint32_t rows[AHEAD + 1];
-        const int64_t n_tiles = x1 - x0;
+        int64_t far_x = x0;
         pointers(far);
 #pragma unroll
         for (int n = 0; n < AHEAD; ++n) {
             rows[n] = kNoRow;
-            if (n < n_tiles) {
-                const Row<TOK> row(a, far);
+            if (far_x < x1) {
+                const Row<TOK, Line> row(a, far);
                 if (n == 0) load_q(cur);
                 else if (far.tile == 0) pointers(far);
                 rows[n] = row.offset(a, far.seg == 0);
                 load_tile(rows[n], ring + n * S::STAGE);
-                far.next(a, segs);
+                far.next(a, segs, far_x);
             } else copies_commit();
         }
         int64_t from = x0;
         int stage = 0, free_stage = AHEAD;
-        for (int64_t i = 0; i < n_tiles; ++i) {
-            const bool ahead = i + AHEAD < n_tiles;
-            rows[AHEAD] = ahead ? Row<TOK>(a, far).offset(a, far.seg == 0) : kNoRow;
+        for (int64_t x = x0; x < x1;) {
+            const bool ahead = far_x < x1;
+            rows[AHEAD] = ahead ? Row<TOK, Line>(a, far).offset(a, far.seg == 0) : kNoRow;
             copies_wait<AHEAD - 1>();
             __syncwarp();                                          // lanes read what others copied; all are done with free_stage
             if (ahead) {
                 if (far.tile == 0) pointers(far);
                 load_tile(rows[AHEAD], ring + free_stage * S::STAGE);
-                far.next(a, segs);
+                far.next(a, segs, far_x);
             } else copies_commit();
             const uint32_t keys = ring + stage * S::STAGE, values = keys + S::PLANE;
             float s[NT][S::SUB][4];
@@ -466,15 +520,17 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
                         }
                     }
                 }
-            const bool last = i + 1 == n_tiles;
-            if (cur.tile + 1 == cur.tiles || last) {
-                flush(cur, from, x0 + i + 1);
-                from = x0 + i + 1;
+            const bool ends = cur.tile + 1 == cur.tiles;
+            const int64_t here = x;
+            Line nxt = cur;
+            nxt.next(a, segs, x);
+            if (ends || x >= x1) {
+                flush(cur, from, here + 1);
+                from = x;
+                if (x >= x1) break;
+                load_q(nxt);
             }
-            if (!last) {
-                cur.next(a, segs);
-                if (cur.tile == 0) load_q(cur);
-            }
+            cur = nxt;
 #pragma unroll
             for (int n = 0; n < AHEAD; ++n) rows[n] = rows[n + 1];
             free_stage = stage;
@@ -512,7 +568,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
         uint8_t *const first = i & 1 ? smem + (i >> 1) * S::WARP_BYTES : first_slot(i >> 1);
         const Pieces from = {first, first_slot(i >> 1), S::SLOT ? S::WARP_BYTES : S::PARTIAL, n};
         uint8_t *const to = i == open[0] || i == open[1] ? cta_parts + (size_t)(blockIdx.x * 2 + (i == open[1])) * S::PARTIAL : nullptr;
-        for (; task < FS; task += S::WARPS) join<S, false>(a, task, from, to, where[0], head0, heads);
+        for (; task < FS; task += S::WARPS) join_few<S, false>(task, from).put(a, to, where[0], head0, heads);
     }
     if (open[0] < 0 && open[1] < 0) return;
     __syncthreads();
@@ -539,7 +595,10 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
         int32_t head0;
         const int32_t heads = heads_of(where[1], &head0);
         const Pieces pieces = {cta_parts + (size_t)(2 * from + 1) * S::PARTIAL, cta_parts + (size_t)(2 * from) * S::PARTIAL, 2 * S::PARTIAL, n};
-        for (int f = w; f < FS; f += S::WARPS) join<S, true>(a, f, pieces, nullptr, where[0], head0, heads);
+        for (int f = w; f < FS; f += S::WARPS) {
+            if (n <= 8) join_few<S, true>(f, pieces).put(a, nullptr, where[0], head0, heads);
+            else join_many<S>(f, pieces).put(a, nullptr, where[0], head0, heads);
+        }
     }
 }
 

@@ -72,10 +72,11 @@ __device__ __forceinline__ int entry_position(int s) { return 4 * ((s & 1) * 2 +
 
 template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_attend_latent(const __grid_constant__ AttendArgs a) {
     constexpr int TOK = S::TOK;
+    using Line = Place<TOK, 0>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t s_full[2];
     __shared__ __align__(8) uint8_t s_live[2][kLatentWarps];       // live positions of a stage's tile, a warp's rows each
-    __shared__ Place<TOK> s_cur, s_far;                            // this tile, and the next one to look up
+    __shared__ Line s_cur, s_far;                            // this tile, and the next one to look up
     __shared__ float s_old[kLatentHeads], s_m[kLatentHeads], s_l[kLatentHeads], s_up[kLatentHeads];
     __shared__ int32_t s_timeout;
     float *const scores = (float *)(smem + S::OFF_S);
@@ -89,7 +90,7 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
     wait_for_earlier();
     OpenSegment *const open = (OpenSegment *)a.scratch;
     uint8_t *const parts = a.scratch + kScratchCounters * sizeof(uint32_t);
-    const Batch<TOK, kLatentWarps, kLatentMinTiles> batch(a, segs);
+    const Batch<TOK, kLatentWarps, kLatentMinTiles, 0> batch(a, segs);
     if (threadIdx.x == 0) {
         if ((int32_t)blockIdx.x >= batch.split.ctas) open[blockIdx.x].pieces = 0;
         s_timeout = 0;
@@ -105,7 +106,8 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
     __syncthreads();
 
     {
-        const Place<TOK> begin = batch.locate(a, segs, c_begin);
+        int64_t x = c_begin;
+        const Line begin = batch.locate(a, segs, x);
         if (threadIdx.x == 0) s_cur = s_far = begin;
     }
     __syncthreads();
@@ -151,8 +153,9 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
                          : "memory");
     };
     // Thread 0 moves s_far on where a barrier stands before and after.
-    auto advance = [&](Place<TOK> &p) {
-        if (threadIdx.x == 0) p.next(a, segs);
+    auto advance = [&](Line &p) {
+        int64_t x = 0;
+        if (threadIdx.x == 0) p.next(a, segs, x);
     };
 #pragma unroll
     for (int k = 0; k < 3; ++k)
@@ -441,7 +444,8 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
             if (ends) {
                 if (threadIdx.x == 0) {
                     s_cur.tile = s_cur.tiles - 1;                  // only kept for the segment's ends
-                    s_cur.next(a, segs);
+                    int64_t x = 0;
+                    s_cur.next(a, segs, x);
                 }
                 __syncthreads();
                 begun = true;
