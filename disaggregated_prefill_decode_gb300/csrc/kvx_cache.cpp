@@ -3,6 +3,7 @@
 // kvx_attend.cu.
 #include "kvx_internal.h"
 
+#include <algorithm>
 #include <cmath>
 #include <limits>
 #include <new>
@@ -33,6 +34,22 @@ static kvx_status device_sms(int32_t *device, int32_t *sms) {
     return KVX_OK;
 }
 
+// Maps of the rows of 8-bit latents for kvx_latent_codes.cu, where it can take them: one shard, in device memory, and rows that
+// end with a head or heads of exactly the elements that it reads, since what lies beyond has to read as zero.
+static void encode_rows(kvx_cache_t c) {
+    const Geom &g = c->g;
+    const bool hnd = g.layout == KVX_LAYOUT_HND;
+    const int64_t rows = g.n_blocks * g.block_size * (hnd ? g.heads_per_shard : 1);
+    if (g.n_planes != 1 || c->cfg.value_type != KVX_E4M3 || g.n_shards != 1 || c->outside_device || rows < 1 ||
+        rows >= std::numeric_limits<int32_t>::max() || (!hnd && g.heads_per_shard > 1 && g.head_dim != kCacheMaxLatent))
+        return;
+    std::vector<CUtensorMap> maps(2 * c->base.size());
+    for (size_t i = 0; i < c->base.size(); ++i)
+        for (int k = 0; k < 2; ++k)
+            if (!encode_rows_map(c->base[i], rows, hnd ? g.head_bytes() : g.row_bytes(), k ? 64 : 128, &maps[2 * i + k])) return;
+    c->row_maps.swap(maps);
+}
+
 // Scratch of the handle, at its first append or attend.
 static kvx_status ready(kvx_cache_t c, cudaStream_t stream) {
     if (c->dev) return KVX_OK;
@@ -50,6 +67,7 @@ static kvx_status ready(kvx_cache_t c, cudaStream_t stream) {
         if (e != cudaSuccess) return cuda_fail(e, "cudaPointerGetAttributes(cache buffer)");
         c->outside_device |= at.type != cudaMemoryTypeDevice;
     }
+    encode_rows(c);
     void *dev = nullptr;
     const size_t bytes = 256 + attend_scratch_bytes(sms, c->g.n_planes == 1);
     st = pool_alloc(&dev, bytes, stream);
@@ -273,6 +291,12 @@ kvx_status kvx_cache_attend(kvx_cache_t c, int32_t layer, const void *q, int64_t
     a.block_pitch16 = (uint32_t)(a.pool.block_pitch / 16);
     a.token_pitch16 = (uint32_t)(a.pool.token_pitch / 16);
     a.latent = g.n_planes == 1;
+    a.row_maps = c->row_maps.empty() ? nullptr : &c->row_maps[2 * (size_t)layer];
+    const bool hnd = g.layout == KVX_LAYOUT_HND;
+    a.map_rows = (int32_t)std::min<int64_t>(g.n_blocks * g.block_size * (hnd ? g.heads_per_shard : 1), std::numeric_limits<int32_t>::max());
+    a.map_block = (uint32_t)(g.block_size * (hnd ? g.heads_per_shard : 1));
+    a.map_head = hnd ? (uint32_t)g.block_size : 0;
+    a.map_col = hnd ? 0 : (uint32_t)g.head_dim;
     a.scratch = c->dev + 256;
     const cudaError_t e = launch_attend(a, f.value_type, f.io_type, c->sms, stream);
     return e == cudaSuccess ? KVX_OK : cuda_fail(e, "launching the attention");

@@ -12,17 +12,12 @@
 // Rows come by bulk copies, two tiles deep. A row's pitch of 608 (1184) bytes, 96 (32) beyond a multiple of
 // 128, keeps both kinds of reads off each other's banks: rows t = 0..3 of the values' reads fall on the four
 // quarters of the banks, and the keys' reads take rows two apart. Two CTAs per SM fill each other's waits.
-#include "kvx_attend.cuh"
-
-#include <algorithm>
+#include "kvx_latent.cuh"
 
 namespace kvx {
 
-constexpr int kLatentWarps = 8, kLatentThreads = 32 * kLatentWarps, kLatentHeads = 16;
-constexpr int kLatentFloat4 = kLatentHeads * kCacheMaxLatentValue / 4;                 // of a partial result
-constexpr int kLatentPartial = kLatentFloat4 * 16 + 2 * kLatentHeads * 4;              // O, m, l
+constexpr int kLatentWarps = 8, kLatentThreads = 32 * kLatentWarps;
 constexpr int kLatentMinTiles = 2;                                                     // of a CTA
-constexpr uint64_t kLatentWaitNs = 2000000000ull;
 
 template <int VT_, int IO_> struct LatentShape {
     static constexpr int VT = VT_, IO = IO_;
@@ -41,30 +36,6 @@ template <int VT_, int IO_> struct LatentShape {
     static constexpr int PENTRY = SPLIT ? 16 : 8;
     static constexpr int OFF_S = 2 * STAGE, OFF_P = OFF_S + 4 * kLatentHeads * TOK * 4;
     static constexpr int BYTES = OFF_P + TOK / 16 * 2 * 32 * PENTRY;
-};
-
-__device__ __forceinline__ uint32_t shared_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
-// Waits for a phase of a stage's barrier, kLatentWaitNs at most.
-__device__ __forceinline__ bool wait_full(uint64_t *bar, uint32_t parity) {
-    uint64_t t0 = 0;
-    for (uint32_t tries = 0;; ++tries) {
-        uint32_t done;
-        asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
-                     : "=r"(done) : "r"(shared_addr(bar)), "r"(parity) : "memory");
-        if (done) return true;
-        if ((tries & 63) == 0) {
-            uint64_t now;
-            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
-            if (!t0) t0 = now;
-            else if (now - t0 > kLatentWaitNs) return false;
-        }
-    }
-}
-
-// What a CTA leaves for the joining kernel: the segment that begins in its stretch and goes on after it (pieces 0: none).
-struct OpenSegment {
-    int32_t r, seg, pieces, unused;
 };
 
 // Position s of the four that an entry of the weights holds, from the first.
@@ -540,15 +511,21 @@ template <int IO> __global__ void __launch_bounds__(kJoinThreads) kvx_attend_lat
 
 size_t latent_scratch_bytes(int32_t sms) { return kScratchCounters * sizeof(uint32_t) + (size_t)4 * sms * kLatentPartial; }
 
+cudaError_t launch_latent_join(const AttendArgs &a, int32_t io, int ctas, int32_t sms, cudaStream_t stream) {
+    if (ctas > kJoinList) return cudaErrorInvalidValue;
+    return launch_after(io == KVX_BF16 ? kvx_attend_latent_join<KVX_BF16> : kvx_attend_latent_join<KVX_F16>, dim3(kJoinCtas * sms),
+                        kJoinThreads, 0, stream, a, ctas);
+}
+
 template <class S> static cudaError_t launch(const AttendArgs &a, int32_t sms, cudaStream_t stream) {
-    if (2 * sms > kJoinList) return cudaErrorInvalidValue;
     static const cudaError_t set = cudaFuncSetAttribute(kvx_attend_latent<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
     if (set != cudaSuccess) return set;
     const cudaError_t e = launch_after(kvx_attend_latent<S>, dim3(2 * sms), kLatentThreads, S::BYTES, stream, a);
-    return e != cudaSuccess ? e : launch_after(kvx_attend_latent_join<S::IO>, dim3(kJoinCtas * sms), kJoinThreads, 0, stream, a, 2 * sms);
+    return e != cudaSuccess ? e : launch_latent_join(a, S::IO, 2 * sms, sms, stream);
 }
 
 cudaError_t launch_attend_latent(const AttendArgs &a, int32_t vt, int32_t io, int32_t sms, cudaStream_t stream) {
+    if (vt == KVX_E4M3 && a.row_maps) return launch_latent_codes(a, io, sms, stream);
     if (vt == KVX_BF16) return launch<LatentShape<KVX_BF16, KVX_BF16>>(a, sms, stream);
     if (vt == KVX_F16) return launch<LatentShape<KVX_F16, KVX_F16>>(a, sms, stream);
     return io == KVX_BF16 ? launch<LatentShape<KVX_E4M3, KVX_BF16>>(a, sms, stream) : launch<LatentShape<KVX_E4M3, KVX_F16>>(a, sms, stream);

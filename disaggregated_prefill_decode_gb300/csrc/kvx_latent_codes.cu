@@ -1,0 +1,469 @@
+// kvx_cache_attend over one plane of 8-bit latents, on the tcgen05 tensor pipe.
+//
+// The 8-bit codes are multiplied as they are, so nothing of the cache passes through registers: a tile of
+// 128 positions is gathered into shared memory by TMA (four rows an instruction, whatever the pages) in
+// 128-byte swizzled chunks of 128 elements, and serves twice as operand A: by rows (K-major) for the scores
+// S = K Q^T, 128 positions x 48, and by columns (MN-major) for the sums O^T += V^T P, four times 128
+// elements x 48. What is not 8 bits wide is split into three codes with a spacing of 2^5, a column each:
+//   x = c1 + c2 / 2^5 + c3 / 2^10,  each the nearest code of what is left,
+// 12 significant bits and more, exact for bf16 queries down to 2^-18 of a query's largest element; so 16
+// query heads make 48 columns. Their sums stand in TMEM apart and are put together in 32 bits.
+//
+// Queries are brought to a largest element in [2^7, 2^8) by a power of two. Weights are taken against a
+// maximum that moves only when a score passes it by more than 2^kSlack, so that O in TMEM is hardly ever
+// rescaled; times 2^5 they stay within the codes' range.
+//
+// Shared memory bounds the products, at 128 bytes a clock: a position is written once (576 bytes) and read
+// twice (576 + 512), and the narrow operands add 400: 16 clocks an SM, where the memory takes 25.
+#include "kvx_latent.cuh"
+
+namespace kvx {
+
+constexpr int kTile = 128;                                     // positions
+constexpr int kCodeThreads = 192;                              // warps 0-3: softmax and outputs; 4: products; 5: copies
+constexpr int kChunk = kTile * 128, kStage = 4 * kChunk + kTile * 64;   // 4 chunks of 128 elements, one of 64
+constexpr int kTerms = 3, kCols = kTerms * kLatentHeads;
+constexpr int kQueryBytes = kCols * kCacheMaxLatent, kWeightBytes = kCols * kTile;
+constexpr int kOffQuery = 2 * kStage, kOffWeight = kOffQuery + kQueryBytes, kCodeBytes = kOffWeight + 2 * kWeightBytes;
+constexpr float kSpacing = 32.0f;
+constexpr float kSlack = 3.0f;                                 // in powers of two
+constexpr float kWeightUp = 32.0f;                             // 2^(kSlack + 5) is within the codes' 448
+constexpr uint32_t kColScores = 0, kColSums = 128, kTmemCols = 512;      // two buffers of scores 64 columns apart, then 4 x 48
+constexpr int kCodeSwitch = 1;                                 // places of the line that a change of segment counts
+
+// Shared memory operands: start, the two strides, swizzle (0 none, 2 of 128 bytes, 4 of 64 bytes).
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t leading, uint32_t stride, uint32_t swizzle) {
+    return (uint64_t)(addr >> 4 & 0x3fff) | (uint64_t)(leading >> 4) << 16 | (uint64_t)(stride >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)swizzle << 61;
+}
+// 128 x 48 products of e4m3 codes with 32-bit sums; both operands by rows, or both by columns.
+constexpr uint32_t kIdescRows = 1u << 4 | (kCols / 8) << 17 | (kTile / 16) << 24;
+constexpr uint32_t kIdescCols = kIdescRows | 1u << 15 | 1u << 16;
+
+__device__ __forceinline__ void tensor_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\ntcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a),
+                 "l"(b), "r"(idesc), "r"((uint32_t)add)
+                 : "memory");
+}
+__device__ __forceinline__ void tensor_commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(shared_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void tensor_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tensor_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 16 columns of this warp's 32 rows of TMEM.
+__device__ __forceinline__ void tmem_load(uint32_t (&x)[16], uint32_t at) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]), "=r"(x[8]), "=r"(x[9]),
+                   "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_store(const uint32_t (&x)[16], uint32_t at) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at), "r"(x[0]),
+                 "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]), "r"(x[8]), "r"(x[9]), "r"(x[10]), "r"(x[11]),
+                 "r"(x[12]), "r"(x[13]), "r"(x[14]), "r"(x[15])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(shared_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Barrier of the four softmax warps, with the disjunction of a condition.
+__device__ __forceinline__ bool softmax_any(bool x) {
+    uint32_t y;
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbarrier.cta.red.or.pred p, 1, 128, q;\nselp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(y) : "r"((uint32_t)x) : "memory");
+    return y;
+}
+
+// Codes of two values, and what is left of them, times the spacing.
+__device__ __forceinline__ uint32_t take_codes(float &x, float &y) {
+    uint16_t c;
+    uint32_t h;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(c) : "f"(x), "f"(y));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+    const float2 f = unpack<KVX_F16>(h);
+    x = (x - f.x) * kSpacing;
+    y = (y - f.y) * kSpacing;
+    return c;
+}
+
+// 16 values, one per query head, over the 32 lanes of the warp: afterwards v[0] of lane x is the result for head_of(x).
+template <class Op> __device__ __forceinline__ float reduce_heads(float (&v)[kLatentHeads], Op op) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int n = 8; n; n >>= 1) {
+        const bool up = lane & 2 * n;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+            v[i] = op(keep, __shfl_xor_sync(~0u, give, 2 * n));
+        }
+    }
+    return op(v[0], __shfl_xor_sync(~0u, v[0], 1));
+}
+__device__ __forceinline__ int head_of(int lane) { return lane >> 1; }
+
+template <int IO> __global__ void __launch_bounds__(kCodeThreads, 1)
+kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap rows128, const __grid_constant__ CUtensorMap rows64) {
+    using Line = Place<kTile, kCodeSwitch>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ __align__(8) uint64_t s_full[2], s_scored[2], s_weighed[2], s_summed[2], s_queried, s_drained;
+    __shared__ uint8_t s_live[2][32];                              // live positions, four a byte
+    __shared__ __align__(16) float s_red[4][kLatentHeads];
+    __shared__ float s_scale[kLatentHeads];
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int32_t s_failed;
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t group = a.n_q_heads / a.n_kv_heads, sets = (group + kLatentHeads - 1) / kLatentHeads, segs = a.n_kv_heads * sets;
+
+    wait_for_earlier();
+    OpenSegment *const open = (OpenSegment *)a.scratch;
+    uint8_t *const parts = a.scratch + kScratchCounters * sizeof(uint32_t);
+    const Batch<kTile, kCodeThreads / 32, 1, kCodeSwitch> batch(a, segs);
+    if ((int32_t)blockIdx.x >= batch.split.ctas) {
+        if (threadIdx.x == 0) open[blockIdx.x].pieces = 0;
+        return;
+    }
+    const int64_t c_begin = batch.split.begin(blockIdx.x), c_end = batch.split.begin(blockIdx.x + 1);
+    int64_t x0 = c_begin;
+    const Line begin = batch.locate(a, segs, x0);
+    if (threadIdx.x == 0) {
+        s_failed = 0;
+        for (int i = 0; i < 2; ++i) {
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_addr(&s_full[i])) : "memory");
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_addr(&s_scored[i])) : "memory");
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 128;" ::"r"(shared_addr(&s_weighed[i])) : "memory");
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_addr(&s_summed[i])) : "memory");
+        }
+        asm volatile("mbarrier.init.shared::cta.b64 [%0], 128;" ::"r"(shared_addr(&s_queried)) : "memory");
+        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_addr(&s_drained)) : "memory");
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (w == 4) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(shared_addr(&s_tmem)), "r"(kTmemCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        tensor_fence_before();
+    }
+    __syncthreads();
+    tensor_fence_after();
+    const uint32_t tmem = s_tmem;
+    // A wait of any role: false when it, or another role's, ran out. Copies and products then stop; the softmax warps, which
+    // meet at barriers, go through their tiles without waiting any more.
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (s_failed) return false;
+        if (wait_full(bar, parity & 1)) return true;
+        s_failed = 1;
+        return false;
+    };
+    OpenSegment opened = {0, 0, 0, 0};
+
+    if (x0 >= c_end) {
+        // nothing but the end of a segment
+    } else if (w == 5) {                                           // copies
+        Line at = begin;
+        int64_t x = x0;
+        const int32_t rows = a.map_rows;
+        int j = 0;
+        for (; x < c_end; ++j) {
+            uint32_t y[4];
+            uint32_t nibble = 0;
+            const int32_t kvh = at.seg / sets;
+            const uint32_t pos0 = (uint32_t)at.first / kTile * kTile + (uint32_t)at.tile * kTile + 4 * lane;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t pos = pos0 + i;
+                y[i] = (uint32_t)rows;                             // beyond the last row: zeros
+                if (pos < (uint32_t)at.first || pos >= (uint32_t)at.len) continue;
+                const uint32_t col = (__umulhi(pos, a.block_mul) + pos) >> a.block_shift, slot = pos - col * (uint32_t)a.pool.block_size;
+                const int32_t blk = a.block_table[at.r * a.table_stride + col];
+                if (blk < 0 || blk >= a.pool.n_blocks) {
+                    if (at.seg == 0) atomicAdd(a.pool.skipped, 1ull);
+                    continue;
+                }
+                y[i] = ((uint32_t)blk * a.map_block + (uint32_t)kvh * a.map_head + slot);
+                nibble |= 1u << i;
+            }
+            if (!__all_sync(~0u, j < 2 || wait(&s_summed[j & 1], (j - 2) >> 1))) break;
+            s_live[j & 1][lane] = (uint8_t)nibble;
+            __syncwarp();
+            const uint32_t bar = shared_addr(&s_full[j & 1]), to = shared_addr(smem + (j & 1) * kStage);
+            if (lane == 0) asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(kStage) : "memory");
+            __syncwarp();
+            const uint32_t col0 = (uint32_t)kvh * a.map_col;
+#pragma unroll
+            for (int c = 0; c < 5; ++c)
+                asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+                             ::"r"(to + c * kChunk + lane * (c < 4 ? 512 : 256)), "l"(c < 4 ? &rows128 : &rows64), "r"(col0 + c * 128), "r"(y[0]),
+                             "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(bar)
+                             : "memory");
+            at.next(a, segs, x);
+        }
+        if (__any_sync(~0u, s_failed))
+            for (int i = max(0, j - 2); i < j; ++i) wait_full(&s_full[i & 1], i >> 1 & 1);      // no copy outlives the CTA
+    } else if (w == 4) {                                           // products
+        if (lane == 0) {
+            Line at = begin;
+            int64_t x = x0;
+            int loads = 0, switches = 0;
+            auto score = [&](int j, bool first) {
+                if (!wait(&s_full[j & 1], j >> 1)) return false;
+                if (first && !wait(&s_queried, switches++)) return false;
+                tensor_fence_after();
+                const uint32_t k = shared_addr(smem + (j & 1) * kStage), q = shared_addr(smem + kOffQuery), d = tmem + kColScores + (j & 1) * 64;
+#pragma unroll
+                for (int i = 0; i < 18; ++i) {
+                    const uint64_t A = i < 16 ? operand(k + (i >> 2) * kChunk + (i & 3) * 32, 16, 1024, 2) : operand(k + 4 * kChunk + (i & 1) * 32, 16, 512, 4);
+                    tensor_mma(d, A, operand(q + i * 2 * (kCols / 8) * 128, (kCols / 8) * 128, 128, 0), kIdescRows, i > 0);
+                }
+                tensor_commit(&s_scored[j & 1]);
+                return true;
+            };
+            bool ok = score(loads, true), first = true;
+            for (int j = 0; ok; ++j) {
+                Line nxt = at;
+                nxt.next(a, segs, x);
+                const bool more = x < c_end, change = nxt.tile == 0;
+                if (more && !change && !(ok = score(j + 1, false))) break;
+                if (!(ok = wait(&s_weighed[j & 1], j >> 1))) break;
+                tensor_fence_after();
+                const uint32_t v = shared_addr(smem + (j & 1) * kStage), p = shared_addr(smem + kOffWeight + (j & 1) * kWeightBytes);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        tensor_mma(tmem + kColSums + c * kCols, operand(v + c * kChunk + i * 4096, 16, 1024, 2), operand(p + i * 512, 128, kTile * 16, 0),
+                                   kIdescCols, !first || i > 0);
+                tensor_commit(&s_summed[j & 1]);
+                if (!more) break;
+                if (change) ok = score(j + 1, true);
+                first = change;
+                at = nxt;
+            }
+            if (!ok) {                                             // no product outlives the CTA
+                tensor_commit(&s_drained);
+                wait_full(&s_drained, 0);
+            }
+        }
+        __syncwarp();
+    } else if (w < 4) {                                            // softmax and outputs: a thread has position threadIdx.x
+        const uint32_t lanes = tmem + ((uint32_t)w << 21);         // this warp's 32 rows
+        float m[kLatentHeads], l[kLatentHeads], scale[kLatentHeads];
+        // Queries of a segment as codes, and what its scores are to be multiplied by.
+        auto query = [&](const Line &p) {
+            const int h = threadIdx.x >> 3, part = threadIdx.x & 7;
+            const int32_t kvh = p.seg / sets, in_group = p.seg % sets * kLatentHeads + h;
+            const uint8_t *src = a.q + p.r * a.q_stride + ((int64_t)kvh * group + in_group) * a.head_dim * 2;
+            const bool real = in_group < group;
+            float top = 0.0f;
+            if (real)
+                for (int d = part * 8; d < a.head_dim; d += 64) {
+                    const uint4 y = __ldg(reinterpret_cast<const uint4 *>(src + d * 2));
+                    for (uint32_t z : {y.x, y.y, y.z, y.w}) {
+                        const float2 f = unpack<IO>(z);
+                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+                }
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+            const int e = top > 0.0f && top < INFINITY ? max(-100, min(100, 7 - ilogbf(top))) : 0;
+            const float up = __int_as_float((127 + e) << 23);
+            if (part == 0) s_scale[h] = top < INFINITY ? a.scale * __int_as_float((127 - e) << 23) : NAN;     // an infinite query: NaN
+            for (int b = part; b < kCacheMaxLatent / 16; b += 8) {
+                uint32_t codes[kTerms][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int d = b * 16 + i * 4;
+                    uint2 y = make_uint2(0, 0);
+                    if (real && d < a.head_dim) y = __ldg(reinterpret_cast<const uint2 *>(src + d * 2));
+                    const float2 f0 = unpack<IO>(y.x), f1 = unpack<IO>(y.y);
+                    float v[4] = {f0.x * up, f0.y * up, f1.x * up, f1.y * up};
+#pragma unroll
+                    for (int k = 0; k < kTerms; ++k) {
+                        const uint32_t lo = take_codes(v[0], v[1]);
+                        codes[k][i] = lo | take_codes(v[2], v[3]) << 16;
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < kTerms; ++k)                   // blocks of 8 columns x 16 elements
+                    *(uint4 *)(smem + kOffQuery + (b * (kCols / 8) + k * 2 + (h >> 3)) * 128 + (h & 7) * 16) =
+                        make_uint4(codes[k][0], codes[k][1], codes[k][2], codes[k][3]);
+            }
+            fence_async();
+            arrive(&s_queried);
+            softmax_any(false);
+        };
+        auto begin_segment = [&]() {
+#pragma unroll
+            for (int h = 0; h < kLatentHeads; ++h) {
+                m[h] = -INFINITY;
+                l[h] = 0.0f;
+                scale[h] = s_scale[h];
+            }
+        };
+        Line at = begin;
+        int64_t x = x0;
+        query(at);
+        begin_segment();
+        bool first = true, begun = at.seg_begin(segs) >= c_begin;  // the segment's first tile here; it begins in this CTA
+        for (int j = 0;; ++j) {
+            wait(&s_scored[j & 1], j >> 1);
+            tensor_fence_after();
+            float s[kLatentHeads];
+            {
+                uint32_t y[kTerms][16];
+#pragma unroll
+                for (int k = 0; k < kTerms; ++k) tmem_load(y[k], lanes + kColScores + (j & 1) * 64 + k * 16);
+                tmem_load_wait();
+                const bool live = s_live[j & 1][threadIdx.x >> 2] >> (threadIdx.x & 3) & 1;
+#pragma unroll
+                for (int h = 0; h < kLatentHeads; ++h) {
+                    const float z = __uint_as_float(y[0][h]) + (__uint_as_float(y[1][h]) + __uint_as_float(y[2][h]) / kSpacing) / kSpacing;
+                    s[h] = live ? z * scale[h] : -INFINITY;
+                }
+            }
+            float over = -INFINITY;
+#pragma unroll
+            for (int h = 0; h < kLatentHeads; ++h) over = fmaxf(over, s[h] - m[h]);
+            if (softmax_any(over > kSlack)) {                      // some maximum moves
+                float v[kLatentHeads];
+#pragma unroll
+                for (int h = 0; h < kLatentHeads; ++h) v[h] = s[h];
+                const float top = reduce_heads(v, [](float p, float q) { return fmaxf(p, q); });
+                if (!(lane & 1)) s_red[w][head_of(lane)] = top;
+                softmax_any(false);
+                float old[kLatentHeads];
+#pragma unroll
+                for (int h = 0; h < kLatentHeads; ++h) {
+                    const float up = fmaxf(m[h], fmaxf(fmaxf(s_red[0][h], s_red[1][h]), fmaxf(s_red[2][h], s_red[3][h])));
+                    old[h] = fast_exp2(m[h] - (up == -INFINITY ? 0.0f : up));
+                    m[h] = up;
+                    l[h] *= old[h];
+                }
+                softmax_any(false);                                // s_red is free again
+                if (!first) {
+                    wait(&s_summed[(j - 1) & 1], (j - 1) >> 1);
+                    tensor_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < 4 * kTerms; ++c) {
+                        uint32_t y[16];
+                        tmem_load(y, lanes + kColSums + c * 16);
+                        tmem_load_wait();
+#pragma unroll
+                        for (int h = 0; h < kLatentHeads; ++h) y[h] = __float_as_uint(__uint_as_float(y[h]) * old[h]);
+                        tmem_store(y, lanes + kColSums + c * 16);
+                    }
+                    tmem_store_wait();
+                }
+            }
+            uint32_t codes[kTerms][4];
+#pragma unroll
+            for (int h = 0; h < kLatentHeads; h += 4) {
+                float v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[i] = fast_exp2(s[h + i] - (m[h + i] == -INFINITY ? 0.0f : m[h + i]));
+                    l[h + i] += v[i];
+                    v[i] *= kWeightUp;
+                }
+#pragma unroll
+                for (int k = 0; k < kTerms; ++k) {
+                    const uint32_t lo = take_codes(v[0], v[1]);
+                    codes[k][h / 4] = lo | take_codes(v[2], v[3]) << 16;
+                }
+            }
+            if (j >= 2) wait(&s_summed[j & 1], (j - 2) >> 1);
+#pragma unroll
+            for (int k = 0; k < kTerms; ++k)                       // blocks of 16 columns x 8 positions
+                *(uint4 *)(smem + kOffWeight + (j & 1) * kWeightBytes + k * kTile * 16 + threadIdx.x * 16) =
+                    make_uint4(codes[k][0], codes[k][1], codes[k][2], codes[k][3]);
+            fence_async();
+            tensor_fence_before();
+            arrive(&s_weighed[j & 1]);
+            first = false;
+
+            const bool ends = at.tile + 1 == at.tiles;
+            Line nxt = at;
+            nxt.next(a, segs, x);
+            const bool more = x < c_end;
+            if (!ends && more) {
+                at = nxt;
+                continue;
+            }
+            if (more) query(nxt);                                  // these scores are read, so the queries are free
+            wait(&s_summed[j & 1], j >> 1);
+            tensor_fence_after();
+            {
+                float v[kLatentHeads];
+#pragma unroll
+                for (int h = 0; h < kLatentHeads; ++h) v[h] = l[h];
+                const float sum = reduce_heads(v, [](float p, float q) { return p + q; });
+                if (!(lane & 1)) s_red[w][head_of(lane)] = sum;
+                softmax_any(false);
+#pragma unroll
+                for (int h = 0; h < kLatentHeads; ++h) l[h] = (s_red[0][h] + s_red[1][h]) + (s_red[2][h] + s_red[3][h]);
+                softmax_any(false);
+            }
+            const bool whole = ends && begun;
+            const int32_t in_group = at.seg % sets * kLatentHeads, head0 = at.seg / sets * group + in_group, heads = min(group - in_group, kLatentHeads);
+            uint8_t *const part = parts + (size_t)(blockIdx.x * 2 + begun) * kLatentPartial;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t y[kTerms][16];
+#pragma unroll
+                for (int k = 0; k < kTerms; ++k) tmem_load(y[k], lanes + kColSums + c * kCols + k * 16);
+                tmem_load_wait();
+                const int d = c * 128 + threadIdx.x;
+#pragma unroll
+                for (int h = 0; h < kLatentHeads; ++h) {
+                    const float z = (__uint_as_float(y[0][h]) + (__uint_as_float(y[1][h]) + __uint_as_float(y[2][h]) / kSpacing) / kSpacing) / kWeightUp;
+                    if (!whole) __stcg((float *)part + partial_at(d, h), z);
+                    else if (h < heads && d < a.v_dim)
+                        ((uint16_t *)(a.out + at.r * a.out_stride))[(int64_t)(head0 + h) * a.v_dim + d] =
+                            (uint16_t)pack<IO>(l[h] == 0.0f ? 0.0f : z * (a.v_scale / l[h]), 0.0f);
+                }
+            }
+            tensor_fence_before();
+#pragma unroll
+            for (int h = 0; h < kLatentHeads; ++h)
+                if ((int)threadIdx.x == h) {
+                    if (!whole) {
+                        __stcg((float *)(part + kLatentFloat4 * 16) + h, m[h]);
+                        __stcg((float *)(part + kLatentFloat4 * 16) + kLatentHeads + h, l[h]);
+                    } else if (a.lse && h < heads)
+                        a.lse[(int64_t)at.r * a.n_q_heads + head0 + h] = l[h] == 0.0f ? -INFINITY : (m[h] + log2f(l[h])) * kLn2;
+                }
+            if (!whole && begun)
+                opened = OpenSegment{at.r, at.seg, batch.split.cta_of(at.seg_begin(segs) + at.tiles - 1) - (int32_t)blockIdx.x + 1, 0};
+            if (!more) break;
+            at = nxt;
+            begin_segment();
+            first = begun = true;
+        }
+    }
+    tensor_fence_before();
+    __syncthreads();
+    if (w == 4) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    if (threadIdx.x == 0) {
+        if (s_failed) atomicAdd(a.pool.skipped + 1, 1ull);
+        open[blockIdx.x] = s_failed ? OpenSegment{0, 0, 0, 0} : opened;
+    }
+}
+
+template <int IO> static cudaError_t launch(const AttendArgs &a, int32_t sms, cudaStream_t stream) {
+    static const cudaError_t set = cudaFuncSetAttribute(kvx_attend_latent_codes<IO>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCodeBytes);
+    if (set != cudaSuccess) return set;
+    const cudaError_t e = launch_after(kvx_attend_latent_codes<IO>, dim3(sms), kCodeThreads, kCodeBytes, stream, a, a.row_maps[0], a.row_maps[1]);
+    return e != cudaSuccess ? e : launch_latent_join(a, IO, sms, sms, stream);
+}
+
+cudaError_t launch_latent_codes(const AttendArgs &a, int32_t io, int32_t sms, cudaStream_t stream) {
+    return io == KVX_BF16 ? launch<KVX_BF16>(a, sms, stream) : launch<KVX_F16>(a, sms, stream);
+}
+
+}  // namespace kvx
