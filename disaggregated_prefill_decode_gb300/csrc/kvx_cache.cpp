@@ -43,10 +43,17 @@ static void encode_rows(kvx_cache_t c) {
     if (g.n_planes != 1 || c->cfg.value_type != KVX_E4M3 || g.n_shards != 1 || c->outside_device || rows < 1 ||
         rows >= std::numeric_limits<int32_t>::max() || (!hnd && g.heads_per_shard > 1 && g.head_dim != kCacheMaxLatent))
         return;
-    std::vector<CUtensorMap> maps(2 * c->base.size());
-    for (size_t i = 0; i < c->base.size(); ++i)
-        for (int k = 0; k < 2; ++k)
-            if (!encode_rows_map(c->base[i], rows, hnd ? g.head_bytes() : g.row_bytes(), k ? 64 : 128, &maps[2 * i + k])) return;
+    const int64_t row_bytes = hnd ? g.head_bytes() : g.row_bytes();
+    int32_t run = 128;
+    while (g.block_size % run) run /= 2;
+    std::vector<RowMaps> maps(c->base.size());
+    for (size_t i = 0; i < maps.size(); ++i)
+        if (!encode_rows_map(c->base[i], rows, row_bytes, 128, run, &maps[i].run128) ||
+            !encode_rows_map(c->base[i], rows, row_bytes, 64, run, &maps[i].run64) ||
+            !encode_rows_map(c->base[i], rows, row_bytes, 128, 1, &maps[i].row128) ||
+            !encode_rows_map(c->base[i], rows, row_bytes, 64, 1, &maps[i].row64))
+            return;
+    c->map_run = run;
     c->row_maps.swap(maps);
 }
 
@@ -291,7 +298,8 @@ kvx_status kvx_cache_attend(kvx_cache_t c, int32_t layer, const void *q, int64_t
     a.block_pitch16 = (uint32_t)(a.pool.block_pitch / 16);
     a.token_pitch16 = (uint32_t)(a.pool.token_pitch / 16);
     a.latent = g.n_planes == 1;
-    a.row_maps = c->row_maps.empty() ? nullptr : &c->row_maps[2 * (size_t)layer];
+    a.row_maps = c->row_maps.empty() ? nullptr : &c->row_maps[(size_t)layer];
+    a.map_run = c->map_run;
     const bool hnd = g.layout == KVX_LAYOUT_HND;
     a.map_rows = (int32_t)std::min<int64_t>(g.n_blocks * g.block_size * (hnd ? g.heads_per_shard : 1), std::numeric_limits<int32_t>::max());
     a.map_block = (uint32_t)(g.block_size * (hnd ? g.heads_per_shard : 1));

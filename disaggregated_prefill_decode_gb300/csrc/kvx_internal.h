@@ -206,6 +206,12 @@ struct AppendArgs {
 };
 cudaError_t launch_append(const AppendArgs &a, int32_t value_type, int32_t io_type, int32_t sms, cudaStream_t stream);
 
+// The rows of one buffer of 8-bit latents, in boxes of 128 and 64 bytes: a run of rows that lie in one block wherever they
+// begin, or single rows for gathers.
+struct RowMaps {
+    CUtensorMap run128, run64, row128, row64;
+};
+
 struct AttendArgs {
     CacheLayer pool;
     const uint8_t *q;
@@ -221,8 +227,8 @@ struct AttendArgs {
     uint32_t block_mul, block_shift;  // position / block_size = (mulhi(position, mul) + position) >> shift, below 2^31
     uint32_t block_pitch16, token_pitch16;   // of the pool, in 16-byte units
     bool latent;                      // one plane
-    const CUtensorMap *row_maps;      // 8-bit latents (host): the rows in boxes of 128 and of 64 bytes, or NULL
-    int32_t map_rows;                 // rows of the maps; block, head and element of the first row a KV head's
+    const RowMaps *row_maps;          // 8-bit latents (host), or NULL
+    int32_t map_rows, map_run;        // rows of the maps, of a run; block, head and element of the first row a KV head's
     uint32_t map_block, map_head, map_col;   // block begins at
     uint8_t *scratch;                 // of the handle: counters (zero between calls), partial results
 };
@@ -247,7 +253,8 @@ struct kvx_cache_s {
     int32_t device = -1;                       // of the scratch, set by the first append or attend
     int32_t sms = 0;
     bool outside_device = false;               // a buffer is not device memory
-    std::vector<CUtensorMap> row_maps;         // 8-bit latents: two per buffer, or none (the driver refused one)
+    std::vector<kvx::RowMaps> row_maps;        // 8-bit latents: per buffer, or none (kvx_cache.cpp, encode_rows)
+    int32_t map_run = 0;                       // rows of a run: the common divisor of the block size and 128
     uint8_t *dev = nullptr;                    // [256 bytes: skipped][scratch of the attend kernels]
 };
 
@@ -341,9 +348,9 @@ bool encode_tensor_maps(kvx_plan_s *pl);
 // TENSOR plans: whether a box (box_n slots x box_k heads, laid out in `order`) is one contiguous span
 // of a side with geometry g (kvx_tiles.cpp).
 bool tensor_side_flat(const Geom &g, int32_t order, int32_t box_n, int32_t box_k);
-// A rank-2 map of a buffer of `rows` rows of row_bytes bytes, with boxes of one row and box_bytes bytes, swizzled over 128
-// or 64 bytes as the box is wide; false when the driver refuses it (kvx_push.cu).
-bool encode_rows_map(void *base, int64_t rows, int64_t row_bytes, int32_t box_bytes, CUtensorMap *out);
+// A rank-2 map of a buffer of `rows` rows of row_bytes bytes, with boxes of box_rows rows and box_bytes bytes, swizzled over
+// 128 or 64 bytes as the box is wide; false when the driver refuses it (kvx_push.cu).
+bool encode_rows_map(void *base, int64_t rows, int64_t row_bytes, int32_t box_bytes, int32_t box_rows, CUtensorMap *out);
 // Checks where the pools' buffers live (first and last buffer of each side) and records it; refuses
 // pageable host memory the GPU cannot reach (kvx_push.cu).
 kvx_status check_pool_memory(kvx_plan_s *pl);

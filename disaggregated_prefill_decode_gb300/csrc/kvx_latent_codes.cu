@@ -1,8 +1,8 @@
 // kvx_cache_attend over one plane of 8-bit latents, on the tcgen05 tensor pipe.
 //
 // The 8-bit codes are multiplied as they are, so nothing of the cache passes through registers: a tile of
-// 128 positions is gathered into shared memory by TMA (four rows an instruction, whatever the pages) in
-// 128-byte swizzled chunks of 128 elements, and serves twice as operand A: by rows (K-major) for the scores
+// 128 positions is brought into shared memory by TMA in 128-byte swizzled chunks of 128 elements, and
+// serves twice as operand A: by rows (K-major) for the scores
 // S = K Q^T, 128 positions x 48, and by columns (MN-major) for the sums O^T += V^T P, four times 128
 // elements x 48. What is not 8 bits wide is split into three codes with a spacing of 2^5, a column each:
 //   x = c1 + c2 / 2^5 + c3 / 2^10,  each the nearest code of what is left,
@@ -12,6 +12,10 @@
 // Queries are brought to a largest element in [2^7, 2^8) by a power of two. Weights are taken against a
 // maximum that moves only when a score passes it by more than 2^kSlack, so that O in TMEM is hardly ever
 // rescaled; times 2^5 they stay within the codes' range.
+//
+// Rows come in boxes of as many as a page holds in a row (the common divisor of the page and the tile);
+// boxes that begin or end a sequence, and pages that 4 does not divide, are gathered four rows at a time,
+// since a row that is not live has to read as zero. Gathers alone took 58 clocks each, 4.9 us a tile.
 //
 // Shared memory bounds the products, at 128 bytes a clock: a position is written once (576 bytes) and read
 // twice (576 + 512), and the narrow operands add 400: 16 clocks an SM, where the memory takes 25.
@@ -110,7 +114,7 @@ template <class Op> __device__ __forceinline__ float reduce_heads(float (&v)[kLa
 __device__ __forceinline__ int head_of(int lane) { return lane >> 1; }
 
 template <int IO> __global__ void __launch_bounds__(kCodeThreads, 1)
-kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap rows128, const __grid_constant__ CUtensorMap rows64) {
+kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_constant__ RowMaps maps) {
     using Line = Place<kTile, kCodeSwitch>;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ __align__(8) uint64_t s_full[2], s_scored[2], s_weighed[2], s_summed[2], s_queried, s_drained;
@@ -168,40 +172,55 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
     } else if (w == 5) {                                           // copies
         Line at = begin;
         int64_t x = x0;
-        const int32_t rows = a.map_rows;
         int j = 0;
         for (; x < c_end; ++j) {
-            uint32_t y[4];
-            uint32_t nibble = 0;
             const int32_t kvh = at.seg / sets;
-            const uint32_t pos0 = (uint32_t)at.first / kTile * kTile + (uint32_t)at.tile * kTile + 4 * lane;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t pos = pos0 + i;
-                y[i] = (uint32_t)rows;                             // beyond the last row: zeros
-                if (pos < (uint32_t)at.first || pos >= (uint32_t)at.len) continue;
+            const uint32_t run = (uint32_t)a.map_run, first = (uint32_t)at.first, len = (uint32_t)at.len;
+            const uint32_t tile0 = first / kTile * kTile + (uint32_t)at.tile * kTile, col0 = (uint32_t)kvh * a.map_col, head = (uint32_t)kvh * a.map_head;
+            // row of a position; beyond the last row, which reads as zeros, for one that is not live
+            auto row_of = [&](uint32_t pos) {
+                if (pos < first || pos >= len) return (uint32_t)a.map_rows;
                 const uint32_t col = (__umulhi(pos, a.block_mul) + pos) >> a.block_shift, slot = pos - col * (uint32_t)a.pool.block_size;
                 const int32_t blk = a.block_table[at.r * a.table_stride + col];
                 if (blk < 0 || blk >= a.pool.n_blocks) {
                     if (at.seg == 0) atomicAdd(a.pool.skipped, 1ull);
-                    continue;
+                    return (uint32_t)a.map_rows;
                 }
-                y[i] = ((uint32_t)blk * a.map_block + (uint32_t)kvh * a.map_head + slot);
-                nibble |= 1u << i;
+                return (uint32_t)blk * a.map_block + head + slot;
+            };
+            // A lane has a run, if there are as many, and four positions. Runs that are live or dead as a whole go in boxes; the
+            // four positions of other runs by a gather. Rows are looked up before the stage is waited for.
+            auto whole = [&](uint32_t pos) { return run >= 4 && (pos + run <= first || pos >= len || (pos >= first && pos + run <= len)); };
+            const uint32_t nothing = (uint32_t)a.map_rows, run0 = tile0 + lane * run, four0 = tile0 + 4 * lane, my_run = 4 * lane / run;
+            const bool boxed = lane * run < kTile && whole(run0), gathered = !whole(tile0 + my_run * run);
+            const uint32_t row = boxed ? row_of(run0) : nothing;
+            uint32_t y[4], live = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                y[k] = gathered ? row_of(four0 + k) : nothing;
+                live |= (uint32_t)(y[k] != nothing) << k;
             }
+            if (__shfl_sync(~0u, row, my_run) != nothing && !gathered) live = 15;
             if (!__all_sync(~0u, j < 2 || wait(&s_summed[j & 1], (j - 2) >> 1))) break;
-            s_live[j & 1][lane] = (uint8_t)nibble;
-            __syncwarp();
             const uint32_t bar = shared_addr(&s_full[j & 1]), to = shared_addr(smem + (j & 1) * kStage);
+            s_live[j & 1][lane] = (uint8_t)live;
+            __syncwarp();
             if (lane == 0) asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(kStage) : "memory");
             __syncwarp();
-            const uint32_t col0 = (uint32_t)kvh * a.map_col;
+            if (boxed)
 #pragma unroll
-            for (int c = 0; c < 5; ++c)
-                asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
-                             ::"r"(to + c * kChunk + lane * (c < 4 ? 512 : 256)), "l"(c < 4 ? &rows128 : &rows64), "r"(col0 + c * 128), "r"(y[0]),
-                             "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(bar)
-                             : "memory");
+                for (int c = 0; c < 5; ++c)
+                    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                                     to + c * kChunk + lane * run * (c < 4 ? 128 : 64)),
+                                 "l"(c < 4 ? &maps.run128 : &maps.run64), "r"(col0 + c * 128), "r"(row), "r"(bar)
+                                 : "memory");
+            if (gathered)
+#pragma unroll
+                for (int c = 0; c < 5; ++c)
+                    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+                                 ::"r"(to + c * kChunk + lane * (c < 4 ? 512 : 256)), "l"(c < 4 ? &maps.row128 : &maps.row64), "r"(col0 + c * 128),
+                                 "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(bar)
+                                 : "memory");
             at.next(a, segs, x);
         }
         if (__any_sync(~0u, s_failed))
@@ -229,7 +248,9 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
                 Line nxt = at;
                 nxt.next(a, segs, x);
                 const bool more = x < c_end, change = nxt.tile == 0;
-                if (more && !change && !(ok = score(j + 1, false))) break;
+                // the next scores before these sums, if the next tile is there
+                const bool early = more && !change && is_full(&s_full[(j + 1) & 1], (j + 1) >> 1 & 1);
+                if (early && !(ok = score(j + 1, false))) break;
                 if (!(ok = wait(&s_weighed[j & 1], j >> 1))) break;
                 tensor_fence_after();
                 const uint32_t v = shared_addr(smem + (j & 1) * kStage), p = shared_addr(smem + kOffWeight + (j & 1) * kWeightBytes);
@@ -241,7 +262,7 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
                                    kIdescCols, !first || i > 0);
                 tensor_commit(&s_summed[j & 1]);
                 if (!more) break;
-                if (change) ok = score(j + 1, true);
+                if (!early) ok = score(j + 1, change);
                 first = change;
                 at = nxt;
             }
@@ -458,7 +479,7 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
 template <int IO> static cudaError_t launch(const AttendArgs &a, int32_t sms, cudaStream_t stream) {
     static const cudaError_t set = cudaFuncSetAttribute(kvx_attend_latent_codes<IO>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCodeBytes);
     if (set != cudaSuccess) return set;
-    const cudaError_t e = launch_after(kvx_attend_latent_codes<IO>, dim3(sms), kCodeThreads, kCodeBytes, stream, a, a.row_maps[0], a.row_maps[1]);
+    const cudaError_t e = launch_after(kvx_attend_latent_codes<IO>, dim3(sms), kCodeThreads, kCodeBytes, stream, a, *a.row_maps);
     return e != cudaSuccess ? e : launch_latent_join(a, IO, sms, sms, stream);
 }
 

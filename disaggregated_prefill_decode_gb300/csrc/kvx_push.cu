@@ -209,11 +209,11 @@ static bool encode_one(const Geom &g, void *base, int32_t box_n, int32_t box_k, 
     return true;
 }
 
-bool encode_rows_map(void *base, int64_t rows, int64_t row_bytes, int32_t box_bytes, CUtensorMap *out) {
+bool encode_rows_map(void *base, int64_t rows, int64_t row_bytes, int32_t box_bytes, int32_t box_rows, CUtensorMap *out) {
     EncodeTiledFn enc = encoder();
     if (!enc || rows < 1) return false;
     const cuuint64_t dim[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows}, stride[1] = {(cuuint64_t)row_bytes};
-    const cuuint32_t box[2] = {(cuuint32_t)box_bytes, 1}, elem[2] = {1, 1};
+    const cuuint32_t box[2] = {(cuuint32_t)box_bytes, (cuuint32_t)box_rows}, elem[2] = {1, 1};
     return enc(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dim, stride, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
                box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
