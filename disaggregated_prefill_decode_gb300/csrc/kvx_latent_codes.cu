@@ -24,7 +24,9 @@
 namespace kvx {
 
 constexpr int kTile = 128;                                     // positions
-constexpr int kCodeThreads = 192;                              // warps 0-3: softmax and outputs; 4: products; 5: copies
+constexpr int kSoftThreads = 256;                              // warps 0-7: softmax and outputs, half of the query heads each four
+constexpr int kCodeThreads = kSoftThreads + 64;                // 8: products; 9: copies
+constexpr int kMine = kLatentHeads / 2;                        // query heads of a softmax thread
 constexpr int kChunk = kTile * 128, kStage = 4 * kChunk + kTile * 64;   // 4 chunks of 128 elements, one of 64
 constexpr int kChunks = 5;                                     // the last one is used up by the scores, the others in their order by the sums
 constexpr int kTerms = 3, kCols = kTerms * kLatentHeads;
@@ -34,6 +36,7 @@ constexpr float kSpacing = 32.0f;
 constexpr float kSlack = 3.0f;                                 // in powers of two
 constexpr float kWeightUp = 32.0f;                             // 2^(kSlack + 5) is within the codes' 448
 constexpr uint32_t kColScores = 0, kColSums = 128, kTmemCols = 512;      // two buffers of scores 64 columns apart, then 4 x 48
+constexpr int kLookAhead = 1;                                  // tiles whose rows are looked up ahead of their copy
 constexpr int kCodeSwitch = 1;                                 // places of the line that a change of segment counts
 
 // Shared memory operands: start, the two strides, swizzle (0 none, 2 of 128 bytes, 4 of 64 bytes).
@@ -59,18 +62,14 @@ __device__ __forceinline__ void tensor_commit(uint64_t *bar) {
 __device__ __forceinline__ void tensor_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tensor_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// 16 columns of this warp's 32 rows of TMEM.
-__device__ __forceinline__ void tmem_load(uint32_t (&x)[16], uint32_t at) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]), "=r"(x[8]), "=r"(x[9]),
-                   "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15])
-                 : "r"(at)
-                 : "memory");
+// 8 columns of this warp's 32 rows of TMEM.
+__device__ __forceinline__ void tmem_load(uint32_t (&x)[kMine], uint32_t at) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]) : "r"(at) : "memory");
 }
-__device__ __forceinline__ void tmem_store(const uint32_t (&x)[16], uint32_t at) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at), "r"(x[0]),
-                 "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]), "r"(x[8]), "r"(x[9]), "r"(x[10]), "r"(x[11]),
-                 "r"(x[12]), "r"(x[13]), "r"(x[14]), "r"(x[15])
+__device__ __forceinline__ void tmem_store(const uint32_t (&x)[kMine], uint32_t at) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
+                 "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
                  : "memory");
 }
 __device__ __forceinline__ void tmem_load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -81,11 +80,11 @@ __device__ __forceinline__ void arrive(uint64_t *bar) {
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// Barrier of the four softmax warps, with the disjunction of a condition.
+// Barrier of the softmax warps, with the disjunction of a condition.
 __device__ __forceinline__ bool softmax_any(bool x) {
     uint32_t y;
-    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbarrier.cta.red.or.pred p, 1, 128, q;\nselp.u32 %0, 1, 0, p;\n}"
-                 : "=r"(y) : "r"((uint32_t)x) : "memory");
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbarrier.cta.red.or.pred p, 1, %2, q;\nselp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(y) : "r"((uint32_t)x), "n"(kSoftThreads) : "memory");
     return y;
 }
 
@@ -101,21 +100,21 @@ __device__ __forceinline__ uint32_t take_codes(float &x, float &y) {
     return c;
 }
 
-// 16 values, one per query head, over the 32 lanes of the warp: afterwards v[0] of lane x is the result for head_of(x).
-template <class Op> __device__ __forceinline__ float reduce_heads(float (&v)[kLatentHeads], Op op) {
+// 8 values, one per query head, over the 32 lanes of the warp: the result is for head lane / 4.
+template <class Op> __device__ __forceinline__ float reduce_heads(float (&v)[kMine], Op op) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int n = 8; n; n >>= 1) {
-        const bool up = lane & 2 * n;
+    for (int n = kMine / 2; n; n >>= 1) {
+        const bool up = lane & 4 * n;
 #pragma unroll
         for (int i = 0; i < n; ++i) {
             const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
-            v[i] = op(keep, __shfl_xor_sync(~0u, give, 2 * n));
+            v[i] = op(keep, __shfl_xor_sync(~0u, give, 4 * n));
         }
     }
+    v[0] = op(v[0], __shfl_xor_sync(~0u, v[0], 2));
     return op(v[0], __shfl_xor_sync(~0u, v[0], 1));
 }
-__device__ __forceinline__ int head_of(int lane) { return lane >> 1; }
 
 template <int IO> __global__ void __launch_bounds__(kCodeThreads, 1)
 kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_constant__ RowMaps maps) {
@@ -150,13 +149,13 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
                 asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_addr(&s_free[i][c])) : "memory");
             }
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_addr(&s_scored[i])) : "memory");
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], 128;" ::"r"(shared_addr(&s_weighed[i])) : "memory");
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_addr(&s_weighed[i])), "n"(kSoftThreads) : "memory");
         }
-        asm volatile("mbarrier.init.shared::cta.b64 [%0], 128;" ::"r"(shared_addr(&s_queried)) : "memory");
+        asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_addr(&s_queried)), "n"(kSoftThreads) : "memory");
         asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_addr(&s_drained)) : "memory");
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (w == 4) {
+    if (w == 8) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(shared_addr(&s_tmem)), "r"(kTmemCols) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         tensor_fence_before();
@@ -176,67 +175,90 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
 
     if (x0 >= c_end) {
         // nothing but the end of a segment
-    } else if (w == 5) {                                           // copies
-        Line at = begin;
-        int64_t x = x0;
-        int issued = 0;                                            // chunks under way or arrived
-        for (int j = 0; x < c_end; ++j) {
+    } else if (w == 9) {                                           // copies
+        // A lane has a run of the tile, if there are as many, and four positions. Runs that are live or dead as a whole go in
+        // boxes; the four positions of other runs by a gather.
+        struct Rows {
+            bool boxed, gathered;
+            uint32_t row, y[4], live, col0;
+        };
+        const uint32_t run = (uint32_t)a.map_run, nothing = (uint32_t)a.map_rows;      // beyond the last row: reads as zeros
+        auto look_up = [&](const Line &at) {
+            Rows o;
             const int32_t kvh = at.seg / sets;
-            const uint32_t run = (uint32_t)a.map_run, first = (uint32_t)at.first, len = (uint32_t)at.len;
-            const uint32_t tile0 = first / kTile * kTile + (uint32_t)at.tile * kTile, col0 = (uint32_t)kvh * a.map_col, head = (uint32_t)kvh * a.map_head;
-            // row of a position; beyond the last row, which reads as zeros, for one that is not live
+            const uint32_t first = (uint32_t)at.first, len = (uint32_t)at.len, tile0 = first / kTile * kTile + (uint32_t)at.tile * kTile;
             auto row_of = [&](uint32_t pos) {
-                if (pos < first || pos >= len) return (uint32_t)a.map_rows;
+                if (pos < first || pos >= len) return nothing;
                 const uint32_t col = (__umulhi(pos, a.block_mul) + pos) >> a.block_shift, slot = pos - col * (uint32_t)a.pool.block_size;
                 const int32_t blk = a.block_table[at.r * a.table_stride + col];
                 if (blk < 0 || blk >= a.pool.n_blocks) {
                     if (at.seg == 0) atomicAdd(a.pool.skipped, 1ull);
-                    return (uint32_t)a.map_rows;
+                    return nothing;
                 }
-                return (uint32_t)blk * a.map_block + head + slot;
+                return (uint32_t)blk * a.map_block + (uint32_t)kvh * a.map_head + slot;
             };
-            // A lane has a run, if there are as many, and four positions. Runs that are live or dead as a whole go in boxes; the
-            // four positions of other runs by a gather. Rows are looked up before the stage is waited for.
             auto whole = [&](uint32_t pos) { return run >= 4 && (pos + run <= first || pos >= len || (pos >= first && pos + run <= len)); };
-            const uint32_t nothing = (uint32_t)a.map_rows, run0 = tile0 + lane * run, four0 = tile0 + 4 * lane, my_run = 4 * lane / run;
-            const bool boxed = lane * run < kTile && whole(run0), gathered = !whole(tile0 + my_run * run);
-            const uint32_t row = boxed ? row_of(run0) : nothing;
-            uint32_t y[4], live = 0;
+            const uint32_t run0 = tile0 + lane * run, four0 = tile0 + 4 * lane, my_run = 4 * lane / run;
+            o.col0 = (uint32_t)kvh * a.map_col;
+            o.boxed = lane * run < kTile && whole(run0);
+            o.gathered = !whole(tile0 + my_run * run);
+            o.row = o.boxed ? row_of(run0) : nothing;
+            o.live = 0;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                y[k] = gathered ? row_of(four0 + k) : nothing;
-                live |= (uint32_t)(y[k] != nothing) << k;
+                o.y[k] = o.gathered ? row_of(four0 + k) : nothing;
+                o.live |= (uint32_t)(o.y[k] != nothing) << k;
             }
-            if (__shfl_sync(~0u, row, my_run) != nothing && !gathered) live = 15;
+            if (__shfl_sync(~0u, o.row, my_run) != nothing && !o.gathered) o.live = 15;
+            return o;
+        };
+        Line at = begin;
+        int64_t x = x0, issued = 0;                                // chunks under way or arrived
+        Rows queue[kLookAhead + 1];
+#pragma unroll
+        for (int i = 0; i < kLookAhead; ++i)
+            if (x < c_end) {
+                queue[i] = look_up(at);
+                at.next(a, segs, x);
+            } else queue[i].col0 = ~0u;
+        for (int j = 0;; ++j) {
+            queue[kLookAhead].col0 = ~0u;
+            if (x < c_end) {
+                queue[kLookAhead] = look_up(at);
+                at.next(a, segs, x);
+            }
+            const Rows rows = queue[0];
+            if (rows.col0 == ~0u) break;
+#pragma unroll
+            for (int i = 0; i < kLookAhead; ++i) queue[i] = queue[i + 1];
             bool ok = true;
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
                 const int c = (i + 4) % kChunks;                   // in the order in which they become free
                 if (!(ok = __all_sync(~0u, j < 2 || wait(&s_free[j & 1][c], (j - 2) >> 1)))) break;
                 const uint32_t bar = shared_addr(&s_full[j & 1][c]), to = shared_addr(smem + (j & 1) * kStage + c * kChunk);
-                if (i == 1) s_live[j & 1][lane] = (uint8_t)live;   // the softmax of tile j - 2 is through with its own
+                if (i == 1) s_live[j & 1][lane] = (uint8_t)rows.live;   // the softmax of tile j - 2 is through with its own
                 __syncwarp();
                 if (lane == 0)
                     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(c < 4 ? kChunk : kChunk / 2) : "memory");
                 __syncwarp();
-                if (boxed)
+                if (rows.boxed)
                     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
                                      to + lane * run * (c < 4 ? 128 : 64)),
-                                 "l"(c < 4 ? &maps.run128 : &maps.run64), "r"(col0 + c * 128), "r"(row), "r"(bar)
+                                 "l"(c < 4 ? &maps.run128 : &maps.run64), "r"(rows.col0 + c * 128), "r"(rows.row), "r"(bar)
                                  : "memory");
-                if (gathered)
+                if (rows.gathered)
                     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
-                                 ::"r"(to + lane * (c < 4 ? 512 : 256)), "l"(c < 4 ? &maps.row128 : &maps.row64), "r"(col0 + c * 128), "r"(y[0]),
-                                 "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(bar)
+                                 ::"r"(to + lane * (c < 4 ? 512 : 256)), "l"(c < 4 ? &maps.row128 : &maps.row64), "r"(rows.col0 + c * 128),
+                                 "r"(rows.y[0]), "r"(rows.y[1]), "r"(rows.y[2]), "r"(rows.y[3]), "r"(bar)
                                  : "memory");
                 issued = 5 * j + i + 1;
             }
             if (!ok) break;
-            at.next(a, segs, x);
         }
         if (__any_sync(~0u, s_failed))                             // no copy outlives the CTA
-            for (int i = max(0, issued - 2 * kChunks); i < issued; ++i) wait_full(&s_full[i / kChunks & 1][(i % kChunks + 4) % kChunks], i / kChunks >> 1 & 1);
-    } else if (w == 4) {                                           // products
+            for (int i = max(0, (int)issued - 2 * kChunks); i < (int)issued; ++i) wait_full(&s_full[i / kChunks & 1][(i % kChunks + 4) % kChunks], i / kChunks >> 1 & 1);
+    } else if (w == 8) {                                           // products
         Line at = begin;
         int64_t x = x0;
         int switches = 0;
@@ -286,19 +308,22 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
             bool summed = j < 0;
             int scored = more && !change ? 0 : kChunks;
             uint64_t since = 0;
-            for (uint32_t tries = 0; !summed || scored < kChunks; ++tries) {
-                if (!summed && __all_sync(~0u, is_full(&s_weighed[j & 1], j >> 1 & 1))) {
+            while (!summed || scored < kChunks) {                  // lanes 0 to 4 look after the chunks, the others after the weights
+                const bool there = lane < kChunks ? is_full(&s_full[(j + 1) & 1][(lane + 4) % kChunks], (j + 1) >> 1 & 1)
+                                                  : is_full(&s_weighed[j & 1], j >> 1 & 1);
+                const uint32_t ready = __ballot_sync(~0u, there);
+                bool moved = false;
+                if (!summed && ready >> 31) {
                     sum(j, first);
-                    summed = true;
-                    since = 0;
-                } else if (scored < kChunks && __all_sync(~0u, is_full(&s_full[(j + 1) & 1][(scored + 4) % kChunks], (j + 1) >> 1 & 1))) {
-                    score_chunk(j + 1, scored++);
-                    since = 0;
-                } else if ((tries & 63) == 0) {
+                    summed = moved = true;
+                }
+                for (; scored < kChunks && ready >> scored & 1; moved = true) score_chunk(j + 1, scored++);
+                if (moved) since = 0;
+                else if (!since) asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(since));
+                else {
                     uint64_t now;
                     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
-                    if (!since) since = now;
-                    if (__any_sync(~0u, s_failed || now - since > kLatentWaitNs)) {
+                    if (__any_sync(~0u, s_failed || now > since + kLatentWaitNs)) {
                         s_failed = 1;
                         ok = false;
                         break;
@@ -317,18 +342,20 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
             tensor_commit(&s_drained);
             wait_full(&s_drained, 0);
         }
-    } else if (w < 4) {                                            // softmax and outputs: a thread has position threadIdx.x
-        const uint32_t lanes = tmem + ((uint32_t)w << 21);         // this warp's 32 rows
-        float m[kLatentHeads], l[kLatentHeads], scale[kLatentHeads];
+    } else if (w < 8) {                                            // softmax and outputs
+        // a thread has a position (an element, of the outputs) and 8 query heads
+        const int here = (w & 3) * 32 + lane, h0 = w >> 2 << 3;
+        const uint32_t lanes = tmem + ((uint32_t)(w & 3) << 21) + h0;          // this warp's 32 rows, its first column
+        float m[kMine], l[kMine], scale[kMine];
         // Queries of a segment as codes, and what its scores are to be multiplied by.
         auto query = [&](const Line &p) {
-            const int h = threadIdx.x >> 3, part = threadIdx.x & 7;
+            const int h = threadIdx.x >> 4, part = threadIdx.x & 15;
             const int32_t kvh = p.seg / sets, in_group = p.seg % sets * kLatentHeads + h;
             const uint8_t *src = a.q + p.r * a.q_stride + ((int64_t)kvh * group + in_group) * a.head_dim * 2;
             const bool real = in_group < group;
             float top = 0.0f;
             if (real)
-                for (int d = part * 8; d < a.head_dim; d += 64) {
+                for (int d = part * 8; d < a.head_dim; d += 128) {
                     const uint4 y = __ldg(reinterpret_cast<const uint4 *>(src + d * 2));
                     for (uint32_t z : {y.x, y.y, y.z, y.w}) {
                         const float2 f = unpack<IO>(z);
@@ -336,11 +363,11 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
                     }
                 }
 #pragma unroll
-            for (int d = 1; d < 8; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+            for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
             const int e = top > 0.0f && top < INFINITY ? max(-100, min(100, 7 - ilogbf(top))) : 0;
             const float up = __int_as_float((127 + e) << 23);
             if (part == 0) s_scale[h] = top < INFINITY ? a.scale * __int_as_float((127 - e) << 23) : NAN;     // an infinite query: NaN
-            for (int b = part; b < kCacheMaxLatent / 16; b += 8) {
+            for (int b = part; b < kCacheMaxLatent / 16; b += 16) {
                 uint32_t codes[kTerms][4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -366,10 +393,10 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
         };
         auto begin_segment = [&]() {
 #pragma unroll
-            for (int h = 0; h < kLatentHeads; ++h) {
+            for (int h = 0; h < kMine; ++h) {
                 m[h] = -INFINITY;
                 l[h] = 0.0f;
-                scale[h] = s_scale[h];
+                scale[h] = s_scale[h0 + h];
             }
         };
         Line at = begin;
@@ -380,33 +407,33 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
         for (int j = 0;; ++j) {
             wait(&s_scored[j & 1], j >> 1);
             tensor_fence_after();
-            float s[kLatentHeads];
+            float s[kMine];
             {
-                uint32_t y[kTerms][16];
+                uint32_t y[kTerms][kMine];
 #pragma unroll
                 for (int k = 0; k < kTerms; ++k) tmem_load(y[k], lanes + kColScores + (j & 1) * 64 + k * 16);
                 tmem_load_wait();
-                const bool live = s_live[j & 1][threadIdx.x >> 2] >> (threadIdx.x & 3) & 1;
+                const bool live = s_live[j & 1][here >> 2] >> (here & 3) & 1;
 #pragma unroll
-                for (int h = 0; h < kLatentHeads; ++h) {
+                for (int h = 0; h < kMine; ++h) {
                     const float z = __uint_as_float(y[0][h]) + (__uint_as_float(y[1][h]) + __uint_as_float(y[2][h]) / kSpacing) / kSpacing;
                     s[h] = live ? z * scale[h] : -INFINITY;
                 }
             }
             float over = -INFINITY;
 #pragma unroll
-            for (int h = 0; h < kLatentHeads; ++h) over = fmaxf(over, s[h] - m[h]);
+            for (int h = 0; h < kMine; ++h) over = fmaxf(over, s[h] - m[h]);
             if (softmax_any(over > kSlack)) {                      // some maximum moves
-                float v[kLatentHeads];
+                float v[kMine];
 #pragma unroll
-                for (int h = 0; h < kLatentHeads; ++h) v[h] = s[h];
+                for (int h = 0; h < kMine; ++h) v[h] = s[h];
                 const float top = reduce_heads(v, [](float p, float q) { return fmaxf(p, q); });
-                if (!(lane & 1)) s_red[w][head_of(lane)] = top;
+                if (!(lane & 3)) s_red[w & 3][h0 + (lane >> 2)] = top;
                 softmax_any(false);
-                float old[kLatentHeads];
+                float old[kMine];
 #pragma unroll
-                for (int h = 0; h < kLatentHeads; ++h) {
-                    const float up = fmaxf(m[h], fmaxf(fmaxf(s_red[0][h], s_red[1][h]), fmaxf(s_red[2][h], s_red[3][h])));
+                for (int h = 0; h < kMine; ++h) {
+                    const float up = fmaxf(m[h], fmaxf(fmaxf(s_red[0][h0 + h], s_red[1][h0 + h]), fmaxf(s_red[2][h0 + h], s_red[3][h0 + h])));
                     old[h] = fast_exp2(m[h] - (up == -INFINITY ? 0.0f : up));
                     m[h] = up;
                     l[h] *= old[h];
@@ -417,19 +444,19 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
                     tensor_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < 4 * kTerms; ++c) {
-                        uint32_t y[16];
+                        uint32_t y[kMine];
                         tmem_load(y, lanes + kColSums + c * 16);
                         tmem_load_wait();
 #pragma unroll
-                        for (int h = 0; h < kLatentHeads; ++h) y[h] = __float_as_uint(__uint_as_float(y[h]) * old[h]);
+                        for (int h = 0; h < kMine; ++h) y[h] = __float_as_uint(__uint_as_float(y[h]) * old[h]);
                         tmem_store(y, lanes + kColSums + c * 16);
                     }
                     tmem_store_wait();
                 }
             }
-            uint32_t codes[kTerms][4];
+            uint32_t codes[kTerms][2];
 #pragma unroll
-            for (int h = 0; h < kLatentHeads; h += 4) {
+            for (int h = 0; h < kMine; h += 4) {
                 float v[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -446,8 +473,7 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
             if (j >= 2) wait(&s_free[j & 1][3], (j - 2) >> 1);
 #pragma unroll
             for (int k = 0; k < kTerms; ++k)                       // blocks of 16 columns x 8 positions
-                *(uint4 *)(smem + kOffWeight + (j & 1) * kWeightBytes + k * kTile * 16 + threadIdx.x * 16) =
-                    make_uint4(codes[k][0], codes[k][1], codes[k][2], codes[k][3]);
+                *(uint2 *)(smem + kOffWeight + (j & 1) * kWeightBytes + k * kTile * 16 + here * 16 + h0) = make_uint2(codes[k][0], codes[k][1]);
             fence_async();
             tensor_fence_before();
             arrive(&s_weighed[j & 1]);
@@ -465,14 +491,14 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
             wait(&s_free[j & 1][3], j >> 1);
             tensor_fence_after();
             {
-                float v[kLatentHeads];
+                float v[kMine];
 #pragma unroll
-                for (int h = 0; h < kLatentHeads; ++h) v[h] = l[h];
+                for (int h = 0; h < kMine; ++h) v[h] = l[h];
                 const float sum = reduce_heads(v, [](float p, float q) { return p + q; });
-                if (!(lane & 1)) s_red[w][head_of(lane)] = sum;
+                if (!(lane & 3)) s_red[w & 3][h0 + (lane >> 2)] = sum;
                 softmax_any(false);
 #pragma unroll
-                for (int h = 0; h < kLatentHeads; ++h) l[h] = (s_red[0][h] + s_red[1][h]) + (s_red[2][h] + s_red[3][h]);
+                for (int h = 0; h < kMine; ++h) l[h] = (s_red[0][h0 + h] + s_red[1][h0 + h]) + (s_red[2][h0 + h] + s_red[3][h0 + h]);
                 softmax_any(false);
             }
             const bool whole = ends && begun;
@@ -480,29 +506,29 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
             uint8_t *const part = parts + (size_t)(blockIdx.x * 2 + begun) * kLatentPartial;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
-                uint32_t y[kTerms][16];
+                uint32_t y[kTerms][kMine];
 #pragma unroll
                 for (int k = 0; k < kTerms; ++k) tmem_load(y[k], lanes + kColSums + c * kCols + k * 16);
                 tmem_load_wait();
-                const int d = c * 128 + threadIdx.x;
+                const int d = c * 128 + here;
 #pragma unroll
-                for (int h = 0; h < kLatentHeads; ++h) {
+                for (int h = 0; h < kMine; ++h) {
                     const float z = (__uint_as_float(y[0][h]) + (__uint_as_float(y[1][h]) + __uint_as_float(y[2][h]) / kSpacing) / kSpacing) / kWeightUp;
-                    if (!whole) __stcg((float *)part + partial_at(d, h), z);
-                    else if (h < heads && d < a.v_dim)
-                        ((uint16_t *)(a.out + at.r * a.out_stride))[(int64_t)(head0 + h) * a.v_dim + d] =
+                    if (!whole) __stcg((float *)part + partial_at(d, h0 + h), z);
+                    else if (h0 + h < heads && d < a.v_dim)
+                        ((uint16_t *)(a.out + at.r * a.out_stride))[(int64_t)(head0 + h0 + h) * a.v_dim + d] =
                             (uint16_t)pack<IO>(l[h] == 0.0f ? 0.0f : z * (a.v_scale / l[h]), 0.0f);
                 }
             }
             tensor_fence_before();
 #pragma unroll
-            for (int h = 0; h < kLatentHeads; ++h)
-                if ((int)threadIdx.x == h) {
+            for (int h = 0; h < kMine; ++h)
+                if (here == h) {
                     if (!whole) {
-                        __stcg((float *)(part + kLatentFloat4 * 16) + h, m[h]);
-                        __stcg((float *)(part + kLatentFloat4 * 16) + kLatentHeads + h, l[h]);
-                    } else if (a.lse && h < heads)
-                        a.lse[(int64_t)at.r * a.n_q_heads + head0 + h] = l[h] == 0.0f ? -INFINITY : (m[h] + log2f(l[h])) * kLn2;
+                        __stcg((float *)(part + kLatentFloat4 * 16) + h0 + h, m[h]);
+                        __stcg((float *)(part + kLatentFloat4 * 16) + kLatentHeads + h0 + h, l[h]);
+                    } else if (a.lse && h0 + h < heads)
+                        a.lse[(int64_t)at.r * a.n_q_heads + head0 + h0 + h] = l[h] == 0.0f ? -INFINITY : (m[h] + log2f(l[h])) * kLn2;
                 }
             if (!whole && begun)
                 opened = OpenSegment{at.r, at.seg, batch.split.cta_of(at.seg_begin(segs) + at.tiles - 1) - (int32_t)blockIdx.x + 1, 0};
@@ -514,7 +540,7 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
     }
     tensor_fence_before();
     __syncthreads();
-    if (w == 4) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    if (w == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
     if (threadIdx.x == 0) {
         if (s_failed) atomicAdd(a.pool.skipped + 1, 1ull);
         open[blockIdx.x] = s_failed ? OpenSegment{0, 0, 0, 0} : opened;
