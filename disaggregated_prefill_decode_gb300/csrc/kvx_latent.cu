@@ -429,10 +429,11 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
     if (threadIdx.x == 0) open[blockIdx.x] = s_timeout ? OpenSegment{0, 0, 0, 0} : opened;
 }
 
-// Joins the segments that go over several CTAs: 64 float4s of a segment's sums at a time, in four groups of 64 threads that take
-// every fourth piece.
+// Joins the segments that go over several CTAs. Up to kJoinFew pieces a thread joins a float4 of the sums by itself, 256 at a time;
+// of more pieces 64 float4s at a time, four groups of 64 threads taking every fourth piece.
 constexpr int kJoinThreads = 256, kJoinSlices = kLatentFloat4 / 64, kJoinCtas = 8;      // CTAs per SM
 constexpr int kJoinList = 512;                                                          // at least the CTAs of the first kernel
+constexpr int kJoinFew = 8;
 
 template <int IO> __global__ void __launch_bounds__(kJoinThreads) kvx_attend_latent_join(const __grid_constant__ AttendArgs a, int ctas) {
     __shared__ int32_t s_list[kJoinList], s_count[kJoinList / 32];
@@ -461,25 +462,70 @@ template <int IO> __global__ void __launch_bounds__(kJoinThreads) kvx_attend_lat
         }
         __syncthreads();
     }
-    const int f = threadIdx.x & 63, part = threadIdx.x >> 6, lane = f & 31, t = lane & 3, g = lane >> 2;
-    for (int item = blockIdx.x; item < n_open * kJoinSlices; item += gridDim.x) {
-        const int cta = s_list[item / kJoinSlices], slice = item % kJoinSlices;
+    // float4 f of the sums of one segment: query head, element, and the outputs
+    auto head_of = [](int f) { return (f >> 7 & 1) * 8 + 2 * (f & 3) + (f >> 6 & 1); };
+    auto element_of = [](int f) { return (f >> 8) * 64 + (f >> 2 & 7) * 8 + (f >> 5 & 1) * 4; };
+    auto put = [&](const OpenSegment &seg, int f, float4 o, float top, float l) {
+        const int q = head_of(f), d = element_of(f);
+        const int32_t in_group = seg.seg % sets * kLatentHeads + q, head = seg.seg / sets * group + in_group;
+        if (in_group >= group) return;
+        const float inv = l == 0.0f ? 0.0f : a.v_scale / l;
+        if (d < a.v_dim)
+            *reinterpret_cast<uint2 *>(a.out + seg.r * a.out_stride + ((int64_t)head * a.v_dim + d) * 2) =
+                make_uint2(pack<IO>(o.x * inv, o.y * inv), pack<IO>(o.z * inv, o.w * inv));
+        if (a.lse && d == 0) a.lse[(int64_t)seg.r * a.n_q_heads + head] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
+    };
+    for (int item = blockIdx.x; item < n_open * (kLatentFloat4 / kJoinThreads); item += gridDim.x) {
+        const int cta = s_list[item / (kLatentFloat4 / kJoinThreads)], f = item % (kLatentFloat4 / kJoinThreads) * kJoinThreads + threadIdx.x, q = head_of(f);
         const OpenSegment seg = open[cta];
-        const int q = (slice >> 1 & 1) * 8 + 2 * t + (slice & 1), d = (slice >> 2) * 64 + g * 8 + (f >> 5) * 4;
+        if (seg.pieces > kJoinFew) continue;
         const uint8_t *const first = parts + (size_t)(2 * cta + 1) * kLatentPartial;         // the others: slot 0 of the CTAs after it
+        float4 y[kJoinFew];
+        float m[kJoinFew], s[kJoinFew], top = -INFINITY, l = 0.0f;
+#pragma unroll
+        for (int x = 0; x < kJoinFew; ++x) {
+            const uint8_t *const p = x ? first + (size_t)(2 * x - 1) * kLatentPartial : first;
+            m[x] = -INFINITY;
+            if (x < seg.pieces) {
+                y[x] = __ldcg((const float4 *)p + f);
+                m[x] = __ldcg((const float *)(p + kLatentFloat4 * 16) + q);
+                s[x] = __ldcg((const float *)(p + kLatentFloat4 * 16) + kLatentHeads + q);
+            }
+            top = fmaxf(top, m[x]);
+        }
+        const float ref = top == -INFINITY ? 0.0f : top;
+        float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll
+        for (int x = 0; x < kJoinFew; ++x)
+            if (x < seg.pieces) {
+                const float z = fast_exp2(m[x] - ref);
+                l += z * s[x];
+                o.x += z * y[x].x;
+                o.y += z * y[x].y;
+                o.z += z * y[x].z;
+                o.w += z * y[x].w;
+            }
+        put(seg, f, o, top, l);
+    }
+    const int f64 = threadIdx.x & 63, part = threadIdx.x >> 6;
+    for (int item = blockIdx.x; item < n_open * kJoinSlices; item += gridDim.x) {
+        const int cta = s_list[item / kJoinSlices], f = item % kJoinSlices * 64 + f64, q = head_of(f);
+        const OpenSegment seg = open[cta];
+        if (seg.pieces <= kJoinFew) continue;
+        const uint8_t *const first = parts + (size_t)(2 * cta + 1) * kLatentPartial;
         auto at = [&](int x) { return x ? first + (size_t)(2 * x - 1) * kLatentPartial : first; };
         float top = -INFINITY, l = 0.0f;
         float4 o = make_float4(0, 0, 0, 0);
 #pragma unroll 4
         for (int x = part; x < seg.pieces; x += 4) top = fmaxf(top, __ldcg((const float *)(at(x) + kLatentFloat4 * 16) + q));
-        s_top[part][f] = top;
+        s_top[part][f64] = top;
         __syncthreads();
-        top = fmaxf(fmaxf(s_top[0][f], s_top[1][f]), fmaxf(s_top[2][f], s_top[3][f]));
+        top = fmaxf(fmaxf(s_top[0][f64], s_top[1][f64]), fmaxf(s_top[2][f64], s_top[3][f64]));
         const float ref = top == -INFINITY ? 0.0f : top;
 #pragma unroll 8
         for (int x = part; x < seg.pieces; x += 4) {
             const float *const ml = (const float *)(at(x) + kLatentFloat4 * 16);
-            const float4 y = __ldcg((const float4 *)at(x) + slice * 64 + f);
+            const float4 y = __ldcg((const float4 *)at(x) + f);
             const float z = fast_exp2(__ldcg(ml + q) - ref);
             l += z * __ldcg(ml + kLatentHeads + q);
             o.x += z * y.x;
@@ -487,24 +533,17 @@ template <int IO> __global__ void __launch_bounds__(kJoinThreads) kvx_attend_lat
             o.z += z * y.z;
             o.w += z * y.w;
         }
-        s_o[part][f] = o;
-        s_sum[part][f] = l;
+        s_o[part][f64] = o;
+        s_sum[part][f64] = l;
         __syncthreads();
         if (part == 0) {
 #pragma unroll
             for (int i = 1; i < 4; ++i) {
-                const float4 y = s_o[i][f];
+                const float4 y = s_o[i][f64];
                 o = make_float4(o.x + y.x, o.y + y.y, o.z + y.z, o.w + y.w);
-                l += s_sum[i][f];
+                l += s_sum[i][f64];
             }
-            const int32_t in_group = seg.seg % sets * kLatentHeads + q, head = seg.seg / sets * group + in_group;
-            if (in_group < group) {
-                const float inv = l == 0.0f ? 0.0f : a.v_scale / l;
-                if (d < a.v_dim)
-                    *reinterpret_cast<uint2 *>(a.out + seg.r * a.out_stride + ((int64_t)head * a.v_dim + d) * 2) =
-                        make_uint2(pack<IO>(o.x * inv, o.y * inv), pack<IO>(o.z * inv, o.w * inv));
-                if (a.lse && d == 0) a.lse[(int64_t)seg.r * a.n_q_heads + head] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
-            }
+            put(seg, f, o, top, l);
         }
     }
 }

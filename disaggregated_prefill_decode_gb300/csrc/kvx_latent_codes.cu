@@ -122,7 +122,7 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ __align__(8) uint64_t s_full[2][kChunks], s_free[2][kChunks];           // chunk by chunk
     __shared__ __align__(8) uint64_t s_scored[2], s_weighed[2], s_queried, s_drained;
-    __shared__ uint8_t s_live[2][32];                              // live positions, four a byte
+    __shared__ uint8_t s_live[3][32];                              // live positions, four a byte
     __shared__ __align__(16) float s_red[4][kLatentHeads];
     __shared__ float s_scale[kLatentHeads];
     __shared__ uint32_t s_tmem;
@@ -231,17 +231,16 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
             if (rows.col0 == ~0u) break;
 #pragma unroll
             for (int i = 0; i < kLookAhead; ++i) queue[i] = queue[i + 1];
+            s_live[j % 3][lane] = (uint8_t)rows.live;              // three of them: tile j - 3 is through, its chunks were free
+            __syncwarp();
             bool ok = true;
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
                 const int c = (i + 4) % kChunks;                   // in the order in which they become free
                 if (!(ok = __all_sync(~0u, j < 2 || wait(&s_free[j & 1][c], (j - 2) >> 1)))) break;
                 const uint32_t bar = shared_addr(&s_full[j & 1][c]), to = shared_addr(smem + (j & 1) * kStage + c * kChunk);
-                if (i == 1) s_live[j & 1][lane] = (uint8_t)rows.live;   // the softmax of tile j - 2 is through with its own
-                __syncwarp();
-                if (lane == 0)
+                if (lane == 0)                                     // a copy of another lane may count before: the phase waits for this
                     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(c < 4 ? kChunk : kChunk / 2) : "memory");
-                __syncwarp();
                 if (rows.boxed)
                     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
                                      to + lane * run * (c < 4 ? 128 : 64)),
@@ -413,7 +412,7 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
 #pragma unroll
                 for (int k = 0; k < kTerms; ++k) tmem_load(y[k], lanes + kColScores + (j & 1) * 64 + k * 16);
                 tmem_load_wait();
-                const bool live = s_live[j & 1][here >> 2] >> (here & 3) & 1;
+                const bool live = s_live[j % 3][here >> 2] >> (here & 3) & 1;
 #pragma unroll
                 for (int h = 0; h < kMine; ++h) {
                     const float z = __uint_as_float(y[0][h]) + (__uint_as_float(y[1][h]) + __uint_as_float(y[2][h]) / kSpacing) / kSpacing;
