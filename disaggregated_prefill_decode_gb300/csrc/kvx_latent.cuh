@@ -34,13 +34,6 @@ __device__ __forceinline__ bool wait_full(uint64_t *bar, uint32_t parity) {
     }
 }
 
-__device__ __forceinline__ bool is_full(uint64_t *bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile("{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
-                 : "=r"(done) : "r"(shared_addr(bar)), "r"(parity) : "memory");
-    return done;
-}
-
 // What a CTA leaves for the joining kernel: the segment that begins in its stretch and goes on after it (pieces 0: none).
 struct OpenSegment {
     int32_t r, seg, pieces, unused;

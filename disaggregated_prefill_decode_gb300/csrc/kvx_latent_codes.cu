@@ -25,7 +25,7 @@ namespace kvx {
 
 constexpr int kTile = 128;                                     // positions
 constexpr int kSoftThreads = 256;                              // warps 0-7: softmax and outputs, half of the query heads each four
-constexpr int kCodeThreads = kSoftThreads + 64;                // 8: products; 9: copies
+constexpr int kCodeThreads = kSoftThreads + 7 * 32;            // 8, 9: products of the scores, of the sums; 10-14: copies, a chunk each
 constexpr int kMine = kLatentHeads / 2;                        // query heads of a softmax thread
 constexpr int kChunk = kTile * 128, kStage = 4 * kChunk + kTile * 64;   // 4 chunks of 128 elements, one of 64
 constexpr int kChunks = 5;                                     // the last one is used up by the scores, the others in their order by the sums
@@ -36,7 +36,6 @@ constexpr float kSpacing = 32.0f;
 constexpr float kSlack = 3.0f;                                 // in powers of two
 constexpr float kWeightUp = 32.0f;                             // 2^(kSlack + 5) is within the codes' 448
 constexpr uint32_t kColScores = 0, kColSums = 128, kTmemCols = 512;      // two buffers of scores 64 columns apart, then 4 x 48
-constexpr int kLookAhead = 1;                                  // tiles whose rows are looked up ahead of their copy
 constexpr int kCodeSwitch = 1;                                 // places of the line that a change of segment counts
 
 // Shared memory operands: start, the two strides, swizzle (0 none, 2 of 128 bytes, 4 of 64 bytes).
@@ -121,7 +120,7 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
     using Line = Place<kTile, kCodeSwitch>;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ __align__(8) uint64_t s_full[2][kChunks], s_free[2][kChunks];           // chunk by chunk
-    __shared__ __align__(8) uint64_t s_scored[2], s_weighed[2], s_queried, s_drained;
+    __shared__ __align__(8) uint64_t s_scored[2], s_weighed[2], s_queried, s_drained[2];
     __shared__ uint8_t s_live[3][32];                              // live positions, four a byte
     __shared__ __align__(16) float s_red[4][kLatentHeads];
     __shared__ float s_scale[kLatentHeads];
@@ -149,10 +148,10 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
                 asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_addr(&s_free[i][c])) : "memory");
             }
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_addr(&s_scored[i])) : "memory");
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_addr(&s_drained[i])) : "memory");
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_addr(&s_weighed[i])), "n"(kSoftThreads) : "memory");
         }
         asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_addr(&s_queried)), "n"(kSoftThreads) : "memory");
-        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_addr(&s_drained)) : "memory");
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (w == 8) {
@@ -173,115 +172,52 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
     };
     OpenSegment opened = {0, 0, 0, 0};
 
+    if (w == 10 && lane == 0)
+        for (const CUtensorMap *m : {&maps.run128, &maps.run64}) asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
     if (x0 >= c_end) {
         // nothing but the end of a segment
-    } else if (w == 9) {                                           // copies
-        // A lane has a run of the tile, if there are as many, and four positions. Runs that are live or dead as a whole go in
-        // boxes; the four positions of other runs by a gather.
-        struct Rows {
-            bool boxed, gathered;
-            uint32_t row, y[4], live, col0;
-        };
-        const uint32_t run = (uint32_t)a.map_run, nothing = (uint32_t)a.map_rows;      // beyond the last row: reads as zeros
-        auto look_up = [&](const Line &at) {
-            Rows o;
-            const int32_t kvh = at.seg / sets;
-            const uint32_t first = (uint32_t)at.first, len = (uint32_t)at.len, tile0 = first / kTile * kTile + (uint32_t)at.tile * kTile;
-            auto row_of = [&](uint32_t pos) {
-                if (pos < first || pos >= len) return nothing;
-                const uint32_t col = (__umulhi(pos, a.block_mul) + pos) >> a.block_shift, slot = pos - col * (uint32_t)a.pool.block_size;
-                const int32_t blk = a.block_table[at.r * a.table_stride + col];
-                if (blk < 0 || blk >= a.pool.n_blocks) {
-                    if (at.seg == 0) atomicAdd(a.pool.skipped, 1ull);
-                    return nothing;
-                }
-                return (uint32_t)blk * a.map_block + (uint32_t)kvh * a.map_head + slot;
-            };
-            auto whole = [&](uint32_t pos) { return run >= 4 && (pos + run <= first || pos >= len || (pos >= first && pos + run <= len)); };
-            const uint32_t run0 = tile0 + lane * run, four0 = tile0 + 4 * lane, my_run = 4 * lane / run;
-            o.col0 = (uint32_t)kvh * a.map_col;
-            o.boxed = lane * run < kTile && whole(run0);
-            o.gathered = !whole(tile0 + my_run * run);
-            o.row = o.boxed ? row_of(run0) : nothing;
-            o.live = 0;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                o.y[k] = o.gathered ? row_of(four0 + k) : nothing;
-                o.live |= (uint32_t)(o.y[k] != nothing) << k;
-            }
-            if (__shfl_sync(~0u, o.row, my_run) != nothing && !o.gathered) o.live = 15;
-            return o;
-        };
-        Line at = begin;
-        int64_t x = x0, issued = 0;                                // chunks under way or arrived
-        Rows queue[kLookAhead + 1];
-#pragma unroll
-        for (int i = 0; i < kLookAhead; ++i)
-            if (x < c_end) {
-                queue[i] = look_up(at);
-                at.next(a, segs, x);
-            } else queue[i].col0 = ~0u;
-        for (int j = 0;; ++j) {
-            queue[kLookAhead].col0 = ~0u;
-            if (x < c_end) {
-                queue[kLookAhead] = look_up(at);
-                at.next(a, segs, x);
-            }
-            const Rows rows = queue[0];
-            if (rows.col0 == ~0u) break;
-#pragma unroll
-            for (int i = 0; i < kLookAhead; ++i) queue[i] = queue[i + 1];
-            s_live[j % 3][lane] = (uint8_t)rows.live;              // three of them: tile j - 3 is through, its chunks were free
-            __syncwarp();
-            bool ok = true;
-#pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
-                const int c = (i + 4) % kChunks;                   // in the order in which they become free
-                if (!(ok = __all_sync(~0u, j < 2 || wait(&s_free[j & 1][c], (j - 2) >> 1)))) break;
-                const uint32_t bar = shared_addr(&s_full[j & 1][c]), to = shared_addr(smem + (j & 1) * kStage + c * kChunk);
-                if (lane == 0)                                     // a copy of another lane may count before: the phase waits for this
-                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(c < 4 ? kChunk : kChunk / 2) : "memory");
-                if (rows.boxed)
-                    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-                                     to + lane * run * (c < 4 ? 128 : 64)),
-                                 "l"(c < 4 ? &maps.run128 : &maps.run64), "r"(rows.col0 + c * 128), "r"(rows.row), "r"(bar)
-                                 : "memory");
-                if (rows.gathered)
-                    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
-                                 ::"r"(to + lane * (c < 4 ? 512 : 256)), "l"(c < 4 ? &maps.row128 : &maps.row64), "r"(rows.col0 + c * 128),
-                                 "r"(rows.y[0]), "r"(rows.y[1]), "r"(rows.y[2]), "r"(rows.y[3]), "r"(bar)
-                                 : "memory");
-                issued = 5 * j + i + 1;
-            }
-            if (!ok) break;
-        }
-        if (__any_sync(~0u, s_failed))                             // no copy outlives the CTA
-            for (int i = max(0, (int)issued - 2 * kChunks); i < (int)issued; ++i) wait_full(&s_full[i / kChunks & 1][(i % kChunks + 4) % kChunks], i / kChunks >> 1 & 1);
-    } else if (w == 8) {                                           // products
+    } else if (w == 8) {                                           // products of the scores, chunk by chunk as they arrive
+        const uint32_t smem0 = shared_addr(smem);                  // operands at their start; the rest are constants, in 16 bytes
+        const uint64_t keys = operand(smem0, 16, 1024, 2), keys_last = operand(smem0 + 4 * kChunk, 16, 512, 4);
+        const uint64_t queries = operand(smem0 + kOffQuery, (kCols / 8) * 128, 128, 0);
         Line at = begin;
         int64_t x = x0;
         int switches = 0;
-        // Operands at their start; what is added to them below are constants in units of 16 bytes.
-        const uint32_t smem0 = shared_addr(smem);
-        const uint64_t keys = operand(smem0, 16, 1024, 2), keys_last = operand(smem0 + 4 * kChunk, 16, 512, 4), values = operand(smem0, 16, 1024, 2);
-        const uint64_t queries = operand(smem0 + kOffQuery, (kCols / 8) * 128, 128, 0), weights = operand(smem0 + kOffWeight, 128, kTile * 16, 0);
-        // The i-th chunk to arrive. No tcgen05 fence: it follows a copy, not other threads' use of TMEM.
-        auto score_chunk = [&](int j, int i) {
+        bool ok = true, first = true;
+        for (int j = 0; ok && x < c_end; ++j) {
             const uint64_t stage = (j & 1) * (kStage / 16);
             const uint32_t d = tmem + kColScores + (j & 1) * 64;
-            if (i == 0) {
-#pragma unroll
-                for (int y = 0; y < 2; ++y)
-                    tensor_mma(d, keys_last + stage + y * 2, queries + (4 * 8 + y * 2) * (kCols / 8) * 8, kIdescRows, y > 0);
-                tensor_commit(&s_free[j & 1][4]);
-            } else {
-                const uint64_t k = keys + stage + (uint32_t)(i - 1) * (kChunk / 16), q = queries + (uint32_t)(i - 1) * (8 * (kCols / 8) * 8);
-#pragma unroll
-                for (int y = 0; y < 4; ++y) tensor_mma(d, k + y * 2, q + y * 2 * (kCols / 8) * 8, kIdescRows, true);
-                if (i == kChunks - 1) tensor_commit(&s_scored[j & 1]);
+            if (j >= 2) {                                          // the scores before are read
+                ok = __all_sync(~0u, wait(&s_weighed[j & 1], (j - 2) >> 1));
+                tensor_fence_after();
             }
-        };
-        auto sum = [&](int j, bool first) {
+            if (ok && first) ok = __all_sync(~0u, wait(&s_queried, switches++));
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                const int c = (i + 4) % kChunks;
+                if (!ok || !(ok = __all_sync(~0u, wait(&s_full[j & 1][c], j >> 1)))) break;
+#pragma unroll
+                for (int y = 0; y < (c < 4 ? 4 : 2); ++y)
+                    tensor_mma(d, (c < 4 ? keys + c * (kChunk / 16) : keys_last) + stage + y * 2, queries + (c * 8 + y * 2) * (kCols / 8) * 8, kIdescRows,
+                               i > 0 || y > 0);
+                if (c == 4) tensor_commit(&s_free[j & 1][4]);
+            }
+            if (ok) tensor_commit(&s_scored[j & 1]);
+            at.next(a, segs, x);
+            first = at.tile == 0;
+        }
+        if (!ok) {                                                 // no product outlives the CTA
+            tensor_commit(&s_drained[0]);
+            wait_full(&s_drained[0], 0);
+        }
+    } else if (w == 9) {                                           // products of the sums
+        const uint32_t smem0 = shared_addr(smem);
+        const uint64_t values = operand(smem0, 16, 1024, 2), weights = operand(smem0 + kOffWeight, 128, kTile * 16, 0);
+        Line at = begin;
+        int64_t x = x0;
+        bool ok = true, first = true;
+        for (int j = 0; x < c_end; ++j) {
+            if (!(ok = __all_sync(~0u, wait(&s_weighed[j & 1], j >> 1)))) break;
             tensor_fence_after();
             const uint64_t v = values + (j & 1) * (kStage / 16), p = weights + (j & 1) * (kWeightBytes / 16);
 #pragma unroll
@@ -291,55 +227,12 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
                     tensor_mma(tmem + kColSums + c * kCols, v + c * (kChunk / 16) + i * 256, p + i * 32, kIdescCols, !first || i > 0);
                 tensor_commit(&s_free[j & 1][c]);
             }
-        };
-        // The sums of tile j and, unless they are of another segment, the scores of tile j + 1: whichever can go on. Tile -1
-        // has nothing to sum.
-        bool ok = true, first = true;
-        for (int j = -1; ok; ++j) {
-            bool change = true, more = true;
-            if (j >= 0) {
-                Line nxt = at;
-                nxt.next(a, segs, x);
-                more = x < c_end;
-                change = nxt.tile == 0;
-                at = nxt;
-            }
-            bool summed = j < 0;
-            int scored = more && !change ? 0 : kChunks;
-            uint64_t since = 0;
-            while (!summed || scored < kChunks) {                  // lanes 0 to 4 look after the chunks, the others after the weights
-                const bool there = lane < kChunks ? is_full(&s_full[(j + 1) & 1][(lane + 4) % kChunks], (j + 1) >> 1 & 1)
-                                                  : is_full(&s_weighed[j & 1], j >> 1 & 1);
-                const uint32_t ready = __ballot_sync(~0u, there);
-                bool moved = false;
-                if (!summed && ready >> 31) {
-                    sum(j, first);
-                    summed = moved = true;
-                }
-                for (; scored < kChunks && ready >> scored & 1; moved = true) score_chunk(j + 1, scored++);
-                if (moved) since = 0;
-                else if (!since) asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(since));
-                else {
-                    uint64_t now;
-                    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
-                    if (__any_sync(~0u, s_failed || now > since + kLatentWaitNs)) {
-                        s_failed = 1;
-                        ok = false;
-                        break;
-                    }
-                }
-            }
-            if (!ok || !more) break;
-            first = change;
-            if (change) {
-                ok = __all_sync(~0u, wait(&s_queried, switches++));
-                for (int i = 0; i < kChunks && ok; ++i)
-                    if ((ok = __all_sync(~0u, wait(&s_full[(j + 1) & 1][(i + 4) % kChunks], (j + 1) >> 1)))) score_chunk(j + 1, i);
-            }
+            at.next(a, segs, x);
+            first = at.tile == 0;
         }
-        if (!ok) {                                             // no product outlives the CTA
-            tensor_commit(&s_drained);
-            wait_full(&s_drained, 0);
+        if (!ok) {
+            tensor_commit(&s_drained[1]);
+            wait_full(&s_drained[1], 0);
         }
     } else if (w < 8) {                                            // softmax and outputs
         // a thread has a position (an element, of the outputs) and 8 query heads
@@ -536,6 +429,77 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
             begin_segment();
             first = begun = true;
         }
+    } else {                                                       // copies of a chunk
+        const int c = w - 10;
+        // A lane has a run of the tile, if there are as many, and four positions. Runs that are live or dead as a whole go in
+        // boxes; the four positions of other runs by a gather.
+        struct Rows {
+            bool boxed, gathered;
+            uint32_t row, y[4], live, col0;
+        };
+        const uint32_t run = (uint32_t)a.map_run, nothing = (uint32_t)a.map_rows;      // beyond the last row: reads as zeros
+        auto look_up = [&](const Line &at) {
+            Rows o;
+            const int32_t kvh = at.seg / sets;
+            const uint32_t first = (uint32_t)at.first, len = (uint32_t)at.len, tile0 = first / kTile * kTile + (uint32_t)at.tile * kTile;
+            auto row_of = [&](uint32_t pos) {
+                if (pos < first || pos >= len) return nothing;
+                const uint32_t col = (__umulhi(pos, a.block_mul) + pos) >> a.block_shift, slot = pos - col * (uint32_t)a.pool.block_size;
+                const int32_t blk = a.block_table[at.r * a.table_stride + col];
+                if (blk < 0 || blk >= a.pool.n_blocks) {
+                    if (at.seg == 0 && c == 0) atomicAdd(a.pool.skipped, 1ull);
+                    return nothing;
+                }
+                return (uint32_t)blk * a.map_block + (uint32_t)kvh * a.map_head + slot;
+            };
+            auto whole = [&](uint32_t pos) { return run >= 4 && (pos + run <= first || pos >= len || (pos >= first && pos + run <= len)); };
+            const uint32_t run0 = tile0 + lane * run, four0 = tile0 + 4 * lane, my_run = 4 * lane / run;
+            o.col0 = (uint32_t)kvh * a.map_col;
+            o.boxed = lane * run < kTile && whole(run0);
+            o.gathered = !whole(tile0 + my_run * run);
+            o.row = o.boxed ? row_of(run0) : nothing;
+            o.live = __shfl_sync(~0u, o.row, my_run) != nothing ? 15 : 0;
+            if (o.gathered) {
+                o.live = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    o.y[k] = row_of(four0 + k);
+                    o.live |= (uint32_t)(o.y[k] != nothing) << k;
+                }
+            }
+            return o;
+        };
+        const CUtensorMap *const run_map = c < 4 ? &maps.run128 : &maps.run64, *const row_map = c < 4 ? &maps.row128 : &maps.row64;
+        const uint32_t wide = c < 4 ? 128 : 64, bytes = wide * kTile;
+        Line at = begin;
+        int64_t x = x0;
+        int issued = 0;
+        Rows rows = look_up(at);
+        for (; x < c_end; ++issued) {
+            const int j = issued;
+            if (!__all_sync(~0u, j < 2 || wait(&s_free[j & 1][c], (j - 2) >> 1))) break;
+            const uint32_t bar = shared_addr(&s_full[j & 1][c]), to = shared_addr(smem + (j & 1) * kStage + c * kChunk);
+            if (c == 0) {
+                s_live[j % 3][lane] = (uint8_t)rows.live;          // tile j - 3 is through, its chunks were free
+                __syncwarp();
+            }
+            if (lane == 0)                                         // a copy of another lane may count before: the phase waits for this
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+            if (rows.boxed)
+                asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                                 to + lane * run * wide),
+                             "l"(run_map), "r"(rows.col0 + c * 128), "r"(rows.row), "r"(bar)
+                             : "memory");
+            if (rows.gathered)
+                asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+                             ::"r"(to + lane * 4 * wide), "l"(row_map), "r"(rows.col0 + c * 128), "r"(rows.y[0]), "r"(rows.y[1]), "r"(rows.y[2]),
+                             "r"(rows.y[3]), "r"(bar)
+                             : "memory");
+            at.next(a, segs, x);
+            if (x < c_end) rows = look_up(at);                     // while this one is under way
+        }
+        if (__any_sync(~0u, s_failed))                             // no copy outlives the CTA
+            for (int j = max(0, issued - 2); j < issued; ++j) wait_full(&s_full[j & 1][c], j >> 1 & 1);
     }
     tensor_fence_before();
     __syncthreads();
