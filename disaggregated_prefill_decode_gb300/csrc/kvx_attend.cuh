@@ -192,7 +192,7 @@ template <int TOK, int WARPS, int MIN, int EXTRA> struct Batch {
         if (blockIdx.x == 0)
             for (int32_t r = threadIdx.x; r < a.n_reqs; r += 32 * WARPS)
                 if (a.seq_len[r] < 0 || a.seq_len[r] > cap) atomicAdd(a.pool.skipped, 1ull);
-        if (per > PER) find(a, divide(split.begin(blockIdx.x), segs));
+        if (per > PER && (int32_t)blockIdx.x < split.ctas) find(a, divide(split.begin(blockIdx.x), segs));
     }
 
     // All threads: the request that holds tile y of the requests' line.

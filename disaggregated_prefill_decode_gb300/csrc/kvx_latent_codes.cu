@@ -129,18 +129,7 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int32_t group = a.n_q_heads / a.n_kv_heads, sets = (group + kLatentHeads - 1) / kLatentHeads, segs = a.n_kv_heads * sets;
 
-    wait_for_earlier();
-    OpenSegment *const open = (OpenSegment *)a.scratch;
-    uint8_t *const parts = a.scratch + kScratchCounters * sizeof(uint32_t);
-    const Batch<kTile, kCodeThreads / 32, 1, kCodeSwitch> batch(a, segs);
-    if ((int32_t)blockIdx.x >= batch.split.ctas) {
-        if (threadIdx.x == 0) open[blockIdx.x].pieces = 0;
-        return;
-    }
-    const int64_t c_begin = batch.split.begin(blockIdx.x), c_end = batch.split.begin(blockIdx.x + 1);
-    int64_t x0 = c_begin;
-    const Line begin = batch.locate(a, segs, x0);
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0) {                                        // what touches no memory, while the kernel before still runs
         s_failed = 0;
         for (int i = 0; i < 2; ++i) {
             for (int c = 0; c < kChunks; ++c) {
@@ -159,6 +148,17 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         tensor_fence_before();
     }
+    if (w == 10 && lane == 0)
+        for (const CUtensorMap *m : {&maps.run128, &maps.run64}) asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+    wait_for_earlier();
+    OpenSegment *const open = (OpenSegment *)a.scratch;
+    uint8_t *const parts = a.scratch + kScratchCounters * sizeof(uint32_t);
+    const Batch<kTile, kCodeThreads / 32, 1, kCodeSwitch> batch(a, segs);
+    const bool works = (int32_t)blockIdx.x < batch.split.ctas;
+    const int64_t c_begin = works ? batch.split.begin(blockIdx.x) : 0, c_end = works ? batch.split.begin(blockIdx.x + 1) : 0;
+    int64_t x0 = c_begin;
+    Line begin = {};
+    if (works) begin = batch.locate(a, segs, x0);
     __syncthreads();
     tensor_fence_after();
     const uint32_t tmem = s_tmem;
@@ -172,10 +172,8 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
     };
     OpenSegment opened = {0, 0, 0, 0};
 
-    if (w == 10 && lane == 0)
-        for (const CUtensorMap *m : {&maps.run128, &maps.run64}) asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
     if (x0 >= c_end) {
-        // nothing but the end of a segment
+        // nothing, or nothing but the end of a segment
     } else if (w == 8) {                                           // products of the scores, chunk by chunk as they arrive
         const uint32_t smem0 = shared_addr(smem);                  // operands at their start; the rest are constants, in 16 bytes
         const uint64_t keys = operand(smem0, 16, 1024, 2), keys_last = operand(smem0 + 4 * kChunk, 16, 512, 4);
@@ -245,39 +243,49 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
             const int32_t kvh = p.seg / sets, in_group = p.seg % sets * kLatentHeads + h;
             const uint8_t *src = a.q + p.r * a.q_stride + ((int64_t)kvh * group + in_group) * a.head_dim * 2;
             const bool real = in_group < group;
+            constexpr int kBlocks = (kCacheMaxLatent / 16 + 15) / 16;  // of 16 elements, for each of a head's 16 threads
+            uint4 y[kBlocks][2];
             float top = 0.0f;
-            if (real)
-                for (int d = part * 8; d < a.head_dim; d += 128) {
-                    const uint4 y = __ldg(reinterpret_cast<const uint4 *>(src + d * 2));
-                    for (uint32_t z : {y.x, y.y, y.z, y.w}) {
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int d = (part + 16 * i) * 16 + k * 8;
+                    y[i][k] = real && d < a.head_dim ? __ldg(reinterpret_cast<const uint4 *>(src + d * 2)) : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    for (uint32_t z : {y[i][k].x, y[i][k].y, y[i][k].z, y[i][k].w}) {
                         const float2 f = unpack<IO>(z);
                         top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
                     }
-                }
 #pragma unroll
             for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
             const int e = top > 0.0f && top < INFINITY ? max(-100, min(100, 7 - ilogbf(top))) : 0;
             const float up = __int_as_float((127 + e) << 23);
             if (part == 0) s_scale[h] = top < INFINITY ? a.scale * __int_as_float((127 - e) << 23) : NAN;     // an infinite query: NaN
-            for (int b = part; b < kCacheMaxLatent / 16; b += 16) {
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i) {
+                const int b = part + 16 * i;
+                if (b >= kCacheMaxLatent / 16) break;
                 uint32_t codes[kTerms][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int d = b * 16 + i * 4;
-                    uint2 y = make_uint2(0, 0);
-                    if (real && d < a.head_dim) y = __ldg(reinterpret_cast<const uint2 *>(src + d * 2));
-                    const float2 f0 = unpack<IO>(y.x), f1 = unpack<IO>(y.y);
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t z0 = k & 1 ? y[i][k >> 1].z : y[i][k >> 1].x, z1 = k & 1 ? y[i][k >> 1].w : y[i][k >> 1].y;
+                    const float2 f0 = unpack<IO>(z0), f1 = unpack<IO>(z1);
                     float v[4] = {f0.x * up, f0.y * up, f1.x * up, f1.y * up};
 #pragma unroll
-                    for (int k = 0; k < kTerms; ++k) {
+                    for (int n = 0; n < kTerms; ++n) {
                         const uint32_t lo = take_codes(v[0], v[1]);
-                        codes[k][i] = lo | take_codes(v[2], v[3]) << 16;
+                        codes[n][k] = lo | take_codes(v[2], v[3]) << 16;
                     }
                 }
 #pragma unroll
-                for (int k = 0; k < kTerms; ++k)                   // blocks of 8 columns x 16 elements
-                    *(uint4 *)(smem + kOffQuery + (b * (kCols / 8) + k * 2 + (h >> 3)) * 128 + (h & 7) * 16) =
-                        make_uint4(codes[k][0], codes[k][1], codes[k][2], codes[k][3]);
+                for (int n = 0; n < kTerms; ++n)                   // blocks of 8 columns x 16 elements
+                    *(uint4 *)(smem + kOffQuery + (b * (kCols / 8) + n * 2 + (h >> 3)) * 128 + (h & 7) * 16) =
+                        make_uint4(codes[n][0], codes[n][1], codes[n][2], codes[n][3]);
             }
             fence_async();
             arrive(&s_queried);

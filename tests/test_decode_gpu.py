@@ -337,6 +337,28 @@ def test_attend_latent_blocks_and_heads(bs, layout, hps):
     check_attend([3, 700, 0, 129], value="e4m3", planes=1, hps=hps, group=16, dim=576, v_dim=512, bs=bs, layout=layout, window=600)
 
 
+@pytest.mark.parametrize("lens", [[1], [127, 128, 129], [640, 0, 64, 300], [5] * 40])
+@pytest.mark.parametrize("bs", [4, 32, 64, 128, 256])
+def test_attend_latent_runs_of_pages(bs, lens):
+    """8-bit latents come in runs of the positions that a page holds in a row; a sequence's ends row by row."""
+    check_attend(lens, value="e4m3", planes=1, hps=1, group=16, dim=576, v_dim=512, bs=bs)
+    check_attend(lens, value="e4m3", planes=1, hps=1, group=16, dim=576, v_dim=512, bs=bs, window=100)
+
+
+@pytest.mark.parametrize("shards,hps,dim,v_dim", [(2, 1, 576, 512), (1, 2, 512, 512), (1, 3, 144, 48)])
+def test_attend_latent_shards_and_heads(shards, hps, dim, v_dim):
+    check_attend([3, 700, 0, 129], value="e4m3", planes=1, shards=shards, hps=hps, group=5, dim=dim, v_dim=v_dim, bs=16)
+
+
+@pytest.mark.parametrize("value", ["bf16", "e4m3"])
+def test_attend_latent_sharp_scores(value):
+    """Maxima that move in many tiles, far apart, and queries of very different sizes."""
+    case = Attend([2000, 300, 1], value=value, planes=1, hps=1, group=16, dim=576, v_dim=512, spread=4.0, scale=0.5)
+    case.q *= torch.logspace(-3, 1, 16)[None, :, None]
+    case.q = case.q.to(case.iodtype)
+    case.check(*case.run())
+
+
 @pytest.mark.parametrize("value", ["bf16", "e4m3"])
 def test_attend_latent_long(value):
     check_attend([30000, 1, 9000], value=value, planes=1, hps=1, group=16, dim=576, v_dim=512, bs=64)
