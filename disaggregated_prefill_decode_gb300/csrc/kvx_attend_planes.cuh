@@ -606,8 +606,9 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
 
 template <class S> static cudaError_t launch(const AttendArgs &a, int32_t sms, cudaStream_t stream) {
     constexpr int bytes = S::WARPS * S::WARP_BYTES;
-    static const cudaError_t set = cudaFuncSetAttribute(kvx_attend_planes<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (set != cudaSuccess) return set;
+    static std::atomic<uint64_t> asked;
+    const cudaError_t e = allow_shared(kvx_attend_planes<S>, bytes, a.device, asked);
+    if (e != cudaSuccess) return e;
     return launch_after(kvx_attend_planes<S>, dim3(sms), S::THREADS, bytes, stream, a);
 }
 

@@ -59,7 +59,12 @@ static void encode_rows(kvx_cache_t c) {
 
 // Scratch of the handle, at its first append or attend.
 static kvx_status ready(kvx_cache_t c, cudaStream_t stream) {
-    if (c->dev) return KVX_OK;
+    if (c->dev) {
+        int dev = 0;
+        const cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+        return dev == c->device ? KVX_OK : fail(KVX_EINVAL, "the cache was first used on device %d, the current one is %d", c->device, dev);
+    }
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     cudaError_t e = cudaStreamIsCapturing(stream, &cap);
     if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
@@ -130,6 +135,10 @@ kvx_status kvx_slot_map(const int32_t *ctx_len, const int32_t *new_len, int32_t 
     if (n_reqs && max_blocks && !block_table) return fail(KVX_EINVAL, "block_table is NULL");
     if (n_free && !free_blocks) return fail(KVX_EINVAL, "free_blocks is NULL");
     if (max_tokens && !slots) return fail(KVX_EINVAL, "slots is NULL");
+    if (((uintptr_t)slots & 7) || ((uintptr_t)tok_off & 7) || ((uintptr_t)result & 7) || ((uintptr_t)positions & 3) ||
+        ((uintptr_t)seq_len & 3) || ((uintptr_t)ctx_len & 3) || ((uintptr_t)new_len & 3) || ((uintptr_t)block_table & 3) ||
+        ((uintptr_t)free_blocks & 3))
+        return fail(KVX_EINVAL, "an array is not on a boundary of its elements");
     if (n_reqs && (seq_len == ctx_len || seq_len == new_len)) return fail(KVX_EINVAL, "seq_len is an input array");
     int32_t device = 0, sms = 0;
     kvx_status st = device_sms(&device, &sms);
@@ -272,6 +281,8 @@ kvx_status kvx_cache_attend(kvx_cache_t c, int32_t layer, const void *q, int64_t
     if (q_stride > ((int64_t)1 << 40) || out_stride > ((int64_t)1 << 40)) return fail(KVX_EINVAL, "stride above 2^40");
     if (!aligned16(q) || !aligned16(out) || (n_reqs > 1 && (q_stride % 8 || out_stride % 8)))
         return fail(KVX_EINVAL, "q and out: pointers and strides must be multiples of 16 bytes");
+    if (((uintptr_t)block_table & 3) || ((uintptr_t)seq_len & 3) || ((uintptr_t)lse & 3))
+        return fail(KVX_EINVAL, "an array is not on a boundary of its elements");
     if (n_reqs == 0) return KVX_OK;
     if ((st = ready(c, stream))) return st;
     if (g.n_planes == 1 && c->outside_device) return fail(KVX_EUNSUPPORTED, "attention over latents outside device memory");
@@ -306,6 +317,7 @@ kvx_status kvx_cache_attend(kvx_cache_t c, int32_t layer, const void *q, int64_t
     a.map_head = hnd ? (uint32_t)g.block_size : 0;
     a.map_col = hnd ? 0 : (uint32_t)g.head_dim;
     a.scratch = c->dev + 256;
+    a.device = c->device;
     const cudaError_t e = launch_attend(a, f.value_type, f.io_type, c->sms, stream);
     return e == cudaSuccess ? KVX_OK : cuda_fail(e, "launching the attention");
 }

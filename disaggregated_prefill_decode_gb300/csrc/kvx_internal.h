@@ -231,6 +231,7 @@ struct AttendArgs {
     int32_t map_rows, map_run;        // rows of the maps, of a run; block, head and element of the first row a KV head's
     uint32_t map_block, map_head, map_col;   // block begins at
     uint8_t *scratch;                 // of the handle: counters (zero between calls), partial results
+    int32_t device;
 };
 constexpr int32_t kScratchCounters = 4096;
 constexpr int32_t kScratchPerSm = 84 << 10;

@@ -557,9 +557,9 @@ cudaError_t launch_latent_join(const AttendArgs &a, int32_t io, int ctas, int32_
 }
 
 template <class S> static cudaError_t launch(const AttendArgs &a, int32_t sms, cudaStream_t stream) {
-    static const cudaError_t set = cudaFuncSetAttribute(kvx_attend_latent<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
-    if (set != cudaSuccess) return set;
-    const cudaError_t e = launch_after(kvx_attend_latent<S>, dim3(2 * sms), kLatentThreads, S::BYTES, stream, a);
+    static std::atomic<uint64_t> asked;
+    cudaError_t e = allow_shared(kvx_attend_latent<S>, S::BYTES, a.device, asked);
+    if (e == cudaSuccess) e = launch_after(kvx_attend_latent<S>, dim3(2 * sms), kLatentThreads, S::BYTES, stream, a);
     return e != cudaSuccess ? e : launch_latent_join(a, S::IO, 2 * sms, sms, stream);
 }
 

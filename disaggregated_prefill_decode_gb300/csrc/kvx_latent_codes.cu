@@ -519,9 +519,9 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
 }
 
 template <int IO> static cudaError_t launch(const AttendArgs &a, int32_t sms, cudaStream_t stream) {
-    static const cudaError_t set = cudaFuncSetAttribute(kvx_attend_latent_codes<IO>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCodeBytes);
-    if (set != cudaSuccess) return set;
-    const cudaError_t e = launch_after(kvx_attend_latent_codes<IO>, dim3(sms), kCodeThreads, kCodeBytes, stream, a, *a.row_maps);
+    static std::atomic<uint64_t> asked;
+    cudaError_t e = allow_shared(kvx_attend_latent_codes<IO>, kCodeBytes, a.device, asked);
+    if (e == cudaSuccess) e = launch_after(kvx_attend_latent_codes<IO>, dim3(sms), kCodeThreads, kCodeBytes, stream, a, *a.row_maps);
     return e != cudaSuccess ? e : launch_latent_join(a, IO, sms, sms, stream);
 }
 

@@ -15,6 +15,15 @@ __device__ __forceinline__ void wait_for_earlier() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// Lets a kernel use `bytes` of dynamic shared memory on `device`, asked for once on each.
+template <class K> static cudaError_t allow_shared(K *kernel, int bytes, int32_t device, std::atomic<uint64_t> &asked) {
+    const uint64_t bit = 1ull << (device & 63);
+    if (asked.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) asked.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
 template <class... P, class... A>
 static cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t shared, cudaStream_t stream, const A &...args) {
     cudaLaunchAttribute attr = {};

@@ -557,14 +557,15 @@ typedef struct kvx_cache_s *kvx_cache_t;
 /*
  * kvx_cache_create -- a typed handle on a pool, for the two calls below. The pool's counts and buffer
  * pointers are copied; its memory stays the caller's. No CUDA call is made here: the first append or
- * attend allocates the handle's scratch (device memory of the current device, a few MiB) and waits for
+ * attend allocates the handle's scratch (device memory of the current device, 13 MiB, or 20 MiB for latents) and waits for
  * it, so make that first call before any stream capture (KVX_EINVAL inside one).
  * Refused: KVX_EINVAL for what contradicts the pool (types and elem_bytes, head counts, v_dim, negative
  * or non-finite values, reserved != 0), KVX_EUNSUPPORTED for more than 64 shards, 2^31 - 1 rows in a
  * buffer or more, head rows (head_dim * elem_bytes, and v_dim * elem_bytes) that are not whole 16-byte
  * vectors, buffers off a 16-byte boundary or of 64 GiB or more, head_dim above 256 (two planes) or 576 (one plane).
- * Calls on one handle use its scratch: their device work must not overlap (one stream, or ordered by
- * events). Handles are independent of one another; several may share a pool.
+ * Calls on one handle use its scratch: one host thread at a time, on the device of the first, and their
+ * device work must not overlap (one stream, or ordered by events). Handles are independent of one
+ * another; several may share a pool.
  */
 kvx_status kvx_cache_create(const kvx_pool *pool, const kvx_cache_config *cfg, kvx_cache_t *out);
 kvx_status kvx_cache_destroy(kvx_cache_t cache);   /* waits for the device; NULL is a no-op */
@@ -588,7 +589,7 @@ kvx_status kvx_cache_append(kvx_cache_t cache, int32_t layer, const void *k, int
  * value are appended first. q: [n_reqs][n_q_heads][head_dim] with q_stride elements from one request to
  * the next, out: [n_reqs][n_q_heads][v_dim] with out_stride, both in io_type, pointers and strides
  * multiples of 16 bytes; lse: [n_reqs][n_q_heads] in 32 bits (the weight with which parts of a cache
- * held in several pools join), or NULL. A request with no positions gets out 0 and lse -inf.
+ * held in several pools join), or NULL; out and lse overlap no input. A request with no positions gets out 0 and lse -inf.
  * seq_len beyond max_blocks * block_size is cut there, a negative one counts as 0, and positions in a
  * block outside the pool are left out; kvx_cache_status reports each of these. KVX_EUNSUPPORTED for
  * latents with v_dim above 512 or outside device memory. Unused slots may hold

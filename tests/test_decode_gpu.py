@@ -400,6 +400,41 @@ def test_attend_leaves_out_what_is_out_of_bounds(planes):
     assert kvx.kvx_cache_status(case.cache) == kvx.KVX_ERANGE
 
 
+@pytest.mark.parametrize("value", ["bf16", "e4m3"])
+def test_attend_latent_many_requests(value):
+    rng = np.random.default_rng(6)
+    check_attend(rng.integers(0, 90, 700).tolist(), value=value, planes=1, hps=1, group=3, dim=576, v_dim=512, bs=16)
+
+
+def pinned(bufs):
+    """The buffers again in pinned host memory, and the tensors that own it."""
+    return [b.cpu().pin_memory() for b in bufs]
+
+
+def test_pool_in_pinned_host_memory():
+    case = Attend([100, 3], dim=64, hps=2, group=2)
+    want = case.run()
+    host = pinned(case.bufs)
+    x = torch.randn((2, 2, 64), device="cuda").to(torch.bfloat16)
+    out = torch.zeros((2, 4 * 64), dtype=torch.bfloat16, device="cuda")
+    with kvx.kvx_cache_create(kvx.Pool(case.geom, host), kvx.KVX_BF16, n_q_heads=4) as c:
+        kvx.kvx_cache_attend(c, 0, case.d_q, 256, case.d_table, case.table.shape[1], case.width, case.d_len, 2, out, 256)
+        slot = int(case.table[1, 0]) * 16 + 5
+        kvx.kvx_cache_append(c, 0, x, 128, x, 128, dev(np.array([slot, -1], np.int64)), 2)
+        assert kvx.kvx_cache_status(c) == kvx.KVX_OK
+    assert torch.equal(out.view(2, 4, 64), want[0])
+    assert all(torch.equal(b.view(torch.bfloat16).view(-1, 2, 64)[slot], x[0].cpu()) for b in host)
+
+
+def test_latents_in_pinned_host_memory_are_refused():
+    case = Attend([100, 3], planes=1, dim=64, hps=1, group=2, v_dim=64)
+    case.run()
+    with kvx.kvx_cache_create(kvx.Pool(case.geom, pinned(case.bufs)), kvx.KVX_BF16, n_q_heads=2) as c:
+        with pytest.raises(kvx.KvxError) as ei:
+            kvx.kvx_cache_attend(c, 0, case.d_q, 128, case.d_table, case.table.shape[1], case.width, case.d_len, 2, case.d_q, 128)
+        assert ei.value.status == kvx.KVX_EUNSUPPORTED
+
+
 @pytest.mark.parametrize("planes", [1, 2])
 def test_attend_strides_streams_and_repeats(planes):
     case = Attend([700, 0, 90, 3000], planes=planes, dim=128, v_dim=128, hps=1, group=8)

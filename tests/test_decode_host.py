@@ -104,7 +104,8 @@ ATTEND = dict(layer=0, q=1 << 20, q_stride=256, block_table=1 << 21, table_strid
 @pytest.mark.parametrize("change", [dict(layer=2), dict(q=None), dict(block_table=None), dict(seq_len=None), dict(out=None),
                                     dict(n_reqs=-1), dict(n_reqs=(1 << 24) + 1), dict(max_blocks=5), dict(max_blocks=-1),
                                     dict(q_stride=255), dict(out_stride=248), dict(q_stride=260), dict(q=(1 << 20) + 8),
-                                    dict(out=(1 << 23) + 4), dict(out_stride=1 << 41)])
+                                    dict(out=(1 << 23) + 4), dict(out_stride=1 << 41), dict(seq_len=(1 << 22) + 2),
+                                    dict(lse=(1 << 24) + 2)])
 def test_attend_refusals(change):
     with kvx.kvx_cache_create(pool(GEOM), value_type=kvx.KVX_BF16, n_q_heads=4) as c:
         refused(kvx.kvx_cache_attend, kvx.KVX_EINVAL, c, **dict(ATTEND, **change))
@@ -125,6 +126,8 @@ SLOTS = dict(ctx_len=1 << 20, new_len=1 << 21, n_reqs=3, block_size=16, free_blo
                                     dict(max_blocks=9), dict(max_blocks=-1), dict(max_tokens=-1), dict(max_tokens=1 << 41),
                                     dict(ctx_len=None), dict(new_len=None), dict(seq_len=None), dict(tok_off=None),
                                     dict(result=None), dict(slots=None), dict(block_table=None), dict(free_blocks=None),
-                                    dict(seq_len=1 << 20), dict(seq_len=1 << 21)])
+                                    dict(seq_len=1 << 20), dict(seq_len=1 << 21), dict(slots=(1 << 25) + 4),
+                                    dict(positions=2), dict(tok_off=(1 << 24) + 4), dict(result=(1 << 27) + 1),
+                                    dict(block_table=(1 << 23) + 2)])
 def test_slot_map_refusals(change):
     refused(kvx.kvx_slot_map, kvx.KVX_EINVAL, **dict(SLOTS, **change))
