@@ -62,7 +62,9 @@ __device__ __forceinline__ int warp_last_at_most(const int64_t *off, int n, int6
     return lo + 31 - __clz(__ballot_sync(~0u, lane < step && lo + lane < n && off[min(lo + lane, n - 1)] <= x));
 }
 
-__device__ __forceinline__ uint32_t blocks_of(uint32_t tokens, uint32_t bs) { return tokens ? (tokens - 1) / bs + 1 : 0; }
+__device__ __forceinline__ uint32_t blocks_of(const SlotArgs &a, uint32_t tokens) {
+    return tokens ? ((__umulhi(tokens - 1, a.block_mul) + tokens - 1) >> a.block_shift) + 1 : 0;
+}
 
 // First tile at or after `lo` that is number `mine` of `of`.
 __device__ __forceinline__ int64_t first_tile(int64_t lo, int64_t mine, int64_t of) { return lo + (mine - lo % of + of) % of; }
@@ -80,18 +82,24 @@ __global__ void __launch_bounds__(kSlotThreads) kvx_slot_map_kernel(const SlotAr
         const int m = min(kReqs, a.n_reqs - r0);
         const int per = (m + kSlotThreads - 1) / kSlotThreads;
         const int i0 = min(m, (int)threadIdx.x * per), i1 = min(m, i0 + per);
+        int32_t c[kReqs / kSlotThreads], w[kReqs / kSlotThreads];
+#pragma unroll
+        for (int k = 0; k < kReqs / kSlotThreads; ++k) {
+            c[k] = i0 + k < i1 ? a.ctx_len[r0 + i0 + k] : 0;
+            w[k] = i0 + k < i1 ? a.new_len[r0 + i0 + k] : 0;
+        }
         Sums mine = {0, 0};
-        for (int i = i0; i < i1; ++i) {
-            const int32_t c = a.ctx_len[r0 + i], w = a.new_len[r0 + i];
-            const int64_t ctx = max(c, 0), end = min(ctx + max(w, 0), inf);
-            const uint32_t had = blocks_of((uint32_t)ctx, bs), need = blocks_of((uint32_t)end, bs);
-            const uint32_t top = (uint32_t)a.max_blocks;
-            bad |= c < 0 || w < 0 || ctx + w > inf || need > top;
-            s_ctx[i] = (int32_t)ctx;
-            s_had[i] = (int32_t)min(had, top);
-            s_tok[i] = end - ctx;                        // turned into sums below
-            s_blk[i] = min(need, top) - min(had, top);
-            mine = mine + Sums{s_tok[i], s_blk[i]};
+#pragma unroll
+        for (int k = 0; k < kReqs / kSlotThreads; ++k) {
+            if (i0 + k >= i1) break;
+            const int64_t ctx = max(c[k], 0), end = min(ctx + max(w[k], 0), inf);
+            const uint32_t had = blocks_of(a, (uint32_t)ctx), need = blocks_of(a, (uint32_t)end), top = (uint32_t)a.max_blocks;
+            bad |= c[k] < 0 || w[k] < 0 || ctx + w[k] > inf || need > top;
+            s_ctx[i0 + k] = (int32_t)ctx;
+            s_had[i0 + k] = (int32_t)min(had, top);
+            s_tok[i0 + k] = end - ctx;                   // turned into sums below
+            s_blk[i0 + k] = min(need, top) - min(had, top);
+            mine = mine + Sums{s_tok[i0 + k], s_blk[i0 + k]};
         }
         Sums total;
         Sums at = cta_exclusive(mine, &total);
