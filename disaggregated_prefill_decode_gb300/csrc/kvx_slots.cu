@@ -133,6 +133,33 @@ __global__ void __launch_bounds__(kSlotThreads) kvx_slot_map_kernel(const SlotAr
              tile * kTokTile < t_end; tile += warps) {
             const int64_t first = tile * kTokTile, from = max(first, base.tok), upto = min(first + kTokTile, t_end);
             const int r_lo = warp_last_at_most(s_tok, m, from - base.tok), r_hi = warp_last_at_most(s_tok, m, upto - 1 - base.tok);
+            if (pairs && r_lo == r_hi && from == first && upto == first + kTokTile) {
+                // all of one request, as nearly all tiles of a long prompt: 32 bits, and a third of the instructions
+                const int32_t p0 = s_ctx[r_lo] + (int32_t)(from - base.tok - s_tok[r_lo]) + 2 * lane, had = s_had[r_lo];
+                const int64_t b0 = base.blk + s_blk[r_lo];         // of the free list: the request's first new block
+                const int32_t end = (int32_t)min((int64_t)a.max_blocks, had + max(a.n_free - b0, (int64_t)0));      // of the blocks it gets
+                const int32_t *const old = a.block_table + (r0 + r_lo) * a.table_stride, *const fresh = a.free_blocks + (b0 - had);
+                auto block = [&](int32_t col) { return col >= end ? -1 : col < had ? old[col] : fresh[col]; };
+                int32_t blk[kTokRounds], next[kTokRounds], rest[kTokRounds];
+#pragma unroll
+                for (int u = 0; u < kTokRounds; ++u) {
+                    const uint32_t p = (uint32_t)(p0 + 64 * u), col = (__umulhi(p, a.block_mul) + p) >> a.block_shift;
+                    rest[u] = (int32_t)(p - col * bs);
+                    blk[u] = block((int32_t)col);
+                    next[u] = rest[u] + 1 == (int32_t)bs ? block((int32_t)col + 1) : blk[u];
+                }
+                longlong2 *const slots = reinterpret_cast<longlong2 *>(a.slots + first) + lane;
+#pragma unroll
+                for (int u = 0; u < kTokRounds; ++u)
+                    slots[32 * u] = make_longlong2(blk[u] < 0 ? -1 : (int64_t)blk[u] * a.block_size + rest[u],
+                                                   next[u] < 0 ? -1 : (int64_t)next[u] * a.block_size + (rest[u] + 1 == (int32_t)bs ? 0 : rest[u] + 1));
+                if (a.positions) {
+                    int2 *const positions = reinterpret_cast<int2 *>(a.positions + first) + lane;
+#pragma unroll
+                    for (int u = 0; u < kTokRounds; ++u) positions[32 * u] = make_int2(p0 + 64 * u, p0 + 64 * u + 1);
+                }
+                continue;
+            }
             int32_t blk[kTokRounds][2], rest[kTokRounds][2], pos[kTokRounds][2];
 #pragma unroll
             for (int u = 0; u < kTokRounds; ++u) {
