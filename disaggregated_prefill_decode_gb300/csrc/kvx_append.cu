@@ -4,7 +4,9 @@
 // A thread keeps one column (plane, head, 8 elements, or 16 that become codes) and walks tokens, so shard,
 // head and element offsets are computed once; only the slot changes. Reads and writes are 16 bytes a thread,
 // and a CTA has as many rows of columns as make whole warps. Bound by memory: each value is read and written
-// once.
+// once. Measured on GB300: 8192 tokens of 8 heads of 128, both planes (67 MB) 11.7 us, 5.8 TB/s; 50001 latents
+// of 576 to 8 bits (87 MB) 14.8 us, 5.9 TB/s (8-byte stores and ragged warps 17.1). With few tokens a thread
+// takes one token instead of four, so that the GPU fills: 16 tokens 4.0 us, the host's time for a call.
 #include "kvx_launch.cuh"
 
 #include <cuda_bf16.h>

@@ -1,17 +1,27 @@
 // kvx_cache_attend over separate key and value planes: the kernel, instantiated per value type in
-// kvx_attend_*.cu (latents: kvx_latent.cu).
+// kvx_attend_*.cu (latents: kvx_latent.cu, kvx_latent_codes.cu).
 //
 // The softmax runs once over the positions with a running maximum m and sum l per query:
 //   m' = max(m, s), l' = l 2^(m - m') + 2^(s - m'), O' = O 2^(m - m') + 2^(s - m') v,
-// scores in units of log2. Bound by memory: each key and value is used by the queries of one KV head
-// only, 2 group flops per element, so all that counts is bytes in flight.
+// scores in units of log2, all of it in 32 bits. Bound by memory: each key and value is used by the queries
+// of one KV head only, 2 group flops per element, so all that counts is bytes in flight and what a call
+// costs before its first and after its last byte.
 //
 // A warp works alone on its stretch of tiles, with a ring of tiles (keys and values of 16 or 32 positions)
 // in shared memory that asynchronous copies fill. S^T = K Q^T takes 16 bytes of a key row as the k
 // elements that a lane gives to the products (the queries are loaded in the same order of elements), and
 // O^T = V^T P^T takes the bytes of two neighbouring positions interleaved, so every lane reads the ring in
 // pieces of 16 bytes and the pieces are swizzled for that alone. Both products have the 8 queries as their
-// narrow side, so a group of up to 8 query heads wastes nothing that the memory would wait for.
+// narrow side, so a group of up to 8 query heads wastes nothing that the memory would wait for, and the
+// warp products (mma.sync) are at 12 % of their rate: the tensor pipe of a whole CTA would have 8 of 128
+// rows to do.
+//
+// What it measured on GB300 (8 KV heads of 128, 8 queries each, bf16): 256 requests of 4608 positions 745
+// us, 6.5 TB/s, 0.96 of the copy rate; 16 requests of 1024 to 8192 57.4 us, of which 45 are the stream at
+// 0.99 of it. Steps on the way: keys and values straight from global memory into registers 125 us (128
+// registers a thread were too few: spills); through rings that each lane filled for itself, 64 bytes of a
+// row an instruction, 75 (256 requests: 953); whole 128-byte lines and this swizzle 61 (745): the requests
+// of half lines had been the limit. 8, 12 and 16 warps a CTA are alike in time; 8 have room for the rings.
 #pragma once
 
 #include "kvx_attend.cuh"
@@ -19,7 +29,9 @@
 namespace kvx {
 
 constexpr int kSharedBytes = 226 << 10;       // of a CTA, one per SM
-constexpr int kSwitchTiles = 2;               // what the change to another segment costs a warp, in tiles: outputs, then queries
+// What the change to another segment costs a warp, in tiles: outputs, then queries. 200 requests with a window of 1024: 47.8 us
+// with 0, 42.1 with 1, 41.6 with 2; long segments the same with all three.
+constexpr int kSwitchTiles = 2;
 
 template <int VT_, int IO_, int D_, int NT_, bool FULL_> struct Shape {
     static constexpr int VT = VT_, IO = IO_, D = D_, NT = NT_;   // D: head_dim rounded up; NT: query sets of 8

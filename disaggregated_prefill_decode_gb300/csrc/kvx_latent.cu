@@ -1,17 +1,24 @@
 // kvx_cache_attend over one plane of latents: keys of head_dim elements whose first v_dim are the values,
-// all of a KV head's query heads (16 at a time) on the same rows.
+// all of a KV head's query heads (16 at a time) on the same rows. Here 16-bit latents, and 8-bit ones that
+// the tensor maps of kvx_latent_codes.cu cannot describe (several shards, heads with a gap); and the kernel
+// that joins the parts of both.
 //
-// Per position 2 (head_dim + v_dim) flops for each query head meet head_dim bytes (or twice that): with 16
-// query heads and 8-bit latents of 576 that is 60 flops a byte, more than the shared work of one warp can
-// feed, and the output of 16 x 512 sums does not fit one warp's registers. So the 8 warps of a CTA take a
-// tile of 64 (32) positions together:
+// Per position 2 (head_dim + v_dim) flops for each query head meet 2 head_dim bytes: 30 flops a byte with 16
+// query heads, more than the shared work of one warp can feed, and the output of 16 x 512 sums does not fit
+// one warp's registers. So the 8 warps of a CTA take a tile of 32 positions (64 of 8 bits) together:
 //   scores   S^T = K Q^T: a warp takes half of the positions and a quarter of the elements, with its part
 //            of the queries in registers; the quarters are summed through shared memory;
 //   softmax  a warp takes two query heads; running maximum and sum stay in its registers;
 //   values   O^T += V^T P^T: a warp takes 64 of the 512 elements, all positions.
-// Rows come by bulk copies, two tiles deep. A row's pitch of 608 (1184) bytes, 96 (32) beyond a multiple of
+// Rows come by bulk copies, two tiles deep, a warp's share each (one warp for all of them was late at every
+// barrier: 293 us where this takes 212). A row's pitch of 1184 (608) bytes, 32 (96) beyond a multiple of
 // 128, keeps both kinds of reads off each other's banks: rows t = 0..3 of the values' reads fall on the four
 // quarters of the banks, and the keys' reads take rows two apart. Two CTAs per SM fill each other's waits.
+//
+// Measured with 16 query heads: 64 requests of 8000 bf16 latents of 576 144 us, 4.1 TB/s; 64 sessions of
+// 2048 to 32768 8-bit ones 212 us, where the tcgen05 kernel takes 122. Bound by instruction issue (1.9 a
+// clock, 95 warp instructions a position). Scores by 8-bit warp products (mma.sync e4m3, queries as two
+// codes) were exact enough but took 395 us: the form costs ten instructions on sm_103a.
 #include "kvx_latent.cuh"
 
 namespace kvx {

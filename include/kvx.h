@@ -10,13 +10,13 @@
  *
  * Conventions shared by every call:
  *  - Device memory (pools, token and id arrays given as device pointers) belongs to the caller.
- *    kvx allocates device memory only for plan descriptors, hash tables and the scratch of
- *    kvx_match_prefix / kvx_block_hashes, and frees it in kvx_plan_destroy / kvx_table_destroy or
- *    before the call returns.
+ *    kvx allocates device memory only for plan descriptors, hash tables, the scratch of caches and that
+ *    of kvx_match_prefix / kvx_block_hashes, and frees it in kvx_plan_destroy / kvx_table_destroy /
+ *    kvx_cache_destroy or before the call returns.
  *  - Host arrays passed in are copied before the call returns; the caller may reuse them.
  *  - Every call returns a kvx_status. On error a one-line reason is stored in a thread-local
  *    buffer (kvx_last_error); no call aborts the process or traps on the device.
- *  - A plan or table is used by one host thread at a time. Different plans are independent.
+ *  - A plan, table or cache is used by one host thread at a time. Different ones are independent.
  *  - Device work runs on the stream the caller passes (plus a library-owned non-blocking stream
  *    for small status read-backs).
  *  - The library keeps per-device state for the life of the process: its push lanes (streams), a
