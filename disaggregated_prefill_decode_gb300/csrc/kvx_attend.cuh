@@ -173,13 +173,17 @@ template <int TOK, int WARPS, int MIN, int EXTRA> struct Batch {
         int64_t total = 0;
         per = (a.n_reqs + 31) / 32;
         if (per <= PER) {
-            int64_t mine = 0;
+            tiles[0] = lane * per < a.n_reqs ? Span<TOK>(a, lane * per).tiles + EXTRA : 0;
+            int64_t mine = tiles[0];
 #pragma unroll
-            for (int k = 0; k < PER; ++k) {
-                const int32_t r = lane * per + k;
-                tiles[k] = k < per && r < a.n_reqs ? Span<TOK>(a, r).tiles + EXTRA : 0;
-                mine += tiles[k];
-            }
+            for (int k = 1; k < PER; ++k) tiles[k] = 0;
+            if (per > 1)                   // else there are 32 requests at most, and a small call is spared the rest
+#pragma unroll
+                for (int k = 1; k < PER; ++k) {
+                    const int32_t r = lane * per + k;
+                    if (k < per && r < a.n_reqs) tiles[k] = Span<TOK>(a, r).tiles + EXTRA;
+                    mine += tiles[k];
+                }
             upto = warp_inclusive(mine);
             total = __shfl_sync(~0u, upto, 31);
         } else {

@@ -17,7 +17,7 @@
 // rows to do.
 //
 // What it measured on GB300 (8 KV heads of 128, 8 queries each, bf16): 256 requests of 4608 positions 745
-// us, 6.5 TB/s, 0.96 of the copy rate; 16 requests of 1024 to 8192 57.4 us, of which 45 are the stream at
+// us, 6.5 TB/s, 0.96 of the copy rate; 16 requests of 1024 to 8192 57.0 us, of which 45 are the stream at
 // 0.99 of it. Steps on the way: keys and values straight from global memory into registers 125 us (128
 // registers a thread were too few: spills); through rings that each lane filled for itself, 64 bytes of a
 // row an instruction, 75 (256 requests: 953); whole 128-byte lines and this swizzle 61 (745): the requests
@@ -242,7 +242,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
     extern __shared__ __align__(16) uint8_t smem[];                // [warp] ring and partial result
     __shared__ int64_t s_seg[S::WARPS][2];                     // first tile of each one's segment; -1: none
     __shared__ int32_t s_where[S::WARPS][2][3];                // request, segment of the request, tiles
-    __shared__ bool s_last[2];
+    __shared__ int32_t s_pieces[2], s_from[2];                 // of the open segments that this CTA has to join, and the first CTA
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int32_t group = a.n_q_heads / a.n_kv_heads, sets = (group + 8 * NT - 1) / (8 * NT), segs = a.n_kv_heads * sets;
 
@@ -402,13 +402,14 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
             rows[n] = kNoRow;
             if (far_x < x1) {
                 const Row<TOK, Line> row(a, far);
-                if (n == 0) load_q(cur);
-                else if (far.tile == 0) pointers(far);
+                if (n == 0 && !S::F8) load_q(cur);                 // 8-bit caches' queries are waited for, so after the copies
+                else if (n && far.tile == 0) pointers(far);
                 rows[n] = row.offset(a, far.seg == 0);
                 load_tile(rows[n], ring + n * S::STAGE);
                 far.next(a, segs, far_x);
             } else copies_commit();
         }
+        if (S::F8 && x0 < x1) load_q(cur);
         int64_t from = x0;
         int stage = 0, free_stage = AHEAD;
         for (int64_t x = x0; x < x1;) {
@@ -585,25 +586,26 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
     if (open[0] < 0 && open[1] < 0) return;
     __syncthreads();
     if (threadIdx.x < 2) {
-        __threadfence();
         const int i = open[threadIdx.x];
-        s_last[threadIdx.x] = false;
+        s_pieces[threadIdx.x] = 0;
         if (i >= 0) {
             const int64_t seg = s_seg[i >> 1][i & 1];
             const int32_t from = split.cta_of(seg), upto = split.cta_of(seg + s_where[i >> 1][i & 1][2] - 1);
-            const bool last = atomicAdd(arrived + from, 1u) == (uint32_t)(upto - from);
-            if (last) arrived[from] = 0;                           // for the next call
-            s_last[threadIdx.x] = last;
-            __threadfence();
+            // releases what the CTA's threads wrote before the barrier, acquires what the other CTAs' did
+            uint32_t before;
+            asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(arrived + from) : "memory");
+            if (before == (uint32_t)(upto - from)) {
+                arrived[from] = 0;                                 // for the next call
+                s_pieces[threadIdx.x] = upto - from + 1;
+                s_from[threadIdx.x] = from;
+            }
         }
     }
     __syncthreads();
     for (int k = 0; k < 2; ++k) {
-        if (!s_last[k]) continue;
-        const int i = open[k];
-        const int64_t seg = s_seg[i >> 1][i & 1];
-        const int32_t *where = s_where[i >> 1][i & 1];
-        const int32_t from = split.cta_of(seg), n = split.cta_of(seg + where[2] - 1) - from + 1;
+        const int n = s_pieces[k];
+        if (!n) continue;
+        const int32_t *where = s_where[open[k] >> 1][open[k] & 1], from = s_from[k];
         int32_t head0;
         const int32_t heads = heads_of(where[1], &head0);
         const Pieces pieces = {cta_parts + (size_t)(2 * from + 1) * S::PARTIAL, cta_parts + (size_t)(2 * from) * S::PARTIAL, 2 * S::PARTIAL, n};
