@@ -1,5 +1,5 @@
 // kvx_cache_attend over separate key and value planes: the kernel, instantiated per value type in
-// kvx_attend_*.cu (latents: kvx_latent.cu, kvx_latent_codes.cu).
+// kvx_attend_*.cu (latents: kvx_latent.cu, kvx_latent_tensor.cu).
 //
 // The softmax runs once over the positions with a running maximum m and sum l per query:
 //   m' = max(m, s), l' = l 2^(m - m') + 2^(s - m'), O' = O 2^(m - m') + 2^(s - m') v,

@@ -34,17 +34,17 @@ static kvx_status device_sms(int32_t *device, int32_t *sms) {
     return KVX_OK;
 }
 
-// Maps of the rows of 8-bit latents for kvx_latent_codes.cu, where it can take them: one shard, in device memory, and rows that
+// Maps of the rows of latents for kvx_latent_tensor.cu, where it can take them: one shard, in device memory, and rows that
 // end with a head or heads of exactly the elements that it reads, since what lies beyond has to read as zero.
 static void encode_rows(kvx_cache_t c) {
     const Geom &g = c->g;
     const bool hnd = g.layout == KVX_LAYOUT_HND;
     const int64_t rows = g.n_blocks * g.block_size * (hnd ? g.heads_per_shard : 1);
-    if (g.n_planes != 1 || c->cfg.value_type != KVX_E4M3 || g.n_shards != 1 || c->outside_device || rows < 1 ||
+    if (g.n_planes != 1 || g.n_shards != 1 || c->outside_device || rows < 1 ||
         rows >= std::numeric_limits<int32_t>::max() || (!hnd && g.heads_per_shard > 1 && g.head_dim != kCacheMaxLatent))
         return;
     const int64_t row_bytes = hnd ? g.head_bytes() : g.row_bytes();
-    int32_t run = 128;
+    int32_t run = 128 / g.elem_bytes;
     while (g.block_size % run) run /= 2;
     std::vector<RowMaps> maps(c->base.size());
     for (size_t i = 0; i < maps.size(); ++i)
@@ -315,7 +315,7 @@ kvx_status kvx_cache_attend(kvx_cache_t c, int32_t layer, const void *q, int64_t
     a.map_rows = (int32_t)std::min<int64_t>(g.n_blocks * g.block_size * (hnd ? g.heads_per_shard : 1), std::numeric_limits<int32_t>::max());
     a.map_block = (uint32_t)(g.block_size * (hnd ? g.heads_per_shard : 1));
     a.map_head = hnd ? (uint32_t)g.block_size : 0;
-    a.map_col = hnd ? 0 : (uint32_t)g.head_dim;
+    a.map_col = hnd ? 0 : (uint32_t)g.head_bytes();
     a.scratch = c->dev + 256;
     a.device = c->device;
     const cudaError_t e = launch_attend(a, f.value_type, f.io_type, c->sms, stream);

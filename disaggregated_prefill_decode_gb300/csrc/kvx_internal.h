@@ -206,7 +206,7 @@ struct AppendArgs {
 };
 cudaError_t launch_append(const AppendArgs &a, int32_t value_type, int32_t io_type, int32_t sms, cudaStream_t stream);
 
-// The rows of one buffer of 8-bit latents, in boxes of 128 and 64 bytes: a run of rows that lie in one block wherever they
+// The rows of one buffer of latents, in boxes of 128 and 64 bytes: a run of rows that lie in one block wherever they
 // begin, or single rows for gathers.
 struct RowMaps {
     CUtensorMap run128, run64, row128, row64;
@@ -227,8 +227,8 @@ struct AttendArgs {
     uint32_t block_mul, block_shift;  // position / block_size = (mulhi(position, mul) + position) >> shift, below 2^31
     uint32_t block_pitch16, token_pitch16;   // of the pool, in 16-byte units
     bool latent;                      // one plane
-    const RowMaps *row_maps;          // 8-bit latents (host), or NULL
-    int32_t map_rows, map_run;        // rows of the maps, of a run; block, head and element of the first row a KV head's
+    const RowMaps *row_maps;          // latents (host), or NULL
+    int32_t map_rows, map_run;        // rows of the maps, of a run; block, head and byte of the first row a KV head's
     uint32_t map_block, map_head, map_col;   // block begins at
     uint8_t *scratch;                 // of the handle: counters (zero between calls), partial results
     int32_t device;
@@ -254,8 +254,8 @@ struct kvx_cache_s {
     int32_t device = -1;                       // of the scratch, set by the first append or attend
     int32_t sms = 0;
     bool outside_device = false;               // a buffer is not device memory
-    std::vector<kvx::RowMaps> row_maps;        // 8-bit latents: per buffer, or none (kvx_cache.cpp, encode_rows)
-    int32_t map_run = 0;                       // rows of a run: the common divisor of the block size and 128
+    std::vector<kvx::RowMaps> row_maps;        // latents: per buffer, or none (kvx_cache.cpp, encode_rows)
+    int32_t map_run = 0;                       // rows of a run: the common divisor of the block size and a tile
     uint8_t *dev = nullptr;                    // [256 bytes: skipped][scratch of the attend kernels]
 };
 

@@ -1,7 +1,7 @@
 // kvx_cache_attend over one plane of latents: keys of head_dim elements whose first v_dim are the values,
-// all of a KV head's query heads (16 at a time) on the same rows. Here 16-bit latents, and 8-bit ones that
-// the tensor maps of kvx_latent_codes.cu cannot describe (several shards, heads with a gap); and the kernel
-// that joins the parts of both.
+// all of a KV head's query heads (16 at a time) on the same rows. Here those that the tensor maps of
+// kvx_latent_tensor.cu cannot describe (several shards, heads with a gap); and the kernel that joins the
+// parts of both.
 //
 // Per position 2 (head_dim + v_dim) flops for each query head meet 2 head_dim bytes: 30 flops a byte with 16
 // query heads, more than the shared work of one warp can feed, and the output of 16 x 512 sums does not fit
@@ -15,8 +15,8 @@
 // 128, keeps both kinds of reads off each other's banks: rows t = 0..3 of the values' reads fall on the four
 // quarters of the banks, and the keys' reads take rows two apart. Two CTAs per SM fill each other's waits.
 //
-// Measured with 16 query heads: 64 requests of 8000 bf16 latents of 576 144 us, 4.1 TB/s; 64 sessions of
-// 2048 to 32768 8-bit ones 212 us, where the tcgen05 kernel takes 122. Bound by instruction issue (1.9 a
+// Measured with 16 query heads: 64 requests of 8000 bf16 latents of 576 144 us, 4.1 TB/s, and 64 sessions of
+// 2048 to 32768 8-bit ones 212 us, where the tcgen05 kernel takes 112 and 122. Bound by instruction issue (1.9 a
 // clock, 95 warp instructions a position). Scores by 8-bit warp products (mma.sync e4m3, queries as two
 // codes) were exact enough but took 395 us: the form costs ten instructions on sm_103a.
 #include "kvx_latent.cuh"
@@ -571,7 +571,7 @@ template <class S> static cudaError_t launch(const AttendArgs &a, int32_t sms, c
 }
 
 cudaError_t launch_attend_latent(const AttendArgs &a, int32_t vt, int32_t io, int32_t sms, cudaStream_t stream) {
-    if (vt == KVX_E4M3 && a.row_maps) return launch_latent_codes(a, io, sms, stream);
+    if (a.row_maps) return launch_latent_tensor(a, vt, io, sms, stream);
     if (vt == KVX_BF16) return launch<LatentShape<KVX_BF16, KVX_BF16>>(a, sms, stream);
     if (vt == KVX_F16) return launch<LatentShape<KVX_F16, KVX_F16>>(a, sms, stream);
     return io == KVX_BF16 ? launch<LatentShape<KVX_E4M3, KVX_BF16>>(a, sms, stream) : launch<LatentShape<KVX_E4M3, KVX_F16>>(a, sms, stream);

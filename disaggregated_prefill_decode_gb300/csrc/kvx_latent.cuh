@@ -40,6 +40,6 @@ struct OpenSegment {
 };
 
 cudaError_t launch_latent_join(const AttendArgs &a, int32_t io, int ctas, int32_t sms, cudaStream_t stream);       // kvx_latent.cu
-cudaError_t launch_latent_codes(const AttendArgs &a, int32_t io, int32_t sms, cudaStream_t stream);                // kvx_latent_codes.cu
+cudaError_t launch_latent_tensor(const AttendArgs &a, int32_t vt, int32_t io, int32_t sms, cudaStream_t stream);   // kvx_latent_tensor.cu
 
 }  // namespace kvx

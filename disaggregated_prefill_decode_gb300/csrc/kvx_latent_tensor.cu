@@ -1,6 +1,6 @@
-// kvx_cache_attend over one plane of 8-bit latents, on the tcgen05 tensor pipe.
+// kvx_cache_attend over one plane of latents, on the tcgen05 tensor pipe.
 //
-// The 8-bit codes are multiplied as they are, so nothing of the cache passes through registers: a tile of
+// Of 8-bit latents the codes are multiplied as they are, so nothing of the cache passes through registers: a tile of
 // 128 positions is brought into shared memory by TMA in 128-byte swizzled chunks of 128 elements, and
 // serves twice as operand A: by rows (K-major) for the scores
 // S = K Q^T, 128 positions x 48, and by columns (MN-major) for the sums O^T += V^T P, four times 128
@@ -9,7 +9,10 @@
 // 12 significant bits and more, exact for bf16 queries down to 2^-18 of a query's largest element; so 16
 // query heads make 48 columns. Their sums stand in TMEM apart and are put together in 32 bits.
 //
-// Queries are brought to a largest element in [2^7, 2^8) by a power of two. Weights are taken against a
+// 16-bit latents go the same way in tiles of 64 positions, the same bytes; a query is one column, a weight
+// two 16-bit values whose sum leaves 2^-17 of it, and a chunk is two pieces of 128 bytes a row.
+//
+// Queries of 8-bit latents are brought to a largest element in [2^7, 2^8) by a power of two. Weights are taken against a
 // maximum that moves only when a score passes it by more than 2^kSlack, so that O in TMEM is hardly ever
 // rescaled; times 2^5 they stay within the codes' range.
 //
@@ -24,7 +27,8 @@
 // copied as soon as its sums are done, by a warp of its own, and multiplied as soon as it is there.
 //
 // Measured, 16 query heads: 64 sessions of 2048 to 32768 positions 122 us (644 MB; 1.7 us a tile, 0.97 of the
-// copy rate, while it streams), 128 requests of 8000 115 us, 5.2 TB/s. Steps on the way: four rows a gather
+// copy rate, while it streams), 128 requests of 8000 115 us, 5.2 TB/s; of 8000 bf16 latents 64 requests 112
+// us, 128 207 us, 5.7 TB/s, which warp products (kvx_latent.cu) took 144 and 270 for. Steps on the way: four rows a gather
 // 408 us; boxes of a page's runs 167; chunk by chunk, products from a converged warp instead of one lane's
 // branch (18 products 0.6 us, not 2.5) 153; eight softmax warps 146; a lighter join 140; a copying warp per
 // chunk, and scores and sums from two warps 123. Prefetching the next tiles into L2 cost 8 to 17 us.
@@ -32,36 +36,52 @@
 
 namespace kvx {
 
-constexpr int kTile = 128;                                     // positions
 constexpr int kSoftThreads = 256;                              // warps 0-7: softmax and outputs, half of the query heads each four
-constexpr int kCodeThreads = kSoftThreads + 7 * 32;            // 8, 9: products of the scores, of the sums; 10-14: copies, a chunk each
+constexpr int kTensorThreads = kSoftThreads + 7 * 32;          // 8, 9: products of the scores, of the sums; 10-14: copies, a chunk each
 constexpr int kMine = kLatentHeads / 2;                        // query heads of a softmax thread
-constexpr int kChunk = kTile * 128, kStage = 4 * kChunk + kTile * 64;   // 4 chunks of 128 elements, one of 64
 constexpr int kChunks = 5;                                     // the last one is used up by the scores, the others in their order by the sums
-constexpr int kTerms = 3, kCols = kTerms * kLatentHeads;
-constexpr int kQueryBytes = kCols * kCacheMaxLatent, kWeightBytes = kCols * kTile;
-constexpr int kOffQuery = 2 * kStage, kOffWeight = kOffQuery + kQueryBytes, kCodeBytes = kOffWeight + 2 * kWeightBytes;
 constexpr float kSpacing = 32.0f;
 constexpr float kSlack = 3.0f;                                 // in powers of two
-constexpr float kWeightUp = 32.0f;                             // 2^(kSlack + 5) is within the codes' 448
-constexpr uint32_t kColScores = 0, kColSums = 128, kTmemCols = 512;      // two buffers of scores 64 columns apart, then 4 x 48
-constexpr int kCodeSwitch = 1;                                 // places of the line that a change of segment counts
+constexpr uint32_t kColScores = 0, kColSums = 128, kTmemCols = 512;      // two buffers of scores 64 columns apart, then 4 x S::WCOLS
+constexpr int kSegmentSwitch = 1;                              // places of the line that a change of segment counts
+
+template <int VT_, int IO_> struct TensorShape {
+    static constexpr int VT = VT_, IO = IO_;
+    static constexpr bool F8 = VT == KVX_E4M3;
+    static constexpr int ESZ = F8 ? 1 : 2;
+    static constexpr int TILE = 128 / ESZ;                        // positions
+    static constexpr int SUBS = ESZ;                              // 128-byte pieces of a row in a chunk of 128 elements
+    static constexpr int SUB = TILE * 128, CHUNK = SUBS * SUB;    // the last chunk has 64 elements
+    static constexpr int STAGE = 4 * CHUNK + CHUNK / 2;
+    static constexpr int LAST = F8 ? 64 : 128;                    // bytes of a row in the last chunk
+    static constexpr int QTERMS = F8 ? 3 : 1, WTERMS = F8 ? 3 : 2;   // columns of a query head in the two products
+    static constexpr int QCOLS = QTERMS * kLatentHeads, WCOLS = WTERMS * kLatentHeads;
+    static constexpr int QUERY = QCOLS * kCacheMaxLatent * ESZ, WEIGHT = WCOLS * TILE * ESZ;
+    static constexpr int OFF_QUERY = 2 * STAGE, OFF_WEIGHT = OFF_QUERY + QUERY, BYTES = OFF_WEIGHT + 2 * WEIGHT;
+    static constexpr float UP = F8 ? 32.0f : 1.0f;                // of the weights: 2^(kSlack + 5) is within the codes' 448
+    static constexpr int ROWS = F8 ? 32 : 16;                     // of the scores in a warp's lanes of TMEM: 64 rows leave half free
+    // M x N products with 32-bit sums: both operands by rows, or both by columns; bf16 is type 1, e4m3 and f16 are 0
+    static constexpr uint32_t IDESC = 1u << 4 | (VT == KVX_BF16 ? 1u << 7 | 1u << 10 : 0);
+    static constexpr uint32_t IDESC_ROWS = IDESC | (QCOLS / 8) << 17 | (TILE / 16) << 24;
+    static constexpr uint32_t IDESC_COLS = IDESC | (WCOLS / 8) << 17 | (128 / 16) << 24 | 1u << 15 | 1u << 16;
+};
 
 // Shared memory operands: start, the two strides, swizzle (0 none, 2 of 128 bytes, 4 of 64 bytes).
 __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t leading, uint32_t stride, uint32_t swizzle) {
     return (uint64_t)(addr >> 4 & 0x3fff) | (uint64_t)(leading >> 4) << 16 | (uint64_t)(stride >> 4) << 32 | (uint64_t)1 << 46 |
            (uint64_t)swizzle << 61;
 }
-// 128 x 48 products of e4m3 codes with 32-bit sums; both operands by rows, or both by columns.
-constexpr uint32_t kIdescRows = 1u << 4 | (kCols / 8) << 17 | (kTile / 16) << 24;
-constexpr uint32_t kIdescCols = kIdescRows | 1u << 15 | 1u << 16;
-
 // Issued by one lane of a converged warp, always the same: the operands are uniform then, and 18 products go out in 0.6 us
 // instead of 2.5 from a branch of one lane.
-__device__ __forceinline__ void tensor_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile("{\n.reg .pred p, e;\nsetp.ne.u32 p, %4, 0;\nelect.sync _|e, 0xffffffff;\n"
-                 "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-                 : "memory");
+template <bool F8> __device__ __forceinline__ void tensor_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    if constexpr (F8)
+        asm volatile("{\n.reg .pred p, e;\nsetp.ne.u32 p, %4, 0;\nelect.sync _|e, 0xffffffff;\n"
+                     "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+                     : "memory");
+    else
+        asm volatile("{\n.reg .pred p, e;\nsetp.ne.u32 p, %4, 0;\nelect.sync _|e, 0xffffffff;\n"
+                     "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+                     : "memory");
 }
 __device__ __forceinline__ void tensor_commit(uint64_t *bar) {
     asm volatile("{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
@@ -124,9 +144,11 @@ template <class Op> __device__ __forceinline__ float reduce_heads(float (&v)[kMi
     return op(v[0], __shfl_xor_sync(~0u, v[0], 1));
 }
 
-template <int IO> __global__ void __launch_bounds__(kCodeThreads, 1)
-kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_constant__ RowMaps maps) {
-    using Line = Place<kTile, kCodeSwitch>;
+template <class S> __global__ void __launch_bounds__(kTensorThreads, 1)
+kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_constant__ RowMaps maps) {
+    constexpr int VT = S::VT, IO = S::IO, QTERMS = S::QTERMS, WTERMS = S::WTERMS;
+    constexpr bool F8 = S::F8;
+    using Line = Place<S::TILE, kSegmentSwitch>;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ __align__(8) uint64_t s_full[2][kChunks], s_free[2][kChunks];           // chunk by chunk
     __shared__ __align__(8) uint64_t s_scored[2], s_weighed[2], s_queried, s_drained[2];
@@ -162,7 +184,7 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
     wait_for_earlier();
     OpenSegment *const open = (OpenSegment *)a.scratch;
     uint8_t *const parts = a.scratch + kScratchCounters * sizeof(uint32_t);
-    const Batch<kTile, kCodeThreads / 32, 1, kCodeSwitch> batch(a, segs);
+    const Batch<S::TILE, kTensorThreads / 32, 1, kSegmentSwitch> batch(a, segs);
     const bool works = (int32_t)blockIdx.x < batch.split.ctas;
     const int64_t c_begin = works ? batch.split.begin(blockIdx.x) : 0, c_end = works ? batch.split.begin(blockIdx.x + 1) : 0;
     int64_t x0 = c_begin;
@@ -185,14 +207,14 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
         // nothing, or nothing but the end of a segment
     } else if (w == 8) {                                           // products of the scores, chunk by chunk as they arrive
         const uint32_t smem0 = shared_addr(smem);                  // operands at their start; the rest are constants, in 16 bytes
-        const uint64_t keys = operand(smem0, 16, 1024, 2), keys_last = operand(smem0 + 4 * kChunk, 16, 512, 4);
-        const uint64_t queries = operand(smem0 + kOffQuery, (kCols / 8) * 128, 128, 0);
+        const uint64_t keys = operand(smem0, 16, 1024, 2), keys_last = operand(smem0 + 4 * S::CHUNK, 16, 8 * S::LAST, F8 ? 4 : 2);
+        const uint64_t queries = operand(smem0 + S::OFF_QUERY, (S::QCOLS / 8) * 128, 128, 0);
         Line at = begin;
         int64_t x = x0;
         int switches = 0;
         bool ok = true, first = true;
         for (int j = 0; ok && x < c_end; ++j) {
-            const uint64_t stage = (j & 1) * (kStage / 16);
+            const uint64_t stage = (j & 1) * (S::STAGE / 16);
             const uint32_t d = tmem + kColScores + (j & 1) * 64;
             if (j >= 2) {                                          // the scores before are read
                 ok = __all_sync(~0u, wait(&s_weighed[j & 1], (j - 2) >> 1));
@@ -204,9 +226,9 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
                 const int c = (i + 4) % kChunks;
                 if (!ok || !(ok = __all_sync(~0u, wait(&s_full[j & 1][c], j >> 1)))) break;
 #pragma unroll
-                for (int y = 0; y < (c < 4 ? 4 : 2); ++y)
-                    tensor_mma(d, (c < 4 ? keys + c * (kChunk / 16) : keys_last) + stage + y * 2, queries + (c * 8 + y * 2) * (kCols / 8) * 8, kIdescRows,
-                               i > 0 || y > 0);
+                for (int y = 0; y < (c < 4 ? 4 * S::SUBS : 2 * S::SUBS); ++y)          // 32 bytes of the rows
+                    tensor_mma<F8>(d, (c < 4 ? keys + c * (S::CHUNK / 16) : keys_last) + stage + y / 4 * (S::SUB / 16) + y % 4 * 2,
+                                   queries + (c * 8 * S::SUBS + y * 2) * (S::QCOLS / 8) * 8, S::IDESC_ROWS, i > 0 || y > 0);
                 if (c == 4) tensor_commit(&s_free[j & 1][4]);
             }
             if (ok) tensor_commit(&s_scored[j & 1]);
@@ -219,19 +241,20 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
         }
     } else if (w == 9) {                                           // products of the sums
         const uint32_t smem0 = shared_addr(smem);
-        const uint64_t values = operand(smem0, 16, 1024, 2), weights = operand(smem0 + kOffWeight, 128, kTile * 16, 0);
+        const uint64_t values = operand(smem0, F8 ? 16 : S::SUB, 1024, 2), weights = operand(smem0 + S::OFF_WEIGHT, 128, S::TILE * 16, 0);
         Line at = begin;
         int64_t x = x0;
         bool ok = true, first = true;
         for (int j = 0; x < c_end; ++j) {
             if (!(ok = __all_sync(~0u, wait(&s_weighed[j & 1], j >> 1)))) break;
             tensor_fence_after();
-            const uint64_t v = values + (j & 1) * (kStage / 16), p = weights + (j & 1) * (kWeightBytes / 16);
+            const uint64_t v = values + (j & 1) * (S::STAGE / 16), p = weights + (j & 1) * (S::WEIGHT / 16);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    tensor_mma(tmem + kColSums + c * kCols, v + c * (kChunk / 16) + i * 256, p + i * 32, kIdescCols, !first || i > 0);
+                for (int i = 0; i < 4; ++i)                        // a quarter of the positions
+                    tensor_mma<F8>(tmem + kColSums + c * S::WCOLS, v + c * (S::CHUNK / 16) + i * (S::SUB / 64), p + i * (S::TILE / 4), S::IDESC_COLS,
+                                   !first || i > 0);
                 tensor_commit(&s_free[j & 1][c]);
             }
             at.next(a, segs, x);
@@ -243,7 +266,8 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
         }
     } else if (w < 8) {                                            // softmax and outputs
         // a thread has a position (an element, of the outputs) and 8 query heads
-        const int here = (w & 3) * 32 + lane, h0 = w >> 2 << 3;
+        const int here = (w & 3) * 32 + lane, pos = (w & 3) * S::ROWS + lane, h0 = w >> 2 << 3;
+        const bool scores = lane < S::ROWS;
         const uint32_t lanes = tmem + ((uint32_t)(w & 3) << 21) + h0;          // this warp's 32 rows, its first column
         float m[kMine], l[kMine], scale[kMine];
         // Queries of a segment as codes, and what its scores are to be multiplied by.
@@ -252,49 +276,57 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
             const int32_t kvh = p.seg / sets, in_group = p.seg % sets * kLatentHeads + h;
             const uint8_t *src = a.q + p.r * a.q_stride + ((int64_t)kvh * group + in_group) * a.head_dim * 2;
             const bool real = in_group < group;
-            constexpr int kBlocks = (kCacheMaxLatent / 16 + 15) / 16;  // of 16 elements, for each of a head's 16 threads
-            uint4 y[kBlocks][2];
-            float top = 0.0f;
+            if constexpr (F8) {
+                constexpr int kBlocks = (kCacheMaxLatent / 16 + 15) / 16;  // of 16 elements, for each of a head's 16 threads
+                uint4 y[kBlocks][2];
+                float top = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kBlocks; ++i)
+                for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int d = (part + 16 * i) * 16 + k * 8;
-                    y[i][k] = real && d < a.head_dim ? __ldg(reinterpret_cast<const uint4 *>(src + d * 2)) : make_uint4(0, 0, 0, 0);
-                }
-#pragma unroll
-            for (int i = 0; i < kBlocks; ++i)
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    for (uint32_t z : {y[i][k].x, y[i][k].y, y[i][k].z, y[i][k].w}) {
-                        const float2 f = unpack<IO>(z);
-                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    for (int k = 0; k < 2; ++k) {
+                        const int d = (part + 16 * i) * 16 + k * 8;
+                        y[i][k] = real && d < a.head_dim ? __ldg(reinterpret_cast<const uint4 *>(src + d * 2)) : make_uint4(0, 0, 0, 0);
                     }
 #pragma unroll
-            for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-            const int e = top > 0.0f && top < INFINITY ? max(-100, min(100, 7 - ilogbf(top))) : 0;
-            const float up = __int_as_float((127 + e) << 23);
-            if (part == 0) s_scale[h] = top < INFINITY ? a.scale * __int_as_float((127 - e) << 23) : NAN;     // an infinite query: NaN
+                for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
-            for (int i = 0; i < kBlocks; ++i) {
-                const int b = part + 16 * i;
-                if (b >= kCacheMaxLatent / 16) break;
-                uint32_t codes[kTerms][4];
+                    for (int k = 0; k < 2; ++k)
+                        for (uint32_t z : {y[i][k].x, y[i][k].y, y[i][k].z, y[i][k].w}) {
+                            const float2 f = unpack<IO>(z);
+                            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                        }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t z0 = k & 1 ? y[i][k >> 1].z : y[i][k >> 1].x, z1 = k & 1 ? y[i][k >> 1].w : y[i][k >> 1].y;
-                    const float2 f0 = unpack<IO>(z0), f1 = unpack<IO>(z1);
-                    float v[4] = {f0.x * up, f0.y * up, f1.x * up, f1.y * up};
+                for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+                const int e = top > 0.0f && top < INFINITY ? max(-100, min(100, 7 - ilogbf(top))) : 0;
+                const float up = __int_as_float((127 + e) << 23);
+                if (part == 0) s_scale[h] = top < INFINITY ? a.scale * __int_as_float((127 - e) << 23) : NAN;     // an infinite query: NaN
 #pragma unroll
-                    for (int n = 0; n < kTerms; ++n) {
-                        const uint32_t lo = take_codes(v[0], v[1]);
-                        codes[n][k] = lo | take_codes(v[2], v[3]) << 16;
+                for (int i = 0; i < kBlocks; ++i) {
+                    const int b = part + 16 * i;
+                    if (b >= kCacheMaxLatent / 16) break;
+                    uint32_t codes[QTERMS][4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t z0 = k & 1 ? y[i][k >> 1].z : y[i][k >> 1].x, z1 = k & 1 ? y[i][k >> 1].w : y[i][k >> 1].y;
+                        const float2 f0 = unpack<IO>(z0), f1 = unpack<IO>(z1);
+                        float v[4] = {f0.x * up, f0.y * up, f1.x * up, f1.y * up};
+#pragma unroll
+                        for (int n = 0; n < QTERMS; ++n) {
+                            const uint32_t lo = take_codes(v[0], v[1]);
+                            codes[n][k] = lo | take_codes(v[2], v[3]) << 16;
+                        }
                     }
-                }
 #pragma unroll
-                for (int n = 0; n < kTerms; ++n)                   // blocks of 8 columns x 16 elements
-                    *(uint4 *)(smem + kOffQuery + (b * (kCols / 8) + n * 2 + (h >> 3)) * 128 + (h & 7) * 16) =
-                        make_uint4(codes[n][0], codes[n][1], codes[n][2], codes[n][3]);
+                    for (int n = 0; n < QTERMS; ++n)                   // blocks of 8 columns x 16 elements
+                        *(uint4 *)(smem + S::OFF_QUERY + (b * (S::QCOLS / 8) + n * 2 + (h >> 3)) * 128 + (h & 7) * 16) =
+                            make_uint4(codes[n][0], codes[n][1], codes[n][2], codes[n][3]);
+                }
+            } else {                                               // as they are, in blocks of 8 columns x 8 elements
+                if (part == 0) s_scale[h] = a.scale;
+#pragma unroll
+                for (int b = part; b < kCacheMaxLatent / 8; b += 16)
+                    *(uint4 *)(smem + S::OFF_QUERY + (b * (S::QCOLS / 8) + (h >> 3)) * 128 + (h & 7) * 16) =
+                        real && b * 8 < a.head_dim ? __ldg(reinterpret_cast<const uint4 *>(src + b * 16)) : make_uint4(0, 0, 0, 0);
             }
             fence_async();
             arrive(&s_queried);
@@ -318,14 +350,15 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
             tensor_fence_after();
             float s[kMine];
             {
-                uint32_t y[kTerms][kMine];
+                uint32_t y[QTERMS][kMine];
 #pragma unroll
-                for (int k = 0; k < kTerms; ++k) tmem_load(y[k], lanes + kColScores + (j & 1) * 64 + k * 16);
+                for (int k = 0; k < QTERMS; ++k) tmem_load(y[k], lanes + kColScores + (j & 1) * 64 + k * 16);
                 tmem_load_wait();
-                const bool live = s_live[j % 3][here >> 2] >> (here & 3) & 1;
+                const bool live = scores && s_live[j % 3][pos >> 2] >> (pos & 3) & 1;
 #pragma unroll
                 for (int h = 0; h < kMine; ++h) {
-                    const float z = __uint_as_float(y[0][h]) + (__uint_as_float(y[1][h]) + __uint_as_float(y[2][h]) / kSpacing) / kSpacing;
+                    float z = __uint_as_float(y[0][h]);
+                    if constexpr (F8) z += (__uint_as_float(y[1][h]) + __uint_as_float(y[2][h]) / kSpacing) / kSpacing;
                     s[h] = live ? z * scale[h] : -INFINITY;
                 }
             }
@@ -352,7 +385,7 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
                     wait(&s_free[(j - 1) & 1][3], (j - 1) >> 1);
                     tensor_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < 4 * kTerms; ++c) {
+                    for (int c = 0; c < 4 * WTERMS; ++c) {
                         uint32_t y[kMine];
                         tmem_load(y, lanes + kColSums + c * 16);
                         tmem_load_wait();
@@ -363,7 +396,7 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
                     tmem_store_wait();
                 }
             }
-            uint32_t codes[kTerms][2];
+            uint32_t parts_of[WTERMS][2 * S::ESZ];                 // 8 heads' weights, term by term
 #pragma unroll
             for (int h = 0; h < kMine; h += 4) {
                 float v[4];
@@ -371,18 +404,31 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
                 for (int i = 0; i < 4; ++i) {
                     v[i] = fast_exp2(s[h + i] - (m[h + i] == -INFINITY ? 0.0f : m[h + i]));
                     l[h + i] += v[i];
-                    v[i] *= kWeightUp;
+                    v[i] *= S::UP;
                 }
+                if constexpr (F8) {
 #pragma unroll
-                for (int k = 0; k < kTerms; ++k) {
-                    const uint32_t lo = take_codes(v[0], v[1]);
-                    codes[k][h / 4] = lo | take_codes(v[2], v[3]) << 16;
+                    for (int k = 0; k < WTERMS; ++k) {
+                        const uint32_t lo = take_codes(v[0], v[1]);
+                        parts_of[k][h / 4] = lo | take_codes(v[2], v[3]) << 16;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; i += 2) {
+                        const uint32_t top = pack<VT>(v[i], v[i + 1]);
+                        const float2 f = unpack<VT>(top);
+                        parts_of[0][(h + i) / 2] = top;
+                        parts_of[1][(h + i) / 2] = pack<VT>(v[i] - f.x, v[i + 1] - f.y);
+                    }
                 }
             }
             if (j >= 2) wait(&s_free[j & 1][3], (j - 2) >> 1);
+            uint8_t *const weights = smem + S::OFF_WEIGHT + (j & 1) * S::WEIGHT + pos * 16;
 #pragma unroll
-            for (int k = 0; k < kTerms; ++k)                       // blocks of 16 columns x 8 positions
-                *(uint2 *)(smem + kOffWeight + (j & 1) * kWeightBytes + k * kTile * 16 + here * 16 + h0) = make_uint2(codes[k][0], codes[k][1]);
+            for (int k = 0; k < WTERMS; ++k)                       // blocks of 16 bytes of columns x 8 positions
+                if constexpr (F8) *(uint2 *)(weights + k * S::TILE * 16 + h0) = make_uint2(parts_of[k][0], parts_of[k][1]);
+                else if (scores)
+                    *(uint4 *)(weights + (k * 2 + (h0 >> 3)) * S::TILE * 16) = make_uint4(parts_of[k][0], parts_of[k][1], parts_of[k][2], parts_of[k][3]);
             fence_async();
             tensor_fence_before();
             arrive(&s_weighed[j & 1]);
@@ -415,14 +461,16 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
             uint8_t *const part = parts + (size_t)(blockIdx.x * 2 + begun) * kLatentPartial;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
-                uint32_t y[kTerms][kMine];
+                uint32_t y[WTERMS][kMine];
 #pragma unroll
-                for (int k = 0; k < kTerms; ++k) tmem_load(y[k], lanes + kColSums + c * kCols + k * 16);
+                for (int k = 0; k < WTERMS; ++k) tmem_load(y[k], lanes + kColSums + c * S::WCOLS + k * 16);
                 tmem_load_wait();
                 const int d = c * 128 + here;
 #pragma unroll
                 for (int h = 0; h < kMine; ++h) {
-                    const float z = (__uint_as_float(y[0][h]) + (__uint_as_float(y[1][h]) + __uint_as_float(y[2][h]) / kSpacing) / kSpacing) / kWeightUp;
+                    float z = __uint_as_float(y[1][h]);
+                    if constexpr (F8) z = (z + __uint_as_float(y[2][h]) / kSpacing) / kSpacing;
+                    z = (z + __uint_as_float(y[0][h])) / S::UP;
                     if (!whole) __stcg((float *)part + partial_at(d, h0 + h), z);
                     else if (h0 + h < heads && d < a.v_dim)
                         ((uint16_t *)(a.out + at.r * a.out_stride))[(int64_t)(head0 + h0 + h) * a.v_dim + d] =
@@ -458,7 +506,7 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
         auto look_up = [&](const Line &at) {
             Rows o;
             const int32_t kvh = at.seg / sets;
-            const uint32_t first = (uint32_t)at.first, len = (uint32_t)at.len, tile0 = first / kTile * kTile + (uint32_t)at.tile * kTile;
+            const uint32_t first = (uint32_t)at.first, len = (uint32_t)at.len, tile0 = first / S::TILE * S::TILE + (uint32_t)at.tile * S::TILE;
             auto row_of = [&](uint32_t pos) {
                 if (pos < first || pos >= len) return nothing;
                 const uint32_t col = (__umulhi(pos, a.block_mul) + pos) >> a.block_shift, slot = pos - col * (uint32_t)a.pool.block_size;
@@ -472,8 +520,8 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
             auto whole = [&](uint32_t pos) { return run >= 4 && (pos + run <= first || pos >= len || (pos >= first && pos + run <= len)); };
             const uint32_t run0 = tile0 + lane * run, four0 = tile0 + 4 * lane, my_run = 4 * lane / run;
             o.col0 = (uint32_t)kvh * a.map_col;
-            o.boxed = lane * run < kTile && whole(run0);
-            o.gathered = !whole(tile0 + my_run * run);
+            o.boxed = lane * run < S::TILE && whole(run0);
+            o.gathered = lane * 4 < S::TILE && !whole(tile0 + my_run * run);
             o.row = o.boxed ? row_of(run0) : nothing;
             o.live = __shfl_sync(~0u, o.row, my_run) != nothing ? 15 : 0;
             if (o.gathered) {
@@ -486,8 +534,9 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
             }
             return o;
         };
-        const CUtensorMap *const run_map = c < 4 ? &maps.run128 : &maps.run64, *const row_map = c < 4 ? &maps.row128 : &maps.row64;
-        const uint32_t wide = c < 4 ? 128 : 64, bytes = wide * kTile;
+        const bool narrow = F8 && c == 4;
+        const CUtensorMap *const run_map = narrow ? &maps.run64 : &maps.run128, *const row_map = narrow ? &maps.row64 : &maps.row128;
+        const uint32_t wide = narrow ? 64 : 128, subs = c < 4 ? S::SUBS : 1, bytes = wide * subs * S::TILE;
         Line at = begin;
         int64_t x = x0;
         int issued = 0;
@@ -495,23 +544,28 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
         for (; x < c_end; ++issued) {
             const int j = issued;
             if (!__all_sync(~0u, j < 2 || wait(&s_free[j & 1][c], (j - 2) >> 1))) break;
-            const uint32_t bar = shared_addr(&s_full[j & 1][c]), to = shared_addr(smem + (j & 1) * kStage + c * kChunk);
+            const uint32_t bar = shared_addr(&s_full[j & 1][c]), chunk = shared_addr(smem + (j & 1) * S::STAGE + c * S::CHUNK);
             if (c == 0) {
                 s_live[j % 3][lane] = (uint8_t)rows.live;          // tile j - 3 is through, its chunks were free
                 __syncwarp();
             }
             if (lane == 0)                                         // a copy of another lane may count before: the phase waits for this
                 asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-            if (rows.boxed)
-                asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-                                 to + lane * run * wide),
-                             "l"(run_map), "r"(rows.col0 + c * 128), "r"(rows.row), "r"(bar)
-                             : "memory");
-            if (rows.gathered)
-                asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
-                             ::"r"(to + lane * 4 * wide), "l"(row_map), "r"(rows.col0 + c * 128), "r"(rows.y[0]), "r"(rows.y[1]), "r"(rows.y[2]),
-                             "r"(rows.y[3]), "r"(bar)
-                             : "memory");
+#pragma unroll
+            for (int i = 0; i < S::SUBS; ++i) {
+                if (i >= subs) break;
+                const uint32_t to = chunk + i * S::SUB, col = rows.col0 + (c * S::SUBS + i) * 128;
+                if (rows.boxed)
+                    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                                     to + lane * run * wide),
+                                 "l"(run_map), "r"(col), "r"(rows.row), "r"(bar)
+                                 : "memory");
+                if (rows.gathered)
+                    asm volatile(
+                        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+                        ::"r"(to + lane * 4 * wide), "l"(row_map), "r"(col), "r"(rows.y[0]), "r"(rows.y[1]), "r"(rows.y[2]), "r"(rows.y[3]), "r"(bar)
+                        : "memory");
+            }
             at.next(a, segs, x);
             if (x < c_end) rows = look_up(at);                     // while this one is under way
         }
@@ -527,15 +581,17 @@ kvx_attend_latent_codes(const __grid_constant__ AttendArgs a, const __grid_const
     }
 }
 
-template <int IO> static cudaError_t launch(const AttendArgs &a, int32_t sms, cudaStream_t stream) {
+template <class S> static cudaError_t launch(const AttendArgs &a, int32_t sms, cudaStream_t stream) {
     static std::atomic<uint64_t> asked;
-    cudaError_t e = allow_shared(kvx_attend_latent_codes<IO>, kCodeBytes, a.device, asked);
-    if (e == cudaSuccess) e = launch_after(kvx_attend_latent_codes<IO>, dim3(sms), kCodeThreads, kCodeBytes, stream, a, *a.row_maps);
-    return e != cudaSuccess ? e : launch_latent_join(a, IO, sms, sms, stream);
+    cudaError_t e = allow_shared(kvx_attend_latent_tensor<S>, S::BYTES, a.device, asked);
+    if (e == cudaSuccess) e = launch_after(kvx_attend_latent_tensor<S>, dim3(sms), kTensorThreads, S::BYTES, stream, a, *a.row_maps);
+    return e != cudaSuccess ? e : launch_latent_join(a, S::IO, sms, sms, stream);
 }
 
-cudaError_t launch_latent_codes(const AttendArgs &a, int32_t io, int32_t sms, cudaStream_t stream) {
-    return io == KVX_BF16 ? launch<KVX_BF16>(a, sms, stream) : launch<KVX_F16>(a, sms, stream);
+cudaError_t launch_latent_tensor(const AttendArgs &a, int32_t vt, int32_t io, int32_t sms, cudaStream_t stream) {
+    if (vt == KVX_BF16) return launch<TensorShape<KVX_BF16, KVX_BF16>>(a, sms, stream);
+    if (vt == KVX_F16) return launch<TensorShape<KVX_F16, KVX_F16>>(a, sms, stream);
+    return io == KVX_BF16 ? launch<TensorShape<KVX_E4M3, KVX_BF16>>(a, sms, stream) : launch<TensorShape<KVX_E4M3, KVX_F16>>(a, sms, stream);
 }
 
 }  // namespace kvx
