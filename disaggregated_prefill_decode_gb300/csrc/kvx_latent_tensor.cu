@@ -1,52 +1,55 @@
 // kvx_cache_attend over one plane of latents, on the tcgen05 tensor pipe.
 //
-// Of 8-bit latents the codes are multiplied as they are, so nothing of the cache passes through registers: a tile of
-// 128 positions is brought into shared memory by TMA in 128-byte swizzled chunks of 128 elements, and
-// serves twice as operand A: by rows (K-major) for the scores
-// S = K Q^T, 128 positions x 48, and by columns (MN-major) for the sums O^T += V^T P, four times 128
-// elements x 48. What is not 8 bits wide is split into three codes with a spacing of 2^5, a column each:
+// Nothing of the cache passes through registers: a tile of 128 positions (64 of 16 bits, the same bytes) is
+// brought into shared memory by TMA, in chunks of 128 elements whose rows are swizzled over 128 bytes, and
+// serves twice as operand A: by rows (K-major) for the scores S = K Q^T, 128 positions x the query columns,
+// and by columns (MN-major) for the sums O^T += V^T P, four times 128 elements x the weight columns.
+//
+// 8-bit latents are multiplied as the codes they are. What is not 8 bits wide is split into three codes with
+// a spacing of 2^5, a column each:
 //   x = c1 + c2 / 2^5 + c3 / 2^10,  each the nearest code of what is left,
-// 12 significant bits and more, exact for bf16 queries down to 2^-18 of a query's largest element; so 16
-// query heads make 48 columns. Their sums stand in TMEM apart and are put together in 32 bits.
+// 12 significant bits and more, exact for bf16 queries down to 2^-18 of a query's largest element, which is
+// brought into [2^7, 2^8) by a power of two. 16-bit latents take a query as it is, and a weight as two
+// values whose sum leaves 2^-17 of it. The columns' sums stand in TMEM apart and are put together in 32 bits.
+// Weights are taken against a maximum that moves only when a score passes it by more than 2^kSlack, so that
+// O in TMEM is hardly ever rescaled; times 2^5 they stay within the codes' range.
 //
-// 16-bit latents go the same way in tiles of 64 positions, the same bytes; a query is one column, a weight
-// two 16-bit values whose sum leaves 2^-17 of it, and a chunk is two pieces of 128 bytes a row.
-//
-// Queries of 8-bit latents are brought to a largest element in [2^7, 2^8) by a power of two. Weights are taken against a
-// maximum that moves only when a score passes it by more than 2^kSlack, so that O in TMEM is hardly ever
-// rescaled; times 2^5 they stay within the codes' range.
+// 16 query heads go at a time, or 32 where a KV head has more than 16: the columns of 32 take TMEM whole
+// (of 8 bits with one buffer of scores, not two), and the cache is read half as often. 64 requests of 8000,
+// 32 heads: 84 us with 32, 111 with 16 (bf16 122, 206).
 //
 // Rows come in boxes of as many as a page holds in a row (the common divisor of the page and the tile);
 // boxes that begin or end a sequence, and pages that 4 does not divide, are gathered four rows at a time,
 // since a row that is not live has to read as zero. Gathers alone took 58 clocks each, 4.9 us a tile.
 //
-// Shared memory bounds the products, at 128 bytes a clock: a position is written once (576 bytes) and read
-// twice (576 + 512), and the narrow operands add 400: 16 clocks an SM, where the memory takes 25. So what
-// counts is that the copies never stop. Two tiles fit, and a tile's way (copy 1.9 us, scores 0.6, softmax
-// 0.5, sums 0.4) is longer than the memory's time for two (3.3 us): each of the five chunks is therefore
-// copied as soon as its sums are done, by a warp of its own, and multiplied as soon as it is there.
+// Shared memory bounds the products, at 128 bytes a clock: 128 positions of 8 bits are written once (576
+// bytes each) and read twice (576 + 512), and the narrow operands of 16 heads add 400: 16 clocks an SM, where
+// the memory takes 25. So what counts is that the copies never stop. Two tiles fit, and a tile's way (copy
+// 1.9 us, scores 0.6, softmax 0.5, sums 0.4) is longer than the memory's time for two (3.3 us): each of the
+// five chunks is therefore copied as soon as its sums are done, by a warp of its own, and multiplied as soon
+// as it is there.
 //
-// Measured, 16 query heads: 64 sessions of 2048 to 32768 positions 122 us (644 MB; 1.7 us a tile, 0.97 of the
-// copy rate, while it streams), 128 requests of 8000 115 us, 5.2 TB/s; of 8000 bf16 latents 64 requests 112
-// us, 128 207 us, 5.7 TB/s, which warp products (kvx_latent.cu) took 144 and 270 for. Steps on the way: four rows a gather
-// 408 us; boxes of a page's runs 167; chunk by chunk, products from a converged warp instead of one lane's
-// branch (18 products 0.6 us, not 2.5) 153; eight softmax warps 146; a lighter join 140; a copying warp per
-// chunk, and scores and sums from two warps 123. Prefetching the next tiles into L2 cost 8 to 17 us.
+// Measured, 16 query heads, 8 bits: 64 sessions of 2048 to 32768 positions 119 us (644 MB; 1.7 us a tile, 0.97
+// of the copy rate, while it streams), 128 requests of 8000 113 us, 5.3 TB/s; bf16: 64 requests of 8000 109
+// us, 128 201 us, 5.9 TB/s, which warp products (kvx_latent.cu) took 144 and 270 for. Steps on the way, 8
+// bits: four rows a gather 408 us; boxes of a page's runs 167; chunk by chunk, products from a converged warp
+// instead of one lane's branch (18 products 0.6 us, not 2.5) 153; eight softmax warps 146; a lighter join
+// 140; a copying warp per chunk, and scores and sums from two warps 123; no query and no scale kept in
+// registers, so no spills, 119. Prefetching the next tiles into L2 cost 8 to 17 us.
 #include "kvx_latent.cuh"
 
 namespace kvx {
 
 constexpr int kSoftThreads = 256;                              // warps 0-7: softmax and outputs, half of the query heads each four
 constexpr int kTensorThreads = kSoftThreads + 7 * 32;          // 8, 9: products of the scores, of the sums; 10-14: copies, a chunk each
-constexpr int kMine = kLatentHeads / 2;                        // query heads of a softmax thread
 constexpr int kChunks = 5;                                     // the last one is used up by the scores, the others in their order by the sums
 constexpr float kSpacing = 32.0f;
 constexpr float kSlack = 3.0f;                                 // in powers of two
-constexpr uint32_t kColScores = 0, kColSums = 128, kTmemCols = 512;      // two buffers of scores 64 columns apart, then 4 x S::WCOLS
+constexpr uint32_t kColScores = 0, kColSums = 128, kTmemCols = 512;      // of TMEM: scores, then 4 x S::WCOLS sums
 constexpr int kSegmentSwitch = 1;                              // places of the line that a change of segment counts
 
-template <int VT_, int IO_> struct TensorShape {
-    static constexpr int VT = VT_, IO = IO_;
+template <int VT_, int IO_, int HEADS_> struct TensorShape {
+    static constexpr int VT = VT_, IO = IO_, HEADS = HEADS_;       // HEADS: query heads at a time
     static constexpr bool F8 = VT == KVX_E4M3;
     static constexpr int ESZ = F8 ? 1 : 2;
     static constexpr int TILE = 128 / ESZ;                        // positions
@@ -55,11 +58,15 @@ template <int VT_, int IO_> struct TensorShape {
     static constexpr int STAGE = 4 * CHUNK + CHUNK / 2;
     static constexpr int LAST = F8 ? 64 : 128;                    // bytes of a row in the last chunk
     static constexpr int QTERMS = F8 ? 3 : 1, WTERMS = F8 ? 3 : 2;   // columns of a query head in the two products
-    static constexpr int QCOLS = QTERMS * kLatentHeads, WCOLS = WTERMS * kLatentHeads;
+    static constexpr int QCOLS = QTERMS * HEADS, WCOLS = WTERMS * HEADS;
+    static constexpr int SBUFS = QCOLS > 64 ? 1 : 2;              // buffers of scores, 64 columns apart
     static constexpr int QUERY = QCOLS * kCacheMaxLatent * ESZ, WEIGHT = WCOLS * TILE * ESZ;
     static constexpr int OFF_QUERY = 2 * STAGE, OFF_WEIGHT = OFF_QUERY + QUERY, BYTES = OFF_WEIGHT + 2 * WEIGHT;
     static constexpr float UP = F8 ? 32.0f : 1.0f;                // of the weights: 2^(kSlack + 5) is within the codes' 448
     static constexpr int ROWS = F8 ? 32 : 16;                     // of the scores in a warp's lanes of TMEM: 64 rows leave half free
+    static constexpr int HALF = HEADS / 2;                        // query heads of four softmax warps
+    static constexpr int MINE = HALF * ROWS / 32;                 // of a thread's scores
+    static_assert(kColSums + 4 * WCOLS <= kTmemCols && MINE * ESZ % 8 == 0, "room in TMEM, weights in pieces of 8 or 16 bytes");
     // M x N products with 32-bit sums: both operands by rows, or both by columns; bf16 is type 1, e4m3 and f16 are 0
     static constexpr uint32_t IDESC = 1u << 4 | (VT == KVX_BF16 ? 1u << 7 | 1u << 10 : 0);
     static constexpr uint32_t IDESC_ROWS = IDESC | (QCOLS / 8) << 17 | (TILE / 16) << 24;
@@ -91,11 +98,11 @@ __device__ __forceinline__ void tensor_fence_before() { asm volatile("tcgen05.fe
 __device__ __forceinline__ void tensor_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
 // 8 columns of this warp's 32 rows of TMEM.
-__device__ __forceinline__ void tmem_load(uint32_t (&x)[kMine], uint32_t at) {
+__device__ __forceinline__ void tmem_load(uint32_t (&x)[8], uint32_t at) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]) : "r"(at) : "memory");
 }
-__device__ __forceinline__ void tmem_store(const uint32_t (&x)[kMine], uint32_t at) {
+__device__ __forceinline__ void tmem_store(const uint32_t (&x)[8], uint32_t at) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
                  "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
                  : "memory");
@@ -128,37 +135,38 @@ __device__ __forceinline__ uint32_t take_codes(float &x, float &y) {
     return c;
 }
 
-// 8 values, one per query head, over the 32 lanes of the warp: the result is for head lane / 4.
-template <class Op> __device__ __forceinline__ float reduce_heads(float (&v)[kMine], Op op) {
+// N values, one per query head, over a group of LANES lanes: the result is for head (lane of the group) / (LANES / N).
+template <int LANES, int N, class Op> __device__ __forceinline__ float reduce_heads(float (&v)[N], Op op) {
     const int lane = threadIdx.x & 31;
+    int d = LANES / 2;
 #pragma unroll
-    for (int n = kMine / 2; n; n >>= 1) {
-        const bool up = lane & 4 * n;
+    for (int n = N / 2; n; n >>= 1, d >>= 1) {
+        const bool up = lane & d;
 #pragma unroll
         for (int i = 0; i < n; ++i) {
             const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
-            v[i] = op(keep, __shfl_xor_sync(~0u, give, 4 * n));
+            v[i] = op(keep, __shfl_xor_sync(~0u, give, d));
         }
     }
-    v[0] = op(v[0], __shfl_xor_sync(~0u, v[0], 2));
-    return op(v[0], __shfl_xor_sync(~0u, v[0], 1));
+#pragma unroll
+    for (int x = LANES / N / 2; x; x >>= 1) v[0] = op(v[0], __shfl_xor_sync(~0u, v[0], x));
+    return v[0];
 }
 
 template <class S> __global__ void __launch_bounds__(kTensorThreads, 1)
 kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_constant__ RowMaps maps) {
-    constexpr int VT = S::VT, IO = S::IO, QTERMS = S::QTERMS, WTERMS = S::WTERMS;
+    constexpr int VT = S::VT, IO = S::IO, QTERMS = S::QTERMS, WTERMS = S::WTERMS, HEADS = S::HEADS, HALF = S::HALF, MINE = S::MINE;
     constexpr bool F8 = S::F8;
     using Line = Place<S::TILE, kSegmentSwitch>;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ __align__(8) uint64_t s_full[2][kChunks], s_free[2][kChunks];           // chunk by chunk
-    __shared__ __align__(8) uint64_t s_scored[2], s_weighed[2], s_queried, s_drained[2];
+    __shared__ __align__(8) uint64_t s_scored[2], s_weighed[2], s_read, s_queried, s_drained[2];
     __shared__ uint8_t s_live[3][32];                              // live positions, four a byte
-    __shared__ __align__(16) float s_red[4][kLatentHeads];
-    __shared__ float s_scale[kLatentHeads];
+    __shared__ __align__(16) float s_red[4][S::HEADS], s_scale[2][S::HEADS], s_old[S::HEADS], s_m[S::HEADS], s_l[S::HEADS];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int32_t s_failed;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int32_t group = a.n_q_heads / a.n_kv_heads, sets = (group + kLatentHeads - 1) / kLatentHeads, segs = a.n_kv_heads * sets;
+    const int32_t group = a.n_q_heads / a.n_kv_heads, sets = (group + HEADS - 1) / HEADS, segs = a.n_kv_heads * sets;
 
     if (threadIdx.x == 0) {                                        // what touches no memory, while the kernel before still runs
         s_failed = 0;
@@ -171,6 +179,7 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_addr(&s_drained[i])) : "memory");
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_addr(&s_weighed[i])), "n"(kSoftThreads) : "memory");
         }
+        asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_addr(&s_read)), "n"(kSoftThreads) : "memory");
         asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_addr(&s_queried)), "n"(kSoftThreads) : "memory");
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -215,9 +224,9 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
         bool ok = true, first = true;
         for (int j = 0; ok && x < c_end; ++j) {
             const uint64_t stage = (j & 1) * (S::STAGE / 16);
-            const uint32_t d = tmem + kColScores + (j & 1) * 64;
-            if (j >= 2) {                                          // the scores before are read
-                ok = __all_sync(~0u, wait(&s_weighed[j & 1], (j - 2) >> 1));
+            const uint32_t d = tmem + kColScores + (S::SBUFS == 2 ? (j & 1) * 64 : 0);
+            if (j >= S::SBUFS) {                                   // the scores before are read
+                ok = __all_sync(~0u, S::SBUFS == 2 ? wait(&s_weighed[j & 1], (j - 2) >> 1) : wait(&s_read, j - 1));
                 tensor_fence_after();
             }
             if (ok && first) ok = __all_sync(~0u, wait(&s_queried, switches++));
@@ -265,49 +274,55 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
             wait_full(&s_drained[1], 0);
         }
     } else if (w < 8) {                                            // softmax and outputs
-        // a thread has a position (an element, of the outputs) and 8 query heads
-        const int here = (w & 3) * 32 + lane, pos = (w & 3) * S::ROWS + lane, h0 = w >> 2 << 3;
-        const bool scores = lane < S::ROWS;
-        const uint32_t lanes = tmem + ((uint32_t)(w & 3) << 21) + h0;          // this warp's 32 rows, its first column
-        float m[kMine], l[kMine], scale[kMine];
+        // A thread has a position and MINE query heads of the scores, an element and HALF of the outputs. The scores of a
+        // tile of 64 positions stand in half of the lanes, which hand half of the heads to the others.
+        const int here = (w & 3) * 32 + lane, half0 = (w >> 2) * HALF;
+        const int pos = (w & 3) * S::ROWS + lane % S::ROWS, h0 = half0 + lane / S::ROWS * MINE;
+        const uint32_t lanes = tmem + ((uint32_t)(w & 3) << 21) + half0;       // this warp's 32 rows, its first column
+        constexpr int kParts = kSoftThreads / HEADS;               // threads of a query
+        float m[MINE], l[MINE];
+        int turn = 0;                                              // of s_scale
         // Queries of a segment as codes, and what its scores are to be multiplied by.
-        auto query = [&](const Line &p) {
-            const int h = threadIdx.x >> 4, part = threadIdx.x & 15;
-            const int32_t kvh = p.seg / sets, in_group = p.seg % sets * kLatentHeads + h;
+        auto query = [&](const Line &p, int turn) {
+            const int h = threadIdx.x / kParts, part = threadIdx.x % kParts;
+            const int32_t kvh = p.seg / sets, in_group = p.seg % sets * HEADS + h;
             const uint8_t *src = a.q + p.r * a.q_stride + ((int64_t)kvh * group + in_group) * a.head_dim * 2;
             const bool real = in_group < group;
             if constexpr (F8) {
-                constexpr int kBlocks = (kCacheMaxLatent / 16 + 15) / 16;  // of 16 elements, for each of a head's 16 threads
-                uint4 y[kBlocks][2];
-                float top = 0.0f;
-#pragma unroll
-                for (int i = 0; i < kBlocks; ++i)
+                constexpr int kBlocks = (kCacheMaxLatent / 16 + kParts - 1) / kParts;          // of 16 elements, for each of a head's threads
+                auto read = [&](int i, uint4 (&y)[2]) {            // twice: kept in registers, they cost the softmax spills
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const int d = (part + 16 * i) * 16 + k * 8;
-                        y[i][k] = real && d < a.head_dim ? __ldg(reinterpret_cast<const uint4 *>(src + d * 2)) : make_uint4(0, 0, 0, 0);
+                        const int d = (part + kParts * i) * 16 + k * 8;
+                        y[k] = real && d < a.head_dim ? __ldg(reinterpret_cast<const uint4 *>(src + d * 2)) : make_uint4(0, 0, 0, 0);
                     }
+                };
+                uint4 y[2];
+                float top = 0.0f;
 #pragma unroll
-                for (int i = 0; i < kBlocks; ++i)
+                for (int i = 0; i < kBlocks; ++i) {
+                    read(i, y);
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
-                        for (uint32_t z : {y[i][k].x, y[i][k].y, y[i][k].z, y[i][k].w}) {
+                        for (uint32_t z : {y[k].x, y[k].y, y[k].z, y[k].w}) {
                             const float2 f = unpack<IO>(z);
                             top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
                         }
+                }
 #pragma unroll
-                for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+                for (int d = 1; d < kParts; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
                 const int e = top > 0.0f && top < INFINITY ? max(-100, min(100, 7 - ilogbf(top))) : 0;
                 const float up = __int_as_float((127 + e) << 23);
-                if (part == 0) s_scale[h] = top < INFINITY ? a.scale * __int_as_float((127 - e) << 23) : NAN;     // an infinite query: NaN
-#pragma unroll
+                if (part == 0) s_scale[turn][h] = top < INFINITY ? a.scale * __int_as_float((127 - e) << 23) : NAN;     // an infinite query: NaN
+#pragma unroll 1
                 for (int i = 0; i < kBlocks; ++i) {
-                    const int b = part + 16 * i;
+                    const int b = part + kParts * i;
                     if (b >= kCacheMaxLatent / 16) break;
+                    read(i, y);
                     uint32_t codes[QTERMS][4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const uint32_t z0 = k & 1 ? y[i][k >> 1].z : y[i][k >> 1].x, z1 = k & 1 ? y[i][k >> 1].w : y[i][k >> 1].y;
+                        const uint32_t z0 = k & 1 ? y[k >> 1].z : y[k >> 1].x, z1 = k & 1 ? y[k >> 1].w : y[k >> 1].y;
                         const float2 f0 = unpack<IO>(z0), f1 = unpack<IO>(z1);
                         float v[4] = {f0.x * up, f0.y * up, f1.x * up, f1.y * up};
 #pragma unroll
@@ -318,13 +333,12 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
                     }
 #pragma unroll
                     for (int n = 0; n < QTERMS; ++n)                   // blocks of 8 columns x 16 elements
-                        *(uint4 *)(smem + S::OFF_QUERY + (b * (S::QCOLS / 8) + n * 2 + (h >> 3)) * 128 + (h & 7) * 16) =
+                        *(uint4 *)(smem + S::OFF_QUERY + (b * (S::QCOLS / 8) + n * (HEADS / 8) + (h >> 3)) * 128 + (h & 7) * 16) =
                             make_uint4(codes[n][0], codes[n][1], codes[n][2], codes[n][3]);
                 }
             } else {                                               // as they are, in blocks of 8 columns x 8 elements
-                if (part == 0) s_scale[h] = a.scale;
 #pragma unroll
-                for (int b = part; b < kCacheMaxLatent / 8; b += 16)
+                for (int b = part; b < kCacheMaxLatent / 8; b += kParts)
                     *(uint4 *)(smem + S::OFF_QUERY + (b * (S::QCOLS / 8) + (h >> 3)) * 128 + (h & 7) * 16) =
                         real && b * 8 < a.head_dim ? __ldg(reinterpret_cast<const uint4 *>(src + b * 16)) : make_uint4(0, 0, 0, 0);
             }
@@ -334,71 +348,90 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
         };
         auto begin_segment = [&]() {
 #pragma unroll
-            for (int h = 0; h < kMine; ++h) {
+            for (int h = 0; h < MINE; ++h) {
                 m[h] = -INFINITY;
                 l[h] = 0.0f;
-                scale[h] = s_scale[h0 + h];
             }
         };
         Line at = begin;
         int64_t x = x0;
-        query(at);
+        query(at, 0);
         begin_segment();
         bool first = true, begun = at.seg_begin(segs) >= c_begin;  // the segment's first tile here; it begins in this CTA
         for (int j = 0;; ++j) {
             wait(&s_scored[j & 1], j >> 1);
             tensor_fence_after();
-            float s[kMine];
+            float s[MINE];
             {
-                uint32_t y[QTERMS][kMine];
+                const bool live = s_live[j % 3][pos >> 2] >> (pos & 3) & 1;
+                float z[HALF];
 #pragma unroll
-                for (int k = 0; k < QTERMS; ++k) tmem_load(y[k], lanes + kColScores + (j & 1) * 64 + k * 16);
-                tmem_load_wait();
-                const bool live = scores && s_live[j % 3][pos >> 2] >> (pos & 3) & 1;
+                for (int i = 0; i < HALF; i += 8) {
+                    uint32_t y[QTERMS][8];
 #pragma unroll
-                for (int h = 0; h < kMine; ++h) {
-                    float z = __uint_as_float(y[0][h]);
-                    if constexpr (F8) z += (__uint_as_float(y[1][h]) + __uint_as_float(y[2][h]) / kSpacing) / kSpacing;
-                    s[h] = live ? z * scale[h] : -INFINITY;
+                    for (int k = 0; k < QTERMS; ++k) tmem_load(y[k], lanes + kColScores + (S::SBUFS == 2 ? (j & 1) * 64 : 0) + k * HEADS + i);
+                    tmem_load_wait();
+#pragma unroll
+                    for (int h = 0; h < 8; ++h) {
+                        z[i + h] = __uint_as_float(y[0][h]);
+                        if constexpr (F8) z[i + h] += (__uint_as_float(y[1][h]) + __uint_as_float(y[2][h]) / kSpacing) / kSpacing;
+                    }
+                }
+                if constexpr (S::SBUFS == 1) {
+                    tensor_fence_before();
+                    arrive(&s_read);
+                }
+#pragma unroll
+                for (int h = 0; h < MINE; ++h) {
+                    if constexpr (F8) s[h] = z[h] * s_scale[turn][h0 + h];
+                    else {
+                        const float other = __shfl_sync(~0u, z[MINE + h], lane % S::ROWS);
+                        s[h] = (lane < S::ROWS ? z[h] : other) * a.scale;
+                    }
+                    if (!live) s[h] = -INFINITY;
                 }
             }
             float over = -INFINITY;
 #pragma unroll
-            for (int h = 0; h < kMine; ++h) over = fmaxf(over, s[h] - m[h]);
+            for (int h = 0; h < MINE; ++h) over = fmaxf(over, s[h] - m[h]);
+            constexpr int kLanes = S::ROWS / MINE;                 // that reduce_heads leaves a head's result in
             if (softmax_any(over > kSlack)) {                      // some maximum moves
-                float v[kMine];
+                float v[MINE];
 #pragma unroll
-                for (int h = 0; h < kMine; ++h) v[h] = s[h];
-                const float top = reduce_heads(v, [](float p, float q) { return fmaxf(p, q); });
-                if (!(lane & 3)) s_red[w & 3][h0 + (lane >> 2)] = top;
+                for (int h = 0; h < MINE; ++h) v[h] = s[h];
+                const float top = reduce_heads<S::ROWS>(v, [](float p, float q) { return fmaxf(p, q); });
+                if (lane % kLanes == 0) s_red[w & 3][h0 + lane % S::ROWS / kLanes] = top;
                 softmax_any(false);
-                float old[kMine];
+                float old[MINE];
 #pragma unroll
-                for (int h = 0; h < kMine; ++h) {
+                for (int h = 0; h < MINE; ++h) {
                     const float up = fmaxf(m[h], fmaxf(fmaxf(s_red[0][h0 + h], s_red[1][h0 + h]), fmaxf(s_red[2][h0 + h], s_red[3][h0 + h])));
                     old[h] = fast_exp2(m[h] - (up == -INFINITY ? 0.0f : up));
                     m[h] = up;
                     l[h] *= old[h];
+                    if (MINE < HALF && (w & 3) == 0 && lane % S::ROWS == 0) s_old[h0 + h] = old[h];
                 }
                 softmax_any(false);                                // s_red is free again
                 if (!first) {
                     wait(&s_free[(j - 1) & 1][3], (j - 1) >> 1);
                     tensor_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < 4 * WTERMS; ++c) {
-                        uint32_t y[kMine];
-                        tmem_load(y, lanes + kColSums + c * 16);
-                        tmem_load_wait();
+                    for (int c = 0; c < 4 * WTERMS; ++c)
 #pragma unroll
-                        for (int h = 0; h < kMine; ++h) y[h] = __float_as_uint(__uint_as_float(y[h]) * old[h]);
-                        tmem_store(y, lanes + kColSums + c * 16);
-                    }
+                        for (int i = 0; i < HALF; i += 8) {
+                            uint32_t y[8];
+                            tmem_load(y, lanes + kColSums + c * HEADS + i);
+                            tmem_load_wait();
+#pragma unroll
+                            for (int h = 0; h < 8; ++h) y[h] = __float_as_uint(__uint_as_float(y[h]) * (MINE < HALF ? s_old[half0 + i + h] : old[(i + h) % MINE]));
+                            tmem_store(y, lanes + kColSums + c * HEADS + i);
+                        }
                     tmem_store_wait();
                 }
             }
-            uint32_t parts_of[WTERMS][2 * S::ESZ];                 // 8 heads' weights, term by term
+            uint32_t terms[WTERMS][MINE * S::ESZ / 4];             // the heads' weights, term by term
 #pragma unroll
-            for (int h = 0; h < kMine; h += 4) {
+            for (int h = 0; h < MINE; h += 4) {
                 float v[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -410,25 +443,26 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
 #pragma unroll
                     for (int k = 0; k < WTERMS; ++k) {
                         const uint32_t lo = take_codes(v[0], v[1]);
-                        parts_of[k][h / 4] = lo | take_codes(v[2], v[3]) << 16;
+                        terms[k][h / 4] = lo | take_codes(v[2], v[3]) << 16;
                     }
                 } else {
 #pragma unroll
                     for (int i = 0; i < 4; i += 2) {
                         const uint32_t top = pack<VT>(v[i], v[i + 1]);
                         const float2 f = unpack<VT>(top);
-                        parts_of[0][(h + i) / 2] = top;
-                        parts_of[1][(h + i) / 2] = pack<VT>(v[i] - f.x, v[i + 1] - f.y);
+                        terms[0][(h + i) / 2] = top;
+                        terms[1][(h + i) / 2] = pack<VT>(v[i] - f.x, v[i + 1] - f.y);
                     }
                 }
             }
             if (j >= 2) wait(&s_free[j & 1][3], (j - 2) >> 1);
-            uint8_t *const weights = smem + S::OFF_WEIGHT + (j & 1) * S::WEIGHT + pos * 16;
 #pragma unroll
-            for (int k = 0; k < WTERMS; ++k)                       // blocks of 16 bytes of columns x 8 positions
-                if constexpr (F8) *(uint2 *)(weights + k * S::TILE * 16 + h0) = make_uint2(parts_of[k][0], parts_of[k][1]);
-                else if (scores)
-                    *(uint4 *)(weights + (k * 2 + (h0 >> 3)) * S::TILE * 16) = make_uint4(parts_of[k][0], parts_of[k][1], parts_of[k][2], parts_of[k][3]);
+            for (int k = 0; k < WTERMS; ++k) {                     // blocks of 16 bytes of columns x 8 positions
+                const int col = (k * HEADS + h0) * S::ESZ;
+                uint8_t *const to = smem + S::OFF_WEIGHT + (j & 1) * S::WEIGHT + col / 16 * S::TILE * 16 + pos * 16 + col % 16;
+                if constexpr (MINE * S::ESZ == 8) *(uint2 *)to = make_uint2(terms[k][0], terms[k][1]);
+                else *(uint4 *)to = make_uint4(terms[k][0], terms[k][1], terms[k][2], terms[k][3]);
+            }
             fence_async();
             tensor_fence_before();
             arrive(&s_weighed[j & 1]);
@@ -442,55 +476,64 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
                 at = nxt;
                 continue;
             }
-            if (more) query(nxt);                                  // these scores are read, so the queries are free
+            if (more) query(nxt, turn ^ 1);                                  // these scores are read, so the queries are free
             wait(&s_free[j & 1][3], j >> 1);
             tensor_fence_after();
             {
-                float v[kMine];
+                float v[MINE];
 #pragma unroll
-                for (int h = 0; h < kMine; ++h) v[h] = l[h];
-                const float sum = reduce_heads(v, [](float p, float q) { return p + q; });
-                if (!(lane & 3)) s_red[w & 3][h0 + (lane >> 2)] = sum;
+                for (int h = 0; h < MINE; ++h) {
+                    v[h] = l[h];
+                    if ((w & 3) == 0 && lane % S::ROWS == 0) s_m[h0 + h] = m[h];
+                }
+                const float sum = reduce_heads<S::ROWS>(v, [](float p, float q) { return p + q; });
+                if (lane % kLanes == 0) s_red[w & 3][h0 + lane % S::ROWS / kLanes] = sum;
                 softmax_any(false);
-#pragma unroll
-                for (int h = 0; h < kMine; ++h) l[h] = (s_red[0][h0 + h] + s_red[1][h0 + h]) + (s_red[2][h0 + h] + s_red[3][h0 + h]);
+                if (threadIdx.x < HEADS)
+                    s_l[threadIdx.x] = (s_red[0][threadIdx.x] + s_red[1][threadIdx.x]) + (s_red[2][threadIdx.x] + s_red[3][threadIdx.x]);
                 softmax_any(false);
             }
             const bool whole = ends && begun;
-            const int32_t in_group = at.seg % sets * kLatentHeads, head0 = at.seg / sets * group + in_group, heads = min(group - in_group, kLatentHeads);
-            uint8_t *const part = parts + (size_t)(blockIdx.x * 2 + begun) * kLatentPartial;
+            const int32_t in_group = at.seg % sets * HEADS, head0 = at.seg / sets * group + in_group, heads = min(group - in_group, HEADS);
+            // partial results are of kLatentHeads heads: the second half of 32 goes where another CTA's would be
+            auto part_of = [&](int h) { return parts + ((size_t)(blockIdx.x + h / kLatentHeads * gridDim.x) * 2 + begun) * kLatentPartial; };
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                uint32_t y[WTERMS][kMine];
+            for (int c = 0; c < 4; ++c)
+#pragma unroll 1
+                for (int i = 0; i < HALF; i += 8) {
+                    uint32_t y[WTERMS][8];
 #pragma unroll
-                for (int k = 0; k < WTERMS; ++k) tmem_load(y[k], lanes + kColSums + c * S::WCOLS + k * 16);
-                tmem_load_wait();
-                const int d = c * 128 + here;
+                    for (int k = 0; k < WTERMS; ++k) tmem_load(y[k], lanes + kColSums + c * S::WCOLS + k * HEADS + i);
+                    tmem_load_wait();
+                    const int d = c * 128 + here;
+                    float *const part = (float *)part_of(half0 + i);
 #pragma unroll
-                for (int h = 0; h < kMine; ++h) {
-                    float z = __uint_as_float(y[1][h]);
-                    if constexpr (F8) z = (z + __uint_as_float(y[2][h]) / kSpacing) / kSpacing;
-                    z = (z + __uint_as_float(y[0][h])) / S::UP;
-                    if (!whole) __stcg((float *)part + partial_at(d, h0 + h), z);
-                    else if (h0 + h < heads && d < a.v_dim)
-                        ((uint16_t *)(a.out + at.r * a.out_stride))[(int64_t)(head0 + h0 + h) * a.v_dim + d] =
-                            (uint16_t)pack<IO>(l[h] == 0.0f ? 0.0f : z * (a.v_scale / l[h]), 0.0f);
+                    for (int n = 0; n < 8; ++n) {
+                        const int h = half0 + i + n;
+                        float z = __uint_as_float(y[1][n]);
+                        if constexpr (F8) z = (z + __uint_as_float(y[2][n]) / kSpacing) / kSpacing;
+                        z = (z + __uint_as_float(y[0][n])) / S::UP;
+                        if (!whole) __stcg(part + partial_at(d, h % kLatentHeads), z);
+                        else if (h < heads && d < a.v_dim)
+                            ((uint16_t *)(a.out + at.r * a.out_stride))[(int64_t)(head0 + h) * a.v_dim + d] =
+                                (uint16_t)pack<IO>(s_l[h] == 0.0f ? 0.0f : z * (a.v_scale / s_l[h]), 0.0f);
+                    }
                 }
-            }
             tensor_fence_before();
-#pragma unroll
-            for (int h = 0; h < kMine; ++h)
-                if (here == h) {
-                    if (!whole) {
-                        __stcg((float *)(part + kLatentFloat4 * 16) + h0 + h, m[h]);
-                        __stcg((float *)(part + kLatentFloat4 * 16) + kLatentHeads + h0 + h, l[h]);
-                    } else if (a.lse && h0 + h < heads)
-                        a.lse[(int64_t)at.r * a.n_q_heads + head0 + h0 + h] = l[h] == 0.0f ? -INFINITY : (m[h] + log2f(l[h])) * kLn2;
-                }
+            if (threadIdx.x < HEADS) {
+                const int h = threadIdx.x;
+                if (!whole) {
+                    float *const ml = (float *)(part_of(h) + kLatentFloat4 * 16) + h % kLatentHeads;
+                    __stcg(ml, s_m[h]);
+                    __stcg(ml + kLatentHeads, s_l[h]);
+                } else if (a.lse && h < heads)
+                    a.lse[(int64_t)at.r * a.n_q_heads + head0 + h] = s_l[h] == 0.0f ? -INFINITY : (s_m[h] + log2f(s_l[h])) * kLn2;
+            }
             if (!whole && begun)
                 opened = OpenSegment{at.r, at.seg, batch.split.cta_of(at.seg_begin(segs) + at.tiles - 1) - (int32_t)blockIdx.x + 1, 0};
             if (!more) break;
             at = nxt;
+            turn ^= 1;
             begin_segment();
             first = begun = true;
         }
@@ -577,7 +620,12 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
     if (w == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
     if (threadIdx.x == 0) {
         if (s_failed) atomicAdd(a.pool.skipped + 1, 1ull);
-        open[blockIdx.x] = s_failed ? OpenSegment{0, 0, 0, 0} : opened;
+        for (int i = 0; i < HEADS / kLatentHeads; ++i) {           // as segments of kLatentHeads
+            const int32_t in_group = opened.seg % sets * HEADS + i * kLatentHeads, of_16 = (group + kLatentHeads - 1) / kLatentHeads;
+            open[blockIdx.x + i * gridDim.x] =
+                s_failed || in_group >= group ? OpenSegment{0, 0, 0, 0}
+                                              : OpenSegment{opened.r, opened.seg / sets * of_16 + in_group / kLatentHeads, opened.pieces, 0};
+        }
     }
 }
 
@@ -585,13 +633,17 @@ template <class S> static cudaError_t launch(const AttendArgs &a, int32_t sms, c
     static std::atomic<uint64_t> asked;
     cudaError_t e = allow_shared(kvx_attend_latent_tensor<S>, S::BYTES, a.device, asked);
     if (e == cudaSuccess) e = launch_after(kvx_attend_latent_tensor<S>, dim3(sms), kTensorThreads, S::BYTES, stream, a, *a.row_maps);
-    return e != cudaSuccess ? e : launch_latent_join(a, S::IO, sms, sms, stream);
+    return e != cudaSuccess ? e : launch_latent_join(a, S::IO, S::HEADS / kLatentHeads * sms, sms, stream);
+}
+
+template <int VT, int IO> static cudaError_t launch_heads(const AttendArgs &a, int32_t sms, cudaStream_t stream) {
+    return a.n_q_heads / a.n_kv_heads > 16 ? launch<TensorShape<VT, IO, 32>>(a, sms, stream) : launch<TensorShape<VT, IO, 16>>(a, sms, stream);
 }
 
 cudaError_t launch_latent_tensor(const AttendArgs &a, int32_t vt, int32_t io, int32_t sms, cudaStream_t stream) {
-    if (vt == KVX_BF16) return launch<TensorShape<KVX_BF16, KVX_BF16>>(a, sms, stream);
-    if (vt == KVX_F16) return launch<TensorShape<KVX_F16, KVX_F16>>(a, sms, stream);
-    return io == KVX_BF16 ? launch<TensorShape<KVX_E4M3, KVX_BF16>>(a, sms, stream) : launch<TensorShape<KVX_E4M3, KVX_F16>>(a, sms, stream);
+    if (vt == KVX_BF16) return launch_heads<KVX_BF16, KVX_BF16>(a, sms, stream);
+    if (vt == KVX_F16) return launch_heads<KVX_F16, KVX_F16>(a, sms, stream);
+    return io == KVX_BF16 ? launch_heads<KVX_E4M3, KVX_BF16>(a, sms, stream) : launch_heads<KVX_E4M3, KVX_F16>(a, sms, stream);
 }
 
 }  // namespace kvx

@@ -364,6 +364,38 @@ def test_attend_latent_long(value):
     check_attend([30000, 1, 9000], value=value, planes=1, hps=1, group=16, dim=576, v_dim=512, bs=64)
 
 
+@pytest.mark.parametrize("value", ["bf16", "f16"])
+@pytest.mark.parametrize("lens", [[1], [63, 64, 65, 128], [640, 0, 64, 300], [5] * 40])
+@pytest.mark.parametrize("bs", [1, 4, 20, 32, 64, 128])
+def test_attend_latent_16_bit_runs_of_pages(value, lens, bs):
+    check_attend(lens, value=value, planes=1, hps=1, group=16, dim=576, v_dim=512, bs=bs)
+    check_attend(lens, value=value, planes=1, hps=1, group=16, dim=576, v_dim=512, bs=bs, window=100)
+
+
+@pytest.mark.parametrize("shards,hps,dim,v_dim,layout", [(2, 1, 576, 512, NHD), (1, 2, 512, 512, NHD), (1, 2, 576, 512, NHD),
+                                                         (1, 3, 144, 48, HND), (1, 1, 72, 8, NHD)])
+@pytest.mark.parametrize("group", [5, 21])
+def test_attend_latent_16_bit_shards_and_heads(shards, hps, dim, v_dim, layout, group):
+    """Both kernels of 16-bit latents: the tensor maps cannot describe several shards, or heads with a gap."""
+    check_attend([3, 700, 0, 129], value="bf16", planes=1, shards=shards, hps=hps, group=group, dim=dim, v_dim=v_dim, bs=16, layout=layout)
+
+
+@pytest.mark.parametrize("value", ["bf16", "f16", "e4m3"])
+@pytest.mark.parametrize("group", [17, 24, 32, 33, 48, 65])
+def test_attend_latent_head_sets(value, group):
+    """32 query heads at a time, in halves of 16: requests that one CTA answers, and long ones that several join."""
+    check_attend([3000, 0, 1, 129, 20000], value=value, planes=1, hps=1, group=group, dim=576, v_dim=512, bs=64)
+    check_attend([90] * 200, value=value, planes=1, hps=1, group=group, dim=576, v_dim=512, bs=16)
+
+
+@pytest.mark.parametrize("value", ["bf16", "f16", "e4m3"])
+def test_attend_latent_head_sets_sharp_scores(value):
+    case = Attend([2000, 300, 1], value=value, planes=1, hps=1, group=32, dim=576, v_dim=512, spread=4.0, scale=0.5)
+    case.q *= torch.logspace(-3, 1, 32)[None, :, None]
+    case.q = case.q.to(case.iodtype)
+    case.check(*case.run())
+
+
 @pytest.mark.parametrize("planes", [1, 2])
 def test_attend_sharp_scores(planes):
     """Scores far apart: weights of one token, of none, and sums whose maximum moves late."""
