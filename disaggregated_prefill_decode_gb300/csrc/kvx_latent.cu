@@ -438,7 +438,7 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
 
 // Joins the segments that go over several CTAs. Up to kJoinFew pieces a thread joins a float4 of the sums by itself, 256 at a time;
 // of more pieces 64 float4s at a time, four groups of 64 threads taking every fourth piece.
-constexpr int kJoinThreads = 256, kJoinSlices = kLatentFloat4 / 64, kJoinCtas = 8;      // CTAs per SM
+constexpr int kJoinThreads = 256, kJoinSlices = kLatentFloat4 / 64, kJoinCtas = 2;      // CTAs per SM: 8 start 1 us later, 1 takes 2 us longer
 constexpr int kJoinList = 512;                                                          // at least the CTAs of the first kernel
 constexpr int kJoinFew = 8;
 
