@@ -162,7 +162,7 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
     __shared__ __align__(8) uint64_t s_full[2][kChunks], s_free[2][kChunks];           // chunk by chunk
     __shared__ __align__(8) uint64_t s_scored[2], s_weighed[2], s_read, s_queried, s_drained[2];
     __shared__ uint8_t s_live[3][32];                              // live positions, four a byte
-    __shared__ __align__(16) float s_red[4][S::HEADS], s_scale[2][S::HEADS], s_old[S::HEADS], s_m[S::HEADS], s_l[S::HEADS];
+    __shared__ __align__(16) float s_red[4][S::HEADS], s_scale[2][S::HEADS], s_old[S::HEADS], s_m[S::HEADS], s_l[S::HEADS], s_inverse[S::HEADS];
     __shared__ uint32_t s_tmem;
     __shared__ volatile int32_t s_failed;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -314,11 +314,13 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
                 const int e = top > 0.0f && top < INFINITY ? max(-100, min(100, 7 - ilogbf(top))) : 0;
                 const float up = __int_as_float((127 + e) << 23);
                 if (part == 0) s_scale[turn][h] = top < INFINITY ? a.scale * __int_as_float((127 - e) << 23) : NAN;     // an infinite query: NaN
+                read(0, y);
 #pragma unroll 1
                 for (int i = 0; i < kBlocks; ++i) {
                     const int b = part + kParts * i;
                     if (b >= kCacheMaxLatent / 16) break;
-                    read(i, y);
+                    uint4 after[2];
+                    read(i + 1, after);
                     uint32_t codes[QTERMS][4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -335,6 +337,8 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
                     for (int n = 0; n < QTERMS; ++n)                   // blocks of 8 columns x 16 elements
                         *(uint4 *)(smem + S::OFF_QUERY + (b * (S::QCOLS / 8) + n * (HEADS / 8) + (h >> 3)) * 128 + (h & 7) * 16) =
                             make_uint4(codes[n][0], codes[n][1], codes[n][2], codes[n][3]);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) y[k] = after[k];
                 }
             } else {                                               // as they are, in blocks of 8 columns x 8 elements
 #pragma unroll
@@ -489,12 +493,16 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
                 const float sum = reduce_heads<S::ROWS>(v, [](float p, float q) { return p + q; });
                 if (lane % kLanes == 0) s_red[w & 3][h0 + lane % S::ROWS / kLanes] = sum;
                 softmax_any(false);
-                if (threadIdx.x < HEADS)
-                    s_l[threadIdx.x] = (s_red[0][threadIdx.x] + s_red[1][threadIdx.x]) + (s_red[2][threadIdx.x] + s_red[3][threadIdx.x]);
+                if (threadIdx.x < HEADS) {
+                    const float all = (s_red[0][threadIdx.x] + s_red[1][threadIdx.x]) + (s_red[2][threadIdx.x] + s_red[3][threadIdx.x]);
+                    s_l[threadIdx.x] = all;
+                    s_inverse[threadIdx.x] = all == 0.0f ? 0.0f : a.v_scale / all;
+                }
                 softmax_any(false);
             }
             const bool whole = ends && begun;
             const int32_t in_group = at.seg % sets * HEADS, head0 = at.seg / sets * group + in_group, heads = min(group - in_group, HEADS);
+            uint16_t *const out = (uint16_t *)(a.out + at.r * a.out_stride) + (int64_t)head0 * a.v_dim;
             // partial results are of kLatentHeads heads: the second half of 32 goes where another CTA's would be
             auto part_of = [&](int h) { return parts + ((size_t)(blockIdx.x + h / kLatentHeads * gridDim.x) * 2 + begun) * kLatentPartial; };
 #pragma unroll 1
@@ -505,18 +513,41 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
 #pragma unroll
                     for (int k = 0; k < WTERMS; ++k) tmem_load(y[k], lanes + kColSums + c * S::WCOLS + k * HEADS + i);
                     tmem_load_wait();
-                    const int d = c * 128 + here;
-                    float *const part = (float *)part_of(half0 + i);
+                    float z[8];
 #pragma unroll
                     for (int n = 0; n < 8; ++n) {
-                        const int h = half0 + i + n;
-                        float z = __uint_as_float(y[1][n]);
-                        if constexpr (F8) z = (z + __uint_as_float(y[2][n]) / kSpacing) / kSpacing;
-                        z = (z + __uint_as_float(y[0][n])) / S::UP;
-                        if (!whole) __stcg(part + partial_at(d, h % kLatentHeads), z);
-                        else if (h < heads && d < a.v_dim)
-                            ((uint16_t *)(a.out + at.r * a.out_stride))[(int64_t)(head0 + h) * a.v_dim + d] =
-                                (uint16_t)pack<IO>(s_l[h] == 0.0f ? 0.0f : z * (a.v_scale / s_l[h]), 0.0f);
+                        z[n] = __uint_as_float(y[1][n]);
+                        if constexpr (F8) z[n] = (z[n] + __uint_as_float(y[2][n]) / kSpacing) / kSpacing;
+                        z[n] = (z[n] + __uint_as_float(y[0][n])) / S::UP;
+                    }
+                    // among four lanes, from 8 heads of an element each to two heads of four elements
+                    const int b0 = lane & 1, b1 = lane >> 1 & 1, d = c * 128 + (here & ~3);
+                    float u[4][2], t[2][4];
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const float keep = b0 ? z[4 + n] : z[n], got = __shfl_xor_sync(~0u, b0 ? z[n] : z[4 + n], 1);
+                        u[n][0] = b0 ? got : keep;
+                        u[n][1] = b0 ? keep : got;
+                    }
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float keep = b1 ? u[2 + n][e] : u[n][e], got = __shfl_xor_sync(~0u, b1 ? u[n][e] : u[2 + n][e], 2);
+                            t[n][e] = b1 ? got : keep;
+                            t[n][2 + e] = b1 ? keep : got;
+                        }
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const int h = half0 + i + b0 * 4 + b1 * 2 + n;
+                        if (!whole) __stcg((float4 *)((float *)part_of(h) + partial_at(d, h % kLatentHeads)), make_float4(t[n][0], t[n][1], t[n][2], t[n][3]));
+                        else if (h < heads && d < a.v_dim) {
+                            const float inverse = s_inverse[h];
+                            const bool none = s_l[h] == 0.0f;
+                            *reinterpret_cast<uint2 *>(out + h * a.v_dim + d) =
+                                none ? make_uint2(0, 0)
+                                     : make_uint2(pack<IO>(t[n][0] * inverse, t[n][1] * inverse), pack<IO>(t[n][2] * inverse, t[n][3] * inverse));
+                        }
                     }
                 }
             tensor_fence_before();
