@@ -36,7 +36,7 @@ __device__ __forceinline__ bool wait_full(uint64_t *bar, uint32_t parity) {
 
 // What a CTA leaves for the joining kernel: the segment that begins in its stretch and goes on after it (pieces 0: none).
 struct OpenSegment {
-    int32_t r, seg, pieces, unused;
+    int32_t r, seg, pieces, cta;       // cta: of the first piece, for the joining kernel alone
 };
 
 cudaError_t launch_latent_join(const AttendArgs &a, int32_t io, int ctas, int32_t sms, cudaStream_t stream);       // kvx_latent.cu
