@@ -32,6 +32,7 @@ constexpr int kSharedBytes = 226 << 10;       // of a CTA, one per SM
 // What the change to another segment costs a warp, in tiles: outputs, then queries. 200 requests with a window of 1024: 47.8 us
 // with 0, 42.1 with 1, 41.6 with 2; long segments the same with all three.
 constexpr int kSwitchTiles = 2;
+constexpr int kJoinAtOnce = 24;               // pieces of a segment that a warp's join loads at once
 
 template <int VT_, int IO_, int D_, int NT_, bool FULL_> struct Shape {
     static constexpr int VT = VT_, IO = IO_, D = D_, NT = NT_;   // D: head_dim rounded up; NT: query sets of 8
@@ -168,10 +169,10 @@ __device__ __forceinline__ Joined<S> join_few(int f, const Pieces &from) {
     return j;
 }
 
-// The same of many in the scratch, 24 at once: lane (g, t) takes the maxima and sums of every eighth for its query, the others'
+// The same of many in the scratch, kJoinAtOnce at once: lane (g, t) takes the maxima and sums of every eighth for its query, the others'
 // weights come by shuffles.
 template <class S> __device__ __noinline__ Joined<S> join_many(int f, const Pieces &from) {
-    constexpr int ROUNDS = 3;
+    constexpr int ROUNDS = kJoinAtOnce / 8;
     const int lane = threadIdx.x & 31, t = lane & 3, g = lane >> 2, n = from.n;
     Joined<S> j(f);
     for (int x0 = 0; x0 < n; x0 += 8 * ROUNDS) {
@@ -247,7 +248,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
     const int32_t group = a.n_q_heads / a.n_kv_heads, sets = (group + 8 * NT - 1) / (8 * NT), segs = a.n_kv_heads * sets;
 
     wait_for_earlier();
-    const Batch<TOK, S::WARPS, S::WARPS, kSwitchTiles> batch(a, segs);
+    const Batch<TOK, S::WARPS, S::WARPS, kSwitchTiles, kJoinAtOnce> batch(a, segs);
     const Split &split = batch.split;
     if ((int32_t)blockIdx.x >= split.ctas) return;
     uint32_t *const arrived = (uint32_t *)a.scratch;

@@ -68,7 +68,7 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
     wait_for_earlier();
     OpenSegment *const open = (OpenSegment *)a.scratch;
     uint8_t *const parts = a.scratch + kScratchCounters * sizeof(uint32_t);
-    const Batch<TOK, kLatentWarps, kLatentMinTiles, 0> batch(a, segs);
+    const Batch<TOK, kLatentWarps, kLatentMinTiles, 0, 0> batch(a, segs);
     if (threadIdx.x == 0) {
         if ((int32_t)blockIdx.x >= batch.split.ctas) open[blockIdx.x].pieces = 0;
         s_timeout = 0;

@@ -196,7 +196,7 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
     wait_for_earlier();
     OpenSegment *const open = (OpenSegment *)a.scratch;
     uint8_t *const parts = a.scratch + kScratchCounters * sizeof(uint32_t);
-    const Batch<S::TILE, kTensorThreads / 32, 1, S::SWITCH> batch(a, segs);
+    const Batch<S::TILE, kTensorThreads / 32, 1, S::SWITCH, 0> batch(a, segs);
     const bool works = (int32_t)blockIdx.x < batch.split.ctas;
     const int64_t c_begin = works ? batch.split.begin(blockIdx.x) : 0, c_end = works ? batch.split.begin(blockIdx.x + 1) : 0;
     int64_t x0 = c_begin;
