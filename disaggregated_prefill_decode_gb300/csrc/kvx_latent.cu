@@ -16,7 +16,7 @@
 // quarters of the banks, and the keys' reads take rows two apart. Two CTAs per SM fill each other's waits.
 //
 // Measured with 16 query heads: 64 requests of 8000 bf16 latents of 576 144 us, 4.1 TB/s, and 64 sessions of
-// 2048 to 32768 8-bit ones 212 us, where the tcgen05 kernel takes 107 and 116. Bound by instruction issue (1.9 a
+// 2048 to 32768 8-bit ones 212 us, where the tcgen05 kernel takes 107 and 115. Bound by instruction issue (1.9 a
 // clock, 95 warp instructions a position). Scores by 8-bit warp products (mma.sync e4m3, queries as two
 // codes) were exact enough but took 395 us: the form costs ten instructions on sm_103a.
 #include "kvx_latent.cuh"

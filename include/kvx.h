@@ -593,8 +593,8 @@ kvx_status kvx_cache_append(kvx_cache_t cache, int32_t layer, const void *k, int
  * seq_len beyond max_blocks * block_size is cut there, a negative one counts as 0, and positions in a
  * block outside the pool are left out; kvx_cache_status reports each of these. KVX_EUNSUPPORTED for
  * latents with v_dim above 512 or outside device memory. Unused slots may hold
- * anything, NaN too. Products are taken in 16 bits with 32-bit sums; two calls on the same inputs give the
- * same bits.
+ * anything, NaN too. Products are of 16-bit values, or of 8-bit codes that add up to 12 bits and more, with
+ * 32-bit sums; two calls on the same inputs give the same bits.
  */
 kvx_status kvx_cache_attend(kvx_cache_t cache, int32_t layer, const void *q, int64_t q_stride,
                             const int32_t *block_table, int64_t table_stride, int32_t max_blocks,
