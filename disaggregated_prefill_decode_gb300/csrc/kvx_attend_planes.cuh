@@ -17,7 +17,7 @@
 // rows to do.
 //
 // What it measured on GB300 (8 KV heads of 128, 8 queries each, bf16): 256 requests of 4608 positions 728
-// us, 6.6 TB/s, 0.98 of the copy rate; 16 requests of 1024 to 8192 55.8 us, of which 45 are the stream at
+// us, 6.6 TB/s, 0.98 of the copy rate; 16 requests of 1024 to 8192 56.5 us, of which 45 are the stream at
 // 0.99 of it. Steps on the way: keys and values straight from global memory into registers 125 us (128
 // registers a thread were too few: spills); through rings that each lane filled for itself, 64 bytes of a
 // row an instruction, 75 (256 requests: 953); whole 128-byte lines and this swizzle 61 (745): the requests
