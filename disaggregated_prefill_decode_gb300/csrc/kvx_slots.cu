@@ -60,7 +60,7 @@ __device__ __forceinline__ int last_at_most(const int64_t *off, int n, int64_t x
     return lo;
 }
 
-// The same by a whole warp, n up to 1024.
+// The same by a whole warp, n up to 1024. x below off[0] has no answer: the ballot would be empty and the search leave the array.
 __device__ __forceinline__ int warp_last_at_most(const int64_t *off, int n, int64_t x) {
     const int lane = threadIdx.x & 31, step = (n + 31) / 32;
     const int lo = (31 - __clz(__ballot_sync(~0u, lane * step < n && off[min(lane * step, n - 1)] <= x))) * step;
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kSlotThreads) kvx_slot_map_kernel(const SlotAr
         const int64_t t_end = min(base.tok + total.tok, a.max_tokens);
         const int lane = threadIdx.x & 31, warps = gridDim.x * (kSlotThreads / 32);
         for (int64_t tile = first_tile(base.tok / kTokTile, (int64_t)(threadIdx.x >> 5) * gridDim.x + blockIdx.x, warps);
-             tile * kTokTile < t_end; tile += warps) {
+             max(tile * kTokTile, base.tok) < t_end; tile += warps) {                 // a pass may add no token, or none below max_tokens
             const int64_t first = tile * kTokTile, from = max(first, base.tok), upto = min(first + kTokTile, t_end);
             const int r_lo = warp_last_at_most(s_tok, m, from - base.tok), r_hi = warp_last_at_most(s_tok, m, upto - 1 - base.tok);
             if (pairs && r_lo == r_hi && from == first && upto == first + kTokTile) {

@@ -108,6 +108,23 @@ def test_slot_map_out_of_range():
     assert check_slot_map(ctx, new, 16, np.arange(1000, 2000, dtype=np.int32), hole, width, total + 90) == kvx.KVX_ERANGE
 
 
+@pytest.mark.parametrize("n,max_tokens", [(1025, 1000), (2048, 1000), (2049, 1000), (3000, 1000), (1025, 999), (2100, 900), (1024, 999),
+                                          (1025, 0), (2100, 1255)])
+def test_slot_map_passes_without_tokens(n, max_tokens):
+    """1000 tokens, no multiple of a tile's, in the first 1024 requests; those after them, other passes of the kernel, idle or
+    with all their tokens beyond max_tokens."""
+    ctx, new = np.arange(n, dtype=np.int32) % 23, np.zeros(n, np.int32)
+    new[:1000] = 1
+    if max_tokens < 1000:
+        new[1024:] = 2
+    table = np.full((n, 4), -1, np.int32)
+    had = -(-ctx // 8)
+    table[np.arange(4) < had[:, None]] = np.arange(had.sum())
+    free = (int(had.sum()) + np.arange(n)).astype(np.int32)
+    status = check_slot_map(ctx, new, 8, free, table, 4, max_tokens)
+    assert status == (kvx.KVX_ERANGE if new.sum() > max_tokens else kvx.KVX_OK)
+
+
 # ------------------------------------------------------------------------------------------------
 # append
 # ------------------------------------------------------------------------------------------------
