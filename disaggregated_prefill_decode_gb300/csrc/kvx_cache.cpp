@@ -318,8 +318,19 @@ kvx_status kvx_cache_attend(kvx_cache_t c, int32_t layer, const void *q, int64_t
     a.map_col = hnd ? 0 : (uint32_t)g.head_bytes();
     a.scratch = c->dev + 256;
     a.device = c->device;
+    a.stall = c->stall;
+    a.wait_ns = a.stall ? kCacheStallWaitNs : kCacheWaitNs;
+    c->stall = 0;
     const cudaError_t e = launch_attend(a, f.value_type, f.io_type, c->sms, stream);
     return e == cudaSuccess ? KVX_OK : cuda_fail(e, "launching the attention");
+}
+
+kvx_status kvx_cache_inject_stall(kvx_cache_t c, int32_t part) {
+    if (!c) return fail(KVX_EINVAL, "cache is NULL");
+    if (part < kStallScores || part > kStallCopies) return fail(KVX_EINVAL, "part %d not in [1, 4]", part);
+    if (c->g.n_planes != 1) return fail(KVX_EUNSUPPORTED, "the stall hook is for caches of latents");
+    c->stall = part;
+    return KVX_OK;
 }
 
 kvx_status kvx_cache_status(kvx_cache_t c, cudaStream_t stream) {

@@ -232,7 +232,13 @@ struct AttendArgs {
     uint32_t map_block, map_head, map_col;   // block begins at
     uint8_t *scratch;                 // of the handle: counters (zero between calls), partial results
     int32_t device;
+    int32_t stall;                    // latents, testing hook (kvx_cache_inject_stall): CTA 0's part that never goes on, 0: none
+    uint64_t wait_ns;                 // latents: limit of a wait for a copy or a product
 };
+// Limit of one such wait, far beyond any copy or product of a tile; and that of a call that kvx_cache_inject_stall prepared.
+constexpr uint64_t kCacheWaitNs = 2000000000ull;       // 2 s
+constexpr uint64_t kCacheStallWaitNs = 1000000ull;     // 1 ms
+enum { kStallScores = 1, kStallSums, kStallSoftmax, kStallCopies };
 constexpr int32_t kScratchCounters = 4096;
 constexpr int32_t kScratchPerSm = 84 << 10;
 cudaError_t launch_attend(const AttendArgs &a, int32_t value_type, int32_t io_type, int32_t sms, cudaStream_t stream);
@@ -256,6 +262,7 @@ struct kvx_cache_s {
     bool outside_device = false;               // a buffer is not device memory
     std::vector<kvx::RowMaps> row_maps;        // latents: per buffer, or none (kvx_cache.cpp, encode_rows)
     int32_t map_run = 0;                       // rows of a run: the common divisor of the block size and a tile
+    int32_t stall = 0;                         // kvx_cache_inject_stall: part of the next attend
     uint8_t *dev = nullptr;                    // [256 bytes: skipped][scratch of the attend kernels]
 };
 

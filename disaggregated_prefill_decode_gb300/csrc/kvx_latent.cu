@@ -52,7 +52,7 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
     constexpr int TOK = S::TOK;
     using Line = Place<TOK, 0>;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint64_t s_full[2];
+    __shared__ uint64_t s_full[2], s_never;
     __shared__ __align__(8) uint8_t s_live[2][kLatentWarps];       // live positions of a stage's tile, a warp's rows each
     __shared__ Line s_cur, s_far;                            // this tile, and the next one to look up
     __shared__ float s_old[kLatentHeads], s_m[kLatentHeads], s_l[kLatentHeads], s_up[kLatentHeads];
@@ -73,6 +73,7 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
         if ((int32_t)blockIdx.x >= batch.split.ctas) open[blockIdx.x].pieces = 0;
         s_timeout = 0;
         for (int i = 0; i < 2; ++i) asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_addr(&s_full[i])), "n"(kLatentWarps) : "memory");
+        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_addr(&s_never)) : "memory");
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if ((int32_t)blockIdx.x >= batch.split.ctas) return;
@@ -208,7 +209,7 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
     for (int32_t k = 0; k < n_tiles; ++k) {
         const int stage = k & 1;
         const uint32_t rows = shared_addr(smem + stage * S::STAGE);
-        if (!wait_full(&s_full[stage], k >> 1 & 1)) s_timeout = 1;
+        if (!wait_full(a.stall && blockIdx.x == 0 ? &s_never : &s_full[stage], a.stall && blockIdx.x == 0 ? 0 : k >> 1 & 1, a.wait_ns)) s_timeout = 1;
 
         // scores: rows g and g + 8 of a product are positions whose low two bits are swapped
         float s[S::MPW][2][4];
@@ -251,7 +252,8 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
                 }
         __syncthreads();
         if (s_timeout) {
-            if (k + 1 < n_tiles) wait_full(&s_full[stage ^ 1], k + 1 >> 1 & 1);   // its copies may be under way
+            for (int i = 0; i < 2; ++i)                            // no copy outlives the CTA: this tile's, and the next one's
+                if (k + i < n_tiles) wait_full(&s_full[stage ^ i], k + i >> 1 & 1, kCacheWaitNs);
             break;
         }
         if (k > 0 && k + 3 < n_tiles) advance(s_far);

@@ -8,7 +8,6 @@ namespace kvx {
 constexpr int kLatentHeads = 16;                                                       // query heads at a time
 constexpr int kLatentFloat4 = kLatentHeads * kCacheMaxLatentValue / 4;                 // of a partial result
 constexpr int kLatentPartial = kLatentFloat4 * 16 + 2 * kLatentHeads * 4;              // O, m, l
-constexpr uint64_t kLatentWaitNs = 2000000000ull;
 
 // Place of value element d of query head h in a partial result: float4s as kvx_latent.cu's lanes hold them.
 __device__ __forceinline__ int partial_at(int d, int h) {
@@ -17,8 +16,8 @@ __device__ __forceinline__ int partial_at(int d, int h) {
 
 __device__ __forceinline__ uint32_t shared_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-// Waits for a phase of a stage's barrier, kLatentWaitNs at most.
-__device__ __forceinline__ bool wait_full(uint64_t *bar, uint32_t parity) {
+// Waits for a phase of a stage's barrier, limit_ns at most. What has to end before a CTA does is waited for with kCacheWaitNs.
+__device__ __forceinline__ bool wait_full(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
     uint64_t t0 = 0;
     for (uint32_t tries = 0;; ++tries) {
         uint32_t done;
@@ -29,7 +28,7 @@ __device__ __forceinline__ bool wait_full(uint64_t *bar, uint32_t parity) {
             uint64_t now;
             asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
             if (!t0) t0 = now;
-            else if (now - t0 > kLatentWaitNs) return false;
+            else if (now - t0 > limit_ns) return false;
         }
     }
 }

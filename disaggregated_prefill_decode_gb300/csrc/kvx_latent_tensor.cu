@@ -163,7 +163,7 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
     using Line = Place<S::TILE, S::SWITCH>;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ __align__(8) uint64_t s_full[2][kChunks], s_free[2][kChunks];           // chunk by chunk
-    __shared__ __align__(8) uint64_t s_scored[2], s_weighed[2], s_read, s_queried, s_drained[2];
+    __shared__ __align__(8) uint64_t s_scored[2], s_weighed[2], s_read, s_queried, s_drained[2], s_never;
     __shared__ uint8_t s_live[3][32];                              // live positions, four a byte
     __shared__ __align__(16) float s_red[4][S::HEADS], s_scale[2][S::HEADS], s_old[S::HEADS], s_m[S::HEADS], s_l[S::HEADS], s_inverse[S::HEADS];
     __shared__ uint32_t s_tmem;
@@ -182,6 +182,7 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_addr(&s_drained[i])) : "memory");
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_addr(&s_weighed[i])), "n"(kSoftThreads) : "memory");
         }
+        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_addr(&s_never)) : "memory");
         asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_addr(&s_read)), "n"(kSoftThreads) : "memory");
         asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_addr(&s_queried)), "n"(kSoftThreads) : "memory");
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -209,10 +210,13 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
     // meet at barriers, go through their tiles without waiting any more.
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (s_failed) return false;
-        if (wait_full(bar, parity & 1)) return true;
+        if (wait_full(bar, parity & 1, a.wait_ns)) return true;
         s_failed = 1;
         return false;
     };
+    // Whether a part goes on: it does, but where the testing hook has it wait for what never comes.
+    auto goes_on = [&](int part) { return a.stall != part || blockIdx.x != 0 || wait(&s_never, 0); };
+    int issued = 0;                                                // copying warps: tiles
     OpenSegment opened = {0, 0, 0, 0};
 
     if (x0 >= c_end) {
@@ -224,7 +228,7 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
         Line at = begin;
         int64_t x = x0;
         int switches = 0;
-        bool ok = true, first = true;
+        bool ok = __all_sync(~0u, goes_on(kStallScores)), first = true;
         for (int j = 0; ok && x < c_end; ++j) {
             const uint64_t stage = (j & 1) * (S::STAGE / 16);
             const uint32_t d = tmem + kColScores + (S::SBUFS == 2 ? (j & 1) * 64 : 0);
@@ -247,18 +251,15 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
             at.next(a, segs, x);
             first = at.tile == 0;
         }
-        if (!ok) {                                                 // no product outlives the CTA
-            tensor_commit(&s_drained[0]);
-            wait_full(&s_drained[0], 0);
-        }
     } else if (w == 9) {                                           // products of the sums
         const uint32_t smem0 = shared_addr(smem);
         const uint64_t values = operand(smem0, F8 ? 16 : S::SUB, 1024, 2), weights = operand(smem0 + S::OFF_WEIGHT, 128, S::TILE * 16, 0);
         Line at = begin;
         int64_t x = x0;
-        bool ok = true, first = true;
+        bool first = true;
+        if (!__all_sync(~0u, goes_on(kStallSums))) x = c_end;
         for (int j = 0; x < c_end; ++j) {
-            if (!(ok = __all_sync(~0u, wait(&s_weighed[j & 1], j >> 1)))) break;
+            if (!__all_sync(~0u, wait(&s_weighed[j & 1], j >> 1))) break;
             tensor_fence_after();
             const uint64_t v = values + (j & 1) * (S::STAGE / 16), p = weights + (j & 1) * (S::WEIGHT / 16);
 #pragma unroll
@@ -271,10 +272,6 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
             }
             at.next(a, segs, x);
             first = at.tile == 0;
-        }
-        if (!ok) {
-            tensor_commit(&s_drained[1]);
-            wait_full(&s_drained[1], 0);
         }
     } else if (w < 8) {                                            // softmax and outputs
         // A thread has a position and MINE query heads of the scores, an element and HALF of the outputs. The scores of a
@@ -362,6 +359,7 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
         };
         Line at = begin;
         int64_t x = x0;
+        goes_on(kStallSoftmax);
         query(at, 0);
         begin_segment();
         bool first = true, begun = at.seg_begin(segs) >= c_begin;  // the segment's first tile here; it begins in this CTA
@@ -616,7 +614,7 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
         const uint32_t wide = narrow ? 64 : 128, subs = c < 4 ? S::SUBS : 1, bytes = wide * subs * S::TILE;
         Line at = begin;
         int64_t x = x0;
-        int issued = 0;
+        if (c == 0 && !__all_sync(~0u, goes_on(kStallCopies))) x = c_end;
         Rows rows = look_up(at);
         for (; x < c_end; ++issued) {
             const int j = issued;
@@ -646,11 +644,18 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
             at.next(a, segs, x);
             if (x < c_end) rows = look_up(at);                     // while this one is under way
         }
-        if (__any_sync(~0u, s_failed))                             // no copy outlives the CTA
-            for (int j = max(0, issued - 2); j < issued; ++j) wait_full(&s_full[j & 1][c], j >> 1 & 1);
     }
     tensor_fence_before();
     __syncthreads();
+    if (s_failed) {                                                // no copy or product outlives the CTA, whoever's wait ran out
+        if (w == 8 || w == 9) {
+            tensor_commit(&s_drained[w - 8]);
+            wait_full(&s_drained[w - 8], 0, kCacheWaitNs);
+        } else if (w > 9)
+            for (int j = max(0, issued - 2); j < issued; ++j) wait_full(&s_full[j & 1][w - 10], j >> 1 & 1, kCacheWaitNs);
+        tensor_fence_before();
+        __syncthreads();
+    }
     if (w == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
     if (threadIdx.x == 0) {
         if (s_failed) atomicAdd(a.pool.skipped + 1, 1ull);

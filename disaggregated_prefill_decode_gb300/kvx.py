@@ -138,6 +138,7 @@ _sig = {
     "kvx_cache_append": (c_i32, [c_vp, c_i32, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp]),
     "kvx_cache_attend": (c_i32, [c_vp, c_i32, c_vp, c_i64, c_vp, c_i64, c_i32, c_vp, c_i32, c_vp, c_i64, c_vp, c_vp]),
     "kvx_cache_status": (c_i32, [c_vp, c_vp]),
+    "kvx_cache_inject_stall": (c_i32, [c_vp, c_i32]),
     "kvx_conn_create": (c_i32, [_P(kvx_conn_config), _P(c_vp)]),
     "kvx_conn_destroy": (c_i32, [c_vp]),
     "kvx_conn_register": (c_i32, [c_vp, c_i64, c_i32, _P(c_i32), c_i32, c_i64]),
@@ -531,6 +532,10 @@ def kvx_cache_status(cache: Cache, stream=None) -> int:
     if st not in (KVX_OK, KVX_ERANGE):
         raise KvxError(st, "kvx_cache_status")
     return st
+
+
+def kvx_cache_inject_stall(cache: Cache, part: int) -> None:
+    _check(_lib.kvx_cache_inject_stall(cache.handle, part), "kvx_cache_inject_stall")
 
 
 # ---------------------------------------------------------------------------------------------

@@ -606,6 +606,13 @@ kvx_status kvx_cache_attend(kvx_cache_t cache, int32_t layer, const void *q, int
  * memory did not arrive within 2 s (the outputs are then not valid), else KVX_OK. */
 kvx_status kvx_cache_status(kvx_cache_t cache, cudaStream_t stream);
 
+/* Testing hook for the bounded waits of the attention over latents: in the handle's next attend every wait is limited to 1 ms
+ * instead of 2 s, and one part of the first CTA (1 the products of the scores, 2 those of the sums, 3 the softmax, 4 the first
+ * copying warp; in the kernel of warp products any of them is the one wait that it has) first waits for a barrier that nothing
+ * arrives at: a wait that can only run out. The CTA then waits for its copies and products in flight and returns, the others
+ * finish, nothing faults, and kvx_cache_status reports KVX_ETIMEDOUT. KVX_EUNSUPPORTED for caches with two planes. */
+kvx_status kvx_cache_inject_stall(kvx_cache_t cache, int32_t part);
+
 /* ------------------------------------------------------------------------------------------------
  * Connector state machine (host only; no CUDA call, usable without a GPU).
  *

@@ -131,3 +131,12 @@ SLOTS = dict(ctx_len=1 << 20, new_len=1 << 21, n_reqs=3, block_size=16, free_blo
                                     dict(block_table=(1 << 23) + 2)])
 def test_slot_map_refusals(change):
     refused(kvx.kvx_slot_map, kvx.KVX_EINVAL, **dict(SLOTS, **change))
+
+
+def test_stall_hook_refusals():
+    with kvx.kvx_cache_create(pool(GEOM), value_type=kvx.KVX_BF16) as c:
+        refused(kvx.kvx_cache_inject_stall, kvx.KVX_EUNSUPPORTED, c, 1)
+    with kvx.kvx_cache_create(pool(LATENT), value_type=kvx.KVX_E4M3, v_dim=512) as c:
+        refused(kvx.kvx_cache_inject_stall, kvx.KVX_EINVAL, c, 0)
+        refused(kvx.kvx_cache_inject_stall, kvx.KVX_EINVAL, c, 5)
+    refused(kvx.kvx_cache_inject_stall, kvx.KVX_EINVAL, c, 1)
