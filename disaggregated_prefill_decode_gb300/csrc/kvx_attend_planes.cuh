@@ -39,9 +39,6 @@ template <int VT_, int IO_, int D_, int NT_, bool FULL_> struct Shape {
     static constexpr bool FULL = FULL_;                           // head_dim is D
     static constexpr bool F8 = VT == KVX_E4M3;
     static constexpr int MT = F8 ? KVX_F16 : VT;                  // type of the products
-    // 8-bit caches with bf16 outputs: f16 weights, whose unit is an eighth of the outputs', suffice. Else a weight is the sum
-    // of two 16-bit values, so that its rounding does not add to the outputs'.
-    static constexpr bool SPLIT = !(F8 && IO == KVX_BF16);
     static constexpr int ESZ = F8 ? 1 : 2;
     static constexpr int TOK = D * ESZ <= 128 ? 32 : 16;          // positions of a tile
     static constexpr int SUB = TOK / 16;
@@ -449,7 +446,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
                     }
                 }
             }
-            uint32_t p_hi[NT][S::SUB][2], p_lo[NT][S::SUB][2];
+            uint32_t p_hi[NT][S::SUB][2], p_lo[NT][S::SUB][2];     // a weight is the sum of two 16-bit values: 2^-17 of it is left, or 2^-23
             if (__any_sync(~0u, lane < TOK && rows[0] == kNoRow)) {
 #pragma unroll
                 for (int u = 0; u < S::SUB; ++u)
@@ -499,10 +496,8 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
                         const float p0 = s[n][u][2 * h], p1 = s[n][u][2 * h + 1];
                         const uint32_t hi = pack<S::MT>(p0, p1);
                         p_hi[n][u][h] = transpose8x8(hi);
-                        if constexpr (S::SPLIT) {
-                            const float2 f = unpack<S::MT>(hi);
-                            p_lo[n][u][h] = transpose8x8(pack<S::MT>(p0 - f.x, p1 - f.y));
-                        }
+                        const float2 f = unpack<S::MT>(hi);
+                        p_lo[n][u][h] = transpose8x8(pack<S::MT>(p0 - f.x, p1 - f.y));
                     }
             }
 #pragma unroll
@@ -529,8 +524,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             mma<S::MT>(o[n][c * (S::PE / 2) + e], av[0], av[1], av[2], av[3], p_hi[n][u][0], p_hi[n][u][1]);
-                            if constexpr (S::SPLIT)
-                                mma<S::MT>(o[n][c * (S::PE / 2) + e], av[0], av[1], av[2], av[3], p_lo[n][u][0], p_lo[n][u][1]);
+                            mma<S::MT>(o[n][c * (S::PE / 2) + e], av[0], av[1], av[2], av[3], p_lo[n][u][0], p_lo[n][u][1]);
                         }
                     }
                 }

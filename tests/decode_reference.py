@@ -69,3 +69,48 @@ def attend_bounds(out, lse, weight, spread, floor, d, n, io, p_unit):
     bound_out = UNIT[io] * (np.abs(out) + rel * weight) + rel * weight + 2.0 ** -25 * floor * (1 if p_unit else 0) + 2.0 ** -24
     bound_lse = score + (n + 64) * 2.0 ** -24 + np.abs(np.where(np.isfinite(lse), lse, 0)) * 2.0 ** -22
     return bound_out, bound_lse
+
+
+# ------------------------------------------------------------------------------------------------
+# bounds for weights held in parts
+# ------------------------------------------------------------------------------------------------
+
+# What the parts of a weight leave of it, at most: relative to the weight, and (small ones) relative to the row's largest.
+#   bf16, two values: the second takes what truncation left, below 2^-7, and is half a unit of its own off: 2^-16. No floor.
+#   f16, two values: below 2^-10, then half a unit: 2^-22. The second's smallest step is 2^-24 of weights taken times 2^15
+#     (2^12 on the tensor pipe), and may be a whole step off: 2^-39 (2^-36).
+#   e4m3, N codes 2^5 apart: each leaves 2^-4 of the power of two below what it stands for, 2^-4-5(N-1) in all; the last
+#     one's smallest step is 2^-9 of weights taken times 2^5, half of it 2^-10-5N.
+PARTS = {"bf16": (2.0 ** -16, 0.0), "f16": (2.0 ** -22, 2.0 ** -39), "f16 tensor": (2.0 ** -22, 2.0 ** -36),
+         "3 codes": (2.0 ** -14, 2.0 ** -25), "4 codes": (2.0 ** -19, 2.0 ** -30)}
+SMALLEST = {"bf16": 2.0 ** -134, "f16": 2.0 ** -25}                       # half an output's smallest step
+
+
+def parts_bounds(out, lse, weight, spread, floor, d, n, io, parts):
+    """As attend_bounds, for weights that are held in parts."""
+    unit, step = PARTS[parts]
+    score = (d + 8) * 2.0 ** -24 * spread + 2.0 ** -20
+    rel = 2 * score[:, None] + unit + (n + 64) * 2.0 ** -24
+    err = rel * weight + step * floor
+    return UNIT[io] * (np.abs(out) + err) + err + SMALLEST[io], score + (n + 64) * 2.0 ** -24 + np.abs(lse) * 2.0 ** -22
+
+
+def paired_values(rng, n, heads, dim, spread):
+    """Keys of nearly equal scores and values in pairs of opposite sign: outputs are small differences of large sums, so that
+    a weight's rounding shows beside the output's. keys, values [n][heads][dim]."""
+    k = rng.standard_normal((n, heads, dim)) * spread
+    half = rng.standard_normal(((n + 1) // 2, heads, dim))
+    return k, np.stack([half, -half], 1).reshape(-1, heads, dim)[:n]
+
+
+def one_large_score(rng, n, heads, dim, gap, scale, q0, size):
+    """One position whose score is `gap` above the others' and whose value is nearly nothing, as the first token's often is.
+    The gap comes from element 0 of the queries, q0. keys, values [n][heads][dim]."""
+    k = rng.standard_normal((n, heads, dim)) * 0.5
+    v = (np.abs(rng.standard_normal((n, heads, dim))) + 0.5) * size
+    at = n // 3
+    k[:, :, 0] = 0
+    k[at] = 0
+    k[at, :, 0] = gap / (q0 * scale)
+    v[at] = 0
+    return k, v

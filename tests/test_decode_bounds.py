@@ -1,0 +1,89 @@
+"""The bounds of tests/decode_reference.py for weights held in parts can tell them from weights that lost a part: the same
+attention in 64 bits with its weights rounded as one or several 16- or 8-bit values, on the inputs that the GPU tests use."""
+import numpy as np
+import pytest
+
+import decode_reference as ref
+
+torch = pytest.importorskip("torch")
+
+TYPE = {"bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def rounded(x, dtype):
+    return torch.from_numpy(x).float().to(dtype).double().numpy()
+
+
+def two_parts(p, kind, parts=2):
+    up = {"bf16": 1.0, "f16": 2.0 ** 15, "f16 tensor": 2.0 ** 12}[kind]
+    t = TYPE[kind.split()[0]]
+    hi = rounded(p * up, t)
+    return (hi + (rounded(p * up - hi, t) if parts == 2 else 0)) / up
+
+
+def codes(p, n):
+    total, left, at = 0.0, p * 32, 32.0
+    for _ in range(n):
+        c = rounded(left, torch.float8_e4m3fn)
+        total, left, at = total + c / at, (left - c) * 32, at * 32
+    return total
+
+
+def worst(q, k, v, scale, io, parts, hold):
+    """Largest |error| / bound of the attention with weights as `hold` makes them."""
+    o, l, weight, spread, floor = ref.attend(q, k, v, scale)
+    b, _ = ref.parts_bounds(o, l, weight, spread, floor, q.shape[1], len(k), io, parts)
+    s = q @ k.T * scale
+    p = np.exp(s - s.max(1, keepdims=True))
+    got = rounded(hold(p) @ v / p.sum(1, keepdims=True), TYPE[io])
+    return (np.abs(got - o) / b).max()
+
+
+def paired(spread, n=6):
+    rng = np.random.default_rng(3)
+    k, v = ref.paired_values(rng, n, 1, 64, spread)
+    return rng.standard_normal((16, 64)), k[:, 0], v[:, 0]
+
+
+@pytest.mark.parametrize("spread", [0.3, 0.02, 0.002])
+@pytest.mark.parametrize("io,kind", [("bf16", "bf16"), ("f16", "f16"), ("bf16", "f16"), ("f16", "f16 tensor")])
+def test_a_lost_second_part_shows(io, kind, spread):
+    q, k, v = paired(spread)
+    assert worst(q, k, v, 0.125, io, kind, lambda p: two_parts(p, kind)) <= 1
+    if spread < 0.1 or kind == io:
+        assert worst(q, k, v, 0.125, io, kind, lambda p: two_parts(p, kind, 1)) > 1
+
+
+@pytest.mark.parametrize("n,io", [(3, "bf16"), (3, "f16")])
+def test_a_lost_code_shows(n, io):
+    """A fourth one of nearly equal weights would not: 2^-14 is beside the output's own rounding."""
+    q, k, v = paired(0.002)
+    assert worst(q, k, v, 0.125, io, f"{n} codes", lambda p: codes(p, n)) <= 1
+    assert worst(q, k, v, 0.125, io, f"{n} codes", lambda p: codes(p, n - 1)) > 1
+
+
+@pytest.mark.parametrize("gap", [16, 18, 24])
+@pytest.mark.parametrize("io,kind", [("f16", "f16"), ("bf16", "f16"), ("f16", "f16 tensor"), ("bf16", "bf16")])
+def test_lost_small_weights_show(io, kind, gap):
+    """Weights far below the largest one: as f16 values that are not brought up first, they are lost."""
+    rng = np.random.default_rng(4)
+    k, v = ref.one_large_score(rng, 8193, 1, 64, gap, 0.125, 8.0, 1000.0)
+    q = rng.standard_normal((4, 64))
+    q[:, 0] = 8.0
+    args = q, k[:, 0], v[:, 0], 0.125, io, kind
+    assert worst(*args, lambda p: two_parts(p, kind)) <= 1
+    if kind != "bf16" and gap > 16:
+        assert worst(*args, lambda p: rounded(p, torch.float16)) > 1
+
+
+@pytest.mark.parametrize("n", [3, 4])
+def test_lost_small_weights_of_codes_show(n):
+    """Four codes hold weights of 2^-26, three are at their end there, as the bound says."""
+    rng = np.random.default_rng(4)
+    k, v = ref.one_large_score(rng, 8193, 1, 64, 18, 0.125, 8.0, 1.0)
+    q = rng.standard_normal((4, 64))
+    q[:, 0] = 8.0
+    args = q, k[:, 0], v[:, 0], 0.125, "bf16"
+    assert worst(*args, f"{n} codes", lambda p: codes(p, n)) <= 1
+    if n == 4:
+        assert worst(*args, f"{n} codes", lambda p: codes(p, n - 1)) > 1

@@ -1,0 +1,98 @@
+"""Precision of the attention's weights: inputs on which a weight's rounding, or the loss of small weights, shows beside the
+output's own rounding, against the 64-bit statement within the bounds of weights held in parts (tests/decode_reference.py)."""
+import numpy as np
+import pytest
+
+import decode_reference as ref
+from test_decode_gpu import HND, NHD, TYPES, Attend, kvx, torch, typed
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    yield
+    torch.cuda.synchronize()
+
+
+class Filled(Attend):
+    """An Attend whose keys and values come from fill(n) -> (keys, values), [n][heads][dim]; of latents the values are the
+    first v_dim elements, the keys those after them, and the queries see the keys alone."""
+
+    def __init__(self, lens, fill, q0=0.0, **kw):
+        super().__init__(lens, **kw)
+        scales = (kw.get("k_scale", 0.03), kw.get("v_scale", 0.05) if len(self.host) == 2 else kw.get("k_scale", 0.03))
+        vt, vdtype, esz = TYPES[self.value]
+        for r, n in enumerate(lens):
+            if not n:
+                continue
+            rows = ref.rows_of(self.table[r], np.arange(n), self.bs, self.geom.n_blocks)
+            k, v = fill(n)
+            planes = (k, v)
+            if len(self.host) == 1:
+                planes = (np.concatenate([v, k], 2),)
+            for p, x in enumerate(planes):
+                x = torch.from_numpy(x).float()
+                scale = scales[p] if self.value == "e4m3" else 1.0
+                x = (x / scale).clamp(-448, 448).to(vdtype) if self.value == "e4m3" else x.to(vdtype)
+                self.host[p][rows] = x.double().numpy() * scale
+                hps = self.geom.heads_per_shard
+                for s in range(self.geom.n_shards):
+                    view = typed(self.bufs[p * self.geom.n_shards + s], self.geom, vdtype)
+                    raw = view.view(torch.uint8 if esz == 1 else torch.int16)
+                    part = x[:, s * hps:(s + 1) * hps].contiguous().view(raw.dtype).cuda()
+                    raw[torch.from_numpy(rows // self.bs).cuda(), torch.from_numpy(rows % self.bs).cuda()] = part
+        first = self.v_dim if len(self.host) == 1 else 0
+        self.q[..., :first] = 0
+        if q0:
+            self.q[..., first] = q0
+
+    def check_parts(self, out, lse, parts):
+        out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        for r, n in enumerate(self.lens):
+            rows = ref.rows_of(self.table[r], np.arange(n), self.bs, self.geom.n_blocks)
+            for h in range(self.heads):
+                hs = slice(h * self.group, (h + 1) * self.group)
+                k, v = self.host[0][rows, h], self.host[-1][rows, h, :self.v_dim]
+                o, l, weight, spread, floor = ref.attend(self.q[r, hs].double().numpy(), k, v, self.scale)
+                if n == 0:
+                    assert (out[r, hs] == 0).all() and (lse[r, hs] == -np.inf).all()
+                    continue
+                b_out, b_lse = ref.parts_bounds(o, l, weight, spread, floor, self.dim, n, self.io, parts)
+                off = np.abs(out[r, hs] - o) / b_out
+                assert (off <= 1).all(), (r, h, n, off.max())
+                assert (np.abs(lse[r, hs] - l) <= b_lse).all(), (r, h, n)
+
+
+# value, io, planes, shards, query heads a KV head, head_dim, v_dim, what a weight is held in
+PLANES = [("bf16", None, 2, 1, 4, 64, 0, "bf16"), ("bf16", None, 2, 2, 12, 128, 0, "bf16"), ("f16", None, 2, 1, 4, 64, 0, "f16"),
+          ("f16", None, 2, 1, 12, 128, 0, "f16"), ("f16", None, 2, 1, 2, 192, 0, "f16"), ("e4m3", "f16", 2, 1, 8, 128, 0, "f16"),
+          ("e4m3", "bf16", 2, 1, 8, 128, 0, "f16"), ("e4m3", "bf16", 2, 1, 16, 64, 0, "f16"), ("e4m3", "bf16", 2, 1, 3, 256, 0, "f16")]
+WARPS = [("bf16", None, 1, 2, 16, 576, 512, "bf16"), ("f16", None, 1, 2, 5, 576, 512, "f16"), ("e4m3", "f16", 1, 2, 16, 576, 512, "f16")]
+TENSOR = [("bf16", None, 1, 1, 16, 576, 512, "bf16"), ("bf16", None, 1, 1, 32, 576, 512, "bf16"), ("f16", None, 1, 1, 16, 576, 512, "f16 tensor"),
+          ("f16", None, 1, 1, 24, 576, 512, "f16 tensor")]
+CODES = [("e4m3", "bf16", 1, 1, 16, 576, 512, "3 codes"), ("e4m3", "f16", 1, 1, 7, 576, 512, "3 codes"),
+         ("e4m3", "bf16", 1, 1, 32, 576, 512, "3 codes"), ("e4m3", "f16", 1, 1, 40, 576, 512, "3 codes")]
+CASES = PLANES + WARPS + TENSOR + CODES
+
+
+def run(fill_of, lens, form, q0=0.0, **kw):
+    value, io, planes, shards, group, dim, v_dim, parts = form
+    rng = np.random.default_rng(11)
+    width = dim - v_dim if planes == 1 else dim
+    case = Filled(lens, lambda n: fill_of(rng, n, shards, dim, v_dim or dim, width, planes), q0=q0, value=value, io=io, planes=planes,
+                  shards=shards, hps=1, group=group, dim=dim, v_dim=v_dim, bs=64, layout=HND if shards == 1 else NHD, seed=5, **kw)
+    case.check_parts(*case.run(), parts)
+    assert kvx.kvx_cache_status(case.cache) == kvx.KVX_OK
+    kvx.kvx_cache_destroy(case.cache)
+
+
+@pytest.mark.parametrize("spread", [0.3, 0.02, 0.002])
+@pytest.mark.parametrize("form", CASES)
+def test_weights_of_nearly_equal_scores(form, spread):
+    def fill(rng, n, heads, dim, v_dim, width, planes):
+        k, v = ref.paired_values(rng, n, heads, max(width, v_dim), spread)
+        return k[..., :width], v[..., :v_dim]
+    run(fill, [2, 3, 0, 6, 17, 40], form)
