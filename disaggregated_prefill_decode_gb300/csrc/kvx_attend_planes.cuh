@@ -3,7 +3,7 @@
 //
 // The softmax runs once over the positions with a running maximum m and sum l per query:
 //   m' = max(m, s), l' = l 2^(m - m') + 2^(s - m'), O' = O 2^(m - m') + 2^(s - m') v,
-// scores in units of log2, all of it in 32 bits. Bound by memory: each key and value is used by the queries
+// scores in units of log2, all of it in 32 bits (with f16 products m' = max(m, s - 15): Shape::UP). Bound by memory: each key and value is used by the queries
 // of one KV head only, 2 group flops per element, so all that counts is bytes in flight and what a call
 // costs before its first and after its last byte.
 //
@@ -39,6 +39,9 @@ template <int VT_, int IO_, int D_, int NT_, bool FULL_> struct Shape {
     static constexpr bool FULL = FULL_;                           // head_dim is D
     static constexpr bool F8 = VT == KVX_E4M3;
     static constexpr int MT = F8 ? KVX_F16 : VT;                  // type of the products
+    // f16 weights are taken times 2^15, by a reference m that far below the maximum: one of 2^-39 of the largest still has a
+    // step of f16. Times 1, those below 2^-25 were lost from the outputs (not from the sum), and 2^-14 had no second value.
+    static constexpr float UP = MT == KVX_F16 ? 15.0f : 0.0f;
     static constexpr int ESZ = F8 ? 1 : 2;
     static constexpr int TOK = D * ESZ <= 128 ? 32 : 16;          // positions of a tile
     static constexpr int SUB = TOK / 16;
@@ -466,7 +469,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
                     for (int u = 1; u < S::SUB; ++u) top = fmaxf(top, fmaxf(s[n][u][i], s[n][u][2 + i]));
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-                    top = fmaxf(m[n][i], top * sc[n][i]);
+                    top = fmaxf(m[n][i], fmaf(top, sc[n][i], -S::UP));
                     const float ref = top == -INFINITY ? 0.0f : top;
                     old[i] = fast_exp2(m[n][i] - ref);
                     m[n][i] = top;

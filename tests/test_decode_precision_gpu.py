@@ -96,3 +96,16 @@ def test_weights_of_nearly_equal_scores(form, spread):
         k, v = ref.paired_values(rng, n, heads, max(width, v_dim), spread)
         return k[..., :width], v[..., :v_dim]
     run(fill, [2, 3, 0, 6, 17, 40], form)
+
+
+@pytest.mark.parametrize("gap", [14, 16, 18, 24])
+@pytest.mark.parametrize("form", PLANES)
+def test_weights_far_below_the_largest(form, gap):
+    """A first position of large score and no value: the output is that of the thousands of small weights beside it."""
+    value, io, planes, shards, group, dim, v_dim, parts = form
+    size = 1000.0 if "f16" in (value, io) else 1.0
+
+    def fill(rng, n, heads, dim, v_dim, width, planes):
+        k, v = ref.one_large_score(rng, n, heads, max(width, v_dim), gap, dim ** -0.5, 8.0, size if planes == 2 or value != "e4m3" else 1.0)
+        return k[..., :width], v[..., :v_dim]
+    run(fill, [8193, 700, 1], form, q0=8.0, k_scale=0.25, v_scale=0.05 * size)
