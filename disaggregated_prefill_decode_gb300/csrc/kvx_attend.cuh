@@ -44,6 +44,14 @@ template <int VT> __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     return y;
 }
 
+// The same, cut off instead of rounded.
+template <int VT> __device__ __forceinline__ uint32_t pack_down(float lo, float hi) {
+    uint32_t y;
+    if constexpr (VT == KVX_BF16) asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+    else asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+    return y;
+}
+
 template <int VT> __device__ __forceinline__ float2 unpack(uint32_t x) {
     if constexpr (VT == KVX_BF16) return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
     else return __half22float2(*reinterpret_cast<const __half2 *>(&x));

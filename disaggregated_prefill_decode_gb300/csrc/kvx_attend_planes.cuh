@@ -42,6 +42,12 @@ template <int VT_, int IO_, int D_, int NT_, bool FULL_> struct Shape {
     // f16 weights are taken times 2^15, by a reference m that far below the maximum: one of 2^-39 of the largest still has a
     // step of f16. Times 1, those below 2^-25 were lost from the outputs (not from the sum), and 2^-14 had no second value.
     static constexpr float UP = MT == KVX_F16 ? 15.0f : 0.0f;
+    // A weight is the sum of PARTS values of the products' type. An infinite element of V has to meet neither a zero nor a
+    // negative one, which would make it NaN: so with 16-bit planes all but the last are cut off, not rounded, and each is at
+    // least LEAST (or the weight). What is left of a weight: f16 2^-22, or 2^-39 of the largest; bf16 2^-22 (two values: 2^-16,
+    // which showed in the outputs' rounding); 8-bit codes are finite, their weights' values rounded: 2^-23.
+    static constexpr float LEAST = MT == KVX_F16 ? 0x1p-24f : 0x1p-126f;
+    static constexpr int PARTS = MT == KVX_F16 ? 2 : 3;
     static constexpr int ESZ = F8 ? 1 : 2;
     static constexpr int TOK = D * ESZ <= 128 ? 32 : 16;          // positions of a tile
     static constexpr int SUB = TOK / 16;
@@ -204,6 +210,7 @@ template <class S> __device__ __noinline__ Joined<S> join_many(int f, const Piec
                 j.l += mine * s[k];
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
+                    if (x0 + 8 * k + x >= n) break;                // not the last one again: 0 times infinity
                     const float w = __shfl_sync(~0u, mine, x * 4 + t);
                     j.o.x += w * y[k][x].x;
                     j.o.y += w * y[k][x].y;
@@ -449,7 +456,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
                     }
                 }
             }
-            uint32_t p_hi[NT][S::SUB][2], p_lo[NT][S::SUB][2];     // a weight is the sum of two 16-bit values: 2^-17 of it is left, or 2^-23
+            uint32_t parts[S::PARTS][NT][S::SUB][2];
             if (__any_sync(~0u, lane < TOK && rows[0] == kNoRow)) {
 #pragma unroll
                 for (int u = 0; u < S::SUB; ++u)
@@ -496,11 +503,16 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
                 for (int u = 0; u < S::SUB; ++u)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float p0 = s[n][u][2 * h], p1 = s[n][u][2 * h + 1];
-                        const uint32_t hi = pack<S::MT>(p0, p1);
-                        p_hi[n][u][h] = transpose8x8(hi);
-                        const float2 f = unpack<S::MT>(hi);
-                        p_lo[n][u][h] = transpose8x8(pack<S::MT>(p0 - f.x, p1 - f.y));
+                        float p0 = s[n][u][2 * h], p1 = s[n][u][2 * h + 1];
+                        const float least0 = fminf(p0, S::LEAST), least1 = fminf(p1, S::LEAST);
+#pragma unroll
+                        for (int k = 0; k < S::PARTS; ++k) {
+                            const uint32_t x = S::F8 || k + 1 == S::PARTS ? pack<S::MT>(p0, p1) : pack_down<S::MT>(p0, p1);
+                            parts[k][n][u][h] = transpose8x8(x);
+                            const float2 f = unpack<S::MT>(x);
+                            p0 = S::F8 ? p0 - f.x : fmaxf(p0 - f.x, least0);
+                            p1 = S::F8 ? p1 - f.y : fmaxf(p1 - f.y, least1);
+                        }
                     }
             }
 #pragma unroll
@@ -525,10 +537,10 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
                             }
                         }
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            mma<S::MT>(o[n][c * (S::PE / 2) + e], av[0], av[1], av[2], av[3], p_hi[n][u][0], p_hi[n][u][1]);
-                            mma<S::MT>(o[n][c * (S::PE / 2) + e], av[0], av[1], av[2], av[3], p_lo[n][u][0], p_lo[n][u][1]);
-                        }
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int k = 0; k < S::PARTS; ++k)
+                                mma<S::MT>(o[n][c * (S::PE / 2) + e], av[0], av[1], av[2], av[3], parts[k][n][u][0], parts[k][n][u][1]);
                     }
                 }
             const bool ends = cur.tile + 1 == cur.tiles;

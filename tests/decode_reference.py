@@ -77,11 +77,12 @@ def attend_bounds(out, lse, weight, spread, floor, d, n, io, p_unit):
 
 # What the parts of a weight leave of it, at most: relative to the weight, and (small ones) relative to the row's largest.
 #   bf16, two values: the second takes what truncation left, below 2^-7, and is half a unit of its own off: 2^-16. No floor.
+#   bf16, three values: the second is cut off too, 2^-14, and the third is 2^-8 off: 2^-22. No floor.
 #   f16, two values: below 2^-10, then half a unit: 2^-22. The second's smallest step is 2^-24 of weights taken times 2^15
 #     (2^12 on the tensor pipe), and may be a whole step off: 2^-39 (2^-36).
 #   e4m3, N codes 2^5 apart: each leaves 2^-4 of the power of two below what it stands for, 2^-4-5(N-1) in all; the last
 #     one's smallest step is 2^-9 of weights taken times 2^5, half of it 2^-10-5N.
-PARTS = {"bf16": (2.0 ** -16, 0.0), "f16": (2.0 ** -22, 2.0 ** -39), "f16 tensor": (2.0 ** -22, 2.0 ** -36),
+PARTS = {"bf16": (2.0 ** -16, 0.0), "bf16 planes": (2.0 ** -22, 0.0), "f16": (2.0 ** -22, 2.0 ** -39), "f16 tensor": (2.0 ** -22, 2.0 ** -36),
          "3 codes": (2.0 ** -14, 2.0 ** -25), "4 codes": (2.0 ** -19, 2.0 ** -30)}
 SMALLEST = {"bf16": 2.0 ** -134, "f16": 2.0 ** -25}                       # half an output's smallest step
 

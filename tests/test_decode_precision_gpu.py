@@ -67,7 +67,7 @@ class Filled(Attend):
 
 
 # value, io, planes, shards, query heads a KV head, head_dim, v_dim, what a weight is held in
-PLANES = [("bf16", None, 2, 1, 4, 64, 0, "bf16"), ("bf16", None, 2, 2, 12, 128, 0, "bf16"), ("f16", None, 2, 1, 4, 64, 0, "f16"),
+PLANES = [("bf16", None, 2, 1, 4, 64, 0, "bf16 planes"), ("bf16", None, 2, 2, 12, 128, 0, "bf16 planes"), ("f16", None, 2, 1, 4, 64, 0, "f16"),
           ("f16", None, 2, 1, 12, 128, 0, "f16"), ("f16", None, 2, 1, 2, 192, 0, "f16"), ("e4m3", "f16", 2, 1, 8, 128, 0, "f16"),
           ("e4m3", "bf16", 2, 1, 8, 128, 0, "f16"), ("e4m3", "bf16", 2, 1, 16, 64, 0, "f16"), ("e4m3", "bf16", 2, 1, 3, 256, 0, "f16")]
 WARPS = [("bf16", None, 1, 2, 16, 576, 512, "bf16"), ("f16", None, 1, 2, 5, 576, 512, "f16"), ("e4m3", "f16", 1, 2, 16, 576, 512, "f16")]
@@ -109,3 +109,39 @@ def test_weights_far_below_the_largest(form, gap):
         k, v = ref.one_large_score(rng, n, heads, max(width, v_dim), gap, dim ** -0.5, 8.0, size if planes == 2 or value != "e4m3" else 1.0)
         return k[..., :width], v[..., :v_dim]
     run(fill, [8193, 700, 1], form, q0=8.0, k_scale=0.25, v_scale=0.05 * size)
+
+
+def raw_values(case, plane):
+    """The values of a plane of one shard and one head, [row][dim]."""
+    return case.bufs[plane].view(TYPES[case.value][1]).view(-1, case.dim)
+
+
+@pytest.mark.parametrize("value", ["bf16", "f16"])
+@pytest.mark.parametrize("group,dim", [(1, 64), (8, 128), (12, 128), (3, 256)])
+@pytest.mark.parametrize("lens,window", [([1, 40, 9000], 0), ([2, 600, 20011], 300)])
+def test_an_infinite_value_gives_that_infinity(value, group, dim, lens, window):
+    """sum p v with one infinite v is that infinity, in that element alone; with two of opposite sign it is NaN."""
+    case = Attend(lens, value=value, dim=dim, hps=1, group=group, window=window, seed=2)
+    before = case.run()
+    v = raw_values(case, 1)
+    rng = np.random.default_rng(1)
+    for r, n in enumerate(lens):
+        first = max(0, n - window) if window else 0
+        for d in range(0, dim, 2):                                         # every other element, a position of its own
+            v[int(ref.rows_of(case.table[r], np.array([rng.integers(first, n)]), 16, case.geom.n_blocks)[0]), d] = (
+                float("inf") if d % 4 else -float("inf"))
+        at = [first, n - 1]
+        rows = ref.rows_of(case.table[r], np.array(at), 16, case.geom.n_blocks)
+        if n > 1:
+            v[int(rows[0]), 1], v[int(rows[1]), 1] = float("inf"), -float("inf")
+        if first:                                                          # before the window: no matter what
+            rows = ref.rows_of(case.table[r], np.arange(first), 16, case.geom.n_blocks)
+            v[torch.from_numpy(rows).cuda(), 3] = float("nan")
+            v[torch.from_numpy(rows).cuda(), 5] = float("inf")
+    out, lse = case.run()
+    assert torch.equal(lse, before[1])
+    d = torch.arange(0, dim, 2, device="cuda")
+    assert (out[:, :, d] == torch.where(d % 4 == 2, float("inf"), -float("inf"))).all()
+    assert torch.equal(out[:, :, 3::2], before[0][:, :, 3::2])
+    assert torch.isnan(out[1:, :, 1]).all() and torch.equal(out[0, :, 1].isnan(), torch.full((group,), lens[0] > 1, device="cuda"))
+    kvx.kvx_cache_destroy(case.cache)
