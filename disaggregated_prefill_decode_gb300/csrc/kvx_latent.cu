@@ -30,7 +30,10 @@ template <int VT_, int IO_> struct LatentShape {
     static constexpr int VT = VT_, IO = IO_;
     static constexpr bool F8 = VT == KVX_E4M3;
     static constexpr int MT = F8 ? KVX_F16 : VT;
-    static constexpr bool SPLIT = !(F8 && IO == KVX_BF16);        // weights in two 16-bit parts, as in kvx_attend_planes.cuh
+    // A weight is the sum of two 16-bit values: 2^-17 of it is left, f16: 2^-23. f16 weights are taken times 2^15, as in
+    // kvx_attend_planes.cuh, so that those of 2^-39 of the largest still count. (An infinite value is an infinite key too, so
+    // its weight is NaN or 0 by the definition, and the parts' signs do not matter here.)
+    static constexpr float UP = MT == KVX_F16 ? 15.0f : 0.0f;
     static constexpr int ESZ = F8 ? 1 : 2;
     static constexpr int TOK = F8 ? 64 : 32;
     static constexpr int KSTEP = F8 ? 4 : 2;                      // products per 64-byte chunk of a row
@@ -40,7 +43,7 @@ template <int VT_, int IO_> struct LatentShape {
     static constexpr int PITCH = kCacheMaxLatent * ESZ + 32;
     static constexpr int STAGE = TOK * PITCH;
     static constexpr int ROWS = TOK / kLatentWarps;               // copied by a warp
-    static constexpr int PENTRY = SPLIT ? 16 : 8;
+    static constexpr int PENTRY = 16;
     static constexpr int OFF_S = 2 * STAGE, OFF_P = OFF_S + 4 * kLatentHeads * TOK * 4;
     static constexpr int BYTES = OFF_P + TOK / 16 * 2 * 32 * PENTRY;
 };
@@ -292,7 +295,7 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
             for (int e = 1; e < E; ++e) top = fmaxf(top, p[e]);
 #pragma unroll
             for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-            top = fmaxf(m, top * scale);
+            top = fmaxf(m, fmaf(top, scale, -S::UP));
             const float ref = top == -INFINITY ? 0.0f : top, old = fast_exp2(m - ref);
             m = top;
             l *= old;
@@ -307,10 +310,8 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
             for (int e = 0; e < E; e += 2) {
                 const uint32_t hi = pack<S::MT>(p[e], p[e + 1]);
                 *(uint32_t *)(to + e * 2) = hi;
-                if constexpr (S::SPLIT) {
-                    const float2 f = unpack<S::MT>(hi);
-                    *(uint32_t *)(to + 8 + e * 2) = pack<S::MT>(p[e] - f.x, p[e + 1] - f.y);
-                }
+                const float2 f = unpack<S::MT>(hi);
+                *(uint32_t *)(to + 8 + e * 2) = pack<S::MT>(p[e] - f.x, p[e + 1] - f.y);
             }
         }
         __syncthreads();
@@ -361,7 +362,7 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
                         mma<S::MT>(o[e][n], av[0], av[1], av[2], av[3], p[n][0], p[n][1]);
-                        if constexpr (S::SPLIT) mma<S::MT>(o[e][n], av[0], av[1], av[2], av[3], p[n][2], p[n][3]);
+                        mma<S::MT>(o[e][n], av[0], av[1], av[2], av[3], p[n][2], p[n][3]);
                     }
                 }
             }

@@ -70,7 +70,8 @@ class Filled(Attend):
 PLANES = [("bf16", None, 2, 1, 4, 64, 0, "bf16 planes"), ("bf16", None, 2, 2, 12, 128, 0, "bf16 planes"), ("f16", None, 2, 1, 4, 64, 0, "f16"),
           ("f16", None, 2, 1, 12, 128, 0, "f16"), ("f16", None, 2, 1, 2, 192, 0, "f16"), ("e4m3", "f16", 2, 1, 8, 128, 0, "f16"),
           ("e4m3", "bf16", 2, 1, 8, 128, 0, "f16"), ("e4m3", "bf16", 2, 1, 16, 64, 0, "f16"), ("e4m3", "bf16", 2, 1, 3, 256, 0, "f16")]
-WARPS = [("bf16", None, 1, 2, 16, 576, 512, "bf16"), ("f16", None, 1, 2, 5, 576, 512, "f16"), ("e4m3", "f16", 1, 2, 16, 576, 512, "f16")]
+WARPS = [("bf16", None, 1, 2, 16, 576, 512, "bf16"), ("f16", None, 1, 2, 5, 576, 512, "f16"), ("e4m3", "f16", 1, 2, 16, 576, 512, "f16"),
+         ("e4m3", "bf16", 1, 2, 16, 576, 512, "f16")]
 TENSOR = [("bf16", None, 1, 1, 16, 576, 512, "bf16"), ("bf16", None, 1, 1, 32, 576, 512, "bf16"), ("f16", None, 1, 1, 16, 576, 512, "f16 tensor"),
           ("f16", None, 1, 1, 24, 576, 512, "f16 tensor")]
 CODES = [("e4m3", "bf16", 1, 1, 16, 576, 512, "3 codes"), ("e4m3", "f16", 1, 1, 7, 576, 512, "3 codes"),
@@ -99,7 +100,7 @@ def test_weights_of_nearly_equal_scores(form, spread):
 
 
 @pytest.mark.parametrize("gap", [14, 16, 18, 24])
-@pytest.mark.parametrize("form", PLANES)
+@pytest.mark.parametrize("form", PLANES + WARPS)
 def test_weights_far_below_the_largest(form, gap):
     """A first position of large score and no value: the output is that of the thousands of small weights beside it."""
     value, io, planes, shards, group, dim, v_dim, parts = form
