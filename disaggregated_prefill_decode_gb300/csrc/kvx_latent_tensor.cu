@@ -62,7 +62,9 @@ template <int VT_, int IO_, int HEADS_> struct TensorShape {
     static constexpr int SBUFS = QCOLS > 64 ? 1 : 2;              // buffers of scores, 64 columns apart
     static constexpr int QUERY = QCOLS * kCacheMaxLatent * ESZ, WEIGHT = WCOLS * TILE * ESZ;
     static constexpr int OFF_QUERY = 2 * STAGE, OFF_WEIGHT = OFF_QUERY + QUERY, BYTES = OFF_WEIGHT + 2 * WEIGHT;
-    static constexpr float UP = F8 ? 32.0f : 1.0f;                // of the weights: 2^(kSlack + 5) is within the codes' 448
+    // Of the weights, up to 2^kSlack: 2^(3 + 5) is within the codes' 448, 2^(3 + 12) within f16, whose two values then have a
+    // step of 2^-36 (times 1, weights below 2^-25 were lost).
+    static constexpr float UP = F8 ? 32.0f : VT == KVX_F16 ? 4096.0f : 1.0f;
     // Places of the line that a change of segment counts: queries, then outputs. 300 requests of up to 1000 8-bit latents: 16 heads
     // 42.3 us with 1, 39.9 with 2, 39.5 with 3; 32 heads 65.2, 59.8, 57.0; long segments the same.
     static constexpr int SWITCH = HEADS / 16 + 1;

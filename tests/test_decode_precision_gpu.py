@@ -100,7 +100,7 @@ def test_weights_of_nearly_equal_scores(form, spread):
 
 
 @pytest.mark.parametrize("gap", [14, 16, 18, 24])
-@pytest.mark.parametrize("form", PLANES + WARPS)
+@pytest.mark.parametrize("form", PLANES + WARPS + TENSOR)
 def test_weights_far_below_the_largest(form, gap):
     """A first position of large score and no value: the output is that of the thousands of small weights beside it."""
     value, io, planes, shards, group, dim, v_dim, parts = form
