@@ -5,14 +5,18 @@
 // serves twice as operand A: by rows (K-major) for the scores S = K Q^T, 128 positions x the query columns,
 // and by columns (MN-major) for the sums O^T += V^T P, four times 128 elements x the weight columns.
 //
-// 8-bit latents are multiplied as the codes they are. What is not 8 bits wide is split into three codes with
-// a spacing of 2^5, a column each:
-//   x = c1 + c2 / 2^5 + c3 / 2^10,  each the nearest code of what is left,
-// 12 significant bits and more, exact for bf16 queries down to 2^-18 of a query's largest element, which is
-// brought into [2^7, 2^8) by a power of two. 16-bit latents take a query as it is, and a weight as two
-// values whose sum leaves 2^-17 of it. The columns' sums stand in TMEM apart and are put together in 32 bits.
-// Weights are taken against a maximum that moves only when a score passes it by more than 2^kSlack, so that
-// O in TMEM is hardly ever rescaled; times 2^5 they stay within the codes' range.
+// 8-bit latents are multiplied as the codes they are. What is not 8 bits wide is split into codes with a
+// spacing of 2^5, a column each:
+//   x = c1 + c2 / 2^5 + c3 / 2^10 (+ c4 / 2^15),  each the nearest code of what is left.
+// A query is three: 14 bits, exact for bf16 down to 2^-18 of its largest element, which is brought into
+// [2^7, 2^8) by a power of two. A weight is four where 16 heads go at a time, which leaves 2^-19 of it, or 2^-30
+// of the row's largest; with 32 heads TMEM has room for three, which leave 2^-14, or 2^-25 of the largest: there
+// thousands of weights that small are lost beside a large one. Four cost 1 % of the time, three for both differed from
+// 32-bit products by 1.4e-4 of the outputs (9.5e-5 now, which is the order of the sums).
+// 16-bit latents take a query as it is, and a weight as two values whose sum leaves 2^-17 of it (f16: 2^-23, or
+// 2^-36 of the largest). The columns' sums stand in TMEM apart and are put together in 32 bits. Weights are taken
+// against a maximum that moves only when a score passes it by more than 2^kSlack, so that O in TMEM is hardly
+// ever rescaled; times 2^5 they stay within the codes' range.
 //
 // 16 query heads go at a time, or 32 where a KV head has more than 16: the columns of 32 take TMEM whole
 // (of 8 bits with one buffer of scores, not two), and the cache is read half as often. 64 requests of 8000,
@@ -35,7 +39,7 @@
 // bits: four rows a gather 408 us; boxes of a page's runs 167; chunk by chunk, products from a converged warp
 // instead of one lane's branch (18 products 0.6 us, not 2.5) 153; eight softmax warps 146; a lighter join
 // 140; a copying warp per chunk, and scores and sums from two warps 123; no query and no scale kept in
-// registers, so no spills, 119; outputs four elements at a time, with no division for each, 116 (4 requests
+// registers, 119 (no spills with 16 heads; 8 bits with 32 heads have 8 bytes); outputs four elements at a time, with no division for each, 116 (4 requests
 // of 100: 11.7, from 14.1); a join in one pass 115. Prefetching the next tiles into L2 cost 8 to 17 us.
 #include "kvx_latent.cuh"
 
@@ -57,7 +61,7 @@ template <int VT_, int IO_, int HEADS_> struct TensorShape {
     static constexpr int SUB = TILE * 128, CHUNK = SUBS * SUB;    // the last chunk has 64 elements
     static constexpr int STAGE = 4 * CHUNK + CHUNK / 2;
     static constexpr int LAST = F8 ? 64 : 128;                    // bytes of a row in the last chunk
-    static constexpr int QTERMS = F8 ? 3 : 1, WTERMS = F8 ? 3 : 2;   // columns of a query head in the two products
+    static constexpr int QTERMS = F8 ? 3 : 1, WTERMS = !F8 ? 2 : HEADS == 16 ? 4 : 3;   // columns of a query head in the two products
     static constexpr int QCOLS = QTERMS * HEADS, WCOLS = WTERMS * HEADS;
     static constexpr int SBUFS = QCOLS > 64 ? 1 : 2;              // buffers of scores, 64 columns apart
     static constexpr int QUERY = QCOLS * kCacheMaxLatent * ESZ, WEIGHT = WCOLS * TILE * ESZ;
@@ -519,9 +523,10 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
                     float z[8];
 #pragma unroll
                     for (int n = 0; n < 8; ++n) {
-                        z[n] = __uint_as_float(y[1][n]);
-                        if constexpr (F8) z[n] = (z[n] + __uint_as_float(y[2][n]) / kSpacing) / kSpacing;
-                        z[n] = (z[n] + __uint_as_float(y[0][n])) / S::UP;
+                        z[n] = __uint_as_float(y[WTERMS - 1][n]);
+#pragma unroll
+                        for (int k = WTERMS - 2; k >= 0; --k) z[n] = __uint_as_float(y[k][n]) + (F8 ? z[n] / kSpacing : z[n]);
+                        z[n] /= S::UP;
                     }
                     // among four lanes, from 8 heads of an element each to two heads of four elements
                     const int b0 = lane & 1, b1 = lane >> 1 & 1, d = c * 128 + (here & ~3);

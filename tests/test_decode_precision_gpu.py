@@ -74,7 +74,7 @@ WARPS = [("bf16", None, 1, 2, 16, 576, 512, "bf16"), ("f16", None, 1, 2, 5, 576,
          ("e4m3", "bf16", 1, 2, 16, 576, 512, "f16")]
 TENSOR = [("bf16", None, 1, 1, 16, 576, 512, "bf16"), ("bf16", None, 1, 1, 32, 576, 512, "bf16"), ("f16", None, 1, 1, 16, 576, 512, "f16 tensor"),
           ("f16", None, 1, 1, 24, 576, 512, "f16 tensor")]
-CODES = [("e4m3", "bf16", 1, 1, 16, 576, 512, "3 codes"), ("e4m3", "f16", 1, 1, 7, 576, 512, "3 codes"),
+CODES = [("e4m3", "bf16", 1, 1, 16, 576, 512, "4 codes"), ("e4m3", "f16", 1, 1, 7, 576, 512, "4 codes"),
          ("e4m3", "bf16", 1, 1, 32, 576, 512, "3 codes"), ("e4m3", "f16", 1, 1, 40, 576, 512, "3 codes")]
 CASES = PLANES + WARPS + TENSOR + CODES
 
@@ -100,7 +100,7 @@ def test_weights_of_nearly_equal_scores(form, spread):
 
 
 @pytest.mark.parametrize("gap", [14, 16, 18, 24])
-@pytest.mark.parametrize("form", PLANES + WARPS + TENSOR)
+@pytest.mark.parametrize("form", CASES)
 def test_weights_far_below_the_largest(form, gap):
     """A first position of large score and no value: the output is that of the thousands of small weights beside it."""
     value, io, planes, shards, group, dim, v_dim, parts = form
