@@ -203,7 +203,9 @@ def _ptr(x) -> int:
     try:
         return x.data_ptr()
     except AttributeError:
-        return int(x)
+        if isinstance(x, (int, np.integer)):
+            return int(x)
+        raise                                                       # a number or an array is no address
 
 
 def _stream(s) -> int:

@@ -1,5 +1,6 @@
 """Refusals of the decode side's calls (kvx_slot_map, kvx_cache_*): every malformed argument is refused
 before any CUDA call, so no GPU is needed; and calls with nothing to do return at once."""
+import numpy as np
 import pytest
 
 import kvx_inputs
@@ -140,3 +141,22 @@ def test_stall_hook_refusals():
         refused(kvx.kvx_cache_inject_stall, kvx.KVX_EINVAL, c, 0)
         refused(kvx.kvx_cache_inject_stall, kvx.KVX_EINVAL, c, 5)
     refused(kvx.kvx_cache_inject_stall, kvx.KVX_EINVAL, c, 1)
+
+
+@pytest.mark.parametrize("x", [3.7, "12", b"16", np.float32(8), np.float64(16), np.zeros(1, np.int64), np.array(16), [16], object()])
+def test_pointers_are_tensors_or_integers(x):
+    """What is neither is refused before the library sees an address made of it."""
+    with pytest.raises(AttributeError):
+        kvx._ptr(x)
+    with kvx.kvx_cache_create(pool(GEOM), value_type=kvx.KVX_BF16) as c:
+        with pytest.raises(AttributeError):
+            kvx.kvx_cache_append(c, **dict(APPEND, n_tokens=0, k=x))
+
+
+def test_pointers_that_are_taken():
+    assert kvx._ptr(None) == 0 and kvx._ptr(4096) == 4096 and kvx._ptr(np.int64(1 << 40)) == 1 << 40
+
+    class Tensor:
+        def data_ptr(self):
+            return 512
+    assert kvx._ptr(Tensor()) == 512
