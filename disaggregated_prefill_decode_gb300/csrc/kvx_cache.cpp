@@ -73,11 +73,16 @@ static kvx_status ready(kvx_cache_t c, cudaStream_t stream) {
     int32_t device = 0, sms = 0;
     kvx_status st = device_sms(&device, &sms);
     if (st) return st;
-    for (void *p : {c->base.front(), c->base.back()}) {
+    int pageable = -1;
+    for (size_t i = 0; i < c->base.size() && c->g.buf_bytes() > 0; ++i) {          // a buffer is a pointer of its own: each of them
         cudaPointerAttributes at;
-        e = cudaPointerGetAttributes(&at, p);
+        e = cudaPointerGetAttributes(&at, c->base[i]);
         if (e != cudaSuccess) return cuda_fail(e, "cudaPointerGetAttributes(cache buffer)");
         c->outside_device |= at.type != cudaMemoryTypeDevice;
+        if (at.type != cudaMemoryTypeUnregistered) continue;
+        if (pageable < 0 && (e = cudaDeviceGetAttribute(&pageable, cudaDevAttrPageableMemoryAccess, device)) != cudaSuccess)
+            return cuda_fail(e, "cudaDeviceGetAttribute(pageable memory access)");
+        if (!pageable) return fail(KVX_EINVAL, "a cache buffer is pageable host memory this GPU cannot access");
     }
     encode_rows(c);
     void *dev = nullptr;
