@@ -84,7 +84,11 @@ static kvx_status ready(kvx_cache_t c, cudaStream_t stream) {
             return cuda_fail(e, "cudaDeviceGetAttribute(pageable memory access)");
         if (!pageable) return fail(KVX_EINVAL, "a cache buffer is pageable host memory this GPU cannot access");
     }
-    encode_rows(c);
+    try {
+        encode_rows(c);
+    } catch (const std::bad_alloc &) {
+        return fail(KVX_ENOMEM, "host allocation failed");
+    }
     void *dev = nullptr;
     const size_t bytes = 256 + attend_scratch_bytes(sms, c->g.n_planes == 1);
     st = pool_alloc(&dev, bytes, stream);
