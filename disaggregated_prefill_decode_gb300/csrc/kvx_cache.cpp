@@ -109,8 +109,9 @@ static void fill_layer(const kvx_cache_t c, int32_t layer, CacheLayer *out) {
     const Geom &g = c->g;
     for (int32_t s = 0; s < g.n_shards; ++s) {
         void *const *at = c->base.data() + (size_t)layer * g.n_planes * g.n_shards + s;
-        out->k[s] = (uint8_t *)at[0];
-        out->v[s] = (uint8_t *)at[g.n_planes == 2 ? g.n_shards : 0];
+        // a pool without blocks may have no memory: the kernels then copy nothing from this address
+        out->k[s] = g.buf_bytes() ? (uint8_t *)at[0] : c->dev;
+        out->v[s] = g.buf_bytes() ? (uint8_t *)at[g.n_planes == 2 ? g.n_shards : 0] : c->dev;
     }
     out->block_pitch = g.block_size * g.row_bytes();
     out->token_pitch = (int32_t)g.token_pitch();

@@ -50,3 +50,21 @@ def test_a_latent_layer_in_host_memory_is_refused():
             with pytest.raises(kvx.KvxError) as ei:
                 attend(case, c, layer=0)
             assert ei.value.status == kvx.KVX_EUNSUPPORTED
+
+
+@pytest.mark.parametrize("form", FORMS + [("bf16", 4, 0), ("e4m3", 12, 0)])
+def test_a_pool_without_blocks(form):
+    """It may have no memory either. Every cached position is out of bounds: reported, outputs 0, and appends skip."""
+    value, group, shards = form
+    planes, dim, v_dim = (1, 576, 512) if shards else (2, 128, 128)
+    case = Attend([0, 70, 3], value=value, planes=planes, shards=max(shards, 1), hps=1, group=group, dim=dim, v_dim=v_dim, bs=64)
+    case.run()
+    n, heads = 3, max(shards, 1)
+    geom = case.geom.replace(n_blocks=0)
+    with create(case, geom, [None] * geom.n_buffers) as c:
+        out = attend(case, c)
+        assert (out == 0).all()
+        assert kvx.kvx_cache_status(c) == kvx.KVX_ERANGE
+        x = torch.zeros((n, heads, dim), dtype=case.iodtype, device="cuda")
+        kvx.kvx_cache_append(c, 0, x, heads * dim, x if planes == 2 else None, heads * dim, dev(np.array([0, -1, 5], np.int64)), n)
+        assert kvx.kvx_cache_status(c) == kvx.KVX_ERANGE and "2 slots" in kvx.kvx_last_error()
