@@ -300,7 +300,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
             copies_commit();
         };
         // Queries of a segment. 8-bit caches multiply in f16: a bf16 row is brought by a power of two to where f16 holds
-        // its elements exactly down to 2^-33 of the largest.
+        // its elements exactly down to 2^-31 of the largest.
         auto load_q = [&](const Line &p) {
             const int32_t kvh = p.seg / sets, first = p.seg % sets * 8 * NT;
 #pragma unroll
@@ -331,7 +331,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
                     }
                     top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-                    const int e = top > 0.0f && top < INFINITY ? max(-100, min(100, 14 - ilogbf(top))) : 0;
+                    const int e = top > 0.0f && top < INFINITY ? max(-126, min(100, 14 - ilogbf(top))) : 0;
                     const float up = __int_as_float((127 + e) << 23);
                     scale *= __int_as_float((127 - e) << 23);
 #pragma unroll

@@ -168,7 +168,7 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
                 }
 #pragma unroll
             for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-            const int e = top > 0.0f && top < INFINITY ? max(-100, min(100, 14 - ilogbf(top))) : 0;
+            const int e = top > 0.0f && top < INFINITY ? max(-126, min(100, 14 - ilogbf(top))) : 0;
             scale = a.scale * __int_as_float((127 - e) << 23);
             if (x == 0) s_up[h] = __int_as_float((127 + e) << 23);
             __syncthreads();

@@ -317,7 +317,7 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
                 }
 #pragma unroll
                 for (int d = 1; d < kParts; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-                const int e = top > 0.0f && top < INFINITY ? max(-100, min(100, 7 - ilogbf(top))) : 0;
+                const int e = top > 0.0f && top < INFINITY ? max(-126, min(100, 7 - ilogbf(top))) : 0;
                 const float up = __int_as_float((127 + e) << 23);
                 if (part == 0) s_scale[turn][h] = top < INFINITY ? a.scale * __int_as_float((127 - e) << 23) : NAN;     // an infinite query: NaN
                 read(0, y);

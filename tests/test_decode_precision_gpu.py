@@ -146,3 +146,19 @@ def test_an_infinite_value_gives_that_infinity(value, group, dim, lens, window):
     assert torch.equal(out[:, :, 3::2], before[0][:, :, 3::2])
     assert torch.isnan(out[1:, :, 1]).all() and torch.equal(out[0, :, 1].isnan(), torch.full((group,), lens[0] > 1, device="cuda"))
     kvx.kvx_cache_destroy(case.cache)
+
+
+@pytest.mark.parametrize("planes,shards,group,dim,v_dim", [(2, 1, 4, 128, 0), (2, 1, 12, 64, 0), (1, 1, 16, 576, 512), (1, 1, 24, 576, 512),
+                                                           (1, 2, 8, 576, 512)])
+@pytest.mark.parametrize("value", ["bf16", "e4m3"])
+@pytest.mark.parametrize("power", [114, -80])
+def test_queries_of_any_size(power, value, planes, shards, group, dim, v_dim):
+    """Queries times a power of two and a scale that undoes it: the same bits."""
+    got = []
+    for p in (0, power):
+        case = Attend([300, 1, 77], value=value, planes=planes, shards=shards, hps=1, group=group, dim=dim, v_dim=v_dim, bs=64,
+                      scale=2.0 ** -4 * 2.0 ** -p, seed=9)
+        case.q = (case.q.double() * 2.0 ** p).to(case.iodtype)
+        got.append(case.run())
+        kvx.kvx_cache_destroy(case.cache)
+    assert torch.isfinite(got[0][0]).all() and torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
