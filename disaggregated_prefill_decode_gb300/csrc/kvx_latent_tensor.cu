@@ -193,14 +193,14 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
         asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_addr(&s_queried)), "n"(kSoftThreads) : "memory");
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (w == 8) {
+    if (w == 10 && lane == 0)
+        for (const CUtensorMap *m : {&maps.run128, &maps.run64}) asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+    wait_for_earlier();
+    if (w == 8) {                                                  // not before: a kernel that still runs may yet ask for this TMEM
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(shared_addr(&s_tmem)), "r"(kTmemCols) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         tensor_fence_before();
     }
-    if (w == 10 && lane == 0)
-        for (const CUtensorMap *m : {&maps.run128, &maps.run64}) asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
-    wait_for_earlier();
     OpenSegment *const open = (OpenSegment *)a.scratch;
     uint8_t *const parts = a.scratch + kScratchCounters * sizeof(uint32_t);
     const Batch<S::TILE, kTensorThreads / 32, 1, S::SWITCH, 0> batch(a, segs);
