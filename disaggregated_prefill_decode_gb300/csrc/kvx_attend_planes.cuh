@@ -210,12 +210,13 @@ template <class S> __device__ __noinline__ Joined<S> join_many(int f, const Piec
                 j.l += mine * s[k];
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
-                    if (x0 + 8 * k + x >= n) break;                // not the last one again: 0 times infinity
                     const float w = __shfl_sync(~0u, mine, x * 4 + t);
-                    j.o.x += w * y[k][x].x;
-                    j.o.y += w * y[k][x].y;
-                    j.o.z += w * y[k][x].z;
-                    j.o.w += w * y[k][x].w;
+                    if (x0 + 8 * k + x < n) {                      // not the last one again: 0 times infinity
+                        j.o.x += w * y[k][x].x;
+                        j.o.y += w * y[k][x].y;
+                        j.o.z += w * y[k][x].z;
+                        j.o.w += w * y[k][x].w;
+                    }
                 }
             }
     }
@@ -523,25 +524,26 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         shared_read(v[j], values + S::value_at(u, j, c, g, t));
+                    uint32_t av[S::PE / 2][4];                      // element 2e, element 2e + 1; the same 8 positions on
 #pragma unroll
-                    for (int e = 0; e < S::PE / 2; ++e) {
-                        uint32_t av[4];                             // element 2e, element 2e + 1; the same 8 positions on
+                    for (int e = 0; e < S::PE / 2; ++e)
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             if constexpr (S::F8) {
                                 const uint32_t x = __byte_perm(v[2 * j][e / 2], v[2 * j + 1][e / 2], e & 1 ? 0x7362 : 0x5140);
-                                f16_of_codes(x, av[2 * j], av[2 * j + 1]);
+                                f16_of_codes(x, av[e][2 * j], av[e][2 * j + 1]);
                             } else {
-                                av[2 * j] = __byte_perm(v[2 * j][e], v[2 * j + 1][e], 0x5410);
-                                av[2 * j + 1] = __byte_perm(v[2 * j][e], v[2 * j + 1][e], 0x7632);
+                                av[e][2 * j] = __byte_perm(v[2 * j][e], v[2 * j + 1][e], 0x5410);
+                                av[e][2 * j + 1] = __byte_perm(v[2 * j][e], v[2 * j + 1][e], 0x7632);
                             }
                         }
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
+                    for (int k = 0; k < S::PARTS; ++k)
 #pragma unroll
-                            for (int k = 0; k < S::PARTS; ++k)
-                                mma<S::MT>(o[n][c * (S::PE / 2) + e], av[0], av[1], av[2], av[3], parts[k][n][u][0], parts[k][n][u][1]);
-                    }
+                        for (int e = 0; e < S::PE / 2; ++e)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                mma<S::MT>(o[n][c * (S::PE / 2) + e], av[e][0], av[e][1], av[e][2], av[e][3], parts[k][n][u][0], parts[k][n][u][1]);
                 }
             const bool ends = cur.tile + 1 == cur.tiles;
             const int64_t here = x;
