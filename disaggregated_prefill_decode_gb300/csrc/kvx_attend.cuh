@@ -168,8 +168,8 @@ constexpr int kJoinTiles = 600;    // see Batch
 // The batch as a CTA sees it: the split over gridDim.x CTAs (of at least MIN tiles each), and how to find a place in it.
 // Where one CTA joins a segment's pieces, PIECES at a time, and there are few segments, not all CTAs get work: a segment of up
 // to kJoinTiles tiles (on the average) goes to PIECES of them, one of up to k^2 kJoinTiles to k PIECES, so that the join takes as
-// long as a stretch. One request on one KV head of 16384 bf16 positions 15.6 us, 22.1 on all CTAs; 32768 19.2, 25.7; 131072
-// 33.3, 38.5. PIECES 0: always all CTAs.
+// long as a stretch. One request on one KV head of 16384 bf16 positions 15.0 us, 22.1 on all CTAs; 32768 18.9, 25.7; 131072
+// 31.7, 38.5. PIECES 0: always all CTAs.
 // Up to 256 requests each warp keeps all the sums, a lane those of up to 8 consecutive requests, with no barrier; beyond that
 // the CTA looks for the request in which its own stretch begins, and its warps go on from there.
 template <int TOK, int WARPS, int MIN, int EXTRA, int PIECES> struct Batch {

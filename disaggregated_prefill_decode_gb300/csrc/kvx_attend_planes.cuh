@@ -13,11 +13,11 @@
 // O^T = V^T P^T takes the bytes of two neighbouring positions interleaved, so every lane reads the ring in
 // pieces of 16 bytes and the pieces are swizzled for that alone. Both products have the 8 queries as their
 // narrow side, so a group of up to 8 query heads wastes nothing that the memory would wait for, and the
-// warp products (mma.sync) are at 12 % of their rate: the tensor pipe of a whole CTA would have 8 of 128
+// warp products (mma.sync) are at 16 % of their rate: the tensor pipe of a whole CTA would have 8 of 128
 // rows to do.
 //
 // What it measured on GB300 (8 KV heads of 128, 8 queries each, bf16): 256 requests of 4608 positions 728
-// us, 6.6 TB/s, 0.98 of the copy rate; 16 requests of 1024 to 8192 56.5 us, of which 45 are the stream at
+// us, 6.6 TB/s, 0.98 of the copy rate; 16 requests of 1024 to 8192 57.4 us, of which 45 are the stream at
 // 0.99 of it. Steps on the way: keys and values straight from global memory into registers 125 us (128
 // registers a thread were too few: spills); through rings that each lane filled for itself, 64 bytes of a
 // row an instruction, 75 (256 requests: 953); whole 128-byte lines and this swizzle 61 (745): the requests

@@ -16,8 +16,8 @@
 // quarters of the banks, and the keys' reads take rows two apart. Two CTAs per SM fill each other's waits.
 //
 // Measured with 16 query heads: 64 requests of 8000 bf16 latents of 576 144 us, 4.1 TB/s, and 64 sessions of
-// 2048 to 32768 8-bit ones 212 us, where the tcgen05 kernel takes 107 and 115. Bound by instruction issue (1.9 a
-// clock, 95 warp instructions a position). Scores by 8-bit warp products (mma.sync e4m3, queries as two
+// 2048 to 32768 8-bit ones 258 us (212 with weights as one f16 value), where the tcgen05 kernel takes 108 and 116. Bound
+// by instruction issue (1.9 a clock, 95 warp instructions a position), with 78 to 142 bytes a thread spilled. Scores by 8-bit warp products (mma.sync e4m3, queries as two
 // codes) were exact enough but took 395 us: the form costs ten instructions on sm_103a.
 #include "kvx_latent.cuh"
 
@@ -442,7 +442,7 @@ template <class S> __global__ void __launch_bounds__(kLatentThreads, 2) kvx_atte
 // Joins the segments that go over several CTAs. Up to kJoinFew pieces a thread joins a float4 of the sums by itself, 256 at a time;
 // of more pieces 64 float4s at a time, four groups of 64 threads taking every fourth piece.
 // Bound by three round trips to L2: the open segments, kept in shared memory with their places, then maxima, sums and results
-// all at once. One request of 32768 8-bit latents, 152 pieces: 16.6 us, 20.6 with the maxima first.
+// all at once. One request of 32768 8-bit latents, 152 pieces: 17.7 us, 4 more with the maxima first.
 constexpr int kJoinThreads = 256, kJoinSlices = kLatentFloat4 / 64, kJoinCtas = 2;      // CTAs per SM: 8 start 1 us later, 1 takes 2 us longer
 constexpr int kJoinList = 512;                                                          // at least the CTAs of the first kernel
 constexpr int kJoinFew = 8;

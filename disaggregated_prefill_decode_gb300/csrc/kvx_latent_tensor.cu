@@ -33,14 +33,15 @@
 // five chunks is therefore copied as soon as its sums are done, by a warp of its own, and multiplied as soon
 // as it is there.
 //
-// Measured, 16 query heads, 8 bits: 64 sessions of 2048 to 32768 positions 115 us (644 MB; 1.7 us a tile, 0.97
-// of the copy rate, while it streams), 128 requests of 8000 112 us, 5.3 TB/s; bf16: 64 requests of 8000 107
+// Measured, 16 query heads, 8 bits: 64 sessions of 2048 to 32768 positions 116 us (644 MB; 1.7 us a tile, 0.97
+// of the copy rate, while it streams), 128 requests of 8000 113 us, 5.2 TB/s; bf16: 64 requests of 8000 108
 // us, 128 201 us, 5.9 TB/s, which warp products (kvx_latent.cu) took 144 and 270 for. Steps on the way, 8
 // bits: four rows a gather 408 us; boxes of a page's runs 167; chunk by chunk, products from a converged warp
 // instead of one lane's branch (18 products 0.6 us, not 2.5) 153; eight softmax warps 146; a lighter join
 // 140; a copying warp per chunk, and scores and sums from two warps 123; no query and no scale kept in
-// registers, 119 (no spills with 16 heads; 8 bits with 32 heads have 8 bytes); outputs four elements at a time, with no division for each, 116 (4 requests
-// of 100: 11.7, from 14.1); a join in one pass 115. Prefetching the next tiles into L2 cost 8 to 17 us.
+// registers, 119 (no spills with 16 heads; 8 bits with 32 heads have 8 bytes); outputs four elements at a time, with
+// no division for each, 116 (4 requests of 100: 11.7, from 14.1); a join in one pass 115; a fourth code of the weights, for
+// their precision, 116. Prefetching the next tiles into L2 cost 8 to 17 us.
 #include "kvx_latent.cuh"
 
 namespace kvx {

@@ -545,7 +545,9 @@ typedef struct kvx_cache_config {
     int32_t v_dim;         /* one-plane pools: the first v_dim elements of a latent are its value
                               (0: head_dim). Two-plane pools: 0 or head_dim */
     int32_t window;        /* a token sees the last `window` cached tokens only (0: all) */
-    float scale;           /* of the products q . k (0: 1 / sqrt(head_dim)) */
+    float scale;           /* of the products q . k (0: 1 / sqrt(head_dim)). Models that absorb a projection into the
+                              latents scale by the head dim before it: pass theirs, as 1 / sqrt(192) for 128 + 64,
+                              where the default of 576 elements is 1 / sqrt(576) */
     float k_scale;         /* KVX_E4M3: scale of the key plane (or the latents); 0: 1 */
     float v_scale;         /* KVX_E4M3: scale of the value plane; 0: 1 (one-plane pools: must be 0 or
                               k_scale) */
@@ -576,7 +578,8 @@ kvx_status kvx_cache_destroy(kvx_cache_t cache);   /* waits for the device; NULL
  * in io_type (strides in elements; multiples of 16 bytes, as the pointers); v is NULL for one-plane
  * pools. 16-bit values are copied; an 8-bit one is the nearest code (ties to even, saturated at 448, NaN
  * kept) of value * (1 / scale) in 32 bits. slots: device array as kvx_slot_map makes it; -1 skips the token,
- * any other slot outside the pool too, and kvx_cache_status reports it. Two tokens with one slot: either.
+ * any other slot outside the pool too, and kvx_cache_status reports it. Two tokens with one slot leave parts of
+ * either there.
  */
 kvx_status kvx_cache_append(kvx_cache_t cache, int32_t layer, const void *k, int64_t k_stride, const void *v,
                             int64_t v_stride, const int64_t *slots, int64_t n_tokens, cudaStream_t stream);
@@ -593,7 +596,7 @@ kvx_status kvx_cache_append(kvx_cache_t cache, int32_t layer, const void *k, int
  * seq_len beyond max_blocks * block_size is cut there, a negative one counts as 0, and positions in a
  * block outside the pool are left out; kvx_cache_status reports each of these. KVX_EUNSUPPORTED for
  * latents with v_dim above 512 or outside device memory. Unused slots may hold
- * anything, NaN too. Products have 32-bit sums; their weights are sums of 16-bit values or 8-bit codes, which leave 2^-16 of a weight
+ * anything, NaN too; an infinite value among the live ones gives that infinity. Products have 32-bit sums; their weights are sums of 16-bit values or 8-bit codes, which leave 2^-16 of a weight
  * at most, or 2^-30 of the largest of the row. Over KVX_E4M3 latents with more than 16 query heads a KV head it is 2^-14, or 2^-25
  * of the largest: thousands of weights that small, beside one large one, are not seen there. Two calls on the same
  * inputs give the same bits.
