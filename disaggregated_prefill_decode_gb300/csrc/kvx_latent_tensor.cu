@@ -27,7 +27,7 @@
 // since a row that is not live has to read as zero. Gathers alone took 58 clocks each, 4.9 us a tile.
 //
 // Shared memory bounds the products, at 128 bytes a clock: 128 positions of 8 bits are written once (576
-// bytes each) and read twice (576 + 512), and the narrow operands of 16 heads add 400: 16 clocks an SM, where
+// bytes each) and read twice (576 + 512), and the narrow operands of 16 heads add 480: 17 clocks an SM, where
 // the memory takes 25. So what counts is that the copies never stop. Two tiles fit, and a tile's way (copy
 // 1.9 us, scores 0.6, softmax 0.5, sums 0.4) is longer than the memory's time for two (3.3 us): each of the
 // five chunks is therefore copied as soon as its sums are done, by a warp of its own, and multiplied as soon
