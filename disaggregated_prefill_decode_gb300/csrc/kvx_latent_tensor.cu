@@ -9,18 +9,22 @@
 // spacing of 2^5, a column each:
 //   x = c1 + c2 / 2^5 + c3 / 2^10 (+ c4 / 2^15),  each the nearest code of what is left.
 // A query is three: 14 bits, exact for bf16 down to 2^-18 of its largest element, which is brought into
-// [2^7, 2^8) by a power of two. A weight is four where 16 heads go at a time, which leaves 2^-19 of it, or 2^-30
-// of the row's largest; with 32 heads TMEM has room for three, which leave 2^-14, or 2^-25 of the largest: there
-// thousands of weights that small are lost beside a large one. Four cost 1 % of the time, three for both differed from
-// 32-bit products by 1.4e-4 of the outputs (9.5e-5 now, which is the order of the sums).
+// [2^7, 2^8) by a power of two; of bf16 queries of 32 heads two, exact down to 2^-14 and 2^-22 of the largest
+// off below. A weight is four, which leave 2^-19 of it, or 2^-30 of the row's largest. With three (2^-14, 2^-25)
+// thousands of weights that small were lost beside a large one, and outputs differed from 32-bit products by 1.4e-4
+// (9.5e-5 now, which is the order of the sums); the fourth costs 16 heads 1 % of the time. 32 heads have no room in
+// TMEM for four columns of sums (4 x 128 are all of it): their second code has the first one's scale and goes into
+// the first one's sums, as a product of its own, and the third is 2^10 from it. That leaves the same of large
+// and of the smallest weights, 2^-9 of one below 2^-15, and costs 7 to 10 % (64 x 8000: 82 us, 76 with three codes; 16 heads at
+// a time with four columns 107, less slack for the maximum, to 2^-27, 87). f16 queries go 16 heads at a time.
 // 16-bit latents take a query as it is, and a weight as two values whose sum leaves 2^-17 of it (f16: 2^-23, or
 // 2^-36 of the largest). The columns' sums stand in TMEM apart and are put together in 32 bits. Weights are taken
 // against a maximum that moves only when a score passes it by more than 2^kSlack, so that O in TMEM is hardly
 // ever rescaled; times 2^5 they stay within the codes' range.
 //
-// 16 query heads go at a time, or 32 where a KV head has more than 16: the columns of 32 take TMEM whole
-// (of 8 bits with one buffer of scores, not two), and the cache is read half as often. 64 requests of 8000,
-// 32 heads: 84 us with 32, 111 with 16 (bf16 122, 206); 76 and 116 since.
+// 16 query heads go at a time, or 32 where a KV head has more than 16: the columns of 32 take TMEM
+// whole, and the cache is read half as often. 64 requests of 8000, 32 heads: bf16 122 us with 32, 206 with 16
+// (117 since).
 //
 // Rows come in boxes of as many as a page holds in a row (the common divisor of the page and the tile);
 // boxes that begin or end a sequence, and pages that 4 does not divide, are gathered four rows at a time,
@@ -39,7 +43,7 @@
 // bits: four rows a gather 408 us; boxes of a page's runs 167; chunk by chunk, products from a converged warp
 // instead of one lane's branch (18 products 0.6 us, not 2.5) 153; eight softmax warps 146; a lighter join
 // 140; a copying warp per chunk, and scores and sums from two warps 123; no query and no scale kept in
-// registers, 119 (no spills with 16 heads; 8 bits with 32 heads have 8 bytes); outputs four elements at a time, with
+// registers, 119 (no spills with 16 heads; 8 bits with 32 heads have 24 bytes); outputs four elements at a time, with
 // no division for each, 116 (4 requests of 100: 11.7, from 14.1); a join in one pass 115; a fourth code of the weights, for
 // their precision, 116. Prefetching the next tiles into L2 cost 8 to 17 us.
 #include "kvx_latent.cuh"
@@ -49,9 +53,8 @@ namespace kvx {
 constexpr int kSoftThreads = 256;                              // warps 0-7: softmax and outputs, half of the query heads each four
 constexpr int kTensorThreads = kSoftThreads + 7 * 32;          // 8, 9: products of the scores, of the sums; 10-14: copies, a chunk each
 constexpr int kChunks = 5;                                     // the last one is used up by the scores, the others in their order by the sums
-constexpr float kSpacing = 32.0f;
 constexpr float kSlack = 3.0f;                                 // in powers of two
-constexpr uint32_t kColScores = 0, kColSums = 128, kTmemCols = 512;      // of TMEM: scores, then 4 x S::WCOLS sums
+constexpr uint32_t kColScores = 0, kColSums = 128, kTmemCols = 512;      // of TMEM: two buffers of scores, then 4 x S::WCOLS sums
 
 template <int VT_, int IO_, int HEADS_> struct TensorShape {
     static constexpr int VT = VT_, IO = IO_, HEADS = HEADS_;       // HEADS: query heads at a time
@@ -62,10 +65,15 @@ template <int VT_, int IO_, int HEADS_> struct TensorShape {
     static constexpr int SUB = TILE * 128, CHUNK = SUBS * SUB;    // the last chunk has 64 elements
     static constexpr int STAGE = 4 * CHUNK + CHUNK / 2;
     static constexpr int LAST = F8 ? 64 : 128;                    // bytes of a row in the last chunk
-    static constexpr int QTERMS = F8 ? 3 : 1, WTERMS = !F8 ? 2 : HEADS == 16 ? 4 : 3;   // columns of a query head in the two products
-    static constexpr int QCOLS = QTERMS * HEADS, WCOLS = WTERMS * HEADS;
-    static constexpr int SBUFS = QCOLS > 64 ? 1 : 2;              // buffers of scores, 64 columns apart
-    static constexpr int QUERY = QCOLS * kCacheMaxLatent * ESZ, WEIGHT = WCOLS * TILE * ESZ;
+    static constexpr bool WIDE = F8 && HEADS > 16;                // the second code of a weight shares the first one's sums
+    static constexpr int QTERMS = !F8 ? 1 : WIDE ? 2 : 3, WTERMS = F8 ? 4 : 2;   // values of a query, of a weight
+    static constexpr int SUMS = WIDE ? 3 : WTERMS;                // columns of a query head in the sums
+    static constexpr int QCOLS = QTERMS * HEADS, WCOLS = SUMS * HEADS;
+    // A weight's k-th value: what is left of it is multiplied by, and its place; a query's codes are 2^5 apart.
+    static __host__ __device__ constexpr float spacing(int k) { return !WIDE ? 32.0f : k == 0 ? 1.0f : k == 1 ? 1024.0f : 32.0f; }
+    static __host__ __device__ constexpr int place(int k) { return !WIDE || k == 0 ? k : k == 1 ? 3 : k - 1; }
+    static __host__ __device__ constexpr float sum_spacing(int k) { return !F8 ? 1.0f : WIDE && k == 0 ? 1024.0f : 32.0f; }   // of sums k and k + 1
+    static constexpr int QUERY = QCOLS * kCacheMaxLatent * ESZ, WEIGHT = WTERMS * HEADS * TILE * ESZ;
     static constexpr int OFF_QUERY = 2 * STAGE, OFF_WEIGHT = OFF_QUERY + QUERY, BYTES = OFF_WEIGHT + 2 * WEIGHT;
     // Of the weights, up to 2^kSlack: 2^(3 + 5) is within the codes' 448, 2^(3 + 12) within f16, whose two values then have a
     // step of 2^-36 (times 1, weights below 2^-25 were lost).
@@ -76,11 +84,13 @@ template <int VT_, int IO_, int HEADS_> struct TensorShape {
     static constexpr int ROWS = F8 ? 32 : 16;                     // of the scores in a warp's lanes of TMEM: 64 rows leave half free
     static constexpr int HALF = HEADS / 2;                        // query heads of four softmax warps
     static constexpr int MINE = HALF * ROWS / 32;                 // of a thread's scores
-    static_assert(kColSums + 4 * WCOLS <= kTmemCols && MINE * ESZ % 8 == 0, "room in TMEM, weights in pieces of 8 or 16 bytes");
+    static_assert(!WIDE || IO == KVX_BF16, "two codes hold a bf16 query, not an f16 one");
+    static_assert(QCOLS <= 64 && kColSums + 4 * WCOLS <= kTmemCols && MINE * ESZ % 8 == 0, "room in TMEM, weights in pieces of 8 or 16 bytes");
     // M x N products with 32-bit sums: both operands by rows, or both by columns; bf16 is type 1, e4m3 and f16 are 0
     static constexpr uint32_t IDESC = 1u << 4 | (VT == KVX_BF16 ? 1u << 7 | 1u << 10 : 0);
     static constexpr uint32_t IDESC_ROWS = IDESC | (QCOLS / 8) << 17 | (TILE / 16) << 24;
     static constexpr uint32_t IDESC_COLS = IDESC | (WCOLS / 8) << 17 | (128 / 16) << 24 | 1u << 15 | 1u << 16;
+    static constexpr uint32_t IDESC_SECOND = IDESC | (HEADS / 8) << 17 | (128 / 16) << 24 | 1u << 15 | 1u << 16;
 };
 
 // Shared memory operands: start, the two strides, swizzle (0 none, 2 of 128 bytes, 4 of 64 bytes).
@@ -134,14 +144,24 @@ __device__ __forceinline__ bool softmax_any(bool x) {
 }
 
 // Codes of two values, and what is left of them, times the spacing.
-__device__ __forceinline__ uint32_t take_codes(float &x, float &y) {
+__device__ __forceinline__ uint32_t take_codes(float &x, float &y, float spacing) {
     uint16_t c;
     uint32_t h;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(c) : "f"(x), "f"(y));
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
     const float2 f = unpack<KVX_F16>(h);
-    x = (x - f.x) * kSpacing;
-    y = (y - f.y) * kSpacing;
+    x = (x - f.x) * spacing;
+    y = (y - f.y) * spacing;
+    return c;
+}
+
+// The same of two f16 values.
+__device__ __forceinline__ uint32_t take_codes(__half2 &x) {
+    uint16_t c;
+    uint32_t h;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(*reinterpret_cast<const uint32_t *>(&x)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+    x = __hmul2(__hsub2(x, *reinterpret_cast<const __half2 *>(&h)), __float2half2_rn(32.0f));
     return c;
 }
 
@@ -170,7 +190,7 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
     using Line = Place<S::TILE, S::SWITCH>;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ __align__(8) uint64_t s_full[2][kChunks], s_free[2][kChunks];           // chunk by chunk
-    __shared__ __align__(8) uint64_t s_scored[2], s_weighed[2], s_read, s_queried, s_drained[2], s_never;
+    __shared__ __align__(8) uint64_t s_scored[2], s_weighed[2], s_queried, s_drained[2], s_never;
     __shared__ uint8_t s_live[3][32];                              // live positions, four a byte
     __shared__ __align__(16) float s_red[4][S::HEADS], s_scale[2][S::HEADS], s_old[S::HEADS], s_m[S::HEADS], s_l[S::HEADS], s_inverse[S::HEADS];
     __shared__ uint32_t s_tmem;
@@ -190,7 +210,6 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_addr(&s_weighed[i])), "n"(kSoftThreads) : "memory");
         }
         asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(shared_addr(&s_never)) : "memory");
-        asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_addr(&s_read)), "n"(kSoftThreads) : "memory");
         asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_addr(&s_queried)), "n"(kSoftThreads) : "memory");
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -238,9 +257,9 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
         bool ok = __all_sync(~0u, goes_on(kStallScores)), first = true;
         for (int j = 0; ok && x < c_end; ++j) {
             const uint64_t stage = (j & 1) * (S::STAGE / 16);
-            const uint32_t d = tmem + kColScores + (S::SBUFS == 2 ? (j & 1) * 64 : 0);
-            if (j >= S::SBUFS) {                                   // the scores before are read
-                ok = __all_sync(~0u, S::SBUFS == 2 ? wait(&s_weighed[j & 1], (j - 2) >> 1) : wait(&s_read, j - 1));
+            const uint32_t d = tmem + kColScores + (j & 1) * 64;
+            if (j >= 2) {                                          // the scores before are read
+                ok = __all_sync(~0u, wait(&s_weighed[j & 1], (j - 2) >> 1));
                 tensor_fence_after();
             }
             if (ok && first) ok = __all_sync(~0u, wait(&s_queried, switches++));
@@ -275,6 +294,11 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
                 for (int i = 0; i < 4; ++i)                        // a quarter of the positions
                     tensor_mma<F8>(tmem + kColSums + c * S::WCOLS, v + c * (S::CHUNK / 16) + i * (S::SUB / 64), p + i * (S::TILE / 4), S::IDESC_COLS,
                                    !first || i > 0);
+                if constexpr (S::WIDE)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        tensor_mma<F8>(tmem + kColSums + c * S::WCOLS, v + c * (S::CHUNK / 16) + i * (S::SUB / 64),
+                                       p + (S::WCOLS / 16) * S::TILE + i * (S::TILE / 4), S::IDESC_SECOND, true);
                 tensor_commit(&s_free[j & 1][c]);
             }
             at.next(a, segs, x);
@@ -336,8 +360,8 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
                         float v[4] = {f0.x * up, f0.y * up, f1.x * up, f1.y * up};
 #pragma unroll
                         for (int n = 0; n < QTERMS; ++n) {
-                            const uint32_t lo = take_codes(v[0], v[1]);
-                            codes[n][k] = lo | take_codes(v[2], v[3]) << 16;
+                            const uint32_t lo = take_codes(v[0], v[1], 32.0f);
+                            codes[n][k] = lo | take_codes(v[2], v[3], 32.0f) << 16;
                         }
                     }
 #pragma unroll
@@ -381,17 +405,16 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
                 for (int i = 0; i < HALF; i += 8) {
                     uint32_t y[QTERMS][8];
 #pragma unroll
-                    for (int k = 0; k < QTERMS; ++k) tmem_load(y[k], lanes + kColScores + (S::SBUFS == 2 ? (j & 1) * 64 : 0) + k * HEADS + i);
+                    for (int k = 0; k < QTERMS; ++k) tmem_load(y[k], lanes + kColScores + (j & 1) * 64 + k * HEADS + i);
                     tmem_load_wait();
 #pragma unroll
                     for (int h = 0; h < 8; ++h) {
                         z[i + h] = __uint_as_float(y[0][h]);
-                        if constexpr (F8) z[i + h] += (__uint_as_float(y[1][h]) + __uint_as_float(y[2][h]) / kSpacing) / kSpacing;
+                        float rest = 0.0f;
+#pragma unroll
+                        for (int k = QTERMS - 1; k > 0; --k) rest = (__uint_as_float(y[k][h]) + rest) / 32.0f;
+                        z[i + h] += rest;
                     }
-                }
-                if constexpr (S::SBUFS == 1) {
-                    tensor_fence_before();
-                    arrive(&s_read);
                 }
 #pragma unroll
                 for (int h = 0; h < MINE; ++h) {
@@ -428,7 +451,7 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
                     wait(&s_free[(j - 1) & 1][3], (j - 1) >> 1);
                     tensor_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < 4 * WTERMS; ++c)
+                    for (int c = 0; c < 4 * S::SUMS; ++c)
 #pragma unroll
                         for (int i = 0; i < HALF; i += 8) {
                             uint32_t y[8];
@@ -453,9 +476,15 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
                 }
                 if constexpr (F8) {
 #pragma unroll
-                    for (int k = 0; k < WTERMS; ++k) {
-                        const uint32_t lo = take_codes(v[0], v[1]);
-                        terms[k][h / 4] = lo | take_codes(v[2], v[3]) << 16;
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t lo = take_codes(v[0], v[1], S::spacing(k));
+                        terms[S::place(k)][h / 4] = lo | take_codes(v[2], v[3], S::spacing(k)) << 16;
+                    }
+                    __half2 y0 = __floats2half2_rn(v[0], v[1]), y1 = __floats2half2_rn(v[2], v[3]);        // 11 bits of what is left suffice
+#pragma unroll
+                    for (int k = 2; k < WTERMS; ++k) {
+                        const uint32_t lo = take_codes(y0);
+                        terms[S::place(k)][h / 4] = lo | take_codes(y1) << 16;
                     }
                 } else {
 #pragma unroll
@@ -517,16 +546,16 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
             for (int c = 0; c < 4; ++c)
 #pragma unroll 1
                 for (int i = 0; i < HALF; i += 8) {
-                    uint32_t y[WTERMS][8];
+                    uint32_t y[S::SUMS][8];
 #pragma unroll
-                    for (int k = 0; k < WTERMS; ++k) tmem_load(y[k], lanes + kColSums + c * S::WCOLS + k * HEADS + i);
+                    for (int k = 0; k < S::SUMS; ++k) tmem_load(y[k], lanes + kColSums + c * S::WCOLS + k * HEADS + i);
                     tmem_load_wait();
                     float z[8];
 #pragma unroll
                     for (int n = 0; n < 8; ++n) {
-                        z[n] = __uint_as_float(y[WTERMS - 1][n]);
+                        z[n] = __uint_as_float(y[S::SUMS - 1][n]);
 #pragma unroll
-                        for (int k = WTERMS - 2; k >= 0; --k) z[n] = __uint_as_float(y[k][n]) + (F8 ? z[n] / kSpacing : z[n]);
+                        for (int k = S::SUMS - 2; k >= 0; --k) z[n] = __uint_as_float(y[k][n]) + z[n] / S::sum_spacing(k);
                         z[n] /= S::UP;
                     }
                     // among four lanes, from 8 heads of an element each to two heads of four elements
@@ -684,7 +713,9 @@ template <class S> static cudaError_t launch(const AttendArgs &a, int32_t sms, c
 }
 
 template <int VT, int IO> static cudaError_t launch_heads(const AttendArgs &a, int32_t sms, cudaStream_t stream) {
-    return a.n_q_heads / a.n_kv_heads > 16 ? launch<TensorShape<VT, IO, 32>>(a, sms, stream) : launch<TensorShape<VT, IO, 16>>(a, sms, stream);
+    if constexpr (VT != KVX_E4M3 || IO == KVX_BF16)                // f16 queries of 32 heads in three codes leave no room for the weights
+        if (a.n_q_heads / a.n_kv_heads > 16) return launch<TensorShape<VT, IO, 32>>(a, sms, stream);
+    return launch<TensorShape<VT, IO, 16>>(a, sms, stream);
 }
 
 cudaError_t launch_latent_tensor(const AttendArgs &a, int32_t vt, int32_t io, int32_t sms, cudaStream_t stream) {

@@ -597,9 +597,8 @@ kvx_status kvx_cache_append(kvx_cache_t cache, int32_t layer, const void *k, int
  * block outside the pool are left out; kvx_cache_status reports each of these. KVX_EUNSUPPORTED for
  * latents with v_dim above 512 or outside device memory. Unused slots may hold
  * anything, NaN too; an infinite value among the live ones gives that infinity. Products have 32-bit sums; their weights are sums of 16-bit values or 8-bit codes, which leave 2^-16 of a weight
- * at most, or 2^-30 of the largest of the row. Over KVX_E4M3 latents with more than 16 query heads a KV head it is 2^-14, or 2^-25
- * of the largest: thousands of weights that small, beside one large one, are not seen there. Two calls on the same
- * inputs give the same bits.
+ * at most, or 2^-30 of the largest of the row (over KVX_E4M3 latents with more than 16 query heads a KV head 2^-9 of weights
+ * below 2^-15 of the largest). Two calls on the same inputs give the same bits.
  */
 kvx_status kvx_cache_attend(kvx_cache_t cache, int32_t layer, const void *q, int64_t q_stride,
                             const int32_t *block_table, int64_t table_stride, int32_t max_blocks,

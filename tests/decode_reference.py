@@ -82,17 +82,22 @@ def attend_bounds(out, lse, weight, spread, floor, d, n, io, p_unit):
 #     (2^12 on the tensor pipe), and may be a whole step off: 2^-39 (2^-36).
 #   e4m3, N codes 2^5 apart: each leaves 2^-4 of the power of two below what it stands for, 2^-4-5(N-1) in all; the last
 #     one's smallest step is 2^-9 of weights taken times 2^5, half of it 2^-10-5N.
+#   e4m3, four codes 1, 2^10 and 2^5 apart (the second is of the first one's scale): the same of large weights and of the smallest.
+#     Between, the first two end at half their step, 2^-10 of weights taken times 2^5, and the other two leave 2^-4-5 of that (the
+#     second of them half a step, where a power of two ends: 2^-10), or of a weight that is smaller.
 PARTS = {"bf16": (2.0 ** -16, 0.0), "bf16 planes": (2.0 ** -22, 0.0), "f16": (2.0 ** -22, 2.0 ** -39), "f16 tensor": (2.0 ** -22, 2.0 ** -36),
-         "3 codes": (2.0 ** -14, 2.0 ** -25), "4 codes": (2.0 ** -19, 2.0 ** -30)}
+         "3 codes": (2.0 ** -14, 2.0 ** -25), "4 codes": (2.0 ** -19, 2.0 ** -30),
+         "4 codes, wide": (2.0 ** -19, 2.0 ** -30, 2.0 ** -9, 2.0 ** -25)}
 SMALLEST = {"bf16": 2.0 ** -134, "f16": 2.0 ** -25}                       # half an output's smallest step
 
 
 def parts_bounds(out, lse, weight, spread, floor, d, n, io, parts):
     """As attend_bounds, for weights that are held in parts."""
-    unit, step = PARTS[parts]
+    unit, step = PARTS[parts][:2]
+    low_unit, low_step = PARTS[parts][2:] or (0.0, 0.0)
     score = (d + 8) * 2.0 ** -24 * spread + 2.0 ** -20
     rel = 2 * score[:, None] + unit + (n + 64) * 2.0 ** -24
-    err = rel * weight + step * floor
+    err = rel * weight + step * floor + np.minimum(low_unit * weight, low_step * floor)
     return UNIT[io] * (np.abs(out) + err) + err + SMALLEST[io], score + (n + 64) * 2.0 ** -24 + np.abs(lse) * 2.0 ** -22
 
 

@@ -32,6 +32,28 @@ def codes(p, n):
     return total
 
 
+def codes_wide(p):
+    """Four codes, the second in the first one's scale."""
+    total, left, at = 0.0, p * 32, 32.0
+    for spacing in (1, 1024, 32, 1):
+        c = rounded(left, torch.float8_e4m3fn)
+        total, left, at = total + c / at, (left - c) * spacing, at * spacing
+    return total
+
+
+@pytest.mark.parametrize("parts", sorted(ref.PARTS))
+def test_what_the_parts_leave(parts):
+    """Weights of all sizes, up to the 2^3 that the maximum may lag behind."""
+    rng = np.random.default_rng(0)
+    p = np.concatenate([2.0 ** rng.uniform(-36, 0, 200000), np.float32(2.0) ** -np.arange(36), 1 - 2.0 ** -np.arange(1, 24)])
+    p = p.astype(np.float32).astype(np.float64)
+    hold = codes_wide if "wide" in parts else (lambda x: codes(x, int(parts[0]))) if "codes" in parts else lambda x: in_parts(x, parts)
+    for lag in (1.0, 8.0) if "codes" in parts else (1.0,):
+        unit, step, low_unit, low_step = (*ref.PARTS[parts], 0.0, 0.0)[:4]
+        off = np.abs(hold(p * lag) / lag - p)
+        assert (off <= unit * p + step / lag + np.minimum(low_unit * p, low_step / lag)).all()
+
+
 def worst(q, k, v, scale, io, parts, hold):
     """Largest |error| / bound of the attention with weights as `hold` makes them."""
     o, l, weight, spread, floor = ref.attend(q, k, v, scale)
@@ -81,7 +103,7 @@ def test_lost_small_weights_show(io, kind, gap):
         assert worst(*args, lambda p: rounded(p, torch.float16)) > 1
 
 
-@pytest.mark.parametrize("n", [3, 4])
+@pytest.mark.parametrize("n", [3, 4, "wide"])
 def test_lost_small_weights_of_codes_show(n):
     """Four codes hold weights of 2^-26, three are at their end there, as the bound says."""
     rng = np.random.default_rng(4)
@@ -89,6 +111,23 @@ def test_lost_small_weights_of_codes_show(n):
     q = rng.standard_normal((4, 64))
     q[:, 0] = 8.0
     args = q, k[:, 0], v[:, 0], 0.125, "bf16"
+    if n == "wide":
+        assert worst(*args, "4 codes, wide", codes_wide) <= 1
+        assert worst(*args, "4 codes, wide", lambda p: codes(p, 3)) > 1
+        return
     assert worst(*args, f"{n} codes", lambda p: codes(p, n)) <= 1
     if n == 4:
         assert worst(*args, f"{n} codes", lambda p: codes(p, n - 1)) > 1
+
+
+@pytest.mark.parametrize("n,left", [(2, -22), (3, -27)])
+def test_what_a_querys_codes_leave(n, left):
+    """bf16 elements of a row whose largest is brought into [2^7, 2^8): what n codes leave of them, in units of the largest."""
+    x = torch.arange(1 << 15, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).float()
+    x = x[torch.isfinite(x) & (x < 256)].double().numpy()
+    rest, at, got = x, 1.0, 0.0
+    for _ in range(n):
+        c = rounded(rest, torch.float8_e4m3fn)
+        got, rest, at = got + c / at, (rest - c) * 32, at * 32
+    assert np.abs(got - x).max() <= 2.0 ** (7 + left)
+    assert (got == x)[x >= 2.0 ** (8 - (14 if n == 2 else 18))].all()

@@ -75,7 +75,8 @@ WARPS = [("bf16", None, 1, 2, 16, 576, 512, "bf16"), ("f16", None, 1, 2, 5, 576,
 TENSOR = [("bf16", None, 1, 1, 16, 576, 512, "bf16"), ("bf16", None, 1, 1, 32, 576, 512, "bf16"), ("f16", None, 1, 1, 16, 576, 512, "f16 tensor"),
           ("f16", None, 1, 1, 24, 576, 512, "f16 tensor")]
 CODES = [("e4m3", "bf16", 1, 1, 16, 576, 512, "4 codes"), ("e4m3", "f16", 1, 1, 7, 576, 512, "4 codes"),
-         ("e4m3", "bf16", 1, 1, 32, 576, 512, "3 codes"), ("e4m3", "f16", 1, 1, 40, 576, 512, "3 codes")]
+         ("e4m3", "bf16", 1, 1, 32, 576, 512, "4 codes, wide"), ("e4m3", "bf16", 1, 1, 70, 576, 512, "4 codes, wide"),
+         ("e4m3", "f16", 1, 1, 40, 576, 512, "4 codes")]
 CASES = PLANES + WARPS + TENSOR + CODES
 
 
@@ -162,3 +163,15 @@ def test_queries_of_any_size(power, value, planes, shards, group, dim, v_dim):
         got.append(case.run())
         kvx.kvx_cache_destroy(case.cache)
     assert torch.isfinite(got[0][0]).all() and torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("form", TENSOR + CODES + WARPS)
+def test_queries_with_a_few_large_elements(form):
+    """The others of the row are far below the largest, which is what 8-bit products bring them up by."""
+    value, io, planes, shards, group, dim, v_dim, parts = form
+    case = Attend([300, 1, 2000], value=value, io=io, planes=planes, shards=shards, hps=1, group=group, dim=dim, v_dim=v_dim, bs=64, seed=13)
+    case.q = case.q.float()
+    case.q[:, :, [5, 200, 570]] *= 300.0
+    case.q = case.q.to(case.iodtype)
+    case.check(*case.run())
+    kvx.kvx_cache_destroy(case.cache)
