@@ -10,7 +10,7 @@
 //   x = c1 + c2 / 2^5 + c3 / 2^10 (+ c4 / 2^15),  each the nearest code of what is left.
 // A query is three: 14 bits, exact for bf16 down to 2^-18 of its largest element, which is brought into
 // [2^7, 2^8) by a power of two; of bf16 queries of 32 heads two, exact down to 2^-14 and 2^-22 of the largest
-// off below. A weight is four, which leave 2^-19 of it, or 2^-30 of the row's largest. With three (2^-14, 2^-25)
+// off below. A weight is four, which leave 2^-18 of it, or 2^-30 of the row's largest. With three (2^-14, 2^-25)
 // thousands of weights that small were lost beside a large one, and outputs differed from 32-bit products by 1.4e-4
 // (9.5e-5 now, which is the order of the sums); the fourth costs 16 heads 1 % of the time. 32 heads have no room in
 // TMEM for four columns of sums (4 x 128 are all of it): their second code has the first one's scale and goes into
@@ -480,7 +480,7 @@ kvx_attend_latent_tensor(const __grid_constant__ AttendArgs a, const __grid_cons
                         const uint32_t lo = take_codes(v[0], v[1], S::spacing(k));
                         terms[S::place(k)][h / 4] = lo | take_codes(v[2], v[3], S::spacing(k)) << 16;
                     }
-                    __half2 y0 = __floats2half2_rn(v[0], v[1]), y1 = __floats2half2_rn(v[2], v[3]);        // 11 bits of what is left suffice
+                    __half2 y0 = __floats2half2_rn(v[0], v[1]), y1 = __floats2half2_rn(v[2], v[3]);   // 11 bits: a quarter of what the last code leaves
 #pragma unroll
                     for (int k = 2; k < WTERMS; ++k) {
                         const uint32_t lo = take_codes(y0);

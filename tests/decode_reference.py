@@ -81,13 +81,14 @@ def attend_bounds(out, lse, weight, spread, floor, d, n, io, p_unit):
 #   f16, two values: below 2^-10, then half a unit: 2^-22. The second's smallest step is 2^-24 of weights taken times 2^15
 #     (2^12 on the tensor pipe), and may be a whole step off: 2^-39 (2^-36).
 #   e4m3, N codes 2^5 apart: each leaves 2^-4 of the power of two below what it stands for, 2^-4-5(N-1) in all; the last
-#     one's smallest step is 2^-9 of weights taken times 2^5, half of it 2^-10-5N.
+#     one's smallest step is 2^-9 of weights taken times 2^5, half of it 2^-10-5N. Of four the last two are taken from an f16
+#     value, 2^-11 off where the last code is 2^-9: a quarter more of each, and 2^-18 for 2^-19.
 #   e4m3, four codes 1, 2^10 and 2^5 apart (the second is of the first one's scale): the same of large weights and of the smallest.
 #     Between, the first two end at half their step, 2^-10 of weights taken times 2^5, and the other two leave 2^-4-5 of that (the
 #     second of them half a step, where a power of two ends: 2^-10), or of a weight that is smaller.
 PARTS = {"bf16": (2.0 ** -16, 0.0), "bf16 planes": (2.0 ** -22, 0.0), "f16": (2.0 ** -22, 2.0 ** -39), "f16 tensor": (2.0 ** -22, 2.0 ** -36),
-         "3 codes": (2.0 ** -14, 2.0 ** -25), "4 codes": (2.0 ** -19, 2.0 ** -30),
-         "4 codes, wide": (2.0 ** -19, 2.0 ** -30, 2.0 ** -9, 2.0 ** -25)}
+         "3 codes": (2.0 ** -14, 2.0 ** -25), "4 codes": (2.0 ** -18, 1.25 * 2.0 ** -30),
+         "4 codes, wide": (2.0 ** -18, 1.25 * 2.0 ** -30, 1.25 * 2.0 ** -9, 1.25 * 2.0 ** -25)}
 SMALLEST = {"bf16": 2.0 ** -134, "f16": 2.0 ** -25}                       # half an output's smallest step
 
 

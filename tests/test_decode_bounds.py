@@ -26,7 +26,9 @@ def in_parts(p, kind, parts=2):
 
 def codes(p, n):
     total, left, at = 0.0, p * 32, 32.0
-    for _ in range(n):
+    for k in range(n):
+        if k == 2 and n == 4:
+            left = rounded(left, torch.float16)
         c = rounded(left, torch.float8_e4m3fn)
         total, left, at = total + c / at, (left - c) * 32, at * 32
     return total
@@ -35,7 +37,9 @@ def codes(p, n):
 def codes_wide(p):
     """Four codes, the second in the first one's scale."""
     total, left, at = 0.0, p * 32, 32.0
-    for spacing in (1, 1024, 32, 1):
+    for k, spacing in enumerate((1, 1024, 32, 1)):
+        if k == 2:
+            left = rounded(left, torch.float16)
         c = rounded(left, torch.float8_e4m3fn)
         total, left, at = total + c / at, (left - c) * spacing, at * spacing
     return total
