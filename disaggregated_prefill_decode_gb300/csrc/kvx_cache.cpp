@@ -12,8 +12,7 @@ using namespace kvx;
 
 static bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
-// x / d = (mulhi(x, mul) + x) >> shift for x below 2^31.
-static void divisor(uint32_t d, uint32_t *mul, uint32_t *shift) {
+void kvx::divisor(uint32_t d, uint32_t *mul, uint32_t *shift) {
     uint32_t s = 0;
     while (((uint64_t)1 << s) < d) ++s;
     *shift = s;
@@ -57,8 +56,8 @@ static void encode_rows(kvx_cache_t c) {
     c->row_maps.swap(maps);
 }
 
-// Scratch of the handle, at its first append or attend.
-static kvx_status ready(kvx_cache_t c, cudaStream_t stream) {
+// Scratch of the handle, at the first call that runs on the device.
+kvx_status kvx::cache_ready(kvx_cache_t c, cudaStream_t stream) {
     if (c->dev) {
         int dev = 0;
         const cudaError_t e = cudaGetDevice(&dev);
@@ -69,7 +68,7 @@ static kvx_status ready(kvx_cache_t c, cudaStream_t stream) {
     cudaError_t e = cudaStreamIsCapturing(stream, &cap);
     if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
     if (cap != cudaStreamCaptureStatusNone)
-        return fail(KVX_EINVAL, "the first append or attend on a cache allocates: make it before the capture");
+        return fail(KVX_EINVAL, "the first call on a cache allocates: make it before the capture");
     int32_t device = 0, sms = 0;
     kvx_status st = device_sms(&device, &sms);
     if (st) return st;
@@ -90,22 +89,24 @@ static kvx_status ready(kvx_cache_t c, cudaStream_t stream) {
         return fail(KVX_ENOMEM, "host allocation failed");
     }
     void *dev = nullptr;
-    const size_t bytes = 256 + attend_scratch_bytes(sms, c->g.n_planes == 1);
-    st = pool_alloc(&dev, bytes, stream);
+    const size_t bases = c->base.size() * sizeof(void *), bytes = (256 + attend_scratch_bytes(sms, c->g.n_planes == 1) + 15) / 16 * 16;
+    st = pool_alloc(&dev, bytes + bases, stream);
     if (st) return st;
     e = cudaMemsetAsync(dev, 0, bytes, stream);
+    if (e == cudaSuccess) e = cudaMemcpyAsync((uint8_t *)dev + bytes, c->base.data(), bases, cudaMemcpyHostToDevice, stream);
     if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) {
         pool_free(dev);
         return cuda_fail(e, "preparing the cache's scratch");
     }
     c->dev = (uint8_t *)dev;
+    c->dev_bases = (uint8_t *const *)(c->dev + bytes);
     c->device = device;
     c->sms = sms;
     return KVX_OK;
 }
 
-static void fill_layer(const kvx_cache_t c, int32_t layer, CacheLayer *out) {
+void kvx::cache_fill_layer(kvx_cache_t c, int32_t layer, CacheLayer *out) {
     const Geom &g = c->g;
     for (int32_t s = 0; s < g.n_shards; ++s) {
         void *const *at = c->base.data() + (size_t)layer * g.n_planes * g.n_shards + s;
@@ -123,7 +124,7 @@ static void fill_layer(const kvx_cache_t c, int32_t layer, CacheLayer *out) {
     out->skipped = (unsigned long long *)c->dev;
 }
 
-static kvx_status check_layer(const kvx_cache_t c, int32_t layer) {
+kvx_status kvx::cache_check_layer(kvx_cache_t c, int32_t layer) {
     if (!c) return fail(KVX_EINVAL, "cache is NULL");
     if (layer < 0 || layer >= c->g.n_layers) return fail(KVX_EINVAL, "layer %d of %d", layer, c->g.n_layers);
     return KVX_OK;
@@ -239,7 +240,7 @@ kvx_status kvx_cache_destroy(kvx_cache_t c) {
 
 kvx_status kvx_cache_append(kvx_cache_t c, int32_t layer, const void *k, int64_t k_stride, const void *v,
                             int64_t v_stride, const int64_t *slots, int64_t n_tokens, cudaStream_t stream) {
-    kvx_status st = check_layer(c, layer);
+    kvx_status st = cache_check_layer(c, layer);
     if (st) return st;
     const Geom &g = c->g;
     if (n_tokens < 0 || n_tokens > std::numeric_limits<int32_t>::max())
@@ -255,9 +256,9 @@ kvx_status kvx_cache_append(kvx_cache_t c, int32_t layer, const void *k, int64_t
         return fail(KVX_EINVAL, "k and v: pointers and strides must be multiples of 16 bytes");
     if (((uintptr_t)slots & 7) != 0) return fail(KVX_EINVAL, "slots is not on an 8-byte boundary");
     if (n_tokens == 0) return KVX_OK;
-    if ((st = ready(c, stream))) return st;
+    if ((st = cache_ready(c, stream))) return st;
     AppendArgs a;
-    fill_layer(c, layer, &a.pool);
+    cache_fill_layer(c, layer, &a.pool);
     a.k = (const uint8_t *)k;
     a.v = (const uint8_t *)v;
     a.k_stride = k_stride * 2;
@@ -277,7 +278,7 @@ kvx_status kvx_cache_attend(kvx_cache_t c, int32_t layer, const void *q, int64_t
                             const int32_t *block_table, int64_t table_stride, int32_t max_blocks,
                             const int32_t *seq_len, int32_t n_reqs, void *out, int64_t out_stride, float *lse,
                             cudaStream_t stream) {
-    kvx_status st = check_layer(c, layer);
+    kvx_status st = cache_check_layer(c, layer);
     if (st) return st;
     const Geom &g = c->g;
     const kvx_cache_config &f = c->cfg;
@@ -294,10 +295,10 @@ kvx_status kvx_cache_attend(kvx_cache_t c, int32_t layer, const void *q, int64_t
     if (((uintptr_t)block_table & 3) || ((uintptr_t)seq_len & 3) || ((uintptr_t)lse & 3))
         return fail(KVX_EINVAL, "an array is not on a boundary of its elements");
     if (n_reqs == 0) return KVX_OK;
-    if ((st = ready(c, stream))) return st;
+    if ((st = cache_ready(c, stream))) return st;
     if (g.n_planes == 1 && c->outside_device) return fail(KVX_EUNSUPPORTED, "attention over latents outside device memory");
     AttendArgs a;
-    fill_layer(c, layer, &a.pool);
+    cache_fill_layer(c, layer, &a.pool);
     a.q = (const uint8_t *)q;
     a.out = (uint8_t *)out;
     a.lse = lse;

@@ -250,6 +250,52 @@ cudaError_t launch_attend_latent(const AttendArgs &a, int32_t value_type, int32_
 size_t attend_scratch_bytes(int32_t sms, bool latent);
 size_t latent_scratch_bytes(int32_t sms);
 
+// ---- pages (kvx_page_calls.cpp, kvx_pages.cu) ----
+struct TableArgs {
+    const int32_t *block_table, *seq_len;
+    int64_t table_stride;
+    int32_t n_reqs, max_blocks, block_size;
+    uint32_t block_mul, block_shift;  // as in AttendArgs
+};
+struct PageArgs {
+    TableArgs t;
+    int32_t *refs, *free_blocks;
+    kvx_page_result *result;
+    int64_t n_blocks;
+};
+struct ForkArgs {
+    TableArgs t;
+    const int32_t *parent, *free_blocks;
+    int32_t *new_table, *new_len, *src, *dst, *first;      // first: per request, the first row that goes on from it
+    kvx_page_result *result;
+    int64_t new_stride, n_free;
+    int32_t n_out;
+};
+struct CompactArgs {
+    TableArgs t;
+    const int32_t *refs;
+    int32_t *new_table, *src, *dst;
+    kvx_page_result *result;
+    int64_t new_stride, n_blocks, max_moves;
+};
+struct PageCopyArgs {
+    uint8_t *const *bufs;             // device: the layers' buffers
+    const int32_t *src, *dst;
+    int64_t n_blocks, vectors;        // vectors: 16-byte ones of a block in one buffer
+    int32_t n_bufs, n_pairs;
+    unsigned long long *skipped;
+};
+cudaError_t launch_pages_free(const PageArgs &a, cudaStream_t stream);
+cudaError_t launch_pages_fork(const ForkArgs &a, cudaStream_t stream);
+cudaError_t launch_pages_compact(const CompactArgs &a, cudaStream_t stream);
+cudaError_t launch_cache_copy(const PageCopyArgs &a, int32_t sms, cudaStream_t stream);
+
+// ---- the handle, for the other files with calls on it (kvx_cache.cpp) ----
+kvx_status cache_check_layer(kvx_cache_t c, int32_t layer);
+kvx_status cache_ready(kvx_cache_t c, cudaStream_t stream);                    // its scratch, allocated by the first call that needs it
+void cache_fill_layer(kvx_cache_t c, int32_t layer, CacheLayer *out);
+void divisor(uint32_t d, uint32_t *mul, uint32_t *shift);                      // x / d = (mulhi(x, mul) + x) >> shift for x below 2^31
+
 }  // namespace kvx
 
 // The object behind kvx_cache_t.
@@ -264,6 +310,7 @@ struct kvx_cache_s {
     int32_t map_run = 0;                       // rows of a run: the common divisor of the block size and a tile
     int32_t stall = 0;                         // kvx_cache_inject_stall: part of the next attend
     uint8_t *dev = nullptr;                    // [256 bytes: skipped][scratch of the attend kernels]
+    uint8_t *const *dev_bases = nullptr;       // behind it: `base` on the device
 };
 
 // The plan object behind kvx_plan_t.

@@ -137,6 +137,12 @@ _sig = {
     "kvx_cache_destroy": (c_i32, [c_vp]),
     "kvx_cache_append": (c_i32, [c_vp, c_i32, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp]),
     "kvx_cache_attend": (c_i32, [c_vp, c_i32, c_vp, c_i64, c_vp, c_i64, c_i32, c_vp, c_i32, c_vp, c_i64, c_vp, c_vp]),
+    "kvx_pages_free": (c_i32, [c_vp, c_i64, c_i32, c_vp, c_i32, c_i32, c_i64, c_vp, c_vp, c_vp, c_vp]),
+    "kvx_pages_fork": (c_i32, [c_vp, c_i64, c_i32, c_vp, c_i32, c_vp, c_i32, c_i32, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp,
+                               c_vp, c_vp, c_vp, c_vp]),
+    "kvx_pages_compact": (c_i32, [c_vp, c_i64, c_i32, c_vp, c_i32, c_i32, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_i64, c_vp,
+                                  c_vp]),
+    "kvx_cache_copy": (c_i32, [c_vp, c_i32, c_i32, c_vp, c_vp, c_i32, c_vp]),
     "kvx_cache_status": (c_i32, [c_vp, c_vp]),
     "kvx_cache_inject_stall": (c_i32, [c_vp, c_i32]),
     "kvx_conn_create": (c_i32, [_P(kvx_conn_config), _P(c_vp)]),
@@ -526,6 +532,37 @@ def kvx_cache_attend(cache: Cache, layer: int, q, q_stride: int, block_table, ta
     _check(_lib.kvx_cache_attend(cache.handle, layer, _ptr(q), q_stride, _ptr(block_table), table_stride, max_blocks,
                                  _ptr(seq_len), n_reqs, _ptr(out), out_stride, _ptr(lse), _stream(stream)),
            "kvx_cache_attend")
+
+
+def kvx_pages_free(block_table, table_stride: int, max_blocks: int, seq_len, n_reqs: int, block_size: int, n_blocks: int,
+                   refs, free_blocks, result, stream=None) -> None:
+    """result: three device int64 (n_held, n_blocks, status)."""
+    _check(_lib.kvx_pages_free(_ptr(block_table), table_stride, max_blocks, _ptr(seq_len), n_reqs, block_size, n_blocks,
+                               _ptr(refs), _ptr(free_blocks), _ptr(result), _stream(stream)), "kvx_pages_free")
+
+
+def kvx_pages_fork(block_table, table_stride: int, max_blocks: int, seq_len, n_reqs: int, parent, n_out: int, block_size: int,
+                   free_blocks, n_free: int, new_table, new_stride: int, new_len, src_blocks, dst_blocks, scratch, result,
+                   stream=None) -> None:
+    """result: three device int64 (n_held, n_blocks, status)."""
+    _check(_lib.kvx_pages_fork(_ptr(block_table), table_stride, max_blocks, _ptr(seq_len), n_reqs, _ptr(parent), n_out,
+                               block_size, _ptr(free_blocks), n_free, _ptr(new_table), new_stride, _ptr(new_len),
+                               _ptr(src_blocks), _ptr(dst_blocks), _ptr(scratch), _ptr(result), _stream(stream)),
+           "kvx_pages_fork")
+
+
+def kvx_pages_compact(block_table, table_stride: int, max_blocks: int, seq_len, n_reqs: int, block_size: int, refs,
+                      n_blocks: int, new_table, new_stride: int, src_blocks, dst_blocks, max_moves: int, result,
+                      stream=None) -> None:
+    """result: three device int64 (n_held, n_blocks, status)."""
+    _check(_lib.kvx_pages_compact(_ptr(block_table), table_stride, max_blocks, _ptr(seq_len), n_reqs, block_size, _ptr(refs),
+                                  n_blocks, _ptr(new_table), new_stride, _ptr(src_blocks), _ptr(dst_blocks), max_moves,
+                                  _ptr(result), _stream(stream)), "kvx_pages_compact")
+
+
+def kvx_cache_copy(cache: Cache, layer_begin: int, layer_end: int, src_blocks, dst_blocks, n_pairs: int, stream=None) -> None:
+    _check(_lib.kvx_cache_copy(cache.handle, layer_begin, layer_end, _ptr(src_blocks), _ptr(dst_blocks), n_pairs,
+                               _stream(stream)), "kvx_cache_copy")
 
 
 def kvx_cache_status(cache: Cache, stream=None) -> int:

@@ -558,9 +558,9 @@ typedef struct kvx_cache_s *kvx_cache_t;
 
 /*
  * kvx_cache_create -- a typed handle on a pool, for the two calls below. The pool's counts and buffer
- * pointers are copied; its memory stays the caller's. No CUDA call is made here: the first append or
- * attend allocates the handle's scratch (device memory of the current device, 13 MiB, or 20 MiB for latents) and waits for
- * it, so make that first call before any stream capture (KVX_EINVAL inside one).
+ * pointers are copied; its memory stays the caller's. No CUDA call is made here: the first call that runs on the
+ * device (an append, attend or copy) allocates the handle's scratch (device memory of the current device, 13 MiB, or 20 MiB for
+ * latents) and waits for it, so make that first call before any stream capture (KVX_EINVAL inside one).
  * Refused: KVX_EINVAL for what contradicts the pool (types and elem_bytes, head counts, v_dim, negative
  * or non-finite values, reserved != 0), KVX_EUNSUPPORTED for more than 64 shards, 2^31 - 1 rows in a
  * buffer or more, head rows (head_dim * elem_bytes, and v_dim * elem_bytes) that are not whole 16-byte
@@ -605,7 +605,70 @@ kvx_status kvx_cache_attend(kvx_cache_t cache, int32_t layer, const void *q, int
                             const int32_t *seq_len, int32_t n_reqs, void *out, int64_t out_stride, float *lse,
                             cudaStream_t stream);
 
-/* Waits for `stream` and returns KVX_ERANGE when an append or attend enqueued on the handle since the
+/* ------------------------------------------------------------------------------------------------
+ * Pages that several requests hold. The tables and lengths alone say who holds what: row r of a table holds its first
+ * ceil(seq_len[r] / block_size) blocks, and a block may stand in several rows. So there are no counts to keep: a request ends by
+ * its length becoming 0, kvx_pages_free then finds the blocks that no row holds, kvx_pages_fork makes the rows of the next step from
+ * those of the last one (samples, beams, requests that ended or moved), and kvx_pages_compact says which blocks to move so that
+ * those in use are the first of the pool; kvx_cache_copy moves them. As for the calls above, tables, lengths and ids are device arrays,
+ * checked on the device, and the calls only enqueue.
+ * ---------------------------------------------------------------------------------------------- */
+
+/* What the calls on pages found (device). */
+typedef struct kvx_page_result {
+    int64_t n_held;        /* blocks that some row holds; kvx_pages_fork: blocks of all new rows, each row's counted */
+    int64_t n_blocks;      /* kvx_pages_free: ids written to free_blocks; kvx_pages_fork: pages to copy, and entries of free_blocks taken or,
+                              when there are too few, needed; kvx_pages_compact: blocks to move */
+    int64_t status;        /* KVX_OK; KVX_ERANGE: a length that is negative or beyond max_blocks * block_size (cut there), a block id
+                              outside the pool or a row of `parent` outside the table (left out); KVX_ENOMEM: n_blocks > n_free or > max_moves */
+} kvx_page_result;
+
+/*
+ * kvx_pages_free -- which blocks of a pool no request holds.
+ * refs[b] (n_blocks entries): how many table entries hold block b. free_blocks (room for n_blocks ids): the blocks that none
+ * holds, ascending, what kvx_slot_map and kvx_pages_fork take; entries behind the last are left as they were.
+ */
+kvx_status kvx_pages_free(const int32_t *block_table, int64_t table_stride, int32_t max_blocks, const int32_t *seq_len, int32_t n_reqs,
+                          int32_t block_size, int64_t n_blocks, int32_t *refs, int32_t *free_blocks, kvx_page_result *result,
+                          cudaStream_t stream);
+
+/*
+ * kvx_pages_fork -- the rows of a new table from those of another: row i goes on from request parent[i] (-1: from none, an
+ * empty row), with its length and its blocks. Rows may share a parent in any order and number; a request that is no row's parent
+ * has ended. Full blocks are shared. A last block that is only in part filled will be written to, so the first row (the lowest i) that
+ * goes on from a request keeps it and each other one gets a block of its own: in row order the next entries of free_blocks, with
+ * the pair (src_blocks[k], dst_blocks[k]) for kvx_cache_copy, to be made before either row is appended to. src_blocks and dst_blocks
+ * have n_out entries, -1 behind the last pair. Without enough free blocks (KVX_ENOMEM) the rows that lack one have -1 there.
+ * new_table: n_out rows of max_blocks entries, new_stride apart, -1 behind a row's blocks; new_len: n_out lengths. Neither may
+ * overlap the table or the lengths they come from. scratch: n_reqs entries, in no particular state.
+ */
+kvx_status kvx_pages_fork(const int32_t *block_table, int64_t table_stride, int32_t max_blocks, const int32_t *seq_len, int32_t n_reqs,
+                          const int32_t *parent, int32_t n_out, int32_t block_size, const int32_t *free_blocks, int64_t n_free,
+                          int32_t *new_table, int64_t new_stride, int32_t *new_len, int32_t *src_blocks, int32_t *dst_blocks,
+                          int32_t *scratch, kvx_page_result *result, cudaStream_t stream);
+
+/*
+ * kvx_pages_compact -- the moves after which the L blocks that are held are the blocks [0, L).
+ * refs: as kvx_pages_free left it for this table. The held blocks from L on, ascending, go to the free ones below L, ascending:
+ * pairs (src_blocks[k], dst_blocks[k]) for kvx_cache_copy, which have to be copied before the new rows are read; -1 behind the
+ * last, up to max_moves. new_table: the rows with their blocks' new ids, other entries as they were; the table itself or memory apart
+ * from it. With more than max_moves moves (KVX_ENOMEM) there are no pairs and the rows stay as they are. Afterwards [L, n_blocks) are free.
+ * A table entry that refs does not count keeps its id, and status is KVX_ERANGE.
+ */
+kvx_status kvx_pages_compact(const int32_t *block_table, int64_t table_stride, int32_t max_blocks, const int32_t *seq_len, int32_t n_reqs,
+                             int32_t block_size, const int32_t *refs, int64_t n_blocks, int32_t *new_table, int64_t new_stride,
+                             int32_t *src_blocks, int32_t *dst_blocks, int64_t max_moves, kvx_page_result *result, cudaStream_t stream);
+
+/*
+ * kvx_cache_copy -- whole blocks of the cache's pool, block src_blocks[k] to block dst_blocks[k] for k < n_pairs, in every plane and
+ * shard of the layers [layer_begin, layer_end). A pair of -1 and -1 is no copy; other ids outside the pool are skipped, and
+ * kvx_cache_status reports them. No block may be the destination of one pair and in another one (either contents may be read, or
+ * parts of either left): kvx_pages_fork and kvx_pages_compact give no such pairs.
+ */
+kvx_status kvx_cache_copy(kvx_cache_t cache, int32_t layer_begin, int32_t layer_end, const int32_t *src_blocks, const int32_t *dst_blocks,
+                          int32_t n_pairs, cudaStream_t stream);
+
+/* Waits for `stream` and returns KVX_ERANGE when a call enqueued on the handle since the
  * last call here skipped a slot, a block or a length out of bounds, KVX_ETIMEDOUT when a copy into shared
  * memory did not arrive within 2 s (the outputs are then not valid), else KVX_OK. */
 kvx_status kvx_cache_status(kvx_cache_t cache, cudaStream_t stream);
