@@ -17,7 +17,8 @@ LIB = os.path.join(PKG, "libkvx.so")
 SOURCES = ["kvx_plan.cpp", "kvx_tiles.cpp", "kvx_conn.cpp", "kvx_copy.cu", "kvx_push.cu", "kvx_match.cu", "kvx_cache.cpp",
            "kvx_slots.cu", "kvx_append.cu", "kvx_attend.cu", "kvx_attend_bf16.cu",
            "kvx_attend_f16.cu", "kvx_attend_e4m3_bf16.cu", "kvx_attend_e4m3_f16.cu", "kvx_latent.cu",
-           "kvx_latent_tensor.cu", "kvx_page_calls.cpp", "kvx_pages.cu"]
+           "kvx_latent_tensor.cu", "kvx_page_calls.cpp", "kvx_pages.cu", "kvx_rotation.cpp",
+           "kvx_rotate.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O3", "-I", INCLUDE, "-I", CSRC]
 

@@ -290,6 +290,25 @@ cudaError_t launch_pages_fork(const ForkArgs &a, cudaStream_t stream);
 cudaError_t launch_pages_compact(const CompactArgs &a, cudaStream_t stream);
 cudaError_t launch_cache_copy(const PageCopyArgs &a, int32_t sms, cudaStream_t stream);
 
+// ---- norm and rotation on the way into the cache (kvx_rotation.cpp, kvx_rotate.cu) ----
+constexpr int32_t kRotateMaxPairs = 128;
+struct RotateArgs {
+    CacheLayer pool;
+    const uint8_t *q, *k, *v, *q_weight, *k_weight;        // weights NULL: no norm
+    uint8_t *q_out;
+    const int32_t *positions;
+    const int64_t *slots;
+    int64_t q_stride, k_stride, v_stride, out_stride;      // bytes
+    int64_t n_tokens, n_rows;         // n_rows: slots of the pool
+    int32_t n_q_heads, n_kv_heads, head_dim, planes;
+    int32_t parts;                    // that a token's heads are cut into
+    int32_t begin, turned, norm_dim;  // elements [begin, begin + turned) turn, the first norm_dim are normed
+    bool pairs;
+    float norm_inverse, eps, magnitude, k_inverse, v_inverse;
+    uint64_t turns[kRotateMaxPairs];  // frequencies, in 2^-64 turns a position
+};
+cudaError_t launch_rotate(const RotateArgs &a, int32_t value_type, int32_t io_type, int32_t sms, cudaStream_t stream);
+
 // ---- the handle, for the other files with calls on it (kvx_cache.cpp) ----
 kvx_status cache_check_layer(kvx_cache_t c, int32_t layer);
 kvx_status cache_ready(kvx_cache_t c, cudaStream_t stream);                    // its scratch, allocated by the first call that needs it
@@ -311,6 +330,13 @@ struct kvx_cache_s {
     int32_t stall = 0;                         // kvx_cache_inject_stall: part of the next attend
     uint8_t *dev = nullptr;                    // [256 bytes: skipped][scratch of the attend kernels]
     uint8_t *const *dev_bases = nullptr;       // behind it: `base` on the device
+};
+
+// The object behind kvx_rotation_t.
+struct kvx_rotation_s {
+    kvx_rotation_config cfg{};                 // defaults filled in
+    double frequency[kvx::kRotateMaxPairs] = {};
+    uint64_t turns[kvx::kRotateMaxPairs] = {};
 };
 
 // The plan object behind kvx_plan_t.

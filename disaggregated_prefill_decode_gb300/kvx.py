@@ -76,6 +76,17 @@ class kvx_cache_config(ctypes.Structure):
                 ("reserved", c_i32 * 4)]
 
 
+KVX_ROTATE_HALVES, KVX_ROTATE_PAIRS = 0, 1
+KVX_ROTATE_PLAIN, KVX_ROTATE_LINEAR, KVX_ROTATE_BANDS, KVX_ROTATE_YARN = range(4)
+c_double = ctypes.c_double
+
+
+class kvx_rotation_config(ctypes.Structure):
+    _fields_ = [("layout", c_i32), ("scaling", c_i32), ("begin", c_i32), ("dim", c_i32), ("norm_dim", c_i32),
+                ("eps", ctypes.c_float), ("base", c_double), ("factor", c_double), ("low", c_double), ("high", c_double),
+                ("original", c_double), ("magnitude", c_double), ("reserved", c_i32 * 4)]
+
+
 MATCH_RESULT_DTYPE = np.dtype([("local_hit_blocks", "<i4"), ("remote_hit_blocks", "<i4"), ("missing_tokens", "<i4"),
                                ("push", "<i4"), ("dst_start", "<i8")])
 assert MATCH_RESULT_DTYPE.itemsize == ctypes.sizeof(kvx_match_result)
@@ -137,6 +148,11 @@ _sig = {
     "kvx_cache_destroy": (c_i32, [c_vp]),
     "kvx_cache_append": (c_i32, [c_vp, c_i32, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp]),
     "kvx_cache_attend": (c_i32, [c_vp, c_i32, c_vp, c_i64, c_vp, c_i64, c_i32, c_vp, c_i32, c_vp, c_i64, c_vp, c_vp]),
+    "kvx_rotation_create": (c_i32, [_P(kvx_rotation_config), _P(c_vp)]),
+    "kvx_rotation_destroy": (c_i32, [c_vp]),
+    "kvx_rotation_get": (c_i32, [c_vp, _P(c_double), c_i32, _P(c_i32), _P(c_double)]),
+    "kvx_cache_append_rotated": (c_i32, [c_vp, c_i32, c_vp, c_vp, c_i64, c_vp, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_i64, c_vp,
+                                         c_vp, c_i64, c_vp]),
     "kvx_pages_free": (c_i32, [c_vp, c_i64, c_i32, c_vp, c_i32, c_i32, c_i64, c_vp, c_vp, c_vp, c_vp]),
     "kvx_pages_fork": (c_i32, [c_vp, c_i64, c_i32, c_vp, c_i32, c_vp, c_i32, c_i32, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp,
                                c_vp, c_vp, c_vp, c_vp]),
@@ -525,6 +541,53 @@ def kvx_cache_append(cache: Cache, layer: int, k, k_stride: int, v, v_stride: in
                      stream=None) -> None:
     _check(_lib.kvx_cache_append(cache.handle, layer, _ptr(k), k_stride, _ptr(v), v_stride, _ptr(slots), n_tokens,
                                  _stream(stream)), "kvx_cache_append")
+
+
+class Rotation:
+    """Owns a kvx_rotation_t; kvx_rotation_destroy (or `with`, or the last reference) frees it."""
+
+    def __init__(self, handle: int):
+        self.handle = handle
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        kvx_rotation_destroy(self)
+
+    def __del__(self):
+        if self.handle:
+            _lib.kvx_rotation_destroy(self.handle)
+
+
+def kvx_rotation_create(layout: int = KVX_ROTATE_HALVES, begin: int = 0, dim: int = 0, scaling: int = KVX_ROTATE_PLAIN,
+                        base: float = 0.0, factor: float = 0.0, low: float = 0.0, high: float = 0.0, original: float = 0.0,
+                        magnitude: float = 0.0, norm_dim: int = 0, eps: float = 0.0) -> Rotation:
+    cfg = kvx_rotation_config(layout, scaling, begin, dim, norm_dim, eps, base, factor, low, high, original, magnitude)
+    out = c_vp()
+    _check(_lib.kvx_rotation_create(ctypes.byref(cfg), ctypes.byref(out)), "kvx_rotation_create")
+    return Rotation(out.value)
+
+
+def kvx_rotation_destroy(rotation: Rotation) -> None:
+    h, rotation.handle = rotation.handle, 0
+    if h:
+        _check(_lib.kvx_rotation_destroy(h), "kvx_rotation_destroy")
+
+
+def kvx_rotation_get(rotation: Rotation) -> tuple:
+    """(frequencies in radians a position, magnitude)"""
+    n, m, f = c_i32(), c_double(), np.zeros(128)
+    _check(_lib.kvx_rotation_get(rotation.handle, f.ctypes.data_as(_P(c_double)), len(f), ctypes.byref(n), ctypes.byref(m)),
+           "kvx_rotation_get")
+    return f[:n.value], m.value
+
+
+def kvx_cache_append_rotated(cache: Cache, layer: int, rotation: Rotation, q, q_stride: int, q_weight, q_out, q_out_stride: int,
+                             k, k_stride: int, k_weight, v, v_stride: int, positions, slots, n_tokens: int, stream=None) -> None:
+    _check(_lib.kvx_cache_append_rotated(cache.handle, layer, rotation.handle, _ptr(q), q_stride, _ptr(q_weight), _ptr(q_out),
+                                         q_out_stride, _ptr(k), k_stride, _ptr(k_weight), _ptr(v), v_stride, _ptr(positions),
+                                         _ptr(slots), n_tokens, _stream(stream)), "kvx_cache_append_rotated")
 
 
 def kvx_cache_attend(cache: Cache, layer: int, q, q_stride: int, block_table, table_stride: int, max_blocks: int,

@@ -584,6 +584,57 @@ kvx_status kvx_cache_destroy(kvx_cache_t cache);   /* waits for the device; NULL
 kvx_status kvx_cache_append(kvx_cache_t cache, int32_t layer, const void *k, int64_t k_stride, const void *v,
                             int64_t v_stride, const int64_t *slots, int64_t n_tokens, cudaStream_t stream);
 
+/* How the elements of a head pair up and turn. Zero fields take the defaults. */
+#define KVX_ROTATE_HALVES 0     /* layout: element i turns with i + dim / 2 of the part that turns */
+#define KVX_ROTATE_PAIRS 1      /* element 2i with 2i + 1 */
+#define KVX_ROTATE_PLAIN 0      /* scaling: pair i turns by f_i = base^(-2i / dim) radians a position */
+#define KVX_ROTATE_LINEAR 1     /* f_i / factor */
+#define KVX_ROTATE_BANDS 2      /* by the turns t = original * f_i / 2 pi over the original context: f_i / factor up to t = low, f_i from
+                                   t = high, between them f_i (r + (1 - r) / factor) with r = (t - low) / (high - low) */
+#define KVX_ROTATE_YARN 3       /* f_i ((1 - r) + r / factor), r rising from 0 to 1 between the pairs that make `high` (0: 32) and `low`
+                                   (0: 1) turns over the original context: those pairs, dim ln(original / (2 pi turns)) / (2 ln base),
+                                   rounded down and up and kept within [0, dim - 1] */
+typedef struct kvx_rotation_config {
+    int32_t layout;
+    int32_t scaling;
+    int32_t begin, dim;    /* elements [begin, begin + dim) of a head turn, the others stay; dim 0: none turn */
+    int32_t norm_dim;      /* the first norm_dim elements of a head are normed together (0: all of it) */
+    float eps;             /* of the norm (0: 1e-6) */
+    double base;           /* 0: 10000 */
+    double factor;         /* >= 1, of the context's length; scaling other than PLAIN */
+    double low, high;      /* turns; BANDS, YARN */
+    double original;       /* positions of the original context; BANDS, YARN */
+    double magnitude;      /* factor of what has turned (0: 1, with YARN 0.1 ln(factor) + 1) */
+    int32_t reserved[4];   /* must be 0 */
+} kvx_rotation_config;
+
+typedef struct kvx_rotation_s *kvx_rotation_t;
+
+/*
+ * kvx_rotation_create -- the frequencies of a rotation, computed once in 64 bits (host only; no CUDA call). A rotation is never
+ * changed, so any number of caches, threads and captured graphs may use one; it may be destroyed once the calls that name it returned.
+ * KVX_EUNSUPPORTED for begin or norm_dim that are no multiples of 8, dim no multiple of 16 (8 for PAIRS) or above 256.
+ * kvx_rotation_get: up to cap frequencies in radians a position (*n receives their number, dim / 2) and the magnitude.
+ */
+kvx_status kvx_rotation_create(const kvx_rotation_config *cfg, kvx_rotation_t *out);
+kvx_status kvx_rotation_destroy(kvx_rotation_t rotation);   /* NULL is a no-op */
+kvx_status kvx_rotation_get(kvx_rotation_t rotation, double *frequencies, int32_t cap, int32_t *n, double *magnitude);
+
+/*
+ * kvx_cache_append_rotated -- kvx_cache_append with what stands before it: every head of the queries and keys is normed, if
+ * there is a weight for it, y = x / sqrt(mean(x^2) + eps) * weight (norm_dim values in io_type, the same for all heads), and its pairs
+ * turned by the token's position, (a, b) -> magnitude * (a cos - b sin, b cos + a sin). Keys, and values as they are, go to
+ * their slots of one layer, queries to q_out: [n_tokens][n_q_heads][head_dim], which may be q itself (with q's stride) and else
+ * overlaps no input. All of it in 32 bits with one rounding at the end, 8-bit codes as in kvx_cache_append; an angle is the position
+ * times a 64-bit frequency, 2^-32 of a turn off at most (the squares' sum must stay below 2^128). q and q_out may both be NULL. positions: as kvx_slot_map
+ * makes them, any int32; NULL if dim is 0. A token with slot -1 is skipped, its row of q_out left as it was; so is one with another slot outside
+ * the pool, and kvx_cache_status reports it. Pointers and strides (elements) are multiples of 16 bytes.
+ */
+kvx_status kvx_cache_append_rotated(kvx_cache_t cache, int32_t layer, kvx_rotation_t rotation, const void *q, int64_t q_stride,
+                                    const void *q_weight, void *q_out, int64_t q_out_stride, const void *k, int64_t k_stride,
+                                    const void *k_weight, const void *v, int64_t v_stride, const int32_t *positions, const int64_t *slots,
+                                    int64_t n_tokens, cudaStream_t stream);
+
 /*
  * kvx_cache_attend -- attention of one new token of each request over its cached tokens in one layer.
  * With the positions t of the last `window` (or all) of request r's seq_len[r] cached tokens:
