@@ -18,7 +18,9 @@ SOURCES = ["kvx_plan.cpp", "kvx_tiles.cpp", "kvx_conn.cpp", "kvx_copy.cu", "kvx_
            "kvx_slots.cu", "kvx_append.cu", "kvx_attend.cu", "kvx_attend_bf16.cu",
            "kvx_attend_f16.cu", "kvx_attend_e4m3_bf16.cu", "kvx_attend_e4m3_f16.cu", "kvx_latent.cu",
            "kvx_latent_tensor.cu", "kvx_page_calls.cpp", "kvx_pages.cu", "kvx_rotation.cpp",
-           "kvx_rotate.cu"]
+           "kvx_rotate.cu", "kvx_shared_calls.cpp", "kvx_shared.cu", "kvx_shared_bf16.cu", "kvx_shared_f16.cu",
+           "kvx_shared_e4m3_bf16.cu", "kvx_shared_e4m3_f16.cu", "kvx_rest_bf16.cu", "kvx_rest_f16.cu", "kvx_rest_e4m3_bf16.cu",
+           "kvx_rest_e4m3_f16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O3", "-I", INCLUDE, "-I", CSRC]
 

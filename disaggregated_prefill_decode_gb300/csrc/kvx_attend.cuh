@@ -100,24 +100,26 @@ struct Split {
 
 // A request's live positions [first, len) and its tiles of TOK positions, aligned to TOK; at least one, so that an
 // empty request is answered too.
-template <int TOK> struct Span {
+// REST: those from start[r] on, where kvx_cache_attend_shared has taken the ones before.
+template <int TOK, bool REST = false> struct Span {
     int32_t len, first, tiles;
     __device__ __forceinline__ Span(const AttendArgs &a, int32_t r) {
         const int64_t cap = (int64_t)a.max_blocks * a.pool.block_size;
         len = (int32_t)min((int64_t)max(a.seq_len[r], 0), cap);
         first = a.window ? max(0, len - a.window) : 0;
+        if constexpr (REST) first = max(first, min(a.start[r], len));
         tiles = max(1, (int32_t)(((uint32_t)len + TOK - 1) / TOK) - first / TOK);
     }
 };
 
 // Where a tile stands in the line. A segment has EXTRA places after its tiles, for what the change to the next one costs: they
 // make the stretches even in time.
-template <int TOK, int EXTRA> struct Place {
+template <int TOK, int EXTRA, bool REST = false> struct Place {
     int32_t r, seg, tile;      // request, segment of the request, tile of the segment
     int64_t before;            // places of the requests before r, per segment
     int32_t len, first, tiles;
     __device__ __forceinline__ void request(const AttendArgs &a) {
-        const Span<TOK> s(a, r);
+        const Span<TOK, REST> s(a, r);
         len = s.len;
         first = s.first;
         tiles = s.tiles;
@@ -172,7 +174,7 @@ constexpr int kJoinTiles = 600;    // see Batch
 // 31.7, 38.5. PIECES 0: always all CTAs.
 // Up to 256 requests each warp keeps all the sums, a lane those of up to 8 consecutive requests, with no barrier; beyond that
 // the CTA looks for the request in which its own stretch begins, and its warps go on from there.
-template <int TOK, int WARPS, int MIN, int EXTRA, int PIECES> struct Batch {
+template <int TOK, int WARPS, int MIN, int EXTRA, int PIECES, bool REST = false> struct Batch {
     static constexpr int PER = 8;
     Split split;
     int32_t per;                       // requests of a lane
@@ -187,7 +189,7 @@ template <int TOK, int WARPS, int MIN, int EXTRA, int PIECES> struct Batch {
         int64_t total = 0;
         per = (a.n_reqs + 31) / 32;
         if (per <= PER) {
-            tiles[0] = lane * per < a.n_reqs ? Span<TOK>(a, lane * per).tiles + EXTRA : 0;
+            tiles[0] = lane * per < a.n_reqs ? Span<TOK, REST>(a, lane * per).tiles + EXTRA : 0;
             int64_t mine = tiles[0];
 #pragma unroll
             for (int k = 1; k < PER; ++k) tiles[k] = 0;
@@ -195,14 +197,14 @@ template <int TOK, int WARPS, int MIN, int EXTRA, int PIECES> struct Batch {
 #pragma unroll
                 for (int k = 1; k < PER; ++k) {
                     const int32_t r = lane * per + k;
-                    if (k < per && r < a.n_reqs) tiles[k] = Span<TOK>(a, r).tiles + EXTRA;
+                    if (k < per && r < a.n_reqs) tiles[k] = Span<TOK, REST>(a, r).tiles + EXTRA;
                     mine += tiles[k];
                 }
             upto = warp_inclusive(mine);
             total = __shfl_sync(~0u, upto, 31);
         } else {
             int64_t mine = 0;
-            for (int32_t r = threadIdx.x; r < a.n_reqs; r += 32 * WARPS) mine += Span<TOK>(a, r).tiles + EXTRA;
+            for (int32_t r = threadIdx.x; r < a.n_reqs; r += 32 * WARPS) mine += Span<TOK, REST>(a, r).tiles + EXTRA;
             cta_exclusive<WARPS>(mine, &total);
         }
         split.tiles = total * segs;
@@ -225,7 +227,7 @@ template <int TOK, int WARPS, int MIN, int EXTRA, int PIECES> struct Batch {
         int64_t base = 0, total;
         for (int32_t c = 0; c < a.n_reqs && base <= y; c += 32 * WARPS) {
             const int32_t r = c + threadIdx.x;
-            const int64_t mine = r < a.n_reqs ? Span<TOK>(a, r).tiles + EXTRA : 0, ex = base + cta_exclusive<WARPS>(mine, &total);
+            const int64_t mine = r < a.n_reqs ? Span<TOK, REST>(a, r).tiles + EXTRA : 0, ex = base + cta_exclusive<WARPS>(mine, &total);
             if (ex <= y && y < ex + mine) {
                 s_r = r;
                 s_before = ex;
@@ -238,10 +240,10 @@ template <int TOK, int WARPS, int MIN, int EXTRA, int PIECES> struct Batch {
     }
 
     // Whole warp: the first tile at or after place x of the line, to which x is moved.
-    __device__ __forceinline__ Place<TOK, EXTRA> locate(const AttendArgs &a, int32_t segs, int64_t &x) const {
+    __device__ __forceinline__ Place<TOK, EXTRA, REST> locate(const AttendArgs &a, int32_t segs, int64_t &x) const {
         const int lane = threadIdx.x & 31;
         const int64_t y = divide(x, segs);
-        Place<TOK, EXTRA> p;
+        Place<TOK, EXTRA, REST> p;
         if (per <= PER) {
             const int at = __ffs(__ballot_sync(~0u, upto > y)) - 1;
             int64_t left = upto;
@@ -255,7 +257,7 @@ template <int TOK, int WARPS, int MIN, int EXTRA, int PIECES> struct Batch {
             int32_t r = r0;
             int64_t before = before0;
             for (;;) {
-                const int64_t n = r + lane < a.n_reqs ? Span<TOK>(a, r + lane).tiles + EXTRA : 0;
+                const int64_t n = r + lane < a.n_reqs ? Span<TOK, REST>(a, r + lane).tiles + EXTRA : 0;
                 const int64_t in = before + warp_inclusive(n);
                 const uint32_t past = __ballot_sync(~0u, in > y);
                 const int at = past ? __ffs(past) - 1 : 31;

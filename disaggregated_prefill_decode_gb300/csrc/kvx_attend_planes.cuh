@@ -37,6 +37,7 @@ constexpr int kJoinAtOnce = 24;               // pieces of a segment that a warp
 template <int VT_, int IO_, int D_, int NT_, bool FULL_> struct Shape {
     static constexpr int VT = VT_, IO = IO_, D = D_, NT = NT_;   // D: head_dim rounded up; NT: query sets of 8
     static constexpr bool FULL = FULL_;                           // head_dim is D
+    static constexpr bool REST = false;                           // see RestShape
     static constexpr bool F8 = VT == KVX_E4M3;
     static constexpr int MT = F8 ? KVX_F16 : VT;                  // type of the products
     // f16 weights are taken times 2^15, by a reference m that far below the maximum: one of 2^-39 of the largest still has a
@@ -80,6 +81,12 @@ template <int VT_, int IO_, int D_, int NT_, bool FULL_> struct Shape {
     static __device__ __forceinline__ int dim(int g, int e) { return e / PE * (8 * PE) + g * PE + e % PE; }
 };
 
+// The positions of requests behind the prefixes that kvx_cache_attend_shared has taken: in the place of outputs, sums in 32 bits
+// that its last kernel joins with those of the prefixes.
+template <class S> struct RestShape : S {
+    static constexpr bool REST = true;
+};
+
 // A partial result in shared memory or in the scratch: O as [set][query of the lane's two][e / 4][lane] float4 of four
 // value elements, then m and l of the queries.
 template <class S> struct Partial {
@@ -116,6 +123,12 @@ template <class S> struct Joined {
         const int lane = threadIdx.x & 31, g = lane >> 2;
         if (!to) {
             const int d = S::dim(g, e4 * 4);
+            if constexpr (S::REST) {
+                const int64_t row = (int64_t)r * a.n_q_heads + head0 + q;
+                if (q < heads && (S::FULL || d < a.head_dim)) *reinterpret_cast<float4 *>(a.rest + row * a.head_dim + d) = o;
+                if (q < heads && e4 == 0 && g == 0) a.rest_ml[row] = make_float2(top, l);
+                return;
+            }
             if (q < heads && (S::FULL || d < a.head_dim)) {
                 const float inv = l == 0.0f ? 0.0f : a.v_scale / l;
                 const uint2 y = make_uint2(pack<S::IO>(o.x * inv, o.y * inv), pack<S::IO>(o.z * inv, o.w * inv));
@@ -247,7 +260,7 @@ template <int TOK, class Line> struct Row {
 
 template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_planes(const __grid_constant__ AttendArgs a) {
     constexpr int TOK = S::TOK, NT = S::NT;
-    using Line = Place<TOK, kSwitchTiles>;
+    using Line = Place<TOK, kSwitchTiles, S::REST>;
     extern __shared__ __align__(16) uint8_t smem[];                // [warp] ring and partial result
     __shared__ int64_t s_seg[S::WARPS][2];                     // first tile of each one's segment; -1: none
     __shared__ int32_t s_where[S::WARPS][2][3];                // request, segment of the request, tiles
@@ -256,7 +269,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
     const int32_t group = a.n_q_heads / a.n_kv_heads, sets = (group + 8 * NT - 1) / (8 * NT), segs = a.n_kv_heads * sets;
 
     wait_for_earlier();
-    const Batch<TOK, S::WARPS, S::WARPS, kSwitchTiles, kJoinAtOnce> batch(a, segs);
+    const Batch<TOK, S::WARPS, S::WARPS, kSwitchTiles, kJoinAtOnce, S::REST> batch(a, segs);
     const Split &split = batch.split;
     if ((int32_t)blockIdx.x >= split.ctas) return;
     uint32_t *const arrived = (uint32_t *)a.scratch;
@@ -373,6 +386,18 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
                     for (int i = 0; i < 2; ++i) {
                         const int32_t qi = first + n * 8 + 2 * t + i, head = kvh * group + qi;
                         if (qi >= group) continue;
+                        if constexpr (S::REST) {
+                            const int64_t row = (int64_t)p.r * a.n_q_heads + head;
+#pragma unroll
+                            for (int e = 0; e < S::NE / 2; e += 2) {
+                                const int d = S::dim(g, 2 * e);
+                                if (S::FULL || d < a.head_dim)
+                                    *reinterpret_cast<float4 *>(a.rest + row * a.head_dim + d) =
+                                        make_float4(o[n][e][i], o[n][e][2 + i], o[n][e + 1][i], o[n][e + 1][2 + i]);
+                            }
+                            if (g == 0) a.rest_ml[row] = make_float2(m[n][i], l[n][i]);
+                            continue;
+                        }
                         const float inv = l[n][i] == 0.0f ? 0.0f : a.v_scale / l[n][i];
                         uint8_t *dst = a.out + p.r * a.out_stride + (int64_t)head * a.head_dim * 2;
 #pragma unroll
@@ -648,6 +673,16 @@ template <int VT, int IO> static cudaError_t launch_planes(const AttendArgs &a, 
     if (a.head_dim <= 64) return wide ? launch<VT, IO, 64, 2>(a, sms, stream) : launch<VT, IO, 64, 1>(a, sms, stream);
     if (a.head_dim <= 128) return wide ? launch<VT, IO, 128, 2>(a, sms, stream) : launch<VT, IO, 128, 1>(a, sms, stream);
     return launch<VT, IO, 256, 1>(a, sms, stream);
+}
+
+// The same for the rest of requests, head dims up to 128.
+template <int VT, int IO, int D, int NT> static cudaError_t launch_rest_shape(const AttendArgs &a, int32_t sms, cudaStream_t stream) {
+    return a.head_dim == D ? launch<RestShape<Shape<VT, IO, D, NT, true>>>(a, sms, stream) : launch<RestShape<Shape<VT, IO, D, NT, false>>>(a, sms, stream);
+}
+template <int VT, int IO> static cudaError_t launch_rest_planes(const AttendArgs &a, int32_t sms, cudaStream_t stream) {
+    const bool wide = a.n_q_heads / a.n_kv_heads > 8;
+    if (a.head_dim <= 64) return wide ? launch_rest_shape<VT, IO, 64, 2>(a, sms, stream) : launch_rest_shape<VT, IO, 64, 1>(a, sms, stream);
+    return wide ? launch_rest_shape<VT, IO, 128, 2>(a, sms, stream) : launch_rest_shape<VT, IO, 128, 1>(a, sms, stream);
 }
 
 }  // namespace kvx

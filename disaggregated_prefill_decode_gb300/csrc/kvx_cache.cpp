@@ -20,7 +20,7 @@ void kvx::divisor(uint32_t d, uint32_t *mul, uint32_t *shift) {
 }
 
 // Multiprocessors of the current device, asked for once.
-static kvx_status device_sms(int32_t *device, int32_t *sms) {
+kvx_status kvx::device_sms(int32_t *device, int32_t *sms) {
     static std::atomic<int32_t> known[64];
     int dev = 0, n = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -128,6 +128,68 @@ kvx_status kvx::cache_check_layer(kvx_cache_t c, int32_t layer) {
     if (!c) return fail(KVX_EINVAL, "cache is NULL");
     if (layer < 0 || layer >= c->g.n_layers) return fail(KVX_EINVAL, "layer %d of %d", layer, c->g.n_layers);
     return KVX_OK;
+}
+
+// The arguments of kvx_cache_attend.
+kvx_status kvx::cache_check_attend(kvx_cache_t c, int32_t layer, const void *q, int64_t q_stride, const int32_t *block_table,
+                    int64_t table_stride, int32_t max_blocks, const int32_t *seq_len, int32_t n_reqs, void *out, int64_t out_stride, float *lse) {
+    kvx_status st = cache_check_layer(c, layer);
+    if (st) return st;
+    const Geom &g = c->g;
+    const kvx_cache_config &f = c->cfg;
+    if (f.v_dim > kCacheMaxLatentValue) return fail(KVX_EUNSUPPORTED, "attention over latents with v_dim %d", f.v_dim);
+    if (n_reqs < 0 || n_reqs > (1 << 24)) return fail(KVX_EINVAL, "n_reqs %d not in [0, 2^24]", n_reqs);
+    if (max_blocks < 0 || table_stride < max_blocks) return fail(KVX_EINVAL, "max_blocks must be >= 0, table_stride >= max_blocks");
+    if (n_reqs && (!q || !out || !seq_len || (max_blocks && !block_table)))
+        return fail(KVX_EINVAL, "q, out, seq_len or block_table is NULL");
+    if (n_reqs > 1 && (q_stride < (int64_t)f.n_q_heads * g.head_dim || out_stride < (int64_t)f.n_q_heads * f.v_dim))
+        return fail(KVX_EINVAL, "strides below a request's elements");
+    if (q_stride > ((int64_t)1 << 40) || out_stride > ((int64_t)1 << 40)) return fail(KVX_EINVAL, "stride above 2^40");
+    if (!aligned16(q) || !aligned16(out) || (n_reqs > 1 && (q_stride % 8 || out_stride % 8)))
+        return fail(KVX_EINVAL, "q and out: pointers and strides must be multiples of 16 bytes");
+    if (((uintptr_t)block_table & 3) || ((uintptr_t)seq_len & 3) || ((uintptr_t)lse & 3))
+        return fail(KVX_EINVAL, "an array is not on a boundary of its elements");
+    return KVX_OK;
+}
+
+void kvx::cache_fill_attend(kvx_cache_t c, int32_t layer, const void *q, int64_t q_stride, const int32_t *block_table,
+                    int64_t table_stride, int32_t max_blocks, const int32_t *seq_len, int32_t n_reqs, void *out, int64_t out_stride, float *lse,
+                    AttendArgs *args) {
+    const Geom &g = c->g;
+    const kvx_cache_config &f = c->cfg;
+    AttendArgs &a = *args;
+    a = AttendArgs{};
+    cache_fill_layer(c, layer, &a.pool);
+    a.q = (const uint8_t *)q;
+    a.out = (uint8_t *)out;
+    a.lse = lse;
+    a.block_table = block_table;
+    a.seq_len = seq_len;
+    a.q_stride = q_stride * 2;
+    a.out_stride = out_stride * 2;
+    a.table_stride = table_stride;
+    a.max_blocks = max_blocks;
+    a.n_reqs = n_reqs;
+    a.n_q_heads = f.n_q_heads;
+    a.n_kv_heads = g.n_shards * g.heads_per_shard;
+    a.head_dim = g.head_dim;
+    a.v_dim = f.v_dim;
+    a.window = f.window;
+    a.scale = (float)((double)f.scale * (double)f.k_scale * 1.4426950408889634);
+    a.v_scale = f.v_scale;
+    divisor((uint32_t)g.block_size, &a.block_mul, &a.block_shift);
+    a.block_pitch16 = (uint32_t)(a.pool.block_pitch / 16);
+    a.token_pitch16 = (uint32_t)(a.pool.token_pitch / 16);
+    a.latent = g.n_planes == 1;
+    a.row_maps = c->row_maps.empty() ? nullptr : &c->row_maps[(size_t)layer];
+    a.map_run = c->map_run;
+    const bool hnd = g.layout == KVX_LAYOUT_HND;
+    a.map_rows = (int32_t)std::min<int64_t>(g.n_blocks * g.block_size * (hnd ? g.heads_per_shard : 1), std::numeric_limits<int32_t>::max());
+    a.map_block = (uint32_t)(g.block_size * (hnd ? g.heads_per_shard : 1));
+    a.map_head = hnd ? (uint32_t)g.block_size : 0;
+    a.map_col = hnd ? 0 : (uint32_t)g.head_bytes();
+    a.scratch = c->dev + 256;
+    a.device = c->device;
 }
 
 extern "C" {
@@ -278,61 +340,17 @@ kvx_status kvx_cache_attend(kvx_cache_t c, int32_t layer, const void *q, int64_t
                             const int32_t *block_table, int64_t table_stride, int32_t max_blocks,
                             const int32_t *seq_len, int32_t n_reqs, void *out, int64_t out_stride, float *lse,
                             cudaStream_t stream) {
-    kvx_status st = cache_check_layer(c, layer);
+    kvx_status st = cache_check_attend(c, layer, q, q_stride, block_table, table_stride, max_blocks, seq_len, n_reqs, out, out_stride, lse);
     if (st) return st;
-    const Geom &g = c->g;
-    const kvx_cache_config &f = c->cfg;
-    if (f.v_dim > kCacheMaxLatentValue) return fail(KVX_EUNSUPPORTED, "attention over latents with v_dim %d", f.v_dim);
-    if (n_reqs < 0 || n_reqs > (1 << 24)) return fail(KVX_EINVAL, "n_reqs %d not in [0, 2^24]", n_reqs);
-    if (max_blocks < 0 || table_stride < max_blocks) return fail(KVX_EINVAL, "max_blocks must be >= 0, table_stride >= max_blocks");
-    if (n_reqs && (!q || !out || !seq_len || (max_blocks && !block_table)))
-        return fail(KVX_EINVAL, "q, out, seq_len or block_table is NULL");
-    if (n_reqs > 1 && (q_stride < (int64_t)f.n_q_heads * g.head_dim || out_stride < (int64_t)f.n_q_heads * f.v_dim))
-        return fail(KVX_EINVAL, "strides below a request's elements");
-    if (q_stride > ((int64_t)1 << 40) || out_stride > ((int64_t)1 << 40)) return fail(KVX_EINVAL, "stride above 2^40");
-    if (!aligned16(q) || !aligned16(out) || (n_reqs > 1 && (q_stride % 8 || out_stride % 8)))
-        return fail(KVX_EINVAL, "q and out: pointers and strides must be multiples of 16 bytes");
-    if (((uintptr_t)block_table & 3) || ((uintptr_t)seq_len & 3) || ((uintptr_t)lse & 3))
-        return fail(KVX_EINVAL, "an array is not on a boundary of its elements");
     if (n_reqs == 0) return KVX_OK;
     if ((st = cache_ready(c, stream))) return st;
-    if (g.n_planes == 1 && c->outside_device) return fail(KVX_EUNSUPPORTED, "attention over latents outside device memory");
+    if (c->g.n_planes == 1 && c->outside_device) return fail(KVX_EUNSUPPORTED, "attention over latents outside device memory");
     AttendArgs a;
-    cache_fill_layer(c, layer, &a.pool);
-    a.q = (const uint8_t *)q;
-    a.out = (uint8_t *)out;
-    a.lse = lse;
-    a.block_table = block_table;
-    a.seq_len = seq_len;
-    a.q_stride = q_stride * 2;
-    a.out_stride = out_stride * 2;
-    a.table_stride = table_stride;
-    a.max_blocks = max_blocks;
-    a.n_reqs = n_reqs;
-    a.n_q_heads = f.n_q_heads;
-    a.n_kv_heads = g.n_shards * g.heads_per_shard;
-    a.head_dim = g.head_dim;
-    a.v_dim = f.v_dim;
-    a.window = f.window;
-    a.scale = (float)((double)f.scale * (double)f.k_scale * 1.4426950408889634);
-    a.v_scale = f.v_scale;
-    divisor((uint32_t)g.block_size, &a.block_mul, &a.block_shift);
-    a.block_pitch16 = (uint32_t)(a.pool.block_pitch / 16);
-    a.token_pitch16 = (uint32_t)(a.pool.token_pitch / 16);
-    a.latent = g.n_planes == 1;
-    a.row_maps = c->row_maps.empty() ? nullptr : &c->row_maps[(size_t)layer];
-    a.map_run = c->map_run;
-    const bool hnd = g.layout == KVX_LAYOUT_HND;
-    a.map_rows = (int32_t)std::min<int64_t>(g.n_blocks * g.block_size * (hnd ? g.heads_per_shard : 1), std::numeric_limits<int32_t>::max());
-    a.map_block = (uint32_t)(g.block_size * (hnd ? g.heads_per_shard : 1));
-    a.map_head = hnd ? (uint32_t)g.block_size : 0;
-    a.map_col = hnd ? 0 : (uint32_t)g.head_bytes();
-    a.scratch = c->dev + 256;
-    a.device = c->device;
+    cache_fill_attend(c, layer, q, q_stride, block_table, table_stride, max_blocks, seq_len, n_reqs, out, out_stride, lse, &a);
     a.stall = c->stall;
     a.wait_ns = a.stall ? kCacheStallWaitNs : kCacheWaitNs;
     c->stall = 0;
-    const cudaError_t e = launch_attend(a, f.value_type, f.io_type, c->sms, stream);
+    const cudaError_t e = launch_attend(a, c->cfg.value_type, c->cfg.io_type, c->sms, stream);
     return e == cudaSuccess ? KVX_OK : cuda_fail(e, "launching the attention");
 }
 

@@ -233,7 +233,10 @@ struct AttendArgs {
     uint8_t *scratch;                 // of the handle: counters (zero between calls), partial results
     int32_t device;
     int32_t stall;                    // latents, testing hook (kvx_cache_inject_stall): CTA 0's part that never goes on, 0: none
-    uint64_t wait_ns;                 // latents: limit of a wait for a copy or a product
+    uint64_t wait_ns;                 // latents, shared prefixes: limit of a wait for a copy or a product
+    const int32_t *start;             // kvx_cache_attend_shared: each request's first position behind its group's prefix,
+    float *rest;                      // and for the ones from there the sums, [request][query head][head_dim],
+    float2 *rest_ml;                  // with their maximum and the weights' sum
 };
 // Limit of one such wait, far beyond any copy or product of a tile; and that of a call that kvx_cache_inject_stall prepared.
 constexpr uint64_t kCacheWaitNs = 2000000000ull;       // 2 s
@@ -249,6 +252,44 @@ cudaError_t launch_attend_e4m3_f16(const AttendArgs &a, int32_t sms, cudaStream_
 cudaError_t launch_attend_latent(const AttendArgs &a, int32_t value_type, int32_t io_type, int32_t sms, cudaStream_t stream);
 size_t attend_scratch_bytes(int32_t sms, bool latent);
 size_t latent_scratch_bytes(int32_t sms);
+
+// ---- shared prefixes (kvx_shared_calls.cpp, kvx_shared.cu, kvx_shared.cuh) ----
+// A unit of the line (kvx_shared.cu writes them): rows [pair * 256, + rows) of a group's queries of one KV head.
+struct SharedUnit {
+    int64_t begin;                     // its first place
+    int32_t first;                     // the group's first request
+    int32_t rows, pair, kvh;
+    int32_t tokens;                    // of the prefix
+    int32_t pairs;                     // units of the group for a KV head
+};
+struct SharedHeader {
+    int64_t places;                    // of the line
+    int32_t units, spare;
+};
+
+struct SharedArgs {
+    AttendArgs a;
+    const int32_t *group_off, *prefix_len;
+    int32_t n_groups, max_units;
+    // the workspace
+    SharedHeader *header;
+    SharedUnit *units;
+    int32_t *start;                    // per request: its prefix' length, or 0
+    int32_t *unit_of, *row_of;         // per request: its group's first unit, its first row among the group's
+    uint8_t *parts;                    // partial results
+};
+constexpr int32_t kSharedMaxDim = 128;
+enum { kStallSharedProducts = 1, kStallSharedSoftmax, kStallSharedCopies };
+int64_t shared_part_bytes(int32_t head_dim);                                   // of a partial result
+cudaError_t launch_attend_shared(const SharedArgs &s, int32_t value_type, int32_t io_type, int32_t sms, cudaStream_t stream);
+cudaError_t launch_shared_bf16(const SharedArgs &s, int32_t sms, cudaStream_t stream);
+cudaError_t launch_shared_f16(const SharedArgs &s, int32_t sms, cudaStream_t stream);
+cudaError_t launch_shared_e4m3_bf16(const SharedArgs &s, int32_t sms, cudaStream_t stream);
+cudaError_t launch_shared_e4m3_f16(const SharedArgs &s, int32_t sms, cudaStream_t stream);
+cudaError_t launch_rest_bf16(const AttendArgs &a, int32_t sms, cudaStream_t stream);
+cudaError_t launch_rest_f16(const AttendArgs &a, int32_t sms, cudaStream_t stream);
+cudaError_t launch_rest_e4m3_bf16(const AttendArgs &a, int32_t sms, cudaStream_t stream);
+cudaError_t launch_rest_e4m3_f16(const AttendArgs &a, int32_t sms, cudaStream_t stream);
 
 // ---- pages (kvx_page_calls.cpp, kvx_pages.cu) ----
 struct TableArgs {
@@ -313,6 +354,13 @@ cudaError_t launch_rotate(const RotateArgs &a, int32_t value_type, int32_t io_ty
 kvx_status cache_check_layer(kvx_cache_t c, int32_t layer);
 kvx_status cache_ready(kvx_cache_t c, cudaStream_t stream);                    // its scratch, allocated by the first call that needs it
 void cache_fill_layer(kvx_cache_t c, int32_t layer, CacheLayer *out);
+kvx_status cache_check_attend(kvx_cache_t c, int32_t layer, const void *q, int64_t q_stride, const int32_t *block_table,
+                              int64_t table_stride, int32_t max_blocks, const int32_t *seq_len, int32_t n_reqs, void *out,
+                              int64_t out_stride, float *lse);
+void cache_fill_attend(kvx_cache_t c, int32_t layer, const void *q, int64_t q_stride, const int32_t *block_table, int64_t table_stride,
+                       int32_t max_blocks, const int32_t *seq_len, int32_t n_reqs, void *out, int64_t out_stride, float *lse,
+                       AttendArgs *args);
+kvx_status device_sms(int32_t *device, int32_t *sms);                          // the current device and its multiprocessors
 void divisor(uint32_t d, uint32_t *mul, uint32_t *shift);                      // x / d = (mulhi(x, mul) + x) >> shift for x below 2^31
 
 }  // namespace kvx
@@ -328,6 +376,7 @@ struct kvx_cache_s {
     std::vector<kvx::RowMaps> row_maps;        // latents: per buffer, or none (kvx_cache.cpp, encode_rows)
     int32_t map_run = 0;                       // rows of a run: the common divisor of the block size and a tile
     int32_t stall = 0;                         // kvx_cache_inject_stall: part of the next attend
+    int32_t shared_stall = 0;                  // kvx_cache_inject_shared_stall: part of the next kvx_cache_attend_shared
     uint8_t *dev = nullptr;                    // [256 bytes: skipped][scratch of the attend kernels]
     uint8_t *const *dev_bases = nullptr;       // behind it: `base` on the device
 };

@@ -47,6 +47,7 @@
 // no division for each, 116 (4 requests of 100: 11.7, from 14.1); a join in one pass 115; a fourth code of the weights, for
 // their precision, 116. Prefetching the next tiles into L2 cost 8 to 17 us.
 #include "kvx_latent.cuh"
+#include "kvx_tensor.cuh"
 
 namespace kvx {
 
@@ -92,48 +93,6 @@ template <int VT_, int IO_, int HEADS_> struct TensorShape {
     static constexpr uint32_t IDESC_COLS = IDESC | (WCOLS / 8) << 17 | (128 / 16) << 24 | 1u << 15 | 1u << 16;
     static constexpr uint32_t IDESC_SECOND = IDESC | (HEADS / 8) << 17 | (128 / 16) << 24 | 1u << 15 | 1u << 16;
 };
-
-// Shared memory operands: start, the two strides, swizzle (0 none, 2 of 128 bytes, 4 of 64 bytes).
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t leading, uint32_t stride, uint32_t swizzle) {
-    return (uint64_t)(addr >> 4 & 0x3fff) | (uint64_t)(leading >> 4) << 16 | (uint64_t)(stride >> 4) << 32 | (uint64_t)1 << 46 |
-           (uint64_t)swizzle << 61;
-}
-// Issued by one lane of a converged warp, always the same: the operands are uniform then, and 18 products go out in 0.6 us
-// instead of 2.5 from a branch of one lane.
-template <bool F8> __device__ __forceinline__ void tensor_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-    if constexpr (F8)
-        asm volatile("{\n.reg .pred p, e;\nsetp.ne.u32 p, %4, 0;\nelect.sync _|e, 0xffffffff;\n"
-                     "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-                     : "memory");
-    else
-        asm volatile("{\n.reg .pred p, e;\nsetp.ne.u32 p, %4, 0;\nelect.sync _|e, 0xffffffff;\n"
-                     "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-                     : "memory");
-}
-__device__ __forceinline__ void tensor_commit(uint64_t *bar) {
-    asm volatile("{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
-                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(shared_addr(bar)) : "memory");
-}
-__device__ __forceinline__ void tensor_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tensor_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// 8 columns of this warp's 32 rows of TMEM.
-__device__ __forceinline__ void tmem_load(uint32_t (&x)[8], uint32_t at) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]) : "r"(at) : "memory");
-}
-__device__ __forceinline__ void tmem_store(const uint32_t (&x)[8], uint32_t at) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
-                 "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ void arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(shared_addr(bar)) : "memory");
-}
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Barrier of the softmax warps, with the disjunction of a condition.
 __device__ __forceinline__ bool softmax_any(bool x) {

@@ -1,0 +1,191 @@
+// kvx_cache_attend_shared: the plan of a batch's shared prefixes, the launches, and the join of what they leave.
+#include "kvx_shared.cuh"
+
+namespace kvx {
+
+constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
+// Prefixes of fewer positions are read by each request: a tile of the tensor pipe is 128.
+constexpr int32_t kSharedLeast = 128;
+
+int64_t shared_part_bytes(int32_t head_dim) { return 2 * kSharedRows * ((int64_t)head_dim * 4 + 8); }
+
+// One CTA. A group of two members or more shares the first P positions, P what it names but at most its shortest member's
+// length. With a window every member's has to reach the start, else each reads its own. Groups that are no ascending
+// stretches of the requests are reported, and then nothing is shared: the results are the same.
+__global__ void __launch_bounds__(kPlanThreads, 1) kvx_shared_plan(const __grid_constant__ SharedArgs s) {
+    __shared__ int32_t s_tokens[kPlanThreads], s_unit[kPlanThreads];
+    __shared__ int64_t s_place[kPlanThreads], s_sums[2][kPlanWarps];
+    wait_for_earlier();
+    const AttendArgs &a = s.a;
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t group = a.n_q_heads / a.n_kv_heads;
+    const int64_t cap = (int64_t)a.max_blocks * a.pool.block_size;
+    bool bad = false;
+    for (int32_t g = threadIdx.x; g < s.n_groups; g += kPlanThreads) {
+        const int32_t lo = s.group_off[g], hi = s.group_off[g + 1];
+        bad |= lo < 0 || hi < lo || hi > a.n_reqs;
+        if (s.prefix_len[g] < 0) atomicAdd(a.pool.skipped, 1ull);
+    }
+    for (int32_t r = threadIdx.x; r < a.n_reqs; r += kPlanThreads) s.start[r] = 0;
+    bad = __syncthreads_or(bad);
+    if (bad && threadIdx.x == 0) atomicAdd(a.pool.skipped, 1ull);
+    int64_t places = 0, units = 0;
+    for (int32_t g0 = 0; !bad && g0 < s.n_groups; g0 += kPlanThreads) {
+        const int32_t n = min(kPlanThreads, s.n_groups - g0);
+        for (int32_t i = w; i < n; i += kPlanWarps) {                  // a warp a group: what it shares
+            const int32_t lo = s.group_off[g0 + i], hi = s.group_off[g0 + i + 1];
+            int32_t least = INT32_MAX, most = 0;
+            for (int32_t r = lo + lane; r < hi; r += 32) {
+                const int32_t len = (int32_t)min((int64_t)max(a.seq_len[r], 0), cap);
+                least = min(least, len);
+                most = max(most, len);
+            }
+            least = __reduce_min_sync(~0u, least);
+            most = __reduce_max_sync(~0u, most);
+            int32_t tokens = hi - lo < 2 ? 0 : min(s.prefix_len[g0 + i], least);
+            if (tokens < kSharedLeast || (a.window && most > a.window)) tokens = 0;
+            if (lane == 0) s_tokens[i] = tokens;
+            if (tokens)
+                for (int32_t r = lo + lane; r < hi; r += 32) {
+                    s.start[r] = tokens;
+                    s.row_of[r] = (r - lo) * group;
+                }
+        }
+        __syncthreads();
+        int64_t my_units = 0, my_places = 0;
+        if ((int32_t)threadIdx.x < n && s_tokens[threadIdx.x]) {
+            const int64_t rows = (int64_t)(s.group_off[g0 + threadIdx.x + 1] - s.group_off[g0 + threadIdx.x]) * group;
+            const int64_t pairs = (rows + 2 * kSharedRows - 1) / (2 * kSharedRows), tiles = shared_tiles(s_tokens[threadIdx.x]);
+            my_units = pairs * a.n_kv_heads;
+            my_places = a.n_kv_heads * (pairs * kSharedSwitch + (pairs - 1) * 2 * tiles +
+                                        tiles * shared_weight((int32_t)(rows - (pairs - 1) * 2 * kSharedRows)));
+        }
+        int64_t u = warp_inclusive(my_units), p = warp_inclusive(my_places);
+        if (lane == 31) s_sums[0][w] = u, s_sums[1][w] = p;
+        __syncthreads();
+        int64_t all_units = 0, all_places = 0;
+        for (int i = 0; i < kPlanWarps; ++i) {
+            if (i == w) u += all_units, p += all_places;
+            all_units += s_sums[0][i];
+            all_places += s_sums[1][i];
+        }
+        s_unit[threadIdx.x] = (int32_t)(units + u - my_units);
+        s_place[threadIdx.x] = places + p - my_places;
+        units += all_units;
+        places += all_places;
+        __syncthreads();
+        for (int32_t i = w; i < n; i += kPlanWarps) {                  // its units
+            const int32_t tokens = s_tokens[i];
+            if (!tokens) continue;
+            const int32_t lo = s.group_off[g0 + i], hi = s.group_off[g0 + i + 1];
+            const int32_t rows = (hi - lo) * group, pairs = (rows + 2 * kSharedRows - 1) / (2 * kSharedRows);
+            const int64_t tiles = shared_tiles(tokens), pair_places = 2 * tiles + kSharedSwitch;
+            const int64_t head_places = (pairs - 1) * pair_places + tiles * shared_weight(rows - (pairs - 1) * 2 * kSharedRows) + kSharedSwitch;
+            for (int64_t j = lane; j < (int64_t)pairs * a.n_kv_heads; j += 32) {
+                const int32_t kvh = (int32_t)(j / pairs), pair = (int32_t)(j - (int64_t)kvh * pairs);
+                SharedUnit x;
+                x.begin = s_place[i] + kvh * head_places + pair * pair_places;
+                x.first = lo;
+                x.rows = min(rows - pair * 2 * kSharedRows, 2 * kSharedRows);
+                x.pair = pair;
+                x.kvh = kvh;
+                x.tokens = tokens;
+                x.pairs = pairs;
+                if (s_unit[i] + j < s.max_units) s.units[s_unit[i] + j] = x;
+            }
+            for (int32_t r = lo + lane; r < hi; r += 32) s.unit_of[r] = s_unit[i];
+        }
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+        s.header->places = places;
+        s.header->units = (int32_t)min(units, (int64_t)s.max_units);
+    }
+}
+
+// The join: a thread has four elements of a row (request, query head), the sums of its own positions and those of the CTAs that its
+// unit went to, eight at a time. Reads and writes are whole sectors: 8 rows x 4 float4 a warp.
+template <int IO, int D> __global__ void __launch_bounds__(256) kvx_shared_join(const __grid_constant__ SharedArgs s, int ctas) {
+    constexpr int C4 = D / 4, ROWS = 256 / C4, AT_ONCE = 8;
+    wait_for_earlier();
+    const AttendArgs &a = s.a;
+    const int c = threadIdx.x / 8 % C4;
+    const int64_t row = (int64_t)blockIdx.x * ROWS + (threadIdx.x & 7) + threadIdx.x / (8 * C4) * 8;
+    if (row >= (int64_t)a.n_reqs * a.n_q_heads || c * 4 >= a.head_dim) return;
+    const int32_t r = (int32_t)(row / a.n_q_heads), head = (int32_t)(row - (int64_t)r * a.n_q_heads), group = a.n_q_heads / a.n_kv_heads;
+    const float2 mine = __ldcg(a.rest_ml + row);
+    float4 o = make_float4(0, 0, 0, 0);
+    float top = -INFINITY, l = 0.0f;
+    if (mine.y != 0.0f) {                                              // also NaN
+        top = mine.x;
+        l = mine.y;
+        o = __ldcg(reinterpret_cast<const float4 *>(a.rest + row * a.head_dim) + c);
+    }
+    if (s.start[r]) {
+        const int32_t kvh = head / group, first = s.unit_of[r], at = s.row_of[r] + head - kvh * group;
+        const int32_t unit = first + kvh * s.units[first].pairs + at / (2 * kSharedRows);
+        const SharedUnit u = s.units[unit];
+        const int weight = shared_weight(u.rows);
+        const Split split = shared_split(s.header->places, ctas);
+        const int32_t from = split.cta_of(u.begin), upto = split.cta_of(u.begin + (int64_t)shared_tiles(u.tokens) * weight - 1);
+        const int64_t bytes = part_bytes(a.head_dim);
+        const int in_slot = at % kSharedRows, slot = weight == 2 ? at % (2 * kSharedRows) / kSharedRows : 0;
+        // with one slot a tile, both slots' sums are parts of the same rows
+        const int64_t step = weight == 2 ? bytes : bytes / 2;
+        const int32_t n = (upto - from + 1) * (weight == 2 ? 1 : 2);
+        const uint8_t *const parts = s.parts + (unit + from) * bytes + slot * (bytes / 2);
+        for (int32_t x0 = 0; x0 < n; x0 += AT_ONCE) {
+            float2 ml[AT_ONCE];
+            float4 y[AT_ONCE];
+            float up = top;
+#pragma unroll
+            for (int x = 0; x < AT_ONCE; ++x) {
+                ml[x] = make_float2(-INFINITY, 0.0f);
+                if (x0 + x < n) {
+                    const uint8_t *const p = parts + (x0 + x) * step;
+                    ml[x] = __ldcg(reinterpret_cast<const float2 *>(p) + in_slot);
+                    y[x] = __ldcg(reinterpret_cast<const float4 *>(p + kSharedRows * 8) + c * kSharedRows + in_slot);
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < AT_ONCE; ++x)
+                if (ml[x].y != 0.0f) up = fmaxf(up, ml[x].x);
+            const float ref = up == -INFINITY ? 0.0f : up, old = fast_exp2(top - ref);
+            top = up;
+            l *= old;
+            o = make_float4(o.x * old, o.y * old, o.z * old, o.w * old);
+#pragma unroll
+            for (int x = 0; x < AT_ONCE; ++x)
+                if (ml[x].y != 0.0f) {                                 // sums without weights were not written
+                    const float by = fast_exp2(ml[x].x - ref);
+                    l = fmaf(by, ml[x].y, l);
+                    o = make_float4(fmaf(by, y[x].x, o.x), fmaf(by, y[x].y, o.y), fmaf(by, y[x].z, o.z), fmaf(by, y[x].w, o.w));
+                }
+        }
+    }
+    const float inverse = l == 0.0f ? 0.0f : a.v_scale / l;
+    *reinterpret_cast<uint2 *>(a.out + r * a.out_stride + ((int64_t)head * a.head_dim + c * 4) * 2) =
+        l == 0.0f ? make_uint2(0, 0) : make_uint2(pack<IO>(o.x * inverse, o.y * inverse), pack<IO>(o.z * inverse, o.w * inverse));
+    if (c == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (top + log2f(l)) * kLn2;
+}
+
+template <int IO> static cudaError_t launch_join(const SharedArgs &s, int32_t sms, cudaStream_t stream) {
+    const int64_t rows = (int64_t)s.a.n_reqs * s.a.n_q_heads;
+    if (s.a.head_dim <= 64) return launch_after(kvx_shared_join<IO, 64>, dim3((unsigned)((rows + 15) / 16)), 256, 0, stream, s, sms);
+    return launch_after(kvx_shared_join<IO, 128>, dim3((unsigned)((rows + 7) / 8)), 256, 0, stream, s, sms);
+}
+
+cudaError_t launch_attend_shared(const SharedArgs &s, int32_t vt, int32_t io, int32_t sms, cudaStream_t stream) {
+    cudaError_t e = launch_after(kvx_shared_plan, dim3(1), kPlanThreads, 0, stream, s);
+    if (e != cudaSuccess) return e;
+    const bool bf16 = io == KVX_BF16;
+    e = vt == KVX_BF16 ? launch_shared_bf16(s, sms, stream) : vt == KVX_F16 ? launch_shared_f16(s, sms, stream)
+        : bf16 ? launch_shared_e4m3_bf16(s, sms, stream) : launch_shared_e4m3_f16(s, sms, stream);
+    if (e != cudaSuccess) return e;
+    e = vt == KVX_BF16 ? launch_rest_bf16(s.a, sms, stream) : vt == KVX_F16 ? launch_rest_f16(s.a, sms, stream)
+        : bf16 ? launch_rest_e4m3_bf16(s.a, sms, stream) : launch_rest_e4m3_f16(s.a, sms, stream);
+    if (e != cudaSuccess) return e;
+    return bf16 ? launch_join<KVX_BF16>(s, sms, stream) : launch_join<KVX_F16>(s, sms, stream);
+}
+
+}  // namespace kvx

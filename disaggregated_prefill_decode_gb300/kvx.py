@@ -148,6 +148,10 @@ _sig = {
     "kvx_cache_destroy": (c_i32, [c_vp]),
     "kvx_cache_append": (c_i32, [c_vp, c_i32, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp]),
     "kvx_cache_attend": (c_i32, [c_vp, c_i32, c_vp, c_i64, c_vp, c_i64, c_i32, c_vp, c_i32, c_vp, c_i64, c_vp, c_vp]),
+    "kvx_cache_shared_bytes": (c_i32, [c_vp, c_i32, c_i32, _P(c_i64)]),
+    "kvx_cache_attend_shared": (c_i32, [c_vp, c_i32, c_vp, c_i64, c_vp, c_i64, c_i32, c_vp, c_i32, c_vp, c_vp, c_i32, c_vp, c_i64,
+                                        c_vp, c_vp, c_i64, c_vp]),
+    "kvx_cache_inject_shared_stall": (c_i32, [c_vp, c_i32]),
     "kvx_rotation_create": (c_i32, [_P(kvx_rotation_config), _P(c_vp)]),
     "kvx_rotation_destroy": (c_i32, [c_vp]),
     "kvx_rotation_get": (c_i32, [c_vp, _P(c_double), c_i32, _P(c_i32), _P(c_double)]),
@@ -595,6 +599,25 @@ def kvx_cache_attend(cache: Cache, layer: int, q, q_stride: int, block_table, ta
     _check(_lib.kvx_cache_attend(cache.handle, layer, _ptr(q), q_stride, _ptr(block_table), table_stride, max_blocks,
                                  _ptr(seq_len), n_reqs, _ptr(out), out_stride, _ptr(lse), _stream(stream)),
            "kvx_cache_attend")
+
+
+def kvx_cache_shared_bytes(cache: Cache, n_reqs: int, n_groups: int) -> int:
+    """Bytes of the workspace of kvx_cache_attend_shared."""
+    n = c_i64()
+    _check(_lib.kvx_cache_shared_bytes(cache.handle, n_reqs, n_groups, ctypes.byref(n)), "kvx_cache_shared_bytes")
+    return n.value
+
+
+def kvx_cache_attend_shared(cache: Cache, layer: int, q, q_stride: int, block_table, table_stride: int, max_blocks: int, seq_len,
+                            n_reqs: int, group_off, prefix_len, n_groups: int, out, out_stride: int, lse, workspace,
+                            workspace_bytes: int, stream=None) -> None:
+    _check(_lib.kvx_cache_attend_shared(cache.handle, layer, _ptr(q), q_stride, _ptr(block_table), table_stride, max_blocks,
+                                        _ptr(seq_len), n_reqs, _ptr(group_off), _ptr(prefix_len), n_groups, _ptr(out), out_stride,
+                                        _ptr(lse), _ptr(workspace), workspace_bytes, _stream(stream)), "kvx_cache_attend_shared")
+
+
+def kvx_cache_inject_shared_stall(cache: Cache, part: int) -> None:
+    _check(_lib.kvx_cache_inject_shared_stall(cache.handle, part), "kvx_cache_inject_shared_stall")
 
 
 def kvx_pages_free(block_table, table_stride: int, max_blocks: int, seq_len, n_reqs: int, block_size: int, n_blocks: int,

@@ -656,6 +656,27 @@ kvx_status kvx_cache_attend(kvx_cache_t cache, int32_t layer, const void *q, int
                             const int32_t *seq_len, int32_t n_reqs, void *out, int64_t out_stride, float *lse,
                             cudaStream_t stream);
 
+/*
+ * kvx_cache_attend_shared -- kvx_cache_attend for a batch in which groups of requests share a prefix, which is read and multiplied once
+ * for all members of a group. The same results, by the same definition, for the same q, table, lengths, out and lse.
+ * Group g is the requests [group_off[g], group_off[g + 1]) (ascending; requests outside every group share nothing), whose first
+ * prefix_len[g] positions hold the same keys and values: in the same blocks, or a block in which the prefix ends in copies of it, as
+ * kvx_pages_fork makes them. They are read through the row of the group's first member, up to the shortest member's length. With a window a
+ * group shares its prefix while the window of every member reaches the first position. Both arrays are device memory, checked there:
+ * a negative prefix_len counts as 0, with a group_off that is no such list nothing is shared, and kvx_cache_status reports either.
+ * Whether a prefix is worth sharing is decided here: short ones (below 128 positions), batches that read little twice (below 24 MiB by
+ * max_blocks), latents and head dims above 128 go to kvx_cache_attend, or read their prefixes themselves.
+ * workspace: kvx_cache_shared_bytes bytes of device memory (0 for caches that do not share), on a 16-byte boundary, in no particular
+ * state and free again after the call's device work; calls whose device work overlaps need workspaces, and handles, of their own.
+ * Weights leave 2^-15 of a weight at most, or 2^-30 of the largest of the row. Two calls on the same inputs give the same bits.
+ */
+kvx_status kvx_cache_shared_bytes(kvx_cache_t cache, int32_t n_reqs, int32_t n_groups, int64_t *bytes);
+kvx_status kvx_cache_attend_shared(kvx_cache_t cache, int32_t layer, const void *q, int64_t q_stride,
+                                   const int32_t *block_table, int64_t table_stride, int32_t max_blocks,
+                                   const int32_t *seq_len, int32_t n_reqs, const int32_t *group_off, const int32_t *prefix_len,
+                                   int32_t n_groups, void *out, int64_t out_stride, float *lse, void *workspace,
+                                   int64_t workspace_bytes, cudaStream_t stream);
+
 /* ------------------------------------------------------------------------------------------------
  * Pages that several requests hold. The tables and lengths alone say who holds what: row r of a table holds its first
  * ceil(seq_len[r] / block_size) blocks, and a block may stand in several rows. So there are no counts to keep: a request ends by
@@ -730,6 +751,10 @@ kvx_status kvx_cache_status(kvx_cache_t cache, cudaStream_t stream);
  * arrives at: a wait that can only run out. The CTA then waits for its copies and products in flight and returns, the others
  * finish, nothing faults, and kvx_cache_status reports KVX_ETIMEDOUT. KVX_EUNSUPPORTED for caches with two planes. */
 kvx_status kvx_cache_inject_stall(kvx_cache_t cache, int32_t part);
+
+/* The same for the shared prefixes of the handle's next kvx_cache_attend_shared: 1 the products, 2 the softmax, 3 the copies.
+ * KVX_EUNSUPPORTED for caches with one plane. */
+kvx_status kvx_cache_inject_shared_stall(kvx_cache_t cache, int32_t part);
 
 /* ------------------------------------------------------------------------------------------------
  * Connector state machine (host only; no CUDA call, usable without a GPU).
