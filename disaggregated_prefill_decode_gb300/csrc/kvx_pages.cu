@@ -2,7 +2,7 @@
 //
 // The first three are one launch each. Their steps depend on one another (count, then place), so they run in one cluster of up
 // to 16 CTAs, whose barrier takes the place of a second launch; sums go from CTA to CTA through distributed shared memory. The
-// flags of the pool's blocks are read as bits: a warp takes 1024 neighbouring blocks, lane i the bits of 32 of them, so that
+// flags of the pool's blocks are read as bits: a warp takes up to 1024 neighbouring blocks, lane i the bits of 32 of them, so that
 // ranks come from population counts and ids are read and written in whole lines. Bound by latency: 4 to 8 barriers and the
 // reads between them.
 #include "kvx_launch.cuh"
@@ -17,9 +17,8 @@ namespace cg = cooperative_groups;
 
 constexpr int kPageThreads = 1024, kPageWarps = kPageThreads / 32;
 constexpr int kPageCluster = 16;                   // CTAs at most
-constexpr int kPassBlocks = kPageWarps * 1024;     // of a CTA, in one pass
 constexpr int kEntries = 4;                        // table entries of a lane at a time
-constexpr int kMovesShared = 8192;                 // moves that the remapping searches in shared memory
+constexpr int kMovesShared = 4096;                 // moves that the remapping has in shared memory
 
 // Blocks that a request holds by its length; bad where the length is negative or beyond its row.
 __device__ __forceinline__ int32_t held_blocks(const TableArgs &t, int32_t r, bool &bad) {
@@ -34,20 +33,39 @@ template <class F> __device__ __forceinline__ void for_entries(int32_t n, int32_
     const int chunks = (width + 32 * kEntries - 1) / (32 * kEntries), lane = threadIdx.x & 31;
     const int64_t items = (int64_t)n * chunks, warps = (int64_t)ranks * kPageWarps;
     for (int64_t i = (int64_t)rank * kPageWarps + (threadIdx.x >> 5); i < items; i += warps) {
-        const int32_t r = (int32_t)(i / chunks);
+        const int32_t r = items >> 32 ? (int32_t)(i / chunks) : (int32_t)((uint32_t)i / (uint32_t)chunks);
         f(r, (int32_t)(i - (int64_t)r * chunks) * (32 * kEntries) + lane);
     }
 }
 
-// Bits of 1024 blocks from `first`: lane i has those of 32 i to 32 i + 31. Set where some request holds the block.
-__device__ __forceinline__ uint32_t held_bits(const int32_t *refs, int64_t first, int64_t n) {
+// The words of 32 blocks' flags over the warps of a launch: a warp takes `words` neighbouring ones at a time, as few as keep all warps busy.
+struct Words {
+    int words;
+    int64_t first, step;               // blocks: of this warp's first word, of all warps in a pass
+    __device__ __forceinline__ Words(int64_t n, int rank, int ranks) {
+        const int64_t warps = (int64_t)ranks * kPageWarps, all = (n + 31) / 32;
+        words = (int)min((all + warps - 1) / warps, (int64_t)32);
+        first = ((int64_t)rank * kPageWarps + (threadIdx.x >> 5)) * words * 32;
+        step = warps * words * 32;
+    }
+};
+
+// Bits of a warp's words from block `first` on: lane i has those of word i. Set where some request holds the block.
+__device__ __forceinline__ uint32_t held_bits(const int32_t *refs, int64_t first, int64_t n, int words) {
     const int lane = threadIdx.x & 31;
     uint32_t mine = 0;
+    for (int i0 = 0; i0 < words; i0 += 8) {
+        int32_t x[8];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const int64_t b = first + i * 32 + lane;
-        const uint32_t bits = __ballot_sync(~0u, b < n && __ldcg(refs + b) > 0);
-        if (lane == i) mine = bits;
+        for (int i = 0; i < 8; ++i) {
+            const int64_t b = first + (i0 + i) * 32 + lane;
+            x[i] = i0 + i < words && b < n ? __ldcg(refs + b) : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t bits = __ballot_sync(~0u, x[i] > 0);
+            if (lane == i0 + i) mine = bits;
+        }
     }
     return mine;
 }
@@ -57,49 +75,70 @@ __device__ __forceinline__ uint32_t bits_below(int64_t first, int64_t end) {
 }
 
 // Exclusive sum over the CTA's threads, and the total.
-__device__ __forceinline__ int32_t page_exclusive(int32_t x, int32_t *total) {
-    __shared__ int32_t sums[kPageWarps];
+__device__ __forceinline__ int64_t page_exclusive(int64_t x, int64_t *total) {
+    __shared__ int64_t sums[kPageWarps];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    int32_t s = x;
+    int64_t s = x;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int32_t o = __shfl_up_sync(~0u, s, d);
+        const int64_t o = __shfl_up_sync(~0u, s, d);
         if (lane >= d) s += o;
     }
     __syncthreads();
     if (lane == 31) sums[w] = s;
     __syncthreads();
-    int32_t y = sums[lane], z = y;
+    int64_t y = sums[lane], z = y;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int32_t o = __shfl_up_sync(~0u, z, d);
+        const int64_t o = __shfl_up_sync(~0u, z, d);
         if (lane >= d) z += o;
     }
     *total = __shfl_sync(~0u, z, 31);
     return __shfl_sync(~0u, z - y, w) + s - x;
 }
 
-// The CTAs' numbers before this one's, and all of them. Two barriers of the cluster, so that *mine may change afterwards.
-__device__ __forceinline__ int64_t cluster_exclusive(cg::cluster_group &cluster, int32_t x, int64_t *total) {
-    __shared__ int32_t mine;
-    if (threadIdx.x == 0) mine = x;
-    cluster.sync();
-    int64_t before = 0, all = 0;
-    for (int i = 0; i < (int)cluster.num_blocks(); ++i) {
-        const int32_t y = *cluster.map_shared_rank(&mine, i);
-        if (i < (int)cluster.block_rank()) before += y;
-        all += y;
+// The CTAs of a launch. Between them a barrier costs a microsecond, most of it the fence that makes their writes visible; a CTA
+// alone is spared it.
+struct Ctas {
+    cg::cluster_group cluster = cg::this_cluster();
+    int rank = cluster.block_rank(), n = cluster.num_blocks();
+    int turn = 0;                      // of the numbers that sum() passes on: one is still read while the next is written
+    __device__ __forceinline__ void sync() {
+        if (n == 1) __syncthreads();
+        else cluster.sync();
     }
-    cluster.sync();
-    *total = all;
-    return before;
-}
+    // The CTAs' numbers before this one's, and all of them, by one barrier.
+    __device__ __forceinline__ int64_t sum(int64_t x, int64_t *total) {
+        __shared__ int64_t mine[2];
+        if (n == 1) {
+            __syncthreads();
+            *total = x;
+            return 0;
+        }
+        if (threadIdx.x == 0) mine[turn] = x;
+        cluster.sync();
+        int64_t before = 0, all = 0;
+        for (int i = 0; i < n; ++i) {
+            const int64_t y = *cluster.map_shared_rank(&mine[turn], i);
+            if (i < rank) before += y;
+            all += y;
+        }
+        turn ^= 1;
+        *total = all;
+        return before;
+    }
+    // No CTA may end while others read what it passed on.
+    __device__ __forceinline__ void end() {
+        if (n > 1) cluster.sync();
+    }
+};
 
 // Ids of set bits, or what else f does with (rank, id): all ids of a line of 32 at a time.
-template <class F> __device__ __forceinline__ void for_bits(uint32_t mine, int64_t first, int64_t rank, F f) {
+template <class F> __device__ __forceinline__ void for_bits(uint32_t mine, int64_t first, int64_t rank, int words, F f) {
     const int lane = threadIdx.x & 31;
+    if (!__any_sync(~0u, mine)) return;
 #pragma unroll 4
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < words; ++i) {
         const uint32_t bits = __shfl_sync(~0u, mine, i);
         const int64_t at = __shfl_sync(~0u, rank, i);
         if (bits >> lane & 1) f(at + __popc(bits & ((1u << lane) - 1)), (int32_t)(first + i * 32 + lane));
@@ -107,11 +146,11 @@ template <class F> __device__ __forceinline__ void for_bits(uint32_t mine, int64
 }
 
 __global__ void __launch_bounds__(kPageThreads, 1) kvx_pages_free_kernel(const PageArgs a) {
-    cg::cluster_group cluster = cg::this_cluster();
-    const int rank = cluster.block_rank(), ranks = cluster.num_blocks();
+    Ctas ctas;
+    const int rank = ctas.rank, ranks = ctas.n;
     wait_for_earlier();
     for (int64_t b = (int64_t)rank * kPageThreads + threadIdx.x; b < a.n_blocks; b += (int64_t)ranks * kPageThreads) a.refs[b] = 0;
-    cluster.sync();
+    ctas.sync();
     bool bad = false;
     for_entries(a.t.n_reqs, a.t.max_blocks, rank, ranks, [&](int32_t r, int32_t col) {
         const int32_t held = held_blocks(a.t, r, bad);
@@ -128,32 +167,34 @@ __global__ void __launch_bounds__(kPageThreads, 1) kvx_pages_free_kernel(const P
     if (a.t.max_blocks == 0)                       // no entries: the lengths are looked at all the same
         for (int32_t r = rank * kPageThreads + threadIdx.x; r < a.t.n_reqs; r += ranks * kPageThreads) held_blocks(a.t, r, bad);
     int64_t any, n_free = 0;
-    cluster_exclusive(cluster, __syncthreads_or(bad), &any);           // its barriers order the counts too
-    for (int64_t pass = 0; pass < a.n_blocks; pass += (int64_t)ranks * kPassBlocks) {
-        const int64_t first = pass + ((int64_t)rank * kPageWarps + (threadIdx.x >> 5)) * 1024, mine_at = first + (threadIdx.x & 31) * 32;
-        const uint32_t mine = first < a.n_blocks ? ~held_bits(a.refs, first, a.n_blocks) & bits_below(mine_at, a.n_blocks) : 0;
-        int32_t total;
-        const int32_t before = page_exclusive(__popc(mine), &total);
-        int64_t all;
-        const int64_t base = n_free + cluster_exclusive(cluster, total, &all);
-        for_bits(mine, first, base + before, [&](int64_t k, int32_t id) { a.free_blocks[k] = id; });
+    ctas.sum(__syncthreads_or(bad), &any);                             // its barrier orders the counts too
+    const Words own(a.n_blocks, rank, ranks);
+    const int lane = threadIdx.x & 31;
+    for (int64_t pass = 0; pass < a.n_blocks; pass += own.step) {
+        const int64_t first = pass + own.first;
+        const uint32_t held = held_bits(a.refs, first, a.n_blocks, own.words);
+        const uint32_t mine = lane < own.words ? ~held & bits_below(first + lane * 32, a.n_blocks) : 0;
+        int64_t total, all;
+        const int64_t before = page_exclusive(__popc(mine), &total), base = n_free + ctas.sum(total, &all);
+        for_bits(mine, first, base + before, own.words, [&](int64_t k, int32_t id) { a.free_blocks[k] = id; });
         n_free += all;
     }
     if (rank == 0 && threadIdx.x == 0) *a.result = {a.n_blocks - n_free, n_free, any ? KVX_ERANGE : KVX_OK};
+    ctas.end();
 }
 
 __global__ void __launch_bounds__(kPageThreads, 1) kvx_pages_fork_kernel(const ForkArgs a) {
-    cg::cluster_group cluster = cg::this_cluster();
-    const int rank = cluster.block_rank(), ranks = cluster.num_blocks();
+    Ctas ctas;
+    const int rank = ctas.rank, ranks = ctas.n;
     wait_for_earlier();
     const int64_t step = (int64_t)ranks * kPageThreads, t0 = (int64_t)rank * kPageThreads + threadIdx.x;
     for (int64_t r = t0; r < a.t.n_reqs; r += step) a.first[r] = INT32_MAX;
-    cluster.sync();
+    ctas.sync();
     for (int64_t i = t0; i < a.n_out; i += step) {
         const int32_t p = a.parent[i];
         if (p >= 0 && p < a.t.n_reqs) atomicMin(a.first + p, (int32_t)i);
     }
-    cluster.sync();
+    ctas.sync();
     bool bad = false;
     int64_t copies = 0, held_all = 0;
     for (int64_t pass = 0; pass < a.n_out; pass += step) {
@@ -173,12 +214,10 @@ __global__ void __launch_bounds__(kPageThreads, 1) kvx_pages_fork_kernel(const F
             last = a.t.block_table[p * a.t.table_stride + held - 1];
             if (last < 0) bad = true, need = false;                    // a page that the row does not hold
         }
-        int32_t total, held_total;
-        const int32_t before = page_exclusive(need, &total);
-        page_exclusive(held, &held_total);
-        int64_t all, held_pass;
-        const int64_t k = copies + cluster_exclusive(cluster, total, &all) + before;
-        cluster_exclusive(cluster, held_total, &held_pass);
+        // both sums in one: pages to copy above, blocks below (at most 2^14 rows a pass, of 2^31 blocks)
+        int64_t total, all;
+        const int64_t in_cta = page_exclusive((int64_t)need << 46 | held, &total), in_all = ctas.sum(total, &all);
+        const int64_t k = copies + ((in_all + in_cta) >> 46);
         int32_t to = -1;
         if (i < a.n_out) a.new_len[i] = len;
         if (need) {
@@ -186,8 +225,8 @@ __global__ void __launch_bounds__(kPageThreads, 1) kvx_pages_fork_kernel(const F
             a.src[k] = to < 0 ? -1 : last;
             a.dst[k] = to < 0 ? -1 : to;
         }
-        copies += all;
-        held_all += held_pass;
+        copies += all >> 46;
+        held_all += all & (((int64_t)1 << 46) - 1);
         const int64_t upto = min(step, a.n_out - pass);
         for_entries((int32_t)upto, a.t.max_blocks, rank, ranks, [&](int32_t r, int32_t col) {
             const int32_t from = a.parent[pass + r];
@@ -203,30 +242,36 @@ __global__ void __launch_bounds__(kPageThreads, 1) kvx_pages_fork_kernel(const F
             for (int e = 0; e < kEntries; ++e)
                 if (col + 32 * e < a.t.max_blocks) out[col + 32 * e] = b[e];
         });
-        cluster.sync();                                                // the row's last entry is written again, after its copy
+        ctas.sync();                                                   // the row's last entry is written again, after its copy
         if (need) a.new_table[i * a.new_stride + held - 1] = to;
     }
     for (int64_t k = copies + t0; k < a.n_out; k += step) a.src[k] = a.dst[k] = -1;
     int64_t any;
-    cluster_exclusive(cluster, __syncthreads_or(bad), &any);
+    ctas.sum(__syncthreads_or(bad), &any);
     if (rank == 0 && threadIdx.x == 0) *a.result = {held_all, copies, copies > a.n_free ? KVX_ENOMEM : any ? KVX_ERANGE : KVX_OK};
+    ctas.end();
 }
 
 __global__ void __launch_bounds__(kPageThreads, 1) kvx_pages_compact_kernel(const CompactArgs a) {
-    __shared__ int32_t s_src[kMovesShared];
-    cg::cluster_group cluster = cg::this_cluster();
-    const int rank = cluster.block_rank(), ranks = cluster.num_blocks();
+    __shared__ int32_t s_moves[2][kMovesShared];
+    Ctas ctas;
+    const int rank = ctas.rank, ranks = ctas.n;
     wait_for_earlier();
-    const int64_t per_pass = (int64_t)ranks * kPassBlocks;
-    const int64_t warp_at = ((int64_t)rank * kPageWarps + (threadIdx.x >> 5)) * 1024, lane_at = (threadIdx.x & 31) * 32;
+    const Words own(a.n_blocks, rank, ranks);
+    const int lane = threadIdx.x & 31;
+    const int64_t lane_at = lane * 32;
+    // Up to a pass, as pools of up to half a million blocks are, the bits are read once.
+    const bool once = a.n_blocks <= own.step;
+    uint32_t bits = once ? held_bits(a.refs, own.first, a.n_blocks, own.words) : 0;
     // blocks held below `end`
     auto count = [&](int64_t end) {
-        int32_t mine = 0, total;
-        for (int64_t first = warp_at; first < end; first += per_pass)
-            mine += __popc(held_bits(a.refs, first, a.n_blocks) & bits_below(first + lane_at, end));
+        int64_t mine = 0, total, all;
+        if (once) mine = __popc(bits & bits_below(own.first + lane_at, end));
+        else
+            for (int64_t first = own.first; first < end; first += own.step)
+                mine += __popc(held_bits(a.refs, first, a.n_blocks, own.words) & bits_below(first + lane_at, end));
         page_exclusive(mine, &total);
-        int64_t all;
-        cluster_exclusive(cluster, total, &all);
+        ctas.sum(total, &all);
         return all;
     };
     // With L blocks held, those held behind the first L go to the free ones among them: the free block b there has rank
@@ -234,57 +279,67 @@ __global__ void __launch_bounds__(kPageThreads, 1) kvx_pages_compact_kernel(cons
     const int64_t held = count(a.n_blocks), below = count(held), moves = held - below;
     const bool fits = moves <= a.max_moves;
     int64_t base = 0;
-    for (int64_t pass = 0; fits && pass < a.n_blocks; pass += per_pass) {
-        const int64_t first = pass + warp_at;
-        const uint32_t bits = first < a.n_blocks ? held_bits(a.refs, first, a.n_blocks) : 0;
-        int32_t total;
-        const int32_t in_cta = page_exclusive(__popc(bits), &total);
-        int64_t all;
-        const int64_t before = base + cluster_exclusive(cluster, total, &all) + in_cta;
+    for (int64_t pass = 0; fits && pass < a.n_blocks; pass += own.step) {
+        const int64_t first = pass + own.first;
+        if (!once) bits = held_bits(a.refs, first, a.n_blocks, own.words);
+        int64_t total, all;
+        const int64_t in_cta = page_exclusive(__popc(bits), &total), before = base + ctas.sum(total, &all) + in_cta;
         base += all;
-        const uint32_t front = bits_below(first + lane_at, held);
+        const uint32_t front = lane < own.words ? bits_below(first + lane_at, held) : 0;
         const uint32_t holes = ~bits & front, movers = bits & ~front;
-        for_bits(holes, first, first + lane_at - before, [&](int64_t k, int32_t id) { a.dst[k] = id; });
+        if (!__any_sync(~0u, holes | movers)) continue;                // of this warp; the loop's barriers are above
+        for_bits(holes, first, first + lane_at - before, own.words, [&](int64_t k, int32_t id) { a.dst[k] = id; });
         // ranks count held blocks alone: those of this lane's line that stand in the front come before its movers
-        for_bits(movers, first, before + __popc(bits & front) - below, [&](int64_t k, int32_t id) { a.src[k] = id; });
+        for_bits(movers, first, before + __popc(bits & front) - below, own.words, [&](int64_t k, int32_t id) { a.src[k] = id; });
     }
     const int64_t n = fits ? moves : 0;
     for (int64_t k = n + (int64_t)rank * kPageThreads + threadIdx.x; k < a.max_moves; k += (int64_t)ranks * kPageThreads) a.src[k] = a.dst[k] = -1;
-    cluster.sync();
-    const bool shared = n <= kMovesShared;
-    if (shared)
-        for (int k = threadIdx.x; k < n; k += kPageThreads) s_src[k] = __ldcg(a.src + k);
-    __syncthreads();
+    ctas.sync();
     bool bad = false;
-    for_entries(a.t.n_reqs, a.t.max_blocks, rank, ranks, [&](int32_t r, int32_t col) {
-        const int32_t mine = held_blocks(a.t, r, bad);
-        const int32_t *row = a.t.block_table + r * a.t.table_stride;
-        int32_t *out = a.new_table + r * a.new_stride;
-        int32_t b[kEntries];
+    // The new id of a block from L on: it stands among the moves, which are ascending.
+    auto remap = [&](const auto &src, const auto &dst) {
+        for_entries(a.t.n_reqs, a.t.max_blocks, rank, ranks, [&](int32_t r, int32_t col) {
+            const int32_t mine = held_blocks(a.t, r, bad);
+            const int32_t *row = a.t.block_table + r * a.t.table_stride;
+            int32_t *out = a.new_table + r * a.new_stride;
+            int32_t b[kEntries], at[kEntries];
+            bool moves[kEntries];
 #pragma unroll
-        for (int e = 0; e < kEntries; ++e) b[e] = col + 32 * e < a.t.max_blocks ? row[col + 32 * e] : -1;
+            for (int e = 0; e < kEntries; ++e) b[e] = col + 32 * e < a.t.max_blocks ? row[col + 32 * e] : -1;
 #pragma unroll
-        for (int e = 0; e < kEntries; ++e) {
-            if (col + 32 * e >= a.t.max_blocks) break;
-            if (col + 32 * e < mine) {
-                if (b[e] < 0 || b[e] >= a.n_blocks) bad = true;
-                else if (b[e] >= held && fits) {
-                    int32_t lo = 0, hi = (int32_t)n;                   // the first not below
-                    while (lo < hi) {
-                        const int32_t mid = (lo + hi) >> 1, x = shared ? s_src[mid] : __ldcg(a.src + mid);
-                        if (x < b[e]) lo = mid + 1; else hi = mid;
-                    }
-                    const bool found = lo < n && (shared ? s_src[lo] : __ldcg(a.src + lo)) == b[e];
-                    if (found) b[e] = __ldcg(a.dst + lo);
-                    bad |= !found;                                     // the counts are not those of this table
+            for (int e = 0; e < kEntries; ++e) {
+                const bool in = col + 32 * e < mine;
+                bad |= in && (b[e] < 0 || b[e] >= a.n_blocks);
+                moves[e] = in && fits && b[e] >= held && b[e] < a.n_blocks;
+                at[e] = 0;
+            }
+            if (moves[0] || moves[1] || moves[2] || moves[3]) {
+                for (int32_t half = n > 0 ? 1 << (31 - __clz((int)n)) : 0; half; half >>= 1)   // how many are below, from the highest bit down
+#pragma unroll
+                    for (int e = 0; e < kEntries; ++e)
+                        if (at[e] + half <= n && src(at[e] + half - 1) < b[e]) at[e] += half;
+#pragma unroll
+                for (int e = 0; e < kEntries; ++e) {
+                    const bool found = moves[e] && at[e] < n && src(at[e]) == b[e];
+                    bad |= moves[e] && !found;                         // the counts are not those of this table
+                    if (found) b[e] = dst(at[e]);
                 }
             }
-            out[col + 32 * e] = b[e];
-        }
-    });
+#pragma unroll
+            for (int e = 0; e < kEntries; ++e)
+                if (col + 32 * e < a.t.max_blocks) out[col + 32 * e] = b[e];
+        });
+    };
+    if (n <= kMovesShared) {
+        for (int k = threadIdx.x; k < n; k += kPageThreads) s_moves[0][k] = __ldcg(a.src + k), s_moves[1][k] = __ldcg(a.dst + k);
+        __syncthreads();
+        remap([&](int64_t k) { return s_moves[0][k]; }, [&](int64_t k) { return s_moves[1][k]; });
+    } else
+        remap([&](int64_t k) { return __ldcg(a.src + k); }, [&](int64_t k) { return __ldcg(a.dst + k); });
     int64_t any;
-    cluster_exclusive(cluster, __syncthreads_or(bad), &any);
+    ctas.sum(__syncthreads_or(bad), &any);
     if (rank == 0 && threadIdx.x == 0) *a.result = {held, moves, !fits ? KVX_ENOMEM : any ? KVX_ERANGE : KVX_OK};
+    ctas.end();
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -364,7 +419,7 @@ template <class A> static cudaError_t launch_cluster(void (*kernel)(A), int64_t 
         if (e != cudaSuccess) return e;
         asked.fetch_or(bit, std::memory_order_relaxed);
     }
-    const unsigned ctas = work <= 4 * kPageThreads ? 1 : work <= 64 * kPageThreads ? 8 : kPageCluster;
+    const unsigned ctas = work <= 16 * kPageThreads ? 1 : work <= 64 * kPageThreads ? 8 : kPageCluster;
     cudaLaunchAttribute attr[2] = {};
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -27,7 +27,7 @@
 namespace kvx {
 
 constexpr int kSharedTile = 128, kSharedRows = 128;                // positions of a tile, rows of a slot
-constexpr int kSharedThreads = 13 * 32;                            // warps 0-7: softmax, four a slot; 8: products; 9-12: copies
+constexpr int kSharedThreads = 16 * 32;                            // warps 0-7: softmax, four a slot; 8: products; 12-15: copies
 constexpr int kSharedLoaders = 128;
 constexpr int kSharedSwitch = 3;                                   // what a change of units counts, in places of the line
 constexpr int kSharedMin = 4;                                      // places of a CTA at least
@@ -75,13 +75,13 @@ template <int VT_, int IO_, int D_> struct SharedShape {
     static constexpr int OFF_RING = 2 * TILE;                      // behind the queries of the two slots
     static constexpr int STAGES = ((224 << 10) - OFF_RING) / TILE < 8 ? ((224 << 10) - OFF_RING) / TILE : 8;
     static constexpr int BYTES = OFF_RING + STAGES * TILE;
-    // Copies go on for LAG items before the oldest is waited for. An item's stage is free again once the item after it has
-    // been multiplied, at the latest, so that one must have been handed over before the stage is waited for.
-    static constexpr int LAG = STAGES - 2;
     static constexpr float UP = MT == KVX_F16 ? 12.0f : 0.0f;      // f16 weights are taken times 2^12, up to 2^15: their step is 2^-36
     static constexpr uint32_t IDESC = 1u << 4 | (MT == KVX_BF16 ? 1u << 7 | 1u << 10 : 0) | (uint32_t)(kSharedRows / 16) << 24;
     static constexpr uint32_t IDESC_SCORES = IDESC | (uint32_t)(kSharedTile / 8) << 17;
     static constexpr uint32_t IDESC_SUMS = IDESC | (uint32_t)(D / 8) << 17 | 1u << 16;        // V by columns
+    // Registers a thread: a softmax warp holds a row's 128 scores. Four warpgroups of 128 at the launch are 512.
+    static constexpr int REGS_SOFTMAX = F8 ? 168 : 184, REGS_PRODUCTS = 64, REGS_COPIES = F8 ? 112 : 80;
+    static_assert(2 * REGS_SOFTMAX + REGS_PRODUCTS + REGS_COPIES <= 512, "a warpgroup would wait for registers that nobody has");
     static constexpr int PIECES = D / 8;                           // of 16 bytes in a row of shared memory
     static_assert(STAGES >= 4, "keys and values of two tiles");
 };
@@ -129,30 +129,34 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 
+// Registers of this warpgroup's threads from here on; what the others give up.
+template <int N> __device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void leave_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // Two weights as two values each.
 template <class S> __device__ __forceinline__ void two_values(float2 p, uint32_t &hi, uint32_t &lo) {
-    const float2 minus = make_float2(-1.0f, -1.0f);
-    if constexpr (S::MT == KVX_BF16) {                             // the lowest bit set: what is cut off is not zero
-        p.x = __uint_as_float(__float_as_uint(p.x) | 1u);
-        p.y = __uint_as_float(__float_as_uint(p.y) | 1u);
+    if constexpr (S::MT == KVX_BF16) {                             // what is cut off, and 2^-23 of the rest: never zero
+        const float2 minus = make_float2(-1.0f + 0x1p-23f, -1.0f + 0x1p-23f);
         hi = __byte_perm(__float_as_uint(p.x), __float_as_uint(p.y), 0x7632);
         const float2 top = make_float2(__uint_as_float(__float_as_uint(p.x) & 0xffff0000u), __uint_as_float(__float_as_uint(p.y) & 0xffff0000u));
         const float2 rest = fma2(top, minus, p);
         lo = pack<KVX_BF16>(rest.x, rest.y);
     } else if constexpr (S::F8) {                                  // 8-bit values are finite
+        const float2 minus = make_float2(-1.0f, -1.0f);
         hi = pack<KVX_F16>(p.x, p.y);
         const float2 rest = fma2(unpack<KVX_F16>(hi), minus, p);
         lo = pack<KVX_F16>(rest.x, rest.y);
     } else {
+        const float2 minus = make_float2(-1.0f, -1.0f);
         hi = pack_down<KVX_F16>(p.x, p.y);
         const float2 rest = fma2(unpack<KVX_F16>(hi), minus, p);
         lo = pack_down<KVX_F16>(rest.x, rest.y) | 0x00010001u;     // cut off to an odd last place
     }
 }
 
-template <int N> __device__ __forceinline__ void copies_wait_at_most(int n) {
-    if (n >= N) copies_wait<N>();
-    else if constexpr (N > 0) copies_wait_at_most<N - 1>(n);
+// This thread's copies so far count as an arrival once they are through.
+__device__ __forceinline__ void copies_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(shared_addr(bar)) : "memory");
 }
 
 template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_attend_shared(const __grid_constant__ SharedArgs s) {
@@ -171,7 +175,7 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
         s_failed = 0;
         auto init = [](uint64_t *bar, int n) { asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_addr(bar)), "r"(n) : "memory"); };
         for (int i = 0; i < S::STAGES; ++i) {
-            init(&s_full[i], kSharedLoaders);
+            init(&s_full[i], S::F8 ? kSharedLoaders : kSharedLoaders + 4);
             init(&s_free[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -222,6 +226,7 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
     work.index = s_first;
 
     if (w < 8) {                                                   // softmax and partial results
+        take_registers<S::REGS_SOFTMAX>();
         const int slot = w >> 2, row = (w & 3) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(w & 3) << 21);
         const uint32_t sums = lanes + kSharedColSums + slot * 128, scores = lanes + kSharedColScores + slot * 128;
@@ -239,63 +244,53 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
                 const uint4 four = *reinterpret_cast<const uint4 *>(s_live[(tiles + (work.both ? i : 2 * i + slot)) & 7]);
                 const uint32_t live[4] = {four.x, four.y, four.z, four.w};
                 const bool all = (four.x & four.y & four.z & four.w) == ~0u;
-                uint32_t x[2][32];
-                float top = -INFINITY;
-                tmem_load32(x[0], scores);
+                uint32_t x[4][32];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    tmem_load_wait();
-                    if (c < 3) tmem_load32(x[(c + 1) & 1], scores + (c + 1) * 32);
-                    float y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    if (all) {
+                for (int c = 0; c < 4; ++c) tmem_load32(x[c], scores + c * 32);
+                tmem_load_wait();
+                if (!all) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) y[k & 3] = fmaxf(y[k & 3], __uint_as_float(x[c & 1][k]));
-                    } else {
+                    for (int c = 0; c < 4; ++c)
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) y[k & 3] = fmaxf(y[k & 3], live[c] >> k & 1 ? __uint_as_float(x[c & 1][k]) : -INFINITY);
-                    }
-                    top = fmaxf(top, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])));
+                        for (int k = 0; k < 32; ++k)
+                            if (!(live[c] >> k & 1)) x[c][k] = 0xff800000u;            // -infinity
                 }
-                tmem_load32(x[0], scores);                         // again, for the weights
-                top = fmaf(top, sc, -S::UP);
+                float y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) y[c] = fmaxf(y[c], __uint_as_float(x[c][k]));
+                const float top = fmaf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), sc, -S::UP);
                 const bool moves = top > m + kSharedSlack;
                 if (__any_sync(~0u, moves)) {                      // the products of this slot's tile before are done: these scores came after
                     const float up = moves ? top : m, old = moves ? fast_exp2(m - up) : 1.0f;
                     m = up;
                     l.x *= old;
                     l.y *= old;
-                    if (i > 0) {
-                        tmem_load_wait();
+                    if (i > 0)
 #pragma unroll 1
-                        for (int c = 0; c < S::D; c += 32) {
-                            uint32_t o[32];
-                            tmem_load32(o, sums + c);
+                        for (int c = 0; c < S::D; c += 8) {
+                            uint32_t o[8];
+                            tmem_load(o, sums + c);
                             tmem_load_wait();
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * old);
-                            tmem_store32(o, sums + c);
+                            for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * old);
+                            tmem_store(o, sums + c);
                         }
-                    }
                 }
                 const float ref = m == -INFINITY ? 0.0f : m;
                 const float2 sc2 = make_float2(sc, sc), ref2 = make_float2(-ref, -ref);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    tmem_load_wait();
-                    if (c < 3) tmem_load32(x[(c + 1) & 1], scores + (c + 1) * 32);
-                    uint32_t y[32];                                // the first values of 32 weights, then the second ones
+                    uint32_t z[32];                                // the first values of 32 weights, then the second ones
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
-                        const float2 z = fma2(make_float2(__uint_as_float(x[c & 1][2 * k]), __uint_as_float(x[c & 1][2 * k + 1])), sc2, ref2);
-                        float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
-                        if (!all) {
-                            if (!(live[c] >> (2 * k) & 1)) p.x = 0.0f;
-                            if (!(live[c] >> (2 * k + 1) & 1)) p.y = 0.0f;
-                        }
+                        const float2 e = fma2(make_float2(__uint_as_float(x[c][2 * k]), __uint_as_float(x[c][2 * k + 1])), sc2, ref2);
+                        const float2 p = make_float2(fast_exp2(e.x), fast_exp2(e.y));
                         l = add2(l, p);
-                        two_values<S>(p, y[k], y[16 + k]);
+                        two_values<S>(p, z[k], z[16 + k]);
                     }
-                    tmem_store32(y, scores + c * 32);
+                    tmem_store32(z, scores + c * 32);
                 }
                 tmem_store_wait();
                 tensor_fence_before();
@@ -326,68 +321,87 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
             tiles += work.n;
             turn += work.n > 0;
         }
-    } else if (w == 8) {                                           // products
+    } else if (w < 12) {                                           // products, by the first of these warps
+        leave_registers<S::REGS_PRODUCTS>();
+        if (w == 8) {
         const uint64_t queries = operand(shared_addr(smem), 16, 1024, 2), ring = operand(shared_addr(smem + S::OFF_RING), 16, 1024, 2);
         const uint64_t values = operand(shared_addr(smem + S::OFF_RING), S::CHUNK, 1024, 2);
-        int item = 0, turn = 0, weighed[2] = {0, 0};
+        // What the operands are made of is the same in all lanes, and comes from reductions, so that the compiler knows it too.
+        const uint32_t columns = __reduce_max_sync(~0u, tmem);
+        int item = 0, turn = 0, weighed = 0;                       // weighed: phases of slot 0, and 2^16 times those of slot 1
         bool ok = __all_sync(~0u, goes_on(kStallSharedProducts));
         for (; ok && work.read(s, c_begin, c_end, units); ++work.index) {
-            const int n = work.n, total = work.both ? 2 * n : n;
+            const int n = (int)__reduce_max_sync(~0u, (uint32_t)work.n);
+            const bool both = __any_sync(~0u, work.both);
+            const int total = both ? 2 * n : n;
             if (n == 0) continue;
             if (!(ok = __all_sync(~0u, wait(&s_queried, turn++)))) break;
+            fence_async();                                         // copies come by the generic proxy, products read by the other
             auto score = [&](int k) {
-                const int slot = k & 1, t = work.both ? k >> 1 : k, at = t ? item + 2 * t - 1 : item, stage = at % S::STAGES;
-                if (!(work.both && slot)) ok = ok && __all_sync(~0u, wait(&s_full[stage], at / S::STAGES));
+                const int slot = k & 1, t = both ? k >> 1 : k, at = t ? item + 2 * t - 1 : item, stage = at % S::STAGES;
+                if (!(both && slot)) {
+                    ok = ok && __all_sync(~0u, wait(&s_full[stage], at / S::STAGES));
+                    fence_async();
+                }
                 if (!ok) return;
-                const uint64_t q = queries + (work.both && slot ? S::TILE / 16 : 0), keys = ring + stage * (S::TILE / 16);
+                const uint64_t q = queries + (both && slot ? S::TILE / 16 : 0), keys = ring + stage * (S::TILE / 16);
+                const uint32_t d = columns + kSharedColScores + slot * 128;
 #pragma unroll
                 for (int y = 0; y < S::D / 16; ++y)                // 32 bytes of the rows
-                    tensor_mma<false>(tmem + kSharedColScores + slot * 128, q + y / 4 * (S::CHUNK / 16) + y % 4 * 2, keys + y / 4 * (S::CHUNK / 16) + y % 4 * 2,
-                                      S::IDESC_SCORES, y > 0);
-                if (!work.both || slot) tensor_commit(&s_free[stage]);
+                    tensor_mma<false>(d, q + y / 4 * (S::CHUNK / 16) + y % 4 * 2, keys + y / 4 * (S::CHUNK / 16) + y % 4 * 2, S::IDESC_SCORES, y > 0);
+                if (!both || slot) tensor_commit(&s_free[stage]);
                 if (k == total - 1) tensor_commit(&s_unqueried);
                 tensor_commit(&s_scored[slot]);
             };
             score(0);
             if (total > 1) score(1);
             for (int k = 0; ok && k < total; ++k) {
-                const int slot = k & 1, t = work.both ? k >> 1 : k, at = t + 1 < n ? item + 2 * t + 2 : item + 2 * n - 1, stage = at % S::STAGES;
-                ok = __all_sync(~0u, wait(&s_weighed[slot], weighed[slot]++));
+                const int slot = k & 1, t = both ? k >> 1 : k, at = t + 1 < n ? item + 2 * t + 2 : item + 2 * n - 1, stage = at % S::STAGES;
+                ok = __all_sync(~0u, wait(&s_weighed[slot], slot ? weighed >> 16 : weighed));
+                weighed = slot ? weighed + 65536 : (weighed & ~0xffff) | ((weighed + 1) & 0xffff);
                 tensor_fence_after();
-                if (!(work.both && slot)) ok = ok && __all_sync(~0u, wait(&s_full[stage], at / S::STAGES));
+                if (!(both && slot)) {
+                    ok = ok && __all_sync(~0u, wait(&s_full[stage], at / S::STAGES));
+                    fence_async();
+                }
                 if (!ok) break;
                 const uint64_t v = values + stage * (S::TILE / 16);
-                const uint32_t p = tmem + kSharedColScores + slot * 128;
+                const uint32_t d = columns + kSharedColSums + slot * 128, p = columns + kSharedColScores + slot * 128;
 #pragma unroll
                 for (int y = 0; y < kSharedTile / 16; ++y)         // 16 positions
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        tensor_mma_tmem(tmem + kSharedColSums + slot * 128, p + y / 2 * 32 + h * 16 + y % 2 * 8, v + y * (2048 / 16), S::IDESC_SUMS,
-                                        k >= 2 || y > 0 || h > 0);
-                if (!work.both || slot) tensor_commit(&s_free[stage]);
+                        tensor_mma_tmem(d, p + y / 2 * 32 + h * 16 + y % 2 * 8, v + y * (2048 / 16), S::IDESC_SUMS, k >= 2 || y > 0 || h > 0);
+                if (!both || slot) tensor_commit(&s_free[stage]);
                 if (k + 2 >= total) tensor_commit(&s_summed[slot]);
                 else score(k + 2);
             }
             item += 2 * n;
         }
+        }
     } else {                                                       // copies
-        const int lw = w - 9;
-        int item = 0, handed = 0, turn = 0, tiles = 0;
+        leave_registers<S::REGS_COPIES>();
+        const int lw = w - 12;
+        int item = 0, turn = 0, tiles = 0;
         bool ok = __all_sync(~0u, goes_on(kStallSharedCopies));
         const uint32_t smem0 = shared_addr(smem);
-        // Position `lane` of this warp's quarter of a tile: its row's offset in its buffer, in 16-byte units.
-        auto look_up = [&](int tile) {
+        // Position `lane` of this warp's quarter of a tile: its block, -2 behind the prefix; then its row's offset in its buffer, in
+        // 16-byte units. In two steps, so that the block's id is on its way a tile ahead.
+        auto block_of = [&](int tile) {
             const uint32_t pos = (uint32_t)tile * kSharedTile + lw * 32 + lane;
+            if (pos >= (uint32_t)work.u.tokens) return -2;
+            return max(a.block_table[work.u.first * a.table_stride + ((__umulhi(pos, a.block_mul) + pos) >> a.block_shift)], -1);
+        };
+        auto row_of = [&](int32_t blk, int tile) {
+            const uint32_t pos = (uint32_t)tile * kSharedTile + lw * 32 + lane, col = (__umulhi(pos, a.block_mul) + pos) >> a.block_shift;
             uint32_t at = kNoRow;
-            if (pos < (uint32_t)work.u.tokens) {
-                const uint32_t col = (__umulhi(pos, a.block_mul) + pos) >> a.block_shift;
-                const int32_t blk = a.block_table[work.u.first * a.table_stride + col];
-                if (blk >= 0 && blk < a.pool.n_blocks)
-                    at = (uint32_t)blk * a.block_pitch16 + (pos - col * (uint32_t)a.pool.block_size) * a.token_pitch16;
-                else if (work.u.kvh == 0 && work.u.pair == 0) atomicAdd(a.pool.skipped, 1ull);
-            }
-            const uint32_t bits = __ballot_sync(~0u, at != kNoRow);
-            return make_uint2(at, bits);
+            if (blk >= 0 && blk < a.pool.n_blocks) at = (uint32_t)blk * a.block_pitch16 + (pos - col * (uint32_t)a.pool.block_size) * a.token_pitch16;
+            else if (blk != -2 && work.u.kvh == 0 && work.u.pair == 0) atomicAdd(a.pool.skipped, 1ull);
+            return at;
+        };
+        auto set_live = [&](int tile, uint32_t row) {
+            const uint32_t bits = __ballot_sync(~0u, row != kNoRow);
+            if (lane == 0) s_live[tile & 7][lw] = bits;
         };
         auto query_row = [&](int r) {                              // of the unit; NULL: none
             if (r >= work.u.rows) return (const uint8_t *)nullptr;
@@ -401,14 +415,6 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
             const bool piece_in = piece * 8 < a.head_dim;
             const uint32_t piece_at = piece / 8 * S::CHUNK;
             auto place = [&](int r) { return piece_at + r * 128 + ((piece % 8) ^ (r & 7)) * 16; };
-            auto settle = [&](int keep) {                          // hands over all but `keep` of the items
-                while (handed < item - keep) {
-                    copies_wait_at_most<S::LAG>(item - handed - 1);
-                    fence_async();
-                    arrive(&s_full[handed % S::STAGES]);
-                    ++handed;
-                }
-            };
             auto put = [&](const uint8_t *from, uint32_t row) {
                 if (item >= S::STAGES) ok = ok && __all_sync(~0u, wait(&s_free[item % S::STAGES], item / S::STAGES - 1));
                 if (!ok) return;
@@ -421,30 +427,32 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
                     const bool in = at != kNoRow && piece_in;
                     copy_async(to + place(lw * 32 + r), from + (in ? (uint64_t)at * 16 : 0), in);
                 }
-                copies_commit();
+                copies_arrive(&s_full[item % S::STAGES]);
+                if (lane == 0) arrive(&s_full[item % S::STAGES]);     // with what it wrote to s_live
                 ++item;
-                settle(S::LAG);
             };
             for (; ok && work.read(s, c_begin, c_end, units); ++work.index) {
                 if (work.n == 0) continue;
                 const int32_t shard = work.u.kvh / a.pool.heads_per_shard;
                 const int64_t head = (int64_t)(work.u.kvh - shard * a.pool.heads_per_shard) * a.pool.head_pitch;
                 const uint8_t *const keys = a.pool.k[shard] + head, *const vals = a.pool.v[shard] + head;
-                uint2 row = look_up(work.t0), next = row;
-                if (lane == 0) s_live[tiles & 7][lw] = row.y;
-                put(keys, row.x);
+                // keys of a tile, then values of the one before
+                uint32_t row = row_of(block_of(work.t0), work.t0), next = row;
+                int32_t blk = work.n > 1 ? block_of(work.t0 + 1) : -2;
+                set_live(tiles, row);
+                put(keys, row);
                 for (int t = 0; ok && t < work.n; ++t) {
                     if (t + 1 < work.n) {
-                        next = look_up(work.t0 + t + 1);
-                        if (lane == 0) s_live[(tiles + t + 1) & 7][lw] = next.y;
-                        put(keys, next.x);
+                        next = row_of(blk, work.t0 + t + 1);
+                        if (t + 2 < work.n) blk = block_of(work.t0 + t + 2);
+                        set_live(tiles + t + 1, next);
+                        put(keys, next);
                     }
                     if (!ok) break;
-                    put(vals, row.x);
+                    put(vals, row);
                     row = next;
                     if (t) continue;
-                    // Queries, once those before have been multiplied, which may need what is on its way.
-                    settle(0);
+                    // Queries, once those before have been multiplied.
                     if (turn) ok = ok && __all_sync(~0u, wait(&s_unqueried, turn - 1));
                     if (!ok) break;
                     for (int b = 0; b < (work.both ? 2 : 1); ++b) {
@@ -457,16 +465,13 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
                             copy_async(smem0 + b * S::TILE + place(lw * 32 + r), in ? (const uint8_t *)p + piece * 16 : a.q, in);
                         }
                     }
-                    copies_commit();
-                    copies_wait<0>();
-                    fence_async();
-                    arrive(&s_queried);
+                    copies_arrive(&s_queried);
                     ++turn;
                 }
                 tiles += work.n;
             }
-            if (ok) settle(0);
-            copies_wait<0>();
+            copies_commit();
+            copies_wait<0>();                                      // none outlives the CTA
         } else {
             // A row has D / 16 pieces of 16 codes; a lane reads READS of its warp's 32 rows.
             constexpr int CODES = S::D / 16, READS = CODES, AT_ONCE = 32 / CODES;
@@ -500,7 +505,6 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
                     write(place(to, r, 2 * piece), z[0], z[1], z[2], z[3]);
                     write(place(to, r, 2 * piece + 1), z[4], z[5], z[6], z[7]);
                 }
-                fence_async();
                 arrive(&s_full[item % S::STAGES]);
                 ++item;
             };
@@ -533,7 +537,6 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
                         write(place(smem0 + b * S::TILE, lw * 32 + r, p), y.x, y.y, y.z, y.w);
                     }
                 }
-                fence_async();
                 arrive(&s_queried);
                 ++turn;
             };
@@ -543,25 +546,28 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
                 const int64_t head = (int64_t)(work.u.kvh - shard * a.pool.heads_per_shard) * a.pool.head_pitch;
                 const uint8_t *const keys = a.pool.k[shard] + head, *const vals = a.pool.v[shard] + head;
                 // keys of tile t + 1, then values of tile t: each read while the one before is written
-                uint2 row = look_up(work.t0), next = row;
-                fetch(x[0], keys, row.x);
-                if (lane == 0) s_live[tiles & 7][lw] = row.y;
+                uint32_t row = row_of(block_of(work.t0), work.t0), next = row;
+                int32_t blk = work.n > 1 ? block_of(work.t0 + 1) : -2;
+                fetch(x[0], keys, row);
+                set_live(tiles, row);
                 load_queries();
                 if (ok) store(x[0]);
                 if (work.n > 1) {
-                    next = look_up(work.t0 + 1);
-                    fetch(x[0], keys, next.x);
+                    next = row_of(blk, work.t0 + 1);
+                    if (work.n > 2) blk = block_of(work.t0 + 2);
+                    fetch(x[0], keys, next);
                 }
                 for (int t = 0; ok && t < work.n; ++t) {
-                    fetch(x[1], vals, row.x);
+                    fetch(x[1], vals, row);
                     if (t + 1 < work.n) {
-                        if (lane == 0) s_live[(tiles + t + 1) & 7][lw] = next.y;
+                        set_live(tiles + t + 1, next);
                         store(x[0]);
                         row = next;
                     }
                     if (t + 2 < work.n) {
-                        next = look_up(work.t0 + t + 2);
-                        fetch(x[0], keys, next.x);
+                        next = row_of(blk, work.t0 + t + 2);
+                        if (t + 3 < work.n) blk = block_of(work.t0 + t + 3);
+                        fetch(x[0], keys, next);
                     }
                     if (ok) store(x[1]);
                 }
