@@ -162,7 +162,7 @@ __device__ __forceinline__ void copies_arrive(uint64_t *bar) {
 template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_attend_shared(const __grid_constant__ SharedArgs s) {
     extern __shared__ __align__(1024) uint8_t smem[];              // queries of the slots, then the ring
     __shared__ __align__(8) uint64_t s_full[S::STAGES], s_free[S::STAGES], s_queried, s_unqueried;
-    __shared__ __align__(8) uint64_t s_scored[2], s_weighed[2], s_summed[2], s_drained, s_never;
+    __shared__ __align__(8) uint64_t s_scored[2], s_weighed[2][2], s_summed[2], s_drained[2], s_never;   // per slot; weights in halves of a tile
     __shared__ __align__(16) uint32_t s_live[8][4];                // live positions of the last tiles
     __shared__ float s_scale[2][2][S::F8 ? kSharedRows : 1];       // by turns of units, per slot: of 8-bit caches' bf16 queries
     __shared__ uint32_t s_tmem;
@@ -176,16 +176,16 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
         auto init = [](uint64_t *bar, int n) { asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_addr(bar)), "r"(n) : "memory"); };
         for (int i = 0; i < S::STAGES; ++i) {
             init(&s_full[i], S::F8 ? kSharedLoaders : kSharedLoaders + 4);
-            init(&s_free[i], 1);
+            init(&s_free[i], 2);                                   // each slot's products, or twice those of the one that took it
         }
         for (int i = 0; i < 2; ++i) {
             init(&s_scored[i], 1);
-            init(&s_weighed[i], kSharedRows);
+            for (int h = 0; h < 2; ++h) init(&s_weighed[i][h], kSharedRows);
             init(&s_summed[i], 1);
+            init(&s_drained[i], 1);
         }
         init(&s_queried, kSharedLoaders);
-        init(&s_unqueried, 1);
-        init(&s_drained, 1);
+        init(&s_unqueried, 2);
         init(&s_never, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -215,6 +215,7 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
     tensor_fence_after();
     const uint32_t tmem = s_tmem;
     auto wait = [&](uint64_t *bar, uint32_t parity) {              // of any role: false when it, or another role's, ran out
+        if (phase_done(bar, parity & 1)) return true;
         if (s_failed) return false;
         if (wait_full(bar, parity & 1, a.wait_ns)) return true;
         s_failed = 1;
@@ -291,10 +292,12 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
                         two_values<S>(p, z[k], z[16 + k]);
                     }
                     tmem_store32(z, scores + c * 32);
+                    if (c & 1) {                                   // half a tile's weights: their products begin
+                        tmem_store_wait();
+                        tensor_fence_before();
+                        arrive(&s_weighed[slot][c >> 1]);
+                    }
                 }
-                tmem_store_wait();
-                tensor_fence_before();
-                arrive(&s_weighed[slot]);
             }
             if (!ok) break;
             // the partial result
@@ -321,63 +324,67 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
             tiles += work.n;
             turn += work.n > 0;
         }
-    } else if (w < 12) {                                           // products, by the first of these warps
+    } else if (w < 12) {                                           // products, of a slot by each of the first two of these warps
         leave_registers<S::REGS_PRODUCTS>();
-        if (w == 8) {
+        // A slot's products are issued in their order by one warp and go through the pipe in it, so that the scores of its next tile
+        // may take the place of the weights as soon as they are issued. What the operands are made of is the same in all lanes;
+        // it comes from reductions, so that the compiler knows it too.
+        const int slot = (int)__reduce_max_sync(~0u, (uint32_t)(w - 8));
+        const uint32_t columns = __reduce_max_sync(~0u, tmem);
         const uint64_t queries = operand(shared_addr(smem), 16, 1024, 2), ring = operand(shared_addr(smem + S::OFF_RING), 16, 1024, 2);
         const uint64_t values = operand(shared_addr(smem + S::OFF_RING), S::CHUNK, 1024, 2);
-        // What the operands are made of is the same in all lanes, and comes from reductions, so that the compiler knows it too.
-        const uint32_t columns = __reduce_max_sync(~0u, tmem);
-        int item = 0, turn = 0, weighed = 0;                       // weighed: phases of slot 0, and 2^16 times those of slot 1
-        bool ok = __all_sync(~0u, goes_on(kStallSharedProducts));
+        const uint32_t scores = columns + kSharedColScores + slot * 128, sums = columns + kSharedColSums + slot * 128;
+        int item = 0, turn = 0, weighed = 0;
+        bool ok = slot < 2 && __all_sync(~0u, goes_on(kStallSharedProducts));
         for (; ok && work.read(s, c_begin, c_end, units); ++work.index) {
             const int n = (int)__reduce_max_sync(~0u, (uint32_t)work.n);
-            const bool both = __any_sync(~0u, work.both);
-            const int total = both ? 2 * n : n;
             if (n == 0) continue;
+            const bool both = __any_sync(~0u, work.both);
+            const int first = both ? 0 : slot, step = both ? 1 : 2;            // the slot's tiles
             if (!(ok = __all_sync(~0u, wait(&s_queried, turn++)))) break;
             fence_async();                                         // copies come by the generic proxy, products read by the other
-            auto score = [&](int k) {
-                const int slot = k & 1, t = both ? k >> 1 : k, at = t ? item + 2 * t - 1 : item, stage = at % S::STAGES;
-                if (!(both && slot)) {
-                    ok = ok && __all_sync(~0u, wait(&s_full[stage], at / S::STAGES));
-                    fence_async();
-                }
+            const uint64_t q = queries + (both ? slot * (S::TILE / 16) : 0);
+            auto release = [&](int stage) {
+                tensor_commit(&s_free[stage]);
+                if (!both) tensor_commit(&s_free[stage]);
+            };
+            auto score = [&](int t) {
+                const int at = t ? item + 2 * t - 1 : item, stage = at % S::STAGES;
+                ok = __all_sync(~0u, wait(&s_full[stage], at / S::STAGES));
                 if (!ok) return;
-                const uint64_t q = queries + (both && slot ? S::TILE / 16 : 0), keys = ring + stage * (S::TILE / 16);
-                const uint32_t d = columns + kSharedColScores + slot * 128;
+                fence_async();
+                const uint64_t keys = ring + stage * (S::TILE / 16);
 #pragma unroll
                 for (int y = 0; y < S::D / 16; ++y)                // 32 bytes of the rows
-                    tensor_mma<false>(d, q + y / 4 * (S::CHUNK / 16) + y % 4 * 2, keys + y / 4 * (S::CHUNK / 16) + y % 4 * 2, S::IDESC_SCORES, y > 0);
-                if (!both || slot) tensor_commit(&s_free[stage]);
-                if (k == total - 1) tensor_commit(&s_unqueried);
+                    tensor_mma<false>(scores, q + y / 4 * (S::CHUNK / 16) + y % 4 * 2, keys + y / 4 * (S::CHUNK / 16) + y % 4 * 2, S::IDESC_SCORES, y > 0);
                 tensor_commit(&s_scored[slot]);
+                release(stage);
+                if (t + step >= n) tensor_commit(&s_unqueried);
             };
-            score(0);
-            if (total > 1) score(1);
-            for (int k = 0; ok && k < total; ++k) {
-                const int slot = k & 1, t = both ? k >> 1 : k, at = t + 1 < n ? item + 2 * t + 2 : item + 2 * n - 1, stage = at % S::STAGES;
-                ok = __all_sync(~0u, wait(&s_weighed[slot], slot ? weighed >> 16 : weighed));
-                weighed = slot ? weighed + 65536 : (weighed & ~0xffff) | ((weighed + 1) & 0xffff);
-                tensor_fence_after();
-                if (!(both && slot)) {
-                    ok = ok && __all_sync(~0u, wait(&s_full[stage], at / S::STAGES));
-                    fence_async();
+            if (first < n) score(first);
+            else tensor_commit(&s_unqueried);
+            for (int t = first; ok && t < n; t += step, ++weighed) {
+                const int at = t + 1 < n ? item + 2 * t + 2 : item + 2 * n - 1, stage = at % S::STAGES;
+                ok = __all_sync(~0u, wait(&s_full[stage], at / S::STAGES));
+                fence_async();
+                const uint64_t v = values + stage * (S::TILE / 16);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    ok = ok && __all_sync(~0u, wait(&s_weighed[slot][h], weighed));
+                    if (!ok) break;
+                    tensor_fence_after();
+#pragma unroll
+                    for (int y = h * 4; y < h * 4 + 4; ++y)        // 16 positions
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            tensor_mma_tmem(sums, scores + y / 2 * 32 + i * 16 + y % 2 * 8, v + y * (2048 / 16), S::IDESC_SUMS, t != first || y > 0 || i > 0);
                 }
                 if (!ok) break;
-                const uint64_t v = values + stage * (S::TILE / 16);
-                const uint32_t d = columns + kSharedColSums + slot * 128, p = columns + kSharedColScores + slot * 128;
-#pragma unroll
-                for (int y = 0; y < kSharedTile / 16; ++y)         // 16 positions
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        tensor_mma_tmem(d, p + y / 2 * 32 + h * 16 + y % 2 * 8, v + y * (2048 / 16), S::IDESC_SUMS, k >= 2 || y > 0 || h > 0);
-                if (!both || slot) tensor_commit(&s_free[stage]);
-                if (k + 2 >= total) tensor_commit(&s_summed[slot]);
-                else score(k + 2);
+                release(stage);
+                if (t + step < n) score(t + step);
+                else tensor_commit(&s_summed[slot]);
             }
             item += 2 * n;
-        }
         }
     } else {                                                       // copies
         leave_registers<S::REGS_COPIES>();
@@ -578,9 +585,9 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
     tensor_fence_before();
     __syncthreads();
     if (s_failed) {                                                // no product outlives the CTA, whoever's wait ran out
-        if (w == 8) {
-            tensor_commit(&s_drained);
-            wait_full(&s_drained, 0, kCacheWaitNs);
+        if (w == 8 || w == 9) {
+            tensor_commit(&s_drained[w - 8]);
+            wait_full(&s_drained[w - 8], 0, kCacheWaitNs);
         }
         tensor_fence_before();
         __syncthreads();
