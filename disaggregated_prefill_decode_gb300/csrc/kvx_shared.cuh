@@ -129,6 +129,12 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // Registers of this warpgroup's threads from here on; what the others give up.
 template <int N> __device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void leave_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -162,7 +168,7 @@ __device__ __forceinline__ void copies_arrive(uint64_t *bar) {
 template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_attend_shared(const __grid_constant__ SharedArgs s) {
     extern __shared__ __align__(1024) uint8_t smem[];              // queries of the slots, then the ring
     __shared__ __align__(8) uint64_t s_full[S::STAGES], s_free[S::STAGES], s_queried, s_unqueried;
-    __shared__ __align__(8) uint64_t s_scored[2], s_weighed[2][2], s_summed[2], s_drained[2], s_never;   // per slot; weights in halves of a tile
+    __shared__ __align__(8) uint64_t s_scored[2], s_weighed[2][4], s_summed[2], s_turn[2], s_drained[2], s_never;   // per slot; weights in quarters of a tile
     __shared__ __align__(16) uint32_t s_live[8][4];                // live positions of the last tiles
     __shared__ float s_scale[2][2][S::F8 ? kSharedRows : 1];       // by turns of units, per slot: of 8-bit caches' bf16 queries
     __shared__ uint32_t s_tmem;
@@ -180,8 +186,9 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
         }
         for (int i = 0; i < 2; ++i) {
             init(&s_scored[i], 1);
-            for (int h = 0; h < 2; ++h) init(&s_weighed[i][h], kSharedRows);
+            for (int h = 0; h < 4; ++h) init(&s_weighed[i][h], kSharedRows);
             init(&s_summed[i], 1);
+            init(&s_turn[i], kSharedRows);
             init(&s_drained[i], 1);
         }
         init(&s_queried, kSharedLoaders);
@@ -231,14 +238,20 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
         const int slot = w >> 2, row = (w & 3) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(w & 3) << 21);
         const uint32_t sums = lanes + kSharedColSums + slot * 128, scores = lanes + kSharedColScores + slot * 128;
-        int tiles = 0, scored = 0, summed = 0, turn = 0;           // tiles of the units before; phases; units with tiles
+        int tiles = 0, scored = 0, summed = 0, turn = 0, round = 0;        // tiles of the units before; phases; units with tiles; turns
         bool ok = goes_on(kStallSharedSoftmax);
         for (; ok && work.read(s, c_begin, c_end, units); ++work.index) {
-            const int steps = work.both ? work.n : (work.n + 1 - slot) / 2;
+            const int steps = work.both ? work.n : (work.n + 1 - slot) / 2, rounds = work.both ? work.n : (work.n + 1) / 2;
             float m = -INFINITY, sc = a.scale;                     // m: of the scores, less UP
             float2 l = make_float2(0.0f, 0.0f);
-            for (int i = 0; i < steps; ++i) {
-                if (!(ok = wait(&s_scored[slot], scored++))) break;
+            for (int i = 0; i < rounds; ++i, ++round) {
+                // The slots' softmaxes take turns: alone one takes half as long, and the pipe has the other's products meanwhile.
+                if (i < steps && !(ok = wait(&s_scored[slot], scored++))) break;
+                if ((slot || round) && !(ok = wait(&s_turn[slot], slot ? round : round - 1))) break;
+                if (i >= steps) {
+                    arrive(&s_turn[slot ^ 1]);
+                    continue;
+                }
                 tensor_fence_after();
                 if constexpr (S::F8 && S::IO == KVX_BF16)
                     if (i == 0) sc = s_scale[turn & 1][work.both ? slot : 0][row];
@@ -258,10 +271,10 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
                 }
                 float y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int k = 0; k < 32; ++k)
+                for (int k = 0; k < 32; k += 2)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) y[c] = fmaxf(y[c], __uint_as_float(x[c][k]));
-                const float top = fmaf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), sc, -S::UP);
+                    for (int c = 0; c < 4; ++c) y[c] = max3(y[c], __uint_as_float(x[c][k]), __uint_as_float(x[c][k + 1]));
+                const float top = fmaf(max3(fmaxf(y[0], y[1]), y[2], y[3]), sc, -S::UP);
                 const bool moves = top > m + kSharedSlack;
                 if (__any_sync(~0u, moves)) {                      // the products of this slot's tile before are done: these scores came after
                     const float up = moves ? top : m, old = moves ? fast_exp2(m - up) : 1.0f;
@@ -291,13 +304,17 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
                         l = add2(l, p);
                         two_values<S>(p, z[k], z[16 + k]);
                     }
-                    tmem_store32(z, scores + c * 32);
-                    if (c & 1) {                                   // half a tile's weights: their products begin
+                    if (c) {                                       // the quarter before is stored by now: its products begin
                         tmem_store_wait();
                         tensor_fence_before();
-                        arrive(&s_weighed[slot][c >> 1]);
+                        arrive(&s_weighed[slot][c - 1]);
                     }
+                    tmem_store32(z, scores + c * 32);
                 }
+                arrive(&s_turn[slot ^ 1]);
+                tmem_store_wait();
+                tensor_fence_before();
+                arrive(&s_weighed[slot][3]);
             }
             if (!ok) break;
             // the partial result
@@ -348,11 +365,13 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
                 tensor_commit(&s_free[stage]);
                 if (!both) tensor_commit(&s_free[stage]);
             };
-            auto score = [&](int t) {
-                const int at = t ? item + 2 * t - 1 : item, stage = at % S::STAGES;
-                ok = __all_sync(~0u, wait(&s_full[stage], at / S::STAGES));
-                if (!ok) return;
+            auto key_stage = [&](int t) { return t ? item + 2 * t - 1 : item; };
+            auto copied = [&](int at) {
+                ok = ok && __all_sync(~0u, wait(&s_full[at % S::STAGES], at / S::STAGES));
                 fence_async();
+            };
+            auto score = [&](int t) {
+                const int stage = key_stage(t) % S::STAGES;
                 const uint64_t keys = ring + stage * (S::TILE / 16);
 #pragma unroll
                 for (int y = 0; y < S::D / 16; ++y)                // 32 bytes of the rows
@@ -361,28 +380,32 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
                 release(stage);
                 if (t + step >= n) tensor_commit(&s_unqueried);
             };
-            if (first < n) score(first);
-            else tensor_commit(&s_unqueried);
+            if (first < n) {
+                copied(key_stage(first));
+                if (!ok) break;
+                score(first);
+            } else tensor_commit(&s_unqueried);
             for (int t = first; ok && t < n; t += step, ++weighed) {
-                const int at = t + 1 < n ? item + 2 * t + 2 : item + 2 * n - 1, stage = at % S::STAGES;
-                ok = __all_sync(~0u, wait(&s_full[stage], at / S::STAGES));
-                fence_async();
-                const uint64_t v = values + stage * (S::TILE / 16);
+                const int at = t + 1 < n ? item + 2 * t + 2 : item + 2 * n - 1;
+                const bool more = t + step < n;
+                copied(at);                                        // while the softmax is at work
+                const uint64_t v = values + at % S::STAGES * (S::TILE / 16);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < 4; ++h) {
                     ok = ok && __all_sync(~0u, wait(&s_weighed[slot][h], weighed));
                     if (!ok) break;
                     tensor_fence_after();
 #pragma unroll
-                    for (int y = h * 4; y < h * 4 + 4; ++y)        // 16 positions
+                    for (int y = 2 * h; y < 2 * h + 2; ++y)        // 16 positions
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
                             tensor_mma_tmem(sums, scores + y / 2 * 32 + i * 16 + y % 2 * 8, v + y * (2048 / 16), S::IDESC_SUMS, t != first || y > 0 || i > 0);
+                    if (h == 2 && more) copied(key_stage(t + step));
                 }
                 if (!ok) break;
-                release(stage);
-                if (t + step < n) score(t + step);
-                else tensor_commit(&s_summed[slot]);
+                if (more) score(t + step);
+                release(at % S::STAGES);
+                if (!more) tensor_commit(&s_summed[slot]);
             }
             item += 2 * n;
         }

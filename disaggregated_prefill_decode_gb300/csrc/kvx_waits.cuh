@@ -23,7 +23,7 @@ __device__ __forceinline__ bool wait_full(uint64_t *bar, uint32_t parity, uint64
         asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
                      : "=r"(done) : "r"(shared_addr(bar)), "r"(parity) : "memory");
         if (done) return true;
-        if ((tries & 63) == 63) {                                  // a reading of the timer takes as long as a short wait
+        if ((tries & 1023) == 1023) {                              // a reading of the timer takes as long as a short wait
             uint64_t now;
             asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
             if (!t0) t0 = now;
