@@ -81,16 +81,23 @@ def test_long_prefix_of_two(value):
     check_shared([(40000, [100, 0])], value=value, group=1, hps=1, dim=64)
 
 
-def test_many_groups():
-    """More groups than the plan takes at a time, and units that each CTA has many of."""
-    rng = np.random.default_rng(3)
-    check_shared([(int(rng.integers(100, 300)), rng.integers(0, 20, int(rng.integers(0, 4))).tolist()) for _ in range(1100)],
-                 group=2, hps=1, dim=64)
+@pytest.mark.parametrize("n", [31, 32, 33, 63, 64, 65, 200, 1100])
+def test_many_groups(n):
+    """Up to the groups that each CTA plans itself and beyond, more than the plan takes at a time, and many units for a CTA."""
+    rng = np.random.default_rng(n)
+    check_shared([(int(rng.integers(100, 300)), rng.integers(0, 20, int(rng.integers(0, 4))).tolist()) for _ in range(n)],
+                 group=2, hps=1 if n > 100 else 3, dim=64)
+
+
+@pytest.mark.parametrize("members,group,hps", [(16, 8, 8), (32, 8, 8), (64, 8, 2), (9, 1, 152), (9, 1, 100), (20, 16, 3), (40, 8, 19)])
+def test_one_group_whose_units_are_alike(members, group, hps):
+    """As many CTAs for each unit, or not, where that would leave too many of them out."""
+    check_shared([(2000, [i % 5 for i in range(members)])], group=group, hps=hps, dim=64)
 
 
 def test_the_tensor_kernel_takes_what_is_worth_it():
     case = Shared([(300, [1, 2])], dim=64)
-    assert launches(case)[1] == 4
+    assert launches(case)[1] > 1
     assert launches(case, max_blocks=case.width)[1] == 1                    # little to read twice
     wide = Shared([(300, [1, 2])], dim=192)
     assert kvx.kvx_cache_shared_bytes(wide.cache, 2, 1) == 0
