@@ -342,10 +342,10 @@ struct RotateArgs {
     int64_t q_stride, k_stride, v_stride, out_stride;      // bytes
     int64_t n_tokens, n_rows;         // n_rows: slots of the pool
     int32_t n_q_heads, n_kv_heads, head_dim, planes;
-    int32_t parts;                    // that a token's heads are cut into
     int32_t begin, turned, norm_dim;  // elements [begin, begin + turned) turn, the first norm_dim are normed
     bool pairs;
     float norm_inverse, eps, magnitude, k_inverse, v_inverse;
+    int32_t device;
     uint64_t turns[kRotateMaxPairs];  // frequencies, in 2^-64 turns a position
 };
 cudaError_t launch_rotate(const RotateArgs &a, int32_t value_type, int32_t io_type, int32_t sms, cudaStream_t stream);

@@ -347,11 +347,11 @@ __global__ void __launch_bounds__(kPageThreads, 1) kvx_pages_compact_kernel(cons
 // grid's warps take pieces of 4 KiB of their pages in turn, eight 16-byte loads of a lane in flight.
 // ------------------------------------------------------------------------------------------------
 
-constexpr int kCopyThreads = 512, kPairs = 4096, kPiece = 8 * 32;      // kPiece: 16-byte vectors
+constexpr int kCopyThreads = 256, kPairs = 4096, kPiece = 8 * 32;      // kPiece: 16-byte vectors
 
 __global__ void __launch_bounds__(kCopyThreads) kvx_cache_copy_kernel(const PageCopyArgs a) {
     __shared__ int2 s_pairs[kPairs];
-    __shared__ int32_t s_n;
+    __shared__ int32_t s_n, s_behind;
     wait_for_earlier();
     const int lane = threadIdx.x & 31;
     const int64_t pieces = (a.vectors + kPiece - 1) / kPiece, warps = (int64_t)gridDim.x * (kCopyThreads / 32);
@@ -359,32 +359,37 @@ __global__ void __launch_bounds__(kCopyThreads) kvx_cache_copy_kernel(const Page
     int64_t done = 0;
     for (int64_t p0 = 0; p0 < a.n_pairs; p0 += kPairs) {
         __syncthreads();
-        if (threadIdx.x == 0) s_n = 0;
+        if (threadIdx.x == 0) s_n = s_behind = 0;
         __syncthreads();
-        for (int64_t p = p0 + threadIdx.x; p < min(p0 + kPairs, (int64_t)a.n_pairs); p += kCopyThreads) {
-            const int32_t x = a.src[p], y = a.dst[p];
+        const int all = (int)min((int64_t)kPairs, a.n_pairs - p0);
+        int n = 0, behind = 0;                                         // pairs of this thread, and the place behind its last one
+        for (int p = threadIdx.x; p < all; p += kCopyThreads) {
+            const int32_t x = a.src[p0 + p], y = a.dst[p0 + p];
             const bool in = x >= 0 && x < a.n_blocks && y >= 0 && y < a.n_blocks;
-            if (in) s_pairs[p - p0] = make_int2(x, y);
-            else {
-                s_pairs[p - p0] = make_int2(-1, -1);
-                if ((x != -1 || y != -1) && blockIdx.x == 0) atomicAdd(a.skipped, 1ull);
-            }
+            s_pairs[p] = in ? make_int2(x, y) : make_int2(-1, -1);
+            if (in) ++n, behind = p + 1;
+            else if ((x != -1 || y != -1) && blockIdx.x == 0) atomicAdd(a.skipped, 1ull);
+        }
+        n = __reduce_add_sync(~0u, n);
+        behind = __reduce_max_sync(~0u, behind);
+        if (lane == 0 && n) {
+            atomicAdd(&s_n, n);
+            atomicMax(&s_behind, behind);
         }
         __syncthreads();
-        // to the front, in order, so that every CTA counts the same pieces
-        if (threadIdx.x < 32) {
-            int n = 0;
-            const int all = (int)min((int64_t)kPairs, a.n_pairs - p0);
-            for (int i = 0; i < all; i += 32) {
-                const int2 x = i + lane < all ? s_pairs[i + lane] : make_int2(-1, -1);
-                const uint32_t in = __ballot_sync(~0u, x.x >= 0);
-                if (x.x >= 0) s_pairs[n + __popc(in & ((1u << lane) - 1))] = x;
-                n += __popc(in);
-                __syncwarp();
+        if (s_n != s_behind) {                                         // not all in front: to the front, in order, so that every CTA counts the same pieces
+            if (threadIdx.x < 32) {
+                int m = 0;
+                for (int i = 0; i < s_behind; i += 32) {
+                    const int2 x = i + lane < s_behind ? s_pairs[i + lane] : make_int2(-1, -1);
+                    const uint32_t in = __ballot_sync(~0u, x.x >= 0);
+                    if (x.x >= 0) s_pairs[m + __popc(in & ((1u << lane) - 1))] = x;
+                    m += __popc(in);
+                    __syncwarp();
+                }
             }
-            if (lane == 0) s_n = n;
+            __syncthreads();
         }
-        __syncthreads();
         const int64_t items = (int64_t)s_n * a.n_bufs * pieces;
         for (; turn < done + items; turn += warps) {
             const int64_t i = turn - done, page = i / pieces;
@@ -451,7 +456,7 @@ cudaError_t launch_pages_compact(const CompactArgs &a, cudaStream_t stream) {
 
 cudaError_t launch_cache_copy(const PageCopyArgs &a, int32_t sms, cudaStream_t stream) {
     const int64_t pieces = (a.vectors + kPiece - 1) / kPiece * a.n_bufs * a.n_pairs;
-    const int64_t ctas = std::min<int64_t>((pieces + kCopyThreads / 32 - 1) / (kCopyThreads / 32), 3 * sms);
+    const int64_t ctas = std::min<int64_t>((pieces + kCopyThreads / 32 - 1) / (kCopyThreads / 32), 4 * sms);
     return launch_after(kvx_cache_copy_kernel, dim3((unsigned)ctas), kCopyThreads, 0, stream, a);
 }
 

@@ -3,11 +3,17 @@
 //
 // A pair (a, b) of a head at position p becomes m (a cos - b sin, b cos + a sin) of p times the pair's frequency. The angle is
 // taken in turns, as a 64-bit fraction: position times frequency modulo 2^64 is the fraction of a turn that counts, exactly,
-// however far the position is (in 32 bits it would be off by 2^-24 of the angle: 0.1 radians at 10^6). Its upper 32 bits go to sincospif.
+// however far the position is (in 32 bits it would be off by 2^-24 of the angle: 0.06 radians at 10^6). Its upper 32 bits go to sincospif.
 //
-// A warp takes one token and some of its heads, 32 / LANES of them at a time. A lane has two vectors of 8 elements of a head
-// (or twice two): with halves, the two that turn with one another, so no element changes lanes; sines and cosines are computed once for all
-// heads. Bound by memory: each value is read and written once, in 16 bytes a lane.
+// A warp takes a token (or a part of its heads), then another one, 32 / LANES heads a round. A lane has two vectors of 8 elements of a head
+// (or twice two): with halves, the two that turn with one another, so no element changes lanes; sines, cosines and their products
+// with the weights are computed once for all heads. Bound by memory: each value is read and written once, in 16 bytes a lane, and what counts
+// is bytes on their way: asynchronous copies of four rounds into places of shared memory that the lane itself reads back.
+//
+// Measured on GB300: 8192 tokens of 64 + 8 + 8 heads of 128 (336 MB) 54.9 us, 6.1 TB/s; 64 latents with 16 query heads 5.3, the host's time for a
+// call. Steps: a warp a token, reads of four heads ahead in registers 86.7 us; a persistent warp, sines by the warp 68; no exceptions for
+// lanes where whole heads turn (31 million instructions, 42) 70; the next rounds' reads over tokens, in registers 74; in shared memory
+// 63 with 24 warps an SM, 58 with 16 (8 rounds ahead 71 and 59: the more rows at once, the slower the memory); tokens in two parts 55.
 #include "kvx_attend.cuh"
 
 #include <cuda_fp8.h>
@@ -16,7 +22,7 @@
 
 namespace kvx {
 
-constexpr int kRotateThreads = 256, kRotateWarps = kRotateThreads / 32;
+constexpr int kRotateThreads = 256, kRotateWarps = kRotateThreads / 32, kRotateParts = 7;
 
 // A lane's two vectors of a head, and what becomes of them.
 struct RotateVecs {
@@ -74,157 +80,237 @@ __device__ __forceinline__ uint2 codes(const float (&y)[8], float inverse) {
     return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
-template <int IO, bool F8, int LANES, int NP>
-__global__ void __launch_bounds__(kRotateThreads) kvx_rotate_kernel(const __grid_constant__ RotateArgs r) {
-    constexpr int AT_ONCE = 32 / LANES, AHEAD = NP == 1 ? 4 : 1;      // heads of a warp; rounds whose reads are under way together
-    wait_for_earlier();
-    const int lane = threadIdx.x & 31, in_head = lane % LANES, which = lane / LANES;
-    const int64_t item = (int64_t)blockIdx.x * kRotateWarps + (threadIdx.x >> 5);
-    const int64_t token = item / r.parts;
-    const int part = (int)(item - token * r.parts);
-    if (token >= r.n_tokens) return;
-    const int64_t slot = r.slots[token];
-    if (slot < 0 || slot >= r.n_rows) {
-        if (slot != -1 && part == 0 && lane == 0) atomicAdd(r.pool.skipped, 1ull);
-        return;
-    }
+enum { kQueries, kKeys, kValues };
+
+// A warp's rounds: 32 / LANES heads of one kind a round, read AHEAD rounds before, over tokens too; a lane's two vectors (or twice two)
+// of one. WHOLE: every element of a head turns, and all of them are normed or none; no lane then has an exception.
+template <int IO, bool F8, int LANES, int NP, bool PAIRS, bool WHOLE> struct Rotate {
+    static constexpr int AT_ONCE = 32 / LANES;                        // heads of a round
+    static constexpr int AHEAD = 4;                                // rounds whose reads are under way
+    static constexpr int RING = AHEAD * NP * 1024;                    // bytes of a warp's ring
+    using Vectors = uint4[NP][2];
+    const RotateArgs &r;
+    float2 *const turned;              // of the warp, in shared memory: sine and cosine of each pair at the token's position
     RotateVecs v[NP];
-    float cosine[NP][8], sine[NP][8];
-    const int64_t pos = r.turned ? r.positions[token] : 0;
+    int slot_of[NP];
+    int64_t token, at_slot;
+    // The weights of a kind of heads, and what they make of the sines and cosines: (a, b) becomes (a by[0] - b by[3], b by[2] + a by[1]).
+    float by[NP][4][8];
+
+    __device__ __forceinline__ Rotate(const RotateArgs &args, float2 *shared) : r(args), turned(shared) {
 #pragma unroll
-    for (int n = 0; n < NP; ++n) {
-        const int s = in_head + LANES * n;
-        v[n] = rotate_vecs(r, s);
+        for (int n = 0; n < NP; ++n) {
+            slot_of[n] = threadIdx.x % LANES + LANES * n;
+            v[n] = rotate_vecs(r, slot_of[n]);
+        }
+    }
+
+    // To a token: each lane has some of the pairs.
+    __device__ __forceinline__ void go(int64_t t, int64_t slot, int64_t pos) {
+        token = t;
+        __syncwarp();
+        for (int p = threadIdx.x & 31; p < r.turned / 2; p += 32) {
+            const int32_t turn = (int32_t)((r.turns[p] * (uint64_t)pos) >> 32);
+            float2 y;
+            sincospif((float)turn * 0x1p-31f, &y.x, &y.y);
+            turned[p] = make_float2(y.x * r.magnitude, y.y * r.magnitude);
+        }
+        __syncwarp();
+        const uint32_t row = (uint32_t)slot, blk = row / (uint32_t)r.pool.block_size;
+        at_slot = (int64_t)blk * r.pool.block_pitch + (int64_t)(row - blk * r.pool.block_size) * r.pool.token_pitch;
+    }
+
+    __device__ __forceinline__ static int which() { return (threadIdx.x & 31) / LANES; }
+
+    __device__ __forceinline__ void weigh(const uint8_t *weight) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            // halves: pair 8 s + i of element i of both vectors; pairs: four of each vector
-            const int at = !r.pairs ? 8 * s + i : i < 4 ? (v[n].a - r.begin / 8) * 4 + i : (v[n].b - r.begin / 8) * 4 + i - 4;
-            cosine[n][i] = 1.0f;
-            sine[n][i] = 0.0f;
-            if (i < 4 || !r.pairs ? v[n].turns_a : v[n].turns_b) {
-                const int32_t turn = (int32_t)((r.turns[at] * (uint64_t)pos) >> 32);
-                sincospif((float)turn * 0x1p-31f, &sine[n][i], &cosine[n][i]);
-                sine[n][i] *= r.magnitude;
-                cosine[n][i] *= r.magnitude;
+        for (int n = 0; n < NP; ++n) {
+            float f[2][8];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (weight && (WHOLE || (k ? v[n].norm_b : v[n].norm_a))) widen<IO>(__ldg(reinterpret_cast<const uint4 *>(weight) + (k ? v[n].b : v[n].a)), f[k]);
+                else
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[k][i] = 1.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {                          // pair i: elements i of both vectors, or 2i and 2i + 1 of all sixteen
+                const float wa = !PAIRS ? f[0][i] : f[i / 4][i % 4 * 2], wb = !PAIRS ? f[1][i] : f[i / 4][i % 4 * 2 + 1];
+                const int at = !PAIRS ? 8 * slot_of[n] + i : i < 4 ? (v[n].a - r.begin / 8) * 4 + i : (v[n].b - r.begin / 8) * 4 + i - 4;
+                const float2 y = WHOLE || (i < 4 || !PAIRS ? v[n].turns_a : v[n].turns_b) ? turned[at] : make_float2(0.0f, 1.0f);
+                by[n][0][i] = wa * y.y;
+                by[n][1][i] = wa * y.x;
+                by[n][2][i] = wb * y.y;
+                by[n][3][i] = wb * y.x;
             }
         }
     }
-    const uint32_t row = (uint32_t)slot, blk = row / (uint32_t)r.pool.block_size;
-    const int64_t at_slot = (int64_t)blk * r.pool.block_pitch + (int64_t)(row - blk * r.pool.block_size) * r.pool.token_pitch;
-    const int heads = r.n_q_heads + r.planes * r.n_kv_heads;          // queries, keys, values
-    const int begin = (int)((int64_t)heads * part / r.parts), end = (int)((int64_t)heads * (part + 1) / r.parts);
-    const int row_bytes = r.head_dim * 2;
-    for (int h0 = begin; h0 < end; h0 += AT_ONCE * AHEAD) {
-        uint4 x[AHEAD][NP][2];
+
+    // What this lane has of round `at` of a kind's heads: into its places of a stage of the ring, which it alone reads back.
+    __device__ __forceinline__ void read(uint32_t stage, const uint8_t *src, int at, int heads) const {
+        const int h = at * AT_ONCE + which();
+        const uint8_t *const p = src + (h < heads ? h : 0) * (r.head_dim * 2);
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u) {
-            const int h = h0 + u * AT_ONCE + which;
-            if (h >= end) continue;
-            const int kv = h - r.n_q_heads;
-            const uint8_t *src = kv < 0 ? r.q + token * r.q_stride + (int64_t)h * row_bytes
-                                 : kv < r.n_kv_heads ? r.k + token * r.k_stride + (int64_t)kv * row_bytes
-                                                     : r.v + token * r.v_stride + (int64_t)(kv - r.n_kv_heads) * row_bytes;
-#pragma unroll
-            for (int n = 0; n < NP; ++n) {
-                x[u][n][0] = v[n].a >= 0 ? __ldcs(reinterpret_cast<const uint4 *>(src) + v[n].a) : make_uint4(0, 0, 0, 0);
-                x[u][n][1] = v[n].b >= 0 ? __ldcs(reinterpret_cast<const uint4 *>(src) + v[n].b) : make_uint4(0, 0, 0, 0);
-            }
+        for (int n = 0; n < NP; ++n) {
+            if (WHOLE || v[n].a >= 0) copy_async(stage + n * 1024, p + v[n].a * 16, h < heads);
+            if (WHOLE || v[n].b >= 0) copy_async(stage + n * 1024 + 512, p + v[n].b * 16, h < heads);
         }
+    }
+    __device__ __forceinline__ static void read_back(Vectors &y, uint32_t stage) {
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u) {
-            if (h0 + u * AT_ONCE >= end) break;                       // the whole warp
-            const int h = h0 + u * AT_ONCE + which, kv = h - r.n_q_heads;
-            const bool in = h < end, value = kv >= r.n_kv_heads;
-            const uint8_t *weight = value ? nullptr : kv < 0 ? r.q_weight : r.k_weight;
-            float y[NP][2][8];
+        for (int n = 0; n < NP; ++n)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t z[4];
+                shared_read(z, stage + n * 1024 + k * 512);
+                y[n][k] = make_uint4(z[0], z[1], z[2], z[3]);
+            }
+    }
+
+    template <int KIND> __device__ __forceinline__ void round(const Vectors &x, int at) const {
+        const int heads = KIND == kQueries ? r.n_q_heads : r.n_kv_heads;
+        const uint8_t *const weight = KIND == kQueries ? r.q_weight : KIND == kKeys ? r.k_weight : nullptr;
+        const int h = at * AT_ONCE + which();
+        float y[NP][2][8];
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+            widen<IO>(x[n][0], y[n][0]);
+            widen<IO>(x[n][1], y[n][1]);
+        }
+        float inverse = 1.0f;
+        if (weight) {
             float sum = 0.0f;
 #pragma unroll
-            for (int n = 0; n < NP; ++n) {
-                if (!in) x[u][n][0] = x[u][n][1] = make_uint4(0, 0, 0, 0);
-                widen<IO>(x[u][n][0], y[n][0]);
-                widen<IO>(x[u][n][1], y[n][1]);
+            for (int n = 0; n < NP; ++n)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (v[n].norm_a) sum = fmaf(y[n][0][i], y[n][0][i], sum);
-                    if (v[n].norm_b) sum = fmaf(y[n][1][i], y[n][1][i], sum);
-                }
-            }
-            if (r.q_weight || r.k_weight) {                           // of the whole warp: some lanes may have other heads
+                for (int k = 0; k < 2; ++k) {
+                    float even = 0.0f, odd = 0.0f;
 #pragma unroll
-                for (int d = 1; d < LANES; d <<= 1) sum += __shfl_xor_sync(~0u, sum, d);
-            }
-            if (weight && in) {
-                const float inverse = rsqrtf(sum * r.norm_inverse + r.eps);
-#pragma unroll
-                for (int n = 0; n < NP; ++n) {
-                    float w[8];
-                    if (v[n].norm_a) {
-                        widen<IO>(__ldg(reinterpret_cast<const uint4 *>(weight) + v[n].a), w);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) y[n][0][i] *= inverse * w[i];
+                    for (int i = 0; i < 8; i += 2) {
+                        even = fmaf(y[n][k][i], y[n][k][i], even);
+                        odd = fmaf(y[n][k][i + 1], y[n][k][i + 1], odd);
                     }
-                    if (v[n].norm_b) {
-                        widen<IO>(__ldg(reinterpret_cast<const uint4 *>(weight) + v[n].b), w);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) y[n][1][i] *= inverse * w[i];
-                    }
+                    sum += WHOLE || (k ? v[n].norm_b : v[n].norm_a) ? even + odd : 0.0f;
                 }
-            }
-            if (!in) continue;
-            if (!value)
 #pragma unroll
-                for (int n = 0; n < NP; ++n) {
-                    if (!r.pairs) {
-                        if (v[n].turns_a)
+            for (int d = 1; d < LANES; d <<= 1) sum += __shfl_xor_sync(~0u, sum, d);
+            inverse = rsqrtf(fmaf(sum, r.norm_inverse, r.eps));
+        }
+        if (h >= heads) return;
+        uint8_t *dst = r.q_out + token * r.out_stride + h * (r.head_dim * 2);
+        if constexpr (KIND != kQueries) {
+            const int shard = h / r.pool.heads_per_shard;
+            dst = (KIND == kKeys ? r.pool.k[shard] : r.pool.v[shard]) + (int64_t)(h - shard * r.pool.heads_per_shard) * r.pool.head_pitch + at_slot;
+        }
+        auto put = [&](int vec, const float (&z)[8]) {
+            if (!WHOLE && vec < 0) return;
+            if constexpr (F8 && KIND != kQueries) reinterpret_cast<uint2 *>(dst)[vec] = codes(z, KIND == kKeys ? r.k_inverse : r.v_inverse);
+            else reinterpret_cast<uint4 *>(dst)[vec] = narrow<IO>(z);
+        };
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float a = y[n][0][i], b = y[n][1][i];
-                                y[n][0][i] = a * cosine[n][i] - b * sine[n][i];
-                                y[n][1][i] = b * cosine[n][i] + a * sine[n][i];
-                            }
-                    } else {
+        for (int n = 0; n < NP; ++n) {
+            if constexpr (KIND != kValues) {
+                const float of_a = WHOLE || v[n].norm_a ? inverse : 1.0f, of_b = WHOLE || v[n].norm_b ? inverse : 1.0f;
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            if (k ? v[n].turns_b : v[n].turns_a)
+                for (int k = 0; k < 2; ++k) {                      // halves: both vectors at once, in the first turn
+                    if (!PAIRS && k) break;
+                    const bool turns = WHOLE || (k ? v[n].turns_b : v[n].turns_a);
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const float a = y[n][k][2 * i], b = y[n][k][2 * i + 1];
-                                    y[n][k][2 * i] = a * cosine[n][4 * k + i] - b * sine[n][4 * k + i];
-                                    y[n][k][2 * i + 1] = b * cosine[n][4 * k + i] + a * sine[n][4 * k + i];
-                                }
+                    for (int i = 0; i < (PAIRS ? 4 : 8); ++i) {
+                        float &a = PAIRS ? y[n][k][2 * i] : y[n][0][i], &b = PAIRS ? y[n][k][2 * i + 1] : y[n][1][i];
+                        const int j = PAIRS ? 4 * k + i : i;
+                        const float sa = a * (PAIRS && k ? of_b : of_a), sb = b * (PAIRS && !k ? of_a : of_b);
+                        a = turns ? sa * by[n][0][j] - sb * by[n][3][j] : sa * by[n][0][j];
+                        b = turns ? sb * by[n][2][j] + sa * by[n][1][j] : sb * by[n][2][j];
                     }
                 }
-            if (kv < 0) {
-                uint4 *dst = reinterpret_cast<uint4 *>(r.q_out + token * r.out_stride + (int64_t)h * row_bytes);
-#pragma unroll
-                for (int n = 0; n < NP; ++n) {
-                    if (v[n].a >= 0) dst[v[n].a] = narrow<IO>(y[n][0]);
-                    if (v[n].b >= 0) dst[v[n].b] = narrow<IO>(y[n][1]);
-                }
-            } else {
-                const int head = value ? kv - r.n_kv_heads : kv, shard = head / r.pool.heads_per_shard;
-                uint8_t *dst = (value ? r.pool.v[shard] : r.pool.k[shard]) + (int64_t)(head - shard * r.pool.heads_per_shard) * r.pool.head_pitch + at_slot;
-                const float inverse = value ? r.v_inverse : r.k_inverse;
-#pragma unroll
-                for (int n = 0; n < NP; ++n)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int vec = k ? v[n].b : v[n].a;
-                        if (vec < 0) continue;
-                        if constexpr (F8) reinterpret_cast<uint2 *>(dst)[vec] = codes(y[n][k], inverse);
-                        else reinterpret_cast<uint4 *>(dst)[vec] = narrow<IO>(y[n][k]);
-                    }
             }
+            put(v[n].a, y[n][0]);
+            put(v[n].b, y[n][1]);
         }
     }
+};
+
+template <int IO, bool F8, int LANES, int NP, bool PAIRS, bool WHOLE>
+__global__ void __launch_bounds__(kRotateThreads, NP == 1 ? 2 : 1) kvx_rotate_kernel(const __grid_constant__ RotateArgs r) {
+    using Warp = Rotate<IO, F8, LANES, NP, PAIRS, WHOLE>;
+    __shared__ float2 s_turned[kRotateWarps][kRotateMaxPairs];
+    extern __shared__ __align__(16) uint8_t s_ring[];
+    wait_for_earlier();
+    Warp warp(r, s_turned[threadIdx.x >> 5]);
+    const int part = blockIdx.y, parts = gridDim.y;
+    const int q_rounds = (r.n_q_heads + Warp::AT_ONCE - 1) / Warp::AT_ONCE, kv_rounds = (r.n_kv_heads + Warp::AT_ONCE - 1) / Warp::AT_ONCE;
+    const int keys = q_rounds, values = q_rounds + kv_rounds, all = q_rounds + r.planes * kv_rounds;       // first rounds
+    const int from = (int)((int64_t)all * part / parts), upto = (int)((int64_t)all * (part + 1) / parts);
+    const int64_t step = (int64_t)gridDim.x * kRotateWarps;
+    int64_t token = (int64_t)blockIdx.x * kRotateWarps + (threadIdx.x >> 5), far = token, slot = -1, pos = 0;
+    int at = from, far_at = from;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(s_ring) + (threadIdx.x >> 5) * Warp::RING + (threadIdx.x & 31) * 16;
+    auto read = [&](int stage) {                                      // the next round to be read
+        if (far < r.n_tokens) {
+            const uint32_t to = ring + stage * (NP * 1024);
+            if (far_at < keys) warp.read(to, r.q + far * r.q_stride, far_at, r.n_q_heads);
+            else if (far_at < values) warp.read(to, r.k + far * r.k_stride, far_at - keys, r.n_kv_heads);
+            else warp.read(to, r.v + far * r.v_stride, far_at - values, r.n_kv_heads);
+            if (++far_at == upto) {
+                far_at = from;
+                far += step;
+            }
+        }
+        copies_commit();
+    };
+    auto look_up = [&](int64_t t) {
+        slot = t < r.n_tokens ? r.slots[t] : -1;
+        pos = t < r.n_tokens && r.turned ? r.positions[t] : 0;
+    };
+    look_up(token);
+    for (int u = 0; u < Warp::AHEAD - 1; ++u) read(u);
+    bool live = false;
+    for (int stage = 0; token < r.n_tokens; stage = stage + 1 == Warp::AHEAD ? 0 : stage + 1) {
+        read(stage ? stage - 1 : Warp::AHEAD - 1);
+        if (at == from) {
+            const int64_t here = slot;
+            live = here >= 0 && here < r.n_rows;
+            if (live) warp.go(token, here, pos);
+            else if (here != -1 && part == 0 && (threadIdx.x & 31) == 0) atomicAdd(r.pool.skipped, 1ull);
+            look_up(token + step);
+        }
+        copies_wait<Warp::AHEAD - 1>();
+        if (live) {
+            if ((at == from && at < values) || at == keys) warp.weigh(at < keys ? r.q_weight : r.k_weight);
+            typename Warp::Vectors x;
+            Warp::read_back(x, ring + stage * (NP * 1024));
+            if (at < keys) warp.template round<kQueries>(x, at);
+            else if (at < values) warp.template round<kKeys>(x, at - keys);
+            else warp.template round<kValues>(x, at - values);
+        }
+        if (++at == upto) {
+            at = from;
+            token += step;
+        }
+    }
+    copies_wait<0>();
 }
 
-template <int IO, bool F8, int LANES, int NP> static cudaError_t launch(RotateArgs a, int32_t sms, cudaStream_t stream) {
-    // A token's heads go to as many warps as fill the GPU: each of them computes the token's sines and cosines again.
-    const int64_t rounds = (a.n_q_heads + a.planes * a.n_kv_heads + 32 / LANES - 1) / (32 / LANES);
-    a.parts = (int32_t)std::min<int64_t>(rounds, std::max<int64_t>(1, (32 * sms + a.n_tokens - 1) / a.n_tokens));
-    const int64_t ctas = (a.n_tokens * a.parts + kRotateWarps - 1) / kRotateWarps;
-    return launch_after(kvx_rotate_kernel<IO, F8, LANES, NP>, dim3((unsigned)ctas), kRotateThreads, 0, stream, a);
+template <int IO, bool F8, int LANES, int NP> static cudaError_t launch(const RotateArgs &a, int32_t sms, cudaStream_t stream) {
+    // A token's heads go to as many warps as give each warp of the GPU some seven parts, so that they end together; each of them computes
+    // the token's sines and cosines again.
+    const int at_once = 32 / LANES, q_rounds = (a.n_q_heads + at_once - 1) / at_once, kv_rounds = (a.n_kv_heads + at_once - 1) / at_once;
+    const int64_t room = (NP == 1 ? 2 : 1) * sms, tokens = (a.n_tokens + kRotateWarps - 1) / kRotateWarps;
+    const int64_t rounds = q_rounds + a.planes * kv_rounds;
+    const unsigned parts = (unsigned)std::min<int64_t>(rounds, std::max<int64_t>(1, kRotateParts * room / tokens));
+    const dim3 grid((unsigned)std::min<int64_t>(tokens, std::max<int64_t>(1, room / parts)), std::min(parts, 65535u));
+    const bool full = a.head_dim == 16 * LANES && a.turned == a.head_dim && (a.norm_dim == a.head_dim || (!a.q_weight && !a.k_weight));
+    constexpr int bytes = kRotateWarps * Rotate<IO, F8, LANES, NP, false, false>::RING;
+    auto start = [&](auto *kernel, std::atomic<uint64_t> &asked) {
+        const cudaError_t e = allow_shared(kernel, bytes, a.device, asked);
+        return e != cudaSuccess ? e : launch_after(kernel, grid, kRotateThreads, bytes, stream, a);
+    };
+    static std::atomic<uint64_t> asked[4];
+    if constexpr (NP == 1)
+        if (full)
+            return a.pairs ? start(kvx_rotate_kernel<IO, F8, LANES, NP, true, true>, asked[0]) : start(kvx_rotate_kernel<IO, F8, LANES, NP, false, true>, asked[1]);
+    return a.pairs ? start(kvx_rotate_kernel<IO, F8, LANES, NP, true, false>, asked[2]) : start(kvx_rotate_kernel<IO, F8, LANES, NP, false, false>, asked[3]);
 }
 
 template <int IO, bool F8> static cudaError_t launch_dim(const RotateArgs &a, int32_t sms, cudaStream_t stream) {

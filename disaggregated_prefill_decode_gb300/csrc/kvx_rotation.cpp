@@ -135,9 +135,9 @@ kvx_status kvx_cache_append_rotated(kvx_cache_t c, int32_t layer, kvx_rotation_t
     a.n_kv_heads = g.n_shards * g.heads_per_shard;
     a.head_dim = g.head_dim;
     a.planes = g.n_planes;
-    a.parts = 1;
     a.begin = f.begin;
     a.turned = f.dim;
+    a.device = c->device;
     a.pairs = f.layout == KVX_ROTATE_PAIRS;
     a.norm_dim = f.norm_dim ? f.norm_dim : g.head_dim;
     a.norm_inverse = 1.0f / a.norm_dim;
