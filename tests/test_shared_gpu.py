@@ -89,6 +89,21 @@ def test_many_groups(n):
                  group=2, hps=1 if n > 100 else 3, dim=64)
 
 
+@pytest.mark.parametrize("value,io", FORMS)
+@pytest.mark.parametrize("dim,layout,group,window", [(64, NHD, 2, 0), (128, HND, 3, 0), (80, NHD, 1, 250), (128, NHD, 17, 0)])
+def test_many_requests(value, io, dim, layout, group, window):
+    """Of every type, with groups of their own, a sliding window, and requests alone and empty."""
+    rng = np.random.default_rng(7)
+    groups = [(int(rng.integers(100, 400)), rng.integers(0, 90, 16).tolist()) for _ in range(20)] + [0, 70]
+    check_shared(groups, value=value, io=io, dim=dim, layout=layout, group=group, hps=2, window=window)
+
+
+@pytest.mark.parametrize("group,hps", [(130, 1), (256, 1), (300, 1), (140, 2)])
+def test_more_than_128_query_heads_to_a_kv_head(group, hps):
+    """Rows of one member in several units."""
+    check_shared([(200, [40, 0, 300]), 150, 0], group=group, hps=hps, dim=64)
+
+
 @pytest.mark.parametrize("members,group,hps", [(16, 8, 8), (32, 8, 8), (64, 8, 2), (9, 1, 152), (9, 1, 100), (20, 16, 3), (40, 8, 19)])
 def test_one_group_whose_units_are_alike(members, group, hps):
     """As many CTAs for each unit, or not, where that would leave too many of them out."""
