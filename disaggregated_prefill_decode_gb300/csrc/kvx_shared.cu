@@ -3,7 +3,7 @@
 
 namespace kvx {
 
-constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanThreads = 512, kPlanWarps = kPlanThreads / 32, kPlanLens = 4096;
 // Prefixes of fewer positions are read by each request: a tile of the tensor pipe is 128.
 constexpr int32_t kSharedLeast = 128;
 
@@ -15,12 +15,15 @@ int64_t shared_part_bytes(int32_t head_dim) { return 2 * kSharedRows * ((int64_t
 __global__ void __launch_bounds__(kPlanThreads, 1) kvx_shared_plan(const __grid_constant__ SharedArgs s) {
     __shared__ int32_t s_tokens[kPlanThreads], s_unit[kPlanThreads];
     __shared__ int64_t s_place[kPlanThreads], s_sums[2][kPlanWarps];
+    __shared__ int32_t s_len[kPlanLens];               // the first requests' lengths, read with the groups and not after them
     wait_for_earlier();
     const AttendArgs &a = s.a;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int32_t group = a.n_q_heads / a.n_kv_heads;
     const int64_t cap = (int64_t)a.max_blocks * a.pool.block_size;
+    auto length = [&](int32_t r) { return (int32_t)min((int64_t)max(a.seq_len[r], 0), cap); };
     bool bad = false;
+    for (int32_t r = threadIdx.x; r < min(a.n_reqs, kPlanLens); r += kPlanThreads) s_len[r] = length(r);
     for (int32_t g = threadIdx.x; g < s.n_groups; g += kPlanThreads) {
         const int32_t lo = s.group_off[g], hi = s.group_off[g + 1];
         bad |= lo < 0 || hi < lo || hi > a.n_reqs;
@@ -36,7 +39,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) kvx_shared_plan(const __grid_
             const int32_t lo = s.group_off[g0 + i], hi = s.group_off[g0 + i + 1];
             int32_t least = INT32_MAX, most = 0;
             for (int32_t r = lo + lane; r < hi; r += 32) {
-                const int32_t len = (int32_t)min((int64_t)max(a.seq_len[r], 0), cap);
+                const int32_t len = r < kPlanLens ? s_len[r] : length(r);
                 least = min(least, len);
                 most = max(most, len);
             }
@@ -81,8 +84,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) kvx_shared_plan(const __grid_
             const int32_t rows = (hi - lo) * group, pairs = (rows + 2 * kSharedRows - 1) / (2 * kSharedRows);
             const int64_t tiles = shared_tiles(tokens), pair_places = 2 * tiles + kSharedSwitch;
             const int64_t head_places = (pairs - 1) * pair_places + tiles * shared_weight(rows - (pairs - 1) * 2 * kSharedRows) + kSharedSwitch;
-            for (int64_t j = lane; j < (int64_t)pairs * a.n_kv_heads; j += 32) {
-                const int32_t kvh = (int32_t)(j / pairs), pair = (int32_t)(j - (int64_t)kvh * pairs);
+            for (int32_t j = lane; j < pairs * a.n_kv_heads; j += 32) {
+                const int32_t kvh = j / pairs, pair = j - kvh * pairs;
                 SharedUnit x;
                 x.begin = s_place[i] + kvh * head_places + pair * pair_places;
                 x.first = lo;
