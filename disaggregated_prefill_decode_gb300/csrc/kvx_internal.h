@@ -275,7 +275,7 @@ struct SharedArgs {
     SharedHeader *header;
     SharedUnit *units;
     int32_t *start;                    // per request: its prefix' length, or 0
-    int32_t *unit_of, *row_of;         // per request: its group's first unit, its first row among the group's
+    int4 *place_of;                    // per request: start, its group's first unit, its first row among the group's, units of the group for a KV head
     uint8_t *parts;                    // partial results
 };
 constexpr int32_t kSharedMaxDim = 128;

@@ -29,7 +29,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) kvx_shared_plan(const __grid_
         bad |= lo < 0 || hi < lo || hi > a.n_reqs;
         if (s.prefix_len[g] < 0) atomicAdd(a.pool.skipped, 1ull);
     }
-    for (int32_t r = threadIdx.x; r < a.n_reqs; r += kPlanThreads) s.start[r] = 0;
+    for (int32_t r = threadIdx.x; r < a.n_reqs; r += kPlanThreads) {
+        s.start[r] = 0;
+        s.place_of[r] = make_int4(0, 0, 0, 0);
+    }
     bad = __syncthreads_or(bad);
     if (bad && threadIdx.x == 0) atomicAdd(a.pool.skipped, 1ull);
     int64_t places = 0, units = 0;
@@ -49,10 +52,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) kvx_shared_plan(const __grid_
             if (tokens < kSharedLeast || (a.window && most > a.window)) tokens = 0;
             if (lane == 0) s_tokens[i] = tokens;
             if (tokens)
-                for (int32_t r = lo + lane; r < hi; r += 32) {
-                    s.start[r] = tokens;
-                    s.row_of[r] = (r - lo) * group;
-                }
+                for (int32_t r = lo + lane; r < hi; r += 32) s.start[r] = tokens;
         }
         __syncthreads();
         int64_t my_units = 0, my_places = 0;
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) kvx_shared_plan(const __grid_
                 x.pairs = pairs;
                 if (s_unit[i] + j < s.max_units) s.units[s_unit[i] + j] = x;
             }
-            for (int32_t r = lo + lane; r < hi; r += 32) s.unit_of[r] = s_unit[i];
+            for (int32_t r = lo + lane; r < hi; r += 32) s.place_of[r] = make_int4(tokens, s_unit[i], (r - lo) * group, pairs);
         }
         __syncthreads();
     }
@@ -116,20 +116,20 @@ template <int IO, int D> __global__ void __launch_bounds__(256) kvx_shared_join(
     const int64_t row = (int64_t)blockIdx.x * ROWS + (threadIdx.x & 7) + threadIdx.x / (8 * C4) * 8;
     if (row >= (int64_t)a.n_reqs * a.n_q_heads || c * 4 >= a.head_dim) return;
     const int32_t r = (int32_t)(row / a.n_q_heads), head = (int32_t)(row - (int64_t)r * a.n_q_heads), group = a.n_q_heads / a.n_kv_heads;
+    const int4 place = __ldcg(s.place_of + r);
+    const int64_t places = s.header->places;
     const float2 mine = __ldcg(a.rest_ml + row);
-    float4 o = make_float4(0, 0, 0, 0);
-    float top = -INFINITY, l = 0.0f;
-    if (mine.y != 0.0f) {                                              // also NaN
-        top = mine.x;
-        l = mine.y;
-        o = __ldcg(reinterpret_cast<const float4 *>(a.rest + row * a.head_dim) + c);
+    float4 o = __ldcg(reinterpret_cast<const float4 *>(a.rest + row * a.head_dim) + c);
+    float top = mine.x, l = mine.y;
+    if (l == 0.0f) {                                                   // no position of its own has a weight
+        top = -INFINITY;
+        o = make_float4(0, 0, 0, 0);
     }
-    if (s.start[r]) {
-        const int32_t kvh = head / group, first = s.unit_of[r], at = s.row_of[r] + head - kvh * group;
-        const int32_t unit = first + kvh * s.units[first].pairs + at / (2 * kSharedRows);
+    if (place.x) {
+        const int32_t kvh = head / group, at = place.z + head - kvh * group, unit = place.y + kvh * place.w + at / (2 * kSharedRows);
         const SharedUnit u = s.units[unit];
         const int weight = shared_weight(u.rows);
-        const Split split = shared_split(s.header->places, ctas);
+        const Split split = shared_split(places, ctas);
         const int32_t from = split.cta_of(u.begin), upto = split.cta_of(u.begin + (int64_t)shared_tiles(u.tokens) * weight - 1);
         const int64_t bytes = part_bytes(a.head_dim);
         const int in_slot = at % kSharedRows, slot = weight == 2 ? at % (2 * kSharedRows) / kSharedRows : 0;

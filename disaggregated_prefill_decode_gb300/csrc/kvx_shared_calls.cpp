@@ -28,7 +28,7 @@ static int64_t lay_out(const kvx_cache_t c, int32_t n_reqs, int32_t n_groups, in
         return base + from;
     };
     uint8_t *const header = take(sizeof(SharedHeader)), *const unit = take(units * (int64_t)sizeof(SharedUnit));
-    uint8_t *const start = take(4 * (int64_t)n_reqs), *const unit_of = take(4 * (int64_t)n_reqs), *const row_of = take(4 * (int64_t)n_reqs);
+    uint8_t *const start = take(4 * (int64_t)n_reqs), *const place_of = take(16 * (int64_t)n_reqs);
     uint8_t *const ml = take(rows * 8), *const rest = take(rows * g.head_dim * 4);
     uint8_t *const parts = take((units + sms) * shared_part_bytes(g.head_dim));
     if (s) {
@@ -36,8 +36,7 @@ static int64_t lay_out(const kvx_cache_t c, int32_t n_reqs, int32_t n_groups, in
         s->units = (SharedUnit *)unit;
         s->max_units = (int32_t)std::min<int64_t>(units, std::numeric_limits<int32_t>::max());
         s->start = (int32_t *)start;
-        s->unit_of = (int32_t *)unit_of;
-        s->row_of = (int32_t *)row_of;
+        s->place_of = (int4 *)place_of;
         s->parts = parts;
         s->a.start = s->start;
         s->a.rest = (float *)rest;
