@@ -517,6 +517,11 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
             };
             // Two pieces of 8 elements beside one another.
             auto place = [&](uint32_t base, int r, int p) { return base + p / 8 * S::CHUNK + r * 128 + ((p % 8) ^ (r & 7)) * 16; };
+            auto read = [&](uint32_t at) {
+                uint4 y;
+                asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w) : "r"(at) : "memory");
+                return y;
+            };
             auto write = [&](uint32_t at, uint32_t y0, uint32_t y1, uint32_t y2, uint32_t y3) {
                 asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(y0), "r"(y1), "r"(y2), "r"(y3) : "memory");
             };
@@ -539,32 +544,54 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
                 ++item;
             };
             // Queries as f16: a bf16 row is brought by a power of two to where f16 holds its elements exactly down to 2^-31 of the largest.
+            // All rows are on their way at once, to the places where the lane that copied them turns them into f16.
             auto load_queries = [&]() {
                 if (turn) ok = ok && __all_sync(~0u, wait(&s_unqueried, turn - 1));
                 if (!ok) return;
                 constexpr int LANES = S::PIECES, ROWS = 32 / LANES;
-                const int p = lane % LANES;
-                for (int b = 0; b < (work.both ? 2 : 1); ++b) {
+                const int p = lane % LANES, slots = work.both ? 2 : 1;
+                for (int b = 0; b < slots; ++b) {
                     const uint64_t mine = (uint64_t)query_row(b * kSharedRows + lw * 32 + lane);
-#pragma unroll 4
+#pragma unroll
                     for (int i = 0; i < LANES; ++i) {
                         const int r = i * ROWS + lane / LANES;
-                        const uint8_t *src = (const uint8_t *)__shfl_sync(~0u, mine, r);
-                        uint4 y = src && p * 8 < a.head_dim ? __ldg(reinterpret_cast<const uint4 *>(src) + p) : make_uint4(0, 0, 0, 0);
-                        if constexpr (S::IO == KVX_BF16) {
-                            float2 f[4] = {unpack<KVX_BF16>(y.x), unpack<KVX_BF16>(y.y), unpack<KVX_BF16>(y.z), unpack<KVX_BF16>(y.w)};
-                            float top = 0.0f;
+                        const uint64_t src = __shfl_sync(~0u, mine, r);
+                        const bool in = src != 0 && p * 8 < a.head_dim;
+                        copy_async(place(smem0 + b * S::TILE, lw * 32 + r, p), in ? (const uint8_t *)src + p * 16 : a.q, in);
+                    }
+                }
+                copies_commit();
+                copies_wait<0>();
+                if constexpr (S::IO == KVX_BF16) {
+                    constexpr int BATCH = 4;                           // whose chains of maxima overlap
+                    for (int b = 0; b < slots; ++b) {
+                        for (int i = 0; i < LANES; i += BATCH) {
+                            uint4 y[BATCH];
+                            float top[BATCH];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fabsf(f[k].x), fabsf(f[k].y)));
+                            for (int k = 0; k < BATCH; ++k) {
+                                y[k] = read(place(smem0 + b * S::TILE, lw * 32 + (i + k) * ROWS + lane / LANES, p));
+                                const float2 f[4] = {unpack<KVX_BF16>(y[k].x), unpack<KVX_BF16>(y[k].y), unpack<KVX_BF16>(y[k].z), unpack<KVX_BF16>(y[k].w)};
+                                top[k] = 0.0f;
 #pragma unroll
-                            for (int d = 1; d < LANES; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-                            const int e = top > 0.0f && top < INFINITY ? max(-126, min(100, 14 - ilogbf(top))) : 0;
-                            const float up = __int_as_float((127 + e) << 23);
-                            y = make_uint4(pack<KVX_F16>(f[0].x * up, f[0].y * up), pack<KVX_F16>(f[1].x * up, f[1].y * up),
-                                           pack<KVX_F16>(f[2].x * up, f[2].y * up), pack<KVX_F16>(f[3].x * up, f[3].y * up));
-                            if (p == 0) s_scale[turn & 1][b][lw * 32 + r] = a.scale * __int_as_float((127 - e) << 23);
+                                for (int j = 0; j < 4; ++j) top[k] = fmaxf(top[k], fmaxf(fabsf(f[j].x), fabsf(f[j].y)));
+                            }
+#pragma unroll
+                            for (int d = 1; d < LANES; d <<= 1)
+#pragma unroll
+                                for (int k = 0; k < BATCH; ++k) top[k] = fmaxf(top[k], __shfl_xor_sync(~0u, top[k], d));
+#pragma unroll
+                            for (int k = 0; k < BATCH; ++k) {
+                                const int r = lw * 32 + (i + k) * ROWS + lane / LANES;
+                                const float2 f[4] = {unpack<KVX_BF16>(y[k].x), unpack<KVX_BF16>(y[k].y), unpack<KVX_BF16>(y[k].z), unpack<KVX_BF16>(y[k].w)};
+                                const int exponent = (__float_as_int(top[k]) >> 23) - 127;         // of numbers below the smallest normal one -127
+                                const int e = top[k] > 0.0f && top[k] < INFINITY ? max(-126, min(100, 14 - exponent)) : 0;
+                                const float up = __int_as_float((127 + e) << 23);
+                                write(place(smem0 + b * S::TILE, r, p), pack<KVX_F16>(f[0].x * up, f[0].y * up), pack<KVX_F16>(f[1].x * up, f[1].y * up),
+                                      pack<KVX_F16>(f[2].x * up, f[2].y * up), pack<KVX_F16>(f[3].x * up, f[3].y * up));
+                                if (p == 0) s_scale[turn & 1][b][r] = a.scale * __int_as_float((127 - e) << 23);
+                            }
                         }
-                        write(place(smem0 + b * S::TILE, lw * 32 + r, p), y.x, y.y, y.z, y.w);
                     }
                 }
                 arrive(&s_queried);

@@ -7,8 +7,11 @@
 
 using namespace kvx;
 
-// What sharing a prefix can save has to be worth its launches: below this many bytes that requests would read again, each reads its own.
-static constexpr int64_t kWorthBytes = 24 << 20;
+// What sharing a prefix can save has to be worth its launches: below this many bytes that requests would read again, which they mostly
+// find in L2, each reads its own. On GB300, 8 KV heads of 128 with 8 query heads each (us, shared / each its own): bf16, one group of 8 on 4096 positions
+// (113 MiB read again) 30.4 / 26.5, on 8192 (226) 32.9 / 42.7; 4 groups of 4 on 2048 (99) 31 / 27, on 4096 (195) 38 / 44; 16 groups of 4 on 1024
+// (204) 46 / 47. 8 bits: one group of 32 on 2048 (128) 33 / 30, on 4096 (252) 35 / 48; 16 groups of 4 on 1024 (102) 49 / 32, on 2048 (198) 61 / 51.
+static constexpr int64_t kWorthBytes = 160 << 20;
 
 static bool can_share(const kvx_cache_t c, int32_t n_reqs) {
     return c->g.n_planes == 2 && c->g.head_dim <= kSharedMaxDim && (int64_t)n_reqs * c->cfg.n_q_heads <= std::numeric_limits<int32_t>::max();
@@ -81,8 +84,8 @@ kvx_status kvx_cache_attend_shared(kvx_cache_t c, int32_t layer, const void *q, 
         if (!workspace || workspace_bytes < need)
             return fail(KVX_EINVAL, "a workspace of %lld bytes is needed (kvx_cache_shared_bytes)", (long long)need);
     }
-    const bool worth = cap > kWorthBytes / token / (n_reqs > 1 ? n_reqs - 1 : 1);
-    if (!shares || !worth)
+    const int64_t again = n_reqs - std::min(n_groups, n_reqs / 2);     // of each group's members all but one
+    if (!shares || cap <= kWorthBytes / token / again)
         return kvx_cache_attend(c, layer, q, q_stride, block_table, table_stride, max_blocks, seq_len, n_reqs, out, out_stride, lse, stream);
     if ((st = cache_ready(c, stream))) return st;
     cache_fill_attend(c, layer, q, q_stride, block_table, table_stride, max_blocks, seq_len, n_reqs, out, out_stride, lse, &s.a);

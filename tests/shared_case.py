@@ -45,7 +45,8 @@ class Shared(Attend):
         """As run. max_blocks is made so large that the batch is worth sharing; the table's rows end in garbage."""
         n, hq = len(self.lens), self.heads * self.group
         off, prefix = self.off if off is None else off, self.prefix if prefix is None else prefix
-        wide = max_blocks or max(self.width, 2 * (32 << 20) // (2 * self.geom.n_shards * self.geom.row_bytes * self.bs))
+        again = max(1, n - min(len(prefix), n // 2))
+        wide = max_blocks or max(self.width, (161 << 20) // (2 * self.geom.n_shards * self.geom.row_bytes * self.bs * again) + 2)
         table = np.full((n, wide), 2 ** 30, np.int32)
         table[:, :min(wide, self.table.shape[1])] = self.table[:, :wide]
         q = torch.zeros((n, hq * self.dim + pad), dtype=self.iodtype)
