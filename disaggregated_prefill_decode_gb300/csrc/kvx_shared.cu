@@ -1,4 +1,9 @@
 // kvx_cache_attend_shared: the plan of a batch's shared prefixes, the launches, and the join of what they leave.
+//
+// Four launches: the plan (one CTA, 5 us), the prefixes, the requests' own positions (12 us for 16 x 400 positions, 21 for 64 x 500), the join
+// (6 us for 16 requests of 64 heads, 8 for 64). 16 samples of a prompt of 8192 38 us in all, 64 requests on 32768 105, 96 8-bit requests in 12
+// groups 52.5. Of launches that start before the one ahead has ended the wait is all that is left; letting them start earlier still
+// (launch_dependents) took SM time from it: 40 to 47 us. A plan in each CTA of the prefixes' kernel took as long: its reads are as cold there.
 #include "kvx_shared.cuh"
 
 namespace kvx {

@@ -9,16 +9,25 @@
 // which each CTA takes an equal stretch, so the load is level whatever the groups; each CTA leaves for a unit one partial result
 // (O, m, l) in the workspace.
 //
-// A CTA has two slots, each with 128 rows of scores and sums in TMEM (S: 128 columns, O: 128) and four softmax warps, a thread a row. With more than
-// 128 rows the slots are the two halves of the rows and share each tile of keys and values; with fewer they are the same rows and
-// take every other tile. So while one slot's scores go through the softmax the tensor pipe has the other's products. The
+// A CTA has two slots, each with 128 rows of scores and sums in TMEM (S: 128 columns, O: 128), four softmax warps, a thread a row, and a
+// warp of its own that issues its products. With more than 128 rows the slots are the two halves of the rows and share each tile of keys and
+// values; with fewer they are the same rows and take every other tile. The slots' softmaxes take turns, so that while one slot's scores
+// go through the softmax the tensor pipe has the other's products; weights are handed over a quarter of a tile at a time. The
 // weights go back into the columns of their scores as operand A, as two 16-bit values each, whose sum leaves 2^-16 of a weight (bf16)
 // or 2^-20 (f16, or 2^-35 of the row's largest). An infinite value must meet neither a zero nor a negative value, which would make it NaN: the first is cut
 // off, not rounded, and the second is never zero.
 //
 // Keys and values come row by row with asynchronous copies of 16 bytes, so pages of any size and layout will do, into rings
-// whose rows of 64 elements are swizzled over 128 bytes: K-major for the scores, MN-major for the sums. 8-bit codes pass through
-// registers and become f16, which holds them exactly.
+// whose rows of 64 elements are swizzled over 128 bytes: K-major for the scores, MN-major for the sums. Their arrival is the copies' own;
+// the proxy fence stands where they are used (where they are made it had each copying thread wait for its copies). 8-bit codes pass through
+// registers and become f16, which holds them exactly; the copies' four warps are bound by that conversion.
+//
+// Bound by the tensor pipe where many rows share (with the weights' second value three products, not two): 64 requests on a document of 32768
+// positions, 64 + 8 heads of 128, 68 us, 1.0 PFLOP/s of scores and sums, 1.5 with the second value, 0.79 of the measured rate; else by what a CTA's one
+// or two units cost apart from their tiles (first keys 3 us, flush 2). Steps, of the same case (us): first form 129; a whole row of scores in
+// registers (setmaxnreg) 113; arrivals without the copying threads, operands made uniform by __reduce_max_sync 85; a product warp for each slot, weights
+// in halves 80; turns and quarters 68. Not kept: turns handed over earlier 68.5, stores of 16 columns 70, whole numbers of CTAs for each unit 73,
+// the requests' own positions as units 127.
 #pragma once
 
 #include "kvx_attend.cuh"
@@ -27,7 +36,7 @@
 namespace kvx {
 
 constexpr int kSharedTile = 128, kSharedRows = 128;                // positions of a tile, rows of a slot
-constexpr int kSharedThreads = 16 * 32;                            // warps 0-7: softmax, four a slot; 8: products; 12-15: copies
+constexpr int kSharedThreads = 16 * 32;                            // warps 0-7: softmax, four a slot; 8, 9: products; 12-15: copies
 constexpr int kSharedLoaders = 128;
 constexpr int kSharedSwitch = 3;                                   // what a change of units counts, in places of the line
 constexpr int kSharedMin = 4;                                      // places of a CTA at least

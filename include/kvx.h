@@ -692,13 +692,14 @@ typedef struct kvx_page_result {
     int64_t n_blocks;      /* kvx_pages_free: ids written to free_blocks; kvx_pages_fork: pages to copy, and entries of free_blocks taken or,
                               when there are too few, needed; kvx_pages_compact: blocks to move */
     int64_t status;        /* KVX_OK; KVX_ERANGE: a length that is negative or beyond max_blocks * block_size (cut there), a block id
-                              outside the pool or a row of `parent` outside the table (left out); KVX_ENOMEM: n_blocks > n_free or > max_moves */
+                              outside the pool or negative, or a row of `parent` outside the table (left out); KVX_ENOMEM: n_blocks > n_free or > max_moves */
 } kvx_page_result;
 
 /*
  * kvx_pages_free -- which blocks of a pool no request holds.
  * refs[b] (n_blocks entries): how many table entries hold block b. free_blocks (room for n_blocks ids): the blocks that none
- * holds, ascending, what kvx_slot_map and kvx_pages_fork take; entries behind the last are left as they were.
+ * holds, ascending, what kvx_slot_map and kvx_pages_fork take; entries behind the last are left as they were, so the n_free of
+ * those calls is at most the n_blocks of this one's result.
  */
 kvx_status kvx_pages_free(const int32_t *block_table, int64_t table_stride, int32_t max_blocks, const int32_t *seq_len, int32_t n_reqs,
                           int32_t block_size, int64_t n_blocks, int32_t *refs, int32_t *free_blocks, kvx_page_result *result,

@@ -50,6 +50,7 @@ def fork(table, lens, bs, parent, free_ids):
             else:
                 if taken < len(free_ids):
                     to = int(free_ids[taken])
+                    bad |= to < 0
                     if to >= 0:
                         src[taken], dst[taken] = rows[p][-1], to
                     new[i, len(rows[p]) - 1] = max(to, -1)

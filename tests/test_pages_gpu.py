@@ -140,6 +140,9 @@ def test_fork_out_of_range():
     hole = table.copy()
     hole[7, (lens[7] - 1) // 16] = -1
     assert check_fork(hole, lens, 16, parent, np.arange(60, dtype=np.int32)) == kvx.KVX_ERANGE
+    free = np.arange(60, dtype=np.int32)
+    free[3] = -1
+    assert check_fork(table, lens, 16, parent, free) == kvx.KVX_ERANGE
     assert check_fork(table[:0], lens[:0], 16, np.full(5, -1, np.int32), np.arange(9, dtype=np.int32)) == kvx.KVX_OK
 
 
