@@ -138,9 +138,7 @@ template <int IO, int D> __global__ void __launch_bounds__(256) kvx_shared_join(
         const int32_t from = split.cta_of(u.begin), upto = split.cta_of(u.begin + (int64_t)shared_tiles(u.tokens) * weight - 1);
         const int64_t bytes = part_bytes(a.head_dim);
         const int in_slot = at % kSharedRows, slot = weight == 2 ? at % (2 * kSharedRows) / kSharedRows : 0;
-        // with one slot a tile, both slots' sums are parts of the same rows
-        const int64_t step = weight == 2 ? bytes : bytes / 2;
-        const int32_t n = (upto - from + 1) * (weight == 2 ? 1 : 2);
+        const int32_t n = upto - from + 1;
         const uint8_t *const parts = s.parts + (unit + from) * bytes + slot * (bytes / 2);
         for (int32_t x0 = 0; x0 < n; x0 += AT_ONCE) {
             float2 ml[AT_ONCE];
@@ -150,7 +148,7 @@ template <int IO, int D> __global__ void __launch_bounds__(256) kvx_shared_join(
             for (int x = 0; x < AT_ONCE; ++x) {
                 ml[x] = make_float2(-INFINITY, 0.0f);
                 if (x0 + x < n) {
-                    const uint8_t *const p = parts + (x0 + x) * step;
+                    const uint8_t *const p = parts + (x0 + x) * bytes;
                     ml[x] = __ldcg(reinterpret_cast<const float2 *>(p) + in_slot);
                     y[x] = __ldcg(reinterpret_cast<const float4 *>(p + kSharedRows * 8) + c * kSharedRows + in_slot);
                 }

@@ -93,6 +93,7 @@ template <int VT_, int IO_, int D_> struct SharedShape {
     static_assert(2 * REGS_SOFTMAX + REGS_PRODUCTS + REGS_COPIES <= 512, "a warpgroup would wait for registers that nobody has");
     static constexpr int PIECES = D / 8;                           // of 16 bytes in a row of shared memory
     static_assert(STAGES >= 4, "keys and values of two tiles");
+    static_assert(BYTES <= (224 << 10), "3 KiB are the barriers' and the slots' maxima and sums");
 };
 
 // The product with operand A in TMEM.
@@ -178,8 +179,10 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
     extern __shared__ __align__(1024) uint8_t smem[];              // queries of the slots, then the ring
     __shared__ __align__(8) uint64_t s_full[S::STAGES], s_free[S::STAGES], s_queried, s_unqueried;
     __shared__ __align__(8) uint64_t s_scored[2], s_weighed[2][4], s_summed[2], s_turn[2], s_drained[2], s_never;   // per slot; weights in quarters of a tile
+    __shared__ __align__(8) uint64_t s_met, s_left;                // both slots' sums of a unit are there; the second slot has read them
+    __shared__ float2 s_ml[2][kSharedRows];                        // of slots that share their rows
     __shared__ __align__(16) uint32_t s_live[8][4];                // live positions of the last tiles
-    __shared__ float s_scale[2][2][S::F8 ? kSharedRows : 1];       // by turns of units, per slot: of 8-bit caches' bf16 queries
+    __shared__ int8_t s_up[2][2][S::F8 ? kSharedRows : 1];         // by turns of units, per slot: powers of two of 8-bit caches' bf16 queries
     __shared__ uint32_t s_tmem;
     __shared__ int32_t s_first;
     __shared__ volatile int32_t s_failed;
@@ -203,6 +206,8 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
         init(&s_queried, kSharedLoaders);
         init(&s_unqueried, 2);
         init(&s_never, 1);
+        init(&s_met, 2 * kSharedRows);
+        init(&s_left, kSharedRows);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     wait_for_earlier();
@@ -247,7 +252,7 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
         const int slot = w >> 2, row = (w & 3) * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(w & 3) << 21);
         const uint32_t sums = lanes + kSharedColSums + slot * 128, scores = lanes + kSharedColScores + slot * 128;
-        int tiles = 0, scored = 0, summed = 0, turn = 0, round = 0;        // tiles of the units before; phases; units with tiles; turns
+        int tiles = 0, scored = 0, summed = 0, turn = 0, round = 0, met = 0;   // tiles of the units before; phases; units with tiles; turns
         bool ok = goes_on(kStallSharedSoftmax);
         for (; ok && work.read(s, c_begin, c_end, units); ++work.index) {
             const int steps = work.both ? work.n : (work.n + 1 - slot) / 2, rounds = work.both ? work.n : (work.n + 1) / 2;
@@ -263,7 +268,7 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
                 }
                 tensor_fence_after();
                 if constexpr (S::F8 && S::IO == KVX_BF16)
-                    if (i == 0) sc = s_scale[turn & 1][work.both ? slot : 0][row];
+                    if (i == 0) sc = a.scale * __int_as_float((127 - s_up[turn & 1][work.both ? slot : 0][row]) << 23);
                 const uint4 four = *reinterpret_cast<const uint4 *>(s_live[(tiles + (work.both ? i : 2 * i + slot)) & 7]);
                 const uint32_t live[4] = {four.x, four.y, four.z, four.w};
                 const bool all = (four.x & four.y & four.z & four.w) == ~0u;
@@ -328,12 +333,45 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
             if (!ok) break;
             // the partial result
             const bool real = (work.both ? slot * kSharedRows : 0) + row < work.u.rows;
-            uint8_t *const part = s.parts + (int64_t)(work.index + blockIdx.x) * part_bytes(a.head_dim) + slot * (part_bytes(a.head_dim) / 2);
+            uint8_t *const part = s.parts + (int64_t)(work.index + blockIdx.x) * part_bytes(a.head_dim) + (work.both ? slot * (part_bytes(a.head_dim) / 2) : 0);
             float4 *const to = reinterpret_cast<float4 *>(part + kSharedRows * 8) + row;
-            if (real) __stcg(reinterpret_cast<float2 *>(part) + row, make_float2(m, l.x + l.y));
-            if (steps) {
-                if (!(ok = wait(&s_summed[slot], summed++))) break;
+            const float2 mine = make_float2(m, l.x + l.y);
+            if (steps && !(ok = wait(&s_summed[slot], summed++))) break;
+            tensor_fence_after();
+            if (!work.both) {                                      // of the same rows: joined here, half of the columns by each slot
+                s_ml[slot][row] = mine;
+                tensor_fence_before();
+                arrive(&s_met);
+                if (!(ok = wait(&s_met, met))) break;
                 tensor_fence_after();
+                const float2 one = s_ml[0][row], two = s_ml[1][row];
+                const float up = fmaxf(one.y != 0.0f ? one.x : -INFINITY, two.y != 0.0f ? two.x : -INFINITY), ref = up == -INFINITY ? 0.0f : up;
+                const float by_one = one.y != 0.0f ? fast_exp2(one.x - ref) : 0.0f, by_two = two.y != 0.0f ? fast_exp2(two.x - ref) : 0.0f;
+                if (slot == 0 && real) __stcg(reinterpret_cast<float2 *>(part) + row, make_float2(up, fmaf(one.y, by_one, two.y * by_two)));
+#pragma unroll 1
+                for (int c = slot * (S::D / 2); c < (slot + 1) * (S::D / 2); c += 32) {
+                    uint32_t o[2][32];
+                    tmem_load32(o[0], lanes + kSharedColSums + c);
+                    tmem_load32(o[1], lanes + kSharedColSums + 128 + c);
+                    tmem_load_wait();
+                    float z[32];
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {                 // sums without weights may be anything
+                        const float p = one.y != 0.0f ? __uint_as_float(o[0][k]) * by_one : 0.0f;
+                        z[k] = two.y != 0.0f ? fmaf(__uint_as_float(o[1][k]), by_two, p) : p;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (real && c + 4 * k < a.head_dim)
+                            __stcg(to + (c / 4 + k) * kSharedRows, make_float4(z[4 * k], z[4 * k + 1], z[4 * k + 2], z[4 * k + 3]));
+                }
+                tensor_fence_before();
+                // The second slot's next products come after the first one's next softmax, which comes after this.
+                if (slot) arrive(&s_left);
+                else if (!(ok = wait(&s_left, met))) break;
+                ++met;
+            } else if (steps) {
+                if (real) __stcg(reinterpret_cast<float2 *>(part) + row, mine);
 #pragma unroll 1
                 for (int c = 0; c < S::D; c += 32) {
                     uint32_t o[32];
@@ -346,7 +384,7 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
                                                                                __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3])));
                 }
                 tensor_fence_before();
-            }
+            } else if (real) __stcg(reinterpret_cast<float2 *>(part) + row, mine);
             tiles += work.n;
             turn += work.n > 0;
         }
@@ -598,7 +636,7 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
                                 const float up = __int_as_float((127 + e) << 23);
                                 write(place(smem0 + b * S::TILE, r, p), pack<KVX_F16>(f[0].x * up, f[0].y * up), pack<KVX_F16>(f[1].x * up, f[1].y * up),
                                       pack<KVX_F16>(f[2].x * up, f[2].y * up), pack<KVX_F16>(f[3].x * up, f[3].y * up));
-                                if (p == 0) s_scale[turn & 1][b][r] = a.scale * __int_as_float((127 - e) << 23);
+                                if (p == 0) s_up[turn & 1][b][r] = (int8_t)e;
                             }
                         }
                     }
