@@ -3,11 +3,11 @@
 A prompt is appended once, its keys normed and rotated on their way into the cache. kvx_pages_fork makes a row for each
 answer from it: full pages are shared, the partial last one is copied. A step, captured in a CUDA graph, finds the free pages
 (kvx_pages_free), gives the new tokens their slots, and per layer rotates and appends them (kvx_cache_append_rotated) and
-attends with the prompt read once for all answers (kvx_cache_attend_shared). Half way some answers end and others are forked
-again, and the pages in use are moved to the pool's front (kvx_pages_compact, kvx_cache_copy). Every output is checked
-against attention over a cache kept on the side, every rotation against its formula.
+attends (kvx_cache_attend_shared, which reads a prompt once for all answers where there is enough to share). Half way some
+answers end and others are forked again, and the pages in use are moved to the pool's front (kvx_pages_compact,
+kvx_cache_copy). Every output is checked against attention over a cache kept on the side, every rotation against its formula.
 
-    python examples/fork_shared_prompt.py [steps]
+    python examples/fork_shared_prompt.py [steps] [answers]
 """
 import os
 import sys
@@ -169,5 +169,6 @@ def main(steps: int = 40, prompt: int = 500, answers: int = 12, seed: int = 0) -
 
 
 if __name__ == "__main__":
-    n_steps = int(sys.argv[1]) if len(sys.argv) > 1 else 40
-    print("%d steps of 12 answers, largest error of an output %.2g, of a rotated value %.2g of its size" % (n_steps, *main(n_steps)))
+    n_steps, n_answers = (int(sys.argv[i]) if len(sys.argv) > i else x for i, x in ((1, 40), (2, 12)))
+    print("%d steps of %d answers, largest error of an output %.2g, of a rotated value %.2g of its size" %
+          (n_steps, n_answers, *main(n_steps, answers=n_answers)))
