@@ -3,7 +3,8 @@
 //
 // A pair (a, b) of a head at position p becomes m (a cos - b sin, b cos + a sin) of p times the pair's frequency. The angle is
 // taken in turns, as a 64-bit fraction: position times frequency modulo 2^64 is the fraction of a turn that counts, exactly,
-// however far the position is (in 32 bits it would be off by 2^-24 of the angle: 0.06 radians at 10^6). Its upper 32 bits go to sincospif.
+// however far the position is (in 32 bits it would be off by 2^-24 of the angle: 0.06 radians at 10^6). Its upper 32 bits go to
+// sincospif, as a float: 2^-26 of a turn. The frequency's own 53 bits are off by 2^-55 of a turn a position.
 //
 // A warp takes a token (or a part of its heads), then another one, 32 / LANES heads a round. A lane has two vectors of 8 elements of a head
 // (or twice two): with halves, the two that turn with one another, so no element changes lanes; sines, cosines and their products

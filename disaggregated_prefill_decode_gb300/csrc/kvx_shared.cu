@@ -1,8 +1,8 @@
 // kvx_cache_attend_shared: the plan of a batch's shared prefixes, the launches, and the join of what they leave.
 //
 // Four launches: the plan (one CTA, 5 us), the prefixes, the requests' own positions (12 us for 16 x 400 positions, 21 for 64 x 500), the join
-// (6 us for 16 requests of 64 heads, 8 for 64). 16 samples of a prompt of 8192 38 us in all, 64 requests on 32768 105, 96 8-bit requests in 12
-// groups 52.5. Of launches that start before the one ahead has ended the wait is all that is left; letting them start earlier still
+// (4 us for 16 requests of 64 heads, 7 for 64). 16 samples of a prompt of 8192 35.6 us in all, 64 requests on 32768 104, 96 8-bit requests in 12
+// groups 52. Of launches that start before the one ahead has ended the wait is all that is left; letting them start earlier still
 // (launch_dependents) took SM time from it: 40 to 47 us. A plan in each CTA of the prefixes' kernel took as long: its reads are as cold there.
 #include "kvx_shared.cuh"
 
@@ -112,9 +112,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) kvx_shared_plan(const __grid_
 }
 
 // The join: a thread has four elements of a row (request, query head), the sums of its own positions and those of the CTAs that its
-// unit went to, eight at a time. Reads and writes are whole sectors: 8 rows x 4 float4 a warp.
+// unit went to, ten at a time (the whole call for 16 samples and for 64 requests on a document: 8 36.7 and 105.3 us, 10 35.6 and 103.9, 12 36.4 and
+// 104.8, 20 36.0 and 111). Reads and writes are whole sectors: 8 rows x 4 float4 a warp.
 template <int IO, int D> __global__ void __launch_bounds__(256) kvx_shared_join(const __grid_constant__ SharedArgs s, int ctas) {
-    constexpr int C4 = D / 4, ROWS = 256 / C4, AT_ONCE = 8;
+    constexpr int C4 = D / 4, ROWS = 256 / C4, AT_ONCE = 10;
     wait_for_earlier();
     const AttendArgs &a = s.a;
     const int c = threadIdx.x / 8 % C4;
