@@ -100,14 +100,21 @@ struct Split {
 
 // A request's live positions [first, len) and its tiles of TOK positions, aligned to TOK; at least one, so that an
 // empty request is answered too.
-// REST: those from start[r] on, where kvx_cache_attend_shared has taken the ones before.
+// REST: those behind the prefix that kvx_cache_attend_shared takes apart, from start[r] on; in batches of up to kRestFew requests the kernel
+// has put that into shared memory itself (`start` is NULL).
+constexpr int32_t kRestFew = 384;
+__device__ __forceinline__ int32_t *rest_start() {
+    __shared__ int32_t start[kRestFew];
+    return start;
+}
+
 template <int TOK, bool REST = false> struct Span {
     int32_t len, first, tiles;
     __device__ __forceinline__ Span(const AttendArgs &a, int32_t r) {
         const int64_t cap = (int64_t)a.max_blocks * a.pool.block_size;
         len = (int32_t)min((int64_t)max(a.seq_len[r], 0), cap);
         first = a.window ? max(0, len - a.window) : 0;
-        if constexpr (REST) first = max(first, min(a.start[r], len));
+        if constexpr (REST) first = max(first, min(a.start ? a.start[r] : rest_start()[r], len));
         tiles = max(1, (int32_t)(((uint32_t)len + TOK - 1) / TOK) - first / TOK);
     }
 };
@@ -208,7 +215,7 @@ template <int TOK, int WARPS, int MIN, int EXTRA, int PIECES, bool REST = false>
             cta_exclusive<WARPS>(mine, &total);
         }
         split.tiles = total * segs;
-        split.ctas = (int32_t)min((int64_t)gridDim.x, divide(split.tiles + MIN - 1, MIN));
+        split.ctas = (int32_t)min((int64_t)gridDim.x - (REST && !a.start), divide(split.tiles + MIN - 1, MIN));
         if constexpr (PIECES > 0) {
             const int64_t segments = (int64_t)a.n_reqs * segs;
             for (int64_t k = 1; PIECES * k * segments < split.ctas; ++k)

@@ -25,6 +25,7 @@
 #pragma once
 
 #include "kvx_attend.cuh"
+#include "kvx_shared_plan.cuh"
 
 namespace kvx {
 
@@ -38,6 +39,8 @@ template <int VT_, int IO_, int D_, int NT_, bool FULL_> struct Shape {
     static constexpr int VT = VT_, IO = IO_, D = D_, NT = NT_;   // D: head_dim rounded up; NT: query sets of 8
     static constexpr bool FULL = FULL_;                           // head_dim is D
     static constexpr bool REST = false;                           // see RestShape
+    using Args = AttendArgs;
+    __host__ __device__ static const AttendArgs &attend(const Args &x) { return x; }
     static constexpr bool F8 = VT == KVX_E4M3;
     static constexpr int MT = F8 ? KVX_F16 : VT;                  // type of the products
     // f16 weights are taken times 2^15, by a reference m that far below the maximum: one of 2^-39 of the largest still has a
@@ -85,6 +88,9 @@ template <int VT_, int IO_, int D_, int NT_, bool FULL_> struct Shape {
 // that its last kernel joins with those of the prefixes.
 template <class S> struct RestShape : S {
     static constexpr bool REST = true;
+    static_assert(S::WARPS * S::WARP_BYTES + kRestFew * 4 + 512 <= (227 << 10), "beside the rings there is room for kRestFew requests");
+    using Args = SharedArgs;
+    __host__ __device__ static const AttendArgs &attend(const Args &x) { return x.a; }
 };
 
 // A partial result in shared memory or in the scratch: O as [set][query of the lane's two][e / 4][lane] float4 of four
@@ -258,7 +264,8 @@ template <int TOK, class Line> struct Row {
     }
 };
 
-template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_planes(const __grid_constant__ AttendArgs a) {
+template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_planes(const __grid_constant__ typename S::Args args) {
+    const AttendArgs &a = S::attend(args);
     constexpr int TOK = S::TOK, NT = S::NT;
     using Line = Place<TOK, kSwitchTiles, S::REST>;
     extern __shared__ __align__(16) uint8_t smem[];                // [warp] ring and partial result
@@ -269,6 +276,8 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
     const int32_t group = a.n_q_heads / a.n_kv_heads, sets = (group + 8 * NT - 1) / (8 * NT), segs = a.n_kv_heads * sets;
 
     wait_for_earlier();
+    if constexpr (S::REST)
+        if (!a.start && plan_few<S::THREADS>(args, smem)) return;
     const Batch<TOK, S::WARPS, S::WARPS, kSwitchTiles, kJoinAtOnce, S::REST> batch(a, segs);
     const Split &split = batch.split;
     if ((int32_t)blockIdx.x >= split.ctas) return;
@@ -655,12 +664,12 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
 
 // ------------------------------------------------------------------------------------------------
 
-template <class S> static cudaError_t launch(const AttendArgs &a, int32_t sms, cudaStream_t stream) {
+template <class S> static cudaError_t launch(const typename S::Args &args, int32_t sms, cudaStream_t stream) {
     constexpr int bytes = S::WARPS * S::WARP_BYTES;
     static std::atomic<uint64_t> asked;
-    const cudaError_t e = allow_shared(kvx_attend_planes<S>, bytes, a.device, asked);
+    const cudaError_t e = allow_shared(kvx_attend_planes<S>, bytes, S::attend(args).device, asked);
     if (e != cudaSuccess) return e;
-    return launch_after(kvx_attend_planes<S>, dim3(sms), S::THREADS, bytes, stream, a);
+    return launch_after(kvx_attend_planes<S>, dim3(sms), S::THREADS, bytes, stream, args);
 }
 
 template <int VT, int IO, int D, int NT> static cudaError_t launch(const AttendArgs &a, int32_t sms, cudaStream_t stream) {
@@ -676,13 +685,13 @@ template <int VT, int IO> static cudaError_t launch_planes(const AttendArgs &a, 
 }
 
 // The same for the rest of requests, head dims up to 128.
-template <int VT, int IO, int D, int NT> static cudaError_t launch_rest_shape(const AttendArgs &a, int32_t sms, cudaStream_t stream) {
-    return a.head_dim == D ? launch<RestShape<Shape<VT, IO, D, NT, true>>>(a, sms, stream) : launch<RestShape<Shape<VT, IO, D, NT, false>>>(a, sms, stream);
+template <int VT, int IO, int D, int NT> static cudaError_t launch_rest_shape(const SharedArgs &s, int32_t sms, cudaStream_t stream) {
+    return s.a.head_dim == D ? launch<RestShape<Shape<VT, IO, D, NT, true>>>(s, sms, stream) : launch<RestShape<Shape<VT, IO, D, NT, false>>>(s, sms, stream);
 }
-template <int VT, int IO> static cudaError_t launch_rest_planes(const AttendArgs &a, int32_t sms, cudaStream_t stream) {
-    const bool wide = a.n_q_heads / a.n_kv_heads > 8;
-    if (a.head_dim <= 64) return wide ? launch_rest_shape<VT, IO, 64, 2>(a, sms, stream) : launch_rest_shape<VT, IO, 64, 1>(a, sms, stream);
-    return wide ? launch_rest_shape<VT, IO, 128, 2>(a, sms, stream) : launch_rest_shape<VT, IO, 128, 1>(a, sms, stream);
+template <int VT, int IO> static cudaError_t launch_rest_planes(const SharedArgs &s, int32_t sms, cudaStream_t stream) {
+    const bool wide = s.a.n_q_heads / s.a.n_kv_heads > 8;
+    if (s.a.head_dim <= 64) return wide ? launch_rest_shape<VT, IO, 64, 2>(s, sms, stream) : launch_rest_shape<VT, IO, 64, 1>(s, sms, stream);
+    return wide ? launch_rest_shape<VT, IO, 128, 2>(s, sms, stream) : launch_rest_shape<VT, IO, 128, 1>(s, sms, stream);
 }
 
 }  // namespace kvx

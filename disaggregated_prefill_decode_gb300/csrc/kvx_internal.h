@@ -234,7 +234,7 @@ struct AttendArgs {
     int32_t device;
     int32_t stall;                    // latents, testing hook (kvx_cache_inject_stall): CTA 0's part that never goes on, 0: none
     uint64_t wait_ns;                 // latents, shared prefixes: limit of a wait for a copy or a product
-    const int32_t *start;             // kvx_cache_attend_shared: each request's first position behind its group's prefix,
+    const int32_t *start;             // kvx_cache_attend_shared: each request's first position behind its group's prefix (NULL: the kernel's to find),
     float *rest;                      // and for the ones from there the sums, [request][query head][head_dim],
     float2 *rest_ml;                  // with their maximum and the weights' sum
 };
@@ -286,10 +286,10 @@ cudaError_t launch_shared_bf16(const SharedArgs &s, int32_t sms, cudaStream_t st
 cudaError_t launch_shared_f16(const SharedArgs &s, int32_t sms, cudaStream_t stream);
 cudaError_t launch_shared_e4m3_bf16(const SharedArgs &s, int32_t sms, cudaStream_t stream);
 cudaError_t launch_shared_e4m3_f16(const SharedArgs &s, int32_t sms, cudaStream_t stream);
-cudaError_t launch_rest_bf16(const AttendArgs &a, int32_t sms, cudaStream_t stream);
-cudaError_t launch_rest_f16(const AttendArgs &a, int32_t sms, cudaStream_t stream);
-cudaError_t launch_rest_e4m3_bf16(const AttendArgs &a, int32_t sms, cudaStream_t stream);
-cudaError_t launch_rest_e4m3_f16(const AttendArgs &a, int32_t sms, cudaStream_t stream);
+cudaError_t launch_rest_bf16(const SharedArgs &s, int32_t sms, cudaStream_t stream);
+cudaError_t launch_rest_f16(const SharedArgs &s, int32_t sms, cudaStream_t stream);
+cudaError_t launch_rest_e4m3_bf16(const SharedArgs &s, int32_t sms, cudaStream_t stream);
+cudaError_t launch_rest_e4m3_f16(const SharedArgs &s, int32_t sms, cudaStream_t stream);
 
 // ---- pages (kvx_page_calls.cpp, kvx_pages.cu) ----
 struct TableArgs {

@@ -3,8 +3,8 @@
 
 namespace kvx {
 
-cudaError_t launch_rest_bf16(const AttendArgs &a, int32_t sms, cudaStream_t stream) {
-    return launch_rest_planes<KVX_BF16, KVX_BF16>(a, sms, stream);
+cudaError_t launch_rest_bf16(const SharedArgs &s, int32_t sms, cudaStream_t stream) {
+    return launch_rest_planes<KVX_BF16, KVX_BF16>(s, sms, stream);
 }
 
 }  // namespace kvx

@@ -9,26 +9,20 @@
 namespace kvx {
 
 constexpr int kPlanThreads = 512, kPlanWarps = kPlanThreads / 32, kPlanLens = 4096;
-// Prefixes of fewer positions are read by each request: a tile of the tensor pipe is 128.
-constexpr int32_t kSharedLeast = 128;
 
 int64_t shared_part_bytes(int32_t head_dim) { return 2 * kSharedRows * ((int64_t)head_dim * 4 + 8); }
 
-// One CTA. A group of two members or more shares the first P positions, P what it names but at most its shortest member's
-// length. With a window every member's has to reach the start, else each reads its own. Groups that are no ascending
-// stretches of the requests are reported, and then nothing is shared: the results are the same.
+// One CTA, for batches of more than kRestFew requests or groups. Groups that are no ascending stretches of the requests are reported,
+// and then nothing is shared: the results are the same.
 __global__ void __launch_bounds__(kPlanThreads, 1) kvx_shared_plan(const __grid_constant__ SharedArgs s) {
-    __shared__ int32_t s_tokens[kPlanThreads], s_unit[kPlanThreads];
-    __shared__ int64_t s_place[kPlanThreads], s_sums[2][kPlanWarps];
+    __shared__ int32_t s_tokens[kPlanThreads];
+    __shared__ PlanRoom<kPlanThreads> s_room;
     __shared__ int32_t s_len[kPlanLens];               // the first requests' lengths, read with the groups and not after them
     wait_for_earlier();
     const AttendArgs &a = s.a;
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int32_t group = a.n_q_heads / a.n_kv_heads;
-    const int64_t cap = (int64_t)a.max_blocks * a.pool.block_size;
-    auto length = [&](int32_t r) { return (int32_t)min((int64_t)max(a.seq_len[r], 0), cap); };
     bool bad = false;
-    for (int32_t r = threadIdx.x; r < min(a.n_reqs, kPlanLens); r += kPlanThreads) s_len[r] = length(r);
+    for (int32_t r = threadIdx.x; r < min(a.n_reqs, kPlanLens); r += kPlanThreads) s_len[r] = request_length(a, r);
     for (int32_t g = threadIdx.x; g < s.n_groups; g += kPlanThreads) {
         const int32_t lo = s.group_off[g], hi = s.group_off[g + 1];
         bad |= lo < 0 || hi < lo || hi > a.n_reqs;
@@ -45,70 +39,15 @@ __global__ void __launch_bounds__(kPlanThreads, 1) kvx_shared_plan(const __grid_
         const int32_t n = min(kPlanThreads, s.n_groups - g0);
         for (int32_t i = w; i < n; i += kPlanWarps) {                  // a warp a group: what it shares
             const int32_t lo = s.group_off[g0 + i], hi = s.group_off[g0 + i + 1];
-            int32_t least = INT32_MAX, most = 0;
-            for (int32_t r = lo + lane; r < hi; r += 32) {
-                const int32_t len = r < kPlanLens ? s_len[r] : length(r);
-                least = min(least, len);
-                most = max(most, len);
-            }
-            least = __reduce_min_sync(~0u, least);
-            most = __reduce_max_sync(~0u, most);
-            int32_t tokens = hi - lo < 2 ? 0 : min(s.prefix_len[g0 + i], least);
-            if (tokens < kSharedLeast || (a.window && most > a.window)) tokens = 0;
+            const int32_t tokens = shared_tokens(a, lo, hi, s.prefix_len[g0 + i], [&](int32_t r) { return r < kPlanLens ? s_len[r] : request_length(a, r); });
             if (lane == 0) s_tokens[i] = tokens;
             if (tokens)
                 for (int32_t r = lo + lane; r < hi; r += 32) s.start[r] = tokens;
         }
         __syncthreads();
-        int64_t my_units = 0, my_places = 0;
-        if ((int32_t)threadIdx.x < n && s_tokens[threadIdx.x]) {
-            const int64_t rows = (int64_t)(s.group_off[g0 + threadIdx.x + 1] - s.group_off[g0 + threadIdx.x]) * group;
-            const int64_t pairs = (rows + 2 * kSharedRows - 1) / (2 * kSharedRows), tiles = shared_tiles(s_tokens[threadIdx.x]);
-            my_units = pairs * a.n_kv_heads;
-            my_places = a.n_kv_heads * (pairs * kSharedSwitch + (pairs - 1) * 2 * tiles +
-                                        tiles * shared_weight((int32_t)(rows - (pairs - 1) * 2 * kSharedRows)));
-        }
-        int64_t u = warp_inclusive(my_units), p = warp_inclusive(my_places);
-        if (lane == 31) s_sums[0][w] = u, s_sums[1][w] = p;
-        __syncthreads();
-        int64_t all_units = 0, all_places = 0;
-        for (int i = 0; i < kPlanWarps; ++i) {
-            if (i == w) u += all_units, p += all_places;
-            all_units += s_sums[0][i];
-            all_places += s_sums[1][i];
-        }
-        s_unit[threadIdx.x] = (int32_t)(units + u - my_units);
-        s_place[threadIdx.x] = places + p - my_places;
-        units += all_units;
-        places += all_places;
-        __syncthreads();
-        for (int32_t i = w; i < n; i += kPlanWarps) {                  // its units
-            const int32_t tokens = s_tokens[i];
-            if (!tokens) continue;
-            const int32_t lo = s.group_off[g0 + i], hi = s.group_off[g0 + i + 1];
-            const int32_t rows = (hi - lo) * group, pairs = (rows + 2 * kSharedRows - 1) / (2 * kSharedRows);
-            const int64_t tiles = shared_tiles(tokens), pair_places = 2 * tiles + kSharedSwitch;
-            const int64_t head_places = (pairs - 1) * pair_places + tiles * shared_weight(rows - (pairs - 1) * 2 * kSharedRows) + kSharedSwitch;
-            for (int32_t j = lane; j < pairs * a.n_kv_heads; j += 32) {
-                const int32_t kvh = j / pairs, pair = j - kvh * pairs;
-                SharedUnit x;
-                x.begin = s_place[i] + kvh * head_places + pair * pair_places;
-                x.first = lo;
-                x.rows = min(rows - pair * 2 * kSharedRows, 2 * kSharedRows);
-                x.pair = pair;
-                x.kvh = kvh;
-                x.tokens = tokens;
-                x.pairs = pairs;
-                if (s_unit[i] + j < s.max_units) s.units[s_unit[i] + j] = x;
-            }
-            for (int32_t r = lo + lane; r < hi; r += 32) s.place_of[r] = make_int4(tokens, s_unit[i], (r - lo) * group, pairs);
-        }
-        __syncthreads();
+        plan_units<kPlanThreads>(s, g0, n, s_tokens, places, units, s_room);
     }
-    if (threadIdx.x == 0) {
-        s.header->places = places;
-        s.header->units = (int32_t)min(units, (int64_t)s.max_units);
-    }
+    plan_header(s, places, units);
 }
 
 // The join: a thread has four elements of a row (request, query head), the sums of its own positions and those of the CTAs that its
@@ -182,15 +121,30 @@ template <int IO> static cudaError_t launch_join(const SharedArgs &s, int32_t sm
     return launch_after(kvx_shared_join<IO, 128>, dim3((unsigned)((rows + 7) / 8)), 256, 0, stream, s, sms);
 }
 
-cudaError_t launch_attend_shared(const SharedArgs &s, int32_t vt, int32_t io, int32_t sms, cudaStream_t stream) {
-    cudaError_t e = launch_after(kvx_shared_plan, dim3(1), kPlanThreads, 0, stream, s);
-    if (e != cudaSuccess) return e;
-    const bool bf16 = io == KVX_BF16;
-    e = vt == KVX_BF16 ? launch_shared_bf16(s, sms, stream) : vt == KVX_F16 ? launch_shared_f16(s, sms, stream)
-        : bf16 ? launch_shared_e4m3_bf16(s, sms, stream) : launch_shared_e4m3_f16(s, sms, stream);
-    if (e != cudaSuccess) return e;
-    e = vt == KVX_BF16 ? launch_rest_bf16(s.a, sms, stream) : vt == KVX_F16 ? launch_rest_f16(s.a, sms, stream)
-        : bf16 ? launch_rest_e4m3_bf16(s.a, sms, stream) : launch_rest_e4m3_f16(s.a, sms, stream);
+static cudaError_t launch_prefixes(const SharedArgs &s, int32_t vt, bool bf16, int32_t sms, cudaStream_t stream) {
+    if (vt == KVX_BF16) return launch_shared_bf16(s, sms, stream);
+    if (vt == KVX_F16) return launch_shared_f16(s, sms, stream);
+    return bf16 ? launch_shared_e4m3_bf16(s, sms, stream) : launch_shared_e4m3_f16(s, sms, stream);
+}
+static cudaError_t launch_rest(const SharedArgs &s, int32_t vt, bool bf16, int32_t sms, cudaStream_t stream) {
+    if (vt == KVX_BF16) return launch_rest_bf16(s, sms, stream);
+    if (vt == KVX_F16) return launch_rest_f16(s, sms, stream);
+    return bf16 ? launch_rest_e4m3_bf16(s, sms, stream) : launch_rest_e4m3_f16(s, sms, stream);
+}
+
+cudaError_t launch_attend_shared(const SharedArgs &args, int32_t vt, int32_t io, int32_t sms, cudaStream_t stream) {
+    SharedArgs s = args;
+    const bool bf16 = io == KVX_BF16, few = s.a.n_reqs <= kRestFew && s.n_groups <= kRestFew;
+    cudaError_t e;
+    if (few) {                                                         // the plan is made beside the requests' own positions
+        s.a.start = nullptr;
+        e = launch_rest(s, vt, bf16, sms, stream);
+        if (e == cudaSuccess) e = launch_prefixes(s, vt, bf16, sms, stream);
+    } else {
+        e = launch_after(kvx_shared_plan, dim3(1), kPlanThreads, 0, stream, s);
+        if (e == cudaSuccess) e = launch_prefixes(s, vt, bf16, sms, stream);
+        if (e == cudaSuccess) e = launch_rest(s, vt, bf16, sms, stream);
+    }
     if (e != cudaSuccess) return e;
     return bf16 ? launch_join<KVX_BF16>(s, sms, stream) : launch_join<KVX_F16>(s, sms, stream);
 }

@@ -30,22 +30,17 @@
 // the requests' own positions as units 127.
 #pragma once
 
-#include "kvx_attend.cuh"
+#include "kvx_shared_plan.cuh"
 #include "kvx_tensor.cuh"
 
 namespace kvx {
 
-constexpr int kSharedTile = 128, kSharedRows = 128;                // positions of a tile, rows of a slot
 constexpr int kSharedThreads = 16 * 32;                            // warps 0-7: softmax, four a slot; 8, 9: products; 12-15: copies
 constexpr int kSharedLoaders = 128;
-constexpr int kSharedSwitch = 3;                                   // what a change of units counts, in places of the line
 constexpr int kSharedMin = 4;                                      // places of a CTA at least
 constexpr float kSharedSlack = 3.0f;                               // by which a score may pass the maximum, in powers of two
 constexpr uint32_t kSharedColSums = 0, kSharedColScores = 256;     // of TMEM: per slot 128
 
-// Two places a tile where both slots take each tile, one where they take turns.
-__host__ __device__ inline int shared_weight(int32_t rows) { return rows > kSharedRows ? 2 : 1; }
-__host__ __device__ inline int32_t shared_tiles(int32_t tokens) { return (int32_t)(((uint32_t)tokens + kSharedTile - 1) / kSharedTile); }
 __device__ __forceinline__ int64_t part_bytes(int32_t head_dim) { return 2 * kSharedRows * ((int64_t)head_dim * 4 + 8); }
 
 __device__ __forceinline__ Split shared_split(int64_t places, int ctas) {

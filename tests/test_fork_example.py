@@ -33,5 +33,5 @@ def test_shared_prompt():
     before = fork_shared_prompt.kvx.kvx_launch_count()
     out, turned = fork_shared_prompt.main(steps=8, prompt=5005, answers=48)
     assert out < 2.0 ** -6 and turned < 2.0 ** -8 + 2.0 ** -9
-    # 12 around the steps; the first step and the capture: free, slots, and of each of two layers a rotated append and four of the attention
-    assert fork_shared_prompt.kvx.kvx_launch_count() - before == 12 + 2 * (2 + 2 * 5)
+    # 12 around the steps; the first step and the capture: free, slots, and of each of two layers a rotated append and three of the attention
+    assert fork_shared_prompt.kvx.kvx_launch_count() - before == 12 + 2 * (2 + 2 * 4)

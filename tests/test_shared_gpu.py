@@ -83,7 +83,7 @@ def test_long_prefix_of_two(value):
 
 @pytest.mark.parametrize("n", [31, 32, 33, 63, 64, 65, 200, 1100])
 def test_many_groups(n):
-    """Up to the groups that each CTA plans itself and beyond, more than the plan takes at a time, and many units for a CTA."""
+    """Beside the requests' own positions or before them, more than the plan takes at a time, and many units for a CTA."""
     rng = np.random.default_rng(n)
     check_shared([(int(rng.integers(100, 300)), rng.integers(0, 20, int(rng.integers(0, 4))).tolist()) for _ in range(n)],
                  group=2, hps=1 if n > 100 else 3, dim=64)
@@ -96,6 +96,40 @@ def test_many_requests(value, io, dim, layout, group, window):
     rng = np.random.default_rng(7)
     groups = [(int(rng.integers(100, 400)), rng.integers(0, 90, 16).tolist()) for _ in range(20)] + [0, 70]
     check_shared(groups, value=value, io=io, dim=dim, layout=layout, group=group, hps=2, window=window)
+
+
+@pytest.mark.parametrize("value,io", FORMS)
+@pytest.mark.parametrize("dim,layout,group,window", [(64, NHD, 2, 0), (128, HND, 3, 0), (80, NHD, 1, 250), (128, NHD, 17, 0)])
+def test_more_requests_than_are_planned_beside_the_rest(value, io, dim, layout, group, window):
+    """The plan is a launch of its own."""
+    rng = np.random.default_rng(8)
+    groups = [(int(rng.integers(100, 400)), rng.integers(0, 60, 16).tolist()) for _ in range(25)] + [0, 70]
+    case = Shared(groups, value=value, io=io, dim=dim, layout=layout, group=group, hps=1, window=window)
+    got, n = launches(case)
+    assert n == 4
+    case.check_parts(*got)
+
+
+@pytest.mark.parametrize("members,n_launches", [(383, 3), (384, 3), (385, 4)])
+def test_where_the_plan_becomes_a_launch(members, n_launches):
+    case = Shared([(200, [i % 9 for i in range(members)])], group=2, hps=1, dim=64)
+    got, n = launches(case)
+    assert n == n_launches
+    case.check_parts(*got)
+
+
+@pytest.mark.parametrize("n_groups,n_launches", [(256, 3), (257, 3), (384, 3), (385, 4), (2000, 4)])
+def test_groups_without_members(n_groups, n_launches):
+    """In front, between and behind those that have some."""
+    case = Shared([(300, [1, 2]), 90, (200, [0, 5, 3])], dim=64)
+    third = n_groups // 3
+    off = [0] * third + [0, 2, 3] + [3] * (n_groups - 2 * third - 3) + [6] * (third + 1)
+    prefix = [7] * third + [300, 90] + [150] * (n_groups - 2 * third - 3) + [200] + [9] * third
+    assert len(off) == n_groups + 1 and len(prefix) == n_groups
+    got, n = launches(case, off=off, prefix=prefix)
+    assert n == n_launches
+    case.check_parts(*got)
+    assert kvx.kvx_cache_status(case.cache) == kvx.KVX_OK
 
 
 @pytest.mark.parametrize("group,hps", [(130, 1), (256, 1), (300, 1), (140, 2)])
