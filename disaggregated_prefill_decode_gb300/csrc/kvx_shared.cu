@@ -1,9 +1,10 @@
-// kvx_cache_attend_shared: the plan of a batch's shared prefixes, the launches, and the join of what they leave.
+// kvx_cache_attend_shared: the launches, the plan of a large batch, and the join of what the other kernels leave.
 //
-// Four launches: the plan (one CTA, 5 us), the prefixes, the requests' own positions (12 us for 16 x 400 positions, 21 for 64 x 500), the join
-// (4 us for 16 requests of 64 heads, 7 for 64). 16 samples of a prompt of 8192 35.6 us in all, 64 requests on 32768 104, 96 8-bit requests in 12
-// groups 52. Of launches that start before the one ahead has ended the wait is all that is left; letting them start earlier still
-// (launch_dependents) took SM time from it: 40 to 47 us. A plan in each CTA of the prefixes' kernel took as long: its reads are as cold there.
+// Three launches: the requests' own positions, with the plan made by one of their CTAs (12 us for 16 x 400 positions, 21 for 64 x 500), the prefixes,
+// the join (4 us for 16 requests of 64 heads, 7 for 64). 16 samples of a prompt of 8192 32.3 us in all, 64 requests on 32768 102, 96 8-bit
+// requests in 12 groups 49. With more than kRestFew requests or groups the plan is a launch of its own before the others (5 us: 34.7, 104 and 51).
+// Of launches that start before the one ahead has ended the wait is all that is left; letting them start earlier still (launch_dependents)
+// took SM time from it: 40 us, 47. A plan in each CTA of the prefixes' kernel took as long as one of its own: its reads are as cold there.
 #include "kvx_shared.cuh"
 
 namespace kvx {

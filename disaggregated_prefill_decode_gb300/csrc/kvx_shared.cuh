@@ -1,6 +1,6 @@
 // kvx_cache_attend_shared over the prefixes that groups of requests share, on the tcgen05 tensor pipe: the kernel, instantiated
-// per value type in kvx_shared_*.cu. What stands around it (the plan before, the join after) is in kvx_shared.cu; each request's own
-// positions go through the kernel of kvx_attend_planes.cuh.
+// per value type in kvx_shared_*.cu. The plan before it is in kvx_shared_plan.cuh, the launches and the join after it in kvx_shared.cu; each
+// request's own positions go through the kernel of kvx_attend_planes.cuh.
 //
 // The queries of all members of a group that read one KV head are the rows of one matrix Q (members x query heads of a KV head), so
 // a prefix is attention with many queries:
@@ -20,7 +20,7 @@
 // Keys and values come row by row with asynchronous copies of 16 bytes, so pages of any size and layout will do, into rings
 // whose rows of 64 elements are swizzled over 128 bytes: K-major for the scores, MN-major for the sums. Their arrival is the copies' own;
 // the proxy fence stands where they are used (where they are made it had each copying thread wait for its copies). 8-bit codes pass through
-// registers and become f16, which holds them exactly; the copies' four warps are bound by that conversion.
+// registers and become f16, which holds them exactly (1000 clocks of the copies' warps for a tile of keys or values).
 //
 // Bound by the tensor pipe where many rows share (with the weights' second value three products, not two): 64 requests on a document of 32768
 // positions, 64 + 8 heads of 128, 68 us, 1.0 PFLOP/s of scores and sums, 1.5 with the second value, 0.79 of the measured rate; else by what a CTA's one

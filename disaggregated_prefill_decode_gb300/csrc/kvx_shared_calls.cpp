@@ -9,9 +9,10 @@ using namespace kvx;
 
 // What sharing a prefix can save has to be worth its launches: below this many bytes that requests would read again, which they mostly
 // find in L2, each reads its own. On GB300, 8 KV heads of 128 with 8 query heads each (us, shared / each its own): bf16, one group of 8 on 4096 positions
-// (113 MiB read again) 30.4 / 26.5, on 8192 (226) 32.9 / 42.7; 4 groups of 4 on 2048 (99) 31 / 27, on 4096 (195) 38 / 44; 16 groups of 4 on 1024
-// (204) 46 / 47. 8 bits: one group of 32 on 2048 (128) 33 / 30, on 4096 (252) 35 / 48; 16 groups of 4 on 1024 (102) 49 / 32, on 2048 (198) 61 / 51.
-static constexpr int64_t kWorthBytes = 160 << 20;
+// (113 MiB read again) 26.6 / 26.5, on 8192 (226) 28.6 / 42.8; one of 64 on 512 (142) 34 / 31; 4 groups of 4 on 2048 (99) 27.9 / 27.3, on 4096 (195)
+// 35 / 44; 16 groups of 4 on 512 (108) 35 / 31, on 1024 (204) 44 / 47. 8 bits: one group of 8 on 8192 (113) 29.1 / 29.4, on 16384 (225) 35 / 47; 4 groups
+// of 16 on 1024 (128) 36 / 32, on 2048 (248) 36 / 50; 16 groups of 4 on 2048 (198) 60 / 50.
+static constexpr int64_t kWorthBytes = 144 << 20;
 
 static bool can_share(const kvx_cache_t c, int32_t n_reqs) {
     return c->g.n_planes == 2 && c->g.head_dim <= kSharedMaxDim && (int64_t)n_reqs * c->cfg.n_q_heads <= std::numeric_limits<int32_t>::max();

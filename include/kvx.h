@@ -664,7 +664,7 @@ kvx_status kvx_cache_attend(kvx_cache_t cache, int32_t layer, const void *q, int
  * kvx_pages_fork makes them. They are read through the row of the group's first member, up to the shortest member's length. With a window a
  * group shares its prefix while the window of every member reaches the first position. Both arrays are device memory, checked there:
  * a negative prefix_len counts as 0, with a group_off that is no such list nothing is shared, and kvx_cache_status reports either.
- * Whether a prefix is worth sharing is decided here: short ones (below 128 positions), batches that read little twice (below 160 MiB by
+ * Whether a prefix is worth sharing is decided here: short ones (below 128 positions), batches that read little twice (below 144 MiB by
  * max_blocks), latents and head dims above 128 go to kvx_cache_attend, or read their prefixes themselves.
  * workspace: kvx_cache_shared_bytes bytes of device memory (0 for caches that do not share), on a 16-byte boundary, in no particular
  * state and free again after the call's device work; calls whose device work overlaps need workspaces, and handles, of their own.

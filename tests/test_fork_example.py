@@ -28,7 +28,7 @@ def test_small_batches_read_the_prompt_themselves(prompt, answers):
 
 
 def test_shared_prompt():
-    """240 MB that each request would read again."""
+    """240 MB that would be read again."""
     import fork_shared_prompt
     before = fork_shared_prompt.kvx.kvx_launch_count()
     out, turned = fork_shared_prompt.main(steps=8, prompt=5005, answers=48)
