@@ -85,7 +85,7 @@ template <int VT_, int IO_, int D_, int NT_, bool FULL_> struct Shape {
 };
 
 // The positions of requests behind the prefixes that kvx_cache_attend_shared has taken: in the place of outputs, sums in 32 bits
-// that its last kernel joins with those of the prefixes.
+// that its last kernel joins with those of the prefixes. It also joins what several CTAs have of a segment, so none waits for another's.
 template <class S> struct RestShape : S {
     static constexpr bool REST = true;
     static_assert(S::WARPS * S::WARP_BYTES + kRestFew * 4 + 512 <= (227 << 10), "beside the rings there is room for kRestFew requests");
@@ -129,12 +129,6 @@ template <class S> struct Joined {
         const int lane = threadIdx.x & 31, g = lane >> 2;
         if (!to) {
             const int d = S::dim(g, e4 * 4);
-            if constexpr (S::REST) {
-                const int64_t row = (int64_t)r * a.n_q_heads + head0 + q;
-                if (q < heads && (S::FULL || d < a.head_dim)) *reinterpret_cast<float4 *>(a.rest + row * a.head_dim + d) = o;
-                if (q < heads && e4 == 0 && g == 0) a.rest_ml[row] = make_float2(top, l);
-                return;
-            }
             if (q < heads && (S::FULL || d < a.head_dim)) {
                 const float inv = l == 0.0f ? 0.0f : a.v_scale / l;
                 const uint2 y = make_uint2(pack<S::IO>(o.x * inv, o.y * inv), pack<S::IO>(o.z * inv, o.w * inv));
@@ -149,6 +143,18 @@ template <class S> struct Joined {
                 __stcg(p.l + q, l);
             }
         }
+    }
+    // REST: the segment's sums, of which `more` CTAs behind this one have more, or (begun) what this CTA adds to another one's.
+    __device__ __forceinline__ void put_rest(const AttendArgs &a, bool begun, int32_t more, int32_t r, int32_t head0, int32_t heads) const {
+        const int g = (threadIdx.x & 31) >> 2, d = S::dim(g, e4 * 4);
+        if (q >= heads) return;
+        const int64_t row = (int64_t)r * a.n_q_heads + head0 + q;
+        uint8_t *const part = a.rest_parts + blockIdx.x * rest_part_bytes(a.head_dim);
+        float *const to = begun ? reinterpret_cast<float *>(part + kRestRows * 8) + q * a.head_dim : a.rest + row * a.head_dim;
+        if (S::FULL || d < a.head_dim) *reinterpret_cast<float4 *>(to + d) = o;
+        if (e4 != 0 || g != 0) return;
+        if (begun) reinterpret_cast<float2 *>(part)[q] = make_float2(top, l);
+        else a.rest_ml[row] = make_float4(top, l, __int_as_float((int32_t)blockIdx.x + 1), __int_as_float(more));
     }
 };
 
@@ -404,7 +410,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
                                     *reinterpret_cast<float4 *>(a.rest + row * a.head_dim + d) =
                                         make_float4(o[n][e][i], o[n][e][2 + i], o[n][e + 1][i], o[n][e + 1][2 + i]);
                             }
-                            if (g == 0) a.rest_ml[row] = make_float2(m[n][i], l[n][i]);
+                            if (g == 0) a.rest_ml[row] = make_float4(m[n][i], l[n][i], 0.0f, 0.0f);
                             continue;
                         }
                         const float inv = l[n][i] == 0.0f ? 0.0f : a.v_scale / l[n][i];
@@ -626,10 +632,15 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
         const int32_t heads = heads_of(where[1], &head0);
         uint8_t *const first = i & 1 ? smem + (i >> 1) * S::WARP_BYTES : first_slot(i >> 1);
         const Pieces from = {first, first_slot(i >> 1), S::SLOT ? S::WARP_BYTES : S::PARTIAL, n};
+        if constexpr (S::REST) {                                   // the pieces of other CTAs are joined with the prefix
+            const int32_t more = i == open[1] ? split.cta_of(s_seg[i >> 1][i & 1] + where[2] - 1) - (int32_t)blockIdx.x : 0;
+            for (; task < FS; task += S::WARPS) join_few<S, false>(task, from).put_rest(a, i == open[0], more, where[0], head0, heads);
+            continue;
+        }
         uint8_t *const to = i == open[0] || i == open[1] ? cta_parts + (size_t)(blockIdx.x * 2 + (i == open[1])) * S::PARTIAL : nullptr;
         for (; task < FS; task += S::WARPS) join_few<S, false>(task, from).put(a, to, where[0], head0, heads);
     }
-    if (open[0] < 0 && open[1] < 0) return;
+    if (S::REST || (open[0] < 0 && open[1] < 0)) return;
     __syncthreads();
     if (threadIdx.x < 2) {
         const int i = open[threadIdx.x];

@@ -236,7 +236,8 @@ struct AttendArgs {
     uint64_t wait_ns;                 // latents, shared prefixes: limit of a wait for a copy or a product
     const int32_t *start;             // kvx_cache_attend_shared: each request's first position behind its group's prefix (NULL: the kernel's to find),
     float *rest;                      // and for the ones from there the sums, [request][query head][head_dim],
-    float2 *rest_ml;                  // with their maximum and the weights' sum
+    float4 *rest_ml;                  // with their maximum, the weights' sum, and (integers) which CTAs have more of them: the first, how many
+    uint8_t *rest_parts;              // what those have, rest_part_bytes each
 };
 // Limit of one such wait, far beyond any copy or product of a tile; and that of a call that kvx_cache_inject_stall prepared.
 constexpr uint64_t kCacheWaitNs = 2000000000ull;       // 2 s
@@ -281,6 +282,9 @@ struct SharedArgs {
 constexpr int32_t kSharedMaxDim = 128;
 enum { kStallSharedProducts = 1, kStallSharedSoftmax, kStallSharedCopies };
 int64_t shared_part_bytes(int32_t head_dim);                                   // of a partial result
+// Of a CTA's part of a segment that another one began: maximum and sum, then O, of up to 16 query heads.
+constexpr int kRestRows = 16;
+__host__ __device__ inline int64_t rest_part_bytes(int32_t head_dim) { return kRestRows * ((int64_t)head_dim * 4 + 8); }
 cudaError_t launch_attend_shared(const SharedArgs &s, int32_t value_type, int32_t io_type, int32_t sms, cudaStream_t stream);
 cudaError_t launch_shared_bf16(const SharedArgs &s, int32_t sms, cudaStream_t stream);
 cudaError_t launch_shared_f16(const SharedArgs &s, int32_t sms, cudaStream_t stream);

@@ -1,8 +1,9 @@
 // kvx_cache_attend_shared: the launches, the plan of a large batch, and the join of what the other kernels leave.
 //
-// Three launches: the requests' own positions, with the plan made by one of their CTAs (12 us for 16 x 400 positions, 21 for 64 x 500), the prefixes,
-// the join (4 us for 16 requests of 64 heads, 7 for 64). 16 samples of a prompt of 8192 32.3 us in all, 64 requests on 32768 102, 96 8-bit
-// requests in 12 groups 49. With more than kRestFew requests or groups the plan is a launch of its own before the others (5 us: 34.7, 104 and 51).
+// Three launches: the requests' own positions, with the plan made by one of their CTAs (11 us for 16 x 400 positions, 22 for 64 x 500), the prefixes,
+// the join (5 us for 16 requests of 64 heads, 8 for 64). 16 samples of a prompt of 8192 30.9 us in all, 64 requests on 32768 100.6, 96 8-bit
+// requests in 12 groups 49.3; with the own positions joined in their kernel, as kvx_cache_attend does, 32.3, 102 and 49.2. With more than kRestFew
+// requests or groups the plan is a launch of its own before the others (2 to 2.4 us more).
 // Of launches that start before the one ahead has ended the wait is all that is left; letting them start earlier still (launch_dependents)
 // took SM time from it: 40 us, 47. A plan in each CTA of the prefixes' kernel took as long as one of its own: its reads are as cold there.
 #include "kvx_shared.cuh"
@@ -62,25 +63,17 @@ template <int IO, int D> __global__ void __launch_bounds__(256) kvx_shared_join(
     const int64_t row = (int64_t)blockIdx.x * ROWS + (threadIdx.x & 7) + threadIdx.x / (8 * C4) * 8;
     if (row >= (int64_t)a.n_reqs * a.n_q_heads || c * 4 >= a.head_dim) return;
     const int32_t r = (int32_t)(row / a.n_q_heads), head = (int32_t)(row - (int64_t)r * a.n_q_heads), group = a.n_q_heads / a.n_kv_heads;
+    const int32_t kvh = head / group, in_group = head - kvh * group;
     const int4 place = __ldcg(s.place_of + r);
     const int64_t places = s.header->places;
-    const float2 mine = __ldcg(a.rest_ml + row);
+    const float4 mine = __ldcg(a.rest_ml + row);
     float4 o = __ldcg(reinterpret_cast<const float4 *>(a.rest + row * a.head_dim) + c);
     float top = mine.x, l = mine.y;
     if (l == 0.0f) {                                                   // no position of its own has a weight
         top = -INFINITY;
         o = make_float4(0, 0, 0, 0);
     }
-    if (place.x) {
-        const int32_t kvh = head / group, at = place.z + head - kvh * group, unit = place.y + kvh * place.w + at / (2 * kSharedRows);
-        const SharedUnit u = s.units[unit];
-        const int weight = shared_weight(u.rows);
-        const Split split = shared_split(places, ctas);
-        const int32_t from = split.cta_of(u.begin), upto = split.cta_of(u.begin + (int64_t)shared_tiles(u.tokens) * weight - 1);
-        const int64_t bytes = part_bytes(a.head_dim);
-        const int in_slot = at % kSharedRows, slot = weight == 2 ? at % (2 * kSharedRows) / kSharedRows : 0;
-        const int32_t n = upto - from + 1;
-        const uint8_t *const parts = s.parts + (unit + from) * bytes + slot * (bytes / 2);
+    auto add = [&](const float2 *ml_at, const float4 *o_at, int64_t bytes, int32_t n) {
         for (int32_t x0 = 0; x0 < n; x0 += AT_ONCE) {
             float2 ml[AT_ONCE];
             float4 y[AT_ONCE];
@@ -89,9 +82,8 @@ template <int IO, int D> __global__ void __launch_bounds__(256) kvx_shared_join(
             for (int x = 0; x < AT_ONCE; ++x) {
                 ml[x] = make_float2(-INFINITY, 0.0f);
                 if (x0 + x < n) {
-                    const uint8_t *const p = parts + (x0 + x) * bytes;
-                    ml[x] = __ldcg(reinterpret_cast<const float2 *>(p) + in_slot);
-                    y[x] = __ldcg(reinterpret_cast<const float4 *>(p + kSharedRows * 8) + c * kSharedRows + in_slot);
+                    ml[x] = __ldcg(reinterpret_cast<const float2 *>(reinterpret_cast<const uint8_t *>(ml_at) + (x0 + x) * bytes));
+                    y[x] = __ldcg(reinterpret_cast<const float4 *>(reinterpret_cast<const uint8_t *>(o_at) + (x0 + x) * bytes));
                 }
             }
 #pragma unroll
@@ -109,6 +101,34 @@ template <int IO, int D> __global__ void __launch_bounds__(256) kvx_shared_join(
                     o = make_float4(fmaf(by, y[x].x, o.x), fmaf(by, y[x].y, o.y), fmaf(by, y[x].z, o.z), fmaf(by, y[x].w, o.w));
                 }
         }
+    };
+    const float2 *ml_at = nullptr;
+    const float4 *o_at = nullptr;
+    int64_t bytes = 0;
+    int32_t n = 0;
+    if (place.x) {                                                     // a member of a group that shares
+        const int32_t at = place.z + in_group, unit = place.y + kvh * place.w + at / (2 * kSharedRows);
+        const SharedUnit u = s.units[unit];
+        const int weight = shared_weight(u.rows);
+        const Split split = shared_split(places, ctas);
+        const int32_t from = split.cta_of(u.begin), upto = split.cta_of(u.begin + (int64_t)shared_tiles(u.tokens) * weight - 1);
+        const int in_slot = at % kSharedRows, slot = weight == 2 ? at % (2 * kSharedRows) / kSharedRows : 0;
+        bytes = part_bytes(a.head_dim);
+        n = upto - from + 1;
+        const uint8_t *const part = s.parts + (unit + from) * bytes + slot * (bytes / 2);
+        ml_at = reinterpret_cast<const float2 *>(part) + in_slot;
+        o_at = reinterpret_cast<const float4 *>(part + kSharedRows * 8) + c * kSharedRows + in_slot;
+    }
+    const int32_t more = __float_as_int(mine.w);
+    for (int k = 0; k < 2; ++k) {                                      // the prefix, then what other CTAs have of the request's own positions
+        add(ml_at, o_at, bytes, n);
+        if (!more) break;
+        bytes = rest_part_bytes(a.head_dim);
+        n = more;
+        const uint8_t *const part = a.rest_parts + __float_as_int(mine.z) * bytes;
+        const int in_set = in_group % (group > 8 ? 16 : 8);
+        ml_at = reinterpret_cast<const float2 *>(part) + in_set;
+        o_at = reinterpret_cast<const float4 *>(part + kRestRows * 8 + (int64_t)in_set * a.head_dim * 4) + c;
     }
     const float inverse = l == 0.0f ? 0.0f : a.v_scale / l;
     *reinterpret_cast<uint2 *>(a.out + r * a.out_stride + ((int64_t)head * a.head_dim + c * 4) * 2) =

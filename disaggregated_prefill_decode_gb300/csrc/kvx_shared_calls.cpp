@@ -33,7 +33,7 @@ static int64_t lay_out(const kvx_cache_t c, int32_t n_reqs, int32_t n_groups, in
     };
     uint8_t *const header = take(sizeof(SharedHeader)), *const unit = take(units * (int64_t)sizeof(SharedUnit));
     uint8_t *const start = take(4 * (int64_t)n_reqs), *const place_of = take(16 * (int64_t)n_reqs);
-    uint8_t *const ml = take(rows * 8), *const rest = take(rows * g.head_dim * 4);
+    uint8_t *const ml = take(rows * 16), *const rest = take(rows * g.head_dim * 4), *const rest_parts = take(sms * rest_part_bytes(g.head_dim));
     uint8_t *const parts = take((units + sms) * shared_part_bytes(g.head_dim));
     if (s) {
         s->header = (SharedHeader *)header;
@@ -44,7 +44,8 @@ static int64_t lay_out(const kvx_cache_t c, int32_t n_reqs, int32_t n_groups, in
         s->parts = parts;
         s->a.start = s->start;
         s->a.rest = (float *)rest;
-        s->a.rest_ml = (float2 *)ml;
+        s->a.rest_ml = (float4 *)ml;
+        s->a.rest_parts = rest_parts;
     }
     return at;
 }

@@ -90,6 +90,13 @@ def test_many_groups(n):
 
 
 @pytest.mark.parametrize("value,io", FORMS)
+@pytest.mark.parametrize("dim,group,rest", [(64, 8, [9000, 0, 700]), (128, 17, [3, 12000]), (80, 3, [40000, 1]), (128, 40, [2500] * 3), (64, 1, [70000, 300])])
+def test_own_positions_of_several_ctas(value, io, dim, group, rest):
+    """A few parts of a request's own positions, and more than are joined at a time."""
+    check_shared([(300, rest), 5000], value=value, io=io, dim=dim, group=group, hps=1)
+
+
+@pytest.mark.parametrize("value,io", FORMS)
 @pytest.mark.parametrize("dim,layout,group,window", [(64, NHD, 2, 0), (128, HND, 3, 0), (80, NHD, 1, 250), (128, NHD, 17, 0)])
 def test_many_requests(value, io, dim, layout, group, window):
     """Of every type, with groups of their own, a sliding window, and requests alone and empty."""
