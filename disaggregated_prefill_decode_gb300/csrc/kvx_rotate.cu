@@ -23,7 +23,7 @@
 
 namespace kvx {
 
-constexpr int kRotateThreads = 256, kRotateWarps = kRotateThreads / 32, kRotateParts = 7;
+constexpr int kRotateThreads = 256, kRotateWarps = kRotateThreads / 32;
 
 // A lane's two vectors of a head, and what becomes of them.
 struct RotateVecs {
@@ -32,8 +32,9 @@ struct RotateVecs {
     bool norm_a, norm_b;
 };
 
-// Slot s of a head: the vectors that turn with one another, or two neighbours in a list of what is left.
-__device__ __forceinline__ RotateVecs rotate_vecs(const RotateArgs &r, int s) {
+// Slot s of a head: the vectors that turn with one another, or two neighbours in a list of what is left. With two slots a lane (NP) those
+// of the first ones are 64 vectors in a row, so that what turns of a latent is in the second ones alone.
+template <int NP> __device__ __forceinline__ RotateVecs rotate_vecs(const RotateArgs &r, int s) {
     const int vecs = r.head_dim / 8, begin = r.begin / 8, turned = r.turned / 8;
     RotateVecs v = {-1, -1, false, false, false, false};
     if (!r.pairs && turned) {
@@ -47,9 +48,9 @@ __device__ __forceinline__ RotateVecs rotate_vecs(const RotateArgs &r, int s) {
             if (t < half && t + half < rest) v.b = t + half < begin ? t + half : t + half + turned;
         }
     } else {
-        const int half = (vecs + 1) / 2;
-        if (s < half) v.a = s;
-        if (s < half && s + half < vecs) v.b = s + half;
+        const int half = (vecs + 1) / 2, a = NP == 1 ? s : s / 32 * 64 + s % 32, b = NP == 1 ? s + half : a + 32;
+        if (NP == 1 ? s < half : a < vecs) v.a = a;
+        if (v.a >= 0 && b < vecs) v.b = b;
         v.turns_a = v.a >= begin && v.a < begin + turned;
         v.turns_b = v.b >= begin && v.b < begin + turned;
     }
@@ -94,6 +95,7 @@ template <int IO, bool F8, int LANES, int NP, bool PAIRS, bool WHOLE> struct Rot
     float2 *const turned;              // of the warp, in shared memory: sine and cosine of each pair at the token's position
     RotateVecs v[NP];
     int slot_of[NP];
+    bool some[NP];                     // whether any lane has something that turns
     int64_t token, at_slot;
     // The weights of a kind of heads, and what they make of the sines and cosines: (a, b) becomes (a by[0] - b by[3], b by[2] + a by[1]).
     float by[NP][4][8];
@@ -102,7 +104,8 @@ template <int IO, bool F8, int LANES, int NP, bool PAIRS, bool WHOLE> struct Rot
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
             slot_of[n] = threadIdx.x % LANES + LANES * n;
-            v[n] = rotate_vecs(r, slot_of[n]);
+            v[n] = rotate_vecs<NP>(r, slot_of[n]);
+            some[n] = WHOLE || __any_sync(~0u, v[n].turns_a || v[n].turns_b);
         }
     }
 
@@ -126,6 +129,7 @@ template <int IO, bool F8, int LANES, int NP, bool PAIRS, bool WHOLE> struct Rot
     __device__ __forceinline__ void weigh(const uint8_t *weight) {
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
+            if (!F8 && !weight && !some[n]) continue;              // copied as they are
             float f[2][8];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -172,9 +176,13 @@ template <int IO, bool F8, int LANES, int NP, bool PAIRS, bool WHOLE> struct Rot
         const int heads = KIND == kQueries ? r.n_q_heads : r.n_kv_heads;
         const uint8_t *const weight = KIND == kQueries ? r.q_weight : KIND == kKeys ? r.k_weight : nullptr;
         const int h = at * AT_ONCE + which();
+        constexpr bool NARROWS = F8 && KIND != kQueries;
         float y[NP][2][8];
+        bool as_is[NP];
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
+            as_is[n] = !NARROWS && (KIND == kValues || (!weight && !some[n]));
+            if (as_is[n]) continue;
             widen<IO>(x[n][0], y[n][0]);
             widen<IO>(x[n][1], y[n][1]);
         }
@@ -210,6 +218,11 @@ template <int IO, bool F8, int LANES, int NP, bool PAIRS, bool WHOLE> struct Rot
         };
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
+            if (as_is[n]) {
+                if (WHOLE || v[n].a >= 0) reinterpret_cast<uint4 *>(dst)[v[n].a] = x[n][0];
+                if (WHOLE || v[n].b >= 0) reinterpret_cast<uint4 *>(dst)[v[n].b] = x[n][1];
+                continue;
+            }
             if constexpr (KIND != kValues) {
                 const float of_a = WHOLE || v[n].norm_a ? inverse : 1.0f, of_b = WHOLE || v[n].norm_b ? inverse : 1.0f;
 #pragma unroll
@@ -294,13 +307,21 @@ __global__ void __launch_bounds__(kRotateThreads, NP == 1 ? 2 : 1) kvx_rotate_ke
 }
 
 template <int IO, bool F8, int LANES, int NP> static cudaError_t launch(const RotateArgs &a, int32_t sms, cudaStream_t stream) {
-    // A token's heads go to as many warps as give each warp of the GPU some seven parts, so that they end together; each of them computes
-    // the token's sines and cosines again.
+    // A token's heads go to `parts` warps, so that a few tokens have the whole GPU and many end together; but what a warp does for a token
+    // (its slot, sines and weights) takes as long as three rounds, and each of them does it again. The time is that of the warp with
+    // the most parts. 8192 tokens of 20 rounds in 1 part 58.6 us, in 2 55.0; 2000 in 1 16.3, in 4 21, in 7 25; 600 in 4 6.9, in 8 8.6; 8192 of 4 rounds in
+    // 1 19.0, in 2 20.6; 1158 latents of 17 rounds in 1 14.5, in 2 17.2, in 7 27.9.
     const int at_once = 32 / LANES, q_rounds = (a.n_q_heads + at_once - 1) / at_once, kv_rounds = (a.n_kv_heads + at_once - 1) / at_once;
     const int64_t room = (NP == 1 ? 2 : 1) * sms, tokens = (a.n_tokens + kRotateWarps - 1) / kRotateWarps;
     const int64_t rounds = q_rounds + a.planes * kv_rounds;
-    const unsigned parts = (unsigned)std::min<int64_t>(rounds, std::max<int64_t>(1, kRotateParts * room / tokens));
-    const dim3 grid((unsigned)std::min<int64_t>(tokens, std::max<int64_t>(1, room / parts)), std::min(parts, 65535u));
+    int64_t parts = 1;
+    double least = 0;
+    for (int64_t p = 1; p <= std::min<int64_t>(rounds, room); ++p) {
+        const int64_t across = std::min(tokens, room / p) * kRotateWarps;      // tokens at a time
+        const double time = (double)((a.n_tokens + across - 1) / across) * (3 + (double)((rounds + p - 1) / p));
+        if (p == 1 || time < least) least = time, parts = p;
+    }
+    const dim3 grid((unsigned)std::min(tokens, room / parts), (unsigned)parts);
     const bool full = a.head_dim == 16 * LANES && a.turned == a.head_dim && (a.norm_dim == a.head_dim || (!a.q_weight && !a.k_weight));
     constexpr int bytes = kRotateWarps * Rotate<IO, F8, LANES, NP, false, false>::RING;
     auto start = [&](auto *kernel, std::atomic<uint64_t> &asked) {
