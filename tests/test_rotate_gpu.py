@@ -170,6 +170,26 @@ def test_latents(value, q_heads):
 
 
 @pytest.mark.parametrize("value", ["bf16", "e4m3"])
+@pytest.mark.parametrize("q_norm,k_norm", [(False, False), (True, False), (False, True)])
+@pytest.mark.parametrize("pairs,begin,turned,norm_dim", [(1, 0, 64, 0), (0, 512, 64, 512), (1, 264, 48, 8), (1, 8, 256, 576), (0, 320, 256, 64), (1, 0, 0, 264)])
+def test_parts_of_wide_heads(value, q_norm, k_norm, pairs, begin, turned, norm_dim):
+    """Two slots of a head for each lane, some of which only copy."""
+    for dim in (576, 520 if begin + turned <= 520 and norm_dim <= 520 and value == "bf16" else 576):
+        c = make(value, None, NHD, dict(layout=pairs), turned, dict(dim=dim, q_heads=3, heads=1, planes=1, block=16, tokens=70, begin=begin, norm_dim=norm_dim,
+                                                                    q_norm=q_norm, k_norm=k_norm, scales=(0.03, 0.0) if value == "e4m3" else (0, 0)))
+        c.check(c.run())
+
+
+@pytest.mark.parametrize("tokens", [2, 9, 76, 152, 305, 611, 1217, 2433])
+@pytest.mark.parametrize("wide", [False, True])
+def test_numbers_of_tokens(tokens, wide):
+    """A token's heads among many warps, a few, or one."""
+    kw = dict(dim=576, q_heads=8, heads=1, planes=1, begin=512, norm_dim=512, q_norm=False) if wide else dict(dim=64, q_heads=24, heads=2)
+    c = make("bf16", None, NHD, dict(layout=int(wide)), 64, dict(kw, tokens=tokens))
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("value", ["bf16", "e4m3"])
 def test_in_place(value):
     c = make(value, None, HND, dict(layout=0), 128, dict(dim=128, q_heads=8, heads=2, tokens=200))
     c.check(c.run(in_place=True))
