@@ -347,7 +347,7 @@ struct RotateArgs {
     int64_t n_tokens, n_rows;         // n_rows: slots of the pool
     int32_t n_q_heads, n_kv_heads, head_dim, planes;
     int32_t begin, turned, norm_dim;  // elements [begin, begin + turned) turn, the first norm_dim are normed
-    bool pairs;
+    bool pairs, line;                 // line: see kvx_rotate_kernel
     float norm_inverse, eps, magnitude, k_inverse, v_inverse;
     int32_t device;
     uint64_t turns[kRotateMaxPairs];  // frequencies, in 2^-64 turns a position

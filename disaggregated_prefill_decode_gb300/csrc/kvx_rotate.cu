@@ -12,7 +12,7 @@
 // is bytes on their way: asynchronous copies of four rounds into places of shared memory that the lane itself reads back.
 //
 // Measured on GB300: 8192 tokens of 64 + 8 + 8 heads of 128 (336 MB) 54.9 us, 6.1 TB/s; 64 latents with 16 query heads 5.3, the host's time for a
-// call, 1158 of them 14.4, 5000 with 24 heads 86 (3.3 TB/s). Steps: a warp a token, reads of four heads ahead in registers 86.7 us; a persistent warp, sines by the warp 68; no exceptions for
+// call, 1158 of them 14.4, 5000 with 24 heads 70 (4.1 TB/s). Steps: a warp a token, reads of four heads ahead in registers 86.7 us; a persistent warp, sines by the warp 68; no exceptions for
 // lanes where whole heads turn (31 million instructions, 42) 70; the next rounds' reads over tokens, in registers 74; in shared memory
 // 63 with 24 warps an SM, 58 with 16 (8 rounds ahead 71 and 59: the more rows at once, the slower the memory); tokens in two parts 55.
 #include "kvx_attend.cuh"
@@ -252,20 +252,30 @@ __global__ void __launch_bounds__(kRotateThreads, NP == 1 ? 2 : 1) kvx_rotate_ke
     extern __shared__ __align__(16) uint8_t s_ring[];
     wait_for_earlier();
     Warp warp(r, s_turned[threadIdx.x >> 5]);
-    const int part = blockIdx.y, parts = gridDim.y;
     const int q_rounds = (r.n_q_heads + Warp::AT_ONCE - 1) / Warp::AT_ONCE, kv_rounds = (r.n_kv_heads + Warp::AT_ONCE - 1) / Warp::AT_ONCE;
     const int keys = q_rounds, values = q_rounds + kv_rounds, all = q_rounds + r.planes * kv_rounds;       // first rounds
-    const int from = (int)((int64_t)all * part / parts), upto = (int)((int64_t)all * (part + 1) / parts);
-    const int64_t step = (int64_t)gridDim.x * kRotateWarps;
-    int64_t token = (int64_t)blockIdx.x * kRotateWarps + (threadIdx.x >> 5), far = token, slot = -1, pos = 0;
-    int at = from, far_at = from;
+    // A warp has rounds [from, upto) of every so-manyth token, or (line) an equal stretch of one line of all tokens' rounds.
+    int from = (int)((uint32_t)all * blockIdx.y / gridDim.y), upto = (int)((uint32_t)all * (blockIdx.y + 1) / gridDim.y);
+    int64_t step = (int64_t)gridDim.x * kRotateWarps, token = (int64_t)blockIdx.x * kRotateWarps + (threadIdx.x >> 5);
+    int64_t left = token < r.n_tokens ? (int64_t)((uint32_t)(r.n_tokens - 1 - token) / (uint32_t)step + 1) * (upto - from) : 0;
+    int at = from;
+    if (NP > 1 && r.line) {
+        const int64_t begin = r.n_tokens * all * token / step;
+        left = r.n_tokens * all * (token + 1) / step - begin;
+        token = begin / all;
+        at = (int)(begin - token * all);
+        step = 1;
+    }
+    int64_t far = token, far_left = left, slot = -1, pos = 0;
+    int far_at = at;
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(s_ring) + (threadIdx.x >> 5) * Warp::RING + (threadIdx.x & 31) * 16;
     auto read = [&](int stage) {                                      // the next round to be read
-        if (far < r.n_tokens) {
+        if (far_left > 0) {
             const uint32_t to = ring + stage * (NP * 1024);
             if (far_at < keys) warp.read(to, r.q + far * r.q_stride, far_at, r.n_q_heads);
             else if (far_at < values) warp.read(to, r.k + far * r.k_stride, far_at - keys, r.n_kv_heads);
             else warp.read(to, r.v + far * r.v_stride, far_at - values, r.n_kv_heads);
+            --far_left;
             if (++far_at == upto) {
                 far_at = from;
                 far += step;
@@ -279,26 +289,27 @@ __global__ void __launch_bounds__(kRotateThreads, NP == 1 ? 2 : 1) kvx_rotate_ke
     };
     look_up(token);
     for (int u = 0; u < Warp::AHEAD - 1; ++u) read(u);
-    bool live = false;
-    for (int stage = 0; token < r.n_tokens; stage = stage + 1 == Warp::AHEAD ? 0 : stage + 1) {
+    bool live = false, fresh = true;
+    for (int stage = 0; left > 0; --left, stage = stage + 1 == Warp::AHEAD ? 0 : stage + 1) {
         read(stage ? stage - 1 : Warp::AHEAD - 1);
-        if (at == from) {
+        if (fresh) {
             const int64_t here = slot;
             live = here >= 0 && here < r.n_rows;
             if (live) warp.go(token, here, pos);
-            else if (here != -1 && part == 0 && (threadIdx.x & 31) == 0) atomicAdd(r.pool.skipped, 1ull);
+            else if (here != -1 && at == 0 && (threadIdx.x & 31) == 0) atomicAdd(r.pool.skipped, 1ull);
             look_up(token + step);
         }
         copies_wait<Warp::AHEAD - 1>();
         if (live) {
-            if ((at == from && at < values) || at == keys) warp.weigh(at < keys ? r.q_weight : r.k_weight);
+            if ((fresh && at < values) || at == keys) warp.weigh(at < keys ? r.q_weight : r.k_weight);
             typename Warp::Vectors x;
             Warp::read_back(x, ring + stage * (NP * 1024));
             if (at < keys) warp.template round<kQueries>(x, at);
             else if (at < values) warp.template round<kKeys>(x, at - keys);
             else warp.template round<kValues>(x, at - values);
         }
-        if (++at == upto) {
+        fresh = ++at == upto;
+        if (fresh) {
             at = from;
             token += step;
         }
@@ -321,12 +332,18 @@ template <int IO, bool F8, int LANES, int NP> static cudaError_t launch(const Ro
         const double time = (double)((a.n_tokens + across - 1) / across) * (3 + (double)((rounds + p - 1) / p));
         if (p == 1 || time < least) least = time, parts = p;
     }
-    const dim3 grid((unsigned)std::min(tokens, room / parts), (unsigned)parts);
+    dim3 grid((unsigned)std::min(tokens, room / parts), (unsigned)parts);
+    // Of wide heads, more tokens than warps: one line of all rounds, of which every warp has as much (5000 latents of 25 rounds 70 us, 86 by whole
+    // tokens; 1158 of 17 15.0, 14.4; 300 7.9, 6.8). Not of others: warps then work on rows far apart, which the memory answers more slowly (8192 tokens of 20
+    // rounds 61 us for 55).
+    RotateArgs args = a;
+    args.line = NP > 1 && (double)a.n_tokens * (rounds + 3) / (room * kRotateWarps) + 3 < 0.92 * least;
+    if (args.line) grid = dim3((unsigned)room);
     const bool full = a.head_dim == 16 * LANES && a.turned == a.head_dim && (a.norm_dim == a.head_dim || (!a.q_weight && !a.k_weight));
     constexpr int bytes = kRotateWarps * Rotate<IO, F8, LANES, NP, false, false>::RING;
     auto start = [&](auto *kernel, std::atomic<uint64_t> &asked) {
         const cudaError_t e = allow_shared(kernel, bytes, a.device, asked);
-        return e != cudaSuccess ? e : launch_after(kernel, grid, kRotateThreads, bytes, stream, a);
+        return e != cudaSuccess ? e : launch_after(kernel, grid, kRotateThreads, bytes, stream, args);
     };
     static std::atomic<uint64_t> asked[4];
     if constexpr (NP == 1)
