@@ -46,6 +46,7 @@ kvx_status kvx_rotation_create(const kvx_rotation_config *cfg, kvx_rotation_t *o
     if (f.begin < 0 || f.dim < 0 || f.norm_dim < 0) return fail(KVX_EINVAL, "begin, dim and norm_dim must be >= 0");
     if (f.begin % 8 || f.norm_dim % 8 || f.dim % (f.layout == KVX_ROTATE_PAIRS ? 8 : 16))
         return fail(KVX_EUNSUPPORTED, "begin and norm_dim must be multiples of 8, dim of 16 (8 for pairs)");
+    if (std::max(f.begin, f.norm_dim) > kCacheMaxLatent) return fail(KVX_EUNSUPPORTED, "begin or norm_dim above %d", kCacheMaxLatent);
     if (f.dim > 2 * kRotateMaxPairs) return fail(KVX_EUNSUPPORTED, "more than %d elements turn", 2 * kRotateMaxPairs);
     if (f.base == 0) f.base = 10000;
     if (!std::isfinite(f.base) || f.base <= 1) return fail(KVX_EINVAL, "base must be above 1");

@@ -613,7 +613,7 @@ typedef struct kvx_rotation_s *kvx_rotation_t;
 /*
  * kvx_rotation_create -- the frequencies of a rotation, computed once in 64 bits (host only; no CUDA call). A rotation is never
  * changed, so any number of caches, threads and captured graphs may use one; it may be destroyed once the calls that name it returned.
- * KVX_EUNSUPPORTED for begin or norm_dim that are no multiples of 8, dim no multiple of 16 (8 for PAIRS) or above 256.
+ * KVX_EUNSUPPORTED for begin or norm_dim that are no multiples of 8 or above 576, dim no multiple of 16 (8 for PAIRS) or above 256.
  * kvx_rotation_get: up to cap frequencies in radians a position (*n receives their number, dim / 2) and the magnitude.
  */
 kvx_status kvx_rotation_create(const kvx_rotation_config *cfg, kvx_rotation_t *out);

@@ -90,3 +90,10 @@ def test_rotations_of_other_heads_are_refused():
         refused(kvx.kvx_cache_append_rotated, kvx.KVX_EINVAL, c, rotation=r, **CALL)
     c = kvx.kvx_cache_create(pool(GEOM), value_type=kvx.KVX_BF16, n_q_heads=4)
     refused(kvx.kvx_cache_append_rotated, kvx.KVX_EINVAL, c, rotation=r, **CALL)
+
+
+@pytest.mark.parametrize("kw", [dict(begin=2 ** 31 - 8, dim=16), dict(begin=2 ** 31 - 16, dim=16), dict(begin=2 ** 31 - 256, dim=256, layout=1),
+                                dict(begin=584, dim=16), dict(begin=584), dict(norm_dim=2 ** 31 - 8), dict(norm_dim=584)])
+def test_parts_beyond_the_widest_head_are_refused(kw):
+    """begin + dim passes 31 bits: a sum that wrapped would be below any head's dim."""
+    refused(kvx.kvx_rotation_create, kvx.KVX_EUNSUPPORTED, **kw)
