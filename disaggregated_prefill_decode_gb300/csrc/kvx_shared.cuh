@@ -230,12 +230,13 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
     __syncthreads();
     tensor_fence_after();
     const uint32_t tmem = s_tmem;
-    auto wait = [&](uint64_t *bar, uint32_t parity) {              // of any role: false when it, or another role's, ran out
-        if (phase_done(bar, parity & 1)) return true;
-        if (s_failed) return false;
-        if (wait_full(bar, parity & 1, a.wait_ns)) return true;
-        s_failed = 1;
-        return false;
+    // Of any role, by a whole warp: false when it, or another role's, ran out. All lanes have the same answer, as they take part in what
+    // follows together (instructions on TMEM): one lane could see a phase that has come just as another one's wait runs out.
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (__all_sync(~0u, phase_done(bar, parity & 1))) return true;
+        const bool ok = __all_sync(~0u, !s_failed && wait_full(bar, parity & 1, a.wait_ns));
+        if (!ok) s_failed = 1;
+        return ok;
     };
     auto goes_on = [&](int part) { return a.stall != part || blockIdx.x != 0 || wait(&s_never, 0); };   // the testing hook
     const int32_t group = a.n_q_heads / a.n_kv_heads;
@@ -394,13 +395,13 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
         const uint64_t values = operand(shared_addr(smem + S::OFF_RING), S::CHUNK, 1024, 2);
         const uint32_t scores = columns + kSharedColScores + slot * 128, sums = columns + kSharedColSums + slot * 128;
         int item = 0, turn = 0, weighed = 0;
-        bool ok = slot < 2 && __all_sync(~0u, goes_on(kStallSharedProducts));
+        bool ok = slot < 2 && goes_on(kStallSharedProducts);
         for (; ok && work.read(s, c_begin, c_end, units); ++work.index) {
             const int n = (int)__reduce_max_sync(~0u, (uint32_t)work.n);
             if (n == 0) continue;
             const bool both = __any_sync(~0u, work.both);
             const int first = both ? 0 : slot, step = both ? 1 : 2;            // the slot's tiles
-            if (!(ok = __all_sync(~0u, wait(&s_queried, turn++)))) break;
+            if (!(ok = wait(&s_queried, turn++))) break;
             fence_async();                                         // copies come by the generic proxy, products read by the other
             const uint64_t q = queries + (both ? slot * (S::TILE / 16) : 0);
             auto release = [&](int stage) {
@@ -409,7 +410,7 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
             };
             auto key_stage = [&](int t) { return t ? item + 2 * t - 1 : item; };
             auto copied = [&](int at) {
-                ok = ok && __all_sync(~0u, wait(&s_full[at % S::STAGES], at / S::STAGES));
+                ok = ok && wait(&s_full[at % S::STAGES], at / S::STAGES);
                 fence_async();
             };
             auto score = [&](int t) {
@@ -434,7 +435,7 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
                 const uint64_t v = values + at % S::STAGES * (S::TILE / 16);
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
-                    ok = ok && __all_sync(~0u, wait(&s_weighed[slot][h], weighed));
+                    ok = ok && wait(&s_weighed[slot][h], weighed);
                     if (!ok) break;
                     tensor_fence_after();
 #pragma unroll
@@ -455,7 +456,7 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
         leave_registers<S::REGS_COPIES>();
         const int lw = w - 12;
         int item = 0, turn = 0, tiles = 0;
-        bool ok = __all_sync(~0u, goes_on(kStallSharedCopies));
+        bool ok = goes_on(kStallSharedCopies);
         const uint32_t smem0 = shared_addr(smem);
         // Position `lane` of this warp's quarter of a tile: its block, -2 behind the prefix; then its row's offset in its buffer, in
         // 16-byte units. In two steps, so that the block's id is on its way a tile ahead.
@@ -488,7 +489,7 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
             const uint32_t piece_at = piece / 8 * S::CHUNK;
             auto place = [&](int r) { return piece_at + r * 128 + ((piece % 8) ^ (r & 7)) * 16; };
             auto put = [&](const uint8_t *from, uint32_t row) {
-                if (item >= S::STAGES) ok = ok && __all_sync(~0u, wait(&s_free[item % S::STAGES], item / S::STAGES - 1));
+                if (item >= S::STAGES) ok = ok && wait(&s_free[item % S::STAGES], item / S::STAGES - 1);
                 if (!ok) return;
                 const uint32_t to = smem0 + S::OFF_RING + item % S::STAGES * S::TILE;
                 from += piece * 16;
@@ -525,7 +526,7 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
                     row = next;
                     if (t) continue;
                     // Queries, once those before have been multiplied.
-                    if (turn) ok = ok && __all_sync(~0u, wait(&s_unqueried, turn - 1));
+                    if (turn) ok = ok && wait(&s_unqueried, turn - 1);
                     if (!ok) break;
                     for (int b = 0; b < (work.both ? 2 : 1); ++b) {
                         const uint64_t mine = (uint64_t)query_row(b * kSharedRows + lw * 32 + lane);
@@ -568,7 +569,7 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
                 asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(y0), "r"(y1), "r"(y2), "r"(y3) : "memory");
             };
             auto store = [&](const uint4 (&y)[READS]) {
-                if (item >= S::STAGES) ok = ok && __all_sync(~0u, wait(&s_free[item % S::STAGES], item / S::STAGES - 1));
+                if (item >= S::STAGES) ok = ok && wait(&s_free[item % S::STAGES], item / S::STAGES - 1);
                 if (!ok) return;
                 const uint32_t to = smem0 + S::OFF_RING + item % S::STAGES * S::TILE;
 #pragma unroll
@@ -588,7 +589,7 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
             // Queries as f16: a bf16 row is brought by a power of two to where f16 holds its elements exactly down to 2^-31 of the largest.
             // All rows are on their way at once, to the places where the lane that copied them turns them into f16.
             auto load_queries = [&]() {
-                if (turn) ok = ok && __all_sync(~0u, wait(&s_unqueried, turn - 1));
+                if (turn) ok = ok && wait(&s_unqueried, turn - 1);
                 if (!ok) return;
                 constexpr int LANES = S::PIECES, ROWS = 32 / LANES;
                 const int p = lane % LANES, slots = work.both ? 2 : 1;
