@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(kSlotThreads) kvx_slot_map_kernel(const SlotAr
     const int64_t inf = INT32_MAX;
     Sums base = {0, 0};
     bool bad = false;                                    // CTA 0: this thread saw a request out of range
+    int32_t last = 0;                                    // its first thread: the last entry of free_blocks that is taken
     const bool pairs = ((uintptr_t)a.slots & 15) == 0 && ((uintptr_t)a.positions & 7) == 0;
     for (int32_t r0 = 0; r0 < a.n_reqs; r0 += kReqs) {
         const int m = min(kReqs, a.n_reqs - r0);
@@ -108,6 +109,8 @@ __global__ void __launch_bounds__(kSlotThreads) kvx_slot_map_kernel(const SlotAr
         }
         Sums total;
         Sums at = cta_exclusive(mine, &total);
+        const int64_t b_end = base.blk + total.blk;
+        if (blockIdx.x == 0 && threadIdx.x == 0 && b_end > 0 && b_end <= a.n_free) last = a.free_blocks[b_end - 1];
         for (int i = i0; i < i1; ++i) {
             const Sums n = {s_tok[i], s_blk[i]};
             s_tok[i] = at.tok;
@@ -123,7 +126,6 @@ __global__ void __launch_bounds__(kSlotThreads) kvx_slot_map_kernel(const SlotAr
                 a.seq_len[r0 + i] = (int32_t)(s_ctx[i] + end - s_tok[i]);
             }
 
-        const int64_t b_end = base.blk + total.blk;
         for (int64_t tile = first_tile(base.blk / kSlotThreads, blockIdx.x, gridDim.x); tile * kSlotThreads < b_end; tile += gridDim.x) {
             const int64_t b = tile * kSlotThreads + threadIdx.x;
             if (b < base.blk || b >= b_end) continue;
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(kSlotThreads) kvx_slot_map_kernel(const SlotAr
          t += (int64_t)gridDim.x * kSlotThreads)
         a.slots[t] = -1;
     if (blockIdx.x == 0) {
-        const bool range = __syncthreads_or(bad) || base.tok > a.max_tokens;
+        const bool range = __syncthreads_or(bad || last < 0) || base.tok > a.max_tokens;
         if (threadIdx.x == 0) {
             a.tok_off[a.n_reqs] = base.tok;
             a.result->n_tokens = base.tok;

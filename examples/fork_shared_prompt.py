@@ -98,6 +98,7 @@ def main(steps: int = 40, prompt: int = 500, answers: int = 12, seed: int = 0) -
         """The rows go on from these rows; their partial pages are copied in every layer."""
         nonlocal kept
         parent.copy_(torch.tensor(parents, **i32))
+        free.fill_(-1)                                                     # behind the free pages: no page, not one of an earlier list
         torch.cuda.synchronize()
         kvx.kvx_pages_free(table, width, width, seq_len, n, BLOCK, n_blocks, refs, free, result, side)
         kvx.kvx_pages_fork(table, width, width, seq_len, n, parent, n, BLOCK, free, n, new_table, width, new_len, src, dst, first, result, side)
@@ -127,6 +128,7 @@ def main(steps: int = 40, prompt: int = 500, answers: int = 12, seed: int = 0) -
 
     def step():
         ctx.copy_(seq_len)
+        free.fill_(-1)
         kvx.kvx_pages_free(table, width, width, ctx, n, BLOCK, n_blocks, refs, free, result, side)
         kvx.kvx_slot_map(ctx, one, n, BLOCK, free, n, table, width, width, n, tok_off, slots, positions, seq_len, result, side)
         for layer in range(LAYERS):

@@ -506,8 +506,9 @@ typedef struct kvx_slot_result {
     int64_t n_blocks;      /* entries of free_blocks taken, or needed when there are too few */
     int64_t status;        /* KVX_OK; KVX_ENOMEM: n_blocks > n_free; KVX_ERANGE: n_tokens > max_tokens,
                               a request longer than max_blocks blocks or 2^31 - 1 tokens, a negative
-                              length, or a token that goes on in a block the table does not hold
-                              (KVX_ENOMEM when both) */
+                              length, a token that goes on in a block the table does not hold, or a
+                              list of free blocks that ends in negative ids and has run out (the last
+                              entry taken is negative) (KVX_ENOMEM when both) */
 } kvx_slot_result;
 
 /*
@@ -699,7 +700,10 @@ typedef struct kvx_page_result {
  * kvx_pages_free -- which blocks of a pool no request holds.
  * refs[b] (n_blocks entries): how many table entries hold block b. free_blocks (room for n_blocks ids): the blocks that none
  * holds, ascending, what kvx_slot_map and kvx_pages_fork take; entries behind the last are left as they were, so the n_free of
- * those calls is at most the n_blocks of this one's result.
+ * those calls is at most the n_blocks of this one's result. A captured step, which has no such number on the host, fills
+ * free_blocks with -1 before this call (a cudaMemsetAsync of 0xff): n_free is then as many as it may take, up to the pool's n_blocks,
+ * and where the list has run out no block is given and both calls report it (KVX_ERANGE). Without that, entries behind the last may
+ * be ids of an earlier step, whose blocks are held by now.
  */
 kvx_status kvx_pages_free(const int32_t *block_table, int64_t table_stride, int32_t max_blocks, const int32_t *seq_len, int32_t n_reqs,
                           int32_t block_size, int64_t n_blocks, int32_t *refs, int32_t *free_blocks, kvx_page_result *result,
