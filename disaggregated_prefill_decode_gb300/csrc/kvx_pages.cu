@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kPageThreads, 1) kvx_pages_fork_kernel(const F
         bool need = held && held * (int64_t)a.t.block_size != len && __ldcg(a.first + p) != (int32_t)i;
         if (need) {
             last = a.t.block_table[p * a.t.table_stride + held - 1];
-            if (last < 0) bad = true, need = false;                    // a page that the row does not hold
+            if (last < 0) need = false;                                // a page that the row lacks, reported below
         }
         // both sums in one: pages to copy above, blocks below (at most 2^14 rows a pass, of 2^31 blocks)
         int64_t total, all;
@@ -232,6 +232,7 @@ __global__ void __launch_bounds__(kPageThreads, 1) kvx_pages_fork_kernel(const F
         copies += all >> 46;
         held_all += all & (((int64_t)1 << 46) - 1);
         const int64_t upto = min(step, a.n_out - pass);
+        int32_t signs = 0;
         for_entries((int32_t)upto, a.t.max_blocks, rank, ranks, [&](int32_t r, int32_t col) {
             const int32_t from = a.parent[pass + r];
             bool ignored = false;
@@ -241,11 +242,14 @@ __global__ void __launch_bounds__(kPageThreads, 1) kvx_pages_fork_kernel(const F
             int32_t *out = a.new_table + (pass + r) * a.new_stride;
             int32_t b[kEntries];
 #pragma unroll
-            for (int e = 0; e < kEntries; ++e) b[e] = col + 32 * e < n ? row[col + 32 * e] : -1;
+            for (int e = 0; e < kEntries; ++e) b[e] = col + 32 * e < n ? row[col + 32 * e] : 0;
 #pragma unroll
-            for (int e = 0; e < kEntries; ++e)
-                if (col + 32 * e < a.t.max_blocks) out[col + 32 * e] = b[e];
+            for (int e = 0; e < kEntries; ++e) {
+                signs |= b[e];
+                if (col + 32 * e < a.t.max_blocks) out[col + 32 * e] = col + 32 * e < n ? b[e] : -1;
+            }
         });
+        bad |= signs < 0;                                              // a page that a parent's row lacks
         ctas.sync();                                                   // the row's last entry is written again, after its copy
         if (need) a.new_table[i * a.new_stride + held - 1] = to;
     }

@@ -693,7 +693,8 @@ typedef struct kvx_page_result {
     int64_t n_blocks;      /* kvx_pages_free: ids written to free_blocks; kvx_pages_fork: pages to copy, and entries of free_blocks taken or,
                               when there are too few, needed; kvx_pages_compact: blocks to move */
     int64_t status;        /* KVX_OK; KVX_ERANGE: a length that is negative or beyond max_blocks * block_size (cut there), a block id
-                              outside the pool or negative, or a row of `parent` outside the table (left out); KVX_ENOMEM: n_blocks > n_free or > max_moves */
+                              outside the pool or negative (kvx_pages_fork, which is not told the pool's size: negative, in the rows that go on; the id is
+                              passed on) or a row of `parent` outside the table (left out); KVX_ENOMEM: n_blocks > n_free or > max_moves */
 } kvx_page_result;
 
 /*
