@@ -34,7 +34,7 @@ __device__ __forceinline__ int32_t held_blocks(const TableArgs &t, int32_t r, bo
 
 // All entries of n rows of `width` columns, kEntries columns of a row for each lane: f(row, first column of the lane's, 32 apart).
 template <class F> __device__ __forceinline__ void for_entries(int32_t n, int32_t width, int rank, int ranks, F f) {
-    const int chunks = (width + 32 * kEntries - 1) / (32 * kEntries), lane = threadIdx.x & 31;
+    const int chunks = (int)(((uint32_t)width + 32 * kEntries - 1) / (32 * kEntries)), lane = threadIdx.x & 31;   // a width may be 2^31 - 1
     const int64_t items = (int64_t)n * chunks, warps = (int64_t)ranks * kPageWarps;
     for (int64_t i = (int64_t)rank * kPageWarps + (threadIdx.x >> 5); i < items; i += warps) {
         const int32_t r = items >> 32 ? (int32_t)(i / chunks) : (int32_t)((uint32_t)i / (uint32_t)chunks);
