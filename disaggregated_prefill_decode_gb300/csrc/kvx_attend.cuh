@@ -11,6 +11,9 @@ namespace kvx {
 
 constexpr uint32_t kNoRow = 0xffffffffu;      // offset of a position that is left out
 constexpr float kLn2 = 0.6931471805599453f;
+// The least scale of an 8-bit cache's scores, which are below 2^32 before it (queries 2^15, codes 2^9, 256 of them), so that it adds less than 2^-94 to
+// one; zero would make NaN of the minus infinity that stands for a position that does not count.
+constexpr float kLeastScale = 0x1p-126f;
 
 // D += A B, 16 x 8 x 16, 32-bit sums. bf16 values for KVX_BF16, else f16.
 template <int VT>

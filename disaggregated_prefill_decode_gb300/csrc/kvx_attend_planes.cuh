@@ -362,7 +362,7 @@ template <class S> __global__ void __launch_bounds__(S::THREADS, 1) kvx_attend_p
                     top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
                     const int e = top > 0.0f && top < INFINITY ? max(-126, min(100, 14 - ilogbf(top))) : 0;
                     const float up = __int_as_float((127 + e) << 23);
-                    scale *= __int_as_float((127 - e) << 23);
+                    scale = fmaxf(scale * __int_as_float((127 - e) << 23), kLeastScale);
 #pragma unroll
                     for (int i = 0; i < S::KCH * S::KSTEP * 2; ++i) {
                         const float2 f = unpack<KVX_BF16>(y[i]);

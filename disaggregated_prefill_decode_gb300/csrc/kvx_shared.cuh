@@ -264,7 +264,7 @@ template <class S> __global__ void __launch_bounds__(kSharedThreads, 1) kvx_atte
                 }
                 tensor_fence_after();
                 if constexpr (S::F8 && S::IO == KVX_BF16)
-                    if (i == 0) sc = a.scale * __int_as_float((127 - s_up[turn & 1][work.both ? slot : 0][row]) << 23);
+                    if (i == 0) sc = fmaxf(a.scale * __int_as_float((127 - s_up[turn & 1][work.both ? slot : 0][row]) << 23), kLeastScale);
                 const uint4 four = *reinterpret_cast<const uint4 *>(s_live[(tiles + (work.both ? i : 2 * i + slot)) & 7]);
                 const uint32_t live[4] = {four.x, four.y, four.z, four.w};
                 const bool all = (four.x & four.y & four.z & four.w) == ~0u;
