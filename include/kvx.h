@@ -659,17 +659,22 @@ kvx_status kvx_cache_attend(kvx_cache_t cache, int32_t layer, const void *q, int
 
 /*
  * kvx_cache_attend_shared -- kvx_cache_attend for a batch in which groups of requests share a prefix, which is read and multiplied once
- * for all members of a group. The same results, by the same definition, for the same q, table, lengths, out and lse.
+ * for all members of a group: the same definition for the same q, table, lengths, out and lse, with weights of a prefix in fewer bits (below).
  * Group g is the requests [group_off[g], group_off[g + 1]) (ascending; requests outside every group share nothing), whose first
  * prefix_len[g] positions hold the same keys and values: in the same blocks, or a block in which the prefix ends in copies of it, as
  * kvx_pages_fork makes them. They are read through the row of the group's first member, up to the shortest member's length. With a window a
  * group shares its prefix while the window of every member reaches the first position. Both arrays are device memory, checked there:
  * a negative prefix_len counts as 0, with a group_off that is no such list nothing is shared, and kvx_cache_status reports either.
  * Whether a prefix is worth sharing is decided here: short ones (below 128 positions), batches that read little twice (below 144 MiB by
- * max_blocks), latents and head dims above 128 go to kvx_cache_attend, or read their prefixes themselves.
+ * max_blocks), latents and head dims above 128 go to kvx_cache_attend, or read their prefixes themselves. A batch that goes to kvx_cache_attend
+ * as a whole (all of these but short prefixes) leaves the two arrays unread, and nothing in them is reported. The bound is the host's, from
+ * max_blocks, as the lengths are on the device: a table much wider than its requests are long takes three launches where one would do.
  * workspace: kvx_cache_shared_bytes bytes of device memory (0 for caches that do not share), on a 16-byte boundary, in no particular
- * state and free again after the call's device work; calls whose device work overlaps need workspaces, and handles, of their own.
- * Weights leave 2^-15 of a weight at most, or 2^-30 of the largest of the row. Two calls on the same inputs give the same bits.
+ * state and free again after the call's device work; calls whose device work overlaps need workspaces, and handles, of their own. Most of
+ * it are, for each KV head, 256 (4 head_dim + 8) bytes a group (of n_reqs / 2 at most) and as many for every 256 rows (requests x query heads
+ * of a KV head).
+ * Weights of a prefix leave 2^-15 of a weight at most, or 2^-30 of the largest of the row, more than kvx_cache_attend's: a batch that comes
+ * to be shared may differ in an output's last place. Two calls on the same inputs give the same bits.
  */
 kvx_status kvx_cache_shared_bytes(kvx_cache_t cache, int32_t n_reqs, int32_t n_groups, int64_t *bytes);
 kvx_status kvx_cache_attend_shared(kvx_cache_t cache, int32_t layer, const void *q, int64_t q_stride,
