@@ -627,7 +627,7 @@ kvx_status kvx_rotation_get(kvx_rotation_t rotation, double *frequencies, int32_
  * turned by the token's position, (a, b) -> magnitude * (a cos - b sin, b cos + a sin). Keys, and values as they are, go to
  * their slots of one layer, queries to q_out: [n_tokens][n_q_heads][head_dim], which may be q itself (with q's stride) and else
  * overlaps no input. All of it in 32 bits with one rounding at the end, 8-bit codes as in kvx_cache_append; an angle is the position
- * times a 64-bit frequency, 2^-25 of a turn off at most below position 2^29, 2^-23 beyond (the squares' sum must stay below 2^128). q and q_out may both be NULL. positions: as kvx_slot_map
+ * times a frequency of kvx_rotation_get, 2^-25 of a turn off at most below position 2^29, 2^-23 beyond (the squares' sum must stay below 2^128). q and q_out may both be NULL. positions: as kvx_slot_map
  * makes them, any int32; NULL if dim is 0. A token with slot -1 is skipped, its row of q_out left as it was; so is one with another slot outside
  * the pool, and kvx_cache_status reports it. Pointers and strides (elements) are multiples of 16 bytes.
  */
