@@ -14,8 +14,9 @@ using namespace kvx;
 // of 16 on 1024 (128) 36 / 32, on 2048 (248) 36 / 50; 16 groups of 4 on 2048 (198) 60 / 50.
 static constexpr int64_t kWorthBytes = 144 << 20;
 
+// Rows are counted in 32 bits, rounded up to whole units of 256.
 static bool can_share(const kvx_cache_t c, int32_t n_reqs) {
-    return c->g.n_planes == 2 && c->g.head_dim <= kSharedMaxDim && (int64_t)n_reqs * c->cfg.n_q_heads <= std::numeric_limits<int32_t>::max();
+    return c->g.n_planes == 2 && c->g.head_dim <= kSharedMaxDim && (int64_t)n_reqs * c->cfg.n_q_heads <= std::numeric_limits<int32_t>::max() - 255;
 }
 
 // Places in the workspace; with `base` NULL only their size.

@@ -36,3 +36,11 @@ def test_no_requests_and_destroyed():
     refused(kvx.kvx_cache_attend_shared, kvx.KVX_EINVAL, c, **CALL)
     refused(kvx.kvx_cache_shared_bytes, kvx.KVX_EINVAL, c, 2, 1)
     refused(kvx.kvx_cache_inject_shared_stall, kvx.KVX_EINVAL, c, 1)
+
+
+def test_rows_that_no_32_bits_count():
+    """Up to 2^31 - 256 rows are shared; beyond, and rounding up to 256 of them passes 31 bits, each request reads its own."""
+    c = kvx.kvx_cache_create(pool(GEOM), value_type=kvx.KVX_BF16, n_q_heads=128)
+    for n in (1 << 24, (1 << 24) - 1):
+        assert kvx.kvx_cache_shared_bytes(c, n, 1) == 0
+    kvx.kvx_cache_destroy(c)
