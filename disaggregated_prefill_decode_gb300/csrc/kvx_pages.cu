@@ -7,8 +7,8 @@
 // reads between them.
 //
 // Measured on GB300: free, 40 requests 6.4 us (12.4 with barriers of a cluster, which one CTA has no need of), 1024 sessions on 87000
-// pages 15.4 (20.3); fork with its copies, 16 rows of 16 layers 8.7 (12.9), 128 beams 12 (16.0); compact with its copies, 12 requests 16.6
-// (39.7 when each entry's move was searched in memory, not in shared memory); 2.7 GB of latents 456 (509).
+// pages 15.4 (20.3); fork with its copies, 16 rows of 16 layers 8.7 (12.9), 128 beams 12.3 (16.0); compact with its copies, 12 requests 16.6
+// (39.7 when each entry's move was searched in memory, not in shared memory); 2.7 GB of latents 463 (509).
 #include "kvx_launch.cuh"
 
 #include <cooperative_groups.h>

@@ -11,7 +11,7 @@
 // with the weights are computed once for all heads. Bound by memory: each value is read and written once, in 16 bytes a lane, and what counts
 // is bytes on their way: asynchronous copies of four rounds into places of shared memory that the lane itself reads back.
 //
-// Measured on GB300: 8192 tokens of 64 + 8 + 8 heads of 128 (336 MB) 54.9 us, 6.1 TB/s; 64 latents with 16 query heads 5.3, the host's time for a
+// Measured on GB300: 8192 tokens of 64 + 8 + 8 heads of 128 (336 MB) 54.7 us, 6.1 TB/s; 64 latents with 16 query heads 5.3, the host's time for a
 // call, 1158 of them 14.4, 5000 with 24 heads 70 (4.1 TB/s). Steps: a warp a token, reads of four heads ahead in registers 86.7 us; a persistent warp, sines by the warp 68; no exceptions for
 // lanes where whole heads turn (31 million instructions, 42) 70; the next rounds' reads over tokens, in registers 74; in shared memory
 // 63 with 24 warps an SM, 58 with 16 (8 rounds ahead 71 and 59: the more rows at once, the slower the memory); tokens in two parts 55.

@@ -1,8 +1,8 @@
 // kvx_cache_attend_shared: the launches, the plan of a large batch, and the join of what the other kernels leave.
 //
 // Three launches: the requests' own positions, with the plan made by one of their CTAs (11 us for 16 x 400 positions, 22 for 64 x 500), the prefixes,
-// the join (5 us for 16 requests of 64 heads, 8 for 64). 16 samples of a prompt of 8192 30.9 us in all, 64 requests on 32768 100.6, 96 8-bit
-// requests in 12 groups 49.3; with the own positions joined in their kernel, as kvx_cache_attend does, 32.3, 102 and 49.2. With more than kRestFew
+// the join (5 us for 16 requests of 64 heads, 8 for 64). 16 samples of a prompt of 8192 30.8 us in all, 64 requests on 32768 102, 96 8-bit
+// requests in 12 groups 49.5; with the own positions joined in their kernel, as kvx_cache_attend does, 1.4, 1.4 and 0 us more. With more than kRestFew
 // requests or groups the plan is a launch of its own before the others (2 to 2.4 us more).
 // Of launches that start before the one ahead has ended the wait is all that is left; letting them start earlier still (launch_dependents)
 // took SM time from it: 40 us, 47. A plan in each CTA of the prefixes' kernel took as long as one of its own: its reads are as cold there.
@@ -53,8 +53,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) kvx_shared_plan(const __grid_
 }
 
 // The join: a thread has four elements of a row (request, query head), the sums of its own positions and those of the CTAs that its
-// unit went to, ten at a time (the whole call for 16 samples and for 64 requests on a document: 8 36.7 and 105.3 us, 10 35.6 and 103.9, 12 36.4 and
-// 104.8, 20 36.0 and 111). Reads and writes are whole sectors: 8 rows x 4 float4 a warp.
+// unit went to, ten at a time: half of the 19 or 20 that one unit for each of 8 KV heads leaves on 152 SMs, so that two rounds take them all (the
+// whole call for 16 samples and for 64 requests on a document, which have such units: 8 36.7 and 105.3 us, 10 35.6 and 103.9, 12 36.4 and 104.8, 20 36.0 and
+// 111). Units in fewer parts take one round, of which the places beyond are predicated. Reads and writes are whole sectors: 8 rows x 4 float4 a warp.
 template <int IO, int D> __global__ void __launch_bounds__(256) kvx_shared_join(const __grid_constant__ SharedArgs s, int ctas) {
     constexpr int C4 = D / 4, ROWS = 256 / C4, AT_ONCE = 10;
     wait_for_earlier();

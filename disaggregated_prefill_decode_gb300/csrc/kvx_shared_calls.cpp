@@ -8,10 +8,11 @@
 using namespace kvx;
 
 // What sharing a prefix can save has to be worth its launches: below this many bytes that requests would read again, which they mostly
-// find in L2, each reads its own. On GB300, 8 KV heads of 128 with 8 query heads each (us, shared / each its own): bf16, one group of 8 on 4096 positions
+// find in L2, each reads its own. One bound for all that the host knows; where a batch breaks even depends on how many of its units' 256 rows are filled
+// and how many units there are besides, so some batches above it lose up to a fifth (8 bits in many small groups, the last ones here). On GB300, 8 KV heads of 128 with 8 query heads each (us, shared / each its own): bf16, one group of 8 on 4096 positions
 // (113 MiB read again) 26.6 / 26.5, on 8192 (226) 28.6 / 42.8; one of 64 on 512 (142) 34 / 31; 4 groups of 4 on 2048 (99) 27.9 / 27.3, on 4096 (195)
 // 35 / 44; 16 groups of 4 on 512 (108) 35 / 31, on 1024 (204) 44 / 47. 8 bits: one group of 8 on 8192 (113) 29.1 / 29.4, on 16384 (225) 35 / 47; 4 groups
-// of 16 on 1024 (128) 36 / 32, on 2048 (248) 36 / 50; 16 groups of 4 on 2048 (198) 60 / 50.
+// of 16 on 1024 (128) 36 / 32, on 2048 (248) 36 / 50; 4 groups of 4 on 8192 (193) 48.8 / 47.4; 16 groups of 4 on 2048 (198) 60 / 50.
 static constexpr int64_t kWorthBytes = 144 << 20;
 
 // Rows are counted in 32 bits, rounded up to whole units of 256.

@@ -11,7 +11,7 @@
 //
 // Measured on GB300: 4.5 M tokens of 256 sessions (54 MB) 13.9 us (two tokens a thread with a bisection of
 // their own 32.5, a bisection for 256 tokens 16.4, 32-bit arithmetic for tiles of one request 13.9); 777
-// requests with 140 thousand tokens 7.5; 16 decoding requests 5.0, which is what the host needs for a call.
+// requests with 140 thousand tokens 7.5; 16 decoding requests 5.2, nearly all of it what the host needs for a call.
 // Bound by the two latencies before the first store where it is small, by issue (2.7 a clock) where it is large.
 #include "kvx_launch.cuh"
 
